@@ -113,9 +113,11 @@ def _parents(rs, nodes, shape, children=4):
 
 
 def _lengths(rs, c):
+    """Context lengths log-uniform over the case's range: its n quantiles, in an order of the seed."""
     lo, hi = c["kv_lo"], c["kv_hi"]
-    kv = np.exp(rs.uniform(math.log(lo), math.log(hi + 0.999), size=c["n"])).astype(np.int64)
-    return np.clip(kv, lo, hi)
+    at = (np.arange(c["n"]) + 0.5) / c["n"]
+    kv = np.exp(math.log(lo) + at * (math.log(hi + 0.999) - math.log(lo))).astype(np.int64)
+    return rs.permutation(np.clip(kv, lo, hi))
 
 
 def _tables(rs, kv):
@@ -148,8 +150,8 @@ def prepare(case, seed):
 def _prepare_tree(c, seed):
     rs, gen = np.random.RandomState(seed), _gen(seed)
     n = c["n"]
-    nodes = rs.randint(c["nodes_lo"], c["nodes_hi"] + 1, size=n)
-    kv = np.maximum(_lengths(rs, c), nodes)
+    nodes = rs.permutation(c["nodes_lo"] + np.arange(n) * (c["nodes_hi"] + 1 - c["nodes_lo"]) // n)
+    kv = _lengths(rs, c)
     num_pages, bt_indptr, bt = _tables(rs, kv)
     qo = np.concatenate([[0], np.cumsum(nodes)])
     parent = np.concatenate([_parents(rs, int(m), c["shape"]) for m in nodes])
@@ -216,7 +218,7 @@ def _prepare_verify(c, seed):
 def _prepare_compact(c, seed):
     rs, gen = np.random.RandomState(seed), _gen(seed)
     n, m = c["n"], c["nodes"]
-    kv = np.maximum(_lengths(rs, c), m)
+    kv = _lengths(rs, c)
     num_pages, bt_indptr, bt = _tables(rs, kv)
     path = np.full((n, 16), -1)
     count = np.minimum(m, 1 + rs.randint(0, 2 * c["accept"] - 1, size=n)) if n > 1 else np.array([c["accept"]])
