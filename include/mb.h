@@ -335,6 +335,110 @@ mb_status mb_sample_greedy(const void *x, int32_t T, const int32_t *rows, int32_
 mb_status mb_embed(const void *table, int32_t vocab, int32_t d, const int32_t *ids, int32_t n, void *out,
                    void *stream);
 
+/* ---------------- drafted tokens (speculative decoding) -------------------
+ * One pass checks several drafted tokens of each request at once.  A request
+ * brings the nodes of a tree: parent[t] is the index, within the request, of
+ * the parent of its node t (less than the node's own index), or -1 for a node
+ * that hangs on the cached prefix.  Node 0 is the last sampled token, whose
+ * keys are not cached yet, the others are drafted continuations of it; a
+ * chain is the tree with parent[i] = i - 1, a plain decode the tree of one
+ * node.  At most MB_MAX_TREE_NODES nodes per request.  A step is
+ *   layers over all nodes (mb_step_tree, mb_stack_step_tree, or a caller's own
+ *   around mb_tree_attention), logits of every node (mb_sample_greedy with
+ *   rows = all), mb_verify_tree, mb_kv_compact,
+ * after which kv_len counts the accepted nodes and the next token is node 0
+ * of the next step.  Descriptor arrays are DEVICE int32 here, as their
+ * contents come from the draft and from mb_verify_tree; what a host check
+ * cannot see is checked by the kernels (mb_device_status with layer NULL). */
+#define MB_MAX_TREE_NODES 128
+
+/* Attention of drafted nodes over the paged cache.  Request r owns rows
+ * [qo_indptr[r], qo_indptr[r+1]) of q and o; its kv_len[r] keys (cached prefix,
+ * then its nodes in order, already appended) lie in pages
+ * bt[bt_indptr[r] ..], token p in slot p % 16 of the table's page p / 16.
+ * Node i sees the whole prefix, its ancestors and itself; scale 1/sqrt(hd).
+ *   q     device bf16 [T][Hq][hd] (rotated), 16-byte aligned
+ *   pool  device bf16 [num_pages][2][Hkv][16][hd] (mb_kv_layout's), 128-byte aligned
+ *   o     device bf16 [T][Hq hd], 16-byte aligned, must not alias q
+ * head_dim 64 or 128, Hq / Hkv at most 8.  workspace: device memory of
+ * mb_tree_attention_workspace_bytes() bytes, 256-byte aligned, needs no
+ * initialisation; a call owns it until it completes (calls on unordered
+ * streams, graphs that may run at once, need one each).  Rows outside every
+ * request are left as they were.  A request that breaks a rule (more than
+ * MB_MAX_TREE_NODES nodes, kv_len below its nodes, a short table, rows outside
+ * [0, T)) records MB_EDEVICE and its rows are left as they were; a page id out
+ * of range is read as page 0, a parent out of range as -1, with MB_EDEVICE.
+ * Non-finite values of keys and values that a node does not see do not reach
+ * it.  Errors: MB_EINVAL, MB_EUNSUPPORTED, MB_ECUDA. */
+mb_status mb_tree_attention(const void *q, const void *pool, void *o, int32_t num_pages, int32_t n_q_heads,
+                            int32_t n_kv_heads, int32_t head_dim, int32_t num_reqs, int32_t T,
+                            const int32_t *qo_indptr, const int32_t *kv_len, const int32_t *bt_indptr,
+                            const int32_t *bt, const int32_t *parent, void *workspace, void *stream);
+int64_t mb_tree_attention_workspace_bytes(void);
+
+/* Verification of drafted tokens against the target's probabilities
+ * p = softmax(logits / temperature) from given random numbers.  Row i of a
+ * request's logits is the target's distribution after node i.  From node 0 on,
+ * the children of the current node are tested in index order; the first to
+ * pass becomes the current node.  Child i with token x passes if
+ *   u_accept[i] (1 - sum of p over tokens refused here) < p(x)   (draft_probs NULL:
+ *                      the draft proposed x for certain; a refused token's p
+ *                      becomes 0, so the same token twice fails the second time)
+ *   u_accept[i] c q(x) < p(x) - a q(x)                  (draft_probs given: q = the row
+ *                      of the current node, its children drawn from q; a = 0 and
+ *                      c = 1 before the first refusal, each refusal sets a += c,
+ *                      then c = sum_y max(0, p(y) - a q(y)))
+ *   x = argmax of the logits, the lowest index among equal maxima   (temperature 0)
+ * When none passes (or there is none, or the path has max_path nodes), the
+ * next token is the first whose cumulative weight exceeds u_final[r] times the
+ * weights' sum; the weights are what the refusals left of p (without refused
+ * tokens, or max(0, p - a q); p itself if nothing is left); at temperature 0
+ * the argmax.  This keeps the target's distribution: Leviathan et al. 2023,
+ * Miao et al. 2024 for trees.  A NaN or -inf logit has probability 0; a row of
+ * nothing else gives token 0.  Weights are summed as integer multiples of
+ * 2^-40 of the largest, so the result does not depend on how the row is split.
+ *   logits       device bf16 [T][vocab], vocab % 8 == 0, 16-byte aligned
+ *   tokens       device int32 [T], the node's token (that of node 0 is not read);
+ *                one outside [0, vocab) is refused and records MB_EDEVICE
+ *   draft_probs  device fp32 [T][vocab], 16-byte aligned, or NULL
+ *   temperature  device fp32 [num_reqs], >= 0 (0: greedy), or NULL: all greedy
+ *   u_accept     device fp32 [T] in [0, 1) (that of node 0 is not read); u_final device fp32
+ *                [num_reqs] in [0, 1); both may be NULL if temperature is
+ *   n_accepted   device int32 [num_reqs]: nodes of the accepted path, node 0 included
+ *   path         device int32 [num_reqs][max_path]: their indices within the
+ *                request, ascending, then -1; max_path >= 1
+ *   next_token   device int32 [num_reqs]
+ * A request without rows gives 0 nodes and next token -1.
+ * Errors: MB_EINVAL, MB_EUNSUPPORTED, MB_ECUDA. */
+mb_status mb_verify_tree(const void *logits, int32_t vocab, const int32_t *tokens, const float *draft_probs,
+                         int32_t num_reqs, int32_t T, const int32_t *qo_indptr, const int32_t *parent,
+                         const float *temperature, const float *u_accept, const float *u_final, int32_t max_path,
+                         int32_t *n_accepted, int32_t *path, int32_t *next_token, void *stream);
+
+/* Moves the accepted path's keys and values behind the prefix, in n_pools
+ * pools (the layers' of a stack) at once: with c = kv_len[r] minus the
+ * request's nodes, token c + path[r][k] goes to c + k for k < n_accepted[r],
+ * and new_kv_len[r] = c + n_accepted[r].  The slots behind keep what they
+ * held.  pools: HOST array of the pools' device bases (mb_kv_layout), each
+ * [num_pages][2][n_kv_heads][16][head_dim] bf16, 16-byte aligned, distinct;
+ * the other arrays device int32 as in mb_verify_tree and mb_tree_attention;
+ * new_kv_len must not alias kv_len.  head_dim % 8 == 0.  A request whose path
+ * is not ascending within its nodes, or whose table or pages break the rules,
+ * records MB_EDEVICE and keeps its cache; its new_kv_len is not written.
+ * Errors: MB_EINVAL, MB_EUNSUPPORTED, MB_ECUDA. */
+mb_status mb_kv_compact(void *const *pools, int32_t n_pools, int32_t num_pages, int32_t n_kv_heads, int32_t head_dim,
+                        int32_t num_reqs, const int32_t *qo_indptr, const int32_t *kv_len, const int32_t *bt_indptr,
+                        const int32_t *bt, const int32_t *n_accepted, const int32_t *path, int32_t max_path,
+                        int32_t *new_kv_len, void *stream);
+
+/* Copies page src[i] onto page dst[i], i < n_pairs, in n_pools pools at once
+ * (a fork of a request: its pages copied for the child).  src and dst: HOST
+ * int32, read during the call (a captured call keeps them); page ids in
+ * [0, num_pages), dst ids distinct and none of them among src (a source may
+ * repeat).  pools as in mb_kv_compact.  Errors: MB_EINVAL, MB_EUNSUPPORTED, MB_ECUDA. */
+mb_status mb_kv_copy_pages(void *const *pools, int32_t n_pools, int32_t num_pages, int32_t n_kv_heads,
+                           int32_t head_dim, const int32_t *src, const int32_t *dst, int32_t n_pairs, void *stream);
+
 /* Adaptive chunk size (llm-stack-book 7.8, "Priority and Preemption Policies",
  * adaptive_chunk_size, and its exercise 4, which applies it in schedule()):
  * from the next mb_sched_pack on, every prefill chunk of a step is capped at

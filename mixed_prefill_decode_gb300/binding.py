@@ -97,6 +97,11 @@ _SIGS = {
     "mb_layer_set_gemm_workspace": (_I32, [_VP, _VP]),
     "mb_sample_greedy": (_I32, [_VP, _I32, _VP, _I32, _I32, ctypes.c_float, _VP, _VP, _I32, _VP, _VP, _VP, _VP]),
     "mb_embed": (_I32, [_VP, _I32, _I32, _VP, _I32, _VP, _VP]),
+    "mb_tree_attention": (_I32, [_VP] * 3 + [_I32] * 6 + [_VP] * 7),
+    "mb_tree_attention_workspace_bytes": (_I64, []),
+    "mb_verify_tree": (_I32, [_VP, _I32, _VP, _VP, _I32, _I32] + [_VP] * 5 + [_I32] + [_VP] * 4),
+    "mb_kv_compact": (_I32, [ctypes.POINTER(_VP)] + [_I32] * 5 + [_VP] * 6 + [_I32, _VP, _VP]),
+    "mb_kv_copy_pages": (_I32, [ctypes.POINTER(_VP)] + [_I32] * 4 + [c_int32_p, c_int32_p, _I32, _VP]),
     "mb_sched_counts": (_I32, [_VP, c_int32_p]),
     "mb_sched_save": (_I32, [_VP, c_int64_p, _I64, c_int64_p]),
     "mb_sched_load": (_I32, [c_int64_p, _I64, ctypes.POINTER(_VP)]),
@@ -294,6 +299,45 @@ def mb_sample_greedy(x, T: int, rows, n_rows: int, d: int, eps: float, g_final, 
 
 def mb_embed(table, vocab: int, d: int, ids, n: int, out, stream=None) -> None:
     _check(lib().mb_embed(_ptr(table), vocab, d, _ptr(ids), n, _ptr(out), stream))
+
+
+# -------------------------------------------------------- drafted tokens
+def mb_tree_attention(q, pool, o, num_pages: int, n_q_heads: int, n_kv_heads: int, head_dim: int, num_reqs: int,
+                      T: int, qo_indptr, kv_len, bt_indptr, bt, parent, workspace, stream=None) -> None:
+    _check(lib().mb_tree_attention(_ptr(q), _ptr(pool), _ptr(o), num_pages, n_q_heads, n_kv_heads, head_dim, num_reqs,
+                                   T, _ptr(qo_indptr), _ptr(kv_len), _ptr(bt_indptr), _ptr(bt), _ptr(parent),
+                                   _ptr(workspace), _ptr(stream)))
+
+
+def mb_tree_attention_workspace_bytes() -> int:
+    return int(lib().mb_tree_attention_workspace_bytes())
+
+
+def mb_verify_tree(logits, vocab: int, tokens, draft_probs, num_reqs: int, T: int, qo_indptr, parent, temperature,
+                   u_accept, u_final, max_path: int, n_accepted, path, next_token, stream=None) -> None:
+    _check(lib().mb_verify_tree(_ptr(logits), vocab, _ptr(tokens), _ptr(draft_probs), num_reqs, T, _ptr(qo_indptr),
+                                _ptr(parent), _ptr(temperature), _ptr(u_accept), _ptr(u_final), max_path,
+                                _ptr(n_accepted), _ptr(path), _ptr(next_token), _ptr(stream)))
+
+
+def _pool_array(pools):
+    return (_VP * len(pools))(*[_ptr(p) for p in pools])
+
+
+def mb_kv_compact(pools: Sequence, num_pages: int, n_kv_heads: int, head_dim: int, num_reqs: int, qo_indptr, kv_len,
+                  bt_indptr, bt, n_accepted, path, max_path: int, new_kv_len, stream=None) -> None:
+    _check(lib().mb_kv_compact(_pool_array(pools), len(pools), num_pages, n_kv_heads, head_dim, num_reqs,
+                               _ptr(qo_indptr), _ptr(kv_len), _ptr(bt_indptr), _ptr(bt), _ptr(n_accepted), _ptr(path),
+                               max_path, _ptr(new_kv_len), _ptr(stream)))
+
+
+def mb_kv_copy_pages(pools: Sequence, num_pages: int, n_kv_heads: int, head_dim: int, src, dst, stream=None) -> None:
+    """src and dst: host sequences of page ids, one pair per page to copy."""
+    src, dst = _i32(src), _i32(dst)
+    if src.ndim != 1 or src.shape != dst.shape:
+        raise ValueError("src and dst must be one-dimensional and of equal length")
+    _check(lib().mb_kv_copy_pages(_pool_array(pools), len(pools), num_pages, n_kv_heads, head_dim, _as_i32p(src),
+                                  _as_i32p(dst), len(src), _ptr(stream)))
 
 
 # ------------------------------------------------------------- scheduler

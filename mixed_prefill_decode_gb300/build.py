@@ -21,7 +21,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libmb.so")
-SOURCES = ["mb_api.cpp", "mb_sched.cpp", "mb_gemm.cu", "mb_attn.cu", "mb_elem.cu"]
+SOURCES = ["mb_api.cpp", "mb_sched.cpp", "mb_gemm.cu", "mb_attn.cu", "mb_elem.cu", "mb_tree.cu",
+           "mb_verify.cu", "mb_pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -10,6 +10,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <iterator>
 #include <mutex>
 #include <new>
 #include <queue>
@@ -1141,6 +1142,128 @@ mb_status mb_embed(const void *table, int32_t vocab, int32_t d, const int32_t *i
   if (st != MB_OK) return st;
   cudaError_t e = mb::embed_rows_run(table, vocab, d, ids, n, out, ctx->err, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return mb::cuda_fail(e, "mb_embed");
+  return MB_OK;
+}
+
+// ------------------------------------------------------- drafted tokens
+int64_t mb_tree_attention_workspace_bytes(void) { return static_cast<int64_t>(mb::tree_workspace_bytes()); }
+
+mb_status mb_tree_attention(const void *q, const void *pool, void *o, int32_t num_pages, int32_t n_q_heads,
+                            int32_t n_kv_heads, int32_t head_dim, int32_t num_reqs, int32_t T,
+                            const int32_t *qo_indptr, const int32_t *kv_len, const int32_t *bt_indptr,
+                            const int32_t *bt, const int32_t *parent, void *workspace, void *stream) {
+  if (!q || !pool || !o || !qo_indptr || !kv_len || !bt_indptr || !bt || !parent || !workspace)
+    return fail(MB_EINVAL, "mb_tree_attention: null argument");
+  if (num_pages <= 0 || n_q_heads <= 0 || n_kv_heads <= 0 || num_reqs < 0 || T < 0)
+    return fail(MB_EINVAL, "mb_tree_attention: sizes must be positive (num_reqs and T may be 0)");
+  if (n_q_heads % n_kv_heads) return fail(MB_EINVAL, "mb_tree_attention: n_q_heads must be a multiple of n_kv_heads");
+  if (head_dim != 64 && head_dim != 128)
+    return fail(MB_EUNSUPPORTED, "mb_tree_attention: head_dim %d (supported: 64, 128)", head_dim);
+  if (n_q_heads / n_kv_heads > 8)
+    return fail(MB_EUNSUPPORTED, "mb_tree_attention: GQA group %d > 8", n_q_heads / n_kv_heads);
+  if (static_cast<int64_t>(num_pages) * 2 * n_kv_heads > INT32_MAX)
+    return fail(MB_EUNSUPPORTED, "mb_tree_attention: pool too large for 32-bit TMA coordinates");
+  if (q == o) return fail(MB_EINVAL, "mb_tree_attention: o must not alias q");
+  if (reinterpret_cast<uintptr_t>(q) % 16 || reinterpret_cast<uintptr_t>(o) % 16)
+    return fail(MB_EINVAL, "mb_tree_attention: q and o must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(pool) % 128) return fail(MB_EINVAL, "mb_tree_attention: pool must be 128-byte aligned");
+  if (reinterpret_cast<uintptr_t>(workspace) % 256)
+    return fail(MB_EINVAL, "mb_tree_attention: workspace must be 256-byte aligned");
+  if (num_reqs == 0 || T == 0) return MB_OK;
+  mb::DeviceCtx *ctx = nullptr;
+  mb_status st = mb::device_ctx(&ctx);
+  if (st != MB_OK) return st;
+  const mb::TreeArgs a = {q,      pool,     o, qo_indptr, kv_len,     bt_indptr, bt,        parent,
+                          num_reqs, T,      n_q_heads, n_kv_heads, head_dim,  num_pages, workspace, ctx->err};
+  const cudaError_t e = mb::tree_attention_run(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return mb::cuda_fail(e, "mb_tree_attention");
+  return MB_OK;
+}
+
+mb_status mb_verify_tree(const void *logits, int32_t vocab, const int32_t *tokens, const float *draft_probs,
+                         int32_t num_reqs, int32_t T, const int32_t *qo_indptr, const int32_t *parent,
+                         const float *temperature, const float *u_accept, const float *u_final, int32_t max_path,
+                         int32_t *n_accepted, int32_t *path, int32_t *next_token, void *stream) {
+  if (!logits || !tokens || !qo_indptr || !parent || !n_accepted || !path || !next_token)
+    return fail(MB_EINVAL, "mb_verify_tree: null argument");
+  if (vocab <= 0 || num_reqs < 0 || T < 0 || max_path < 1)
+    return fail(MB_EINVAL, "mb_verify_tree: vocab and max_path must be positive, num_reqs and T not negative");
+  if (temperature && (!u_accept || !u_final))
+    return fail(MB_EINVAL, "mb_verify_tree: sampling needs u_accept and u_final");
+  if (vocab % 8) return fail(MB_EUNSUPPORTED, "mb_verify_tree: vocab must be a multiple of 8");
+  if (vocab > (1 << 20)) return fail(MB_EUNSUPPORTED, "mb_verify_tree: vocab > 2^20");
+  if (num_reqs > (1 << 24)) return fail(MB_EUNSUPPORTED, "mb_verify_tree: num_reqs > 2^24");
+  if (reinterpret_cast<uintptr_t>(logits) % 16 || reinterpret_cast<uintptr_t>(draft_probs) % 16)
+    return fail(MB_EINVAL, "mb_verify_tree: logits and draft_probs must be 16-byte aligned");
+  if (num_reqs == 0) return MB_OK;
+  mb::DeviceCtx *ctx = nullptr;
+  mb_status st = mb::device_ctx(&ctx);
+  if (st != MB_OK) return st;
+  const mb::VerifyArgs a = {logits,  tokens,     draft_probs, qo_indptr,  parent, temperature, u_accept, u_final,
+                            n_accepted, path, next_token,  num_reqs, T,      vocab,       max_path, ctx->err};
+  const cudaError_t e = mb::verify_tree_run(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return mb::cuda_fail(e, "mb_verify_tree");
+  return MB_OK;
+}
+
+// The pools of a page operation: present, aligned, distinct.
+static mb_status check_pools(const char *who, void *const *pools, int32_t n_pools, int32_t num_pages,
+                             int32_t n_kv_heads, int32_t head_dim) {
+  if (!pools || n_pools <= 0 || num_pages <= 0 || n_kv_heads <= 0 || head_dim <= 0)
+    return fail(MB_EINVAL, "%s: null pools, or a size that is not positive", who);
+  if (head_dim % 8) return fail(MB_EUNSUPPORTED, "%s: head_dim must be a multiple of 8", who);
+  std::vector<const void *> seen(pools, pools + n_pools);
+  for (const void *p : seen)
+    if (!p || reinterpret_cast<uintptr_t>(p) % 16) return fail(MB_EINVAL, "%s: pools must be 16-byte aligned", who);
+  std::sort(seen.begin(), seen.end());
+  if (std::adjacent_find(seen.begin(), seen.end()) != seen.end())
+    return fail(MB_EINVAL, "%s: a pool is listed twice", who);
+  return MB_OK;
+}
+
+mb_status mb_kv_compact(void *const *pools, int32_t n_pools, int32_t num_pages, int32_t n_kv_heads, int32_t head_dim,
+                        int32_t num_reqs, const int32_t *qo_indptr, const int32_t *kv_len, const int32_t *bt_indptr,
+                        const int32_t *bt, const int32_t *n_accepted, const int32_t *path, int32_t max_path,
+                        int32_t *new_kv_len, void *stream) {
+  mb_status st = check_pools("mb_kv_compact", pools, n_pools, num_pages, n_kv_heads, head_dim);
+  if (st != MB_OK) return st;
+  if (!qo_indptr || !kv_len || !bt_indptr || !bt || !n_accepted || !path || !new_kv_len)
+    return fail(MB_EINVAL, "mb_kv_compact: null argument");
+  if (num_reqs < 0 || max_path < 1) return fail(MB_EINVAL, "mb_kv_compact: num_reqs < 0 or max_path < 1");
+  if (new_kv_len == kv_len) return fail(MB_EINVAL, "mb_kv_compact: new_kv_len must not alias kv_len");
+  if (num_reqs == 0) return MB_OK;
+  mb::DeviceCtx *ctx = nullptr;
+  st = mb::device_ctx(&ctx);
+  if (st != MB_OK) return st;
+  const mb::CompactArgs a = {pools,     n_pools, num_pages, n_kv_heads, head_dim, num_reqs,   max_path, qo_indptr, kv_len,
+                             bt_indptr, bt,      n_accepted, path,      new_kv_len, ctx->err};
+  const cudaError_t e = mb::kv_compact_run(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return mb::cuda_fail(e, "mb_kv_compact");
+  return MB_OK;
+}
+
+mb_status mb_kv_copy_pages(void *const *pools, int32_t n_pools, int32_t num_pages, int32_t n_kv_heads,
+                           int32_t head_dim, const int32_t *src, const int32_t *dst, int32_t n_pairs, void *stream) {
+  mb_status st = check_pools("mb_kv_copy_pages", pools, n_pools, num_pages, n_kv_heads, head_dim);
+  if (st != MB_OK) return st;
+  if (n_pairs < 0 || (n_pairs > 0 && (!src || !dst))) return fail(MB_EINVAL, "mb_kv_copy_pages: bad page lists");
+  for (int32_t i = 0; i < n_pairs; ++i)
+    if (src[i] < 0 || src[i] >= num_pages || dst[i] < 0 || dst[i] >= num_pages)
+      return fail(MB_EINVAL, "mb_kv_copy_pages: pair %d (%d to %d) outside [0, %d)", i, src[i], dst[i], num_pages);
+  std::vector<int32_t> d(dst, dst + n_pairs), s(src, src + n_pairs), both;
+  std::sort(d.begin(), d.end());
+  std::sort(s.begin(), s.end());
+  if (std::adjacent_find(d.begin(), d.end()) != d.end())
+    return fail(MB_EINVAL, "mb_kv_copy_pages: a page is written twice");
+  std::set_intersection(d.begin(), d.end(), s.begin(), s.end(), std::back_inserter(both));
+  if (!both.empty()) return fail(MB_EINVAL, "mb_kv_copy_pages: page %d is both read and written", both[0]);
+  if (n_pairs == 0) return MB_OK;
+  mb::DeviceCtx *ctx = nullptr;
+  st = mb::device_ctx(&ctx);
+  if (st != MB_OK) return st;
+  const cudaError_t e = mb::kv_copy_pages_run(pools, n_pools, n_kv_heads, head_dim, src, dst, n_pairs,
+                                              static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return mb::cuda_fail(e, "mb_kv_copy_pages");
   return MB_OK;
 }
 

@@ -100,4 +100,44 @@ struct AttnArgs {
 // Prefill-chunk tiles and persistent decode workers (both tcgen05) in one launch.
 cudaError_t attention_run(const AttnArgs &a, cudaStream_t st);
 
+// ---- drafted tokens ----
+constexpr int kMaxTreeNodes = 128;        // nodes of one request's tree
+constexpr int kMaxPoolsPerLaunch = 128;   // pools of one page-operation launch (their bases are kernel arguments)
+
+struct TreeArgs {
+  const void *q;            // [T][Hq][hd] bf16 (rotated)
+  const void *pool;         // [P][2][Hkv][16][hd]
+  void *o;                  // [T][Hq hd] bf16
+  const int32_t *qo_indptr, *kv_len, *bt_indptr, *bt, *parent;   // device
+  int n_reqs, T, Hq, Hkv, hd, num_pages;
+  void *workspace;          // tree_workspace_bytes()
+  int *err;
+};
+size_t tree_workspace_bytes();
+cudaError_t tree_attention_run(const TreeArgs &a, cudaStream_t st);
+
+struct VerifyArgs {
+  const void *logits;       // [T][vocab] bf16
+  const int32_t *tokens;    // [T]
+  const float *probs;       // [T][vocab] or null
+  const int32_t *qo_indptr, *parent;
+  const float *temperature, *u_accept, *u_final;
+  int32_t *n_accepted, *path, *next_token;
+  int n_reqs, T, vocab, max_path;
+  int *err;
+};
+cudaError_t verify_tree_run(const VerifyArgs &a, cudaStream_t st);
+
+struct CompactArgs {
+  void *const *pools;       // host array of device pointers
+  int n_pools, num_pages, Hkv, hd, n_reqs, max_path;
+  const int32_t *qo_indptr, *kv_len, *bt_indptr, *bt, *count, *path;
+  int32_t *new_kv_len;
+  int *err;
+};
+cudaError_t kv_compact_run(const CompactArgs &a, cudaStream_t st);
+// src and dst: host page ids (checked by the caller)
+cudaError_t kv_copy_pages_run(void *const *pools, int n_pools, int Hkv, int hd, const int32_t *src, const int32_t *dst,
+                              int n_pairs, cudaStream_t st);
+
 }  // namespace mb
