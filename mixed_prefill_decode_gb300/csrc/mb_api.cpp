@@ -74,21 +74,35 @@ cudaError_t encode_tmap_2d(CUtensorMap *map, const void *base, uint64_t inner, u
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t encode_tmap_5d(CUtensorMap *map, const void *base, const uint64_t dims[5], const uint64_t strides_bytes[4],
-                           const uint32_t box[5]) {
+cudaError_t encode_tmap(CUtensorMap *map, const void *base, int rank, const uint64_t *dims,
+                        const uint64_t *strides_bytes, const uint32_t *box) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
   cuuint64_t d[5], st[4];
   cuuint32_t b[5], estr[5] = {1, 1, 1, 1, 1};
-  for (int i = 0; i < 5; ++i) {
+  for (int i = 0; i < rank; ++i) {
     d[i] = dims[i];
     b[i] = box[i];
   }
-  for (int i = 0; i < 4; ++i) st[i] = strides_bytes[i];
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), d, st, b, estr,
+  for (int i = 0; i + 1 < rank; ++i) st[i] = strides_bytes[i];
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), d, st, b, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// The attention kernels fetch one (page, K or V, head) block of 16 x hd per
+// copy, as a 5-D view: (64 hd elements, 8 slots, hd/64 halves, 2 slot
+// groups, page*2*Hkv + kv*Hkv + head).  In shared memory that lands as
+// [slot group][hd half][8 slots][128 B], 128-byte swizzled: every 8 keys of
+// one hd half form a swizzle atom, and consecutive atoms of a half sit
+// hd/64 KB apart, which the tensor-core descriptors step over uniformly.
+cudaError_t encode_kv_tmap(CUtensorMap *map, const void *base, uint64_t blocks, int hd) {
+  const uint64_t h = hd, nh = h / 64;
+  const uint64_t dims[5] = {64, 8, nh, kPage / 8, blocks};
+  const uint64_t strides[4] = {h * 2, 128, 8 * h * 2, kPage * h * 2};
+  const uint32_t box[5] = {64, 8, static_cast<uint32_t>(nh), kPage / 8, 1};
+  return encode_tmap(map, base, 5, dims, strides, box);
 }
 
 // ------------------------------------------------------ per-device context
@@ -933,17 +947,7 @@ mb_status mb_kv_alloc(mb_layer *L, int32_t num_pages, void *dev_buf, mb_kv **out
     }
     kv->owned = true;
   }
-  // The attention kernels fetch one (page, K or V, head) block of 16 x hd per
-  // copy, as a 5-D view: (64 hd elements, 8 slots, hd/64 halves, 2 slot
-  // groups, page*2*Hkv + kv*Hkv + head).  In shared memory that lands as
-  // [slot group][hd half][8 slots][128 B], 128-byte swizzled: every 8 keys of
-  // one hd half form a swizzle atom, and consecutive atoms of a half sit
-  // hd/64 KB apart, which the tensor-core descriptors step over uniformly.
-  const uint64_t nh = static_cast<uint64_t>(hd) / 64;
-  const uint64_t dims5[5] = {64, 8, nh, MB_PAGE_TOKENS / 8, static_cast<uint64_t>(z)};
-  const uint64_t strides5[4] = {static_cast<uint64_t>(hd) * 2, 128, 8ull * hd * 2, MB_PAGE_TOKENS * hd * 2ull};
-  const uint32_t box5[5] = {64, 8, static_cast<uint32_t>(nh), MB_PAGE_TOKENS / 8, 1};
-  cudaError_t e = mb::encode_tmap_5d(&kv->tmap, kv->base, dims5, strides5, box5);
+  cudaError_t e = mb::encode_kv_tmap(&kv->tmap, kv->base, static_cast<uint64_t>(z), static_cast<int>(hd));
   if (e != cudaSuccess) {
     if (kv->owned) cudaFree(kv->base);
     delete kv;

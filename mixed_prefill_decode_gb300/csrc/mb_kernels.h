@@ -13,8 +13,11 @@ constexpr int kPage = 16;
 // not link libcuda, so it loads on machines without a driver) ----
 cudaError_t encode_tmap_2d(CUtensorMap *map, const void *base, uint64_t inner, uint64_t outer,
                            uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer);
-cudaError_t encode_tmap_5d(CUtensorMap *map, const void *base, const uint64_t dims[5], const uint64_t strides_bytes[4],
-                           const uint32_t box[5]);
+// bf16 tensor of any rank up to 5, 128-byte swizzle (strides[i]: of dimension i + 1)
+cudaError_t encode_tmap(CUtensorMap *map, const void *base, int rank, const uint64_t *dims,
+                        const uint64_t *strides_bytes, const uint32_t *box);
+// The KV pool's map: one (page, K/V, head) block of 16 x hd per copy, blocks = pages * 2 * Hkv
+cudaError_t encode_kv_tmap(CUtensorMap *map, const void *base, uint64_t blocks, int hd);
 int device_sm_count();
 
 // ---- token-batched GEMM on tcgen05 ----

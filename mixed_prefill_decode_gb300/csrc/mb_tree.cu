@@ -9,12 +9,45 @@
 //   o_i = sum_j p_ij v_j,   p_i = softmax_j (q_i . k_j / sqrt(hd)),
 //   j in {0 .. c - 1} + {c + a : a an ancestor of i, or i}
 //
-// for every q-head; q-head h reads KV head h / (Hq / Hkv).
+// for every q-head; q-head h reads KV head h / G, G = Hq / Hkv.
+//
+// What bounds it: every key and value of the prefix is read once for all
+// nodes and heads that share it, 4 hd bytes per key and KV head, against
+// 4 hd n G operations: n G operations a byte.  The ratio of the measured
+// tensor and copy rates is 285, so trees of up to about 285 / G nodes are
+// bound by HBM and larger ones by the tensor cores and the softmax.
+//
+// Layout of the work.  The rows that share a KV head, (node, q-head of the
+// group), row = node G + g, are the M side of the products: 128 / G nodes make
+// a query tile of up to 128 rows, loaded by one 3-D copy per 64 columns.  A
+// unit is one or two query tiles of a (request, KV head) and all of its
+// 128-key blocks, staged once for both tiles:
+//
+//   S = Q K^T        tcgen05, M = 128 rows, N = 128 keys, K = hd, in TMEM
+//   softmax          one thread per row: its maximum and sum need no exchange
+//   O += P V         P (bf16, written over S) is the A operand from TMEM, V the
+//                    MN-major B operand straight from its stage
+//
+// S has two buffers: with two tiles they take turns (one tile's products run
+// during the other's softmax), with one tile its even and odd blocks do.
+//
+// Schedule.  All units of the batch lie on one line, weighted by their blocks
+// (and a constant per unit); CTA w of W takes the w-th of W equal parts, so
+// every SM streams the same amount whatever the lengths, and a unit cut by a
+// border is computed in pieces: fp32 partials (o, m, l) in the workspace, two
+// slots per CTA, merged by log-sum-exp in a second small kernel.  Every CTA
+// works the parts out by itself from the device descriptor (a scan over the
+// requests), so nothing is planned on the host and a captured call follows
+// new contents.  The merge is a kernel of its own rather than the work of a
+// tile's last CTA: one CTA would have to read up to 152 partials of 256 rows
+// alone, and waiting for one another would tie the CTAs of concurrent calls.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "mb_kernels.h"
 #include "mb_launch.cuh"
@@ -26,135 +59,883 @@ namespace {
 using namespace dev;
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kMaxTreeCtas = 160;   // CTAs of a launch at most (one per SM); sizes the workspace
+constexpr int kRecBytes = 8192;     // workspace: one record of 8 ints per CTA, then the partials
+// The schedule's weights: a block of one query tile, a block of two, a unit's
+// start and end, and the least a CTA takes.
+constexpr int kCost1 = 2, kCost2 = 3, kCostUnit = 3, kMinShare = 8;
 
 struct TreeParams {
-  const __nv_bfloat16 *q, *pool;
   __nv_bfloat16 *o;
+  const __nv_bfloat16 *q, *pool;
   const int32_t *qo_indptr, *kv_len, *bt_indptr, *bt, *parent;
-  int n_reqs, T, Hq, Hkv, num_pages;
+  int n_reqs, T, Hq, Hkv, G, num_pages;
   float scale_log2;
+  int32_t *rec;
+  float *part;   // [2 slots per CTA][256 rows][hd + 4]: o, m, l, pad
   int *err;
 };
 
-// One CTA per (token, KV head); each warp takes every fourth key.
 template <int HD>
-__global__ void __launch_bounds__(128) tree_simple_kernel(const TreeParams p) {
-  constexpr int PER = HD / 32;
-  __shared__ uint32_t sees[kMaxTreeNodes / 32];
-  __shared__ float s_m[4][8], s_l[4][8], s_o[4][8][HD];
-  pdl_wait();
-  pdl_trigger();
-  const int t = blockIdx.x, hk = blockIdx.y;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = p.Hq / p.Hkv;
-  int lo = 0, hi = p.n_reqs;   // the request r with qo[r] <= t < qo[r + 1]
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (p.qo_indptr[mid + 1] <= t) lo = mid + 1;
-    else hi = mid;
+struct TreeCfg {
+  static constexpr int NH = HD / 64;
+  static constexpr int TILE_BYTES = 128 * 128;       // [128 rows][64 bf16]
+  static constexpr int QT_BYTES = NH * TILE_BYTES;
+  static constexpr int KV_BYTES = NH * TILE_BYTES;   // a block of K or of V, as [8-key group][hd half][8 keys][128 B]
+  static constexpr int ATOM_STRIDE = NH * 1024;
+  static constexpr int PAGE_BYTES = 2 * ATOM_STRIDE;
+  // K runs one block ahead of V (S comes before P V).
+  static constexpr int NK = HD == 128 ? 3 : 6;
+  static constexpr int NV = HD == 128 ? 2 : 5;
+  static constexpr int NSEG = 4;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = OFF_Q + 2 * QT_BYTES;
+  static constexpr int OFF_V = OFF_K + NK * KV_BYTES;
+  static constexpr int OFF_CTRL = OFF_V + NV * KV_BYTES;
+  static constexpr int SMEM = OFF_CTRL + 2048;
+  static constexpr int THREADS = 320;                // TMA, MMA, 2 x 4 softmax warps
+  static constexpr uint32_t IDESC_S = idesc_bf16(128, 128, false);
+  static constexpr uint32_t IDESC_PV = idesc_bf16(128, HD, true);
+  static constexpr uint32_t TMEM_COLS = 512;         // S/P buffers at 0 and 128, O of the two tiles from 256
+  static constexpr uint32_t O_COL = 256;
+};
+
+// A piece of a unit, as the producer tells it to the other roles.
+struct Seg {
+  int32_t nb;         // blocks [j0, j0 + nb); 0: no more pieces
+  int32_t j0, qt;     // first block, query tiles
+  int32_t t0, i0;     // the request's first row, the unit's first node
+  int32_t hk, c, kv;
+  int32_t nodes;      // of the unit
+  int32_t slot;       // partial slot, -1: the unit is whole
+  int32_t qb;         // Q buffer of tile 0 (tile 1: the other one)
+  int32_t b0;         // the request's first block table entry
+  uint32_t odd[4];    // nodes whose V row holds an infinity or a NaN (set by the softmax)
+  uint8_t parent[kMaxTreeNodes];   // 0xFF: none
+};
+
+template <int HD>
+struct Ctrl {
+  using C = TreeCfg<HD>;
+  uint64_t q_full[2], q_empty[2];
+  uint64_t k_full[C::NK], k_empty[C::NK], v_full[C::NV], v_empty[C::NV];
+  // S and P V products are done: by query tile, then by the tile's items in
+  // turn.  (Two products of a tile can be done before its warps look: the
+  // second barrier keeps their phases apart.  A third waits for the first's P.)
+  uint64_t s_full[2][2], o_full[2][2];
+  uint64_t p_full[2];              // by S buffer
+  uint64_t seg_full[C::NSEG], seg_empty[C::NSEG];
+  uint64_t done;
+  Seg seg[C::NSEG];
+  int64_t wsum[C::THREADS / 32];
+  int64_t start_base;
+  int32_t start_req;
+  uint32_t tmem;
+  int abort;
+};
+
+// What the schedule needs to know of a request.
+struct Req {
+  int t0, n, kv, b0, nkb;
+  int full, rem;   // units of 2 NT nodes, and the nodes of the last one if it is smaller
+  int64_t head;    // cost of one KV head
+};
+
+// (an invalid request costs nothing: it is skipped and reported)
+__device__ __forceinline__ Req load_req(const TreeParams &p, int r, bool *bad) {
+  Req q;
+  q.t0 = p.qo_indptr[r];
+  q.n = p.qo_indptr[r + 1] - q.t0;
+  q.kv = p.kv_len[r];
+  q.b0 = p.bt_indptr[r];
+  const int pages = p.bt_indptr[r + 1] - q.b0;
+  *bad = q.t0 < 0 || q.n < 0 || q.n > kMaxTreeNodes || q.t0 + q.n > p.T || q.kv < q.n || q.kv > (1 << 24) || q.b0 < 0 ||
+         (q.kv + kPage - 1) / kPage > pages;
+  if (*bad) q.n = 0;
+  q.nkb = (q.kv + 127) / 128;
+  const int nt2 = 2 * (128 / p.G);
+  q.full = q.n / nt2;
+  q.rem = q.n % nt2;
+  q.head = static_cast<int64_t>(q.full) * (kCostUnit + kCost2 * static_cast<int64_t>(q.nkb));
+  if (q.rem) q.head += kCostUnit + (2 * q.rem > nt2 ? kCost2 : kCost1) * static_cast<int64_t>(q.nkb);
+  if (q.n == 0) q.head = 0;
+  return q;
+}
+
+__device__ __forceinline__ float max3f(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// p = 2^(s scale + negm) of 64 logits, as bf16 pairs, added into `sum`.
+__device__ __forceinline__ void probs64(const float (&sv)[64], float2 sc2, float negm, uint32_t (&pk)[32], float2 &sum) {
+  const float2 nm = make_float2(negm, negm);
+#pragma unroll
+  for (int c = 0; c < 64; c += 2) {
+    const float2 x = __ffma2_rn(make_float2(sv[c], sv[c + 1]), sc2, nm);
+    const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+    sum = __fadd2_rn(sum, make_float2(p0, p1));
+    pk[c / 2] = pack_bf16x2(p0, p1);
   }
-  if (lo == p.n_reqs) return;   // a row behind the last request
-  const int r = lo, t0 = p.qo_indptr[r], n = p.qo_indptr[r + 1] - t0, kv = p.kv_len[r], c = kv - n;
-  const int pages = p.bt_indptr[r + 1] - p.bt_indptr[r];
-  if (n > kMaxTreeNodes || t0 < 0 || t0 + n > p.T || c < 0 || (kv + 15) / 16 > pages || p.bt_indptr[r] < 0) {
-    if (threadIdx.x == 0) atomicExch(p.err, kErrBounds);
+}
+
+template <int HD>
+__global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
+    tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmKV,
+                const __grid_constant__ TreeParams p) {
+  using C = TreeCfg<HD>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t *sQ = smem + C::OFF_Q;
+  uint8_t *sK = smem + C::OFF_K;
+  uint8_t *sV = smem + C::OFF_V;
+  static_assert(sizeof(Ctrl<HD>) <= 2048, "control area");
+  Ctrl<HD> &ct = *reinterpret_cast<Ctrl<HD> *>(smem + C::OFF_CTRL);
+  volatile int *abort_flag = &ct.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (smem_u32(smem) & 1023u) {   // the swizzled layouts need a 1024-aligned base
+    pdl_wait();
+    if (threadIdx.x == 0) {
+      atomicExch(p.err, kErrBounds);
+      p.rec[blockIdx.x * 8] = 0;
+    }
     return;
   }
-  const int32_t *table = p.bt + p.bt_indptr[r];
-  const int i = t - t0;
-  if (threadIdx.x < kMaxTreeNodes / 32) sees[threadIdx.x] = 0;
-  __syncthreads();
   if (threadIdx.x == 0) {
-    int x = i;
-    while (x >= 0) {
-      sees[x >> 5] |= 1u << (x & 31);
-      int up = p.parent[t0 + x];
-      if (up < -1 || up >= x) {
-        atomicExch(p.err, kErrBounds);
-        up = -1;
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&ct.q_full[b], 1);
+      mbar_init(&ct.q_empty[b], 1);
+      mbar_init(&ct.s_full[b][0], 1);
+      mbar_init(&ct.s_full[b][1], 1);
+      mbar_init(&ct.p_full[b], 128);
+      mbar_init(&ct.o_full[b][0], 1);
+      mbar_init(&ct.o_full[b][1], 1);
+    }
+    for (int s = 0; s < C::NK; ++s) {
+      mbar_init(&ct.k_full[s], 1);
+      mbar_init(&ct.k_empty[s], 1);
+    }
+    for (int s = 0; s < C::NV; ++s) {
+      mbar_init(&ct.v_full[s], 1);
+      mbar_init(&ct.v_empty[s], 1);
+    }
+    for (int s = 0; s < C::NSEG; ++s) {
+      mbar_init(&ct.seg_full[s], 1);
+      mbar_init(&ct.seg_empty[s], 9);   // the MMA issuer and the 8 softmax warps
+    }
+    mbar_init(&ct.done, 1);
+    ct.abort = 0;
+    ct.start_req = -1;
+    fence_mbar_init();
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmKV);
+  }
+  if (warp == 1) {
+    tmem_alloc(&ct.tmem, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  pdl_wait();   // the descriptor, q, the pool and o belong to earlier kernels of the stream
+  pdl_trigger();
+
+  // ---- this CTA's part of the line: [x0, x1) of `total`
+  const int W_max = gridDim.x, cta = blockIdx.x;
+  const int per = (p.n_reqs + C::THREADS - 1) / C::THREADS;
+  const int r_lo = min(p.n_reqs, static_cast<int>(threadIdx.x) * per), r_hi = min(p.n_reqs, r_lo + per);
+  int64_t mine = 0;
+  for (int r = r_lo; r < r_hi; ++r) {
+    bool bad;
+    mine += load_req(p, r, &bad).head * p.Hkv;
+    if (bad && cta == 0) atomicExch(p.err, kErrBounds);
+  }
+  int64_t inc = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, inc, off);
+    if (lane >= off) inc += v;
+  }
+  if (lane == 31) ct.wsum[warp] = inc;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ct.tmem;
+  int64_t total = 0, pre = inc - mine;
+#pragma unroll
+  for (int w = 0; w < C::THREADS / 32; ++w) {
+    if (w < warp) pre += ct.wsum[w];
+    total += ct.wsum[w];
+  }
+  const int64_t W = total / kMinShare < 1 ? (total > 0 ? 1 : 0) : (total / kMinShare < W_max ? total / kMinShare : W_max);
+  const bool active = cta < W;
+  const int64_t x0 = active ? total * cta / W : 0, x1 = active ? total * (cta + 1) / W : 0;
+  if (active && pre <= x0 && x0 < pre + mine) {
+    for (int r = r_lo; r < r_hi; ++r) {
+      bool bad;
+      const int64_t c = load_req(p, r, &bad).head * p.Hkv;
+      if (x0 < pre + c) {
+        ct.start_req = r;
+        ct.start_base = pre;
+        break;
       }
-      x = up;
+      pre += c;
     }
   }
   __syncthreads();
-  float q[8][PER], o[8][PER], m[8], l[8];
+
+  if (!active) {
+    if (threadIdx.x == 0) p.rec[cta * 8] = 0;
+  } else if (warp == 0) {
+    // ------------------------------------------------ schedule, TMA producer
+    // The whole warp: lane 0 waits and arms each stage, a block's 8 pages go
+    // out as one copy per lane.  The K of a block goes out before the V of
+    // the block before it; the page ids of the next block are loaded a block
+    // ahead, the next request's descriptor when its predecessor starts.
+    const int G = p.G, NT = 128 / G;
+    int32_t rec[5] = {0, 0, 0, 0, 0};
+    int r = ct.start_req;
+    int64_t base = ct.start_base;
+    bool bad;
+    Req q = load_req(p, r, &bad);
+    Req nx{};
+    if (r + 1 < p.n_reqs) nx = load_req(p, r + 1, &bad);
+    // the unit that x0 lies in
+    int64_t off = x0 - base;
+    int hk = static_cast<int>(off / q.head);
+    base += hk * q.head;
+    off -= hk * q.head;
+    const int64_t big0 = kCostUnit + kCost2 * static_cast<int64_t>(q.nkb);
+    int u = static_cast<int>(min(static_cast<int64_t>(q.full), off / big0));
+    base += u * big0;
+    int kcnt = 0, vcnt = 0, nseg = 0, quse[2] = {0, 0}, qsel = 0;
+    bool ok = true;
+    // the block whose V is still to be sent
+    int pv_np = 0, pv_page = 0, pv_hk = 0;
+    bool pv_have = false;
+    auto send = [&](bool is_v, int np, int page, int h) -> bool {
+      const int ns = is_v ? C::NV : C::NK;
+      int &cnt = is_v ? vcnt : kcnt;
+      const int st = cnt % ns;
+      uint64_t *full = (is_v ? ct.v_full : ct.k_full) + st;
+      uint64_t *empty = (is_v ? ct.v_empty : ct.k_empty) + st;
+      bool good = true;
+      if (lane == 0) {
+        good = mbar_wait(empty, ((cnt / ns) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer);
+        if (good) mbar_arrive_expect_tx(full, np * C::NH * 2048);
+      }
+      good = __shfl_sync(0xffffffffu, good, 0);
+      if (!good) return false;
+      if (lane < np)
+        tma_load_5d((is_v ? sV : sK) + st * C::KV_BYTES + lane * C::PAGE_BYTES, &tmKV, full, 0, 0, 0, 0,
+                    (page * 2 + (is_v ? 1 : 0)) * p.Hkv + h);
+      ++cnt;
+      return true;
+    };
+    while (ok && base < x1) {
+      // the unit (hk, u) of request r, on the line from `base`
+      const int nodes = u < q.full ? 2 * NT : q.rem;
+      const int qt = nodes > NT ? 2 : 1;
+      const int b = qt == 2 ? kCost2 : kCost1;
+      const int64_t cost = kCostUnit + static_cast<int64_t>(b) * q.nkb;
+      auto cut = [&](int64_t x) {   // blocks of the unit that lie before x
+        const int64_t d = x - base - kCostUnit;
+        return d <= 0 ? 0 : static_cast<int>(min(static_cast<int64_t>(q.nkb), (d + b - 1) / b));
+      };
+      auto owner = [&](int j) {     // the CTA whose part holds block j: the last w with total w / W <= its place
+        return static_cast<int>(((base + kCostUnit + static_cast<int64_t>(b) * j + 1) * W - 1) / total);
+      };
+      const int j0 = cut(x0), j1 = cut(x1);
+      if (j1 > j0) {
+        const int first = owner(0), last = owner(q.nkb - 1);
+        const int i0 = u * 2 * NT;
+        const int32_t *table = p.bt + q.b0;
+        const int n_pages = (q.kv + kPage - 1) / kPage;
+        auto page_of = [&](int blk) {
+          int pg = lane < 8 && 8 * blk + lane < n_pages ? table[8 * blk + lane] : 0;
+          if (pg < 0 || pg >= p.num_pages) {
+            atomicExch(p.err, kErrBounds);
+            pg = 0;
+          }
+          return pg;
+        };
+        int cur = page_of(j0), nxt = j0 + 1 < j1 ? page_of(j0 + 1) : 0;
+        const bool tail = 128 * j1 > q.kv - q.n;   // some of the piece's keys are nodes
+        int32_t par[4] = {-1, -1, -1, -1};
+        if (tail)
 #pragma unroll
-  for (int g = 0; g < 8; ++g) {
-    m[g] = -INFINITY;
-    l[g] = 0.f;
+          for (int k = 0; k < 4; ++k)
+            if (lane + 32 * k < q.n) par[k] = p.parent[q.t0 + lane + 32 * k];
+        // what is left of the piece before
+        if (pv_have) ok = send(true, pv_np, pv_page, pv_hk);
+        pv_have = false;
+        // tell the other roles
+        const int ss = nseg % C::NSEG;
+        if (ok) {
+          if (lane == 0) ok = mbar_wait(&ct.seg_empty[ss], ((nseg / C::NSEG) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer);
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+        if (!ok) break;
+        Seg &sg = ct.seg[ss];
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-      o[g][k] = 0.f;
-      q[g][k] = g < G ? __bfloat162float(p.q[(static_cast<size_t>(t) * p.Hq + hk * G + g) * HD + lane + 32 * k]) : 0.f;
+        for (int k = 0; k < 4; ++k) {
+          const int i = lane + 32 * k;
+          if (i < q.n && tail) {
+            if (par[k] < -1 || par[k] >= i) {
+              atomicExch(p.err, kErrBounds);
+              par[k] = -1;
+            }
+            sg.parent[i] = static_cast<uint8_t>(par[k]);
+          }
+        }
+        if (lane < 4) sg.odd[lane] = 0;
+        if (lane == 0) {
+          sg.nb = j1 - j0;
+          sg.j0 = j0;
+          sg.qt = qt;
+          sg.t0 = q.t0;
+          sg.i0 = i0;
+          sg.hk = hk;
+          sg.c = q.kv - q.n;
+          sg.kv = q.kv;
+          sg.nodes = nodes;
+          sg.slot = first == last ? -1 : 2 * cta + (cta == first ? 1 : 0);
+          sg.qb = qsel;
+          sg.b0 = q.b0;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ct.seg_full[ss]);
+        ++nseg;
+        if (first != last && cta == first) {
+          rec[0] = last - first + 1;
+          rec[1] = q.t0;
+          rec[2] = i0;
+          rec[3] = hk;
+          rec[4] = nodes * G;
+        }
+        // the query tiles
+        if (lane == 0)
+          for (int t = 0; t < qt && ok; ++t) {
+            const int qb = qsel ^ t;
+            ok = mbar_wait(&ct.q_empty[qb], (quse[qb] & 1) ^ 1, abort_flag, p.err, kErrWaitProducer);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&ct.q_full[qb], C::NH * G * NT * 128);
+            for (int ch = 0; ch < C::NH; ++ch)
+              tma_load_3d(sQ + qb * C::QT_BYTES + ch * C::TILE_BYTES, &tmQ, &ct.q_full[qb], ch * 64, hk * G,
+                          q.t0 + i0 + t * NT);
+          }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        for (int t = 0; t < qt; ++t) ++quse[qsel ^ t];
+        if (qt == 1) qsel ^= 1;
+        for (int j = j0; j < j1 && ok; ++j) {
+          const int np = min(8, n_pages - 8 * j);
+          const int after = j + 2 < j1 ? page_of(j + 2) : 0;
+          ok = send(false, np, cur, hk);
+          if (ok && pv_have) ok = send(true, pv_np, pv_page, pv_hk);
+          pv_np = np;
+          pv_page = cur;
+          pv_hk = hk;
+          pv_have = true;
+          cur = nxt;
+          nxt = after;
+        }
+      }
+      // the next unit on the line
+      base += cost;
+      if (++u == q.full + (q.rem ? 1 : 0)) {
+        u = 0;
+        if (++hk == p.Hkv) {
+          hk = 0;
+          do {
+            ++r;
+            if (r >= p.n_reqs) break;
+            q = nx;
+            if (r + 1 < p.n_reqs) nx = load_req(p, r + 1, &bad);
+          } while (q.n == 0);
+          if (r >= p.n_reqs) break;
+        }
+      }
     }
-  }
-  for (int j = warp; j < kv; j += 4) {
-    if (j >= c && !((sees[(j - c) >> 5] >> ((j - c) & 31)) & 1u)) continue;
-    const int page = table[j / kPage];
-    if (page < 0 || page >= p.num_pages) {
-      if (lane == 0) atomicExch(p.err, kErrBounds);
-      continue;
-    }
-    const __nv_bfloat16 *kr = p.pool + ((static_cast<size_t>(page) * 2 * p.Hkv + hk) * kPage + j % kPage) * HD;
-    const __nv_bfloat16 *vr = kr + static_cast<size_t>(p.Hkv) * kPage * HD;
-    float kx[PER], vx[PER];
-#pragma unroll
-    for (int k = 0; k < PER; ++k) {
-      kx[k] = __bfloat162float(kr[lane + 32 * k]);
-      vx[k] = __bfloat162float(vr[lane + 32 * k]);
-    }
-#pragma unroll
-    for (int g = 0; g < 8; ++g) {
-      if (g >= G) break;
-      float s = 0.f;
-#pragma unroll
-      for (int k = 0; k < PER; ++k) s = fmaf(q[g][k], kx[k], s);
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-      s *= p.scale_log2;
-      const float mn = fmaxf(m[g], s);
-      const float al = ex2_approx(m[g] - mn), pr = ex2_approx(s - mn);
-      m[g] = mn;
-      l[g] = fmaf(l[g], al, pr);
-#pragma unroll
-      for (int k = 0; k < PER; ++k) o[g][k] = fmaf(o[g][k], al, pr * vx[k]);
-    }
-  }
-#pragma unroll
-  for (int g = 0; g < 8; ++g) {
-    if (g >= G) break;
+    if (ok && pv_have) ok = send(true, pv_np, pv_page, pv_hk);
     if (lane == 0) {
-      s_m[warp][g] = m[g];
-      s_l[warp][g] = l[g];
+      if (ok) {
+        const int ss = nseg % C::NSEG;
+        if (mbar_wait(&ct.seg_empty[ss], ((nseg / C::NSEG) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer)) {
+          ct.seg[ss].nb = 0;
+          mbar_arrive(&ct.seg_full[ss]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 5; ++k) p.rec[cta * 8 + k] = rec[k];
+      // after an abort, let copies in flight land before the CTA exits (bounded)
+      if (!ok || *abort_flag) {
+        const uint64_t t_start = globaltimer();
+        auto drain = [&](uint64_t *bar, int use) {
+          while (!mbar_try_wait(smem_u32(bar), use & 1) && globaltimer() - t_start < kWaitLimitNs) {
+          }
+        };
+        for (int i = max(0, kcnt - C::NK); i < kcnt; ++i) drain(&ct.k_full[i % C::NK], i / C::NK);
+        for (int i = max(0, vcnt - C::NV); i < vcnt; ++i) drain(&ct.v_full[i % C::NV], i / C::NV);
+        for (int b = 0; b < 2; ++b)
+          if (quse[b] > 0) drain(&ct.q_full[b], quse[b] - 1);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ------------------------------------------------------- MMA issuer
+      // Items in order: block by block, tile by tile.  S of an item goes out
+      // as soon as its K (and Q) landed and the P V before the last one is
+      // issued (its S buffer is then free, in order); P V as soon as P is
+      // written and V landed.  S runs on into the next piece.
+      const uint64_t qd0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t kd0 = sdesc_sw128(smem_u32(sK), 16, C::ATOM_STRIDE);
+      const uint64_t vd0 = sdesc_sw128(smem_u32(sV), 1024, C::ATOM_STRIDE);
+      struct Cursor {
+        int seg, blk, item;      // pieces, blocks and items before it
+        int nb, qt, qb, lb, t;   // the piece, and the place in it
+        bool in;
+      };
+      Cursor s{0, 0, 0, 0, 0, 0, 0, 0, false}, v{0, 0, 0, 0, 0, 0, 0, 0, false};
+      int quse[2] = {0, 0}, n_s[2] = {0, 0}, n_o[2] = {0, 0};   // Q buffers used up; S and P V products of each tile
+      bool s_end = false;
+      uint64_t t_idle = globaltimer();
+      auto enter = [&](Cursor &x) {
+        const Seg &sg = ct.seg[x.seg % C::NSEG];
+        x.nb = sg.nb;
+        x.qt = sg.qt;
+        x.qb = sg.qb;
+        x.lb = x.t = 0;
+        x.in = true;
+      };
+      for (uint32_t spin = 0;; ++spin) {
+        bool progress = false;
+        if (!s_end && s.item < v.item + 2) {
+          if (!s.in && mbar_test_wait(smem_u32(&ct.seg_full[s.seg % C::NSEG]), (s.seg / C::NSEG) & 1)) {
+            enter(s);
+            if (s.nb == 0) s_end = true;
+          }
+          if (s.in && !s_end) {
+            const int qb = s.qb ^ s.t, st = s.blk % C::NK;
+            if ((s.lb > 0 || mbar_test_wait(smem_u32(&ct.q_full[qb]), quse[qb] & 1)) &&
+                mbar_test_wait(smem_u32(&ct.k_full[st]), (s.blk / C::NK) & 1)) {
+              tc_fence_after();
+              const uint32_t d = tmem + 128 * (s.item & 1);
+              const uint64_t qd = qd0 + static_cast<uint64_t>((qb * C::QT_BYTES) >> 4);
+              const uint64_t kd = kd0 + static_cast<uint64_t>((st * C::KV_BYTES) >> 4);
+#pragma unroll
+              for (int ch = 0; ch < C::NH; ++ch)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  mma_bf16(d, qd + ((ch * C::TILE_BYTES + kk * 32) >> 4), kd + ((ch * 1024 + kk * 32) >> 4), C::IDESC_S,
+                           (ch > 0 || kk > 0) ? 1u : 0u);
+              mma_commit(&ct.s_full[s.t][n_s[s.t]++ & 1]);
+              if (s.lb == s.nb - 1) {
+                mma_commit(&ct.q_empty[qb]);
+                ++quse[qb];
+              }
+              ++s.item;
+              if (++s.t == s.qt) {
+                mma_commit(&ct.k_empty[st]);
+                s.t = 0;
+                ++s.blk;
+                if (++s.lb == s.nb) {
+                  s.in = false;
+                  ++s.seg;
+                }
+              }
+              progress = true;
+            }
+          }
+        }
+        if (v.item < s.item) {
+          if (!v.in) enter(v);   // S of the piece is out: its record is there
+          const int st = v.blk % C::NV;
+          if (mbar_test_wait(smem_u32(&ct.p_full[v.item & 1]), (v.item >> 1) & 1) &&
+              mbar_test_wait(smem_u32(&ct.v_full[st]), (v.blk / C::NV) & 1)) {
+            tc_fence_after();
+            const uint64_t vd = vd0 + static_cast<uint64_t>((st * C::KV_BYTES) >> 4);
+            const uint32_t pcol = tmem + 128 * (v.item & 1);
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)   // 16 keys (two atoms) per MMA; hd halves 1 KB apart
+              mma_bf16_ts(tmem + C::O_COL + HD * v.t, pcol + ks * 8, vd + ((ks * 2 * C::ATOM_STRIDE) >> 4), C::IDESC_PV,
+                          (v.lb > 0 || ks > 0) ? 1u : 0u);
+            mma_commit(&ct.o_full[v.t][n_o[v.t]++ & 1]);
+            ++v.item;
+            if (++v.t == v.qt) {
+              mma_commit(&ct.v_empty[st]);
+              v.t = 0;
+              ++v.blk;
+              if (++v.lb == v.nb) {
+                v.in = false;
+                mbar_arrive(&ct.seg_empty[v.seg % C::NSEG]);
+                ++v.seg;
+              }
+            }
+            progress = true;
+          }
+        }
+        if (s_end && v.item == s.item) break;
+        if (progress) {
+          t_idle = globaltimer();
+        } else if ((spin & 15u) == 15u) {
+          if (*abort_flag) break;
+          if (globaltimer() - t_idle > kWaitLimitNs) {
+            *abort_flag = 1;
+            atomicExch(p.err, kErrWaitMma);
+            break;
+          }
+        }
+      }
+      // every MMA issued above has completed before TMEM is freed
+      mma_commit(&ct.done);
+      const uint64_t t_end = globaltimer();
+      while (!mbar_try_wait(smem_u32(&ct.done), 0) && globaltimer() - t_end < kWaitLimitNs) {
+      }
+    }
+  } else {
+    // ------------------------------------------------- softmax / epilogue
+    const int t = (warp - 2) >> 2;          // query tile of this warp group
+    const int qu = warp & 3;                // TMEM lane quarter
+    const int row = qu * 32 + lane;         // row of the tile; also the key of a block it looks after
+    const uint32_t lane_base = static_cast<uint32_t>(qu * 32) << 16;
+    const uint32_t o_col = tmem + lane_base + C::O_COL + HD * t;
+    constexpr float kRescaleAbove = 8.f;    // log2 units
+    const float scale = p.scale_log2;
+    const float2 sc2 = make_float2(scale, scale);
+    const int G = p.G, NT = 128 / G;
+    int nseg = 0, item0 = 0, blk0 = 0, pv0 = 0;
+    bool ok = true;
+    while (true) {
+      const int ss = nseg % C::NSEG;
+      bool fail = !mbar_wait(&ct.seg_full[ss], (nseg / C::NSEG) & 1, abort_flag, p.err, kErrWaitSoftmax);
+      if (__any_sync(0xffffffffu, fail)) break;   // tcgen05.ld below is warp-collective
+      Seg &sg = ct.seg[ss];
+      const int nb = sg.nb;
+      if (nb == 0) break;
+      const int qt = sg.qt, j0 = sg.j0, c = sg.c, kv = sg.kv;
+      const int rows = (t == 0 ? min(sg.nodes, NT) : sg.nodes - NT) * G;   // <= 0: no such tile
+      if (t >= qt) {
+        item0 += nb;
+        blk0 += nb;
+        ++nseg;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ct.seg_empty[ss]);
+        continue;
+      }
+      const bool idle = qu * 32 >= rows;     // no rows for this warp (it still looks after keys)
+      const int node = sg.i0 + t * NT + row / G;
+      // the nodes that this row's node sees
+      uint32_t see[4] = {0, 0, 0, 0};
+      if (row < rows && 128 * (j0 + nb) > c)
+        for (uint32_t x = node; x != 0xFF;) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (static_cast<int>(x >> 5) == k) see[k] |= 1u << (x & 31);
+          x = sg.parent[x];
+        }
+      float m_ref = -INFINITY, l = 0.f;
+      for (int lb = 0; lb < nb; ++lb) {
+        const int item = item0 + lb * qt + t, sb = item & 1;
+        const uint32_t s_col = tmem + lane_base + 128 * sb;
+        const int j = j0 + lb, key0 = 128 * j;
+        const int mine_n = pv0 + lb;         // this tile's items before it
+        fail = !mbar_wait(&ct.s_full[t][mine_n & 1], (mine_n >> 1) & 1, abort_flag, p.err, kErrWaitSoftmax);
+        if (__any_sync(0xffffffffu, fail)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const bool full = key0 + 128 <= c;   // only prefix keys: visible to every row
+        if (!idle) {
+          // which keys of the block this row sees
+          uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
+          if (!full) {
+            const int d = key0 - c;          // node index of the block's first key
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int f = d + 32 * k;      // node index of this word's first key
+              uint32_t w = 0;
+              if (f <= -32) {
+                w = ~0u;
+              } else {
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {
+                  const int sh = 32 * a - f;   // word a of `see` starts at this bit of the word
+                  if (sh >= 0 && sh < 32) w |= see[a] << sh;
+                  if (sh < 0 && sh > -32) w |= see[a] >> -sh;
+                }
+                if (f < 0) w |= (1u << -f) - 1u;
+              }
+              vis[k] = w;
+            }
+          }
+          // One pass over S while the row's reference maximum holds; if a row
+          // of the warp rose more than 2^8 above it (always at the piece's
+          // first block), the reference moves, O is rescaled and the
+          // probabilities are taken again from S, intact until P is stored.
+          uint32_t pk_lo[32], pk_hi[32];
+          float2 lsum = make_float2(0.f, 0.f);
+          float mq0 = -INFINITY, mq1 = -INFINITY, mq2 = -INFINITY, mq3 = -INFINITY;
+          const bool have_ref = lb > 0;
+          float negm = m_ref == -INFINITY ? 0.f : -m_ref;
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            float sv[64];
+            tmem_ld64(s_col + 64 * hh, sv);
+            if (!full)
+#pragma unroll
+              for (int e = 0; e < 64; ++e)
+                if (!((vis[2 * hh + (e >> 5)] >> (e & 31)) & 1u)) sv[e] = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 64; e += 8) {
+              mq0 = max3f(mq0, sv[e], sv[e + 1]);
+              mq1 = max3f(mq1, sv[e + 2], sv[e + 3]);
+              mq2 = max3f(mq2, sv[e + 4], sv[e + 5]);
+              mq3 = max3f(mq3, sv[e + 6], sv[e + 7]);
+            }
+            if (have_ref) probs64(sv, sc2, negm, hh ? pk_hi : pk_lo, lsum);
+          }
+          const float mx = fmaxf(fmaxf(mq0, mq1), fmaxf(mq2, mq3)) * scale;
+          const bool grow = !have_ref || mx > m_ref + kRescaleAbove;
+          if (__any_sync(0xffffffffu, grow)) {
+            if (lb > 0) {
+              // O holds the blocks before: their P V must be done
+              const int prev_n = mine_n - 1;
+              fail = !mbar_wait(&ct.o_full[t][prev_n & 1], (prev_n >> 1) & 1, abort_flag, p.err, kErrWaitSoftmax);
+              if (__any_sync(0xffffffffu, fail)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const float alpha = grow ? ex2_approx(m_ref - mx) : 1.f;
+#pragma unroll
+              for (int cc = 0; cc < HD / 32; ++cc) {
+                float v[32];
+                tmem_ld32(o_col + cc * 32, v);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[k] *= alpha;
+                tmem_st32(o_col + cc * 32, v);
+              }
+              if (grow) l *= alpha;
+            }
+            if (grow) m_ref = mx;
+            negm = m_ref == -INFINITY ? 0.f : -m_ref;   // a row that has seen nothing yet
+            lsum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              float sv[64];
+              tmem_ld64(s_col + 64 * hh, sv);
+              if (!full)
+#pragma unroll
+                for (int e = 0; e < 64; ++e)
+                  if (!((vis[2 * hh + (e >> 5)] >> (e & 31)) & 1u)) sv[e] = -INFINITY;
+              probs64(sv, sc2, negm, hh ? pk_hi : pk_lo, lsum);
+            }
+          }
+          l += lsum.x + lsum.y;
+          // P over S: keys 0-63 in columns 0-31, keys 64-127 in 32-63
+          tmem_st32u(s_col, pk_lo);
+          tmem_st32u(s_col + 32, pk_hi);
+        }
+        if (!full && t == 0) {
+          // Keys that some row does not see: P is 0 there, but 0 times an
+          // infinity or a NaN is not.  V rows past the request's last key hold
+          // anything: zeroed.  A node's V row with a non-finite value is zeroed
+          // too and the node marked; the rows that do see it add its part at the
+          // end.  (Warp group 0 does it, before its P is ready; tile 1's product
+          // with this block is issued after tile 0's.)
+          const int vb = blk0 + lb;
+          fail = !mbar_wait(&ct.v_full[vb % C::NV], (vb / C::NV) & 1, abort_flag, p.err, kErrWaitSoftmax);
+          if (__any_sync(0xffffffffu, fail)) {
+            ok = false;
+            break;
+          }
+          const int key = key0 + row;
+          uint8_t *vrow = sV + (vb % C::NV) * C::KV_BYTES + (row >> 3) * C::ATOM_STRIDE + (row & 7) * 128;
+          bool wipe = key >= kv;
+          if (key >= c && !wipe) {
+            uint32_t special = 0;
+#pragma unroll
+            for (int ch = 0; ch < C::NH; ++ch)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(vrow + ch * 1024 + ((k + lane) & 7) * 16);
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  special |= ((w[e] & 0x7F80u) == 0x7F80u || (w[e] & 0x7F800000u) == 0x7F800000u) ? 1u : 0u;
+              }
+            if (special) {
+              wipe = true;
+              atomicOr(&sg.odd[(key - c) >> 5], 1u << ((key - c) & 31));
+            }
+          }
+          if (wipe) {
+#pragma unroll
+            for (int ch = 0; ch < C::NH; ++ch)
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<uint4 *>(vrow + ch * 1024 + ((k + lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        mbar_arrive(&ct.p_full[sb]);
+      }
+      // ---- the piece is done: its output, or its partial
+      const int last_n = pv0 + nb - 1;
+      fail = !ok || !mbar_wait(&ct.o_full[t][last_n & 1], (last_n >> 1) & 1, abort_flag, p.err, kErrWaitSoftmax);
+      if (__any_sync(0xffffffffu, fail)) break;
+      tc_fence_after();
+      if (!idle) {
+        const bool valid = row < rows;
+        const uint32_t odd[4] = {sg.odd[0] & see[0], sg.odd[1] & see[1], sg.odd[2] & see[2], sg.odd[3] & see[3]};
+        const bool any_odd = valid && (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
+        const int tok = sg.t0 + node, head = sg.hk * G + row % G;
+        // one marked node's part: p v, p from the same logit in fp32
+        auto add_odd = [&](float (&v)[32], int col) {
+          for (int a = 0; a < kMaxTreeNodes; ++a) {
+            if (!((odd[a >> 5] >> (a & 31)) & 1u)) continue;
+            const int pos = c + a;
+            int pg = p.bt[sg.b0 + pos / kPage];
+            if (pg < 0 || pg >= p.num_pages) pg = 0;
+            const __nv_bfloat16 *kr = p.pool + ((static_cast<size_t>(pg) * 2 * p.Hkv + sg.hk) * kPage + pos % kPage) * HD;
+            const __nv_bfloat16 *vr = kr + static_cast<size_t>(p.Hkv) * kPage * HD;
+            const __nv_bfloat16 *qr = p.q + (static_cast<size_t>(tok) * p.Hq + head) * HD;
+            float s = 0.f;
+            for (int k = 0; k < HD; ++k) s = fmaf(__bfloat162float(qr[k]), __bfloat162float(kr[k]), s);
+            const float pr = ex2_approx(fmaf(s, scale, m_ref == -INFINITY ? 0.f : -m_ref));
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = fmaf(pr, __bfloat162float(vr[col + k]), v[k]);
+          }
+        };
+        if (sg.slot < 0) {
+          const float inv = 1.f / l;
+          uint4 *dst = reinterpret_cast<uint4 *>(p.o + (static_cast<size_t>(tok) * p.Hq + head) * HD);
+#pragma unroll
+          for (int cc = 0; cc < HD / 32; ++cc) {
+            float v[32];
+            tmem_ld32(o_col + cc * 32, v);
+            if (any_odd) add_odd(v, cc * 32);
+            if (valid)
+#pragma unroll
+              for (int v8 = 0; v8 < 4; ++v8)
+                dst[cc * 4 + v8] = make_uint4(pack_bf16x2(v[8 * v8] * inv, v[8 * v8 + 1] * inv),
+                                              pack_bf16x2(v[8 * v8 + 2] * inv, v[8 * v8 + 3] * inv),
+                                              pack_bf16x2(v[8 * v8 + 4] * inv, v[8 * v8 + 5] * inv),
+                                              pack_bf16x2(v[8 * v8 + 6] * inv, v[8 * v8 + 7] * inv));
+          }
+        } else {
+          // rows in node order: tile 1's behind tile 0's
+          float *dst = p.part + (static_cast<size_t>(sg.slot) * 256 + t * NT * G + row) * (HD + 4);
+#pragma unroll
+          for (int cc = 0; cc < HD / 32; ++cc) {
+            float v[32];
+            tmem_ld32(o_col + cc * 32, v);
+            if (any_odd) add_odd(v, cc * 32);
+            if (valid)
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                reinterpret_cast<float4 *>(dst + cc * 32)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          }
+          if (valid) {
+            dst[HD] = m_ref;
+            dst[HD + 1] = l;
+          }
+        }
+      }
+      tc_fence_before();
+      item0 += nb * qt;
+      blk0 += nb;
+      pv0 += nb;
+      ++nseg;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ct.seg_empty[ss]);
+    }
+    tc_fence_before();
+  }
+
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// Merge of the units that were cut: CTA (w, y) takes every gridDim.y-th row
+// group of the unit whose first piece CTA w computed.
+//   o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,   M = max_s m_s
+// One warp per row; lane s holds piece s's (m, l), the hd row is spread over
+// the lanes, so the loads of all pieces are in flight at once.
+template <int HD>
+__global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
+  constexpr int PER = HD / 32;
+  using Vec = typename std::conditional<HD == 128, float4, float2>::type;
+  pdl_wait();
+  pdl_trigger();
+  const int w = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t *rec = p.rec + w * 8;
+  const int pieces = rec[0];
+  if (pieces == 0) return;
+  const int t0 = rec[1], i0 = rec[2], hk = rec[3], rows = rec[4];
+  for (int row = blockIdx.y * 8 + warp; row < rows; row += gridDim.y * 8) {
+    // piece 0 in slot 2 w + 1, piece s > 0 in slot 2 (w + s)
+    auto src = [&](int s) { return p.part + (static_cast<size_t>(s == 0 ? 2 * w + 1 : 2 * (w + s)) * 256 + row) * (HD + 4); };
+    float M = -INFINITY;
+    for (int s = lane; s < pieces; s += 32) M = fmaxf(M, src(s)[HD]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float L = 0.f, acc[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) acc[k] = 0.f;
+    for (int s0 = 0; s0 < pieces; s0 += 32) {
+      float wgt = 0.f;
+      if (s0 + lane < pieces) {
+        const float *x = src(s0 + lane);
+        // (a piece in which the row saw nothing has m = -inf)
+        wgt = x[HD] == -INFINITY ? 0.f : ex2_approx(x[HD] - M);
+        L = fmaf(wgt, x[HD + 1], L);
+      }
+      const int ns = min(32, pieces - s0);
+#pragma unroll 4
+      for (int s = 0; s < ns; ++s) {
+        const float ws = __shfl_sync(0xffffffffu, wgt, s);
+        const Vec x = reinterpret_cast<const Vec *>(src(s0 + s))[lane];
+        const float *xf = reinterpret_cast<const float *>(&x);
+        // (weight 0: the part may hold anything)
+#pragma unroll
+        for (int k = 0; k < PER; ++k) acc[k] = ws != 0.f ? fmaf(ws, xf[k], acc[k]) : acc[k];
+      }
     }
 #pragma unroll
-    for (int k = 0; k < PER; ++k) s_o[warp][g][lane + 32 * k] = o[g][k];
+    for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+    const float inv = 1.f / L;
+    const int tok = t0 + i0 + row / p.G, head = hk * p.G + row % p.G;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + (static_cast<size_t>(tok) * p.Hq + head) * HD + lane * PER);
+#pragma unroll
+    for (int k = 0; k < PER / 2; ++k) dst[k] = pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
   }
-  __syncthreads();
-  for (int e = threadIdx.x; e < G * HD; e += 128) {
-    const int g = e / HD, d = e % HD;
-    float M = -INFINITY;
-    for (int w = 0; w < 4; ++w) M = fmaxf(M, s_m[w][g]);
-    float L = 0.f, acc = 0.f;
-    for (int w = 0; w < 4; ++w) {
-      const float a = s_l[w][g] > 0.f ? ex2_approx(s_m[w][g] - M) : 0.f;
-      L = fmaf(a, s_l[w][g], L);
-      if (a > 0.f) acc = fmaf(a, s_o[w][g][d], acc);
-    }
-    p.o[(static_cast<size_t>(t) * p.Hq + hk * G + g) * HD + d] = __float2bfloat16_rn(acc / L);
-  }
+}
+
+template <int HD>
+cudaError_t launch_tree(const CUtensorMap &tq, const CUtensorMap &tkv, const TreeParams &p, int ctas, cudaStream_t st) {
+  using C = TreeCfg<HD>;
+  cudaError_t e = ensure_max_smem(reinterpret_cast<const void *>(tree_kernel<HD>), C::SMEM);
+  if (e == cudaSuccess) e = launch_pdl(tree_kernel<HD>, dim3(ctas), dim3(C::THREADS), C::SMEM, st, 1, tq, tkv, p);
+  if (e == cudaSuccess) e = launch_pdl(tree_merge_kernel<HD>, dim3(ctas, 4), dim3(256), 0, st, 1, p);
+  return e;
 }
 
 }  // namespace
 
-size_t tree_workspace_bytes() { return 256; }
+size_t tree_workspace_bytes() {
+  return kRecBytes + static_cast<size_t>(2) * kMaxTreeCtas * 256 * (128 + 4) * sizeof(float);
+}
 
 cudaError_t tree_attention_run(const TreeArgs &a, cudaStream_t st) {
   if (a.n_reqs <= 0 || a.T <= 0) return cudaSuccess;
   TreeParams p;
+  p.o = static_cast<__nv_bfloat16 *>(a.o);
   p.q = static_cast<const __nv_bfloat16 *>(a.q);
   p.pool = static_cast<const __nv_bfloat16 *>(a.pool);
-  p.o = static_cast<__nv_bfloat16 *>(a.o);
   p.qo_indptr = a.qo_indptr;
   p.kv_len = a.kv_len;
   p.bt_indptr = a.bt_indptr;
@@ -164,11 +945,22 @@ cudaError_t tree_attention_run(const TreeArgs &a, cudaStream_t st) {
   p.T = a.T;
   p.Hq = a.Hq;
   p.Hkv = a.Hkv;
+  p.G = a.Hq / a.Hkv;
   p.num_pages = a.num_pages;
   p.scale_log2 = kLog2e / sqrtf(static_cast<float>(a.hd));
+  p.rec = static_cast<int32_t *>(a.workspace);
+  p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + kRecBytes);
   p.err = a.err;
-  if (a.hd == 128) return launch_pdl(tree_simple_kernel<128>, dim3(a.T, a.Hkv), dim3(128), 0, st, 1, p);
-  return launch_pdl(tree_simple_kernel<64>, dim3(a.T, a.Hkv), dim3(128), 0, st, 1, p);
+  CUtensorMap tq, tkv;
+  const uint64_t hd = a.hd;
+  const uint64_t dq[3] = {hd, static_cast<uint64_t>(a.Hq), static_cast<uint64_t>(a.T)};
+  const uint64_t sq[2] = {hd * 2, hd * 2 * a.Hq};
+  const uint32_t bq[3] = {64, static_cast<uint32_t>(p.G), static_cast<uint32_t>(128 / p.G)};
+  cudaError_t e = encode_tmap(&tq, a.q, 3, dq, sq, bq);
+  if (e == cudaSuccess) e = encode_kv_tmap(&tkv, a.pool, static_cast<uint64_t>(a.num_pages) * 2 * a.Hkv, a.hd);
+  if (e != cudaSuccess) return e;
+  const int ctas = std::min(device_sm_count(), kMaxTreeCtas);
+  return a.hd == 128 ? launch_tree<128>(tq, tkv, p, ctas, st) : launch_tree<64>(tq, tkv, p, ctas, st);
 }
 
 }  // namespace mb
