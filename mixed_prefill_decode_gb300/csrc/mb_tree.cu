@@ -28,8 +28,12 @@
 //   O += P V         P (bf16, written over S) is the A operand from TMEM, V the
 //                    MN-major B operand straight from its stage
 //
-// S has two buffers: with two tiles they take turns (one tile's products run
-// during the other's softmax), with one tile its even and odd blocks do.
+// Two groups of four softmax warps take turns, each with an S buffer and an O
+// accumulator of its own: with two tiles each has one of them, with one tile
+// they take its even and odd blocks, as if each computed a piece, and the group
+// of the last block joins the two (O of both is in the same TMEM lanes, m and
+// l go through shared memory).  So products run during the other group's
+// softmax, and one group's output during the other's next unit.
 //
 // Schedule.  All units of the batch lie on one line, weighted by their blocks
 // (and a constant per unit); CTA w of W takes the w-th of W equal parts, so
@@ -62,8 +66,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxTreeCtas = 160;   // CTAs of a launch at most (one per SM); sizes the workspace
 constexpr int kRecBytes = 8192;     // workspace: one record of 8 ints per CTA, then the partials
 // The schedule's weights: a block of one query tile, a block of two, a unit's
-// start and end, and the least a CTA takes.
-constexpr int kCost1 = 2, kCost2 = 3, kCostUnit = 3, kMinShare = 8;
+// start and end, and the least a CTA takes (at least kCost2, so that no CTA
+// between the first and the last of a unit is left without a block).
+constexpr int kCost1 = 2, kCost2 = 3, kCostUnit = 3, kMinShare = 3;
 
 struct TreeParams {
   __nv_bfloat16 *o;
@@ -85,18 +90,19 @@ struct TreeCfg {
   static constexpr int ATOM_STRIDE = NH * 1024;
   static constexpr int PAGE_BYTES = 2 * ATOM_STRIDE;
   // K runs one block ahead of V (S comes before P V).
-  static constexpr int NK = HD == 128 ? 3 : 6;
-  static constexpr int NV = HD == 128 ? 2 : 5;
+  static constexpr int NK = HD == 128 ? 2 : 5;
+  static constexpr int NV = HD == 128 ? 3 : 6;
   static constexpr int NSEG = 4;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = OFF_Q + 2 * QT_BYTES;
   static constexpr int OFF_V = OFF_K + NK * KV_BYTES;
   static constexpr int OFF_CTRL = OFF_V + NV * KV_BYTES;
-  static constexpr int SMEM = OFF_CTRL + 2048;
+  static constexpr int OFF_ML = OFF_CTRL + 2048;     // (m, l) of 128 rows, from one warp group to the other
+  static constexpr int SMEM = OFF_ML + 1024;
   static constexpr int THREADS = 320;                // TMA, MMA, 2 x 4 softmax warps
   static constexpr uint32_t IDESC_S = idesc_bf16(128, 128, false);
   static constexpr uint32_t IDESC_PV = idesc_bf16(128, HD, true);
-  static constexpr uint32_t TMEM_COLS = 512;         // S/P buffers at 0 and 128, O of the two tiles from 256
+  static constexpr uint32_t TMEM_COLS = 512;         // S/P buffers at 0 and 128, O of the two groups from 256
   static constexpr uint32_t O_COL = 256;
 };
 
@@ -114,31 +120,32 @@ struct Seg {
   uint8_t parent[kMaxTreeNodes];   // 0xFF: none
 };
 
-template <int HD>
-struct Ctrl {
-  using C = TreeCfg<HD>;
-  uint64_t q_full[2], q_empty[2];
-  uint64_t k_full[C::NK], k_empty[C::NK], v_full[C::NV], v_empty[C::NV];
-  // S and P V products are done: by query tile, then by the tile's items in
-  // turn.  (Two products of a tile can be done before its warps look: the
-  // second barrier keeps their phases apart.  A third waits for the first's P.)
-  uint64_t s_full[2][2], o_full[2][2];
-  uint64_t p_full[2];              // by S buffer
-  uint64_t seg_full[C::NSEG], seg_empty[C::NSEG];
-  uint64_t done;
-  Seg seg[C::NSEG];
-  int64_t wsum[C::THREADS / 32];
-  int64_t start_base;
-  int32_t start_req;
-  uint32_t tmem;
-  int abort;
-};
-
 // What the schedule needs to know of a request.
 struct Req {
   int t0, n, kv, b0, nkb;
   int full, rem;   // units of 2 NT nodes, and the nodes of the last one if it is smaller
   int64_t head;    // cost of one KV head
+};
+
+template <int HD>
+struct Ctrl {
+  using C = TreeCfg<HD>;
+  uint64_t q_full[2], q_empty[2];
+  uint64_t k_full[C::NK], k_empty[C::NK], v_full[C::NV], v_empty[C::NV];
+  // By warp group.  (A group's next S waits for the P V of its last, so no
+  // phase is passed before the group has seen the one before it.)
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t ml_full[2];    // the group's (m, l) are in shared memory
+  uint64_t ml_empty[2];   // the other group has read them and this group's O
+  uint64_t seg_full[C::NSEG], seg_empty[C::NSEG];
+  uint64_t done;
+  Seg seg[C::NSEG];
+  int64_t wsum[C::THREADS / 32];
+  int64_t start_base;
+  Req start;
+  int32_t start_req;
+  uint32_t tmem;
+  int abort;
 };
 
 // (an invalid request costs nothing: it is skipped and reported)
@@ -180,6 +187,56 @@ __device__ __forceinline__ void probs64(const float (&sv)[64], float2 sc2, float
   }
 }
 
+// Takes the logits of keys that a row does not see out of a block of S (to
+// -inf, in TMEM): `first` is the node index of the block's first key (negative
+// while it is a key of the prefix), `see` the nodes that the row's node sees.
+// A pass of its own, out of line, for the one or two blocks of a unit that
+// hold nodes: it keeps the loop over the prefix short.
+__device__ __noinline__ void mask_block(uint32_t s_col, int first, const uint4 see) {
+  const uint32_t w[4] = {see.x, see.y, see.z, see.w};
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    const int f = first + 32 * k;   // node index of this word's first key
+    uint32_t vis = 0;
+    if (f <= -32) continue;         // prefix keys
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const int sh = 32 * a - f;    // word a of `see` starts at this bit
+      if (sh >= 0 && sh < 32) vis |= w[a] << sh;
+      if (sh < 0 && sh > -32) vis |= w[a] >> -sh;
+    }
+    if (f < 0) vis |= (1u << -f) - 1u;
+    float v[32];
+    tmem_ld32(s_col + 32 * k, v);
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (!((vis >> e) & 1u)) v[e] = -INFINITY;
+    tmem_st32(s_col + 32 * k, v);
+  }
+}
+
+// Adds to 32 columns of a row's o the parts p v of marked nodes (their V rows
+// hold an infinity or a NaN and left the product) that the row sees, p from
+// the same logit in fp32.  m: the reference that o is relative to.
+template <int HD>
+__device__ __noinline__ void add_odd(const TreeParams &p, const Seg &sg, uint4 see, int tok, int head, float m, int col,
+                                     float *v) {
+  const uint32_t w[4] = {sg.odd[0] & see.x, sg.odd[1] & see.y, sg.odd[2] & see.z, sg.odd[3] & see.w};
+  for (int a = 0; a < kMaxTreeNodes; ++a) {
+    if (!((w[a >> 5] >> (a & 31)) & 1u)) continue;
+    const int pos = sg.c + a;
+    int pg = p.bt[sg.b0 + pos / kPage];
+    if (pg < 0 || pg >= p.num_pages) pg = 0;
+    const __nv_bfloat16 *kr = p.pool + ((static_cast<size_t>(pg) * 2 * p.Hkv + sg.hk) * kPage + pos % kPage) * HD;
+    const __nv_bfloat16 *vr = kr + static_cast<size_t>(p.Hkv) * kPage * HD;
+    const __nv_bfloat16 *qr = p.q + (static_cast<size_t>(tok) * p.Hq + head) * HD;
+    float s = 0.f;
+    for (int k = 0; k < HD; ++k) s = fmaf(__bfloat162float(qr[k]), __bfloat162float(kr[k]), s);
+    const float pr = ex2_approx(fmaf(s, p.scale_log2, m == -INFINITY ? 0.f : -m));
+    for (int k = 0; k < 32; ++k) v[k] = fmaf(pr, __bfloat162float(vr[col + k]), v[k]);
+  }
+}
+
 template <int HD>
 __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmKV,
@@ -205,11 +262,11 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ct.q_full[b], 1);
       mbar_init(&ct.q_empty[b], 1);
-      mbar_init(&ct.s_full[b][0], 1);
-      mbar_init(&ct.s_full[b][1], 1);
+      mbar_init(&ct.s_full[b], 1);
       mbar_init(&ct.p_full[b], 128);
-      mbar_init(&ct.o_full[b][0], 1);
-      mbar_init(&ct.o_full[b][1], 1);
+      mbar_init(&ct.o_full[b], 1);
+      mbar_init(&ct.ml_full[b], 128);
+      mbar_init(&ct.ml_empty[b], 128);
     }
     for (int s = 0; s < C::NK; ++s) {
       mbar_init(&ct.k_full[s], 1);
@@ -242,9 +299,11 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
   const int per = (p.n_reqs + C::THREADS - 1) / C::THREADS;
   const int r_lo = min(p.n_reqs, static_cast<int>(threadIdx.x) * per), r_hi = min(p.n_reqs, r_lo + per);
   int64_t mine = 0;
+  Req last{};
   for (int r = r_lo; r < r_hi; ++r) {
     bool bad;
-    mine += load_req(p, r, &bad).head * p.Hkv;
+    last = load_req(p, r, &bad);
+    mine += last.head * p.Hkv;
     if (bad && cta == 0) atomicExch(p.err, kErrBounds);
   }
   int64_t inc = mine;
@@ -270,9 +329,11 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
   if (active && pre <= x0 && x0 < pre + mine) {
     for (int r = r_lo; r < r_hi; ++r) {
       bool bad;
-      const int64_t c = load_req(p, r, &bad).head * p.Hkv;
+      if (per > 1) last = load_req(p, r, &bad);
+      const int64_t c = last.head * p.Hkv;
       if (x0 < pre + c) {
         ct.start_req = r;
+        ct.start = last;
         ct.start_base = pre;
         break;
       }
@@ -294,7 +355,7 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
     int r = ct.start_req;
     int64_t base = ct.start_base;
     bool bad;
-    Req q = load_req(p, r, &bad);
+    Req q = ct.start;
     Req nx{};
     if (r + 1 < p.n_reqs) nx = load_req(p, r + 1, &bad);
     // the unit that x0 lies in
@@ -323,6 +384,10 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
       }
       good = __shfl_sync(0xffffffffu, good, 0);
       if (!good) return false;
+      if (lane < np && (page < 0 || page >= p.num_pages)) {
+        atomicExch(p.err, kErrBounds);
+        page = 0;
+      }
       if (lane < np)
         tma_load_5d((is_v ? sV : sK) + st * C::KV_BYTES + lane * C::PAGE_BYTES, &tmKV, full, 0, 0, 0, 0,
                     (page * 2 + (is_v ? 1 : 0)) * p.Hkv + h);
@@ -348,14 +413,7 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
         const int i0 = u * 2 * NT;
         const int32_t *table = p.bt + q.b0;
         const int n_pages = (q.kv + kPage - 1) / kPage;
-        auto page_of = [&](int blk) {
-          int pg = lane < 8 && 8 * blk + lane < n_pages ? table[8 * blk + lane] : 0;
-          if (pg < 0 || pg >= p.num_pages) {
-            atomicExch(p.err, kErrBounds);
-            pg = 0;
-          }
-          return pg;
-        };
+        auto page_of = [&](int blk) { return lane < 8 && 8 * blk + lane < n_pages ? table[8 * blk + lane] : 0; };
         int cur = page_of(j0), nxt = j0 + 1 < j1 ? page_of(j0 + 1) : 0;
         const bool tail = 128 * j1 > q.kv - q.n;   // some of the piece's keys are nodes
         int32_t par[4] = {-1, -1, -1, -1};
@@ -366,7 +424,22 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
         // what is left of the piece before
         if (pv_have) ok = send(true, pv_np, pv_page, pv_hk);
         pv_have = false;
-        // tell the other roles
+        // the query tiles
+        if (lane == 0)
+          for (int t = 0; t < qt && ok; ++t) {
+            const int qb = qsel ^ t;
+            ok = mbar_wait(&ct.q_empty[qb], (quse[qb] & 1) ^ 1, abort_flag, p.err, kErrWaitProducer);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&ct.q_full[qb], C::NH * G * NT * 128);
+            for (int ch = 0; ch < C::NH; ++ch)
+              tma_load_3d(sQ + qb * C::QT_BYTES + ch * C::TILE_BYTES, &tmQ, &ct.q_full[qb], ch * 64, hk * G,
+                          q.t0 + i0 + t * NT);
+            ++quse[qb];
+          }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        // the first K, then the piece's record for the other roles
+        const int np0 = min(8, n_pages - 8 * j0);
+        if (ok) ok = send(false, np0, cur, hk);
         const int ss = nseg % C::NSEG;
         if (ok) {
           if (lane == 0) ok = mbar_wait(&ct.seg_empty[ss], ((nseg / C::NSEG) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer);
@@ -410,21 +483,14 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
           rec[3] = hk;
           rec[4] = nodes * G;
         }
-        // the query tiles
-        if (lane == 0)
-          for (int t = 0; t < qt && ok; ++t) {
-            const int qb = qsel ^ t;
-            ok = mbar_wait(&ct.q_empty[qb], (quse[qb] & 1) ^ 1, abort_flag, p.err, kErrWaitProducer);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&ct.q_full[qb], C::NH * G * NT * 128);
-            for (int ch = 0; ch < C::NH; ++ch)
-              tma_load_3d(sQ + qb * C::QT_BYTES + ch * C::TILE_BYTES, &tmQ, &ct.q_full[qb], ch * 64, hk * G,
-                          q.t0 + i0 + t * NT);
-          }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        for (int t = 0; t < qt; ++t) ++quse[qsel ^ t];
         if (qt == 1) qsel ^= 1;
-        for (int j = j0; j < j1 && ok; ++j) {
+        pv_np = np0;
+        pv_page = cur;
+        pv_hk = hk;
+        pv_have = true;
+        cur = nxt;
+        nxt = j0 + 2 < j1 ? page_of(j0 + 2) : 0;
+        for (int j = j0 + 1; j < j1 && ok; ++j) {
           const int np = min(8, n_pages - 8 * j);
           const int after = j + 2 < j1 ? page_of(j + 2) : 0;
           ok = send(false, np, cur, hk);
@@ -493,7 +559,7 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
         bool in;
       };
       Cursor s{0, 0, 0, 0, 0, 0, 0, 0, false}, v{0, 0, 0, 0, 0, 0, 0, 0, false};
-      int quse[2] = {0, 0}, n_s[2] = {0, 0}, n_o[2] = {0, 0};   // Q buffers used up; S and P V products of each tile
+      int quse[2] = {0, 0};
       bool s_end = false;
       uint64_t t_idle = globaltimer();
       auto enter = [&](Cursor &x) {
@@ -525,7 +591,7 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
                 for (int kk = 0; kk < 4; ++kk)
                   mma_bf16(d, qd + ((ch * C::TILE_BYTES + kk * 32) >> 4), kd + ((ch * 1024 + kk * 32) >> 4), C::IDESC_S,
                            (ch > 0 || kk > 0) ? 1u : 0u);
-              mma_commit(&ct.s_full[s.t][n_s[s.t]++ & 1]);
+              mma_commit(&ct.s_full[s.item & 1]);
               if (s.lb == s.nb - 1) {
                 mma_commit(&ct.q_empty[qb]);
                 ++quse[qb];
@@ -551,12 +617,14 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
               mbar_test_wait(smem_u32(&ct.v_full[st]), (v.blk / C::NV) & 1)) {
             tc_fence_after();
             const uint64_t vd = vd0 + static_cast<uint64_t>((st * C::KV_BYTES) >> 4);
-            const uint32_t pcol = tmem + 128 * (v.item & 1);
+            const int w = v.item & 1;               // warp group, S buffer, O accumulator
+            const uint32_t pcol = tmem + 128 * w;
+            const bool first = v.lb < (v.qt == 1 ? 2 : 1);   // the group's first block of the piece
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)   // 16 keys (two atoms) per MMA; hd halves 1 KB apart
-              mma_bf16_ts(tmem + C::O_COL + HD * v.t, pcol + ks * 8, vd + ((ks * 2 * C::ATOM_STRIDE) >> 4), C::IDESC_PV,
-                          (v.lb > 0 || ks > 0) ? 1u : 0u);
-            mma_commit(&ct.o_full[v.t][n_o[v.t]++ & 1]);
+              mma_bf16_ts(tmem + C::O_COL + HD * w, pcol + ks * 8, vd + ((ks * 2 * C::ATOM_STRIDE) >> 4), C::IDESC_PV,
+                          (!first || ks > 0) ? 1u : 0u);
+            mma_commit(&ct.o_full[w]);
             ++v.item;
             if (++v.t == v.qt) {
               mma_commit(&ct.v_empty[st]);
@@ -591,16 +659,21 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
     }
   } else {
     // ------------------------------------------------- softmax / epilogue
-    const int t = (warp - 2) >> 2;          // query tile of this warp group
+    const int w = (warp - 2) >> 2;          // warp group: it takes every second item
     const int qu = warp & 3;                // TMEM lane quarter
     const int row = qu * 32 + lane;         // row of the tile; also the key of a block it looks after
     const uint32_t lane_base = static_cast<uint32_t>(qu * 32) << 16;
-    const uint32_t o_col = tmem + lane_base + C::O_COL + HD * t;
+    const uint32_t s_col = tmem + lane_base + 128 * w;
+    const uint32_t o_col = tmem + lane_base + C::O_COL + HD * w;
+    const uint32_t o_other = tmem + lane_base + C::O_COL + HD * (w ^ 1);
+    float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
     constexpr float kRescaleAbove = 8.f;    // log2 units
     const float scale = p.scale_log2;
     const float2 sc2 = make_float2(scale, scale);
-    const int G = p.G, NT = 128 / G;
-    int nseg = 0, item0 = 0, blk0 = 0, pv0 = 0;
+    const int G = p.G, NT = 128 / G, row_node = row / G, row_head = row % G;
+    int nseg = 0, item0 = 0, blk0 = 0;
+    int lent[2] = {0, 0};     // times that group 0, 1 left its part of a piece to the other
+    bool lending = false;     // the other group may still be reading this one's O and (m, l)
     bool ok = true;
     while (true) {
       const int ss = nseg % C::NSEG;
@@ -610,33 +683,35 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
       const int nb = sg.nb;
       if (nb == 0) break;
       const int qt = sg.qt, j0 = sg.j0, c = sg.c, kv = sg.kv;
-      const int rows = (t == 0 ? min(sg.nodes, NT) : sg.nodes - NT) * G;   // <= 0: no such tile
-      if (t >= qt) {
-        item0 += nb;
-        blk0 += nb;
+      const int items = nb * qt;
+      const int lb0 = (item0 & 1) ^ w;       // this group's first item of the piece
+      const int t = qt == 2 ? lb0 : 0;       // its query tile
+      if (lb0 >= items) {                    // one block, and it is the other group's
+        ++item0;
+        ++blk0;
         ++nseg;
         __syncwarp();
         if (lane == 0) mbar_arrive(&ct.seg_empty[ss]);
         continue;
       }
+      const int rows = (t == 0 ? min(sg.nodes, NT) : sg.nodes - NT) * G;
       const bool idle = qu * 32 >= rows;     // no rows for this warp (it still looks after keys)
-      const int node = sg.i0 + t * NT + row / G;
+      const int node = sg.i0 + t * NT + row_node;
       // the nodes that this row's node sees
-      uint32_t see[4] = {0, 0, 0, 0};
+      uint4 see = make_uint4(0, 0, 0, 0);
       if (row < rows && 128 * (j0 + nb) > c)
-        for (uint32_t x = node; x != 0xFF;) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (static_cast<int>(x >> 5) == k) see[k] |= 1u << (x & 31);
-          x = sg.parent[x];
+        for (uint32_t x = node; x != 0xFF; x = sg.parent[x]) {
+          const uint32_t bit = 1u << (x & 31), a = x >> 5;
+          see.x |= a == 0 ? bit : 0;
+          see.y |= a == 1 ? bit : 0;
+          see.z |= a == 2 ? bit : 0;
+          see.w |= a == 3 ? bit : 0;
         }
       float m_ref = -INFINITY, l = 0.f;
-      for (int lb = 0; lb < nb; ++lb) {
-        const int item = item0 + lb * qt + t, sb = item & 1;
-        const uint32_t s_col = tmem + lane_base + 128 * sb;
+      for (int li = lb0; li < items; li += 2) {
+        const int item = item0 + li, lb = qt == 2 ? li >> 1 : li;
         const int j = j0 + lb, key0 = 128 * j;
-        const int mine_n = pv0 + lb;         // this tile's items before it
-        fail = !mbar_wait(&ct.s_full[t][mine_n & 1], (mine_n >> 1) & 1, abort_flag, p.err, kErrWaitSoftmax);
+        fail = !mbar_wait(&ct.s_full[w], (item >> 1) & 1, abort_flag, p.err, kErrWaitSoftmax);
         if (__any_sync(0xffffffffu, fail)) {
           ok = false;
           break;
@@ -644,28 +719,7 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
         tc_fence_after();
         const bool full = key0 + 128 <= c;   // only prefix keys: visible to every row
         if (!idle) {
-          // which keys of the block this row sees
-          uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
-          if (!full) {
-            const int d = key0 - c;          // node index of the block's first key
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int f = d + 32 * k;      // node index of this word's first key
-              uint32_t w = 0;
-              if (f <= -32) {
-                w = ~0u;
-              } else {
-#pragma unroll
-                for (int a = 0; a < 4; ++a) {
-                  const int sh = 32 * a - f;   // word a of `see` starts at this bit of the word
-                  if (sh >= 0 && sh < 32) w |= see[a] << sh;
-                  if (sh < 0 && sh > -32) w |= see[a] >> -sh;
-                }
-                if (f < 0) w |= (1u << -f) - 1u;
-              }
-              vis[k] = w;
-            }
-          }
+          if (!full) mask_block(s_col, key0 - c, see);
           // One pass over S while the row's reference maximum holds; if a row
           // of the warp rose more than 2^8 above it (always at the piece's
           // first block), the reference moves, O is rescaled and the
@@ -673,16 +727,12 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
           uint32_t pk_lo[32], pk_hi[32];
           float2 lsum = make_float2(0.f, 0.f);
           float mq0 = -INFINITY, mq1 = -INFINITY, mq2 = -INFINITY, mq3 = -INFINITY;
-          const bool have_ref = lb > 0;
+          const bool have_ref = li >= 2;
           float negm = m_ref == -INFINITY ? 0.f : -m_ref;
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
             float sv[64];
             tmem_ld64(s_col + 64 * hh, sv);
-            if (!full)
-#pragma unroll
-              for (int e = 0; e < 64; ++e)
-                if (!((vis[2 * hh + (e >> 5)] >> (e & 31)) & 1u)) sv[e] = -INFINITY;
 #pragma unroll
             for (int e = 0; e < 64; e += 8) {
               mq0 = max3f(mq0, sv[e], sv[e + 1]);
@@ -695,10 +745,9 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
           const float mx = fmaxf(fmaxf(mq0, mq1), fmaxf(mq2, mq3)) * scale;
           const bool grow = !have_ref || mx > m_ref + kRescaleAbove;
           if (__any_sync(0xffffffffu, grow)) {
-            if (lb > 0) {
-              // O holds the blocks before: their P V must be done
-              const int prev_n = mine_n - 1;
-              fail = !mbar_wait(&ct.o_full[t][prev_n & 1], (prev_n >> 1) & 1, abort_flag, p.err, kErrWaitSoftmax);
+            if (li >= 2) {
+              // O holds the group's blocks before: their P V must be done
+              fail = !mbar_wait(&ct.o_full[w], ((item - 2) >> 1) & 1, abort_flag, p.err, kErrWaitSoftmax);
               if (__any_sync(0xffffffffu, fail)) {
                 ok = false;
                 break;
@@ -722,10 +771,6 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
             for (int hh = 0; hh < 2; ++hh) {
               float sv[64];
               tmem_ld64(s_col + 64 * hh, sv);
-              if (!full)
-#pragma unroll
-                for (int e = 0; e < 64; ++e)
-                  if (!((vis[2 * hh + (e >> 5)] >> (e & 31)) & 1u)) sv[e] = -INFINITY;
               probs64(sv, sc2, negm, hh ? pk_hi : pk_lo, lsum);
             }
           }
@@ -739,8 +784,8 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
           // infinity or a NaN is not.  V rows past the request's last key hold
           // anything: zeroed.  A node's V row with a non-finite value is zeroed
           // too and the node marked; the rows that do see it add its part at the
-          // end.  (Warp group 0 does it, before its P is ready; tile 1's product
-          // with this block is issued after tile 0's.)
+          // end.  (Tile 0's warp group does it, before its P is ready; tile 1's
+          // product with this block is issued after tile 0's.)
           const int vb = blk0 + lb;
           fail = !mbar_wait(&ct.v_full[vb % C::NV], (vb / C::NV) & 1, abort_flag, p.err, kErrWaitSoftmax);
           if (__any_sync(0xffffffffu, fail)) {
@@ -752,15 +797,15 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
           bool wipe = key >= kv;
           if (key >= c && !wipe) {
             uint32_t special = 0;
-#pragma unroll
+#pragma unroll 1
             for (int ch = 0; ch < C::NH; ++ch)
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
                 const uint4 x = *reinterpret_cast<const uint4 *>(vrow + ch * 1024 + ((k + lane) & 7) * 16);
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  special |= ((w[e] & 0x7F80u) == 0x7F80u || (w[e] & 0x7F800000u) == 0x7F800000u) ? 1u : 0u;
+                  special |= ((y[e] & 0x7F80u) == 0x7F80u || (y[e] & 0x7F800000u) == 0x7F800000u) ? 1u : 0u;
               }
             if (special) {
               wipe = true;
@@ -776,75 +821,93 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
           }
           fence_proxy_async_smem();
         }
-        tc_fence_before();
-        mbar_arrive(&ct.p_full[sb]);
-      }
-      // ---- the piece is done: its output, or its partial
-      const int last_n = pv0 + nb - 1;
-      fail = !ok || !mbar_wait(&ct.o_full[t][last_n & 1], (last_n >> 1) & 1, abort_flag, p.err, kErrWaitSoftmax);
-      if (__any_sync(0xffffffffu, fail)) break;
-      tc_fence_after();
-      if (!idle) {
-        const bool valid = row < rows;
-        const uint32_t odd[4] = {sg.odd[0] & see[0], sg.odd[1] & see[1], sg.odd[2] & see[2], sg.odd[3] & see[3]};
-        const bool any_odd = valid && (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
-        const int tok = sg.t0 + node, head = sg.hk * G + row % G;
-        // one marked node's part: p v, p from the same logit in fp32
-        auto add_odd = [&](float (&v)[32], int col) {
-          for (int a = 0; a < kMaxTreeNodes; ++a) {
-            if (!((odd[a >> 5] >> (a & 31)) & 1u)) continue;
-            const int pos = c + a;
-            int pg = p.bt[sg.b0 + pos / kPage];
-            if (pg < 0 || pg >= p.num_pages) pg = 0;
-            const __nv_bfloat16 *kr = p.pool + ((static_cast<size_t>(pg) * 2 * p.Hkv + sg.hk) * kPage + pos % kPage) * HD;
-            const __nv_bfloat16 *vr = kr + static_cast<size_t>(p.Hkv) * kPage * HD;
-            const __nv_bfloat16 *qr = p.q + (static_cast<size_t>(tok) * p.Hq + head) * HD;
-            float s = 0.f;
-            for (int k = 0; k < HD; ++k) s = fmaf(__bfloat162float(qr[k]), __bfloat162float(kr[k]), s);
-            const float pr = ex2_approx(fmaf(s, scale, m_ref == -INFINITY ? 0.f : -m_ref));
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = fmaf(pr, __bfloat162float(vr[col + k]), v[k]);
+        if (lending) {
+          // P V of this item overwrites O: the other group must have read it
+          fail = !mbar_wait(&ct.ml_empty[w], (lent[w] - 1) & 1, abort_flag, p.err, kErrWaitSoftmax);
+          if (__any_sync(0xffffffffu, fail)) {
+            ok = false;
+            break;
           }
-        };
-        if (sg.slot < 0) {
+          lending = false;
+        }
+        tc_fence_before();
+        mbar_arrive(&ct.p_full[w]);
+      }
+      if (!ok) break;
+      // ---- the piece is done: its output, or its partial
+      const int last_item = item0 + items - 1;
+      const bool joint = qt == 1 && nb > 1;         // both groups had blocks of the tile
+      if (joint && (last_item & 1) != w) {
+        // the other group has the last block: it gets this one's m and l
+        ml[row] = make_float2(m_ref, l);
+        ++lent[w];
+        lending = true;
+        tc_fence_before();
+        mbar_arrive(&ct.ml_full[w]);
+      } else {
+        const int mine_last = qt == 2 ? item0 + items - 2 + lb0 : last_item;
+        fail = !mbar_wait(&ct.o_full[w], (mine_last >> 1) & 1, abort_flag, p.err, kErrWaitSoftmax);
+        float wa = 1.f, wb = 0.f;                     // weights of this group's O and the other's
+        if (joint) {
+          if (!fail) fail = !mbar_wait(&ct.ml_full[w ^ 1], lent[w ^ 1] & 1, abort_flag, p.err, kErrWaitSoftmax);
+          ++lent[w ^ 1];
+          if (!fail) fail = !mbar_wait(&ct.o_full[w ^ 1], ((last_item - 1) >> 1) & 1, abort_flag, p.err, kErrWaitSoftmax);
+          const float2 o = ml[row];
+          const float M = fmaxf(m_ref, o.x);
+          wa = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - M);
+          wb = o.x == -INFINITY ? 0.f : ex2_approx(o.x - M);
+          l = wa * l + wb * o.y;
+          m_ref = M;
+        }
+        if (__any_sync(0xffffffffu, fail)) break;
+        tc_fence_after();
+        if (!idle) {
+          const bool valid = row < rows;
+          const bool odd = valid && ((sg.odd[0] & see.x) | (sg.odd[1] & see.y) | (sg.odd[2] & see.z) | (sg.odd[3] & see.w));
+          const int tok = sg.t0 + node, head = sg.hk * G + row_head, slot = sg.slot;
           const float inv = 1.f / l;
           uint4 *dst = reinterpret_cast<uint4 *>(p.o + (static_cast<size_t>(tok) * p.Hq + head) * HD);
-#pragma unroll
+          // (partial rows in node order: tile 1's behind tile 0's)
+          float *part = p.part + (static_cast<size_t>(max(slot, 0)) * 256 + t * NT * G + row) * (HD + 4);
+#pragma unroll 1
           for (int cc = 0; cc < HD / 32; ++cc) {
             float v[32];
-            tmem_ld32(o_col + cc * 32, v);
-            if (any_odd) add_odd(v, cc * 32);
-            if (valid)
+            if (joint) {
+              float x[32];
+              tmem_ld32x2(o_col + cc * 32, o_other + cc * 32, v, x);
 #pragma unroll
-              for (int v8 = 0; v8 < 4; ++v8)
-                dst[cc * 4 + v8] = make_uint4(pack_bf16x2(v[8 * v8] * inv, v[8 * v8 + 1] * inv),
-                                              pack_bf16x2(v[8 * v8 + 2] * inv, v[8 * v8 + 3] * inv),
-                                              pack_bf16x2(v[8 * v8 + 4] * inv, v[8 * v8 + 5] * inv),
-                                              pack_bf16x2(v[8 * v8 + 6] * inv, v[8 * v8 + 7] * inv));
-          }
-        } else {
-          // rows in node order: tile 1's behind tile 0's
-          float *dst = p.part + (static_cast<size_t>(sg.slot) * 256 + t * NT * G + row) * (HD + 4);
+              for (int k = 0; k < 32; ++k) v[k] = wa * v[k] + wb * x[k];
+            } else {
+              tmem_ld32(o_col + cc * 32, v);
+            }
+            if (odd) {
+              float x[32];
 #pragma unroll
-          for (int cc = 0; cc < HD / 32; ++cc) {
-            float v[32];
-            tmem_ld32(o_col + cc * 32, v);
-            if (any_odd) add_odd(v, cc * 32);
-            if (valid)
+              for (int k = 0; k < 32; ++k) x[k] = v[k];
+              add_odd<HD>(p, sg, see, tok, head, m_ref, cc * 32, x);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] = x[k];
+            }
+            if (valid && slot < 0) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                dst[cc * 4 + k] = make_uint4(pack_bf16x2(v[8 * k] * inv, v[8 * k + 1] * inv),
+                                             pack_bf16x2(v[8 * k + 2] * inv, v[8 * k + 3] * inv),
+                                             pack_bf16x2(v[8 * k + 4] * inv, v[8 * k + 5] * inv),
+                                             pack_bf16x2(v[8 * k + 6] * inv, v[8 * k + 7] * inv));
+            } else if (valid) {
 #pragma unroll
               for (int k = 0; k < 8; ++k)
-                reinterpret_cast<float4 *>(dst + cc * 32)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                reinterpret_cast<float4 *>(part + cc * 32)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            }
           }
-          if (valid) {
-            dst[HD] = m_ref;
-            dst[HD + 1] = l;
-          }
+          if (valid && slot >= 0) *reinterpret_cast<float2 *>(part + HD) = make_float2(m_ref, l);
         }
+        tc_fence_before();
+        if (joint) mbar_arrive(&ct.ml_empty[w ^ 1]);
       }
-      tc_fence_before();
-      item0 += nb * qt;
+      item0 += items;
       blk0 += nb;
-      pv0 += nb;
       ++nseg;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ct.seg_empty[ss]);
