@@ -148,14 +148,22 @@ struct Ctrl {
   int abort;
 };
 
+// Its words of the descriptor (loaded well before they are worked on).
+struct RawReq {
+  int q0, q1, kv, b0, b1;
+};
+__device__ __forceinline__ RawReq load_raw(const TreeParams &p, int r) {
+  return {p.qo_indptr[r], p.qo_indptr[r + 1], p.kv_len[r], p.bt_indptr[r], p.bt_indptr[r + 1]};
+}
+
 // (an invalid request costs nothing: it is skipped and reported)
-__device__ __forceinline__ Req load_req(const TreeParams &p, int r, bool *bad) {
+__device__ __forceinline__ Req make_req(const TreeParams &p, const RawReq x, bool *bad) {
   Req q;
-  q.t0 = p.qo_indptr[r];
-  q.n = p.qo_indptr[r + 1] - q.t0;
-  q.kv = p.kv_len[r];
-  q.b0 = p.bt_indptr[r];
-  const int pages = p.bt_indptr[r + 1] - q.b0;
+  q.t0 = x.q0;
+  q.n = x.q1 - x.q0;
+  q.kv = x.kv;
+  q.b0 = x.b0;
+  const int pages = x.b1 - x.b0;
   *bad = q.t0 < 0 || q.n < 0 || q.n > kMaxTreeNodes || q.t0 + q.n > p.T || q.kv < q.n || q.kv > (1 << 24) || q.b0 < 0 ||
          (q.kv + kPage - 1) / kPage > pages;
   if (*bad) q.n = 0;
@@ -175,17 +183,20 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
   return d;
 }
 
-// p = 2^(s scale + negm) of 64 logits, as bf16 pairs, added into `sum`.
-__device__ __forceinline__ void probs64(const float (&sv)[64], float2 sc2, float negm, uint32_t (&pk)[32], float2 &sum) {
+// p = 2^(s scale + negm) of N logits, as bf16 pairs, added into `sum`.
+template <int N>
+__device__ __forceinline__ void probs(const float (&sv)[N], float2 sc2, float negm, uint32_t (&pk)[N / 2], float2 &sum) {
   const float2 nm = make_float2(negm, negm);
 #pragma unroll
-  for (int c = 0; c < 64; c += 2) {
+  for (int c = 0; c < N; c += 2) {
     const float2 x = __ffma2_rn(make_float2(sv[c], sv[c + 1]), sc2, nm);
     const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
     sum = __fadd2_rn(sum, make_float2(p0, p1));
     pk[c / 2] = pack_bf16x2(p0, p1);
   }
 }
+
+__device__ __noinline__ int64_t div64(int64_t a, int64_t b) { return a / b; }
 
 // Takes the logits of keys that a row does not see out of a block of S (to
 // -inf, in TMEM): `first` is the node index of the block's first key (negative
@@ -302,7 +313,7 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
   Req last{};
   for (int r = r_lo; r < r_hi; ++r) {
     bool bad;
-    last = load_req(p, r, &bad);
+    last = make_req(p, load_raw(p, r), &bad);
     mine += last.head * p.Hkv;
     if (bad && cta == 0) atomicExch(p.err, kErrBounds);
   }
@@ -325,11 +336,11 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
   }
   const int64_t W = total / kMinShare < 1 ? (total > 0 ? 1 : 0) : (total / kMinShare < W_max ? total / kMinShare : W_max);
   const bool active = cta < W;
-  const int64_t x0 = active ? total * cta / W : 0, x1 = active ? total * (cta + 1) / W : 0;
+  const int64_t x0 = active ? div64(total * cta, W) : 0, x1 = active ? div64(total * (cta + 1), W) : 0;
   if (active && pre <= x0 && x0 < pre + mine) {
     for (int r = r_lo; r < r_hi; ++r) {
       bool bad;
-      if (per > 1) last = load_req(p, r, &bad);
+      if (per > 1) last = make_req(p, load_raw(p, r), &bad);
       const int64_t c = last.head * p.Hkv;
       if (x0 < pre + c) {
         ct.start_req = r;
@@ -356,15 +367,15 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
     int64_t base = ct.start_base;
     bool bad;
     Req q = ct.start;
-    Req nx{};
-    if (r + 1 < p.n_reqs) nx = load_req(p, r + 1, &bad);
+    RawReq nx{};
+    if (r + 1 < p.n_reqs) nx = load_raw(p, r + 1);
     // the unit that x0 lies in
     int64_t off = x0 - base;
-    int hk = static_cast<int>(off / q.head);
+    int hk = static_cast<int>(div64(off, q.head));
     base += hk * q.head;
     off -= hk * q.head;
     const int64_t big0 = kCostUnit + kCost2 * static_cast<int64_t>(q.nkb);
-    int u = static_cast<int>(min(static_cast<int64_t>(q.full), off / big0));
+    int u = static_cast<int>(min(static_cast<int64_t>(q.full), div64(off, big0)));
     base += u * big0;
     int kcnt = 0, vcnt = 0, nseg = 0, quse[2] = {0, 0}, qsel = 0;
     bool ok = true;
@@ -402,10 +413,12 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
       const int64_t cost = kCostUnit + static_cast<int64_t>(b) * q.nkb;
       auto cut = [&](int64_t x) {   // blocks of the unit that lie before x
         const int64_t d = x - base - kCostUnit;
-        return d <= 0 ? 0 : static_cast<int>(min(static_cast<int64_t>(q.nkb), (d + b - 1) / b));
+        if (d <= 0) return 0;
+        const int64_t n = qt == 2 ? (d + kCost2 - 1) / kCost2 : (d + kCost1 - 1) / kCost1;
+        return static_cast<int>(min(static_cast<int64_t>(q.nkb), n));
       };
       auto owner = [&](int j) {     // the CTA whose part holds block j: the last w with total w / W <= its place
-        return static_cast<int>(((base + kCostUnit + static_cast<int64_t>(b) * j + 1) * W - 1) / total);
+        return static_cast<int>(div64((base + kCostUnit + static_cast<int64_t>(b) * j + 1) * W - 1, total));
       };
       const int j0 = cut(x0), j1 = cut(x1);
       if (j1 > j0) {
@@ -512,8 +525,8 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
           do {
             ++r;
             if (r >= p.n_reqs) break;
-            q = nx;
-            if (r + 1 < p.n_reqs) nx = load_req(p, r + 1, &bad);
+            q = make_req(p, nx, &bad);
+            if (r + 1 < p.n_reqs) nx = load_raw(p, r + 1);
           } while (q.n == 0);
           if (r >= p.n_reqs) break;
         }
@@ -561,7 +574,7 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
       Cursor s{0, 0, 0, 0, 0, 0, 0, 0, false}, v{0, 0, 0, 0, 0, 0, 0, 0, false};
       int quse[2] = {0, 0};
       bool s_end = false;
-      uint64_t t_idle = globaltimer();
+      uint64_t t_idle = 0;
       auto enter = [&](Cursor &x) {
         const Seg &sg = ct.seg[x.seg % C::NSEG];
         x.nb = sg.nb;
@@ -570,7 +583,7 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
         x.lb = x.t = 0;
         x.in = true;
       };
-      for (uint32_t spin = 0;; ++spin) {
+      for (uint32_t spin = 1;; ++spin) {   // rounds without progress
         bool progress = false;
         if (!s_end && s.item < v.item + 2) {
           if (!s.in && mbar_test_wait(smem_u32(&ct.seg_full[s.seg % C::NSEG]), (s.seg / C::NSEG) & 1)) {
@@ -641,9 +654,11 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
         }
         if (s_end && v.item == s.item) break;
         if (progress) {
-          t_idle = globaltimer();
-        } else if ((spin & 15u) == 15u) {
+          spin = 0;
+          t_idle = 0;
+        } else if ((spin & 255u) == 0) {
           if (*abort_flag) break;
+          if (t_idle == 0) t_idle = globaltimer();
           if (globaltimer() - t_idle > kWaitLimitNs) {
             *abort_flag = 1;
             atomicExch(p.err, kErrWaitMma);
@@ -740,7 +755,7 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
               mq2 = max3f(mq2, sv[e + 4], sv[e + 5]);
               mq3 = max3f(mq3, sv[e + 6], sv[e + 7]);
             }
-            if (have_ref) probs64(sv, sc2, negm, hh ? pk_hi : pk_lo, lsum);
+            if (have_ref) probs<64>(sv, sc2, negm, hh ? pk_hi : pk_lo, lsum);
           }
           const float mx = fmaxf(fmaxf(mq0, mq1), fmaxf(mq2, mq3)) * scale;
           const bool grow = !have_ref || mx > m_ref + kRescaleAbove;
@@ -754,7 +769,7 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
               }
               tc_fence_after();
               const float alpha = grow ? ex2_approx(m_ref - mx) : 1.f;
-#pragma unroll
+#pragma unroll 1
               for (int cc = 0; cc < HD / 32; ++cc) {
                 float v[32];
                 tmem_ld32(o_col + cc * 32, v);
@@ -766,18 +781,22 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
             }
             if (grow) m_ref = mx;
             negm = m_ref == -INFINITY ? 0.f : -m_ref;   // a row that has seen nothing yet
+            // P of 32 keys goes over 16 columns of S that have been read
             lsum = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              float sv[64];
-              tmem_ld64(s_col + 64 * hh, sv);
-              probs64(sv, sc2, negm, hh ? pk_hi : pk_lo, lsum);
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+              float sv[32];
+              uint32_t pk[16];
+              tmem_ld32(s_col + 32 * k, sv);
+              probs<32>(sv, sc2, negm, pk, lsum);
+              tmem_st16u(s_col + 16 * k, pk);
             }
+          } else {
+            // P over S: keys 0-63 in columns 0-31, keys 64-127 in 32-63
+            tmem_st32u(s_col, pk_lo);
+            tmem_st32u(s_col + 32, pk_hi);
           }
           l += lsum.x + lsum.y;
-          // P over S: keys 0-63 in columns 0-31, keys 64-127 in 32-63
-          tmem_st32u(s_col, pk_lo);
-          tmem_st32u(s_col + 32, pk_hi);
         }
         if (!full && t == 0) {
           // Keys that some row does not see: P is 0 there, but 0 times an
@@ -926,24 +945,69 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
 // Merge of the units that were cut: CTA (w, y) takes every gridDim.y-th row
 // group of the unit whose first piece CTA w computed.
 //   o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,   M = max_s m_s
-// One warp per row; lane s holds piece s's (m, l), the hd row is spread over
-// the lanes, so the loads of all pieces are in flight at once.
+// One warp takes a row, lane s holding piece s's (m, l), with the loads of all
+// pieces in flight at once; where there are many rows of few pieces, 8 lanes
+// take a row and a warp four at a time (16 trees of 64 nodes at 8,192 keys, 256
+// rows a unit: 158 us in all against 165; one tree of 6 nodes at 1,125 keys,
+// 24 rows of 8 pieces: 18 us against 13.6, so it is for more than 64 rows).
 template <int HD>
-__global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
-  constexpr int PER = HD / 32;
-  using Vec = typename std::conditional<HD == 128, float4, float2>::type;
+__global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeParams p) {
   pdl_wait();
   pdl_trigger();
   const int w = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int32_t *rec = p.rec + w * 8;
-  const int pieces = rec[0];
+  const int4 rec = *reinterpret_cast<const int4 *>(p.rec + w * 8);
+  const int rows = p.rec[w * 8 + 4];
+  const int pieces = rec.x;
   if (pieces == 0) return;
-  const int t0 = rec[1], i0 = rec[2], hk = rec[3], rows = rec[4];
+  // piece 0 in slot 2 w + 1, piece s > 0 in slot 2 (w + s)
+  auto src = [&](int s, int row) {
+    return p.part + (static_cast<size_t>(s == 0 ? 2 * w + 1 : 2 * (w + s)) * 256 + row) * (HD + 4);
+  };
+  auto out = [&](int row) {
+    const int tok = rec.y + rec.z + row / p.G, head = rec.w * p.G + row % p.G;
+    return p.o + (static_cast<size_t>(tok) * p.Hq + head) * HD;
+  };
+  if (pieces <= 8 && rows > 64) {
+    constexpr int PER = HD / 32;   // float4s of a lane: columns 4 (lane + 8 k)
+    const int l8 = lane & 7;
+    for (int row = (blockIdx.y * 8 + warp) * 4 + (lane >> 3); row < rows; row += gridDim.y * 32) {
+      float M = -INFINITY, L = 0.f;
+      float4 acc[PER];
+#pragma unroll
+      for (int k = 0; k < PER; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+      for (int s = 0; s < pieces; ++s) {
+        const float *x = src(s, row);
+        float4 v[PER];
+#pragma unroll
+        for (int k = 0; k < PER; ++k) v[k] = reinterpret_cast<const float4 *>(x)[l8 + 8 * k];
+        const float2 ml = *reinterpret_cast<const float2 *>(x + HD);
+        if (ml.x == -INFINITY) continue;   // the row saw nothing in this piece
+        const float mn = fmaxf(M, ml.x);
+        const float a = ex2_approx(M - mn), b = ex2_approx(ml.x - mn);
+        M = mn;
+        L = fmaf(L, a, b * ml.y);
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+          acc[k].x = fmaf(acc[k].x, a, b * v[k].x);
+          acc[k].y = fmaf(acc[k].y, a, b * v[k].y);
+          acc[k].z = fmaf(acc[k].z, a, b * v[k].z);
+          acc[k].w = fmaf(acc[k].w, a, b * v[k].w);
+        }
+      }
+      const float inv = 1.f / L;
+      uint2 *dst = reinterpret_cast<uint2 *>(out(row));
+#pragma unroll
+      for (int k = 0; k < PER; ++k)
+        dst[l8 + 8 * k] = make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv), pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+    }
+    return;
+  }
+  constexpr int PER = HD / 32;
+  using Vec = typename std::conditional<HD == 128, float4, float2>::type;
   for (int row = blockIdx.y * 8 + warp; row < rows; row += gridDim.y * 8) {
-    // piece 0 in slot 2 w + 1, piece s > 0 in slot 2 (w + s)
-    auto src = [&](int s) { return p.part + (static_cast<size_t>(s == 0 ? 2 * w + 1 : 2 * (w + s)) * 256 + row) * (HD + 4); };
     float M = -INFINITY;
-    for (int s = lane; s < pieces; s += 32) M = fmaxf(M, src(s)[HD]);
+    for (int s = lane; s < pieces; s += 32) M = fmaxf(M, src(s, row)[HD]);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     float L = 0.f, acc[PER];
@@ -952,8 +1016,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
     for (int s0 = 0; s0 < pieces; s0 += 32) {
       float wgt = 0.f;
       if (s0 + lane < pieces) {
-        const float *x = src(s0 + lane);
-        // (a piece in which the row saw nothing has m = -inf)
+        const float *x = src(s0 + lane, row);
         wgt = x[HD] == -INFINITY ? 0.f : ex2_approx(x[HD] - M);
         L = fmaf(wgt, x[HD + 1], L);
       }
@@ -961,9 +1024,9 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
 #pragma unroll 4
       for (int s = 0; s < ns; ++s) {
         const float ws = __shfl_sync(0xffffffffu, wgt, s);
-        const Vec x = reinterpret_cast<const Vec *>(src(s0 + s))[lane];
+        const Vec x = reinterpret_cast<const Vec *>(src(s0 + s, row))[lane];
         const float *xf = reinterpret_cast<const float *>(&x);
-        // (weight 0: the part may hold anything)
+        // (weight 0: the row saw nothing in the piece)
 #pragma unroll
         for (int k = 0; k < PER; ++k) acc[k] = ws != 0.f ? fmaf(ws, xf[k], acc[k]) : acc[k];
       }
@@ -971,8 +1034,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
     const float inv = 1.f / L;
-    const int tok = t0 + i0 + row / p.G, head = hk * p.G + row % p.G;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + (static_cast<size_t>(tok) * p.Hq + head) * HD + lane * PER);
+    uint32_t *dst = reinterpret_cast<uint32_t *>(out(row) + lane * PER);
 #pragma unroll
     for (int k = 0; k < PER / 2; ++k) dst[k] = pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
   }
