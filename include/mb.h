@@ -396,8 +396,8 @@ int64_t mb_tree_attention_workspace_bytes(void);
  * the argmax.  This keeps the target's distribution: Leviathan et al. 2023,
  * Miao et al. 2024 for trees.  A NaN or -inf logit has probability 0; a row of
  * nothing else gives token 0.  Weights are summed as integer multiples of
- * 2^-40 of the largest, so the result does not depend on how the row is split.
- *   logits       device bf16 [T][vocab], vocab % 8 == 0, 16-byte aligned
+ * 2^-41 of the largest, so the result does not depend on how the row is split.
+ *   logits       device bf16 [T][vocab], vocab % 8 == 0 and at most 2^19, 16-byte aligned
  *   tokens       device int32 [T], the node's token (that of node 0 is not read);
  *                one outside [0, vocab) is refused and records MB_EDEVICE
  *   draft_probs  device fp32 [T][vocab], 16-byte aligned, or NULL

@@ -10,6 +10,7 @@ fails loudly.
 
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import re
@@ -100,8 +101,8 @@ _SIGS = {
     "mb_tree_attention": (_I32, [_VP] * 3 + [_I32] * 6 + [_VP] * 7),
     "mb_tree_attention_workspace_bytes": (_I64, []),
     "mb_verify_tree": (_I32, [_VP, _I32, _VP, _VP, _I32, _I32] + [_VP] * 5 + [_I32] + [_VP] * 4),
-    "mb_kv_compact": (_I32, [ctypes.POINTER(_VP)] + [_I32] * 5 + [_VP] * 6 + [_I32, _VP, _VP]),
-    "mb_kv_copy_pages": (_I32, [ctypes.POINTER(_VP)] + [_I32] * 4 + [c_int32_p, c_int32_p, _I32, _VP]),
+    "mb_kv_compact": (_I32, [_VP] + [_I32] * 5 + [_VP] * 6 + [_I32, _VP, _VP]),
+    "mb_kv_copy_pages": (_I32, [_VP] + [_I32] * 4 + [_VP, _VP, _I32, _VP]),
     "mb_sched_counts": (_I32, [_VP, c_int32_p]),
     "mb_sched_save": (_I32, [_VP, c_int64_p, _I64, c_int64_p]),
     "mb_sched_load": (_I32, [c_int64_p, _I64, ctypes.POINTER(_VP)]),
@@ -138,11 +139,12 @@ def header_symbols() -> list:
 
 
 def _ptr(x) -> Optional[int]:
-    if x is None:
-        return None
-    if hasattr(x, "data_ptr"):
-        return int(x.data_ptr())
-    return int(x)
+    if x is None or type(x) is int:
+        return x
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        return int(x)
 
 
 def _check(st: int) -> None:
@@ -152,6 +154,8 @@ def _check(st: int) -> None:
 
 
 def _i32(a) -> np.ndarray:
+    if type(a) is np.ndarray and a.dtype == np.int32 and a.flags.c_contiguous:
+        return a
     return np.ascontiguousarray(np.asarray(a, dtype=np.int32))
 
 
@@ -320,13 +324,22 @@ def mb_verify_tree(logits, vocab: int, tokens, draft_probs, num_reqs: int, T: in
                                 _ptr(n_accepted), _ptr(path), _ptr(next_token), _ptr(stream)))
 
 
-def _pool_array(pools):
-    return (_VP * len(pools))(*[_ptr(p) for p in pools])
+def _pool_array(pools) -> array.array:
+    """Host array of the pools' device addresses (0 for None)."""
+    try:
+        return array.array("Q", [p.data_ptr() for p in pools])
+    except AttributeError:
+        return array.array("Q", [_ptr(p) or 0 for p in pools])
+
+
+def _addr(a: np.ndarray) -> int:
+    return a.__array_interface__["data"][0]
 
 
 def mb_kv_compact(pools: Sequence, num_pages: int, n_kv_heads: int, head_dim: int, num_reqs: int, qo_indptr, kv_len,
                   bt_indptr, bt, n_accepted, path, max_path: int, new_kv_len, stream=None) -> None:
-    _check(lib().mb_kv_compact(_pool_array(pools), len(pools), num_pages, n_kv_heads, head_dim, num_reqs,
+    bases = _pool_array(pools)
+    _check(lib().mb_kv_compact(bases.buffer_info()[0], len(bases), num_pages, n_kv_heads, head_dim, num_reqs,
                                _ptr(qo_indptr), _ptr(kv_len), _ptr(bt_indptr), _ptr(bt), _ptr(n_accepted), _ptr(path),
                                max_path, _ptr(new_kv_len), _ptr(stream)))
 
@@ -336,8 +349,9 @@ def mb_kv_copy_pages(pools: Sequence, num_pages: int, n_kv_heads: int, head_dim:
     src, dst = _i32(src), _i32(dst)
     if src.ndim != 1 or src.shape != dst.shape:
         raise ValueError("src and dst must be one-dimensional and of equal length")
-    _check(lib().mb_kv_copy_pages(_pool_array(pools), len(pools), num_pages, n_kv_heads, head_dim, _as_i32p(src),
-                                  _as_i32p(dst), len(src), _ptr(stream)))
+    bases = _pool_array(pools)
+    _check(lib().mb_kv_copy_pages(bases.buffer_info()[0], len(bases), num_pages, n_kv_heads, head_dim, _addr(src),
+                                  _addr(dst), len(src), _ptr(stream)))
 
 
 # ------------------------------------------------------------- scheduler

@@ -1195,7 +1195,7 @@ mb_status mb_verify_tree(const void *logits, int32_t vocab, const int32_t *token
   if (temperature && (!u_accept || !u_final))
     return fail(MB_EINVAL, "mb_verify_tree: sampling needs u_accept and u_final");
   if (vocab % 8) return fail(MB_EUNSUPPORTED, "mb_verify_tree: vocab must be a multiple of 8");
-  if (vocab > (1 << 20)) return fail(MB_EUNSUPPORTED, "mb_verify_tree: vocab > 2^20");
+  if (vocab > (1 << 19)) return fail(MB_EUNSUPPORTED, "mb_verify_tree: vocab > 2^19");
   if (num_reqs > (1 << 24)) return fail(MB_EUNSUPPORTED, "mb_verify_tree: num_reqs > 2^24");
   if (reinterpret_cast<uintptr_t>(logits) % 16 || reinterpret_cast<uintptr_t>(draft_probs) % 16)
     return fail(MB_EINVAL, "mb_verify_tree: logits and draft_probs must be 16-byte aligned");

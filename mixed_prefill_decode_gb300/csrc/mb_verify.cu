@@ -19,9 +19,17 @@
 //    passes if u (1 - refused mass) < p(x); a refused token's p becomes 0.
 //  * temperature 0: child x passes if it is the argmax.
 //
-// The walk from node to node is serial and reads one row per accepted node,
-// so a request is given to a cluster of CTAs that shares each row, and the
-// rows of nodes that are never reached are not read.
+// What bounds it: the walk from node to node is serial, and a step of it is the
+// latency of one row (load, maximum and sum, exchange), so a request is given
+// to a cluster of CTAs that shares each row, and the rows of nodes that are
+// never reached are not read.  A thread keeps its part of the row in shared memory
+// (copied asynchronously) between the maximum, the sum and the draw.
+//
+// The tests compare in fp32 (the special-function unit's exponentials); the
+// draw at the end needs accurate weights (mb_fixexp.cuh, some 28 instructions
+// each, for one row per request, two after a refusal with draft
+// probabilities).  A table of the weights of all bf16 logits in shared memory
+// was slower than computing them: its random 8-byte reads took 7 cycles a warp.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -41,8 +49,8 @@ using namespace dev;
 
 constexpr int kVerThreads = 512;
 constexpr int kVerWarps = kVerThreads / 32;
-constexpr int kMaxCluster = 16;
-
+constexpr int kMaxCluster = 8;
+constexpr int kMaxHeld = 17;   // vectors that a thread holds at most: a row of 2^19 logits over 8 CTAs
 struct VerifyParams {
   const __nv_bfloat16 *logits;
   const int32_t *tokens;
@@ -73,29 +81,133 @@ __device__ __forceinline__ void st_cluster64(const void *local, uint32_t rank, i
 
 struct VerifySmem {
   Exchange ex;
-  float tab_hi[32], tab_lo[32];
+  int64_t vec[32 * kMaxHeld];    // the drawing warp: weights of its vectors
+  uint32_t tab_fix[32];
+  float tab_scaled[32];
   float wm[kVerWarps], wz[kVerWarps];
   int32_t wi[kVerWarps];
   int64_t ws[kVerWarps];
   int16_t parent[kMaxTreeNodes];
   int16_t child[kMaxTreeNodes];
+  int32_t token[kMaxTreeNodes];
+  float u[kMaxTreeNodes], logit[kMaxTreeNodes], q[kMaxTreeNodes];   // of the node's token in its parent's rows
   int32_t gone[kMaxTreeNodes];   // refused tokens of the current node (no draft probabilities)
-  int32_t n_child, n_gone, state, next;
-  double a, c;
+  int32_t n_child, n_gone, state;
+  float kh, kl, az_hi, az_lo;
+  int64_t pick;
 };
 
-__global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_constant__ VerifyParams p) {
-  __shared__ VerifySmem sm;
+// (at file scope, so that the functions below address it as shared memory)
+__shared__ VerifySmem sm;
+
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// The larger of two pairs of bf16, a NaN giving way to a number.
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+__device__ __forceinline__ float bf16_of(const uint4 &raw, int e) {
+  const uint32_t w = e < 4 ? (e < 2 ? raw.x : raw.y) : (e < 6 ? raw.z : raw.w);
+  return (e & 1) ? bf16hi(w) : bf16lo(w);
+}
+
+// What a weight depends on beside its logit and draft probability.
+struct WeightCtx {
+  float m, kh, kl;         // weight 2^((l - m) k), k = kh + kl
+  float az_hi, az_lo;      // less az q
+  bool probs;
+  int n_gone;
+};
+
+// Integer weight (multiple of 2^-41) of one logit: 2^((l - m) k), less az q.
+__device__ __forceinline__ int64_t weight_of(const WeightCtx &c, float l, float q) {
+  const int64_t w = fix_exp(l, c.m, c.kh, c.kl, sm.tab_fix, sm.tab_scaled);
+  if (!c.probs) return w;
+  const float ph = fminf(q * c.az_hi, 2.f);   // (from 1 on the weight is 0)
+  const float pl = ph < 2.f ? fmaf(q, c.az_hi, -ph) + q * c.az_lo : 0.f;
+  return max(w - to_fix(ph, pl), static_cast<int64_t>(0));
+}
+
+// Weight of vector v (8 tokens), refused tokens left out.
+__device__ __forceinline__ int64_t vector_weight(const WeightCtx &c, uint4 raw, int v, float4 qa,
+                                              float4 qb) {
+  int64_t sum = weight_of(c, bf16_of(raw, 0), qa.x) + weight_of(c, bf16_of(raw, 1), qa.y) +
+                weight_of(c, bf16_of(raw, 2), qa.z) + weight_of(c, bf16_of(raw, 3), qa.w) +
+                weight_of(c, bf16_of(raw, 4), qb.x) + weight_of(c, bf16_of(raw, 5), qb.y) +
+                weight_of(c, bf16_of(raw, 6), qb.z) + weight_of(c, bf16_of(raw, 7), qb.w);
+  for (int g = 0; g < c.n_gone; ++g) {   // (only without draft probabilities)
+    const int tok = sm.gone[g];
+    if ((tok >> 3) == v) sum -= weight_of(c, bf16_of(raw, tok & 7), 0.f);
+  }
+  return sum;
+}
+
+// A thread's part of the row, and the state of the cluster's exchange.
+struct Part {
+  const uint4 *x;    // held vectors, kVerThreads apart
+  int nk, v0;        // their number, and the first one's place in the row (then every 32nd)
+  int C, rank;
+  int parity;        // exchange buffer of the next round
+};
+
+__device__ __forceinline__ float4 load_q(const float *qrow, int v) {
+  return qrow ? __ldg(reinterpret_cast<const float4 *>(qrow) + v) : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+// Sums of the weights over each warp's part (sm.ws), the CTA's, and (from the
+// exchange) the row's; the sum before this CTA's part goes to *before.  All
+// threads of the cluster.  Out of line: it is called in four places.
+__device__ __noinline__ int64_t weight_sums(Part &t, const WeightCtx &c, const float *qrow, int64_t *before) {
+  __syncthreads();   // sm.ws has been read
+  int64_t sum = 0;
+  float4 qa = make_float4(0.f, 0.f, 0.f, 0.f), qb = qa;
+  if (t.nk > 0) qa = load_q(qrow, 2 * t.v0), qb = load_q(qrow, 2 * t.v0 + 1);
+#pragma unroll 1
+  for (int k = 0; k < t.nk; ++k) {
+    const int v = t.v0 + 32 * k;
+    float4 na = qa, nb = qb;   // the next vector's draft probabilities, in flight meanwhile
+    if (k + 1 < t.nk) na = load_q(qrow, 2 * v + 64), nb = load_q(qrow, 2 * v + 65);
+    sum += vector_weight(c, t.x[k * kVerThreads], v, qa, qb);
+    qa = na, qb = nb;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  if ((threadIdx.x & 31) == 0) sm.ws[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  int64_t mine = 0;
+#pragma unroll
+  for (int w = 0; w < kVerWarps; ++w) mine += sm.ws[w];
+  *before = 0;
+  if (t.C == 1) return mine;
+  if (threadIdx.x < t.C) st_cluster64(&sm.ex.s[t.parity][t.rank], threadIdx.x, mine);
+  cluster_sync();
+  int64_t total = 0;
+  for (int k = 0; k < t.C; ++k) {
+    if (k == t.rank) *before = total;
+    total += sm.ex.s[t.parity][k];
+  }
+  t.parity ^= 1;
+  return total;
+}
+
+__global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_constant__ VerifyParams p) {
+  extern __shared__ __align__(16) uint4 held[];   // vector k of thread t at k kVerThreads + t
   const int C = p.cluster;
   const uint32_t rank = C > 1 ? cluster_ctarank() : 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x < 32) {
-    sm.tab_hi[threadIdx.x] = p.tab.hi[threadIdx.x];
-    sm.tab_lo[threadIdx.x] = p.tab.lo[threadIdx.x];
+    sm.tab_fix[threadIdx.x] = p.tab.fix[threadIdx.x];
+    sm.tab_scaled[threadIdx.x] = p.tab.scaled[threadIdx.x];
   }
   pdl_wait();
   pdl_trigger();
-  cluster_sync();   // every CTA of the cluster runs before one writes into another
+  if (C > 1) cluster_sync();   // every CTA of the cluster runs before one writes into another
   const int r = blockIdx.x / C;
   const int t0 = p.qo_indptr[r], n = p.qo_indptr[r + 1] - t0;
   int32_t *path = p.path + static_cast<int64_t>(r) * p.max_path;
@@ -111,14 +223,29 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_consta
     }
     return;
   }
+  // this CTA's vectors of a row, and this warp's part of them: lane l holds
+  // vectors w0 + l + 32 k, so a warp's sums cover consecutive tokens
+  const int nv = p.vocab / 8;
+  const int c0 = static_cast<int>(static_cast<int64_t>(nv) * rank / C), c1 = static_cast<int>(static_cast<int64_t>(nv) * (rank + 1) / C);
+  const int w0 = c0 + (c1 - c0) * warp / kVerWarps, w1 = c0 + (c1 - c0) * (warp + 1) / kVerWarps;
+  const int nk = (w1 - w0 - lane + 31) / 32;       // this thread's vectors
+  uint4 *x = held + threadIdx.x;
+  auto load_row = [&](int node) {
+    const uint4 *row = reinterpret_cast<const uint4 *>(p.logits + (static_cast<size_t>(t0) + node) * p.vocab);
+    for (int k = 0; k < nk; ++k) cp_async16(x + k * kVerThreads, row + w0 + lane + 32 * k);
+  };
+  load_row(0);
   float temp = p.temperature ? p.temperature[r] : 0.f;
   if (!(temp >= 0.f)) {
     if (threadIdx.x == 0) atomicExch(p.err, kErrBounds);
     temp = 0.f;
   }
   const bool greedy = temp == 0.f;
-  const double kd = greedy ? 0.0 : fmin(1.4426950408889634074 / static_cast<double>(temp), 1e30);
-  const float kh = static_cast<float>(kd), kl = static_cast<float>(kd - static_cast<double>(kh));
+  if (threadIdx.x == 0) {   // (FP64 is slow: one thread's work)
+    const double kd = greedy ? 0.0 : fmin(1.4426950408889634074 / static_cast<double>(temp), 1e30);
+    sm.kh = static_cast<float>(kd);
+    sm.kl = static_cast<float>(kd - static_cast<double>(sm.kh));
+  }
   for (int i = threadIdx.x; i < n; i += kVerThreads) {
     int up = p.parent[t0 + i];
     if (up < -1 || up >= i) {
@@ -126,295 +253,302 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_consta
       up = -1;
     }
     sm.parent[i] = static_cast<int16_t>(up);
+    const int tok = i > 0 ? p.tokens[t0 + i] : 0;
+    if (tok < 0 || tok >= p.vocab) atomicExch(p.err, kErrBounds);
+    sm.token[i] = tok < 0 || tok >= p.vocab ? -1 : tok;
+    sm.u[i] = greedy ? 0.f : p.u_accept[t0 + i];
+    const size_t at = (static_cast<size_t>(t0) + max(up, 0)) * p.vocab + max(sm.token[i], 0);
+    sm.logit[i] = greedy ? 0.f : __bfloat162float(p.logits[at]);
+    sm.q[i] = greedy || !p.probs ? 0.f : p.probs[at];
   }
   __syncthreads();
 
-  // this CTA's vectors (of 8 logits) of a row, and this warp's part of them
-  const int nv = p.vocab / 8;
-  const int c0 = static_cast<int>(static_cast<int64_t>(nv) * rank / C), c1 = static_cast<int>(static_cast<int64_t>(nv) * (rank + 1) / C);
-  const int w0 = c0 + static_cast<int>(static_cast<int64_t>(c1 - c0) * warp / kVerWarps);
-  const int w1 = c0 + static_cast<int>(static_cast<int64_t>(c1 - c0) * (warp + 1) / kVerWarps);
-  int parity = 0;
+  const float kh = sm.kh, kl = sm.kl;
   int cur = 0, len = 1;
 
-  // Integer weights of one vector: e = 2^((l - m) k), less a z q (as
-  // az_hi + az_lo per unit of q) where draft probabilities take part, refused
-  // tokens at 0; in units of 2^-40.
-  auto weights = [&](const uint4 &raw, int v, float m, const float *qrow, float az_hi, float az_lo, int n_gone,
-                     int64_t (&w)[8]) {
-    const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
-    float q[8];
-    if (qrow) {
-      const float4 qa = reinterpret_cast<const float4 *>(qrow)[2 * v], qb = reinterpret_cast<const float4 *>(qrow)[2 * v + 1];
-      q[0] = qa.x, q[1] = qa.y, q[2] = qa.z, q[3] = qa.w, q[4] = qb.x, q[5] = qb.y, q[6] = qb.z, q[7] = qb.w;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float l = (e & 1) ? bf16hi(x[e >> 1]) : bf16lo(x[e >> 1]);
-      float hi, lo;
-      fix_exp(l, m, kh, kl, sm.tab_hi, sm.tab_lo, &hi, &lo);
-      if (qrow) {
-        const float ph = q[e] * az_hi, pl = fmaf(q[e], az_hi, -ph) + q[e] * az_lo;
-        const float d = hi - ph, bb = d - hi;
-        const float de = (hi - (d - bb)) - (ph + bb);
-        lo = de + (lo - pl);
-        hi = d;
-        if (!(hi + lo > 0.f)) hi = lo = 0.f;
-      }
-      w[e] = to_fix(hi, lo);
-      if (w[e] < 0) w[e] = 0;
-    }
-    for (int g = 0; g < n_gone; ++g) {
-      const int tok = sm.gone[g];
-      if ((tok >> 3) == v)
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if ((tok & 7) == e) w[e] = 0;
-    }
-  };
-  // Sums of the weights over this warp's part (sm.ws), this CTA's, and (from
-  // the exchange) the row's; the sum before this CTA's part goes to *before.
-  auto weight_sums = [&](const uint4 *row, float m, const float *qrow, float az_hi, float az_lo, int n_gone,
-                         int64_t *before) -> int64_t {
-    int64_t sum = 0;
-    for (int v = w0 + lane; v < w1; v += 32) {
-      int64_t w[8];
-      weights(row[v], v, m, qrow, az_hi, az_lo, n_gone, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum += w[e];
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (lane == 0) sm.ws[warp] = sum;
-    __syncthreads();
-    int64_t mine = 0;
-#pragma unroll
-    for (int w = 0; w < kVerWarps; ++w) mine += sm.ws[w];
-    if (threadIdx.x < C) st_cluster64(&sm.ex.s[parity][rank], threadIdx.x, mine);
-    cluster_sync();
-    int64_t total = 0, pre = 0;
-    for (int k = 0; k < C; ++k) {
-      if (k == static_cast<int>(rank)) pre = total;
-      total += sm.ex.s[parity][k];
-    }
-    parity ^= 1;
-    *before = pre;
-    return total;
-  };
+  Part part{x, nk, w0 + lane, C, static_cast<int>(rank), 0};
 
   while (true) {
-    const uint4 *row = reinterpret_cast<const uint4 *>(p.logits + (static_cast<size_t>(t0) + cur) * p.vocab);
-    // children of cur, in index order
+    const __nv_bfloat16 *row = p.logits + (static_cast<size_t>(t0) + cur) * p.vocab;
+    // Children of cur, in index order; warp 0's lanes hold the first 32
+    // children's values.
+    int n_child = 0;
+    int c_tok = -1;
+    float c_u = 2.f, c_l = -INFINITY, c_q = 0.f;
+    // the values of 32 children from `first` on (warp 0)
+    auto load_children = [&](int first) {
+      c_tok = -1;
+      if (first + lane < n_child) {
+        const int node = sm.child[first + lane];
+        c_tok = sm.token[node];
+        c_u = sm.u[node];
+        c_l = sm.logit[node];
+        c_q = sm.q[node];
+      }
+    };
     if (warp == 0) {
-      int cnt = 0;
       if (len < p.max_path)
         for (int b = 0; b < n; b += 32) {
           const bool is = b + lane < n && b + lane > 0 && sm.parent[b + lane] == cur;
           const uint32_t mask = __ballot_sync(0xffffffffu, is);
-          if (is) sm.child[cnt + __popc(mask & ((1u << lane) - 1))] = static_cast<int16_t>(b + lane);
-          cnt += __popc(mask);
+          if (is) sm.child[n_child + __popc(mask & ((1u << lane) - 1))] = static_cast<int16_t>(b + lane);
+          n_child += __popc(mask);
         }
-      if (lane == 0) sm.n_child = cnt;
+      if (lane == 0) sm.n_child = n_child;
+      __syncwarp();
+      load_children(0);
     }
-    // the row's maximum (and the lowest index that has it)
-    float bm = -INFINITY;
-    int bi = 0x7fffffff;
-    for (int v = w0 + lane; v < w1; v += 32) {
-      const uint4 raw = row[v];
-      const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float l = (e & 1) ? bf16hi(x[e >> 1]) : bf16lo(x[e >> 1]);
-        if (l > bm) {   // indices ascend within a thread: the first maximum stays
-          bm = l;
-          bi = 8 * v + e;
-        }
+    // the next row is most likely the first child's: its part goes to L2 meanwhile
+    {
+      int node = n;
+      if (len < p.max_path) {
+        const int i0 = cur + 1 + lane;
+        for (int i = i0; i < n && node == n; i += 32)
+          if (sm.parent[i] == cur) node = i;
+        node = __reduce_min_sync(0xffffffffu, node);
+      }
+      if (node < n) {
+        const char *next = reinterpret_cast<const char *>(p.logits + (static_cast<size_t>(t0) + node) * p.vocab) + 16ll * w0;
+        for (int b = 128 * lane; b < 16 * (w1 - w0); b += 128 * 32)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(next + b));
       }
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      const float om = __shfl_xor_sync(0xffffffffu, bm, off);
-      const int oi = __shfl_xor_sync(0xffffffffu, bi, off);
-      if (om > bm || (om == bm && oi < bi)) bm = om, bi = oi;
+    // The row's maximum (and, greedy, the lowest index that has it), with the
+    // sum of 2^((l - max) k) beside it: per thread, warp, CTA, cluster.
+    float bm = -INFINITY, z = 0.f;
+    int bi = 0x7fffffff;
+    cp_async_wait();
+    uint32_t pm = 0xFF80FF80u;   // -inf
+#pragma unroll 2
+    for (int k = 0; k < nk; ++k) {
+      const uint4 v = x[k * kVerThreads];   // (a NaN is passed over)
+      pm = max_bf16x2(max_bf16x2(pm, v.x), max_bf16x2(v.y, max_bf16x2(v.z, v.w)));
     }
-    if (lane == 0) sm.wm[warp] = bm, sm.wi[warp] = bi;
-    __syncthreads();
-    bm = -INFINITY;
-    bi = 0x7fffffff;
+    bm = fmaxf(bf16lo(pm), bf16hi(pm));
+    if (greedy) {
+      for (int k = nk - 1; k >= 0; --k) {
+        const uint4 v = x[k * kVerThreads];
 #pragma unroll
-    for (int w = 0; w < kVerWarps; ++w)
-      if (sm.wm[w] > bm || (sm.wm[w] == bm && sm.wi[w] < bi)) bm = sm.wm[w], bi = sm.wi[w];
-    const int n_child = sm.n_child;
-    float z = 0.f;
-    if (!greedy && n_child > 0) {
-      // sum of 2^((l - bm) k), relative to this CTA's maximum
-      for (int v = w0 + lane; v < w1; v += 32) {
-        const uint4 raw = row[v];
-        const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
+        for (int e = 7; e >= 0; --e)
+          if (bf16_of(v, e) == bm) bi = 8 * (w0 + lane + 32 * k) + e;
+      }
+      if (bm == -INFINITY) bi = 0x7fffffff;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float l = (e & 1) ? bf16hi(x[e >> 1]) : bf16lo(x[e >> 1]);
-          z += l == bm ? 1.f : fmaxf(ex2_approx((l - bm) * kh), 0.f);   // a NaN counts 0
-        }
+      for (int off = 16; off > 0; off >>= 1) {
+        const float om = __shfl_xor_sync(0xffffffffu, bm, off);
+        const int oi = __shfl_xor_sync(0xffffffffu, bi, off);
+        if (om > bm || (om == bm && oi < bi)) bm = om, bi = oi;
+      }
+    } else {
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, off));
+      // relative to the warp's maximum (finite, or -inf: then there is nothing, or +inf: they share)
+      const float ref = fabsf(bm) == INFINITY ? 0.f : bm;
+#pragma unroll 2
+      for (int k = 0; k < nk; ++k) {
+        const uint4 v = x[k * kVerThreads];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z += fmaxf(ex2_approx((bf16_of(v, e) - ref) * kh), 0.f);   // (a NaN counts 0)
+      }
+      if (fabsf(bm) == INFINITY) {
+        z = 0.f;
+        if (bm > 0.f)
+          for (int k = 0; k < nk; ++k)
+            for (int e = 0; e < 8; ++e) z += bf16_of(x[k * kVerThreads], e) == bm ? 1.f : 0.f;
       }
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
-      if (lane == 0) sm.wz[warp] = z;
-      __syncthreads();
-      z = 0.f;
-#pragma unroll
-      for (int w = 0; w < kVerWarps; ++w) z += sm.wz[w];
-      if (bm == -INFINITY) z = 0.f;
     }
-    if (threadIdx.x < C) {
-      st_cluster32(&sm.ex.m[parity][rank], threadIdx.x, __float_as_uint(bm));
-      st_cluster32(&sm.ex.z[parity][rank], threadIdx.x, __float_as_uint(z));
-      st_cluster32(&sm.ex.idx[parity][rank], threadIdx.x, static_cast<uint32_t>(bi));
+    if (lane == 0) sm.wm[warp] = bm, sm.wz[warp] = z, sm.wi[warp] = bi;
+    __syncthreads();
+    n_child = sm.n_child;
+    // n (maximum, sum, index) triples, one per lane: of all together.  Every
+    // warp does it, so nothing has to be told to the others.
+    auto join = [&](float &m, float &s, int &i, int n) {
+      float top_m = m;
+      for (int off = n >> 1; off > 0; off >>= 1) top_m = fmaxf(top_m, __shfl_xor_sync(0xffffffffu, top_m, off));
+      s = m == top_m ? s : m == -INFINITY || top_m == INFINITY ? 0.f : s * ex2_approx((m - top_m) * kh);
+      i = m == top_m ? i : 0x7fffffff;
+      for (int off = n >> 1; off > 0; off >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, off);
+        i = min(i, __shfl_xor_sync(0xffffffffu, i, off));
+      }
+      m = top_m;
+    };
+    float m = sm.wm[lane % kVerWarps], Z = sm.wz[lane % kVerWarps];
+    int top = sm.wi[lane % kVerWarps];
+    join(m, Z, top, kVerWarps);
+    if (C > 1) {
+      if (threadIdx.x < C) {
+        st_cluster32(&sm.ex.m[part.parity][rank], threadIdx.x, __float_as_uint(m));
+        st_cluster32(&sm.ex.z[part.parity][rank], threadIdx.x, __float_as_uint(Z));
+        st_cluster32(&sm.ex.idx[part.parity][rank], threadIdx.x, static_cast<uint32_t>(top));
+      }
+      cluster_sync();
+      m = sm.ex.m[part.parity][lane % C], Z = sm.ex.z[part.parity][lane % C], top = sm.ex.idx[part.parity][lane % C];
+      join(m, Z, top, C);
+      part.parity ^= 1;
     }
-    cluster_sync();
-    float m = -INFINITY;
-    int top = 0x7fffffff;
-    for (int k = 0; k < C; ++k) {
-      const float om = sm.ex.m[parity][k];
-      const int oi = sm.ex.idx[parity][k];
-      if (om > m || (om == m && oi < top)) m = om, top = oi;
-    }
-    float Z = 0.f;
-    for (int k = 0; k < C; ++k) {
-      const float om = sm.ex.m[parity][k];
-      Z += om == m ? sm.ex.z[parity][k] : sm.ex.z[parity][k] * ex2_approx((om - m) * kh);
-    }
-    parity ^= 1;
     if (m == -INFINITY) top = 0;   // no token has a chance: token 0
 
-    // the children's tests: every CTA comes to the same answer
+    // the children's tests, by warp 0: every CTA comes to the same answer
     int taken = -1;
     int64_t total = 0, before = 0;
     int final_gone = 0;
     const float *qrow = nullptr;
-    float az_hi = 0.f, az_lo = 0.f;
+    WeightCtx ctx{m, kh, kl, 0.f, 0.f, p.probs != nullptr, 0};
     bool have_sums = false;
-    if (greedy || m == -INFINITY) {
-      if (greedy)
-        for (int k = 0; k < n_child && taken < 0; ++k)
-          if (p.tokens[t0 + sm.child[k]] == top) taken = sm.child[k];
-      if (taken < 0) {
-        if (rank == 0 && threadIdx.x == 0) p.next_token[r] = top;
-        if (rank == 0 && threadIdx.x == 0) path[len - 1] = cur;
-        break;
-      }
-    } else if (!p.probs) {
-      if (threadIdx.x == 0) {
+    if (rank == 0 && threadIdx.x == 0) path[len - 1] = cur;
+    if (greedy || !p.probs) {
+      if (warp == 0) {
+        int state = -1, n_gone = 0;
         double gone = 0.0;
-        int n_gone = 0;
-        sm.state = -1;
-        for (int k = 0; k < n_child; ++k) {
-          const int node = sm.child[k];
-          const int x = p.tokens[t0 + node];
-          if (x < 0 || x >= p.vocab) {
-            atomicExch(p.err, kErrBounds);
+        for (int first = 0; first < n_child && state < 0; first += 32) {
+          if (first > 0) load_children(first);
+          if (greedy) {
+            const uint32_t hit = __ballot_sync(0xffffffffu, c_tok == top);
+            if (hit) state = sm.child[first + __ffs(hit) - 1];
             continue;
           }
-          bool dup = false;
-          for (int g = 0; g < n_gone; ++g) dup |= sm.gone[g] == x;
-          if (dup) continue;
-          const float l = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(row)[x]);
-          const float e = l == m ? 1.f : fmaxf(ex2_approx((l - m) * kh), 0.f);
-          if (static_cast<double>(p.u_accept[t0 + node]) * (static_cast<double>(Z) - gone) < static_cast<double>(e)) {
-            sm.state = node;
-            break;
+          const float c_e = c_l == m ? 1.f : fmaxf(ex2_approx((c_l - m) * kh), 0.f);
+          // (the lanes' first comparisons at once, while nothing is refused yet)
+          const uint32_t easy = __ballot_sync(0xffffffffu, c_u * Z < c_e);
+          for (int k = 0; k < min(32, n_child - first); ++k) {
+            const int tok = __shfl_sync(0xffffffffu, c_tok, k);
+            const float e = __shfl_sync(0xffffffffu, c_e, k), u = __shfl_sync(0xffffffffu, c_u, k);
+            bool dup = tok < 0;   // an invalid token, or one refused before: it has no chance
+            for (int g = lane; g < n_gone; g += 32) dup |= sm.gone[g] == tok;
+            if (__any_sync(0xffffffffu, dup)) continue;
+            const bool pass = n_gone == 0 ? (easy >> k) & 1u
+                                          : static_cast<double>(u) * (static_cast<double>(Z) - gone) < static_cast<double>(e);
+            if (m != -INFINITY && pass) {
+              state = sm.child[first + k];
+              break;
+            }
+            if (lane == 0) sm.gone[n_gone] = tok;
+            __syncwarp();
+            ++n_gone;
+            gone += static_cast<double>(e);
           }
-          sm.gone[n_gone++] = x;
-          gone += static_cast<double>(e);
         }
-        sm.n_gone = n_gone;
+        if (lane == 0) sm.state = state, sm.n_gone = n_gone;
       }
       __syncthreads();
       taken = sm.state;
       final_gone = sm.n_gone;
-    } else {
+    } else if (m != -INFINITY) {
       const float *q = p.probs + (static_cast<size_t>(t0) + cur) * p.vocab;
-      double a = 0.0, c = 1.0, zd = Z;   // c in units of the row's sum z
+      // a, c and the row's sum z (c in units of z) are warp 0's
+      double a = 0.0, c = 1.0, zd = Z;
       for (int k = 0; k < n_child; ++k) {
-        if (threadIdx.x == 0) {
-          const int node = sm.child[k];
-          const int x = p.tokens[t0 + node];
-          sm.state = 0;
-          if (x < 0 || x >= p.vocab) {
-            atomicExch(p.err, kErrBounds);
-          } else {
-            const float l = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(row)[x]);
-            float hi, lo;
-            fix_exp(l, m, kh, kl, sm.tab_hi, sm.tab_lo, &hi, &lo);
-            const double px = (static_cast<double>(hi) + static_cast<double>(lo)) / zd, qx = q[x];
-            if (static_cast<double>(p.u_accept[t0 + node]) * c * qx < px - a * qx) sm.state = 1;
+        if (warp == 0) {
+          if (k > 0 && k % 32 == 0) load_children(k);
+          int pass = 0;
+          if (k == 0) {
+            pass = c_tok >= 0 && c_u * (c_q * Z) < (c_l == m ? 1.f : fmaxf(ex2_approx((c_l - m) * kh), 0.f));
+          } else if (lane == k % 32 && c_tok >= 0) {   // both sides times z
+            const double ex = static_cast<double>(fix_exp(c_l, m, kh, kl, sm.tab_fix, sm.tab_scaled)) * 0x1p-41;
+            const double qz = static_cast<double>(c_q) * zd;
+            pass = static_cast<double>(c_u) * c * qz < ex - a * qz;
           }
+          if (lane == k % 32) sm.state = pass;
         }
         __syncthreads();
-        const bool pass = sm.state == 1;
-        __syncthreads();
-        if (pass) {
+        if (sm.state != 0) {
           taken = sm.child[k];
           break;
         }
         if (!qrow) {   // the first refusal: the row's sum to full accuracy
-          zd = static_cast<double>(weight_sums(row, m, nullptr, 0.f, 0.f, 0, &before)) * 0x1p-40;
+          ctx.probs = false;
+          const int64_t z = weight_sums(part, ctx, nullptr, &before);
+          ctx.probs = true;
+          if (warp == 0) zd = static_cast<double>(z) * 0x1p-41;
           qrow = q;
         }
-        a += c;
-        const double az = a * zd;
-        az_hi = static_cast<float>(az);
-        az_lo = static_cast<float>(az - static_cast<double>(az_hi));
-        total = weight_sums(row, m, qrow, az_hi, az_lo, 0, &before);
-        c = static_cast<double>(total) * 0x1p-40 / zd;
+        if (warp == 0) {
+          a += c;
+          const double az = a * zd;
+          if (lane == 0) {
+            sm.az_hi = static_cast<float>(az);
+            sm.az_lo = static_cast<float>(az - static_cast<double>(sm.az_hi));
+          }
+        }
+        __syncthreads();
+        ctx.az_hi = sm.az_hi;
+        ctx.az_lo = sm.az_lo;
+        total = weight_sums(part, ctx, qrow, &before);
+        if (warp == 0) c = static_cast<double>(total) * 0x1p-41 / zd;
         have_sums = true;
       }
     }
-    if (rank == 0 && threadIdx.x == 0) path[len - 1] = cur;
     if (taken >= 0) {
       cur = taken;
       ++len;
-      __syncthreads();   // sm.child, sm.gone and sm.state are read before the next node writes them
+      load_row(cur);
+      __syncthreads();   // what this node left in shared memory is read before the next node writes there
       continue;
     }
+    if (greedy || m == -INFINITY) {
+      if (rank == 0 && threadIdx.x == 0) p.next_token[r] = top;
+      break;
+    }
     // none accepted: one token of what is left
-    if (!have_sums) total = weight_sums(row, m, nullptr, 0.f, 0.f, final_gone, &before);
+    if (!have_sums) {
+      ctx.n_gone = final_gone;
+      ctx.probs = false;
+      total = weight_sums(part, ctx, nullptr, &before);
+    }
     if (total == 0) {    // the refusals left nothing: p itself
       qrow = nullptr;
-      final_gone = 0;
-      total = weight_sums(row, m, nullptr, 0.f, 0.f, 0, &before);
+      ctx = {m, kh, kl, 0.f, 0.f, false, 0};
+      total = weight_sums(part, ctx, nullptr, &before);
     }
-    const double uf = static_cast<double>(p.u_final[r]);
-    int64_t pick = uf > 0.0 ? static_cast<int64_t>(fmin(uf, 1.0) * static_cast<double>(total)) : 0;
-    if (pick > total - 1) pick = total - 1;
+    if (threadIdx.x == 0) {
+      const double uf = static_cast<double>(p.u_final[r]);
+      const int64_t at = uf > 0.0 ? static_cast<int64_t>(fmin(uf, 1.0) * static_cast<double>(total)) : 0;
+      sm.pick = min(at, total - 1);
+    }
+    __syncthreads();
+    const int64_t pick = sm.pick;
     // the first token whose cumulative weight is above pick
     int64_t at = before;
     for (int w = 0; w < warp; ++w) at += sm.ws[w];
     if (at <= pick && pick < at + sm.ws[warp]) {
-      for (int v0 = w0; v0 < w1; v0 += 32) {
-        int64_t w[8], sum = 0;
-        const int v = v0 + lane;
-        if (v < w1) {
-          weights(row[v], v, m, qrow, az_hi, az_lo, final_gone, w);
+      // (this warp alone) its vectors' weights, in token order; then 8 lanes'
+      // worth each, the vector, the token
+      const int v0 = w0 + lane, nvec = w1 - w0;
+#pragma unroll 1
+      for (int k = 0; k < nk; ++k) {
+        const int v = v0 + 32 * k;
+        sm.vec[32 * k + lane] = vector_weight(ctx, x[k * kVerThreads], v, load_q(qrow, 2 * v), load_q(qrow, 2 * v + 1));
+      }
+      __syncwarp();
+      const int per = (nvec + 31) / 32, lo = min(nvec, lane * per), hi = min(nvec, lo + per);
+      int64_t sum = 0;
+      for (int i = lo; i < hi; ++i) sum += sm.vec[i];
+      int64_t inc = sum;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sum += w[e];
-        }
-        int64_t inc = sum;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const int64_t o = __shfl_up_sync(0xffffffffu, inc, off);
-          if (lane >= off) inc += o;
-        }
-        int64_t run = at + inc - sum;
-        if (run <= pick && pick < run + sum) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (run <= pick && pick < run + w[e]) p.next_token[r] = 8 * v + e;
-            run += w[e];
+      for (int off = 1; off < 32; off <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += o;
+      }
+      int64_t run = at + inc - sum;
+      if (run <= pick && pick < run + sum) {
+        int i = lo;
+        while (pick >= run + sm.vec[i]) run += sm.vec[i++];
+        const int first = 8 * (w0 + i);
+#pragma unroll 1
+        for (int e = 0; e < 8; ++e) {
+          const int tok = first + e;
+          bool out = false;
+          for (int g = 0; g < ctx.n_gone; ++g) out |= sm.gone[g] == tok;
+          const int64_t w = out ? 0 : weight_of(ctx, __bfloat162float(row[tok]), qrow ? qrow[tok] : 0.f);
+          if (pick < run + w) {
+            p.next_token[r] = tok;
+            break;
           }
+          run += w;
         }
-        at += __shfl_sync(0xffffffffu, inc, 31);
-        if (at > pick) break;
       }
     }
     break;
@@ -444,11 +578,26 @@ cudaError_t verify_tree_run(const VerifyArgs &a, cudaStream_t st) {
   p.vocab = a.vocab;
   p.T = a.T;
   p.max_path = a.max_path;
-  p.cluster = 1;
+  // CTAs per request: enough that a CTA holds at most 32,768 of the row's
+  // logits, then as many as still fit the GPU twice over with at least 4,096
+  // logits each.
+  int cluster = 1;
+  while (cluster < kMaxCluster && a.vocab > cluster * 32768) cluster *= 2;
+  while (cluster < kMaxCluster && static_cast<int64_t>(a.n_reqs) * cluster * 2 <= 2 * device_sm_count() &&
+         a.vocab >= cluster * 2 * 4096)
+    cluster *= 2;
+  p.cluster = cluster;
   static const FixExpTable table = fix_exp_table();
   p.tab = table;
   p.err = a.err;
-  return launch_pdl(verify_kernel, dim3(a.n_reqs * p.cluster), dim3(kVerThreads), 0, st, p.cluster, p);
+  // a warp holds a 16th of the CTA's part, rounded up
+  const int per_cta = (a.vocab / 8 + cluster - 1) / cluster;
+  const int per_thread = ((per_cta + kVerWarps - 1) / kVerWarps + 31) / 32;
+  const int smem = per_thread * kVerThreads * 16;
+  const cudaError_t e = ensure_max_smem(reinterpret_cast<const void *>(verify_kernel), kMaxHeld * kVerThreads * 16);
+  if (e != cudaSuccess) return e;
+  if (per_thread > kMaxHeld) return cudaErrorInvalidValue;
+  return launch_pdl(verify_kernel, dim3(a.n_reqs * cluster), dim3(kVerThreads), smem, st, cluster, p);
 }
 
 }  // namespace mb
