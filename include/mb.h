@@ -164,6 +164,23 @@ mb_status mb_stack_step(mb_stack *stack, mb_kv *const *kvs, const mb_batch *batc
 int32_t mb_stack_last_launches(const mb_stack *stack);
 mb_status mb_stack_destroy(mb_stack *stack);
 
+/* mb_step and mb_stack_step with drafted tokens (see "drafted tokens" below):
+ * parent is a HOST int32 array of T entries, parent[t] the index within its
+ * request of the parent of that request's token t (less than its own index),
+ * or -1 for a token that follows the cached prefix.  Token i is stored in the
+ * cache at place cached + i, rotated for position cached + depth(i) (a root's
+ * depth is 0), and sees the prefix, its ancestors and itself.  A request whose
+ * tokens form a chain (parent[i] = i - 1) is an ordinary prefill chunk or
+ * decode row of any length, so all kinds mix in one batch; any other has at
+ * most MB_MAX_TREE_NODES tokens.  parent == NULL: mb_step, mb_stack_step.  In
+ * mb_layer_timing the trees' attention counts as attn_merge.  Errors: those of
+ * mb_step, MB_EINVAL (a parent out of range), MB_EUNSUPPORTED (too many nodes),
+ * MB_ENOMEM (the first step with trees allocates a workspace). */
+mb_status mb_step_tree(mb_layer *layer, mb_kv *kv, const mb_batch *batch, const int32_t *parent, const void *x_in,
+                       void *x_out, void *stream);
+mb_status mb_stack_step_tree(mb_stack *stack, mb_kv *const *kvs, const mb_batch *batch, const int32_t *parent,
+                             const void *x_in, void *x_out, void *stream);
+
 /* Check a batch descriptor against the rules above, on the host only (no
  * device work; usable without a GPU).  num_pages: pool size; max_tokens: the
  * layer's limit on T.  Errors: MB_EINVAL with a message naming the first
@@ -186,7 +203,8 @@ mb_status mb_layer_buffer(const mb_layer *layer, int32_t which, void **ptr, int6
 /* Per-kernel timing of subsequent steps (CUDA events on the step's stream).
  * mb_layer_timing returns the accumulated milliseconds of each launch kind
  * since enable, in the order: rmsnorm_attn, gemm_qkv, rope_append,
- * attention (prefill-chunk tiles and decode rows, one grid), attn_merge,
+ * attention (prefill-chunk tiles and decode rows, one grid), attn_merge (the
+ * attention of drafted trees),
  * gemm_o, rmsnorm_ffn, gemm_gate_up, gemm_down (n <= 9), and the number of
  * steps timed.  It synchronises on the
  * recorded events. */

@@ -73,6 +73,8 @@ _SIGS = {
     "mb_kv_layout": (_I32, [_VP, c_int64_p, ctypes.POINTER(_VP)]),
     "mb_kv_free": (_I32, [_VP]),
     "mb_step": (_I32, [_VP, _VP, ctypes.POINTER(mb_batch), _VP, _VP, _VP]),
+    "mb_step_tree": (_I32, [_VP, _VP, ctypes.POINTER(mb_batch), c_int32_p, _VP, _VP, _VP]),
+    "mb_stack_step_tree": (_I32, [_VP, ctypes.POINTER(_VP), ctypes.POINTER(mb_batch), c_int32_p, _VP, _VP, _VP]),
     "mb_batch_validate": (_I32, [ctypes.POINTER(mb_batch), _I32, _I32]),
     "mb_device_status": (_I32, [_VP, _VP]),
     "mb_layer_buffer": (_I32, [_VP, _I32, ctypes.POINTER(_VP), c_int64_p]),
@@ -211,6 +213,20 @@ def mb_step(layer: int, kv: int, batch: Batch, x_in, x_out, stream=None) -> None
     _check(lib().mb_step(layer, kv, ctypes.byref(batch.c), _ptr(x_in), _ptr(x_out), _ptr(stream)))
 
 
+def _parents(batch: Batch, parent) -> np.ndarray:
+    parent = _i32(parent)
+    if parent.shape != (int(batch.qo_indptr[-1]),):
+        raise ValueError("parent must have one entry per token of the batch")
+    return parent
+
+
+def mb_step_tree(layer: int, kv: int, batch: Batch, parent, x_in, x_out, stream=None) -> None:
+    """parent: one host int per token (or None: mb_step)."""
+    par = None if parent is None else _parents(batch, parent)
+    _check(lib().mb_step_tree(layer, kv, ctypes.byref(batch.c), None if par is None else _as_i32p(par), _ptr(x_in),
+                              _ptr(x_out), _ptr(stream)))
+
+
 def mb_batch_validate(batch: Batch, num_pages: int, max_tokens: int) -> None:
     _check(lib().mb_batch_validate(ctypes.byref(batch.c), num_pages, max_tokens))
 
@@ -284,6 +300,14 @@ def mb_stack_create(layers: Sequence[int], use_graphs: bool = True) -> int:
 def mb_stack_step(stack: int, kvs: Sequence[int], batch: Batch, x_in, x_out, stream=None) -> None:
     arr = (_VP * len(kvs))(*kvs)
     _check(lib().mb_stack_step(stack, arr, ctypes.byref(batch.c), _ptr(x_in), _ptr(x_out), _ptr(stream)))
+
+
+def mb_stack_step_tree(stack: int, kvs: Sequence[int], batch: Batch, parent, x_in, x_out, stream=None) -> None:
+    """parent: one host int per token (or None: mb_stack_step)."""
+    arr = (_VP * len(kvs))(*kvs)
+    par = None if parent is None else _parents(batch, parent)
+    _check(lib().mb_stack_step_tree(stack, arr, ctypes.byref(batch.c), None if par is None else _as_i32p(par),
+                                    _ptr(x_in), _ptr(x_out), _ptr(stream)))
 
 
 def mb_stack_last_launches(stack: int) -> int:
@@ -434,8 +458,8 @@ class Layer:
         self.handle = mb_layer_create(self.desc, self.w)
         self.kv = mb_kv_alloc(self.handle, num_pages, kv_buf)
 
-    def step(self, batch: Batch, x_in, x_out, stream=None) -> None:
-        mb_step(self.handle, self.kv, batch, x_in, x_out, stream)
+    def step(self, batch: Batch, x_in, x_out, stream=None, parent=None) -> None:
+        mb_step_tree(self.handle, self.kv, batch, parent, x_in, x_out, stream)
 
     def buffer(self, which: int):
         return mb_layer_buffer(self.handle, which)

@@ -223,6 +223,7 @@ struct mb_layer {
   float *part = nullptr;
   size_t part_cap = 0;  // floats, counters included
   size_t ctr_cap = 0;   // 4-byte words of counters at the start
+  void *tree_ws = nullptr;   // workspace of the tree attention (from the first step with trees on)
   // last step
   int32_t last_T = 0;
   int32_t last_launches = 0;
@@ -250,15 +251,16 @@ struct GraphKey {
   int n_reqs, n_tiles, n_items, n_merge, n_chunk_slots, gemm_ctas, dec_workers;
   size_t ctr_cap;
   const void *gws;
-  size_t offs[8];
+  size_t offs[11];
   const void *db, *part, *x_in, *x_out, *kv0;
+  bool trees;
   int dec_sms;
   bool operator==(const GraphKey &o) const {
     return T == o.T && n_reqs == o.n_reqs && n_tiles == o.n_tiles && n_items == o.n_items &&
            n_merge == o.n_merge && n_chunk_slots == o.n_chunk_slots && gemm_ctas == o.gemm_ctas &&
            dec_workers == o.dec_workers &&
            ctr_cap == o.ctr_cap && gws == o.gws &&
-           std::equal(offs, offs + 8, o.offs) && db == o.db && part == o.part &&
+           std::equal(offs, offs + 11, o.offs) && trees == o.trees && db == o.db && part == o.part &&
            x_in == o.x_in && x_out == o.x_out && kv0 == o.kv0 && dec_sms == o.dec_sms;
   }
 };
@@ -295,7 +297,7 @@ mb_status alloc_dev(void **p, size_t bytes, const char *what) {
 }
 
 void free_layer_mem(mb_layer *L) {
-  void *ptrs[] = {L->xn, L->qkv, L->q, L->o, L->h, L->hn, L->a, L->err, L->dblob, L->part};
+  void *ptrs[] = {L->xn, L->qkv, L->q, L->o, L->h, L->hn, L->a, L->err, L->dblob, L->part, L->tree_ws};
   for (void *p : ptrs)
     if (p) cudaFree(p);
   for (auto &s : L->ring) {
@@ -480,7 +482,11 @@ int plan_chunk_units(std::vector<ChunkTile> tiles, int sms, std::vector<ChunkUni
 // work lists live in the uploaded blob, and their sizes.
 struct StepPlan {
   int64_t T = 0;
+  int n_reqs = 0;
   size_t o_qo = 0, o_kv = 0, o_bti = 0, o_bt = 0, o_treq = 0, o_tpos = 0, o_tiles = 0, o_items = 0;
+  // a step with drafted trees: each token's place, parent, and which requests are trees
+  bool trees = false;
+  size_t o_tslot = 0, o_par = 0, o_tree = 0;
   int n_tiles = 0, n_items = 0, n_merge = 0;   // n_tiles: chunk units; n_merge: decode split groups
   int n_chunk_slots = 0;                       // partial slots of split chunk tiles
   int dec_workers = 0;                         // decode worker CTAs the plan is for
@@ -488,10 +494,31 @@ struct StepPlan {
   int64_t upload_bytes = 0;
 };
 
+// Parents of a step's tokens (within their request), against the rules of
+// include/mb.h.  tree[r]: request r is not a plain chain.
+mb_status validate_parents(const mb_batch *b, const int32_t *parent, std::vector<int32_t> *tree, bool *any) {
+  const int n = b->num_reqs;
+  tree->assign(static_cast<size_t>(n), 0);
+  *any = false;
+  for (int r = 0; r < n; ++r) {
+    const int32_t t0 = b->qo_indptr[r], qo = b->qo_indptr[r + 1] - t0;
+    for (int32_t i = 0; i < qo; ++i) {
+      if (parent[t0 + i] < -1 || parent[t0 + i] >= i)
+        return mb::fail(MB_EINVAL, "batch: request %d, token %d has parent %d outside [-1, %d)", r, i, parent[t0 + i], i);
+      if (parent[t0 + i] != i - 1) (*tree)[r] = 1;
+    }
+    if ((*tree)[r] && qo > MB_MAX_TREE_NODES)
+      return mb::fail(MB_EUNSUPPORTED, "batch: request %d is a tree of %d nodes (at most %d)", r, qo, MB_MAX_TREE_NODES);
+    *any |= (*tree)[r] != 0;
+  }
+  return MB_OK;
+}
+
 // Host part of a step: per-token tables, attention work lists (chunk tiles,
 // decode splits, merge list), one upload through `L`'s pinned ring into its
-// device blob.  The batch has been validated.
-mb_status prepare_step(mb_layer *L, const mb_batch *b, int64_t T, cudaStream_t s, StepPlan *plan) {
+// device blob.  The batch has been validated.  parent: host, or null for a
+// step without drafted trees.
+mb_status prepare_step(mb_layer *L, const mb_batch *b, const int32_t *parent, int64_t T, cudaStream_t s, StepPlan *plan) {
   mb::DeviceCtx *ctx = nullptr;
   mb_status st = mb::device_ctx(&ctx);
   if (st != MB_OK) return st;
@@ -499,6 +526,13 @@ mb_status prepare_step(mb_layer *L, const mb_batch *b, int64_t T, cudaStream_t s
   const int n = b->num_reqs;
   const int Hq = d.n_q_heads, Hkv = d.n_kv_heads, hd = d.head_dim, G = Hq / Hkv;
   const int64_t nb = b->bt_indptr[n];
+  std::vector<int32_t> tree;
+  bool trees = false;
+  if (parent && (st = validate_parents(b, parent, &tree, &trees)) != MB_OK) return st;
+  // (the requests of the chunk tiles and decode rows)
+  auto plain = [&](int r) { return !trees || !tree[r]; };
+  if (trees && !L->tree_ws && (st = alloc_dev(&L->tree_ws, mb::tree_workspace_bytes(), "tree attention workspace")) != MB_OK)
+    return st;
   std::vector<int32_t> &hb = L->hbuf;
   hb.clear();
   auto sec = [&](size_t count) {
@@ -508,6 +542,7 @@ mb_status prepare_step(mb_layer *L, const mb_batch *b, int64_t T, cudaStream_t s
   };
   StepPlan &P = *plan;
   P.T = T;
+  P.n_reqs = n;
   // Section order: everything whose size depends only on (n, T, tiles,
   // items) first, the block tables (whose length changes with every prefix)
   // last, so that batches of one geometry share every offset and a captured
@@ -517,6 +552,14 @@ mb_status prepare_step(mb_layer *L, const mb_batch *b, int64_t T, cudaStream_t s
   P.o_bti = sec(n + 1);
   P.o_treq = sec(T);
   P.o_tpos = sec(T);
+  P.trees = trees;
+  if (trees) {
+    P.o_tslot = sec(T);
+    P.o_par = sec(T);
+    P.o_tree = sec(n);
+    std::copy(parent, parent + T, hb.begin() + P.o_par);
+    std::copy(tree.begin(), tree.end(), hb.begin() + P.o_tree);
+  }
   std::copy(b->qo_indptr, b->qo_indptr + n + 1, hb.begin() + P.o_qo);
   std::copy(b->kv_len, b->kv_len + n, hb.begin() + P.o_kv);
   std::copy(b->bt_indptr, b->bt_indptr + n + 1, hb.begin() + P.o_bti);
@@ -526,13 +569,19 @@ mb_status prepare_step(mb_layer *L, const mb_batch *b, int64_t T, cudaStream_t s
     for (int32_t t = t0; t1 > t; ++t) {
       hb[P.o_treq + t] = r;
       hb[P.o_tpos + t] = c + (t - t0);
+      if (trees) {
+        // place cached + index, position cached + depth (its parent's is known)
+        const int32_t up = parent[t];
+        hb[P.o_tslot + t] = c + (t - t0);
+        hb[P.o_tpos + t] = up < 0 ? c : hb[P.o_tpos + t0 + up] + 1;
+      }
     }
   }
   // chunk tiles: 256 query rows (two 128-row tiles) of one q-head each
   std::vector<ChunkTile> tiles;
   for (int r = 0; r < n; ++r) {
     const int32_t qo = b->qo_indptr[r + 1] - b->qo_indptr[r];
-    if (qo > 1) {
+    if (qo > 1 && plain(r)) {
       const int32_t c = b->kv_len[r] - qo;
       for (int32_t i0 = 0; i0 < qo; i0 += 256) {
         const int32_t rows = std::min(256, qo - i0);
@@ -564,7 +613,7 @@ mb_status prepare_step(mb_layer *L, const mb_batch *b, int64_t T, cudaStream_t s
   std::vector<std::pair<int32_t, int32_t>> decs;   // (request, 128-key blocks)
   int64_t dec_blocks = 0;
   for (int r = 0; r < n; ++r) {
-    if (b->qo_indptr[r + 1] - b->qo_indptr[r] != 1) continue;
+    if (b->qo_indptr[r + 1] - b->qo_indptr[r] != 1 || !plain(r)) continue;
     const int32_t nblk = (pages_for(b->kv_len[r]) + 7) / 8;
     decs.push_back({r, nblk});
     dec_blocks += static_cast<int64_t>(nblk) * Hkv;
@@ -745,6 +794,7 @@ mb_status launch_layer(mb_layer *L, mb_layer *W, mb_kv *kv, const StepPlan &P, c
   ra.pool = kv->base;
   ra.tok_req = db + P.o_treq;
   ra.tok_pos = db + P.o_tpos;
+  ra.tok_slot = P.trees ? db + P.o_tslot : nullptr;
   ra.bt_indptr = db + P.o_bti;
   ra.bt = db + P.o_bt;
   ra.g_q = L->w.g_q;
@@ -795,7 +845,13 @@ mb_status launch_layer(mb_layer *L, mb_layer *W, mb_kv *kv, const StepPlan &P, c
   if ((st = chk(mb::attention_run(aa, s), "attention")) != MB_OK) return st;
   *launches += (aa.n_tiles + aa.n_items) > 0;
   mark(4);
-  // (split merging happens inside the attention launch)
+  // (split merging happens inside the attention launch; drafted trees have one of their own)
+  if (P.trees) {
+    mb::TreeArgs ta = {W->q, kv->base, W->o, db + P.o_qo, db + P.o_kv, db + P.o_bti, db + P.o_bt, db + P.o_par,
+                       P.n_reqs, Ti, Hq, Hkv, hd, kv->num_pages, W->tree_ws, W->err, db + P.o_tree};
+    if ((st = chk(mb::tree_attention_run(ta, s), "tree attention")) != MB_OK) return st;
+    *launches += 2;
+  }
   mark(5);
   if ((st = chk(mb::gemm_run(W->o, L->w.w_o, &L->tm_wo, W->h, x_in, Ti, d.d_model, hqd, mb::kEpiResidual, W->gws,
                              W->err, s), "gemm o")) != MB_OK)
@@ -1273,6 +1329,11 @@ mb_status mb_kv_copy_pages(void *const *pools, int32_t n_pools, int32_t num_page
 
 // ------------------------------------------------------------------ step
 mb_status mb_step(mb_layer *L, mb_kv *kv, const mb_batch *b, const void *x_in, void *x_out, void *stream) {
+  return mb_step_tree(L, kv, b, nullptr, x_in, x_out, stream);
+}
+
+mb_status mb_step_tree(mb_layer *L, mb_kv *kv, const mb_batch *b, const int32_t *parent, const void *x_in, void *x_out,
+                       void *stream) {
   if (!L || !kv || !b || !x_in || !x_out) return fail(MB_EINVAL, "mb_step: null argument");
   if (kv->layer != L) return fail(MB_EINVAL, "mb_step: kv pool belongs to another layer");
   if (x_in == x_out) return fail(MB_EINVAL, "mb_step: x_out must not alias x_in");
@@ -1293,7 +1354,7 @@ mb_status mb_step(mb_layer *L, mb_kv *kv, const mb_batch *b, const void *x_in, v
   if (st != MB_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   StepPlan plan;
-  if ((st = prepare_step(L, b, T, s, &plan)) != MB_OK) return st;
+  if ((st = prepare_step(L, b, parent, T, s, &plan)) != MB_OK) return st;
   EventSet *es = nullptr;
   if (L->timing) {
     if (L->ev_used == 4096 && (st = flush_timing(L)) != MB_OK) return st;
@@ -1348,6 +1409,11 @@ mb_status mb_stack_create(mb_layer *const *layers, int32_t n_layers, int32_t use
 
 mb_status mb_stack_step(mb_stack *S, mb_kv *const *kvs, const mb_batch *b, const void *x_in, void *x_out,
                         void *stream) {
+  return mb_stack_step_tree(S, kvs, b, nullptr, x_in, x_out, stream);
+}
+
+mb_status mb_stack_step_tree(mb_stack *S, mb_kv *const *kvs, const mb_batch *b, const int32_t *parent,
+                             const void *x_in, void *x_out, void *stream) {
   if (!S || !kvs || !b || !x_in || !x_out) return fail(MB_EINVAL, "mb_stack_step: null argument");
   if (x_in == x_out) return fail(MB_EINVAL, "mb_stack_step: x_out must not alias x_in");
   if (reinterpret_cast<uintptr_t>(x_in) % 16 || reinterpret_cast<uintptr_t>(x_out) % 16)
@@ -1373,7 +1439,7 @@ mb_status mb_stack_step(mb_stack *S, mb_kv *const *kvs, const mb_batch *b, const
   if (st != MB_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   StepPlan plan;
-  if ((st = prepare_step(L0, b, T, s, &plan)) != MB_OK) return st;
+  if ((st = prepare_step(L0, b, parent, T, s, &plan)) != MB_OK) return st;
 
   // Every launch of the L layers depends on the batch only through the
   // plan's sizes and the (fixed) buffers, so one captured graph serves every
@@ -1391,9 +1457,10 @@ mb_status mb_stack_step(mb_stack *S, mb_kv *const *kvs, const mb_batch *b, const
   key.gemm_ctas = L0->gws.max_ctas;   // every layer's GEMMs run on layer 0's workspace
   key.dec_workers = plan.dec_workers;
   key.gws = L0->gws.partials;
-  const size_t offs[8] = {plan.o_qo, plan.o_kv, plan.o_bti, plan.o_bt, plan.o_treq, plan.o_tpos, plan.o_tiles,
-                          plan.o_items};
-  std::copy(offs, offs + 8, key.offs);
+  const size_t offs[11] = {plan.o_qo,    plan.o_kv,    plan.o_bti,   plan.o_bt,  plan.o_treq, plan.o_tpos,
+                           plan.o_tiles, plan.o_items, plan.o_tslot, plan.o_par, plan.o_tree};
+  std::copy(offs, offs + 11, key.offs);
+  key.trees = plan.trees;
   key.db = plan.db;
   key.part = L0->part;
   key.x_in = x_in;

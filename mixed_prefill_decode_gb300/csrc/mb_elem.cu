@@ -113,7 +113,7 @@ struct RopeParams {
   const __nv_bfloat16 *qkv;
   __nv_bfloat16 *q_out;
   __nv_bfloat16 *pool;
-  const int32_t *tok_req, *tok_pos, *bt_indptr, *bt;
+  const int32_t *tok_req, *tok_pos, *tok_slot, *bt_indptr, *bt;
   const __nv_bfloat16 *g_q, *g_k;
   int Hq, Hkv, qk_norm, num_pages;
   float eps;
@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopePar
   };
   load_round(0);
   const int pos = p.tok_pos[t];
+  const int place = p.tok_slot ? p.tok_slot[t] : pos;   // (a drafted node's position is its depth's)
   for (int i = threadIdx.x; i < HALF; i += kRopeThreads) {
     const float fp = static_cast<float>(pos);
     const float hi = fp * p.f_hi[i];
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopePar
   }
   if (threadIdx.x == kRopeThreads - 32) {   // the last warp looks the page up
     const int req = p.tok_req[t];
-    const int page = p.bt[p.bt_indptr[req] + pos / kPage];
+    const int page = p.bt[p.bt_indptr[req] + place / kPage];
     s_page = (page < 0 || page >= p.num_pages) ? -1 : page;
   }
   __syncthreads();
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopePar
     if (threadIdx.x == 0) atomicExch(p.err, kErrBounds);
     return;
   }
-  const int slot = pos % kPage;
+  const int slot = place % kPage;
   for (int base = 0; base < heads; base += NW * MAXH) {
     if (base > 0) load_round(base);
 #pragma unroll
@@ -356,6 +357,7 @@ cudaError_t rope_append_run(const RopeArgs &a, cudaStream_t st) {
   p.pool = static_cast<__nv_bfloat16 *>(a.pool);
   p.tok_req = a.tok_req;
   p.tok_pos = a.tok_pos;
+  p.tok_slot = a.tok_slot;
   p.bt_indptr = a.bt_indptr;
   p.bt = a.bt;
   p.g_q = static_cast<const __nv_bfloat16 *>(a.g_q);

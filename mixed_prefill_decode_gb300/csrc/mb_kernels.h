@@ -63,7 +63,8 @@ struct RopeArgs {
   void *q_out;              // [T][Hq][hd] bf16
   void *pool;               // [P][2][Hkv][16][hd] bf16
   const int32_t *tok_req;   // [T] request of each token
-  const int32_t *tok_pos;   // [T] absolute position of each token
+  const int32_t *tok_pos;   // [T] absolute position of each token (its rotation)
+  const int32_t *tok_slot;  // [T] place of each token in its request's cache, or null: its position
   const int32_t *bt_indptr; // [n+1]
   const int32_t *bt;        // block tables
   const void *g_q, *g_k;    // [hd] bf16 or null
@@ -115,6 +116,7 @@ struct TreeArgs {
   int n_reqs, T, Hq, Hkv, hd, num_pages;
   void *workspace;          // tree_workspace_bytes()
   int *err;
+  const int32_t *is_tree = nullptr;   // [n_reqs], or null: requests to leave alone hold 0
 };
 size_t tree_workspace_bytes();
 cudaError_t tree_attention_run(const TreeArgs &a, cudaStream_t st);

@@ -73,7 +73,7 @@ constexpr int kCost1 = 2, kCost2 = 3, kCostUnit = 3, kMinShare = 3;
 struct TreeParams {
   __nv_bfloat16 *o;
   const __nv_bfloat16 *q, *pool;
-  const int32_t *qo_indptr, *kv_len, *bt_indptr, *bt, *parent;
+  const int32_t *qo_indptr, *kv_len, *bt_indptr, *bt, *parent, *is_tree;
   int n_reqs, T, Hq, Hkv, G, num_pages;
   float scale_log2;
   int32_t *rec;
@@ -150,10 +150,10 @@ struct Ctrl {
 
 // Its words of the descriptor (loaded well before they are worked on).
 struct RawReq {
-  int q0, q1, kv, b0, b1;
+  int q0, q1, kv, b0, b1, tree;
 };
 __device__ __forceinline__ RawReq load_raw(const TreeParams &p, int r) {
-  return {p.qo_indptr[r], p.qo_indptr[r + 1], p.kv_len[r], p.bt_indptr[r], p.bt_indptr[r + 1]};
+  return {p.qo_indptr[r], p.qo_indptr[r + 1], p.kv_len[r], p.bt_indptr[r], p.bt_indptr[r + 1], p.is_tree ? p.is_tree[r] : 1};
 }
 
 // (an invalid request costs nothing: it is skipped and reported)
@@ -166,7 +166,8 @@ __device__ __forceinline__ Req make_req(const TreeParams &p, const RawReq x, boo
   const int pages = x.b1 - x.b0;
   *bad = q.t0 < 0 || q.n < 0 || q.n > kMaxTreeNodes || q.t0 + q.n > p.T || q.kv < q.n || q.kv > (1 << 24) || q.b0 < 0 ||
          (q.kv + kPage - 1) / kPage > pages;
-  if (*bad) q.n = 0;
+  *bad = *bad && x.tree;
+  if (*bad || !x.tree) q.n = 0;
   q.nkb = (q.kv + 127) / 128;
   const int nt2 = 2 * (128 / p.G);
   q.full = q.n / nt2;
@@ -1066,6 +1067,7 @@ cudaError_t tree_attention_run(const TreeArgs &a, cudaStream_t st) {
   p.bt_indptr = a.bt_indptr;
   p.bt = a.bt;
   p.parent = a.parent;
+  p.is_tree = a.is_tree;
   p.n_reqs = a.n_reqs;
   p.T = a.T;
   p.Hq = a.Hq;
