@@ -20,6 +20,7 @@
 #include "mb.h"
 #include "mb_internal.h"
 #include "mb_kernels.h"
+#include "mb_spec.h"
 
 
 namespace mb {
@@ -91,6 +92,11 @@ cudaError_t encode_tmap(CUtensorMap *map, const void *base, int rank, const uint
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t encode_tmap_5d(CUtensorMap *map, const void *base, const uint64_t dims[5], const uint64_t strides_bytes[4],
+                           const uint32_t box[5]) {
+  return encode_tmap(map, base, 5, dims, strides_bytes, box);
+}
+
 // The attention kernels fetch one (page, K or V, head) block of 16 x hd per
 // copy, as a 5-D view: (64 hd elements, 8 slots, hd/64 halves, 2 slot
 // groups, page*2*Hkv + kv*Hkv + head).  In shared memory that lands as
@@ -102,7 +108,7 @@ cudaError_t encode_kv_tmap(CUtensorMap *map, const void *base, uint64_t blocks, 
   const uint64_t dims[5] = {64, 8, nh, kPage / 8, blocks};
   const uint64_t strides[4] = {h * 2, 128, 8 * h * 2, kPage * h * 2};
   const uint32_t box[5] = {64, 8, static_cast<uint32_t>(nh), kPage / 8, 1};
-  return encode_tmap(map, base, 5, dims, strides, box);
+  return encode_tmap_5d(map, base, dims, strides, box);
 }
 
 // ------------------------------------------------------ per-device context
@@ -794,7 +800,6 @@ mb_status launch_layer(mb_layer *L, mb_layer *W, mb_kv *kv, const StepPlan &P, c
   ra.pool = kv->base;
   ra.tok_req = db + P.o_treq;
   ra.tok_pos = db + P.o_tpos;
-  ra.tok_slot = P.trees ? db + P.o_tslot : nullptr;
   ra.bt_indptr = db + P.o_bti;
   ra.bt = db + P.o_bt;
   ra.g_q = L->w.g_q;
@@ -808,7 +813,9 @@ mb_status launch_layer(mb_layer *L, mb_layer *W, mb_kv *kv, const StepPlan &P, c
   ra.eps = d.rms_eps;
   ra.theta = d.rope_theta;
   ra.err = W->err;
-  if ((st = chk(mb::rope_append_run(ra, s), "rope/append")) != MB_OK) return st;
+  if ((st = chk(P.trees ? mb::rope_append_tree_run(ra, db + P.o_tslot, s) : mb::rope_append_run(ra, s),
+                "rope/append")) != MB_OK)
+    return st;
   ++*launches;
   mark(3);
   CUtensorMap tm_q, tm_qd;

@@ -11,6 +11,7 @@
 #include <cstdint>
 
 #include "mb_kernels.h"
+#include "mb_spec.h"
 #include "mb_launch.cuh"
 #include "mb_ptx.cuh"
 
@@ -349,7 +350,9 @@ cudaError_t embed_rows_run(const void *table, int vocab, int d, const int32_t *i
                     vocab, d, ids, static_cast<__nv_bfloat16 *>(out), err);
 }
 
-cudaError_t rope_append_run(const RopeArgs &a, cudaStream_t st) {
+cudaError_t rope_append_run(const RopeArgs &a, cudaStream_t st) { return rope_append_tree_run(a, nullptr, st); }
+
+cudaError_t rope_append_tree_run(const RopeArgs &a, const int32_t *tok_slot, cudaStream_t st) {
   if (a.T <= 0) return cudaSuccess;
   RopeParams p;
   p.qkv = static_cast<const __nv_bfloat16 *>(a.qkv);
@@ -357,7 +360,7 @@ cudaError_t rope_append_run(const RopeArgs &a, cudaStream_t st) {
   p.pool = static_cast<__nv_bfloat16 *>(a.pool);
   p.tok_req = a.tok_req;
   p.tok_pos = a.tok_pos;
-  p.tok_slot = a.tok_slot;
+  p.tok_slot = tok_slot;
   p.bt_indptr = a.bt_indptr;
   p.bt = a.bt;
   p.g_q = static_cast<const __nv_bfloat16 *>(a.g_q);

@@ -8,9 +8,9 @@
 #include <algorithm>
 #include <cstdint>
 
-#include "mb_kernels.h"
 #include "mb_launch.cuh"
 #include "mb_ptx.cuh"
+#include "mb_spec.h"
 
 namespace mb {
 namespace {

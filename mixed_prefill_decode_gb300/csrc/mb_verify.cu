@@ -38,9 +38,9 @@
 #include <cstdint>
 
 #include "mb_fixexp.cuh"
-#include "mb_kernels.h"
 #include "mb_launch.cuh"
 #include "mb_ptx.cuh"
+#include "mb_spec.h"
 
 namespace mb {
 namespace {
