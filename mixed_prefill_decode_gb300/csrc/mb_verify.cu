@@ -93,7 +93,7 @@ struct VerifySmem {
   float u[kMaxTreeNodes], logit[kMaxTreeNodes], q[kMaxTreeNodes];   // of the node's token in its parent's rows
   int32_t gone[kMaxTreeNodes];   // refused tokens of the current node (no draft probabilities)
   int32_t n_child, n_gone, state;
-  float kh, kl, az_hi, az_lo;
+  float kh, kl, az_hi, az_lo, u_final;
   int64_t pick;
 };
 
@@ -120,38 +120,106 @@ __device__ __forceinline__ float bf16_of(const uint4 &raw, int e) {
 // What a weight depends on beside its logit and draft probability.
 struct WeightCtx {
   float m, kh, kl;         // weight 2^((l - m) k), k = kh + kl
+  float d_max;             // m - l from which on it is 2^-48
   float az_hi, az_lo;      // less az q
   bool probs;
   int n_gone;
 };
 
-// Integer weight (multiple of 2^-41) of one logit: 2^((l - m) k), less az q.
-__device__ __forceinline__ int64_t weight_of(const WeightCtx &c, float l, float q) {
-  const int64_t w = fix_exp(l, c.m, c.kh, c.kl, sm.tab_fix, sm.tab_scaled);
-  if (!c.probs) return w;
-  const float ph = fminf(q * c.az_hi, 2.f);   // (from 1 on the weight is 0)
-  const float pl = ph < 2.f ? fmaf(q, c.az_hi, -ph) + q * c.az_lo : 0.f;
-  return max(w - to_fix(ph, pl), static_cast<int64_t>(0));
+// Two weights as fix_exp computes them, in packed fp32: v 2^(11 - s) in units
+// of 2^-41.  D: m - l.
+__device__ __forceinline__ void weight_pair(const WeightCtx &c, float2 D, uint32_t (&v)[2], int32_t (&s)[2]) {
+  constexpr float kMagic = 12582912.f;      // 1.5 2^23
+  constexpr int32_t kMagicBits = 0x4B400000;
+  auto both = [](float x) { return make_float2(x, x); };
+  D.x = fminf(D.x, c.d_max);   // (an infinity, a NaN: 2^-48, which rounds to 0)
+  D.y = fminf(D.y, c.d_max);
+  const float2 y = __fmul2_rn(D, both(-c.kh));                                   // y - r = -D k
+  const float2 r = __ffma2_rn(D, both(c.kl), __ffma2_rn(D, both(c.kh), y));
+  const float2 t = __ffma2_rn(y, both(32.f), both(kMagic));
+  const float2 n = __fadd2_rn(t, both(-kMagic));
+  const float2 f = __ffma2_rn(r, both(-1.f), __ffma2_rn(n, both(-0.03125f), y));
+  float2 g = __ffma2_rn(f, both(0.0096181291f), both(0.0555041087f));
+  g = __ffma2_rn(g, f, both(0.2402265070f));
+  g = __ffma2_rn(g, f, both(0.6931471806f));
+  g = __fmul2_rn(g, f);
+  const int32_t t0 = __float_as_int(t.x), t1 = __float_as_int(t.y);
+  s[0] = (kMagicBits - t0 + 31) >> 5;
+  s[1] = (kMagicBits - t1 + 31) >> 5;
+  v[0] = sm.tab_fix[t0 & 31] + static_cast<uint32_t>(__float2int_rn(sm.tab_scaled[t0 & 31] * g.x));
+  v[1] = sm.tab_fix[t1 & 31] + static_cast<uint32_t>(__float2int_rn(sm.tab_scaled[t1 & 31] * g.y));
 }
 
-// Weight of vector v (8 tokens), refused tokens left out.
-__device__ __forceinline__ int64_t vector_weight(const WeightCtx &c, uint4 raw, int v, float4 qa,
-                                              float4 qb) {
-  int64_t sum = weight_of(c, bf16_of(raw, 0), qa.x) + weight_of(c, bf16_of(raw, 1), qa.y) +
-                weight_of(c, bf16_of(raw, 2), qa.z) + weight_of(c, bf16_of(raw, 3), qa.w) +
-                weight_of(c, bf16_of(raw, 4), qb.x) + weight_of(c, bf16_of(raw, 5), qb.y) +
-                weight_of(c, bf16_of(raw, 6), qb.z) + weight_of(c, bf16_of(raw, 7), qb.w);
-  for (int g = 0; g < c.n_gone; ++g) {   // (only without draft probabilities)
-    const int tok = sm.gone[g];
-    if ((tok >> 3) == v) sum -= weight_of(c, bf16_of(raw, tok & 7), 0.f);
+// The weight from v and s: in 32 bits if it is below 2^-11 (s >= 12), in 64.
+__device__ __forceinline__ int32_t small_weight(uint32_t v, int32_t s) {
+  return static_cast<int32_t>(((v >> min(s - 12, 31)) + 1) >> 1);
+}
+__device__ __forceinline__ int64_t large_weight(uint32_t v, int32_t s) {
+  return static_cast<int64_t>((((static_cast<uint64_t>(v) << 12) >> s) + 1) >> 1);
+}
+// az q in units of 2^-41, beside a small weight (at most 2^30, more than any of
+// them) and beside any (at most 2, more than any).
+template <typename Int>
+__device__ __forceinline__ Int fixed_q(const WeightCtx &c, float q) {
+  constexpr float kTop = sizeof(Int) == 4 ? 0x1p-11f : 2.f;
+  const float h = q * c.az_hi, l = fmaf(q, c.az_hi, -h) + q * c.az_lo;
+  return h < kTop ? static_cast<Int>(to_fix(h, l)) : static_cast<Int>(kTop * 0x1p41f);
+}
+
+// Weights of two tokens together (probs: q0, q1), in 32 or 64 bits.
+__device__ __forceinline__ int64_t pair_weight(const WeightCtx &c, float2 D, float q0, float q1) {
+  uint32_t v[2];
+  int32_t s[2];
+  weight_pair(c, D, v, s);
+  if (__any_sync(0xffffffffu, min(s[0], s[1]) < 12)) {
+    const int64_t w0 = large_weight(v[0], s[0]), w1 = large_weight(v[1], s[1]);
+    if (!c.probs) return w0 + w1;
+    return max(w0 - fixed_q<int64_t>(c, q0), static_cast<int64_t>(0)) + max(w1 - fixed_q<int64_t>(c, q1), static_cast<int64_t>(0));
   }
+  const int32_t w0 = small_weight(v[0], s[0]), w1 = small_weight(v[1], s[1]);
+  if (!c.probs) return static_cast<uint32_t>(w0) + static_cast<uint32_t>(w1);
+  return static_cast<uint32_t>(max(w0 - fixed_q<int32_t>(c, q0), 0)) + static_cast<uint32_t>(max(w1 - fixed_q<int32_t>(c, q1), 0));
+}
+
+// m - l, with a row's infinities in order: l = m gives 0, less than m = +inf everything.
+__device__ __forceinline__ float below(const WeightCtx &c, float l) { return l == c.m ? 0.f : c.m - l; }
+
+// The weight of one token (any lane by itself).
+__device__ __noinline__ int64_t token_weight(const WeightCtx &c, float l, float q) {
+  uint32_t v[2];
+  int32_t s[2];
+  weight_pair(c, make_float2(below(c, l), 0.f), v, s);
+  const int64_t w = large_weight(v[0], s[0]);
+  return c.probs ? max(w - fixed_q<int64_t>(c, q), static_cast<int64_t>(0)) : w;
+}
+
+// Weight of vector v (8 tokens, at x), refused tokens left out.  By all lanes
+// of a warp (live: the lane has such a vector).
+__device__ __forceinline__ int64_t vector_weight(const WeightCtx &c, const uint4 *x, int v, bool live, float4 qa, float4 qb) {
+  const uint4 raw = live ? *x : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);   // -inf
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  const float q[8] = {qa.x, qa.y, qa.z, qa.w, qb.x, qb.y, qb.z, qb.w};
+  int64_t sum = 0;
+  if (c.m < INFINITY) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      sum += pair_weight(c, make_float2(c.m - bf16lo(w[e]), c.m - bf16hi(w[e])), q[2 * e], q[2 * e + 1]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum += token_weight(c, bf16_of(raw, e), q[e]);
+  }
+  if (live)
+    for (int g = 0; g < c.n_gone; ++g) {   // (only without draft probabilities)
+      const int tok = sm.gone[g];
+      if ((tok >> 3) == v) sum -= token_weight(c, __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(x)[tok & 7]), 0.f);
+    }
   return sum;
 }
 
 // A thread's part of the row, and the state of the cluster's exchange.
 struct Part {
   const uint4 *x;    // held vectors, kVerThreads apart
-  int nk, v0;        // their number, and the first one's place in the row (then every 32nd)
+  int nk, nk_warp, v0;   // their number, the most of a lane, and the first one's place in the row (then every 32nd)
   int C, rank;
   int parity;        // exchange buffer of the next round
 };
@@ -169,11 +237,11 @@ __device__ __noinline__ int64_t weight_sums(Part &t, const WeightCtx &c, const f
   float4 qa = make_float4(0.f, 0.f, 0.f, 0.f), qb = qa;
   if (t.nk > 0) qa = load_q(qrow, 2 * t.v0), qb = load_q(qrow, 2 * t.v0 + 1);
 #pragma unroll 1
-  for (int k = 0; k < t.nk; ++k) {
+  for (int k = 0; k < t.nk_warp; ++k) {
     const int v = t.v0 + 32 * k;
     float4 na = qa, nb = qb;   // the next vector's draft probabilities, in flight meanwhile
     if (k + 1 < t.nk) na = load_q(qrow, 2 * v + 64), nb = load_q(qrow, 2 * v + 65);
-    sum += vector_weight(c, t.x[k * kVerThreads], v, qa, qb);
+    sum += vector_weight(c, t.x + k * kVerThreads, v, k < t.nk, qa, qb);
     qa = na, qb = nb;
   }
 #pragma unroll
@@ -242,7 +310,8 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
   }
   const bool greedy = temp == 0.f;
   if (threadIdx.x == 0) {   // (FP64 is slow: one thread's work)
-    const double kd = greedy ? 0.0 : fmin(1.4426950408889634074 / static_cast<double>(temp), 1e30);
+    const double kd = greedy ? 0.0 : fmax(fmin(1.4426950408889634074 / static_cast<double>(temp), 1e30), 1e-30);
+    sm.u_final = greedy ? 0.f : p.u_final[r];
     sm.kh = static_cast<float>(kd);
     sm.kl = static_cast<float>(kd - static_cast<double>(sm.kh));
   }
@@ -263,10 +332,10 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
   }
   __syncthreads();
 
-  const float kh = sm.kh, kl = sm.kl;
+  const float kh = sm.kh, kl = sm.kl, d_max = fminf(48.f / fmaxf(kh, 1e-30f), 3e38f);
   int cur = 0, len = 1;
 
-  Part part{x, nk, w0 + lane, C, static_cast<int>(rank), 0};
+  Part part{x, nk, (w1 - w0 + 31) / 32, w0 + lane, C, static_cast<int>(rank), 0};
 
   while (true) {
     const __nv_bfloat16 *row = p.logits + (static_cast<size_t>(t0) + cur) * p.vocab;
@@ -396,7 +465,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
     int64_t total = 0, before = 0;
     int final_gone = 0;
     const float *qrow = nullptr;
-    WeightCtx ctx{m, kh, kl, 0.f, 0.f, p.probs != nullptr, 0};
+    WeightCtx ctx{m, kh, kl, d_max, 0.f, 0.f, p.probs != nullptr, 0};
     bool have_sums = false;
     if (rank == 0 && threadIdx.x == 0) path[len - 1] = cur;
     if (greedy || !p.probs) {
@@ -500,11 +569,11 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
     }
     if (total == 0) {    // the refusals left nothing: p itself
       qrow = nullptr;
-      ctx = {m, kh, kl, 0.f, 0.f, false, 0};
+      ctx = {m, kh, kl, d_max, 0.f, 0.f, false, 0};
       total = weight_sums(part, ctx, nullptr, &before);
     }
     if (threadIdx.x == 0) {
-      const double uf = static_cast<double>(p.u_final[r]);
+      const double uf = static_cast<double>(sm.u_final);
       const int64_t at = uf > 0.0 ? static_cast<int64_t>(fmin(uf, 1.0) * static_cast<double>(total)) : 0;
       sm.pick = min(at, total - 1);
     }
@@ -518,9 +587,10 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
       // worth each, the vector, the token
       const int v0 = w0 + lane, nvec = w1 - w0;
 #pragma unroll 1
-      for (int k = 0; k < nk; ++k) {
+      for (int k = 0; k < part.nk_warp; ++k) {
         const int v = v0 + 32 * k;
-        sm.vec[32 * k + lane] = vector_weight(ctx, x[k * kVerThreads], v, load_q(qrow, 2 * v), load_q(qrow, 2 * v + 1));
+        const float *q = k < nk ? qrow : nullptr;
+        sm.vec[32 * k + lane] = vector_weight(ctx, x + k * kVerThreads, v, k < nk, load_q(q, 2 * v), load_q(q, 2 * v + 1));
       }
       __syncwarp();
       const int per = (nvec + 31) / 32, lo = min(nvec, lane * per), hi = min(nvec, lo + per);
@@ -533,23 +603,25 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
         if (lane >= off) inc += o;
       }
       int64_t run = at + inc - sum;
-      if (run <= pick && pick < run + sum) {
-        int i = lo;
+      int i = lo;
+      const bool mine = run <= pick && pick < run + sum;
+      if (mine)
         while (pick >= run + sm.vec[i]) run += sm.vec[i++];
-        const int first = 8 * (w0 + i);
-#pragma unroll 1
-        for (int e = 0; e < 8; ++e) {
-          const int tok = first + e;
-          bool out = false;
-          for (int g = 0; g < ctx.n_gone; ++g) out |= sm.gone[g] == tok;
-          const int64_t w = out ? 0 : weight_of(ctx, __bfloat162float(row[tok]), qrow ? qrow[tok] : 0.f);
-          if (pick < run + w) {
-            p.next_token[r] = tok;
-            break;
-          }
-          run += w;
-        }
+      const int from = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+      const int first = 8 * (w0 + __shfl_sync(0xffffffffu, i, from));
+      run = __shfl_sync(0xffffffffu, run, from);
+      // its 8 tokens, one a lane
+      const int tok = first + (lane & 7);
+      bool out = false;
+      for (int g = 0; g < ctx.n_gone; ++g) out |= sm.gone[g] == tok;
+      const int64_t w = out ? 0 : token_weight(ctx, __bfloat162float(row[tok]), qrow ? qrow[tok] : 0.f);
+      inc = w;
+#pragma unroll
+      for (int off = 1; off < 8; off <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, inc, off, 8);
+        if ((lane & 7) >= off) inc += o;
       }
+      if (lane < 8 && run + inc - w <= pick && pick < run + inc) p.next_token[r] = tok;
     }
     break;
   }

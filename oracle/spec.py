@@ -100,7 +100,9 @@ def target_row(logits: np.ndarray, temperature: float) -> np.ndarray:
     top = z.max()
     if top == -np.inf:
         return np.zeros_like(z)
-    e = np.where(z == top, 1.0, np.exp(np.where(z == top, 0.0, z - top) / temperature))
+    below = z != top
+    e = np.ones_like(z)
+    e[below] = np.exp((z[below] - top) / temperature)
     return e / e.sum()
 
 

@@ -15,8 +15,9 @@ with V and o to bf16 at the end is off by at most
 
 Verification: whole numbers, equal to the oracle's.  The cases keep clear of
 borders closer than the kernel resolves: 1e-6 in probability for the
-acceptance tests (fp32 sums and exponentials, 2^-21), 1e-9 for the last draw
-(weights accurate to 2^-36, rounded to 2^-40).
+acceptance tests (fp32 sums and exponentials, 2^-21), 4e-9 for the last draw
+(each weight off by at most 2^-29 of itself, in the sum below the border and in
+the total: 2 2^-29).
 
 Page operations: bit-exact."""
 
@@ -319,7 +320,7 @@ class Drafts:
     def check(self, got, max_path=16, sampling=True):
         count, path, nxt = got
         for r, (p, tok, (tests, last)) in enumerate(self.expect(max_path, sampling)):
-            assert tests > 1e-6 and last > 1e-9, "the case sits on a border"
+            assert tests > 1e-6 and last > 4e-9, "the case sits on a border"
             assert list(path[r]) == p + [-1] * (max_path - len(p)) and count[r] == len(p) and nxt[r] == tok, \
                 (r, p, tok, list(path[r]), count[r], nxt[r])
 
