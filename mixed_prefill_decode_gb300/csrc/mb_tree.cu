@@ -17,6 +17,14 @@
 // tensor and copy rates is 285, so trees of up to about 285 / G nodes are
 // bound by HBM and larger ones by the tensor cores and the softmax.
 //
+// Measured (head_dim 128, G = 4, 8 KV heads): 16 trees of 8 nodes at 8,192
+// keys 96 us, 5.6 TB/s, 83 % of a copy's rate; 64 trees of 8 at 1,125 keys
+// 67 us, 4.5 TB/s (a CTA has 3.4 units of 9 blocks each, and every unit's end
+// waits for its last softmax and product); 16 trees of 64 nodes at 8,192 keys
+// 156 us, 1.10 PFLOP/s of bf16, 57 % of a plain matrix product's rate, bound
+// by the softmax's exponentials and the turns of the two warp groups; one tree
+// of 6 nodes at 1,125 keys 14 us, two launches and the chain of one block.
+//
 // Layout of the work.  The rows that share a KV head, (node, q-head of the
 // group), row = node G + g, are the M side of the products: 128 / G nodes make
 // a query tile of up to 128 rows, loaded by one 3-D copy per 64 columns.  A
@@ -67,8 +75,11 @@ constexpr int kMaxTreeCtas = 160;   // CTAs of a launch at most (one per SM); si
 constexpr int kRecBytes = 8192;     // workspace: one record of 8 ints per CTA, then the partials
 // The schedule's weights: a block of one query tile, a block of two, a unit's
 // start and end, and the least a CTA takes (at least kCost2, so that no CTA
-// between the first and the last of a unit is left without a block).
-constexpr int kCost1 = 2, kCost2 = 3, kCostUnit = 3, kMinShare = 3;
+// between the first and the last of a unit is left without a block).  A unit's
+// start and end cost what 2.5 blocks do: weighted by 3, 96 trees of 13 nodes at
+// 24 to 8,192 keys took 237 us, by 5 233, by 8 235; 64 at 1,125 keys 66.7, 66.8
+// and 67.3.
+constexpr int kCost1 = 2, kCost2 = 3, kCostUnit = 5, kMinShare = 3;
 
 struct TreeParams {
   __nv_bfloat16 *o;
@@ -231,9 +242,12 @@ __device__ __noinline__ int64_t div64(int64_t a, int64_t b) { return a / b; }
 // Takes the logits of keys that a row does not see out of a block of S (to
 // -inf, in TMEM): `first` is the node index of the block's first key (negative
 // while it is a key of the prefix), `see` the nodes that the row's node sees.
-// A pass of its own, out of line, for the one or two blocks of a unit that
-// hold nodes: it keeps the loop over the prefix short.
-__device__ __noinline__ void mask_block(uint32_t s_col, int first, const uint4 see) {
+// A pass of its own, for the one or two blocks of a unit that hold nodes: it
+// keeps the loop over the prefix short.  (Inline: as a call, 256 trees of 8
+// nodes at 300 keys took 142 us against 126, and 96 of 13 at up to 8,192 240
+// against 234; add_odd, which almost no call reaches, is better out of line:
+// inline, the 256 trees took 134 us.)
+__device__ __forceinline__ void mask_block(uint32_t s_col, int first, const uint4 see) {
   const uint32_t w[4] = {see.x, see.y, see.z, see.w};
 #pragma unroll 1
   for (int k = 0; k < 4; ++k) {
