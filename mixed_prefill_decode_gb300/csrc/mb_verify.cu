@@ -121,17 +121,18 @@ __device__ __forceinline__ float bf16_of(const uint4 &raw, int e) {
 struct WeightCtx {
   float m, kh, kl;         // weight 2^((l - m) k), k = kh + kl
   float d_max;             // m - l from which on it is 2^-48
-  float az_hi, az_lo;      // less az q
-  bool probs;
+  float az_hi, az_lo;      // less az q (both times 2^20)
+  float q_small, q_any;    // q from which on az q is above 2^-11, above 1
   int n_gone;
 };
 
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 // Two weights as fix_exp computes them, in packed fp32: v 2^(11 - s) in units
 // of 2^-41.  D: m - l.
-__device__ __forceinline__ void weight_pair(const WeightCtx &c, float2 D, uint32_t (&v)[2], int32_t (&s)[2]) {
+__device__ __forceinline__ void weight_pair(const WeightCtx &c, float2 D, uint32_t *v, int32_t *s) {
   constexpr float kMagic = 12582912.f;      // 1.5 2^23
   constexpr int32_t kMagicBits = 0x4B400000;
-  auto both = [](float x) { return make_float2(x, x); };
   D.x = fminf(D.x, c.d_max);   // (an infinity, a NaN: 2^-48, which rounds to 0)
   D.y = fminf(D.y, c.d_max);
   const float2 y = __fmul2_rn(D, both(-c.kh));                                   // y - r = -D k
@@ -157,61 +158,93 @@ __device__ __forceinline__ int32_t small_weight(uint32_t v, int32_t s) {
 __device__ __forceinline__ int64_t large_weight(uint32_t v, int32_t s) {
   return static_cast<int64_t>((((static_cast<uint64_t>(v) << 12) >> s) + 1) >> 1);
 }
-// az q in units of 2^-41, beside a small weight (at most 2^30, more than any of
-// them) and beside any (at most 2, more than any).
-template <typename Int>
-__device__ __forceinline__ Int fixed_q(const WeightCtx &c, float q) {
-  constexpr float kTop = sizeof(Int) == 4 ? 0x1p-11f : 2.f;
-  const float h = q * c.az_hi, l = fmaf(q, c.az_hi, -h) + q * c.az_lo;
-  return h < kTop ? static_cast<Int>(to_fix(h, l)) : static_cast<Int>(kTop * 0x1p41f);
-}
 
-// Weights of two tokens together (probs: q0, q1), in 32 or 64 bits.
-__device__ __forceinline__ int64_t pair_weight(const WeightCtx &c, float2 D, float q0, float q1) {
-  uint32_t v[2];
-  int32_t s[2];
-  weight_pair(c, D, v, s);
-  if (__any_sync(0xffffffffu, min(s[0], s[1]) < 12)) {
-    const int64_t w0 = large_weight(v[0], s[0]), w1 = large_weight(v[1], s[1]);
-    if (!c.probs) return w0 + w1;
-    return max(w0 - fixed_q<int64_t>(c, q0), static_cast<int64_t>(0)) + max(w1 - fixed_q<int64_t>(c, q1), static_cast<int64_t>(0));
-  }
-  const int32_t w0 = small_weight(v[0], s[0]), w1 = small_weight(v[1], s[1]);
-  if (!c.probs) return static_cast<uint32_t>(w0) + static_cast<uint32_t>(w1);
-  return static_cast<uint32_t>(max(w0 - fixed_q<int32_t>(c, q0), 0)) + static_cast<uint32_t>(max(w1 - fixed_q<int32_t>(c, q1), 0));
+// az q of two tokens in units of 2^-41, as hi 2^21 + lo.  A q above `top` (a
+// NaN too) counts as that: az q is then more than any weight beside it.
+__device__ __forceinline__ void fixed_q(const WeightCtx &c, float2 q, float top, int32_t (&hi)[2], int32_t (&lo)[2]) {
+  constexpr float kMagic = 12582912.f;
+  constexpr int32_t kMagicBits = 0x4B400000;
+  q.x = fminf(q.x, top);
+  q.y = fminf(q.y, top);
+  const float2 x = __fmul2_rn(q, both(c.az_hi));
+  const float2 l = __ffma2_rn(q, both(c.az_lo), __ffma2_rn(q, both(c.az_hi), make_float2(-x.x, -x.y)));
+  const float2 a = __fadd2_rn(x, both(kMagic));
+  const float2 n = __fadd2_rn(a, both(-kMagic));
+  const float2 rem = __fadd2_rn(__ffma2_rn(n, both(-1.f), x), l);
+  const float2 b = __ffma2_rn(rem, both(0x1p21f), both(kMagic));
+  hi[0] = __float_as_int(a.x) - kMagicBits;
+  hi[1] = __float_as_int(a.y) - kMagicBits;
+  lo[0] = __float_as_int(b.x) - kMagicBits;
+  lo[1] = __float_as_int(b.y) - kMagicBits;
 }
 
 // m - l, with a row's infinities in order: l = m gives 0, less than m = +inf everything.
 __device__ __forceinline__ float below(const WeightCtx &c, float l) { return l == c.m ? 0.f : c.m - l; }
 
 // The weight of one token (any lane by itself).
-__device__ __noinline__ int64_t token_weight(const WeightCtx &c, float l, float q) {
+__device__ __noinline__ int64_t token_weight(const WeightCtx &c, float l, bool probs, float q) {
   uint32_t v[2];
-  int32_t s[2];
+  int32_t s[2], hi[2], lo[2];
   weight_pair(c, make_float2(below(c, l), 0.f), v, s);
   const int64_t w = large_weight(v[0], s[0]);
-  return c.probs ? max(w - fixed_q<int64_t>(c, q), static_cast<int64_t>(0)) : w;
+  if (!probs) return w;
+  fixed_q(c, both(q), c.q_any, hi, lo);
+  return max(w - (static_cast<int64_t>(hi[0]) << 21) - lo[0], static_cast<int64_t>(0));
 }
 
-// Weight of vector v (8 tokens, at x), refused tokens left out.  By all lanes
-// of a warp (live: the lane has such a vector).
+// Weight of vector v (8 tokens, at x; q: their draft probabilities), refused
+// tokens left out.  By all lanes of a warp (live: the lane has such a vector).
+// The 8 weights are computed side by side and their sum in 32 bits a pair,
+// unless one of the warp's 256 is 2^-11 or more.
+template <bool PROBS>
 __device__ __forceinline__ int64_t vector_weight(const WeightCtx &c, const uint4 *x, int v, bool live, float4 qa, float4 qb) {
   const uint4 raw = live ? *x : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);   // -inf
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
   const float q[8] = {qa.x, qa.y, qa.z, qa.w, qb.x, qb.y, qb.z, qb.w};
   int64_t sum = 0;
   if (c.m < INFINITY) {
+    uint32_t wv[8];
+    int32_t ws[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      sum += pair_weight(c, make_float2(c.m - bf16lo(w[e]), c.m - bf16hi(w[e])), q[2 * e], q[2 * e + 1]);
-  } else {
+      weight_pair(c, make_float2(c.m - bf16lo(w[e]), c.m - bf16hi(w[e])), wv + 2 * e, ws + 2 * e);
+    const int least = min(min(min(ws[0], ws[1]), min(ws[2], ws[3])), min(min(ws[4], ws[5]), min(ws[6], ws[7])));
+    if (__any_sync(0xffffffffu, least < 12)) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum += token_weight(c, bf16_of(raw, e), q[e]);
+      for (int e = 0; e < 8; e += 2) {
+        int64_t a = large_weight(wv[e], ws[e]), b = large_weight(wv[e + 1], ws[e + 1]);
+        if (PROBS) {
+          int32_t hi[2], lo[2];
+          fixed_q(c, make_float2(q[e], q[e + 1]), c.q_any, hi, lo);
+          a = max(a - (static_cast<int64_t>(hi[0]) << 21) - lo[0], static_cast<int64_t>(0));
+          b = max(b - (static_cast<int64_t>(hi[1]) << 21) - lo[1], static_cast<int64_t>(0));
+        }
+        sum += a + b;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        int32_t a = small_weight(wv[e], ws[e]), b = small_weight(wv[e + 1], ws[e + 1]);
+        if (PROBS) {
+          int32_t hi[2], lo[2];
+          fixed_q(c, make_float2(q[e], q[e + 1]), c.q_small, hi, lo);
+          a = max(a - (hi[0] << 21) - lo[0], 0);
+          b = max(b - (hi[1] << 21) - lo[1], 0);
+        }
+        sum += static_cast<uint32_t>(a) + static_cast<uint32_t>(b);
+      }
+    }
+  } else {
+#pragma unroll 1
+    for (int e = 0; e < 8; ++e) {
+      const float lg = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(x)[e]);
+      if (live) sum += token_weight(c, lg, PROBS, e < 4 ? (e < 2 ? (e ? qa.y : qa.x) : (e == 2 ? qa.z : qa.w)) : (e < 6 ? (e == 4 ? qb.x : qb.y) : (e == 6 ? qb.z : qb.w)));
+    }
   }
-  if (live)
-    for (int g = 0; g < c.n_gone; ++g) {   // (only without draft probabilities)
+  if (!PROBS && live)
+    for (int g = 0; g < c.n_gone; ++g) {
       const int tok = sm.gone[g];
-      if ((tok >> 3) == v) sum -= token_weight(c, __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(x)[tok & 7]), 0.f);
+      if ((tok >> 3) == v) sum -= token_weight(c, __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(x)[tok & 7]), false, 0.f);
     }
   return sum;
 }
@@ -224,24 +257,23 @@ struct Part {
   int parity;        // exchange buffer of the next round
 };
 
-__device__ __forceinline__ float4 load_q(const float *qrow, int v) {
-  return qrow ? __ldg(reinterpret_cast<const float4 *>(qrow) + v) : make_float4(0.f, 0.f, 0.f, 0.f);
-}
+__device__ __forceinline__ float4 load_q(const float *qrow, int v) { return __ldg(reinterpret_cast<const float4 *>(qrow) + v); }
 
 // Sums of the weights over each warp's part (sm.ws), the CTA's, and (from the
 // exchange) the row's; the sum before this CTA's part goes to *before.  All
 // threads of the cluster.  Out of line: it is called in four places.
+template <bool PROBS>
 __device__ __noinline__ int64_t weight_sums(Part &t, const WeightCtx &c, const float *qrow, int64_t *before) {
   __syncthreads();   // sm.ws has been read
   int64_t sum = 0;
   float4 qa = make_float4(0.f, 0.f, 0.f, 0.f), qb = qa;
-  if (t.nk > 0) qa = load_q(qrow, 2 * t.v0), qb = load_q(qrow, 2 * t.v0 + 1);
+  if (PROBS && t.nk > 0) qa = load_q(qrow, 2 * t.v0), qb = load_q(qrow, 2 * t.v0 + 1);
 #pragma unroll 1
   for (int k = 0; k < t.nk_warp; ++k) {
     const int v = t.v0 + 32 * k;
     float4 na = qa, nb = qb;   // the next vector's draft probabilities, in flight meanwhile
-    if (k + 1 < t.nk) na = load_q(qrow, 2 * v + 64), nb = load_q(qrow, 2 * v + 65);
-    sum += vector_weight(c, t.x + k * kVerThreads, v, k < t.nk, qa, qb);
+    if (PROBS && k + 1 < t.nk) na = load_q(qrow, 2 * v + 64), nb = load_q(qrow, 2 * v + 65);
+    sum += vector_weight<PROBS>(c, t.x + k * kVerThreads, v, k < t.nk, qa, qb);
     qa = na, qb = nb;
   }
 #pragma unroll
@@ -303,30 +335,36 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
     for (int k = 0; k < nk; ++k) cp_async16(x + k * kVerThreads, row + w0 + lane + 32 * k);
   };
   load_row(0);
-  float temp = p.temperature ? p.temperature[r] : 0.f;
-  if (!(temp >= 0.f)) {
-    if (threadIdx.x == 0) atomicExch(p.err, kErrBounds);
-    temp = 0.f;
+  // The request's words, each thread's loads side by side.
+  const float temp_in = p.temperature ? p.temperature[r] : 0.f;
+  const int i = threadIdx.x;   // its node
+  int up = -1, tok = 0;
+  float u = 0.f, u_last = 0.f;
+  if (i < n) {
+    up = p.parent[t0 + i];
+    if (i > 0) tok = p.tokens[t0 + i];
+    if (i > 0 && p.temperature) u = p.u_accept[t0 + i];
   }
+  if (threadIdx.x == kVerThreads - 1 && p.temperature) u_last = p.u_final[r];
+  const bool temp_ok = temp_in >= 0.f;
+  const float temp = temp_ok ? temp_in : 0.f;
   const bool greedy = temp == 0.f;
-  if (threadIdx.x == 0) {   // (FP64 is slow: one thread's work)
+  if (threadIdx.x == kVerThreads - 1) {   // (FP64 is slow: one thread's work, of a warp without nodes)
+    if (!temp_ok) atomicExch(p.err, kErrBounds);
     const double kd = greedy ? 0.0 : fmax(fmin(1.4426950408889634074 / static_cast<double>(temp), 1e30), 1e-30);
-    sm.u_final = greedy ? 0.f : p.u_final[r];
+    sm.u_final = u_last;
     sm.kh = static_cast<float>(kd);
     sm.kl = static_cast<float>(kd - static_cast<double>(sm.kh));
   }
-  for (int i = threadIdx.x; i < n; i += kVerThreads) {
-    int up = p.parent[t0 + i];
-    if (up < -1 || up >= i) {
-      if (rank == 0) atomicExch(p.err, kErrBounds);
-      up = -1;
-    }
+  static_assert(kMaxTreeNodes < kVerThreads, "one thread a node");
+  if (i < n) {
+    const bool bad_up = up < -1 || up >= i, bad_tok = tok < 0 || tok >= p.vocab;
+    if (bad_up || bad_tok) atomicExch(p.err, kErrBounds);
+    if (bad_up) up = -1;
     sm.parent[i] = static_cast<int16_t>(up);
-    const int tok = i > 0 ? p.tokens[t0 + i] : 0;
-    if (tok < 0 || tok >= p.vocab) atomicExch(p.err, kErrBounds);
-    sm.token[i] = tok < 0 || tok >= p.vocab ? -1 : tok;
-    sm.u[i] = greedy ? 0.f : p.u_accept[t0 + i];
-    const size_t at = (static_cast<size_t>(t0) + max(up, 0)) * p.vocab + max(sm.token[i], 0);
+    sm.token[i] = bad_tok ? -1 : tok;
+    sm.u[i] = u;
+    const size_t at = (static_cast<size_t>(t0) + max(up, 0)) * p.vocab + (bad_tok ? 0 : tok);
     sm.logit[i] = greedy ? 0.f : __bfloat162float(p.logits[at]);
     sm.q[i] = greedy || !p.probs ? 0.f : p.probs[at];
   }
@@ -465,7 +503,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
     int64_t total = 0, before = 0;
     int final_gone = 0;
     const float *qrow = nullptr;
-    WeightCtx ctx{m, kh, kl, d_max, 0.f, 0.f, p.probs != nullptr, 0};
+    WeightCtx ctx{m, kh, kl, d_max, 0.f, 0.f, 0.f, 0.f, 0};
     bool have_sums = false;
     if (rank == 0 && threadIdx.x == 0) path[len - 1] = cur;
     if (greedy || !p.probs) {
@@ -528,9 +566,9 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
           break;
         }
         if (!qrow) {   // the first refusal: the row's sum to full accuracy
-          ctx.probs = false;
-          const int64_t z = weight_sums(part, ctx, nullptr, &before);
-          ctx.probs = true;
+          for (int b = 32 * lane; b < 8 * (w1 - w0); b += 32 * 32)   // its draft probabilities go to L2 meanwhile
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 8 * w0 + b));
+          const int64_t z = weight_sums<false>(part, ctx, nullptr, &before);
           if (warp == 0) zd = static_cast<double>(z) * 0x1p-41;
           qrow = q;
         }
@@ -538,14 +576,17 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
           a += c;
           const double az = a * zd;
           if (lane == 0) {
-            sm.az_hi = static_cast<float>(az);
-            sm.az_lo = static_cast<float>(az - static_cast<double>(sm.az_hi));
+            const float h = static_cast<float>(az);
+            sm.az_hi = h * 0x1p20f;
+            sm.az_lo = static_cast<float>(az - static_cast<double>(h)) * 0x1p20f;
           }
         }
         __syncthreads();
         ctx.az_hi = sm.az_hi;
         ctx.az_lo = sm.az_lo;
-        total = weight_sums(part, ctx, qrow, &before);
+        ctx.q_small = 513.f / ctx.az_hi;      // (in units of 2^-20, and one more)
+        ctx.q_any = 1048577.f / ctx.az_hi;
+        total = weight_sums<true>(part, ctx, qrow, &before);
         if (warp == 0) c = static_cast<double>(total) * 0x1p-41 / zd;
         have_sums = true;
       }
@@ -564,13 +605,12 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
     // none accepted: one token of what is left
     if (!have_sums) {
       ctx.n_gone = final_gone;
-      ctx.probs = false;
-      total = weight_sums(part, ctx, nullptr, &before);
+      total = weight_sums<false>(part, ctx, nullptr, &before);
     }
     if (total == 0) {    // the refusals left nothing: p itself
       qrow = nullptr;
-      ctx = {m, kh, kl, d_max, 0.f, 0.f, false, 0};
-      total = weight_sums(part, ctx, nullptr, &before);
+      ctx = {m, kh, kl, d_max, 0.f, 0.f, 0.f, 0.f, 0};
+      total = weight_sums<false>(part, ctx, nullptr, &before);
     }
     if (threadIdx.x == 0) {
       const double uf = static_cast<double>(sm.u_final);
@@ -586,11 +626,17 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
       // (this warp alone) its vectors' weights, in token order; then 8 lanes'
       // worth each, the vector, the token
       const int v0 = w0 + lane, nvec = w1 - w0;
+      const float4 qa0 = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
       for (int k = 0; k < part.nk_warp; ++k) {
         const int v = v0 + 32 * k;
-        const float *q = k < nk ? qrow : nullptr;
-        sm.vec[32 * k + lane] = vector_weight(ctx, x + k * kVerThreads, v, k < nk, load_q(q, 2 * v), load_q(q, 2 * v + 1));
+        if (qrow) {
+          float4 qa = make_float4(0.f, 0.f, 0.f, 0.f), qb = qa;
+          if (k < nk) qa = load_q(qrow, 2 * v), qb = load_q(qrow, 2 * v + 1);
+          sm.vec[32 * k + lane] = vector_weight<true>(ctx, x + k * kVerThreads, v, k < nk, qa, qb);
+        } else {
+          sm.vec[32 * k + lane] = vector_weight<false>(ctx, x + k * kVerThreads, v, k < nk, qa0, qa0);
+        }
       }
       __syncwarp();
       const int per = (nvec + 31) / 32, lo = min(nvec, lane * per), hi = min(nvec, lo + per);
@@ -614,7 +660,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
       const int tok = first + (lane & 7);
       bool out = false;
       for (int g = 0; g < ctx.n_gone; ++g) out |= sm.gone[g] == tok;
-      const int64_t w = out ? 0 : token_weight(ctx, __bfloat162float(row[tok]), qrow ? qrow[tok] : 0.f);
+      const int64_t w = out ? 0 : token_weight(ctx, __bfloat162float(row[tok]), qrow != nullptr, qrow ? qrow[tok] : 0.f);
       inc = w;
 #pragma unroll
       for (int off = 1; off < 8; off <<= 1) {
