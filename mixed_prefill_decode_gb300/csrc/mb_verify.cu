@@ -47,10 +47,11 @@ namespace {
 
 using namespace dev;
 
-constexpr int kVerThreads = 512;
+constexpr int kVerThreads = 256;   // (512 and two CTAs an SM: 64 chains 84 us against 79, 256 of 3 317 against 239)
+constexpr int kVerPerSm = 4;       // CTAs an SM holds
 constexpr int kVerWarps = kVerThreads / 32;
-constexpr int kMaxCluster = 8;
-constexpr int kMaxHeld = 17;   // vectors that a thread holds at most: a row of 2^19 logits over 8 CTAs
+constexpr int kMaxCluster = 16;
+constexpr int kMaxHeld = 17;   // vectors that a thread holds at most: a row of 2^19 logits over 16 CTAs
 struct VerifyParams {
   const __nv_bfloat16 *logits;
   const int32_t *tokens;
@@ -296,7 +297,7 @@ __device__ __noinline__ int64_t weight_sums(Part &t, const WeightCtx &c, const f
   return total;
 }
 
-__global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_constant__ VerifyParams p) {
+__global__ void __launch_bounds__(kVerThreads, kVerPerSm) verify_kernel(const __grid_constant__ VerifyParams p) {
   extern __shared__ __align__(16) uint4 held[];   // vector k of thread t at k kVerThreads + t
   const int C = p.cluster;
   const uint32_t rank = C > 1 ? cluster_ctarank() : 0;
@@ -696,13 +697,15 @@ cudaError_t verify_tree_run(const VerifyArgs &a, cudaStream_t st) {
   p.vocab = a.vocab;
   p.T = a.T;
   p.max_path = a.max_path;
-  // CTAs per request: enough that a CTA holds at most 32,768 of the row's
-  // logits, then as many as still fit the GPU twice over with at least 4,096
-  // logits each.
+  // CTAs per request: enough that a CTA holds at most 20,480 of the row's
+  // logits (four such fit an SM), then as many as still fit the GPU together,
+  // with at least 2,048 logits each; 16 (beyond what every GPU takes) with at
+  // least 4,096: one chain of 5, vocabulary 128,256, 29 us against 35 with 8;
+  // 16 trees of 24, vocabulary 50,264, 25 us against 23.
   int cluster = 1;
-  while (cluster < kMaxCluster && a.vocab > cluster * 32768) cluster *= 2;
-  while (cluster < kMaxCluster && static_cast<int64_t>(a.n_reqs) * cluster * 2 <= 2 * device_sm_count() &&
-         a.vocab >= cluster * 2 * 4096)
+  while (cluster < kMaxCluster && a.vocab > cluster * 20480) cluster *= 2;
+  while (cluster < kMaxCluster && static_cast<int64_t>(a.n_reqs) * cluster * 2 <= kVerPerSm * device_sm_count() &&
+         a.vocab >= cluster * 2 * (cluster < 8 ? 2048 : 4096))
     cluster *= 2;
   p.cluster = cluster;
   static const FixExpTable table = fix_exp_table();
@@ -714,6 +717,11 @@ cudaError_t verify_tree_run(const VerifyArgs &a, cudaStream_t st) {
   const int smem = per_thread * kVerThreads * 16;
   const cudaError_t e = ensure_max_smem(reinterpret_cast<const void *>(verify_kernel), kMaxHeld * kVerThreads * 16);
   if (e != cudaSuccess) return e;
+  if (cluster > 8) {
+    const cudaError_t e16 = cudaFuncSetAttribute(reinterpret_cast<const void *>(verify_kernel),
+                                                 cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e16 != cudaSuccess) return e16;
+  }
   if (per_thread > kMaxHeld) return cudaErrorInvalidValue;
   return launch_pdl(verify_kernel, dim3(a.n_reqs * cluster), dim3(kVerThreads), smem, st, cluster, p);
 }
