@@ -15,7 +15,7 @@
 // precision; one entry per shared-memory bank, so lookups do not conflict),
 // 2^f - 1 from the first four terms of its Taylor series in fp32: it is below
 // 0.011, so its rounding is 2^-31 of the result.  The product is an integer
-// from the table's entry on.  About 28 instructions.
+// from the table's entry on.
 #pragma once
 
 #include <cmath>

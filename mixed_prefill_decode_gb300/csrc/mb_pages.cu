@@ -1,7 +1,10 @@
 // Page operations on the KV pools of a stack: the accepted path of a
 // drafted tree moved to the positions behind the prefix, and whole pages
 // copied.  Pure data movement: each byte is read once and written once, so
-// HBM bounds the large calls and the launch the small ones.
+// HBM bounds the large calls and the launch the small ones.  Measured: 256
+// pages of 64 KB in 40 pools 193 us, 6.9 TB/s read and written (a plain copy:
+// 6.8); one page in 32 pools 1.9 us in a graph; the accepted paths of 64 requests
+// in 40 pools, 84 MB, 16.7 us, 5.0 TB/s (rows of 256 bytes, 4 KB apart).
 
 #include <cuda_runtime.h>
 
@@ -26,7 +29,9 @@ struct PoolList {
 // one head's K or V row) of every token that moves.  path is strictly
 // increasing, so the token bound for index k comes from path[k] >= k: a
 // thread that takes its moves in ascending order reads every source before
-// it overwrites it, and no other thread touches its column.
+// it overwrites it, and no other thread touches its column.  Eight loads of a
+// thread go out before the first store: with one at a time a path of 8 nodes
+// would take eight round trips to HBM in a row.
 constexpr int kCompactThreads = 256;
 constexpr int kCompactBatch = 8;   // moves whose loads are in flight together
 
@@ -95,7 +100,9 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------- page copies
-// One CTA per (slice of a page, pair, pool).
+// One CTA per (slice of a page, pair, pool); the pairs travel as kernel
+// arguments, so nothing is copied to the device first and a captured call
+// keeps its own.
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 8;   // 16-byte loads in flight per thread: 32 KB a CTA
 

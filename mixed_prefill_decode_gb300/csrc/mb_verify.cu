@@ -22,14 +22,24 @@
 // What bounds it: the walk from node to node is serial, and a step of it is the
 // latency of one row (load, maximum and sum, exchange), so a request is given
 // to a cluster of CTAs that shares each row, and the rows of nodes that are
-// never reached are not read.  A thread keeps its part of the row in shared memory
-// (copied asynchronously) between the maximum, the sum and the draw.
+// never reached are not read.  A thread keeps its part of the row in shared
+// memory (copied asynchronously) between the maximum, the sum and the draw.
 //
 // The tests compare in fp32 (the special-function unit's exponentials); the
-// draw at the end needs accurate weights (mb_fixexp.cuh, some 28 instructions
-// each, for one row per request, two after a refusal with draft
-// probabilities).  A table of the weights of all bf16 logits in shared memory
-// was slower than computing them: its random 8-byte reads took 7 cycles a warp.
+// draw at the end needs accurate weights (mb_fixexp.cuh), for one row per
+// request, two after a refusal with draft probabilities.  Their arithmetic is
+// what a full GPU spends most of its time on.
+//
+// Measured: one chain of 5 drafted tokens, vocabulary 128,256, with draft
+// probabilities, 28 us, some 3.5 us a node; 64 such 78 us, of which a node's
+// step takes about 5 us and an accurate pass over the row 10 to 15 (the walks
+// read 82 MB: 1.1 TB/s); 16 trees of 24, vocabulary 50,264, 21 us; 6 tokens,
+// greedy, vocabulary 32,000, 7 us.  Tried and dropped: a table of the weights
+// of all bf16 logits in shared memory (its random 8-byte reads took 7 cycles a
+// warp); an only child's row fetched over its parent's, with its maximum and
+// sum computed during the parent's exchange (64 chains 80 us: what it hides is
+// latency that the SM's other CTAs hide already, and a refusal has to fetch the
+// parent's row again).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -104,6 +114,8 @@ __shared__ VerifySmem sm;
 __device__ __forceinline__ void cp_async16(void *dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // The larger of two pairs of bf16, a NaN giving way to a number.
@@ -372,57 +384,11 @@ __global__ void __launch_bounds__(kVerThreads, kVerPerSm) verify_kernel(const __
   __syncthreads();
 
   const float kh = sm.kh, kl = sm.kl, d_max = fminf(48.f / fmaxf(kh, 1e-30f), 3e38f);
-  int cur = 0, len = 1;
-
   Part part{x, nk, (w1 - w0 + 31) / 32, w0 + lane, C, static_cast<int>(rank), 0};
 
-  while (true) {
-    const __nv_bfloat16 *row = p.logits + (static_cast<size_t>(t0) + cur) * p.vocab;
-    // Children of cur, in index order; warp 0's lanes hold the first 32
-    // children's values.
-    int n_child = 0;
-    int c_tok = -1;
-    float c_u = 2.f, c_l = -INFINITY, c_q = 0.f;
-    // the values of 32 children from `first` on (warp 0)
-    auto load_children = [&](int first) {
-      c_tok = -1;
-      if (first + lane < n_child) {
-        const int node = sm.child[first + lane];
-        c_tok = sm.token[node];
-        c_u = sm.u[node];
-        c_l = sm.logit[node];
-        c_q = sm.q[node];
-      }
-    };
-    if (warp == 0) {
-      if (len < p.max_path)
-        for (int b = 0; b < n; b += 32) {
-          const bool is = b + lane < n && b + lane > 0 && sm.parent[b + lane] == cur;
-          const uint32_t mask = __ballot_sync(0xffffffffu, is);
-          if (is) sm.child[n_child + __popc(mask & ((1u << lane) - 1))] = static_cast<int16_t>(b + lane);
-          n_child += __popc(mask);
-        }
-      if (lane == 0) sm.n_child = n_child;
-      __syncwarp();
-      load_children(0);
-    }
-    // the next row is most likely the first child's: its part goes to L2 meanwhile
-    {
-      int node = n;
-      if (len < p.max_path) {
-        const int i0 = cur + 1 + lane;
-        for (int i = i0; i < n && node == n; i += 32)
-          if (sm.parent[i] == cur) node = i;
-        node = __reduce_min_sync(0xffffffffu, node);
-      }
-      if (node < n) {
-        const char *next = reinterpret_cast<const char *>(p.logits + (static_cast<size_t>(t0) + node) * p.vocab) + 16ll * w0;
-        for (int b = 128 * lane; b < 16 * (w1 - w0); b += 128 * 32)
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(next + b));
-      }
-    }
-    // The row's maximum (and, greedy, the lowest index that has it), with the
-    // sum of 2^((l - max) k) beside it: per thread, warp, CTA, cluster.
+  // A row's maximum (and, greedy, the lowest index that has it) and the sum of
+  // 2^((l - max) k) over this warp's part, to sm.wm, wz, wi.
+  auto warp_part = [&]() {
     float bm = -INFINITY, z = 0.f;
     int bi = 0x7fffffff;
     cp_async_wait();
@@ -468,37 +434,82 @@ __global__ void __launch_bounds__(kVerThreads, kVerPerSm) verify_kernel(const __
       for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
     }
     if (lane == 0) sm.wm[warp] = bm, sm.wz[warp] = z, sm.wi[warp] = bi;
-    __syncthreads();
-    n_child = sm.n_child;
-    // n (maximum, sum, index) triples, one per lane: of all together.  Every
-    // warp does it, so nothing has to be told to the others.
-    auto join = [&](float &m, float &s, int &i, int n) {
-      float top_m = m;
-      for (int off = n >> 1; off > 0; off >>= 1) top_m = fmaxf(top_m, __shfl_xor_sync(0xffffffffu, top_m, off));
-      s = m == top_m ? s : m == -INFINITY || top_m == INFINITY ? 0.f : s * ex2_approx((m - top_m) * kh);
-      i = m == top_m ? i : 0x7fffffff;
-      for (int off = n >> 1; off > 0; off >>= 1) {
-        s += __shfl_xor_sync(0xffffffffu, s, off);
-        i = min(i, __shfl_xor_sync(0xffffffffu, i, off));
-      }
-      m = top_m;
-    };
-    float m = sm.wm[lane % kVerWarps], Z = sm.wz[lane % kVerWarps];
-    int top = sm.wi[lane % kVerWarps];
-    join(m, Z, top, kVerWarps);
-    if (C > 1) {
-      if (threadIdx.x < C) {
-        st_cluster32(&sm.ex.m[part.parity][rank], threadIdx.x, __float_as_uint(m));
-        st_cluster32(&sm.ex.z[part.parity][rank], threadIdx.x, __float_as_uint(Z));
-        st_cluster32(&sm.ex.idx[part.parity][rank], threadIdx.x, static_cast<uint32_t>(top));
-      }
-      cluster_sync();
-      m = sm.ex.m[part.parity][lane % C], Z = sm.ex.z[part.parity][lane % C], top = sm.ex.idx[part.parity][lane % C];
-      join(m, Z, top, C);
-      part.parity ^= 1;
+  };
+  // n (maximum, sum, index) triples, one per lane: of all together.
+  auto join = [&](float &m, float &s, int &i, int n) {
+    float top_m = m;
+    for (int off = n >> 1; off > 0; off >>= 1) top_m = fmaxf(top_m, __shfl_xor_sync(0xffffffffu, top_m, off));
+    s = m == top_m ? s : m == -INFINITY || top_m == INFINITY ? 0.f : s * ex2_approx((m - top_m) * kh);
+    i = m == top_m ? i : 0x7fffffff;
+    for (int off = n >> 1; off > 0; off >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, off);
+      i = min(i, __shfl_xor_sync(0xffffffffu, i, off));
     }
-    if (m == -INFINITY) top = 0;   // no token has a chance: token 0
+    m = top_m;
+  };
 
+  int cur = 0, len = 1;
+
+  while (true) {
+    warp_part();
+    // its children, in index order
+    if (warp == 0) {
+      int n_child = 0;
+      if (len < p.max_path)
+        for (int b = 0; b < n; b += 32) {
+          const bool is = b + lane < n && b + lane > 0 && sm.parent[b + lane] == cur;
+          const uint32_t mask = __ballot_sync(0xffffffffu, is);
+          if (is) sm.child[n_child + __popc(mask & ((1u << lane) - 1))] = static_cast<int16_t>(b + lane);
+          n_child += __popc(mask);
+        }
+      if (lane == 0) sm.n_child = n_child;
+    }
+    __syncthreads();
+    // the CTA's part for the others
+    if (warp == 0) {
+      float m = sm.wm[lane % kVerWarps], s = sm.wz[lane % kVerWarps];
+      int i = sm.wi[lane % kVerWarps];
+      join(m, s, i, kVerWarps);
+      if (C == 1 && lane == 0) sm.ex.m[part.parity][0] = m, sm.ex.z[part.parity][0] = s, sm.ex.idx[part.parity][0] = i;
+      if (C > 1 && lane < C) {
+        st_cluster32(&sm.ex.m[part.parity][rank], lane, __float_as_uint(m));
+        st_cluster32(&sm.ex.z[part.parity][rank], lane, __float_as_uint(s));
+        st_cluster32(&sm.ex.idx[part.parity][rank], lane, static_cast<uint32_t>(i));
+      }
+      __syncwarp();
+    }
+    if (C > 1) cluster_arrive();
+    const int n_child = sm.n_child;
+    if (n_child > 0) {   // the next row is most likely the first child's: its part goes to L2 meanwhile
+      const char *next = reinterpret_cast<const char *>(p.logits + (static_cast<size_t>(t0) + sm.child[0]) * p.vocab) + 16ll * w0;
+      for (int b = 128 * lane; b < 16 * (w1 - w0); b += 128 * 32)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(next + b));
+    }
+    // the row's maximum, sum and argmax from the CTAs' (every warp for itself)
+    if (C > 1)
+      cluster_wait();
+    else
+      __syncthreads();
+    float m = sm.ex.m[part.parity][lane % C], Z = sm.ex.z[part.parity][lane % C];
+    int top = sm.ex.idx[part.parity][lane % C];
+    join(m, Z, top, C);
+    part.parity ^= 1;
+    if (m == -INFINITY) top = 0;   // no token has a chance: token 0
+    const __nv_bfloat16 *row = p.logits + (static_cast<size_t>(t0) + cur) * p.vocab;
+    // warp 0's lanes hold 32 children's values, from `first` on
+    int c_tok = -1;
+    float c_u = 2.f, c_l = -INFINITY, c_q = 0.f;
+    auto load_children = [&](int first) {
+      c_tok = -1;
+      if (first + lane < n_child) {
+        const int node = sm.child[first + lane];
+        c_tok = sm.token[node];
+        c_u = sm.u[node];
+        c_l = sm.logit[node];
+        c_q = sm.q[node];
+      }
+    };
+    if (warp == 0) load_children(0);
     // the children's tests, by warp 0: every CTA comes to the same answer
     int taken = -1;
     int64_t total = 0, before = 0;
