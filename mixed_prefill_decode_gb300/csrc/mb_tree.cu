@@ -77,7 +77,7 @@ constexpr int kRecBytes = 8192;     // workspace: one record of 8 ints per CTA, 
 // start and end, and the least a CTA takes (at least kCost2, so that no CTA
 // between the first and the last of a unit is left without a block).  A unit's
 // start and end cost what 2.5 blocks do: weighted by 3, 96 trees of 13 nodes at
-// 24 to 8,192 keys took 237 us, by 5 233, by 8 235; 64 at 1,125 keys 66.7, 66.8
+// 1,024 to 8,192 keys took 237 us, by 5 233, by 8 235; 64 at 1,125 keys 66.7, 66.8
 // and 67.3.
 constexpr int kCost1 = 2, kCost2 = 3, kCostUnit = 5, kMinShare = 3;
 
