@@ -375,6 +375,7 @@ mb_status mb_embed(const void *table, int32_t vocab, int32_t d, const int32_t *i
  * then its nodes in order, already appended) lie in pages
  * bt[bt_indptr[r] ..], token p in slot p % 16 of the table's page p / 16.
  * Node i sees the whole prefix, its ancestors and itself; scale 1/sqrt(hd).
+ * A request has at most 2^24 keys.
  *   q     device bf16 [T][Hq][hd] (rotated), 16-byte aligned
  *   pool  device bf16 [num_pages][2][Hkv][16][hd] (mb_kv_layout's), 128-byte aligned
  *   o     device bf16 [T][Hq hd], 16-byte aligned, must not alias q
@@ -383,8 +384,8 @@ mb_status mb_embed(const void *table, int32_t vocab, int32_t d, const int32_t *i
  * initialisation; a call owns it until it completes (calls on unordered
  * streams, graphs that may run at once, need one each).  Rows outside every
  * request are left as they were.  A request that breaks a rule (more than
- * MB_MAX_TREE_NODES nodes, kv_len below its nodes, a short table, rows outside
- * [0, T)) records MB_EDEVICE and its rows are left as they were; a page id out
+ * MB_MAX_TREE_NODES nodes, kv_len below its nodes or above 2^24, a short table,
+ * rows outside [0, T)) records MB_EDEVICE and its rows are left as they were; a page id out
  * of range is read as page 0, a parent out of range as -1, with MB_EDEVICE.
  * Non-finite values of keys and values that a node does not see do not reach
  * it.  Errors: MB_EINVAL, MB_EUNSUPPORTED, MB_ECUDA. */

@@ -50,12 +50,15 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const __grid_c
   pdl_wait();
   pdl_trigger();
   const int r = blockIdx.x;
-  const int t0 = p.qo_indptr[r], n = p.qo_indptr[r + 1] - t0, kv = p.kv_len[r], c = kv - n;
-  const int b0 = p.bt_indptr[r], pages = p.bt_indptr[r + 1] - b0;
+  const int t0 = p.qo_indptr[r], t1 = p.qo_indptr[r + 1], kv = p.kv_len[r];
+  const int b0 = p.bt_indptr[r], b1 = p.bt_indptr[r + 1];
   const int cnt = p.count[r];
+  // (compared before they are subtracted: the words may be anything)
+  const bool order = t0 >= 0 && t1 >= t0 && b0 >= 0 && b1 >= b0;
+  const int n = order ? t1 - t0 : 0, pages = order ? b1 - b0 : 0, c = kv < n ? -1 : kv - n;
   if (threadIdx.x == 0) s_n = 0;
-  bool bad = n < 0 || n > kMaxTreeNodes || c < 0 || b0 < 0 || (static_cast<int64_t>(kv) + kPage - 1) / kPage > pages || cnt < 0 || cnt > n ||
-             cnt > p.max_path;
+  bool bad = !order || n > kMaxTreeNodes || c < 0 || (static_cast<int64_t>(kv) + kPage - 1) / kPage > pages || cnt < 0 ||
+             cnt > n || cnt > p.max_path;
   __syncthreads();
   if (!bad) {
     const int64_t page_vecs = 2ll * p.Hkv * kPage * p.vec_per_row;

@@ -171,12 +171,12 @@ __device__ __forceinline__ RawReq load_raw(const TreeParams &p, int r) {
 __device__ __forceinline__ Req make_req(const TreeParams &p, const RawReq x, bool *bad) {
   Req q;
   q.t0 = x.q0;
-  q.n = x.q1 - x.q0;
   q.kv = x.kv;
   q.b0 = x.b0;
-  const int pages = x.b1 - x.b0;
-  *bad = q.t0 < 0 || q.n < 0 || q.n > kMaxTreeNodes || q.t0 + q.n > p.T || q.kv < q.n || q.kv > (1 << 24) || q.b0 < 0 ||
-         (q.kv + kPage - 1) / kPage > pages;
+  // (compared before they are subtracted: the words may be anything)
+  const bool order = x.q0 >= 0 && x.q1 >= x.q0 && x.q1 <= p.T && x.b0 >= 0 && x.b1 >= x.b0;
+  q.n = order ? x.q1 - x.q0 : 0;
+  *bad = !order || q.n > kMaxTreeNodes || q.kv < q.n || q.kv > (1 << 24) || (q.kv + kPage - 1) / kPage > x.b1 - x.b0;
   *bad = *bad && x.tree;
   if (*bad || !x.tree) q.n = 0;
   q.nkb = (q.kv + 127) / 128;

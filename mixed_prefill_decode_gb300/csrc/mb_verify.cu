@@ -322,9 +322,11 @@ __global__ void __launch_bounds__(kVerThreads, kVerPerSm) verify_kernel(const __
   pdl_trigger();
   if (C > 1) cluster_sync();   // every CTA of the cluster runs before one writes into another
   const int r = blockIdx.x / C;
-  const int t0 = p.qo_indptr[r], n = p.qo_indptr[r + 1] - t0;
+  const int t0 = p.qo_indptr[r], t1 = p.qo_indptr[r + 1];
   int32_t *path = p.path + static_cast<int64_t>(r) * p.max_path;
-  const bool bad = t0 < 0 || n < 0 || n > kMaxTreeNodes || t0 + n > p.T;
+  const bool order = t0 >= 0 && t1 >= t0 && t1 <= p.T;   // (compared before they are subtracted: the words may be anything)
+  const int n = order ? t1 - t0 : 0;
+  const bool bad = !order || n > kMaxTreeNodes;
   if (bad || n == 0) {
     if (rank == 0) {
       if (threadIdx.x == 0) {

@@ -419,6 +419,123 @@ def test_verify_reports_bad_descriptors(mb):
         mb.mb_device_status(None, _stream())
 
 
+@pytest.mark.parametrize("mode", ["points", "probs"])
+@pytest.mark.parametrize("sizes,vocab,kind,seed", [([128, 70, 33], 96, "star", 21), ([90], 40000, "star", 22),
+                                                   ([3], 1 << 19, "chain", 23), ([2, 3], 262144, "star", 24),
+                                                   ([5, 5], 65536, "wide", 25)])
+def test_verify_many_children_and_large_vocabularies(mb, mode, sizes, vocab, kind, seed):
+    """More children than a warp has lanes; every cluster size up to the largest row."""
+    d = Drafts(sizes, vocab, mode, seed, kind, agree=0.1 if sizes[0] > 30 else 0.7)
+    got = d.run(mb)
+    mb.mb_device_status(None, _stream())
+    d.check(got)
+
+
+def test_verify_draft_equal_to_the_target_and_useless_drafts(mb):
+    """q = p: a refusal leaves nothing or next to nothing, and the draw still has
+    a token.  A q of 1 on the child, 0 elsewhere, and not a number elsewhere: no
+    weight becomes negative."""
+    V = 4096
+    d = Drafts([2, 2, 2, 2], V, "probs", 26, "chain", temps=[1, 1, 1, 1])
+    p = np.exp(f64(d.logits) - f64(d.logits).max(1, keepdims=True))
+    p /= p.sum(1, keepdims=True)
+    d.probs[:] = p.astype(np.float32)
+    for r in (1, 2, 3):
+        d.probs[2 * r] = 0.0
+        d.probs[2 * r, d.tokens[2 * r + 1]] = 1.0
+    d.probs[6, :7] = np.nan
+    d.u_accept[:] = 1.0 - 2.0 ** -24
+    got = d.run(mb)
+    mb.mb_device_status(None, _stream())
+    assert np.all(got[0] >= 1) and np.all((got[2] >= 0) & (got[2] < V))
+    for r in (1, 2):
+        p_child = p[2 * r, d.tokens[2 * r + 1]]
+        if got[0][r] == 1:
+            assert d.u_accept[2 * r + 1] >= p_child * (1 - 1e-6) and got[2][r] != d.tokens[2 * r + 1]
+    if got[0][3] == 1:
+        assert got[2][3] >= 7   # a q that is not a number takes the token away
+
+
+def test_rows_given_by_words_that_wrap_around_are_refused(mb):
+    """qo_indptr words whose difference overflows to a valid size."""
+    t = Trees([(50, 40)], 2, 4, 128, 45)
+    wrap = np.array([2 ** 31 - 21, -2 ** 31 + 19], np.int32)   # 40 rows by subtraction in 32 bits
+    t.run(mb, qo=wrap)
+    with pytest.raises(mb.MbError) as e:
+        mb.mb_device_status(None, _stream())
+    assert e.value.status == mb.MB_EDEVICE
+    assert np.all(t.o.view(torch.int16).cpu().numpy().view(np.uint16) == SENT)
+    d = Drafts([40], 64, "points", 27, "wide")
+    d.qo = wrap
+    count, path, nxt = d.run(mb)
+    with pytest.raises(mb.MbError):
+        mb.mb_device_status(None, _stream())
+    assert count[0] == 0 and nxt[0] == -1 and np.all(path == -1)
+    pool = torch.zeros((4, 2, 2, 16, 64), dtype=torch.bfloat16, device="cuda")
+    new = torch.full((1,), -7, dtype=torch.int32, device="cuda")
+    mb.mb_kv_compact([pool], 4, 2, 64, 1, _i32(wrap), _i32([60]), _i32([0, 4]), _i32([0, 1, 2, 3]), _i32([1]),
+                     _i32([[0]]), 1, new, _stream())
+    with pytest.raises(mb.MbError):
+        mb.mb_device_status(None, _stream())
+    assert new.item() == -7
+
+
+def test_verify_and_compact_in_a_graph_beside_another_stream(mb):
+    """Verification and compaction captured together follow new logits, numbers
+    and paths, while eager calls run on another stream."""
+    sizes, V, hkv, hd = [6, 9, 1, 13], 8192, 2, 64
+    d = Drafts(sizes, V, "points", 28, "wide")
+    e = Drafts(sizes, V, "points", 29, "wide")
+    other = Drafts([7, 3], 32000, "probs", 30, "wide")
+    n, L = len(sizes), 16
+    kv = np.array([20 + s for s in sizes], np.int32)
+    need = (kv + 15) // 16
+    bti = np.concatenate([[0], np.cumsum(need)]).astype(np.int32)
+    bt = np.arange(bti[-1]).astype(np.int32)[::-1].copy()
+    rng = np.random.default_rng(31)
+    pools = rng.integers(0, 1 << 16, size=(2, int(bti[-1]), 2, hkv, 16, hd)).astype(np.uint16)
+    d.run(mb)
+    v = d.dev
+    dev = [to_dev(p) for p in pools]
+    out = [torch.full(s, -7, dtype=torch.int32, device="cuda") for s in ((n,), (n, L), (n,))]
+    dkv, dbti, dbt = _i32(kv), _i32(bti), _i32(bt)
+    new = torch.zeros_like(dkv)
+
+    def step():
+        s = _stream()
+        mb.mb_verify_tree(v["logits"], V, v["tokens"], v["probs"], n, d.T, v["qo"], v["parent"], v["temp"], v["ua"], v["uf"],
+                          L, *out, s)
+        mb.mb_kv_compact(dev, int(bti[-1]), hkv, hd, n, v["qo"], dkv, dbti, dbt, out[0], out[1], L, new, s)
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    s2 = torch.cuda.Stream()
+    s2.wait_stream(torch.cuda.current_stream())
+    for case in (e, d):
+        for k, a in (("logits", to_dev(case.logits)), ("tokens", _i32(case.tokens)), ("parent", _i32(case.parent)),
+                     ("temp", torch.from_numpy(case.temp).cuda()), ("ua", torch.from_numpy(case.u_accept).cuda()),
+                     ("uf", torch.from_numpy(case.u_final).cuda())):
+            v[k].copy_(a)
+        for x, p in zip(dev, pools):
+            x.copy_(to_dev(p))
+        torch.cuda.synchronize()
+        g.replay()
+        with torch.cuda.stream(s2):
+            beside = other.run(mb)
+        torch.cuda.synchronize()
+        mb.mb_device_status(None, _stream())
+        got = [x.cpu().numpy() for x in out]
+        case.check(got, L)
+        other.check(beside)
+        paths = [list(got[1][r, :got[0][r]]) for r in range(n)]
+        for x, p in zip(dev, pools):
+            want = p.copy()
+            lens = OS.compact(want, case.qo, kv, bti, bt, paths)
+            assert np.array_equal(from_dev(x), want)
+        assert np.array_equal(new.cpu().numpy(), lens)
+
+
 # --------------------------------------------------------- page operations
 @pytest.mark.parametrize("hkv,hd,layers", [(2, 64, 1), (8, 128, 3), (1, 128, 130), (3, 40, 2)])
 def test_compact_moves_the_path_and_nothing_else(mb, hkv, hd, layers):
