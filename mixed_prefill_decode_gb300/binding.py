@@ -356,10 +356,6 @@ def _pool_array(pools) -> array.array:
         return array.array("Q", [_ptr(p) or 0 for p in pools])
 
 
-def _addr(a: np.ndarray) -> int:
-    return a.__array_interface__["data"][0]
-
-
 def mb_kv_compact(pools: Sequence, num_pages: int, n_kv_heads: int, head_dim: int, num_reqs: int, qo_indptr, kv_len,
                   bt_indptr, bt, n_accepted, path, max_path: int, new_kv_len, stream=None) -> None:
     bases = _pool_array(pools)
@@ -373,9 +369,11 @@ def mb_kv_copy_pages(pools: Sequence, num_pages: int, n_kv_heads: int, head_dim:
     src, dst = _i32(src), _i32(dst)
     if src.ndim != 1 or src.shape != dst.shape:
         raise ValueError("src and dst must be one-dimensional and of equal length")
-    bases = _pool_array(pools)
-    _check(lib().mb_kv_copy_pages(bases.buffer_info()[0], len(bases), num_pages, n_kv_heads, head_dim, _addr(src),
-                                  _addr(dst), len(src), _ptr(stream)))
+    bases, n = _pool_array(pools), len(src)
+    # (a copy's address costs less than numpy's way to its own)
+    src, dst = array.array("i", src.tobytes()), array.array("i", dst.tobytes())
+    _check(lib().mb_kv_copy_pages(bases.buffer_info()[0], len(bases), num_pages, n_kv_heads, head_dim,
+                                  src.buffer_info()[0], dst.buffer_info()[0], n, _ptr(stream)))
 
 
 # ------------------------------------------------------------- scheduler
