@@ -18,12 +18,12 @@
 // bound by HBM and larger ones by the tensor cores and the softmax.
 //
 // Measured (head_dim 128, G = 4, 8 KV heads): 16 trees of 8 nodes at 8,192
-// keys 96 us, 5.6 TB/s, 83 % of a copy's rate; 64 trees of 8 at 1,125 keys
-// 67 us, 4.5 TB/s (a CTA has 3.4 units of 9 blocks each, and every unit's end
+// keys 95 us, 5.7 TB/s, 84 % of a copy's rate; 64 trees of 8 at 1,125 keys
+// 66 us, 4.6 TB/s (a CTA has 3.4 units of 9 blocks each, and every unit's end
 // waits for its last softmax and product); 16 trees of 64 nodes at 8,192 keys
-// 156 us, 1.10 PFLOP/s of bf16, 57 % of a plain matrix product's rate, bound
+// 154 us, 0.89 PFLOP/s of bf16, 46 % of a plain matrix product's rate, bound
 // by the softmax's exponentials and the turns of the two warp groups; one tree
-// of 6 nodes at 1,125 keys 14 us, two launches and the chain of one block.
+// of 6 nodes at 1,125 keys 12.5 us, two launches and the chain of one block.
 //
 // Layout of the work.  The rows that share a KV head, (node, q-head of the
 // group), row = node G + g, are the M side of the products: 128 / G nodes make
@@ -989,11 +989,13 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
 // Merge of the units that were cut: CTA (w, y) takes every gridDim.y-th row
 // group of the unit whose first piece CTA w computed.
 //   o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,   M = max_s m_s
-// One warp takes a row, lane s holding piece s's (m, l), with the loads of all
-// pieces in flight at once; where there are many rows of few pieces, 8 lanes
-// take a row and a warp four at a time (16 trees of 64 nodes at 8,192 keys, 256
-// rows a unit: 158 us in all against 165; one tree of 6 nodes at 1,125 keys,
-// 24 rows of 8 pieces: 18 us against 13.6, so it is for more than 64 rows).
+// One warp takes a row, lane s holding piece s's (m, l); the first pieces' rows
+// are loaded beside them, not after the weights are known (one tree of 6 nodes at
+// 1,125 keys 12.5 us in all against 13.9, at 8,192 keys 16.5 against 18.8).
+// Where there are many rows of few pieces, 8 lanes take a row and a warp four at
+// a time (16 trees of 64 nodes at 8,192 keys, 256 rows a unit: 158 us in all
+// against 165; one tree of 6 nodes, 24 rows of 8 pieces: 18 us against 13.6, so
+// it is for more than 64 rows).
 template <int HD>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeParams p) {
   pdl_wait();
@@ -1049,30 +1051,39 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
   }
   constexpr int PER = HD / 32;
   using Vec = typename std::conditional<HD == 128, float4, float2>::type;
+  constexpr int AHEAD = 4;   // pieces whose rows are in flight together, from before their weights are known
   for (int row = blockIdx.y * 8 + warp; row < rows; row += gridDim.y * 8) {
-    float M = -INFINITY;
-    for (int s = lane; s < pieces; s += 32) M = fmaxf(M, src(s, row)[HD]);
+    Vec x[AHEAD];
+    auto fetch = [&](int s0) {
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u)
+        if (s0 + u < pieces) x[u] = reinterpret_cast<const Vec *>(src(s0 + u, row))[lane];
+    };
+    auto m_and_l = [&](int s) {
+      return s < pieces ? *reinterpret_cast<const float2 *>(src(s, row) + HD) : make_float2(-INFINITY, 0.f);
+    };
+    float2 ml = m_and_l(lane);
+    fetch(0);
+    float M = ml.x;
+    for (int s = lane + 32; s < pieces; s += 32) M = fmaxf(M, src(s, row)[HD]);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     float L = 0.f, acc[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) acc[k] = 0.f;
     for (int s0 = 0; s0 < pieces; s0 += 32) {
-      float wgt = 0.f;
-      if (s0 + lane < pieces) {
-        const float *x = src(s0 + lane, row);
-        wgt = x[HD] == -INFINITY ? 0.f : ex2_approx(x[HD] - M);
-        L = fmaf(wgt, x[HD + 1], L);
-      }
-      const int ns = min(32, pieces - s0);
-#pragma unroll 4
-      for (int s = 0; s < ns; ++s) {
-        const float ws = __shfl_sync(0xffffffffu, wgt, s);
-        const Vec x = reinterpret_cast<const Vec *>(src(s0 + s, row))[lane];
-        const float *xf = reinterpret_cast<const float *>(&x);
-        // (weight 0: the row saw nothing in the piece)
+      if (s0 > 0) ml = m_and_l(s0 + lane);
+      const float wgt = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+      L = fmaf(wgt, ml.y, L);
+      for (int s = 0; s < 32 && s0 + s < pieces; s += AHEAD) {
 #pragma unroll
-        for (int k = 0; k < PER; ++k) acc[k] = ws != 0.f ? fmaf(ws, xf[k], acc[k]) : acc[k];
+        for (int u = 0; u < AHEAD; ++u) {
+          const float ws = __shfl_sync(0xffffffffu, wgt, s + u);   // (0: no such piece, or the row saw nothing in it)
+          const float *xf = reinterpret_cast<const float *>(&x[u]);
+#pragma unroll
+          for (int k = 0; k < PER; ++k) acc[k] = ws != 0.f ? fmaf(ws, xf[k], acc[k]) : acc[k];
+        }
+        fetch(s0 + s + AHEAD);
       }
     }
 #pragma unroll
