@@ -31,13 +31,13 @@
 // what a full GPU spends most of its time on.
 //
 // Measured: one chain of 5 drafted tokens, vocabulary 128,256, with draft
-// probabilities, 28 us, some 3.5 us a node; 64 such 78 us, of which a node's
+// probabilities, 27.5 us, some 3.5 us a node; 64 such 75 us, of which a node's
 // step takes about 5 us and an accurate pass over the row 10 to 15 (the walks
 // read 82 MB: 1.1 TB/s); 16 trees of 24, vocabulary 50,264, 21 us; 6 tokens,
 // greedy, vocabulary 32,000, 7 us.  Tried and dropped: a table of the weights
 // of all bf16 logits in shared memory (its random 8-byte reads took 7 cycles a
 // warp); an only child's row fetched over its parent's, with its maximum and
-// sum computed during the parent's exchange (64 chains 80 us: what it hides is
+// sum computed during the parent's exchange (64 chains 80 us against 78: what it hides is
 // latency that the SM's other CTAs hide already, and a refusal has to fetch the
 // parent's row again).
 
@@ -132,7 +132,7 @@ __device__ __forceinline__ float bf16_of(const uint4 &raw, int e) {
 
 // What a weight depends on beside its logit and draft probability.
 struct WeightCtx {
-  float m, kh, kl;         // weight 2^((l - m) k), k = kh + kl
+  float m, kh32, kl32;     // weight 2^((l - m) k), 32 k = kh32 + kl32
   float d_max;             // m - l from which on it is 2^-48
   float az_hi, az_lo;      // less az q (both times 2^20)
   float q_small, q_any;    // q from which on az q is above 2^-11, above 1
@@ -144,22 +144,18 @@ __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 // Two weights as fix_exp computes them, in packed fp32: v 2^(11 - s) in units
 // of 2^-41.  D: m - l.
 __device__ __forceinline__ void weight_pair(const WeightCtx &c, float2 D, uint32_t *v, int32_t *s) {
-  constexpr float kMagic = 12582912.f;      // 1.5 2^23
-  constexpr int32_t kMagicBits = 0x4B400000;
   D.x = fminf(D.x, c.d_max);   // (an infinity, a NaN: 2^-48, which rounds to 0)
   D.y = fminf(D.y, c.d_max);
-  const float2 y = __fmul2_rn(D, both(-c.kh));                                   // y - r = -D k
-  const float2 r = __ffma2_rn(D, both(c.kl), __ffma2_rn(D, both(c.kh), y));
-  const float2 t = __ffma2_rn(y, both(32.f), both(kMagic));
-  const float2 n = __fadd2_rn(t, both(-kMagic));
-  const float2 f = __ffma2_rn(r, both(-1.f), __ffma2_rn(n, both(-0.03125f), y));
-  float2 g = __ffma2_rn(f, both(0.0096181291f), both(0.0555041087f));
-  g = __ffma2_rn(g, f, both(0.2402265070f));
-  g = __ffma2_rn(g, f, both(0.6931471806f));
+  const float2 t = __ffma2_rn(D, both(c.kh32), both(kFixMagic));
+  const float2 n = __fadd2_rn(t, both(-kFixMagic));
+  const float2 f = __ffma2_rn(D, both(-c.kl32), __ffma2_rn(D, both(-c.kh32), n));
+  float2 g = __ffma2_rn(f, both(kFixC4), both(kFixC3));
+  g = __ffma2_rn(g, f, both(kFixC2));
+  g = __ffma2_rn(g, f, both(kFixC1));
   g = __fmul2_rn(g, f);
   const int32_t t0 = __float_as_int(t.x), t1 = __float_as_int(t.y);
-  s[0] = (kMagicBits - t0 + 31) >> 5;
-  s[1] = (kMagicBits - t1 + 31) >> 5;
+  s[0] = (t0 - kFixMagicBits + 31) >> 5;
+  s[1] = (t1 - kFixMagicBits + 31) >> 5;
   v[0] = sm.tab_fix[t0 & 31] + static_cast<uint32_t>(__float2int_rn(sm.tab_scaled[t0 & 31] * g.x));
   v[1] = sm.tab_fix[t1 & 31] + static_cast<uint32_t>(__float2int_rn(sm.tab_scaled[t1 & 31] * g.y));
 }
@@ -172,23 +168,16 @@ __device__ __forceinline__ int64_t large_weight(uint32_t v, int32_t s) {
   return static_cast<int64_t>((((static_cast<uint64_t>(v) << 12) >> s) + 1) >> 1);
 }
 
-// az q of two tokens in units of 2^-41, as hi 2^21 + lo.  A q above `top` (a
-// NaN too) counts as that: az q is then more than any weight beside it.
-__device__ __forceinline__ void fixed_q(const WeightCtx &c, float2 q, float top, int32_t (&hi)[2], int32_t (&lo)[2]) {
-  constexpr float kMagic = 12582912.f;
-  constexpr int32_t kMagicBits = 0x4B400000;
-  q.x = fminf(q.x, top);
-  q.y = fminf(q.y, top);
-  const float2 x = __fmul2_rn(q, both(c.az_hi));
-  const float2 l = __ffma2_rn(q, both(c.az_lo), __ffma2_rn(q, both(c.az_hi), make_float2(-x.x, -x.y)));
-  const float2 a = __fadd2_rn(x, both(kMagic));
-  const float2 n = __fadd2_rn(a, both(-kMagic));
-  const float2 rem = __fadd2_rn(__ffma2_rn(n, both(-1.f), x), l);
-  const float2 b = __ffma2_rn(rem, both(0x1p21f), both(kMagic));
-  hi[0] = __float_as_int(a.x) - kMagicBits;
-  hi[1] = __float_as_int(a.y) - kMagicBits;
-  lo[0] = __float_as_int(b.x) - kMagicBits;
-  lo[1] = __float_as_int(b.y) - kMagicBits;
+// az q in units of 2^-41, as hi 2^21 + lo.  A q above `top` (a NaN too) counts
+// as that: az q is then more than any weight beside it.  (In packed fp32, two
+// tokens at a time, 64 chains took 77.6 us against 76.3.)
+__device__ __forceinline__ void fixed_q(const WeightCtx &c, float q, float top, int32_t &hi, int32_t &lo) {
+  q = fminf(q, top);
+  const float x = q * c.az_hi, l = fmaf(q, c.az_lo, fmaf(q, c.az_hi, -x));
+  const float a = x + kFixMagic;
+  const float b = fmaf((x - (a - kFixMagic)) + l, 0x1p21f, kFixMagic);
+  hi = __float_as_int(a) - kFixMagicBits;
+  lo = __float_as_int(b) - kFixMagicBits;
 }
 
 // m - l, with a row's infinities in order: l = m gives 0, less than m = +inf everything.
@@ -197,12 +186,12 @@ __device__ __forceinline__ float below(const WeightCtx &c, float l) { return l =
 // The weight of one token (any lane by itself).
 __device__ __noinline__ int64_t token_weight(const WeightCtx &c, float l, bool probs, float q) {
   uint32_t v[2];
-  int32_t s[2], hi[2], lo[2];
+  int32_t s[2], hi, lo;
   weight_pair(c, make_float2(below(c, l), 0.f), v, s);
   const int64_t w = large_weight(v[0], s[0]);
   if (!probs) return w;
-  fixed_q(c, both(q), c.q_any, hi, lo);
-  return max(w - (static_cast<int64_t>(hi[0]) << 21) - lo[0], static_cast<int64_t>(0));
+  fixed_q(c, q, c.q_any, hi, lo);
+  return max(w - (static_cast<int64_t>(hi) << 21) - lo, static_cast<int64_t>(0));
 }
 
 // Weight of vector v (8 tokens, at x; q: their draft probabilities), refused
@@ -224,27 +213,29 @@ __device__ __forceinline__ int64_t vector_weight(const WeightCtx &c, const uint4
     const int least = min(min(min(ws[0], ws[1]), min(ws[2], ws[3])), min(min(ws[4], ws[5]), min(ws[6], ws[7])));
     if (__any_sync(0xffffffffu, least < 12)) {
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        int64_t a = large_weight(wv[e], ws[e]), b = large_weight(wv[e + 1], ws[e + 1]);
+      for (int e = 0; e < 8; ++e) {
+        int64_t a = large_weight(wv[e], ws[e]);
         if (PROBS) {
-          int32_t hi[2], lo[2];
-          fixed_q(c, make_float2(q[e], q[e + 1]), c.q_any, hi, lo);
-          a = max(a - (static_cast<int64_t>(hi[0]) << 21) - lo[0], static_cast<int64_t>(0));
-          b = max(b - (static_cast<int64_t>(hi[1]) << 21) - lo[1], static_cast<int64_t>(0));
+          int32_t hi, lo;
+          fixed_q(c, q[e], c.q_any, hi, lo);
+          a = max(a - (static_cast<int64_t>(hi) << 21) - lo, static_cast<int64_t>(0));
         }
-        sum += a + b;
+        sum += a;
       }
     } else {
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
-        int32_t a = small_weight(wv[e], ws[e]), b = small_weight(wv[e + 1], ws[e + 1]);
-        if (PROBS) {
-          int32_t hi[2], lo[2];
-          fixed_q(c, make_float2(q[e], q[e + 1]), c.q_small, hi, lo);
-          a = max(a - (hi[0] << 21) - lo[0], 0);
-          b = max(b - (hi[1] << 21) - lo[1], 0);
+        int32_t a[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          a[h] = small_weight(wv[e + h], ws[e + h]);
+          if (PROBS) {
+            int32_t hi, lo;
+            fixed_q(c, q[e + h], c.q_small, hi, lo);
+            a[h] = max(a[h] - (hi << 21) - lo, 0);
+          }
         }
-        sum += static_cast<uint32_t>(a) + static_cast<uint32_t>(b);
+        sum += static_cast<uint32_t>(a[0]) + static_cast<uint32_t>(a[1]);
       }
     }
   } else {
@@ -517,7 +508,7 @@ __global__ void __launch_bounds__(kVerThreads, kVerPerSm) verify_kernel(const __
     int64_t total = 0, before = 0;
     int final_gone = 0;
     const float *qrow = nullptr;
-    WeightCtx ctx{m, kh, kl, d_max, 0.f, 0.f, 0.f, 0.f, 0};
+    WeightCtx ctx{m, 32.f * kh, 32.f * kl, d_max, 0.f, 0.f, 0.f, 0.f, 0};
     bool have_sums = false;
     if (rank == 0 && threadIdx.x == 0) path[len - 1] = cur;
     if (greedy || !p.probs) {
@@ -623,7 +614,7 @@ __global__ void __launch_bounds__(kVerThreads, kVerPerSm) verify_kernel(const __
     }
     if (total == 0) {    // the refusals left nothing: p itself
       qrow = nullptr;
-      ctx = {m, kh, kl, d_max, 0.f, 0.f, 0.f, 0.f, 0};
+      ctx = {m, 32.f * kh, 32.f * kl, d_max, 0.f, 0.f, 0.f, 0.f, 0};
       total = weight_sums<false>(part, ctx, nullptr, &before);
     }
     if (threadIdx.x == 0) {
