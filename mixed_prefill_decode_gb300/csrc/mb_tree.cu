@@ -237,6 +237,13 @@ __device__ __forceinline__ void probs(const float (&sv)[N], float2 sc2, float ne
   }
 }
 
+// One lane of a converged warp (the same one each time).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
+  return is != 0;
+}
+
 __device__ __noinline__ int64_t div64(int64_t a, int64_t b) { return a / b; }
 
 // Takes the logits of keys that a row does not see out of a block of S (to
@@ -304,7 +311,7 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
   static_assert(sizeof(Ctrl<HD>) <= 2048, "control area");
   Ctrl<HD> &ct = *reinterpret_cast<Ctrl<HD> *>(smem + C::OFF_CTRL);
   volatile int *abort_flag = &ct.abort;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;   // (known uniform)
   if (smem_u32(smem) & 1023u) {   // the swizzled layouts need a 1024-aligned base
     pdl_wait();
     if (threadIdx.x == 0) {
@@ -371,7 +378,7 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ct.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ct.tmem, 0);
   int64_t total = 0, pre = inc - mine;
 #pragma unroll
   for (int w = 0; w < C::THREADS / 32; ++w) {
@@ -601,47 +608,52 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ------------------------------------------------------- MMA issuer
-      // Items in order: block by block, tile by tile.  S of an item goes out
-      // as soon as its K (and Q) landed and the P V before the last one is
-      // issued (its S buffer is then free, in order); P V as soon as P is
-      // written and V landed.  S runs on into the next piece.
-      const uint64_t qd0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
-      const uint64_t kd0 = sdesc_sw128(smem_u32(sK), 16, C::ATOM_STRIDE);
-      const uint64_t vd0 = sdesc_sw128(smem_u32(sV), 1024, C::ATOM_STRIDE);
-      struct Cursor {
-        int seg, blk, item;      // pieces, blocks and items before it
-        int nb, qt, qb, lb, t;   // the piece, and the place in it
-        bool in;
-      };
-      Cursor s{0, 0, 0, 0, 0, 0, 0, 0, false}, v{0, 0, 0, 0, 0, 0, 0, 0, false};
-      int quse[2] = {0, 0};
-      bool s_end = false;
-      uint64_t t_idle = 0;
-      auto enter = [&](Cursor &x) {
-        const Seg &sg = ct.seg[x.seg % C::NSEG];
-        x.nb = sg.nb;
-        x.qt = sg.qt;
-        x.qb = sg.qb;
-        x.lb = x.t = 0;
-        x.in = true;
-      };
-      for (uint32_t spin = 1;; ++spin) {   // rounds without progress
-        bool progress = false;
-        if (!s_end && s.item < v.item + 2) {
-          if (!s.in && mbar_test_wait(smem_u32(&ct.seg_full[s.seg % C::NSEG]), (s.seg / C::NSEG) & 1)) {
-            enter(s);
-            if (s.nb == 0) s_end = true;
-          }
-          if (s.in && !s_end) {
-            const int qb = s.qb ^ s.t, st = s.blk % C::NK;
-            if ((s.lb > 0 || mbar_test_wait(smem_u32(&ct.q_full[qb]), quse[qb] & 1)) &&
-                mbar_test_wait(smem_u32(&ct.k_full[st]), (s.blk / C::NK) & 1)) {
-              tc_fence_after();
-              const uint32_t d = tmem + 128 * (s.item & 1);
-              const uint64_t qd = qd0 + static_cast<uint64_t>((qb * C::QT_BYTES) >> 4);
-              const uint64_t kd = kd0 + static_cast<uint64_t>((st * C::KV_BYTES) >> 4);
+    // --------------------------------------------------------- MMA issuer
+    // Items in order: block by block, tile by tile.  S of an item goes out
+    // as soon as its K (and Q) landed and the P V before the last one is
+    // issued (its S buffer is then free, in order); P V as soon as P is
+    // written and V landed.  S runs on into the next piece.  The whole warp
+    // keeps the books, in step, and one elected lane issues.
+    const uint64_t qd0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
+    const uint64_t kd0 = sdesc_sw128(smem_u32(sK), 16, C::ATOM_STRIDE);
+    const uint64_t vd0 = sdesc_sw128(smem_u32(sV), 1024, C::ATOM_STRIDE);
+    struct Cursor {
+      int seg, blk, item;      // pieces, blocks and items before it
+      int nb, qt, qb, lb, t;   // the piece, and the place in it
+      bool in;
+    };
+    Cursor s{0, 0, 0, 0, 0, 0, 0, 0, false}, v{0, 0, 0, 0, 0, 0, 0, 0, false};
+    int quse[2] = {0, 0};
+    bool s_end = false;
+    uint64_t t_idle = 0;
+    auto uni = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    auto ready = [](uint64_t *bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_test_wait(smem_u32(bar), parity)) != 0;
+    };
+    auto enter = [&](Cursor &x) {
+      const Seg &sg = ct.seg[x.seg % C::NSEG];
+      x.nb = uni(sg.nb);
+      x.qt = uni(sg.qt);
+      x.qb = uni(sg.qb);
+      x.lb = x.t = 0;
+      x.in = true;
+    };
+    for (uint32_t spin = 1;; ++spin) {   // rounds without progress
+      bool progress = false;
+      if (!s_end && s.item < v.item + 2) {
+        if (!s.in && ready(&ct.seg_full[s.seg % C::NSEG], (s.seg / C::NSEG) & 1)) {
+          enter(s);
+          if (s.nb == 0) s_end = true;
+        }
+        if (s.in && !s_end) {
+          const int qb = s.qb ^ s.t, st = s.blk % C::NK;
+          if ((s.lb > 0 || ready(&ct.q_full[qb], quse[qb] & 1)) && ready(&ct.k_full[st], (s.blk / C::NK) & 1)) {
+            tc_fence_after();
+            const uint32_t d = tmem + 128 * (s.item & 1);
+            const uint64_t qd = qd0 + static_cast<uint64_t>((qb * C::QT_BYTES) >> 4);
+            const uint64_t kd = kd0 + static_cast<uint64_t>((st * C::KV_BYTES) >> 4);
+            const bool last = s.lb == s.nb - 1, k_done = s.t + 1 == s.qt;
+            if (elect_one()) {
 #pragma unroll
               for (int ch = 0; ch < C::NH; ++ch)
 #pragma unroll
@@ -649,73 +661,79 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
                   mma_bf16(d, qd + ((ch * C::TILE_BYTES + kk * 32) >> 4), kd + ((ch * 1024 + kk * 32) >> 4), C::IDESC_S,
                            (ch > 0 || kk > 0) ? 1u : 0u);
               mma_commit(&ct.s_full[s.item & 1]);
-              if (s.lb == s.nb - 1) {
-                mma_commit(&ct.q_empty[qb]);
-                ++quse[qb];
-              }
-              ++s.item;
-              if (++s.t == s.qt) {
-                mma_commit(&ct.k_empty[st]);
-                s.t = 0;
-                ++s.blk;
-                if (++s.lb == s.nb) {
-                  s.in = false;
-                  ++s.seg;
-                }
-              }
-              progress = true;
+              if (last) mma_commit(&ct.q_empty[qb]);
+              if (k_done) mma_commit(&ct.k_empty[st]);
             }
-          }
-        }
-        if (v.item < s.item) {
-          if (!v.in) enter(v);   // S of the piece is out: its record is there
-          const int st = v.blk % C::NV;
-          if (mbar_test_wait(smem_u32(&ct.p_full[v.item & 1]), (v.item >> 1) & 1) &&
-              mbar_test_wait(smem_u32(&ct.v_full[st]), (v.blk / C::NV) & 1)) {
-            tc_fence_after();
-            const uint64_t vd = vd0 + static_cast<uint64_t>((st * C::KV_BYTES) >> 4);
-            const int w = v.item & 1;               // warp group, S buffer, O accumulator
-            const uint32_t pcol = tmem + 128 * w;
-            const bool first = v.lb < (v.qt == 1 ? 2 : 1);   // the group's first block of the piece
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)   // 16 keys (two atoms) per MMA; hd halves 1 KB apart
-              mma_bf16_ts(tmem + C::O_COL + HD * w, pcol + ks * 8, vd + ((ks * 2 * C::ATOM_STRIDE) >> 4), C::IDESC_PV,
-                          (!first || ks > 0) ? 1u : 0u);
-            mma_commit(&ct.o_full[w]);
-            ++v.item;
-            if (++v.t == v.qt) {
-              mma_commit(&ct.v_empty[st]);
-              v.t = 0;
-              ++v.blk;
-              if (++v.lb == v.nb) {
-                v.in = false;
-                mbar_arrive(&ct.seg_empty[v.seg % C::NSEG]);
-                ++v.seg;
+            __syncwarp();
+            if (last) ++quse[qb];
+            ++s.item;
+            if (++s.t == s.qt) {
+              s.t = 0;
+              ++s.blk;
+              if (++s.lb == s.nb) {
+                s.in = false;
+                ++s.seg;
               }
             }
             progress = true;
           }
         }
-        if (s_end && v.item == s.item) break;
-        if (progress) {
-          spin = 0;
-          t_idle = 0;
-        } else if ((spin & 255u) == 0) {
-          if (*abort_flag) break;
-          if (t_idle == 0) t_idle = globaltimer();
-          if (globaltimer() - t_idle > kWaitLimitNs) {
-            *abort_flag = 1;
-            atomicExch(p.err, kErrWaitMma);
-            break;
+      }
+      if (v.item < s.item) {
+        if (!v.in) enter(v);   // S of the piece is out: its record is there
+        const int st = v.blk % C::NV;
+        if (ready(&ct.p_full[v.item & 1], (v.item >> 1) & 1) && ready(&ct.v_full[st], (v.blk / C::NV) & 1)) {
+          tc_fence_after();
+          const uint64_t vd = vd0 + static_cast<uint64_t>((st * C::KV_BYTES) >> 4);
+          const int w = v.item & 1;               // warp group, S buffer, O accumulator
+          const uint32_t pcol = tmem + 128 * w;
+          const bool first = v.lb < (v.qt == 1 ? 2 : 1);   // the group's first block of the piece
+          const bool v_done = v.t + 1 == v.qt, last = v_done && v.lb + 1 == v.nb;
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)   // 16 keys (two atoms) per MMA; hd halves 1 KB apart
+              mma_bf16_ts(tmem + C::O_COL + HD * w, pcol + ks * 8, vd + ((ks * 2 * C::ATOM_STRIDE) >> 4), C::IDESC_PV,
+                          (!first || ks > 0) ? 1u : 0u);
+            mma_commit(&ct.o_full[w]);
+            if (v_done) mma_commit(&ct.v_empty[st]);
+            if (last) mbar_arrive(&ct.seg_empty[v.seg % C::NSEG]);
           }
+          __syncwarp();
+          ++v.item;
+          if (++v.t == v.qt) {
+            v.t = 0;
+            ++v.blk;
+            if (++v.lb == v.nb) {
+              v.in = false;
+              ++v.seg;
+            }
+          }
+          progress = true;
         }
       }
-      // every MMA issued above has completed before TMEM is freed
-      mma_commit(&ct.done);
-      const uint64_t t_end = globaltimer();
-      while (!mbar_try_wait(smem_u32(&ct.done), 0) && globaltimer() - t_end < kWaitLimitNs) {
+      if (s_end && v.item == s.item) break;
+      if (progress) {
+        spin = 0;
+        t_idle = 0;
+      } else if ((spin & 255u) == 0) {
+        if (t_idle == 0) t_idle = globaltimer();
+        const bool late = globaltimer() - t_idle > kWaitLimitNs;
+        if (__any_sync(0xffffffffu, late || *abort_flag)) {
+          if (__any_sync(0xffffffffu, late) && lane == 0) {
+            *abort_flag = 1;
+            atomicExch(p.err, kErrWaitMma);
+          }
+          break;
+        }
       }
     }
+    // every MMA issued above has completed before TMEM is freed
+    if (elect_one()) mma_commit(&ct.done);
+    __syncwarp();
+    const uint64_t t_end = globaltimer();
+    while (!mbar_try_wait(smem_u32(&ct.done), 0) && globaltimer() - t_end < kWaitLimitNs) {
+    }
+    __syncwarp();
   } else {
     // ------------------------------------------------- softmax / epilogue
     const int w = (warp - 2) >> 2;          // warp group: it takes every second item
