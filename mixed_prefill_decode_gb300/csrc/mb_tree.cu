@@ -299,6 +299,58 @@ __device__ __noinline__ void add_odd(const TreeParams &p, const Seg &sg, uint4 s
   }
 }
 
+// What a warp's rows need on their way out of TMEM.
+template <int HD>
+struct Rows {
+  const TreeParams *p;
+  const Seg *sg;
+  uint4 see;
+  int tok, head;
+  uint32_t o_col, o_other;   // this group's O, the other's
+  bool joint, whole, cut;    // o = wa o + wb o_other; to o, or to a partial (neither: no row)
+  float wa, wb, inv, m;
+  uint4 *dst;
+  float *part;
+};
+
+// The rows of a warp to o, or to a partial.  Rolled: the code of a unit's end is
+// cold each time it is reached, and with four copies of the loop's body 256
+// trees of 8 nodes at 300 keys took 121 us against 99.  (ODD, almost never, is
+// out of line for the same reason.)
+template <int HD, bool ODD>
+__device__ __forceinline__ void write_rows(const Rows<HD> &r, bool odd) {
+#pragma unroll 1
+  for (int cc = 0; cc < HD / 32; ++cc) {
+    float v[32];
+    if (r.joint) {
+      float x[32];
+      tmem_ld32x2(r.o_col + cc * 32, r.o_other + cc * 32, v, x);
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] = r.wa * v[k] + r.wb * x[k];
+    } else {
+      tmem_ld32(r.o_col + cc * 32, v);
+    }
+    if (ODD && odd) add_odd<HD>(*r.p, *r.sg, r.see, r.tok, r.head, r.m, cc * 32, v);
+    if (r.whole) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        r.dst[cc * 4 + k] = make_uint4(pack_bf16x2(v[8 * k] * r.inv, v[8 * k + 1] * r.inv),
+                                       pack_bf16x2(v[8 * k + 2] * r.inv, v[8 * k + 3] * r.inv),
+                                       pack_bf16x2(v[8 * k + 4] * r.inv, v[8 * k + 5] * r.inv),
+                                       pack_bf16x2(v[8 * k + 6] * r.inv, v[8 * k + 7] * r.inv));
+    } else if (r.cut) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        reinterpret_cast<float4 *>(r.part + cc * 32)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+    }
+  }
+}
+
+template <int HD>
+__device__ __noinline__ void write_odd(const Rows<HD> &r, bool odd) {
+  write_rows<HD, true>(r, odd);
+}
+
 template <int HD>
 __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmKV,
@@ -797,14 +849,31 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
         const bool full = key0 + 128 <= c;   // only prefix keys: visible to every row
         if (!idle) {
           if (!full) mask_block(s_col, key0 - c, see);
-          // One pass over S while the row's reference maximum holds; if a row
-          // of the warp rose more than 2^8 above it (always at the piece's
-          // first block), the reference moves, O is rescaled and the
-          // probabilities are taken again from S, intact until P is stored.
+          // The group's first block of the piece sets each row's reference
+          // maximum.  From then on one pass over S while it holds; if a row of
+          // the warp rose more than 2^8 above it, the reference moves, O is
+          // rescaled and the probabilities are taken again from S, intact
+          // until P is stored.
           uint32_t pk_lo[32], pk_hi[32];
           float2 lsum = make_float2(0.f, 0.f);
           float mq0 = -INFINITY, mq1 = -INFINITY, mq2 = -INFINITY, mq3 = -INFINITY;
-          const bool have_ref = li >= 2;
+          if (li < 2) {
+            float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+              float sv[32];
+              tmem_ld32(s_col + 32 * k, sv);
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                m0 = max3f(m0, sv[e], sv[e + 1]);
+                m1 = max3f(m1, sv[e + 2], sv[e + 3]);
+              }
+            }
+            m_ref = fmaxf(m0, m1) * scale;
+          }
+          // (Always so.  As a condition it keeps the exponentials behind the
+          // maxima: in one piece, 16 trees of 64 nodes took 145 us against 142.)
+          const bool apart = nb > 0;
           float negm = m_ref == -INFINITY ? 0.f : -m_ref;
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
@@ -817,10 +886,10 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
               mq2 = max3f(mq2, sv[e + 4], sv[e + 5]);
               mq3 = max3f(mq3, sv[e + 6], sv[e + 7]);
             }
-            if (have_ref) probs<64>(sv, sc2, negm, hh ? pk_hi : pk_lo, lsum);
+            if (apart) probs<64>(sv, sc2, negm, hh ? pk_hi : pk_lo, lsum);
           }
           const float mx = fmaxf(fmaxf(mq0, mq1), fmaxf(mq2, mq3)) * scale;
-          const bool grow = !have_ref || mx > m_ref + kRescaleAbove;
+          const bool grow = mx > m_ref + kRescaleAbove;
           if (__any_sync(0xffffffffu, grow)) {
             if (li >= 2) {
               // O holds the group's blocks before: their P V must be done
@@ -950,38 +1019,12 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
           uint4 *dst = reinterpret_cast<uint4 *>(p.o + (static_cast<size_t>(tok) * p.Hq + head) * HD);
           // (partial rows in node order: tile 1's behind tile 0's)
           float *part = p.part + (static_cast<size_t>(max(slot, 0)) * 256 + t * NT * G + row) * (HD + 4);
-#pragma unroll 1
-          for (int cc = 0; cc < HD / 32; ++cc) {
-            float v[32];
-            if (joint) {
-              float x[32];
-              tmem_ld32x2(o_col + cc * 32, o_other + cc * 32, v, x);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] = wa * v[k] + wb * x[k];
-            } else {
-              tmem_ld32(o_col + cc * 32, v);
-            }
-            if (odd) {
-              float x[32];
-#pragma unroll
-              for (int k = 0; k < 32; ++k) x[k] = v[k];
-              add_odd<HD>(p, sg, see, tok, head, m_ref, cc * 32, x);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] = x[k];
-            }
-            if (valid && slot < 0) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                dst[cc * 4 + k] = make_uint4(pack_bf16x2(v[8 * k] * inv, v[8 * k + 1] * inv),
-                                             pack_bf16x2(v[8 * k + 2] * inv, v[8 * k + 3] * inv),
-                                             pack_bf16x2(v[8 * k + 4] * inv, v[8 * k + 5] * inv),
-                                             pack_bf16x2(v[8 * k + 6] * inv, v[8 * k + 7] * inv));
-            } else if (valid) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                reinterpret_cast<float4 *>(part + cc * 32)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-            }
-          }
+          const Rows<HD> out{&p, &sg, see, tok, head, o_col, o_other, joint, valid && slot < 0, valid && slot >= 0,
+                             wa, wb, inv, m_ref, dst, part};
+          if (__any_sync(0xffffffffu, odd))
+            write_odd<HD>(out, odd);
+          else
+            write_rows<HD, false>(out, false);
           if (valid && slot >= 0) *reinterpret_cast<float2 *>(part + HD) = make_float2(m_ref, l);
         }
         tc_fence_before();
