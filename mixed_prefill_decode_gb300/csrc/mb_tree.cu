@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
     // ------------------------------------------------ schedule, TMA producer
     // The whole warp: lane 0 waits and arms each stage, a block's 8 pages go
     // out as one copy per lane.  The K of a block goes out before the V of
-    // the block before it; the page ids of the next block are loaded a block
+    // the block before it, as a rule; the page ids of the next block are loaded a block
     // ahead, the next request's descriptor when its predecessor starts.
     const int G = p.G, NT = 128 / G;
     int32_t rec[5] = {0, 0, 0, 0, 0};
@@ -507,6 +507,11 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
                     (page * 2 + (is_v ? 1 : 0)) * p.Hkv + h);
       ++cnt;
       return true;
+    };
+    auto room = [&](bool is_v) {   // whether the next stage is free
+      const int ns = is_v ? C::NV : C::NK, cnt = is_v ? vcnt : kcnt;
+      uint64_t *empty = (is_v ? ct.v_empty : ct.k_empty) + cnt % ns;
+      return __all_sync(0xffffffffu, mbar_test_wait(smem_u32(empty), ((cnt / ns) & 1) ^ 1)) != 0;
     };
     while (ok && base < x1) {
       // the unit (hk, u) of request r, on the line from `base`
@@ -609,8 +614,13 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
         for (int j = j0 + 1; j < j1 && ok; ++j) {
           const int np = min(8, n_pages - 8 * j);
           const int after = j + 2 < j1 ? page_of(j + 2) : 0;
-          ok = send(false, np, cur, hk);
-          if (ok && pv_have) ok = send(true, pv_np, pv_page, pv_hk);
+          // With two tiles K's stages are held for long: a V that has one free
+          // does not wait for the K before it (16 trees of 64 nodes at 8,192
+          // keys 132 us against 141; with one tile it gained nothing).
+          const bool v_first = qt == 2 && pv_have && room(true) && !room(false);
+          if (v_first) ok = send(true, pv_np, pv_page, pv_hk);
+          if (ok) ok = send(false, np, cur, hk);
+          if (ok && pv_have && !v_first) ok = send(true, pv_np, pv_page, pv_hk);
           pv_np = np;
           pv_page = cur;
           pv_hk = hk;
