@@ -18,12 +18,13 @@
 // bound by HBM and larger ones by the tensor cores and the softmax.
 //
 // Measured (head_dim 128, G = 4, 8 KV heads): 16 trees of 8 nodes at 8,192
-// keys 95 us, 5.7 TB/s, 84 % of a copy's rate; 64 trees of 8 at 1,125 keys
-// 66 us, 4.6 TB/s (a CTA has 3.4 units of 9 blocks each, and every unit's end
+// keys 91 us, 5.9 TB/s, 87 % of a copy's rate; 64 trees of 8 at 1,125 keys
+// 59 us, 5.2 TB/s (a CTA has 3.4 units of 9 blocks each, and every unit's end
 // waits for its last softmax and product); 16 trees of 64 nodes at 8,192 keys
-// 154 us, 0.89 PFLOP/s of bf16, 46 % of a plain matrix product's rate, bound
-// by the softmax's exponentials and the turns of the two warp groups; one tree
-// of 6 nodes at 1,125 keys 12.5 us, two launches and the chain of one block.
+// 131.5 us, 1.05 PFLOP/s of bf16, 54 % of a plain matrix product's rate, bound
+// by the chain S, softmax, P V of the two warp groups (128 us with all keys in
+// L2); one tree of 6 nodes at 1,125 keys 12 us, two launches and the chain of
+// one block.
 //
 // Layout of the work.  The rows that share a KV head, (node, q-head of the
 // group), row = node G + g, are the M side of the products: 128 / G nodes make
@@ -460,10 +461,13 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
     if (threadIdx.x == 0) p.rec[cta * 8] = 0;
   } else if (warp == 0) {
     // ------------------------------------------------ schedule, TMA producer
-    // The whole warp: lane 0 waits and arms each stage, a block's 8 pages go
-    // out as one copy per lane.  The K of a block goes out before the V of
-    // the block before it, as a rule; the page ids of the next block are loaded a block
-    // ahead, the next request's descriptor when its predecessor starts.
+    // The whole warp: all lanes wait for each stage (waiting in one and telling
+    // the others took 229 us against 222 for 96 trees of 13 nodes at 1,024 to
+    // 8,192 keys), lane 0 arms it, a block's 8 pages go out as one copy per lane
+    // (by one elected lane in turn: 225 us unrolled, 287 rolled).  The K of a
+    // block goes out before the V of the block before it, as a rule; the page ids
+    // of the next block are loaded a block ahead, the next request's descriptor
+    // when its predecessor starts.
     const int G = p.G, NT = 128 / G;
     int32_t rec[5] = {0, 0, 0, 0, 0};
     int r = ct.start_req;
@@ -491,17 +495,13 @@ __global__ void __launch_bounds__(TreeCfg<HD>::THREADS, 1)
       const int st = cnt % ns;
       uint64_t *full = (is_v ? ct.v_full : ct.k_full) + st;
       uint64_t *empty = (is_v ? ct.v_empty : ct.k_empty) + st;
-      bool good = true;
-      if (lane == 0) {
-        good = mbar_wait(empty, ((cnt / ns) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer);
-        if (good) mbar_arrive_expect_tx(full, np * C::NH * 2048);
-      }
-      good = __shfl_sync(0xffffffffu, good, 0);
-      if (!good) return false;
+      if (!__all_sync(0xffffffffu, mbar_wait(empty, ((cnt / ns) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer))) return false;
       if (lane < np && (page < 0 || page >= p.num_pages)) {
         atomicExch(p.err, kErrBounds);
         page = 0;
       }
+      if (lane == 0) mbar_arrive_expect_tx(full, np * C::NH * 2048);
+      __syncwarp();
       if (lane < np)
         tma_load_5d((is_v ? sV : sK) + st * C::KV_BYTES + lane * C::PAGE_BYTES, &tmKV, full, 0, 0, 0, 0,
                     (page * 2 + (is_v ? 1 : 0)) * p.Hkv + h);
