@@ -597,3 +597,48 @@ def test_copy_pages(mb, hkv, hd, layers, pages, pairs):
     pools[:, dst] = pools[:, src]
     for i in range(layers):
         assert np.array_equal(from_dev(dev[i]), pools[i])
+
+
+def test_pages_beyond_32_bit_offsets(mb):
+    """The same pages at the far end of a pool of more than 2^32 bytes (and of
+    2^32 elements): the same attention, the same moves, the same copies."""
+    t = Trees([(300, 9), (5, 20), (1200, 3)], 8, 4, 128, 51).run(mb)
+    small = from_dev(t.o)
+    t.check(small)
+    far = 140000                                  # pages of 64 KB: 9.2 GB
+    big = torch.empty((far + t.P, 2, 8, 16, 128), dtype=torch.bfloat16, device="cuda")
+    assert big.numel() > 2 ** 32
+    big[far:].copy_(t.dpool)
+    o = to_dev(np.full((t.T, 8 * 4 * 128), SENT, np.uint16))
+    d = t.dev
+    bt = _i32(t.bt + far)
+    mb.mb_tree_attention(t.dq, big, o, far + t.P, 32, 8, 128, 3, t.T, d["qo"], d["kv"], d["bti"], bt, d["parent"], t.work,
+                         _stream())
+    mb.mb_device_status(None, _stream())
+    assert np.array_equal(from_dev(o), small)
+    n, path = np.array([3, 4, 2], np.int32), np.array([[0, 4, 8, -1], [0, 1, 7, 19], [0, 2, -1, -1]], np.int32)
+    new = torch.zeros(3, dtype=torch.int32, device="cuda")
+    mb.mb_kv_compact([big], far + t.P, 8, 128, 3, d["qo"], d["kv"], d["bti"], bt, _i32(n), _i32(path), 4, new, _stream())
+    want = t.pool.copy()
+    lens = OS.compact(want, t.qo, t.kv, t.bti, t.bt, [list(path[r, :n[r]]) for r in range(3)])
+    assert np.array_equal(from_dev(big[far:]), want) and np.array_equal(new.cpu().numpy(), lens)
+    mb.mb_kv_copy_pages([big], far + t.P, 8, 128, [far + 1, far + 2], [far + 4, 3], _stream())
+    mb.mb_device_status(None, _stream())
+    want[4] = want[1]
+    assert np.array_equal(from_dev(big[far:]), want) and np.array_equal(from_dev(big[3]), want[2])
+
+
+def test_tree_attention_on_another_stream_than_its_tensors(mb):
+    """A call on a side stream behind the tensors' own, and a batch of the most
+    nodes in every request at once with one that has none."""
+    t = Trees([(700, 128), (0, 0), (129, 128), (15, 128)], 1, 8, 64, 52, kind="star")
+    s = torch.cuda.Stream()
+    t.run(mb)
+    first = from_dev(t.o)
+    t.check(first)
+    t.o.view(torch.int16).fill_(SENT)
+    s.wait_stream(torch.cuda.current_stream())
+    t.call(mb, stream=s.cuda_stream)
+    torch.cuda.current_stream().wait_stream(s)
+    assert np.array_equal(from_dev(t.o), first)
+    mb.mb_device_status(None, s.cuda_stream)
