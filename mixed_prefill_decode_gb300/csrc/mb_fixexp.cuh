@@ -48,29 +48,21 @@ constexpr float kFixC1 = static_cast<float>(0.69314718055994531 / 32), kFixC2 = 
                 kFixC3 = static_cast<float>(0.055504108664821580 / 0x1p15),
                 kFixC4 = static_cast<float>(0.0096181291076284772 / 0x1p20);
 
-// 2^((l - m) k) in units of 2^-41, rounded to nearest; k = kh + kl >= 0, l <=
-// m.  0 for a NaN or -inf logit; l == m gives exactly 1 (m = +inf too).  (l - m
-// is a float; it is exact for bf16 logits unless |l| is below about 2^-16 m.)
-__host__ __device__ __forceinline__ int64_t fix_exp(float l, float m, float kh, float kl, const uint32_t *tab_fix,
-                                                    const float *tab_scaled) {
-  const float d_max = fminf(48.f / fmaxf(kh, 1e-30f), 3e38f);
-  const float d = fminf(m - l, d_max);   // (a NaN too: 2^-48 rounds to 0)
-  union {
-    float f;
-    int32_t i;
-  } t;
-  t.f = fmaf(d, 32.f * kh, kFixMagic);
-  const float f = fmaf(d, -32.f * kl, fmaf(d, -32.f * kh, t.f - kFixMagic));
+// 2^((l - m) k) to the same accuracy, before it is rounded to a multiple of
+// 2^-41; k = kh + kl >= 0, l <= m.  0 for a NaN or -inf logit and below 2^-960;
+// l == m gives exactly 1 (m = +inf too).  (l - m is a float; it is exact for
+// bf16 logits unless |l| is below about 2^-16 m.)
+__device__ __forceinline__ double fix_exp(float l, float m, float kh, float kl, const uint32_t *tab_fix,
+                                          const float *tab_scaled) {
+  if (l == m) return 1.0;
+  const float d = m - l;
+  if (!(d < fminf(960.f / fmaxf(kh, 1e-30f), 3e38f))) return 0.0;
+  const float t = fmaf(d, 32.f * kh, kFixMagic);
+  const float f = fmaf(d, -32.f * kl, fmaf(d, -32.f * kh, t - kFixMagic));
   const float g = f * fmaf(f, fmaf(f, fmaf(f, kFixC4, kFixC3), kFixC2), kFixC1);
-  const int32_t i = t.i & 31, s = (t.i - kFixMagicBits + 31) >> 5;   // the exponent: -s, and the table's
-#ifdef __CUDA_ARCH__
-  const int32_t add = __float2int_rn(tab_scaled[i] * g);
-#else
-  const int32_t add = static_cast<int32_t>(std::lrint(tab_scaled[i] * g));
-#endif
-  // units of 2^-42, then rounded to 2^-41
-  const uint64_t w = static_cast<uint64_t>(tab_fix[i] + static_cast<uint32_t>(add)) << 12;
-  return l == m ? int64_t{1} << kFixBits : static_cast<int64_t>(((w >> s) + 1) >> 1);
+  const int32_t n = __float_as_int(t), i = n & 31, s = (n - kFixMagicBits + 31) >> 5;   // the exponent: -s, and the table's
+  const uint32_t v = tab_fix[i] + static_cast<uint32_t>(__float2int_rn(tab_scaled[i] * g));   // 2^30 2^(s + ...)
+  return static_cast<double>(v) * __hiloint2double((1023 - 30 - s) << 20, 0);
 }
 
 }  // namespace mb

@@ -25,10 +25,13 @@
 // never reached are not read.  A thread keeps its part of the row in shared
 // memory (copied asynchronously) between the maximum, the sum and the draw.
 //
-// The tests compare in fp32 (the special-function unit's exponentials); the
-// draw at the end needs accurate weights (mb_fixexp.cuh), for one row per
-// request, two after a refusal with draft probabilities.  Their arithmetic is
-// what a full GPU spends most of its time on.
+// The tests compare in fp32 (the special-function unit's exponentials).  Where
+// that is too close to tell (so also where little is left of p: a child of p =
+// 0.9999 refused), after a refusal with draft probabilities and for the draw at
+// the end, the row is summed with accurate weights (mb_fixexp.cuh): as integers,
+// so that no decision depends on how many CTAs share the row.  That is one pass
+// over the last row as a rule, two after a refusal with draft probabilities.
+// Its arithmetic is what a full GPU spends most of its time on.
 //
 // Measured: one chain of 5 drafted tokens, vocabulary 128,256, with draft
 // probabilities, 27.5 us, some 3.5 us a node; 64 such 74 us, of which a node's
@@ -61,6 +64,13 @@ constexpr int kVerThreads = 256;   // (512 and two CTAs an SM: 64 chains 84 us a
 constexpr int kVerPerSm = 4;       // CTAs an SM holds
 constexpr int kVerWarps = kVerThreads / 32;
 constexpr int kMaxCluster = 16;
+// A test in fp32, u (z - refused) q < e, is repeated with accurate sums where
+// its sides are apart by less than this part of u z q + e.  The exponent of a
+// weight, at most 126 (m - l) k, is rounded three times: e is off by 126 ln 2 3
+// 2^-24 = 1.6e-5; in z and the refused ones' sum weights below 2^-45 count
+// nothing: 6e-6 each, and up to 80 and 127 additions in a row: 1.3e-5.  In all
+// 1.6e-5 e + 2.6e-5 u z q.
+constexpr float kNear = 0x1p-14f;
 constexpr int kMaxHeld = 17;   // vectors that a thread holds at most: a row of 2^19 logits over 16 CTAs
 struct VerifyParams {
   const __nv_bfloat16 *logits;
@@ -103,10 +113,14 @@ struct VerifySmem {
   int32_t token[kMaxTreeNodes];
   float u[kMaxTreeNodes], logit[kMaxTreeNodes], q[kMaxTreeNodes];   // of the node's token in its parent's rows
   int32_t gone[kMaxTreeNodes];   // refused tokens of the current node (no draft probabilities)
-  int32_t n_child, n_gone, state;
+  int64_t gone_w[kMaxTreeNodes]; // their weights, of those refused since the row was summed
+  int32_t n_child, n_gone, at, state;
   float kh, kl, az_hi, az_lo, u_final;
   int64_t pick;
 };
+
+// What a child's test comes to (also where a child's index may stand).
+enum : int { kRefused = -1, kNearBorder = -2, kPassed = -3 };
 
 // (at file scope, so that the functions below address it as shared memory)
 __shared__ VerifySmem sm;
@@ -136,13 +150,12 @@ struct WeightCtx {
   float d_max;             // m - l from which on it is 2^-48
   float az_hi, az_lo;      // less az q (both times 2^20)
   float q_small, q_any;    // q from which on az q is above 2^-11, above 1
-  int n_gone;
 };
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // Two weights as fix_exp computes them, in packed fp32: v 2^(11 - s) in units
-// of 2^-41.  D: m - l.
+// of 2^-41, to be rounded.  D: m - l.
 __device__ __forceinline__ void weight_pair(const WeightCtx &c, float2 D, uint32_t *v, int32_t *s) {
   D.x = fminf(D.x, c.d_max);   // (an infinity, a NaN: 2^-48, which rounds to 0)
   D.y = fminf(D.y, c.d_max);
@@ -194,12 +207,12 @@ __device__ __noinline__ int64_t token_weight(const WeightCtx &c, float l, bool p
   return max(w - (static_cast<int64_t>(hi) << 21) - lo, static_cast<int64_t>(0));
 }
 
-// Weight of vector v (8 tokens, at x; q: their draft probabilities), refused
-// tokens left out.  By all lanes of a warp (live: the lane has such a vector).
+// Weight of a vector (8 tokens, at x; q: their draft probabilities).  By all
+// lanes of a warp (live: the lane has such a vector).
 // The 8 weights are computed side by side and their sum in 32 bits a pair,
 // unless one of the warp's 256 is 2^-11 or more.
 template <bool PROBS>
-__device__ __forceinline__ int64_t vector_weight(const WeightCtx &c, const uint4 *x, int v, bool live, float4 qa, float4 qb) {
+__device__ __forceinline__ int64_t vector_weight(const WeightCtx &c, const uint4 *x, bool live, float4 qa, float4 qb) {
   const uint4 raw = live ? *x : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);   // -inf
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
   const float q[8] = {qa.x, qa.y, qa.z, qa.w, qb.x, qb.y, qb.z, qb.w};
@@ -245,11 +258,6 @@ __device__ __forceinline__ int64_t vector_weight(const WeightCtx &c, const uint4
       if (live) sum += token_weight(c, lg, PROBS, e < 4 ? (e < 2 ? (e ? qa.y : qa.x) : (e == 2 ? qa.z : qa.w)) : (e < 6 ? (e == 4 ? qb.x : qb.y) : (e == 6 ? qb.z : qb.w)));
     }
   }
-  if (!PROBS && live)
-    for (int g = 0; g < c.n_gone; ++g) {
-      const int tok = sm.gone[g];
-      if ((tok >> 3) == v) sum -= token_weight(c, __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(x)[tok & 7]), false, 0.f);
-    }
   return sum;
 }
 
@@ -277,7 +285,7 @@ __device__ __noinline__ int64_t weight_sums(Part &t, const WeightCtx &c, const f
     const int v = t.v0 + 32 * k;
     float4 na = qa, nb = qb;   // the next vector's draft probabilities, in flight meanwhile
     if (PROBS && k + 1 < t.nk) na = load_q(qrow, 2 * v + 64), nb = load_q(qrow, 2 * v + 65);
-    sum += vector_weight<PROBS>(c, t.x + k * kVerThreads, v, k < t.nk, qa, qb);
+    sum += vector_weight<PROBS>(c, t.x + k * kVerThreads, k < t.nk, qa, qb);
     qa = na, qb = nb;
   }
 #pragma unroll
@@ -452,6 +460,20 @@ __global__ void __launch_bounds__(kVerThreads, kVerPerSm) verify_kernel(const __
     m = top_m;
   };
 
+  // A test in fp32: a < e, `scale` the terms that a is the difference of.
+  auto fast_test = [](float a, float scale, float e) {
+    const bool near = fabsf(a - e) <= kNear * (scale + e) || (e == 0.f && a < 0x1p-100f);   // (e may have been flushed to 0)
+    return near ? kNearBorder : a < e ? kPassed : kRefused;
+  };
+  // Refused tokens (from the from-th on) leave the held row.
+  auto drop_gone = [&](int from, int to) {
+    for (int g = from; g < to; ++g) {
+      const int tok = sm.gone[g], at = (tok >> 3) - w0;   // the vector's place in the warp's part
+      if (at >= 0 && at < w1 - w0 && (at & 31) == lane)
+        reinterpret_cast<uint16_t *>(x + (at >> 5) * kVerThreads)[tok & 7] = 0xFF80u;   // -inf
+    }
+  };
+
   int cur = 0, len = 1;
 
   while (true) {
@@ -499,7 +521,6 @@ __global__ void __launch_bounds__(kVerThreads, kVerPerSm) verify_kernel(const __
     join(m, Z, top, C);
     part.parity ^= 1;
     if (m == -INFINITY) top = 0;   // no token has a chance: token 0
-    const __nv_bfloat16 *row = p.logits + (static_cast<size_t>(t0) + cur) * p.vocab;
     // warp 0's lanes hold 32 children's values, from `first` on
     int c_tok = -1;
     float c_u = 2.f, c_l = -INFINITY, c_q = 0.f;
@@ -517,77 +538,109 @@ __global__ void __launch_bounds__(kVerThreads, kVerPerSm) verify_kernel(const __
     // the children's tests, by warp 0: every CTA comes to the same answer
     int taken = -1;
     int64_t total = 0, before = 0;
-    int final_gone = 0;
+    int n_gone = 0, n_summed = 0;   // refused tokens (no draft probabilities): all, and those left out of `total`
     const float *qrow = nullptr;
-    WeightCtx ctx{m, 32.f * kh, 32.f * kl, d_max, 0.f, 0.f, 0.f, 0.f, 0};
+    WeightCtx ctx{m, 32.f * kh, 32.f * kl, d_max, 0.f, 0.f, 0.f, 0.f};
     bool have_sums = false;
     if (rank == 0 && threadIdx.x == 0) path[len - 1] = cur;
-    if (greedy || !p.probs) {
+    if (greedy) {
       if (warp == 0) {
-        int state = -1, n_gone = 0;
-        double gone = 0.0;
+        int state = -1;
         for (int first = 0; first < n_child && state < 0; first += 32) {
           if (first > 0) load_children(first);
-          if (greedy) {
-            const uint32_t hit = __ballot_sync(0xffffffffu, c_tok == top);
-            if (hit) state = sm.child[first + __ffs(hit) - 1];
-            continue;
-          }
-          const float c_e = c_l == m ? 1.f : fmaxf(ex2_approx((c_l - m) * kh), 0.f);
-          // (the lanes' first comparisons at once, while nothing is refused yet)
-          const uint32_t easy = __ballot_sync(0xffffffffu, c_u * Z < c_e);
-          for (int k = 0; k < min(32, n_child - first); ++k) {
-            const int tok = __shfl_sync(0xffffffffu, c_tok, k);
-            const float e = __shfl_sync(0xffffffffu, c_e, k), u = __shfl_sync(0xffffffffu, c_u, k);
-            bool dup = tok < 0;   // an invalid token, or one refused before: it has no chance
-            for (int g = lane; g < n_gone; g += 32) dup |= sm.gone[g] == tok;
-            if (__any_sync(0xffffffffu, dup)) continue;
-            const bool pass = n_gone == 0 ? (easy >> k) & 1u
-                                          : static_cast<double>(u) * (static_cast<double>(Z) - gone) < static_cast<double>(e);
-            if (m != -INFINITY && pass) {
-              state = sm.child[first + k];
-              break;
-            }
-            if (lane == 0) sm.gone[n_gone] = tok;
-            __syncwarp();
-            ++n_gone;
-            gone += static_cast<double>(e);
-          }
+          const uint32_t hit = __ballot_sync(0xffffffffu, c_tok == top);
+          if (hit) state = sm.child[first + __ffs(hit) - 1];
         }
-        if (lane == 0) sm.state = state, sm.n_gone = n_gone;
+        if (lane == 0) sm.state = state;
       }
       __syncthreads();
       taken = sm.state;
-      final_gone = sm.n_gone;
+    } else if (m != -INFINITY && !p.probs) {
+      // The row's fp32 sum serves as long as it can tell; then the weights of the
+      // tokens left are summed, and the ones refused after that leave the sum
+      // (warp 0's `left`).
+      int64_t left = 0;
+      float gone = 0.f;
+      for (int k = 0; k < n_child;) {
+        if (warp == 0) {
+          int state = kRefused;
+          for (; k < n_child; ++k) {
+            if (k % 32 == 0) load_children(k);
+            const int tok = __shfl_sync(0xffffffffu, c_tok, k % 32);
+            const float l = __shfl_sync(0xffffffffu, c_l, k % 32), u = __shfl_sync(0xffffffffu, c_u, k % 32);
+            bool dup = tok < 0;   // an invalid token, or one refused before: it has no chance
+            for (int g = lane; g < n_gone; g += 32) dup |= sm.gone[g] == tok;
+            if (__any_sync(0xffffffffu, dup)) continue;
+            int64_t w = 0;
+            if (have_sums) {
+              const double e = fix_exp(l, m, kh, kl, sm.tab_fix, sm.tab_scaled);
+              state = left > 0 && static_cast<double>(u) * (static_cast<double>(left) * 0x1p-41) < e ? kPassed : kRefused;
+              if (state != kRefused) break;
+              w = token_weight(ctx, l, false, 0.f);
+              left -= w;
+            } else {
+              const float e = l == m ? 1.f : fmaxf(ex2_approx((l - m) * kh), 0.f);
+              state = fast_test(u * (Z - gone), u * Z, e);
+              if (state != kRefused) break;
+              gone += e;
+            }
+            if (lane == 0) sm.gone[n_gone] = tok, sm.gone_w[n_gone] = w;
+            __syncwarp();
+            ++n_gone;
+          }
+          if (lane == 0) sm.state = state == kPassed ? sm.child[k] : state == kNearBorder ? kNearBorder : -1, sm.n_gone = n_gone, sm.at = k;
+        }
+        __syncthreads();
+        const int state = sm.state;
+        n_gone = sm.n_gone;
+        k = sm.at;
+        if (state != kNearBorder) {
+          taken = state;
+          break;
+        }
+        drop_gone(0, n_gone);
+        left = total = weight_sums<false>(part, ctx, nullptr, &before);
+        n_summed = n_gone;
+        have_sums = true;
+      }
     } else if (m != -INFINITY) {
       const float *q = p.probs + (static_cast<size_t>(t0) + cur) * p.vocab;
       // a, c and the row's sum z (c in units of z) are warp 0's
-      double a = 0.0, c = 1.0, zd = Z;
-      for (int k = 0; k < n_child; ++k) {
+      double a = 0.0, c = 1.0, zd = 0.0;
+      bool exact = false;   // z is known to full accuracy
+      for (int k = 0; k < n_child;) {
         if (warp == 0) {
           if (k > 0 && k % 32 == 0) load_children(k);
-          int pass = 0;
-          if (k == 0) {
-            pass = c_tok >= 0 && c_u * (c_q * Z) < (c_l == m ? 1.f : fmaxf(ex2_approx((c_l - m) * kh), 0.f));
-          } else if (lane == k % 32 && c_tok >= 0) {   // both sides times z
-            const double ex = static_cast<double>(fix_exp(c_l, m, kh, kl, sm.tab_fix, sm.tab_scaled)) * 0x1p-41;
-            const double qz = static_cast<double>(c_q) * zd;
-            pass = static_cast<double>(c_u) * c * qz < ex - a * qz;
+          if (lane == k % 32) {
+            int state = kRefused;
+            if (c_tok < 0) {
+            } else if (!exact) {
+              const float uqz = c_u * (c_q * Z);
+              state = fast_test(uqz, uqz, c_l == m ? 1.f : fmaxf(ex2_approx((c_l - m) * kh), 0.f));
+            } else {   // both sides times z
+              const double ex = fix_exp(c_l, m, kh, kl, sm.tab_fix, sm.tab_scaled);
+              const double qz = static_cast<double>(c_q) * zd;
+              if (static_cast<double>(c_u) * c * qz < ex - a * qz) state = kPassed;
+            }
+            sm.state = state;
           }
-          if (lane == k % 32) sm.state = pass;
         }
         __syncthreads();
-        if (sm.state != 0) {
+        const int state = sm.state;
+        if (state == kPassed) {
           taken = sm.child[k];
           break;
         }
-        if (!qrow) {   // the first refusal: the row's sum to full accuracy
+        if (!exact) {   // the first refusal, or too close: the row's sum to full accuracy
           for (int b = 32 * lane; b < 8 * (w1 - w0); b += 32 * 32)   // its draft probabilities go to L2 meanwhile
             asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 8 * w0 + b));
           const int64_t z = weight_sums<false>(part, ctx, nullptr, &before);
           if (warp == 0) zd = static_cast<double>(z) * 0x1p-41;
-          qrow = q;
+          exact = true;
         }
+        if (state == kNearBorder) continue;   // (the same child again)
+        ++k;
+        qrow = q;
         if (warp == 0) {
           a += c;
           const double az = a * zd;
@@ -619,14 +672,20 @@ __global__ void __launch_bounds__(kVerThreads, kVerPerSm) verify_kernel(const __
       break;
     }
     // none accepted: one token of what is left
-    if (!have_sums) {
-      ctx.n_gone = final_gone;
+    drop_gone(n_summed, n_gone);
+    if (have_sums) {
+      for (int g = n_summed; g < n_gone; ++g) total -= sm.gone_w[g];   // (those refused since)
+    } else {
       total = weight_sums<false>(part, ctx, nullptr, &before);
+      n_summed = n_gone;
     }
     if (total == 0) {    // the refusals left nothing: p itself
+      load_row(cur);
+      cp_async_wait();
       qrow = nullptr;
-      ctx = {m, 32.f * kh, 32.f * kl, d_max, 0.f, 0.f, 0.f, 0.f, 0};
+      ctx = {m, 32.f * kh, 32.f * kl, d_max, 0.f, 0.f, 0.f, 0.f};
       total = weight_sums<false>(part, ctx, nullptr, &before);
+      n_summed = n_gone;
     }
     if (threadIdx.x == 0) {
       const double uf = static_cast<double>(sm.u_final);
@@ -636,9 +695,14 @@ __global__ void __launch_bounds__(kVerThreads, kVerPerSm) verify_kernel(const __
     __syncthreads();
     const int64_t pick = sm.pick;
     // the first token whose cumulative weight is above pick
-    int64_t at = before;
+    int64_t at = before, own = sm.ws[warp];
     for (int w = 0; w < warp; ++w) at += sm.ws[w];
-    if (at <= pick && pick < at + sm.ws[warp]) {
+    for (int g = n_summed; g < n_gone; ++g) {
+      const int v = sm.gone[g] >> 3;
+      at -= v < w0 ? sm.gone_w[g] : 0;
+      own -= v >= w0 && v < w1 ? sm.gone_w[g] : 0;
+    }
+    if (at <= pick && pick < at + own) {
       // (this warp alone) its vectors' weights, in token order; then 8 lanes'
       // worth each, the vector, the token
       const int v0 = w0 + lane, nvec = w1 - w0;
@@ -649,9 +713,9 @@ __global__ void __launch_bounds__(kVerThreads, kVerPerSm) verify_kernel(const __
         if (qrow) {
           float4 qa = make_float4(0.f, 0.f, 0.f, 0.f), qb = qa;
           if (k < nk) qa = load_q(qrow, 2 * v), qb = load_q(qrow, 2 * v + 1);
-          sm.vec[32 * k + lane] = vector_weight<true>(ctx, x + k * kVerThreads, v, k < nk, qa, qb);
+          sm.vec[32 * k + lane] = vector_weight<true>(ctx, x + k * kVerThreads, k < nk, qa, qb);
         } else {
-          sm.vec[32 * k + lane] = vector_weight<false>(ctx, x + k * kVerThreads, v, k < nk, qa0, qa0);
+          sm.vec[32 * k + lane] = vector_weight<false>(ctx, x + k * kVerThreads, k < nk, qa0, qa0);
         }
       }
       __syncwarp();
@@ -670,13 +734,13 @@ __global__ void __launch_bounds__(kVerThreads, kVerPerSm) verify_kernel(const __
       if (mine)
         while (pick >= run + sm.vec[i]) run += sm.vec[i++];
       const int from = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
-      const int first = 8 * (w0 + __shfl_sync(0xffffffffu, i, from));
+      const int vec = min(__shfl_sync(0xffffffffu, i, from), nvec - 1);
       run = __shfl_sync(0xffffffffu, run, from);
       // its 8 tokens, one a lane
-      const int tok = first + (lane & 7);
-      bool out = false;
-      for (int g = 0; g < ctx.n_gone; ++g) out |= sm.gone[g] == tok;
-      const int64_t w = out ? 0 : token_weight(ctx, __bfloat162float(row[tok]), qrow != nullptr, qrow ? qrow[tok] : 0.f);
+      const int tok = 8 * (w0 + vec) + (lane & 7);
+      const uint4 *hv = held + (vec >> 5) * kVerThreads + 32 * warp + (vec & 31);
+      const int64_t w = token_weight(ctx, __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(hv)[lane & 7]), qrow != nullptr,
+                                     qrow ? qrow[tok] : 0.f);
       inc = w;
 #pragma unroll
       for (int off = 1; off < 8; off <<= 1) {
