@@ -415,10 +415,12 @@ int64_t mb_tree_attention_workspace_bytes(void);
  * the argmax.  This keeps the target's distribution: Leviathan et al. 2023,
  * Miao et al. 2024 for trees.  A NaN or -inf logit has probability 0; a row of
  * nothing else gives token 0.  What a test or the draw decides by is a sum of
- * weights, each good to 2^-29 and summed as an integer multiple of 2^-41 of the
- * largest (tests that fp32 settles aside), so it is off by 2^-29 and vocab 2^-42
- * times the largest weight, and does not depend on how the row is split: the
- * same request gets the same answer in any batch.
+ * weights, each good to 2^-29 and summed as an integer multiple of 2^-41 of a
+ * reference weight (tests that fp32 settles aside), so it is off by 2^-29 and
+ * vocab 2^-42 references, and does not depend on how the row is split: the same
+ * request gets the same answer in any batch.  The reference is the row's largest
+ * weight; without draft probabilities it is never more than what the refusals
+ * left of the row.
  *   logits       device bf16 [T][vocab], vocab % 8 == 0 and at most 2^19, 16-byte aligned
  *   tokens       device int32 [T], the node's token (that of node 0 is not read);
  *                one outside [0, vocab) is refused and records MB_EDEVICE

@@ -24,7 +24,7 @@
 
 namespace mb {
 
-constexpr int kFixBits = 41;
+constexpr int64_t kFixOne = int64_t{1} << 41;   // a weight of 1
 
 struct FixExpTable {
   uint32_t fix[32];   // 2^(-i/32 + (i > 0)), in [1, 2), in units of 2^-30

@@ -114,7 +114,7 @@ struct VerifySmem {
   float u[kMaxTreeNodes], logit[kMaxTreeNodes], q[kMaxTreeNodes];   // of the node's token in its parent's rows
   int32_t gone[kMaxTreeNodes];   // refused tokens of the current node (no draft probabilities)
   int64_t gone_w[kMaxTreeNodes]; // their weights, of those refused since the row was summed
-  int32_t n_child, n_gone, at, state;
+  int32_t n_child, n_gone, at, state, low;
   float kh, kl, az_hi, az_lo, u_final;
   int64_t pick;
 };
@@ -306,6 +306,29 @@ __device__ __noinline__ int64_t weight_sums(Part &t, const WeightCtx &c, const f
   }
   t.parity ^= 1;
   return total;
+}
+
+// The largest logit that the cluster's CTAs hold.  All threads.
+__device__ __noinline__ float row_max(Part &t) {
+  __syncthreads();   // sm.wm has been read
+  uint32_t pm = 0xFF80FF80u;   // -inf (a NaN is passed over)
+  for (int k = 0; k < t.nk; ++k) {
+    const uint4 v = t.x[k * kVerThreads];
+    pm = max_bf16x2(max_bf16x2(pm, v.x), max_bf16x2(v.y, max_bf16x2(v.z, v.w)));
+  }
+  float m = fmaxf(bf16lo(pm), bf16hi(pm));
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  if ((threadIdx.x & 31) == 0) sm.wm[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kVerWarps; ++w) m = fmaxf(m, sm.wm[w]);
+  if (t.C == 1) return m;
+  if (threadIdx.x < t.C) st_cluster32(&sm.ex.m[t.parity][t.rank], threadIdx.x, __float_as_uint(m));
+  cluster_sync();
+  for (int k = 0; k < t.C; ++k) m = fmaxf(m, sm.ex.m[t.parity][k]);
+  t.parity ^= 1;
+  return m;
 }
 
 __global__ void __launch_bounds__(kVerThreads, kVerPerSm) verify_kernel(const __grid_constant__ VerifyParams p) {
@@ -539,6 +562,7 @@ __global__ void __launch_bounds__(kVerThreads, kVerPerSm) verify_kernel(const __
     int taken = -1;
     int64_t total = 0, before = 0;
     int n_gone = 0, n_summed = 0;   // refused tokens (no draft probabilities): all, and those left out of `total`
+    bool low = false;               // what is left weighs less than the reference
     const float *qrow = nullptr;
     WeightCtx ctx{m, 32.f * kh, 32.f * kl, d_max, 0.f, 0.f, 0.f, 0.f};
     bool have_sums = false;
@@ -558,7 +582,10 @@ __global__ void __launch_bounds__(kVerThreads, kVerPerSm) verify_kernel(const __
     } else if (m != -INFINITY && !p.probs) {
       // The row's fp32 sum serves as long as it can tell; then the weights of the
       // tokens left are summed, and the ones refused after that leave the sum
-      // (warp 0's `left`).
+      // (warp 0's `left`).  The weights' reference is the row's maximum, or, when
+      // that was refused and less than its weight is left, the maximum of what is
+      // left: the sum is at least one reference, so the roundings to 2^-41 of it
+      // are as small a part of the sum as in a whole row.
       int64_t left = 0;
       float gone = 0.f;
       for (int k = 0; k < n_child;) {
@@ -573,7 +600,9 @@ __global__ void __launch_bounds__(kVerThreads, kVerPerSm) verify_kernel(const __
             if (__any_sync(0xffffffffu, dup)) continue;
             int64_t w = 0;
             if (have_sums) {
-              const double e = fix_exp(l, m, kh, kl, sm.tab_fix, sm.tab_scaled);
+              if (left > 0 && left < kFixOne) state = kNearBorder;
+              if (state != kRefused) break;
+              const double e = fix_exp(l, ctx.m, kh, kl, sm.tab_fix, sm.tab_scaled);
               state = left > 0 && static_cast<double>(u) * (static_cast<double>(left) * 0x1p-41) < e ? kPassed : kRefused;
               if (state != kRefused) break;
               w = token_weight(ctx, l, false, 0.f);
@@ -588,18 +617,25 @@ __global__ void __launch_bounds__(kVerThreads, kVerPerSm) verify_kernel(const __
             __syncwarp();
             ++n_gone;
           }
-          if (lane == 0) sm.state = state == kPassed ? sm.child[k] : state == kNearBorder ? kNearBorder : -1, sm.n_gone = n_gone, sm.at = k;
+          if (lane == 0) {
+            sm.state = state == kPassed ? sm.child[k] : state == kNearBorder ? kNearBorder : -1;
+            sm.n_gone = n_gone;
+            sm.at = k;
+            sm.low = n_gone > 0 && (have_sums ? left < kFixOne : Z - gone < 0.99f);
+          }
         }
         __syncthreads();
         const int state = sm.state;
         n_gone = sm.n_gone;
+        low = sm.low;
         k = sm.at;
         if (state != kNearBorder) {
           taken = state;
           break;
         }
-        drop_gone(0, n_gone);
-        left = total = weight_sums<false>(part, ctx, nullptr, &before);
+        drop_gone(n_summed, n_gone);
+        if (low) ctx.m = row_max(part);
+        left = total = ctx.m == -INFINITY ? 0 : weight_sums<false>(part, ctx, nullptr, &before);
         n_summed = n_gone;
         have_sums = true;
       }
@@ -673,10 +709,11 @@ __global__ void __launch_bounds__(kVerThreads, kVerPerSm) verify_kernel(const __
     }
     // none accepted: one token of what is left
     drop_gone(n_summed, n_gone);
-    if (have_sums) {
+    if (have_sums && !low) {
       for (int g = n_summed; g < n_gone; ++g) total -= sm.gone_w[g];   // (those refused since)
     } else {
-      total = weight_sums<false>(part, ctx, nullptr, &before);
+      if (low) ctx.m = row_max(part);
+      total = ctx.m == -INFINITY ? 0 : weight_sums<false>(part, ctx, nullptr, &before);
       n_summed = n_gone;
     }
     if (total == 0) {    // the refusals left nothing: p itself

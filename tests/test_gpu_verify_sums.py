@@ -8,7 +8,9 @@ p' apart by more than
   2^-28 + V 2^-42 / S     relative to p'
 (2^-29 of the child's weight, the sum's error) the decision is the exact one,
 and it is the same whatever the batch, hence the number of CTAs, the row is
-summed in.  The logits here are 0 or at least 2^-16 of a row's largest, so that
+summed in.  Without draft probabilities the reference is the largest weight or
+the largest left, whichever gives S >= 1; a border of the draw, a partial sum
+over S, is off by at most 2 (2^-29 + V 2^-42).  The logits here are 0 or at least 2^-16 of a row's largest, so that
 l - m is exact."""
 
 import numpy as np
@@ -154,3 +156,57 @@ def test_a_decision_does_not_depend_on_the_batch(mb, mode):
         assert np.array_equal(a[:70], b)
     for k in range(3):
         assert np.array_equal(full[k][:24], np.concatenate([x[k] for x in alone]))
+
+
+@pytest.mark.parametrize("vocab", [4096, 128256])
+def test_a_child_behind_one_that_took_nearly_everything(mb, vocab):
+    """What is left is measured by itself, however little it is."""
+    _check_second_child(mb, _after_refusal([1e-3, 1e-5, 1e-6, 4e-7], 12, vocab, 9 + vocab), lambda left: 2.0 ** -28 + vocab * 2.0 ** -42)
+
+
+@pytest.mark.parametrize("children", [1, 3])
+@pytest.mark.parametrize("vocab", [4096, 128256])
+def test_the_draw_behind_a_refused_child_that_took_nearly_everything(mb, vocab, children):
+    """u_final a tenth of a token's width inside it, from either side.  Three
+    children: the others hold 0.9 of what the first left and are refused too."""
+    lefts, per = [0.6, 1e-2, 1e-4, 1e-5, 1e-6, 4e-7], 10
+    s = Stars(len(lefts) * per, vocab, children, 77 + vocab + children)
+    s.u[:, 2:] = 1.0 - 2.0 ** -24
+    for r in range(s.n):
+        T, kids, scale = np.float64(s.temp[r]), s.tokens[r, 1:], 1.0
+        s.root[r, kids] = -np.inf
+        for k, out in zip(kids[::-1], ([0.3, 0.9] if children > 1 else []) + [1 - lefts[r // per]]):
+            rest = T * np.log(np.sum(np.exp(s.root[r] / T)))
+            s.root[r, k] = rest + T * np.log(out / (1 - out))
+    lg, want = s.settle(), []
+    tol = 2.0 ** -28 + vocab * 2.0 ** -41
+    for r in range(s.n):
+        w = s.weights(r, lg)
+        w[s.tokens[r, 1:]] = 0.0
+        cum = np.concatenate([[0.0], np.cumsum(w / w.sum())])
+        width = np.diff(cum)
+        t = s.rng.choice(np.nonzero(width > 60 * tol)[0])
+        s.u_final[r] = np.float32(cum[t] + (0.1 if r % 2 else 0.9) * width[t])
+        assert cum[t] + 3 * tol < s.u_final[r] < cum[t + 1] - 3 * tol
+        want.append(t)
+    count, path, nxt = s.run(mb, np.arange(s.n))
+    assert np.all(count == 1) and np.array_equal(nxt, want)
+
+
+def test_nothing_or_one_token_is_left(mb):
+    """A second child that is all that is left is certain, whatever u; u = 1 (not
+    below 1, as it should be) refuses it too, and the draw is from p itself."""
+    s = Stars(40, 64, 2, 5)
+    s.root[:] = -np.inf
+    for r in range(s.n):
+        s.root[r, s.tokens[r, 1:]] = [3.0, 1.0]
+    s.bits = W.f32_to_bf16_bits(s.root.astype(np.float32))
+    count, path, nxt = s.run(mb, np.arange(s.n))
+    assert np.all(count == 2) and np.all(path[:, 1] == 2)
+    s.u[:] = 1.0
+    count, path, nxt = s.run(mb, np.arange(s.n))
+    lg = f64(s.bits)
+    for r in range(s.n):
+        w = s.weights(r, lg)
+        assert abs(s.u_final[r] - w[:s.tokens[r, 1:].max()].sum() / w.sum()) > 1e-6
+        assert count[r] == 1 and nxt[r] == np.argmax(np.cumsum(w / w.sum()) > s.u_final[r])
