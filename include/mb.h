@@ -423,7 +423,8 @@ int64_t mb_tree_attention_workspace_bytes(void);
  * left of the row.
  *   logits       device bf16 [T][vocab], vocab % 8 == 0 and at most 2^19, 16-byte aligned
  *   tokens       device int32 [T], the node's token (that of node 0 is not read);
- *                one outside [0, vocab) is refused and records MB_EDEVICE
+ *                a child whose token is outside [0, vocab) is passed over, as if it
+ *                were not there, and records MB_EDEVICE
  *   draft_probs  device fp32 [T][vocab], 16-byte aligned, or NULL
  *   temperature  device fp32 [num_reqs], >= 0 (0: greedy), or NULL: all greedy
  *   u_accept     device fp32 [T] in [0, 1) (that of node 0 is not read); u_final device fp32

@@ -120,7 +120,7 @@ struct VerifySmem {
 };
 
 // What a child's test comes to (also where a child's index may stand).
-enum : int { kRefused = -1, kNearBorder = -2, kPassed = -3 };
+enum : int { kRefused = -1, kNearBorder = -2, kPassed = -3, kNoToken = -4 };
 
 // (at file scope, so that the functions below address it as shared memory)
 __shared__ VerifySmem sm;
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(kVerThreads, kVerPerSm) verify_kernel(const __
             if (k % 32 == 0) load_children(k);
             const int tok = __shfl_sync(0xffffffffu, c_tok, k % 32);
             const float l = __shfl_sync(0xffffffffu, c_l, k % 32), u = __shfl_sync(0xffffffffu, c_u, k % 32);
-            bool dup = tok < 0;   // an invalid token, or one refused before: it has no chance
+            bool dup = tok < 0;   // an invalid token: passed over; one refused before: it has no chance
             for (int g = lane; g < n_gone; g += 32) dup |= sm.gone[g] == tok;
             if (__any_sync(0xffffffffu, dup)) continue;
             int64_t w = 0;
@@ -650,6 +650,7 @@ __global__ void __launch_bounds__(kVerThreads, kVerPerSm) verify_kernel(const __
           if (lane == k % 32) {
             int state = kRefused;
             if (c_tok < 0) {
+              state = kNoToken;   // (it was not drawn from q: p stays as it is)
             } else if (!exact) {
               const float uqz = c_u * (c_q * Z);
               state = fast_test(uqz, uqz, c_l == m ? 1.f : fmaxf(ex2_approx((c_l - m) * kh), 0.f));
@@ -666,6 +667,11 @@ __global__ void __launch_bounds__(kVerThreads, kVerPerSm) verify_kernel(const __
         if (state == kPassed) {
           taken = sm.child[k];
           break;
+        }
+        if (state == kNoToken) {
+          ++k;
+          __syncthreads();   // sm.state has been read
+          continue;
         }
         if (!exact) {   // the first refusal, or too close: the row's sum to full accuracy
           for (int b = 32 * lane; b < 8 * (w1 - w0); b += 32 * 32)   // its draft probabilities go to L2 meanwhile

@@ -1,0 +1,67 @@
+"""Calls of the drafted-token operators at the edge of what they are given."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import spec as OS
+from gpu_util import f64
+from test_gpu_verify_sums import Stars
+
+pytestmark = pytest.mark.gpu
+
+
+def _stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _with_drafts(n, vocab, children, seed):
+    """Requests whose children are drawn from draft probabilities near the target's."""
+    s = Stars(n, vocab, children, seed)
+    lg = s.settle()
+    s.probs = np.empty((n, vocab), np.float32)
+    for r in range(n):
+        q = s.weights(r, lg) * np.exp(0.7 * s.rng.standard_normal(vocab))
+        s.probs[r] = q / q.sum()
+        q = s.probs[r].astype(np.float64)
+        s.tokens[r, 1:] = s.rng.choice(vocab, size=children, p=q / q.sum())
+    s.u = s.rng.random(s.u.shape, dtype=np.float32)
+    return s
+
+
+def _expect(s, max_path=4):
+    """The oracle's answers; a case at a border is not one to ask about."""
+    lg, out = f64(s.bits), []
+    for r in range(s.n):
+        rows = np.zeros((s.m, s.V))
+        rows[0] = lg[r]
+        q = None
+        if s.probs is not None:
+            q = np.zeros((s.m, s.V))
+            q[0] = s.probs[r]
+        path, nxt, (test, last) = OS.verify(rows, s.tokens[r], q, [-1] + [0] * (s.m - 1), float(s.temp[r]),
+                                            s.u[r].astype(np.float64), float(s.u_final[r]), max_path)
+        assert test > 1e-6 and last > 1e-7
+        out.append((len(path), path + [-1] * (max_path - len(path)), nxt))
+    return out
+
+
+def _same(got, want):
+    for r, (n, path, nxt) in enumerate(want):
+        assert (got[0][r], list(got[1][r]), got[2][r]) == (n, path, nxt), r
+
+
+@pytest.mark.parametrize("drafts", [False, True])
+@pytest.mark.parametrize("token", [-1, 4096, 2 ** 31 - 1, -2 ** 31])
+def test_a_child_with_no_token_of_the_vocabulary_is_passed_over(mb, drafts, token):
+    """Whichever child it is, the others and the draw are as without it."""
+    s = _with_drafts(48, 4096, 3, 11)
+    if not drafts:
+        s.probs = None
+    for r in range(s.n):
+        s.tokens[r, 1 + r % 3] = token
+    got = s.run(mb, np.arange(s.n), check=False)
+    with pytest.raises(mb.MbError) as e:
+        mb.mb_device_status(None, _stream())
+    assert e.value.status == mb.MB_EDEVICE
+    _same(got, _expect(s))
