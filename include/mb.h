@@ -425,7 +425,8 @@ int64_t mb_tree_attention_workspace_bytes(void);
  *   tokens       device int32 [T], the node's token (that of node 0 is not read);
  *                a child whose token is outside [0, vocab) is passed over, as if it
  *                were not there, and records MB_EDEVICE
- *   draft_probs  device fp32 [T][vocab], 16-byte aligned, or NULL
+ *   draft_probs  device fp32 [T][vocab], 16-byte aligned, or NULL; one below 0 counts
+ *                as 0, a NaN as more than any p (its token is refused and not drawn)
  *   temperature  device fp32 [num_reqs], >= 0 (0: greedy), or NULL: all greedy
  *   u_accept     device fp32 [T] in [0, 1) (that of node 0 is not read); u_final device fp32
  *                [num_reqs] in [0, 1); both may be NULL if temperature is

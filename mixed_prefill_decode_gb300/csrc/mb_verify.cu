@@ -182,10 +182,11 @@ __device__ __forceinline__ int64_t large_weight(uint32_t v, int32_t s) {
 }
 
 // az q in units of 2^-41, as hi 2^21 + lo.  A q above `top` (a NaN too) counts
-// as that: az q is then more than any weight beside it.  (In packed fp32, two
+// as that: az q is then more than any weight beside it.  One below 0 counts as
+// 0: no weight grows, and the sums stay within 64 bits.  (In packed fp32, two
 // tokens at a time, 64 chains took 77.6 us against 76.3.)
 __device__ __forceinline__ void fixed_q(const WeightCtx &c, float q, float top, int32_t &hi, int32_t &lo) {
-  q = fminf(q, top);
+  q = fmaxf(fminf(q, top), 0.f);
   const float x = q * c.az_hi, l = fmaf(q, c.az_lo, fmaf(q, c.az_hi, -x));
   const float a = x + kFixMagic;
   const float b = fmaf((x - (a - kFixMagic)) + l, 0x1p21f, kFixMagic);
@@ -403,7 +404,8 @@ __global__ void __launch_bounds__(kVerThreads, kVerPerSm) verify_kernel(const __
     sm.u[i] = u;
     const size_t at = (static_cast<size_t>(t0) + max(up, 0)) * p.vocab + (bad_tok ? 0 : tok);
     sm.logit[i] = greedy ? 0.f : __bfloat162float(p.logits[at]);
-    sm.q[i] = greedy || !p.probs ? 0.f : p.probs[at];
+    const float q = greedy || !p.probs ? 0.f : p.probs[at];
+    sm.q[i] = q < 0.f ? 0.f : q;   // (a NaN stays one: the child is refused)
   }
   __syncthreads();
 

@@ -65,3 +65,20 @@ def test_a_child_with_no_token_of_the_vocabulary_is_passed_over(mb, drafts, toke
         mb.mb_device_status(None, _stream())
     assert e.value.status == mb.MB_EDEVICE
     _same(got, _expect(s))
+
+
+def test_negative_draft_probabilities_count_as_zero(mb):
+    """Small ones, and ones that are no probabilities at all, the children's own among them."""
+    s = _with_drafts(40, 4096, 2, 12)
+    s.probs[0, 0] = 0.25   # (of request 0 only: so that a sum above 1 is among them)
+    at = s.rng.random(s.probs.shape) < 0.3
+    for r in range(s.n):
+        at[r, s.tokens[r, 1 + r % 2]] = r % 4 == 0
+    clean = np.where(at, np.float32(0.0), s.probs)
+    bad = np.array([-1e-6, -0.3, -1.0, -3e38, -np.inf], np.float32)[s.rng.integers(0, 5, size=s.probs.shape)]
+    s.probs = clean
+    want = s.run(mb, np.arange(s.n))
+    _same(want, _expect(s))
+    s.probs = np.where(at, bad, clean)
+    for a, b in zip(s.run(mb, np.arange(s.n)), want):
+        assert np.array_equal(a, b)
