@@ -367,7 +367,8 @@ mb_status mb_embed(const void *table, int32_t vocab, int32_t d, const int32_t *i
  * after which kv_len counts the accepted nodes and the next token is node 0
  * of the next step.  Descriptor arrays are DEVICE int32 here, as their
  * contents come from the draft and from mb_verify_tree; what a host check
- * cannot see is checked by the kernels (mb_device_status with layer NULL). */
+ * cannot see is checked by the kernels (mb_device_status with layer NULL).  No
+ * output of these calls may overlap another output or an input (MB_EINVAL). */
 #define MB_MAX_TREE_NODES 128
 
 /* Attention of drafted nodes over the paged cache.  Request r owns rows
@@ -378,7 +379,7 @@ mb_status mb_embed(const void *table, int32_t vocab, int32_t d, const int32_t *i
  * A request has at most 2^24 keys.
  *   q     device bf16 [T][Hq][hd] (rotated), 16-byte aligned
  *   pool  device bf16 [num_pages][2][Hkv][16][hd] (mb_kv_layout's), 128-byte aligned
- *   o     device bf16 [T][Hq hd], 16-byte aligned, must not alias q
+ *   o     device bf16 [T][Hq hd], 16-byte aligned
  * head_dim 64 or 128, Hq / Hkv at most 8.  workspace: device memory of
  * mb_tree_attention_workspace_bytes() bytes, 256-byte aligned, needs no
  * initialisation; a call owns it until it completes (calls on unordered
@@ -447,8 +448,8 @@ mb_status mb_verify_tree(const void *logits, int32_t vocab, const int32_t *token
  * and new_kv_len[r] = c + n_accepted[r].  The slots behind keep what they
  * held.  pools: HOST array of the pools' device bases (mb_kv_layout), each
  * [num_pages][2][n_kv_heads][16][head_dim] bf16, 16-byte aligned, distinct;
- * the other arrays device int32 as in mb_verify_tree and mb_tree_attention;
- * new_kv_len must not alias kv_len.  head_dim % 8 == 0.  A request whose path
+ * the other arrays device int32 as in mb_verify_tree and mb_tree_attention.
+ * head_dim % 8 == 0.  A request whose path
  * is not ascending within its nodes, or whose table or pages break the rules,
  * records MB_EDEVICE and keeps its cache; its new_kv_len is not written.
  * Errors: MB_EINVAL, MB_EUNSUPPORTED, MB_ECUDA. */

@@ -10,6 +10,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <iterator>
 #include <mutex>
 #include <new>
@@ -1213,6 +1214,30 @@ mb_status mb_embed(const void *table, int32_t vocab, int32_t d, const int32_t *i
 }
 
 // ------------------------------------------------------- drafted tokens
+// Memory that a call reads or writes (no bytes: an argument left out).
+struct Range {
+  const char *name;
+  const void *at;
+  int64_t bytes;
+};
+
+// MB_EINVAL if an output lies over an input or over another output: requests
+// and pools run side by side, so one would read what another has written.
+static mb_status check_apart(const char *who, std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
+  auto over = [](const Range &a, const Range &b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+    return a.at && b.at && a.bytes > 0 && b.bytes > 0 &&
+           (x < y ? y - x < static_cast<uint64_t>(a.bytes) : x - y < static_cast<uint64_t>(b.bytes));
+  };
+  for (auto o = outs.begin(); o != outs.end(); ++o) {
+    for (auto b = outs.begin(); b != o; ++b)
+      if (over(*o, *b)) return fail(MB_EINVAL, "%s: %s and %s overlap", who, b->name, o->name);
+    for (const Range &in : ins)
+      if (over(*o, in)) return fail(MB_EINVAL, "%s: %s overlaps %s", who, o->name, in.name);
+  }
+  return MB_OK;
+}
+
 int64_t mb_tree_attention_workspace_bytes(void) { return static_cast<int64_t>(mb::tree_workspace_bytes()); }
 
 mb_status mb_tree_attention(const void *q, const void *pool, void *o, int32_t num_pages, int32_t n_q_heads,
@@ -1230,15 +1255,25 @@ mb_status mb_tree_attention(const void *q, const void *pool, void *o, int32_t nu
     return fail(MB_EUNSUPPORTED, "mb_tree_attention: GQA group %d > 8", n_q_heads / n_kv_heads);
   if (static_cast<int64_t>(num_pages) * 2 * n_kv_heads > INT32_MAX)
     return fail(MB_EUNSUPPORTED, "mb_tree_attention: pool too large for 32-bit TMA coordinates");
-  if (q == o) return fail(MB_EINVAL, "mb_tree_attention: o must not alias q");
   if (reinterpret_cast<uintptr_t>(q) % 16 || reinterpret_cast<uintptr_t>(o) % 16)
     return fail(MB_EINVAL, "mb_tree_attention: q and o must be 16-byte aligned");
   if (reinterpret_cast<uintptr_t>(pool) % 128) return fail(MB_EINVAL, "mb_tree_attention: pool must be 128-byte aligned");
   if (reinterpret_cast<uintptr_t>(workspace) % 256)
     return fail(MB_EINVAL, "mb_tree_attention: workspace must be 256-byte aligned");
   if (num_reqs == 0 || T == 0) return MB_OK;
+  const int64_t reqs = 4ll * num_reqs, rows = 2ll * T * n_q_heads * head_dim;
+  mb_status st = check_apart("mb_tree_attention",
+                             {{"o", o, rows}, {"workspace", workspace, mb_tree_attention_workspace_bytes()}},
+                             {{"q", q, rows},
+                              {"pool", pool, 64ll * num_pages * n_kv_heads * head_dim},
+                              {"qo_indptr", qo_indptr, reqs + 4},
+                              {"kv_len", kv_len, reqs},
+                              {"bt_indptr", bt_indptr, reqs + 4},
+                              {"bt", bt, 4},
+                              {"parent", parent, 4ll * T}});
+  if (st != MB_OK) return st;
   mb::DeviceCtx *ctx = nullptr;
-  mb_status st = mb::device_ctx(&ctx);
+  st = mb::device_ctx(&ctx);
   if (st != MB_OK) return st;
   const mb::TreeArgs a = {q,      pool,     o, qo_indptr, kv_len,     bt_indptr, bt,        parent,
                           num_reqs, T,      n_q_heads, n_kv_heads, head_dim,  num_pages, workspace, ctx->err};
@@ -1263,8 +1298,20 @@ mb_status mb_verify_tree(const void *logits, int32_t vocab, const int32_t *token
   if (reinterpret_cast<uintptr_t>(logits) % 16 || reinterpret_cast<uintptr_t>(draft_probs) % 16)
     return fail(MB_EINVAL, "mb_verify_tree: logits and draft_probs must be 16-byte aligned");
   if (num_reqs == 0) return MB_OK;
+  const int64_t reqs = 4ll * num_reqs, words = 4ll * T, row = 2ll * T * vocab;
+  mb_status st = check_apart("mb_verify_tree",
+                             {{"n_accepted", n_accepted, reqs}, {"path", path, reqs * max_path}, {"next_token", next_token, reqs}},
+                             {{"logits", logits, row},
+                              {"tokens", tokens, words},
+                              {"draft_probs", draft_probs, 2 * row},
+                              {"qo_indptr", qo_indptr, reqs + 4},
+                              {"parent", parent, words},
+                              {"temperature", temperature, reqs},
+                              {"u_accept", u_accept, words},
+                              {"u_final", u_final, reqs}});
+  if (st != MB_OK) return st;
   mb::DeviceCtx *ctx = nullptr;
-  mb_status st = mb::device_ctx(&ctx);
+  st = mb::device_ctx(&ctx);
   if (st != MB_OK) return st;
   const mb::VerifyArgs a = {logits,  tokens,     draft_probs, qo_indptr,  parent, temperature, u_accept, u_final,
                             n_accepted, path, next_token,  num_reqs, T,      vocab,       max_path, ctx->err};
@@ -1297,7 +1344,15 @@ mb_status mb_kv_compact(void *const *pools, int32_t n_pools, int32_t num_pages, 
   if (!qo_indptr || !kv_len || !bt_indptr || !bt || !n_accepted || !path || !new_kv_len)
     return fail(MB_EINVAL, "mb_kv_compact: null argument");
   if (num_reqs < 0 || max_path < 1) return fail(MB_EINVAL, "mb_kv_compact: num_reqs < 0 or max_path < 1");
-  if (new_kv_len == kv_len) return fail(MB_EINVAL, "mb_kv_compact: new_kv_len must not alias kv_len");
+  const int64_t reqs = 4ll * num_reqs;
+  st = check_apart("mb_kv_compact", {{"new_kv_len", new_kv_len, reqs}},
+                   {{"kv_len", kv_len, reqs},
+                    {"qo_indptr", qo_indptr, reqs + 4},
+                    {"bt_indptr", bt_indptr, reqs + 4},
+                    {"bt", bt, 4},
+                    {"n_accepted", n_accepted, reqs},
+                    {"path", path, reqs * max_path}});
+  if (st != MB_OK) return st;
   if (num_reqs == 0) return MB_OK;
   mb::DeviceCtx *ctx = nullptr;
   st = mb::device_ctx(&ctx);
