@@ -447,7 +447,7 @@ mb_status mb_verify_tree(const void *logits, int32_t vocab, const int32_t *token
  * request's nodes, token c + path[r][k] goes to c + k for k < n_accepted[r],
  * and new_kv_len[r] = c + n_accepted[r].  The slots behind keep what they
  * held.  pools: HOST array of the pools' device bases (mb_kv_layout), each
- * [num_pages][2][n_kv_heads][16][head_dim] bf16, 16-byte aligned, distinct;
+ * [num_pages][2][n_kv_heads][16][head_dim] bf16, 16-byte aligned, none over another;
  * the other arrays device int32 as in mb_verify_tree and mb_tree_attention.
  * head_dim % 8 == 0.  A request whose path
  * is not ascending within its nodes, or whose table or pages break the rules,

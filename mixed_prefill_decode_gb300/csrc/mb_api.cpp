@@ -1320,7 +1320,7 @@ mb_status mb_verify_tree(const void *logits, int32_t vocab, const int32_t *token
   return MB_OK;
 }
 
-// The pools of a page operation: present, aligned, distinct.
+// The pools of a page operation: present, aligned, apart.
 static mb_status check_pools(const char *who, void *const *pools, int32_t n_pools, int32_t num_pages,
                              int32_t n_kv_heads, int32_t head_dim) {
   if (!pools || n_pools <= 0 || num_pages <= 0 || n_kv_heads <= 0 || head_dim <= 0)
@@ -1330,8 +1330,11 @@ static mb_status check_pools(const char *who, void *const *pools, int32_t n_pool
   for (const void *p : seen)
     if (!p || reinterpret_cast<uintptr_t>(p) % 16) return fail(MB_EINVAL, "%s: pools must be 16-byte aligned", who);
   std::sort(seen.begin(), seen.end());
-  if (std::adjacent_find(seen.begin(), seen.end()) != seen.end())
-    return fail(MB_EINVAL, "%s: a pool is listed twice", who);
+  // (a pool's bytes, beyond 2^63 for the largest arguments)
+  const double bytes = 64.0 * num_pages * n_kv_heads * head_dim;
+  for (size_t i = 1; i < seen.size(); ++i)
+    if (static_cast<double>(reinterpret_cast<uintptr_t>(seen[i]) - reinterpret_cast<uintptr_t>(seen[i - 1])) < bytes)
+      return fail(MB_EINVAL, "%s: two pools are the same or overlap", who);
   return MB_OK;
 }
 

@@ -71,3 +71,17 @@ def test_compact_refuses_new_lengths_over_an_input(mb, other):
     for at in (a[other] + COMPACT_IN[other] - 4, a[other] - 8):
         _refused(mb, lambda: mb.mb_kv_compact([64 * G, 65 * G], 8, 2, 64, 3, a["qo_indptr"], a["kv_len"], a["bt_indptr"],
                                               a["bt"], a["n_accepted"], a["path"], 4, at), ("new_kv_len", other))
+
+
+POOL = 8 * 2 * 2 * 16 * 64 * 2   # bytes of a pool of 8 pages, 2 heads of 64
+
+
+@pytest.mark.parametrize("pools", [[G, G + POOL - 16], [3 * G, G, 3 * G - POOL + 16], [G, 2 * G, G + 16]])
+def test_page_operations_refuse_pools_over_one_another(mb, pools):
+    _refused(mb, lambda: mb.mb_kv_copy_pages(pools, 8, 2, 64, [1], [2]), ())
+    a = _args(COMPACT_IN)
+    _refused(mb, lambda: mb.mb_kv_compact(pools, 8, 2, 64, 3, *(16 * G + a[k] for k in COMPACT_IN), 4, 64 * G), ())
+
+
+def test_page_operations_take_pools_side_by_side(mb):
+    mb.mb_kv_copy_pages([G, G + POOL, G - POOL], 8, 2, 64, [], [])
