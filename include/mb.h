@@ -175,7 +175,9 @@ mb_status mb_stack_destroy(mb_stack *stack);
  * most MB_MAX_TREE_NODES tokens.  parent == NULL: mb_step, mb_stack_step.  In
  * mb_layer_timing the trees' attention counts as attn_merge.  Errors: those of
  * mb_step, MB_EINVAL (a parent out of range), MB_EUNSUPPORTED (too many nodes),
- * MB_ENOMEM (the first step with trees allocates a workspace). */
+ * MB_ENOMEM (the first step with trees on a device allocates a workspace of
+ * mb_tree_attention_workspace_bytes(), so it must not be captured; see
+ * mb_layer_set_gemm_workspace for layers that step concurrently). */
 mb_status mb_step_tree(mb_layer *layer, mb_kv *kv, const mb_batch *batch, const int32_t *parent, const void *x_in,
                        void *x_out, void *stream);
 mb_status mb_stack_step_tree(mb_stack *stack, mb_kv *const *kvs, const mb_batch *batch, const int32_t *parent,
@@ -229,7 +231,9 @@ mb_status mb_layer_set_gemm_sms(mb_layer *layer, int32_t n);
 /* The layer's GEMM workspace (fp32 partial tiles and tile tickets): device
  * memory of mb_gemm_workspace_bytes() bytes, 256-byte aligned, zero-filled,
  * owned by the caller; NULL returns to the device's shared one.  Layers that
- * step concurrently on different streams need workspaces of their own.
+ * step concurrently on different streams need workspaces of their own.  A
+ * layer with one also allocates a workspace of its own at its first step with
+ * trees (mb_step_tree); all others share one per device.
  * Errors: MB_EINVAL, MB_ECUDA, MB_EUNSUPPORTED. */
 mb_status mb_layer_set_gemm_workspace(mb_layer *layer, void *workspace);
 mb_status mb_layer_timing(mb_layer *layer, double *ms, int32_t n, int64_t *steps);

@@ -117,6 +117,7 @@ struct DeviceCtx {
   int sms = 0;
   int cc_major = 0, cc_minor = 0;
   void *gemm_ws = nullptr;  // shared GEMM partial workspace
+  void *tree_ws = nullptr;  // shared workspace of the steps' tree attention (from the first step with trees on)
   int *err = nullptr;       // error word for standalone calls
 };
 static std::mutex g_dev_mu;
@@ -230,7 +231,7 @@ struct mb_layer {
   float *part = nullptr;
   size_t part_cap = 0;  // floats, counters included
   size_t ctr_cap = 0;   // 4-byte words of counters at the start
-  void *tree_ws = nullptr;   // workspace of the tree attention (from the first step with trees on)
+  void *tree_ws = nullptr;   // its own workspace of the tree attention (only with a GEMM workspace of its own)
   // last step
   int32_t last_T = 0;
   int32_t last_launches = 0;
@@ -259,7 +260,7 @@ struct GraphKey {
   size_t ctr_cap;
   const void *gws;
   size_t offs[11];
-  const void *db, *part, *x_in, *x_out, *kv0;
+  const void *db, *part, *x_in, *x_out, *kv0, *tree_ws;
   bool trees;
   int dec_sms;
   bool operator==(const GraphKey &o) const {
@@ -267,7 +268,7 @@ struct GraphKey {
            n_merge == o.n_merge && n_chunk_slots == o.n_chunk_slots && gemm_ctas == o.gemm_ctas &&
            dec_workers == o.dec_workers &&
            ctr_cap == o.ctr_cap && gws == o.gws &&
-           std::equal(offs, offs + 11, o.offs) && trees == o.trees && db == o.db && part == o.part &&
+           std::equal(offs, offs + 11, o.offs) && trees == o.trees && tree_ws == o.tree_ws && db == o.db && part == o.part &&
            x_in == o.x_in && x_out == o.x_out && kv0 == o.kv0 && dec_sms == o.dec_sms;
   }
 };
@@ -494,6 +495,7 @@ struct StepPlan {
   // a step with drafted trees: each token's place, parent, and which requests are trees
   bool trees = false;
   size_t o_tslot = 0, o_par = 0, o_tree = 0;
+  void *tree_ws = nullptr;
   int n_tiles = 0, n_items = 0, n_merge = 0;   // n_tiles: chunk units; n_merge: decode split groups
   int n_chunk_slots = 0;                       // partial slots of split chunk tiles
   int dec_workers = 0;                         // decode worker CTAs the plan is for
@@ -521,6 +523,24 @@ mb_status validate_parents(const mb_batch *b, const int32_t *parent, std::vector
   return MB_OK;
 }
 
+// Workspace of a step's tree attention.  Layers that share the device's GEMM
+// workspace step in order, so they share one of these too (43 MB at most: one
+// a layer would be 1.7 GB in a model of 40); a layer with a GEMM workspace of
+// its own may step beside others and gets one of its own.
+mb_status step_tree_workspace(mb_layer *L, mb::DeviceCtx *ctx, void **out) {
+  if (static_cast<void *>(L->gws.partials) != ctx->gemm_ws) {
+    mb_status st = MB_OK;
+    if (!L->tree_ws) st = alloc_dev(&L->tree_ws, mb::tree_workspace_bytes(), "tree attention workspace");
+    *out = L->tree_ws;
+    return st;
+  }
+  std::lock_guard<std::mutex> lk(mb::g_dev_mu);
+  mb_status st = MB_OK;
+  if (!ctx->tree_ws) st = alloc_dev(&ctx->tree_ws, mb::tree_workspace_bytes(), "tree attention workspace");
+  *out = ctx->tree_ws;
+  return st;
+}
+
 // Host part of a step: per-token tables, attention work lists (chunk tiles,
 // decode splits, merge list), one upload through `L`'s pinned ring into its
 // device blob.  The batch has been validated.  parent: host, or null for a
@@ -538,8 +558,8 @@ mb_status prepare_step(mb_layer *L, const mb_batch *b, const int32_t *parent, in
   if (parent && (st = validate_parents(b, parent, &tree, &trees)) != MB_OK) return st;
   // (the requests of the chunk tiles and decode rows)
   auto plain = [&](int r) { return !trees || !tree[r]; };
-  if (trees && !L->tree_ws && (st = alloc_dev(&L->tree_ws, mb::tree_workspace_bytes(), "tree attention workspace")) != MB_OK)
-    return st;
+  void *tree_ws = nullptr;
+  if (trees && (st = step_tree_workspace(L, ctx, &tree_ws)) != MB_OK) return st;
   std::vector<int32_t> &hb = L->hbuf;
   hb.clear();
   auto sec = [&](size_t count) {
@@ -560,6 +580,7 @@ mb_status prepare_step(mb_layer *L, const mb_batch *b, const int32_t *parent, in
   P.o_treq = sec(T);
   P.o_tpos = sec(T);
   P.trees = trees;
+  P.tree_ws = tree_ws;
   if (trees) {
     P.o_tslot = sec(T);
     P.o_par = sec(T);
@@ -856,7 +877,7 @@ mb_status launch_layer(mb_layer *L, mb_layer *W, mb_kv *kv, const StepPlan &P, c
   // (split merging happens inside the attention launch; drafted trees have one of their own)
   if (P.trees) {
     mb::TreeArgs ta = {W->q, kv->base, W->o, db + P.o_qo, db + P.o_kv, db + P.o_bti, db + P.o_bt, db + P.o_par,
-                       P.n_reqs, Ti, Hq, Hkv, hd, kv->num_pages, W->tree_ws, W->err, db + P.o_tree};
+                       P.n_reqs, Ti, Hq, Hkv, hd, kv->num_pages, P.tree_ws, W->err, db + P.o_tree};
     if ((st = chk(mb::tree_attention_run(ta, s), "tree attention")) != MB_OK) return st;
     *launches += 2;
   }
@@ -1526,6 +1547,7 @@ mb_status mb_stack_step_tree(mb_stack *S, mb_kv *const *kvs, const mb_batch *b, 
                            plan.o_tiles, plan.o_items, plan.o_tslot, plan.o_par, plan.o_tree};
   std::copy(offs, offs + 11, key.offs);
   key.trees = plan.trees;
+  key.tree_ws = plan.tree_ws;
   key.db = plan.db;
   key.part = L0->part;
   key.x_in = x_in;

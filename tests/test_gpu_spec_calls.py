@@ -5,7 +5,8 @@ import pytest
 import torch
 
 from oracle import spec as OS
-from gpu_util import f64
+from mixed_prefill_decode_gb300 import workload as W
+from gpu_util import f64, from_dev, to_dev
 from test_gpu_verify_sums import Stars
 
 pytestmark = pytest.mark.gpu
@@ -82,3 +83,64 @@ def test_negative_draft_probabilities_count_as_zero(mb):
     s.probs = np.where(at, bad, clean)
     for a, b in zip(s.run(mb, np.arange(s.n)), want):
         assert np.array_equal(a, b)
+
+
+def _tree_layers(mb, count, seed=3):
+    """Layers of one shape with their pools and a batch of trees for each."""
+    shape, reqs = W.SMALL_GQA, [(700, 24), (90, 5), (1500, 60), (33, 1)]
+    wl = W.Workload("spec", shape, reqs, seed)
+    weights, x, batch, pool = W.materialize(wl)
+    rng = np.random.default_rng(seed)
+    parent = np.concatenate([[-1] + [int(rng.integers(0, i)) for i in range(1, q)] for _, q in reqs]).astype(np.int32)
+    dw = {k: to_dev(v) for k, v in weights.items()}
+    layers = []
+    for i in range(count):
+        dx = to_dev(x) * (1.0 + 0.25 * i)
+        layers.append((mb.Layer(shape.as_dict(), dw, batch.num_tokens, pool.shape[0], kv_buf=to_dev(pool.reshape(-1))), dx,
+                       torch.empty_like(dx)))
+    return layers, mb.Batch.of(batch), parent
+
+
+def test_layers_that_step_in_order_share_a_workspace(mb):
+    """The first step with trees of each further layer costs no 43 MB."""
+    layers, batch, parent = _tree_layers(mb, 5)
+    for L, x, y in layers:
+        L.step(batch, x, y, _stream())
+    L, x, y = layers[0]
+    L.step(batch, x, y, _stream(), parent=parent)
+    torch.cuda.synchronize()
+    free = torch.cuda.mem_get_info()[0]
+    for L, x, y in layers[1:]:
+        L.step(batch, x, y, _stream(), parent=parent)
+        mb.mb_device_status(L.handle, _stream())
+    assert free - torch.cuda.mem_get_info()[0] < mb.mb_tree_attention_workspace_bytes()
+    for L, _, _ in layers:
+        L.close()
+
+
+def test_layers_that_step_at_once_have_workspaces_of_their_own(mb):
+    """Two layers with GEMM workspaces of their own on two streams, each as alone."""
+    layers, batch, parent = _tree_layers(mb, 3)
+    alone = []
+    for L, x, y in layers:
+        L.step(batch, x, y, _stream(), parent=parent)
+        mb.mb_device_status(L.handle, _stream())
+        alone.append(from_dev(y))
+    ws, streams = [], [torch.cuda.Stream() for _ in layers]
+    for i, (L, x, y) in enumerate(layers):
+        if i > 0:   # (layer 0 keeps the device's)
+            ws.append(torch.zeros(mb.mb_gemm_workspace_bytes(), dtype=torch.uint8, device="cuda"))
+            mb.mb_layer_set_gemm_workspace(L.handle, ws[-1])
+        mb.mb_layer_set_gemm_sms(L.handle, 48)   # (3 x 48 CTAs fit the GPU together)
+        L.step(batch, x, y, _stream(), parent=parent)
+    torch.cuda.synchronize()
+    want = [from_dev(y) for _, _, y in layers]
+    for _ in range(20):
+        for (L, x, y), s in zip(layers, streams):
+            L.step(batch, x, y, s.cuda_stream, parent=parent)
+    torch.cuda.synchronize()
+    for (L, _, y), w, a in zip(layers, want, alone):
+        mb.mb_device_status(L.handle, _stream())
+        assert np.array_equal(from_dev(y), w)
+        assert np.max(np.abs(f64(w) - f64(a))) <= 2e-2 * np.max(np.abs(f64(a)))   # (fewer CTAs: other K splits)
+        L.close()
