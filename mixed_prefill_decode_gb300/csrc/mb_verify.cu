@@ -33,16 +33,19 @@
 // over the last row as a rule, two after a refusal with draft probabilities.
 // Its arithmetic is what a full GPU spends most of its time on.
 //
-// Measured: one chain of 5 drafted tokens, vocabulary 128,256, with draft
-// probabilities, 27.5 us, some 3.5 us a node; 64 such 74 us, of which a node's
-// step takes about 5 us and an accurate pass over the row 10 to 15 (the walks
-// read 82 MB: 1.1 TB/s); 16 trees of 24, vocabulary 50,264, 21 us; 6 tokens,
-// greedy, vocabulary 32,000, 7 us.  Tried and dropped: a table of the weights
-// of all bf16 logits in shared memory (its random 8-byte reads took 7 cycles a
-// warp); an only child's row fetched over its parent's, with its maximum and
-// sum computed during the parent's exchange (64 chains 80 us against 78: what it hides is
-// latency that the SM's other CTAs hide already, and a refusal has to fetch the
-// parent's row again).
+// Measured (replays of a graph, the mean of four sets of inputs: a call takes as
+// long as its longest walk): one chain of 5 drafted tokens, vocabulary 128,256,
+// with draft probabilities, 30 us, some 3.5 us a node; 64 such 76 us, of which a
+// node's step takes about 5 us and an accurate pass over the row 10 to 15 (the
+// walks read 82 MB: 1.1 TB/s); 64 without draft probabilities 52 us; 16 trees of
+// 24, vocabulary 50,264, 22.7 us; 6 tokens, greedy, vocabulary 32,000, 8 to 19 us
+// by the length of the path.  Tried and dropped: a table of the weights of all
+// bf16 logits in shared memory (its random 8-byte reads took 7 cycles a warp);
+// accurate sums after every refusal (16 trees 29.3 us against 23.6: most tests
+// are far from their border); an only child's row fetched over its parent's, with
+// its maximum and sum computed during the parent's exchange (64 chains 80 us
+// against 78: what it hides is latency that the SM's other CTAs hide already, and
+// a refusal has to fetch the parent's row again).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -71,7 +74,8 @@ constexpr int kMaxCluster = 16;
 // nothing: 6e-6 each, and up to 80 and 127 additions in a row: 1.3e-5.  In all
 // 1.6e-5 e + 2.6e-5 u z q.
 constexpr float kNear = 0x1p-14f;
-constexpr int kMaxHeld = 17;   // vectors that a thread holds at most: a row of 2^19 logits over 16 CTAs
+constexpr int kMaxVocab = 1 << 19;
+constexpr int kMaxHeld = kMaxVocab / 8 / kMaxCluster / kVerThreads;   // vectors that a thread holds at most
 struct VerifyParams {
   const __nv_bfloat16 *logits;
   const int32_t *tokens;
@@ -822,10 +826,11 @@ cudaError_t verify_tree_run(const VerifyArgs &a, cudaStream_t st) {
   p.T = a.T;
   p.max_path = a.max_path;
   // CTAs per request: enough that a CTA holds at most 20,480 of the row's
-  // logits (four such fit an SM), then as many as still fit the GPU together,
-  // with at least 2,048 logits each; 16 (beyond what every GPU takes) with at
-  // least 4,096: one chain of 5, vocabulary 128,256, 29 us against 35 with 8;
-  // 16 trees of 24, vocabulary 50,264, 25 us against 23.
+  // logits (four such fit an SM; with more than 16 times that in the vocabulary
+  // 16 hold up to 32,768, three an SM), then as many as still fit the GPU
+  // together, with at least 2,048 logits each; 16 (beyond what every GPU takes)
+  // with at least 4,096: one chain of 5, vocabulary 128,256, 29.8 us against
+  // 36.0 with 8; 16 trees of 24, vocabulary 50,264, 24.2 us against 22.6.
   int cluster = 1;
   while (cluster < kMaxCluster && a.vocab > cluster * 20480) cluster *= 2;
   while (cluster < kMaxCluster && static_cast<int64_t>(a.n_reqs) * cluster * 2 <= kVerPerSm * device_sm_count() &&
@@ -835,7 +840,7 @@ cudaError_t verify_tree_run(const VerifyArgs &a, cudaStream_t st) {
   static const FixExpTable table = fix_exp_table();
   p.tab = table;
   p.err = a.err;
-  // a warp holds a 16th of the CTA's part, rounded up
+  // a warp holds an eighth of the CTA's part, rounded up
   const int per_cta = (a.vocab / 8 + cluster - 1) / cluster;
   const int per_thread = ((per_cta + kVerWarps - 1) / kVerWarps + 31) / 32;
   const int smem = per_thread * kVerThreads * 16;
