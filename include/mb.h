@@ -192,8 +192,9 @@ mb_status mb_batch_validate(const mb_batch *batch, int32_t num_pages, int32_t ma
 /* Synchronise `stream` and report any error word the kernels recorded since
  * the last call (then clears it).  MB_EDEVICE if one was set.  layer: that
  * layer's steps; NULL: the standalone calls on the current device (mb_gemm,
- * mb_sample_greedy, mb_embed and mb_gemm_noalloc).  With NULL it allocates
- * nothing, so callers of mb_gemm_noalloc can use it too. */
+ * mb_sample_greedy, mb_embed, mb_tree_attention, mb_verify_tree, mb_kv_compact
+ * and mb_gemm_noalloc).  With NULL it allocates nothing, so callers of
+ * mb_gemm_noalloc can use it too. */
 mb_status mb_device_status(mb_layer *layer, void *stream);
 
 /* Device pointer and byte size of an intermediate of the last step, for
@@ -380,7 +381,9 @@ mb_status mb_embed(const void *table, int32_t vocab, int32_t d, const int32_t *i
  * then its nodes in order, already appended) lie in pages
  * bt[bt_indptr[r] ..], token p in slot p % 16 of the table's page p / 16.
  * Node i sees the whole prefix, its ancestors and itself; scale 1/sqrt(hd).
- * A request has at most 2^24 keys.
+ * A request has at most 2^24 keys.  Logits, maxima, sums and o are fp32; the
+ * probabilities are rounded to bf16 for their product with V, as in mb_step, and
+ * o to bf16 at the end.
  *   q     device bf16 [T][Hq][hd] (rotated), 16-byte aligned
  *   pool  device bf16 [num_pages][2][Hkv][16][hd] (mb_kv_layout's), 128-byte aligned
  *   o     device bf16 [T][Hq hd], 16-byte aligned
@@ -425,14 +428,16 @@ int64_t mb_tree_attention_workspace_bytes(void);
  * vocab 2^-42 references, and does not depend on how the row is split: the same
  * request gets the same answer in any batch.  The reference is the row's largest
  * weight; without draft probabilities it is never more than what the refusals
- * left of the row.
+ * left of the row.  (A logit of less than 2^-16 of the row's largest is taken to
+ * 2^-24 of that: its weight is good to 2^-24 of its exponent.)
  *   logits       device bf16 [T][vocab], vocab % 8 == 0 and at most 2^19, 16-byte aligned
  *   tokens       device int32 [T], the node's token (that of node 0 is not read);
  *                a child whose token is outside [0, vocab) is passed over, as if it
  *                were not there, and records MB_EDEVICE
  *   draft_probs  device fp32 [T][vocab], 16-byte aligned, or NULL; one below 0 counts
  *                as 0, a NaN as more than any p (its token is refused and not drawn)
- *   temperature  device fp32 [num_reqs], >= 0 (0: greedy), or NULL: all greedy
+ *   temperature  device fp32 [num_reqs], >= 0 (0: greedy), or NULL: all greedy; one
+ *                below 0 or not a number counts as 0 and records MB_EDEVICE
  *   u_accept     device fp32 [T] in [0, 1) (that of node 0 is not read); u_final device fp32
  *                [num_reqs] in [0, 1); both may be NULL if temperature is
  *   n_accepted   device int32 [num_reqs]: nodes of the accepted path, node 0 included
@@ -450,13 +455,14 @@ mb_status mb_verify_tree(const void *logits, int32_t vocab, const int32_t *token
  * pools (the layers' of a stack) at once: with c = kv_len[r] minus the
  * request's nodes, token c + path[r][k] goes to c + k for k < n_accepted[r],
  * and new_kv_len[r] = c + n_accepted[r].  The slots behind keep what they
- * held.  pools: HOST array of the pools' device bases (mb_kv_layout), each
- * [num_pages][2][n_kv_heads][16][head_dim] bf16, 16-byte aligned, none over another;
- * the other arrays device int32 as in mb_verify_tree and mb_tree_attention.
- * head_dim % 8 == 0.  A request whose path
- * is not ascending within its nodes, or whose table or pages break the rules,
- * records MB_EDEVICE and keeps its cache; its new_kv_len is not written.
- * Errors: MB_EINVAL, MB_EUNSUPPORTED, MB_ECUDA. */
+ * held.  A request's nodes lie in pages of its own: requests that share pages
+ * (of a common prefix) have the ones from token c on apart.  pools: HOST array of
+ * the pools' device bases (mb_kv_layout), each [num_pages][2][n_kv_heads][16]
+ * [head_dim] bf16, 16-byte aligned, none over another; the other arrays device
+ * int32 as in mb_verify_tree and mb_tree_attention.  head_dim % 8 == 0.  A
+ * request whose path is not ascending within its nodes, or whose table or pages
+ * break the rules, records MB_EDEVICE and keeps its cache; its new_kv_len is not
+ * written.  Errors: MB_EINVAL, MB_EUNSUPPORTED, MB_ECUDA. */
 mb_status mb_kv_compact(void *const *pools, int32_t n_pools, int32_t num_pages, int32_t n_kv_heads, int32_t head_dim,
                         int32_t num_reqs, const int32_t *qo_indptr, const int32_t *kv_len, const int32_t *bt_indptr,
                         const int32_t *bt, const int32_t *n_accepted, const int32_t *path, int32_t max_path,

@@ -85,6 +85,18 @@ def test_negative_draft_probabilities_count_as_zero(mb):
         assert np.array_equal(a, b)
 
 
+def test_a_temperature_that_is_none_is_greedy(mb):
+    """Below 0 or not a number: as 0, and reported."""
+    s = Stars(4, 4096, 2, 13)
+    lg = s.settle()
+    s.tokens[:, 2] = np.argmax(lg, 1)
+    s.temp[:] = [-1.0, np.nan, -np.inf, 0.0]
+    got = s.run(mb, np.arange(4), check=False)
+    with pytest.raises(mb.MbError):
+        mb.mb_device_status(None, _stream())
+    assert np.all(got[0] == 2) and np.all(got[1][:, 1] == 2) and np.all(got[2] == 0)   # (the child's row is all zeros: token 0)
+
+
 def _tree_layers(mb, count, seed=3):
     """Layers of one shape with their pools and a batch of trees for each."""
     shape, reqs = W.SMALL_GQA, [(700, 24), (90, 5), (1500, 60), (33, 1)]
