@@ -85,7 +85,7 @@ NCU_TRAFFIC = {
                      "capture": "ncu DRAM bytes of bench.py --case llama_T576, the third GEMM of the fourth step"},
     # mean over the 16 chunk-alone launches of the prompt sweep (one capture
     # of each: bench.py --case chunk_all), as the roofline's time is
-    "attention_chunk": {"bytes": 174.656480e6, "sha256_16": "54ba0a175bd95688",
+    "attention_chunk": {"bytes": 174.422640e6, "sha256_16": "a1179153cfc8b730",
                         "sources": ("csrc/mb_attn.cu", "csrc/mb_ptx.cuh", "csrc/mb_kernels.h", "csrc/mb_api.cpp"),
                         "capture": "ncu DRAM bytes of bench.py --case chunk_all, the 16 launches of the second pass"},
 }
