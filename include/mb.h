@@ -192,8 +192,8 @@ mb_status mb_batch_validate(const mb_batch *batch, int32_t num_pages, int32_t ma
 /* Synchronise `stream` and report any error word the kernels recorded since
  * the last call (then clears it).  MB_EDEVICE if one was set.  layer: that
  * layer's steps; NULL: the standalone calls on the current device (mb_gemm,
- * mb_sample_greedy, mb_embed, mb_tree_attention, mb_verify_tree, mb_kv_compact
- * and mb_gemm_noalloc).  With NULL it allocates nothing, so callers of
+ * mb_sample_greedy, mb_embed, mb_tree_attention, mb_verify_tree, mb_kv_compact,
+ * mb_batch_tables, mb_tables_release, the mb_latent calls and mb_gemm_noalloc).  With NULL it allocates nothing, so callers of
  * mb_gemm_noalloc can use it too. */
 mb_status mb_device_status(mb_layer *layer, void *stream);
 
@@ -475,6 +475,105 @@ mb_status mb_kv_compact(void *const *pools, int32_t n_pools, int32_t num_pages, 
  * repeat).  pools as in mb_kv_compact.  Errors: MB_EINVAL, MB_EUNSUPPORTED, MB_ECUDA. */
 mb_status mb_kv_copy_pages(void *const *pools, int32_t n_pools, int32_t num_pages, int32_t n_kv_heads,
                            int32_t head_dim, const int32_t *src, const int32_t *dst, int32_t n_pairs, void *stream);
+
+/* ---------------- descriptors built on the GPU -----------------------------
+ * The calls above that take DEVICE descriptors (and the mb_latent ones below)
+ * can have them built there, so that a captured step follows its own lengths
+ * without the host.  The caller keeps, in device memory:
+ *   tables  int32 [max_slots][max_pages]: the pages of the request in each row
+ *   owned   int32 [max_slots]: how many pages the row holds
+ *   ring    int32 [num_pages] and state int32 [4] = {head, count, 0, 0}: the
+ *           free pages are ring[(head + i) % num_pages], i < count
+ * A free row has owned 0.  Calls on the same rows or ring must be ordered.
+ *
+ * mb_batch_tables describes a batch of num_reqs requests: request r sits in row
+ * slots[r], has cached[r] tokens in the cache and brings new_tokens[r] (0
+ * allowed) more.  It needs max(0, ceil((cached + new) / 16) - owned) pages; it
+ * is granted them, and its tokens, if it needs none or if its need and those of
+ * all requests before it fit the free pages.  Granted pages are taken from the
+ * ring's head in request order and appended to the row; a request that is not
+ * granted brings no tokens this time and keeps what it has.  Outputs:
+ *   qo_indptr, bt_indptr [num_reqs + 1], kv_len [num_reqs]: the descriptor, with
+ *           kv_len = cached + granted tokens and ceil(kv_len / 16) pages listed
+ *   bt      [bt_cap]: the pages
+ *   tok_req, tok_pos, tok_slot [T]: each token's request, position and place in
+ *           the cache (page * 16 + position % 16); -1 behind the last token
+ * A second call with the same lengths gives the same descriptor (the pages are
+ * owned by then), so a step that keeps fewer tokens than it brought passes the
+ * smaller `cached` next time.  A request that breaks a rule (a row outside
+ * [0, max_slots) or given twice, a negative length, cached beyond its pages,
+ * more than max_pages pages) records MB_EDEVICE and counts as a request with no
+ * tokens, keys or pages.  If the granted tokens exceed T, or the pages bt_cap,
+ * the batch is empty (tok_* all -1), nothing changes hands and MB_EDEVICE is recorded.  A page
+ * id in the ring or a row outside [0, num_pages) records MB_EDEVICE and gives
+ * its tokens tok_slot -1.  num_reqs at most 8192, max_slots 65536, max_pages
+ * 2^20, num_pages below 2^27, T and bt_cap below 2^30.  All arrays device int32.
+ * Errors: MB_EINVAL, MB_EUNSUPPORTED, MB_ECUDA. */
+mb_status mb_batch_tables(const int32_t *slots, const int32_t *cached, const int32_t *new_tokens, int32_t num_reqs,
+                          int32_t T, int32_t bt_cap, int32_t *tables, int32_t *owned, int32_t max_slots,
+                          int32_t max_pages, const int32_t *ring, int32_t *state, int32_t num_pages,
+                          int32_t *qo_indptr, int32_t *kv_len, int32_t *bt_indptr, int32_t *bt, int32_t *tok_req,
+                          int32_t *tok_pos, int32_t *tok_slot, void *stream);
+
+/* Appends the pages of the requests in rows slots[0 .. n) to the ring's end, in
+ * that order and each request's in its row's, and sets the rows' owned to 0.  A
+ * row outside [0, max_slots) or given twice records MB_EDEVICE and is passed
+ * over; if the ring has no room for the pages nothing changes and MB_EDEVICE is
+ * recorded.  Errors: MB_EINVAL, MB_EUNSUPPORTED, MB_ECUDA. */
+mb_status mb_tables_release(const int32_t *slots, int32_t n, const int32_t *tables, int32_t *owned, int32_t max_slots,
+                            int32_t max_pages, int32_t *ring, int32_t *state, int32_t num_pages, void *stream);
+
+/* ---------------- latent attention ----------------------------------------
+ * A layer whose keys and values are linear maps of one vector per token caches
+ * that vector (`rank` numbers, normalised) and one rotated key of 64 numbers
+ * shared by all heads: pool device bf16 [num_pages][16][rank + 64], vector then
+ * key, token p of a request in slot p % 16 of its table's page p / 16.  Head h
+ * has w_kv[h] = [2 head_dim][rank]: W_uk (keys), then W_uv (values), and attends by
+ *   s_j = scale (q_nope . (W_uk c_j) + q_rope . k_j),  o = sum_j softmax(s)_j (W_uv c_j)
+ * where token i of a request sees keys 0 .. kv_len - n + i (n its tokens).
+ * head_dim 64 or 128, rank 256 or 512, 1 to 128 heads.
+ *   q       device bf16 [T][heads][head_dim + 64]; the first head_dim of a row
+ *           are q_nope (the last 64 are read by mb_latent_append only)
+ *   q_rope  device bf16 [T][heads][64], rotated
+ *   w_kv    device bf16 [heads][2 head_dim][rank]
+ *   o       device bf16 [T][heads * head_dim]
+ * Descriptor arrays are DEVICE int32 as in mb_tree_attention, but the first
+ * request may start at any row (qo_indptr[0] >= 0), so a batch of decodes and
+ * chunks is two calls on parts of one descriptor; a request may have no tokens.
+ * Rows outside every request are left as they were.  A request that breaks a
+ * rule (kv_len below its tokens or above 2^24, a short table, rows outside
+ * [0, T)) records MB_EDEVICE and its rows are left as they were; a page id out
+ * of range is read as page 0, with MB_EDEVICE.  A vector or key that is not
+ * finite makes the rows that see it NaN and reaches no other.  Logits, maxima,
+ * sums and accumulators are fp32; rounded to bf16 on the way are the
+ * probabilities, for their product with the values, and what a weight product
+ * gives to the next one (q_nope W_uk and sum_j p_j c_j in the absorbed form, the
+ * keys and values in the expanded one).  workspace: 256-byte aligned device
+ * memory, needs no initialisation; a call owns it until it completes (calls on
+ * unordered streams, graphs that may run at once, need one each).  No output may
+ * overlap an input.  T at most 2^20.  Errors: MB_EINVAL, MB_EUNSUPPORTED, MB_ECUDA. */
+
+/* The new tokens' cache rows, and their queries' rotation: token t of T goes to
+ * place tok_slot[t] (page * 16 + slot; -1: the row is passed over) with
+ *   pool[tok_slot[t]] = [ RMSNorm(ckv[t][0 .. rank)) * gain,  RoPE(ckv[t][rank .. rank + 64)) ]
+ *   q_rope[t][h] = RoPE(q[t][h][head_dim .. head_dim + 64))
+ * RoPE as in mb_step (rotate-half, angle = tok_pos * theta^(-2i/64)), tok_pos in
+ * [0, 2^24].  ckv: device bf16, rows of ld elements (ld >= rank + 64, a multiple
+ * of 8), 16-byte aligned; gain device bf16 [rank]; places distinct.  A place or
+ * position out of range records MB_EDEVICE and its row is passed over. */
+mb_status mb_latent_append(const void *ckv, int64_t ld, const void *q, const void *gain, void *pool, void *q_rope,
+                           const int32_t *tok_pos, const int32_t *tok_slot, int32_t T, int32_t num_pages,
+                           int32_t n_heads, int32_t head_dim, int32_t rank, float rms_eps, float rope_theta,
+                           void *stream);
+
+/* Attention in the absorbed form, for decodes and a few drafted tokens: W_uk is
+ * applied to the queries and W_uv to the outputs, and the cached rows are read
+ * as they are, once for all heads (and for up to 64 / heads tokens of a request). */
+mb_status mb_latent_attention(const void *q, const void *q_rope, const void *w_kv, const void *pool, void *o,
+                              int32_t num_pages, int32_t n_heads, int32_t head_dim, int32_t rank, float scale,
+                              int32_t num_reqs, int32_t T, const int32_t *qo_indptr, const int32_t *kv_len,
+                              const int32_t *bt_indptr, const int32_t *bt, void *workspace, void *stream);
+int64_t mb_latent_attention_workspace_bytes(int32_t T, int32_t n_heads, int32_t rank);
 
 /* Adaptive chunk size (llm-stack-book 7.8, "Priority and Preemption Policies",
  * adaptive_chunk_size, and its exercise 4, which applies it in schedule()):

@@ -105,6 +105,11 @@ _SIGS = {
     "mb_verify_tree": (_I32, [_VP, _I32, _VP, _VP, _I32, _I32] + [_VP] * 5 + [_I32] + [_VP] * 4),
     "mb_kv_compact": (_I32, [_VP] + [_I32] * 5 + [_VP] * 6 + [_I32, _VP, _VP]),
     "mb_kv_copy_pages": (_I32, [_VP] + [_I32] * 4 + [_VP, _VP, _I32, _VP]),
+    "mb_batch_tables": (_I32, [_VP] * 3 + [_I32] * 3 + [_VP] * 2 + [_I32] * 2 + [_VP] * 2 + [_I32] + [_VP] * 8),
+    "mb_tables_release": (_I32, [_VP, _I32, _VP, _VP, _I32, _I32, _VP, _VP, _I32, _VP]),
+    "mb_latent_append": (_I32, [_VP, _I64] + [_VP] * 6 + [_I32] * 5 + [ctypes.c_float] * 2 + [_VP]),
+    "mb_latent_attention": (_I32, [_VP] * 5 + [_I32] * 4 + [ctypes.c_float] + [_I32] * 2 + [_VP] * 6),
+    "mb_latent_attention_workspace_bytes": (_I64, [_I32] * 3),
     "mb_sched_counts": (_I32, [_VP, c_int32_p]),
     "mb_sched_save": (_I32, [_VP, c_int64_p, _I64, c_int64_p]),
     "mb_sched_load": (_I32, [c_int64_p, _I64, ctypes.POINTER(_VP)]),
@@ -374,6 +379,41 @@ def mb_kv_copy_pages(pools: Sequence, num_pages: int, n_kv_heads: int, head_dim:
     src, dst = array.array("i", src.tobytes()), array.array("i", dst.tobytes())
     _check(lib().mb_kv_copy_pages(bases.buffer_info()[0], len(bases), num_pages, n_kv_heads, head_dim,
                                   src.buffer_info()[0], dst.buffer_info()[0], n, _ptr(stream)))
+
+
+# ----------------------------------------- descriptors built on the GPU
+def mb_batch_tables(slots, cached, new_tokens, num_reqs: int, T: int, bt_cap: int, tables, owned, max_slots: int,
+                    max_pages: int, ring, state, num_pages: int, qo_indptr, kv_len, bt_indptr, bt, tok_req, tok_pos,
+                    tok_slot, stream=None) -> None:
+    _check(lib().mb_batch_tables(_ptr(slots), _ptr(cached), _ptr(new_tokens), num_reqs, T, bt_cap, _ptr(tables),
+                                 _ptr(owned), max_slots, max_pages, _ptr(ring), _ptr(state), num_pages,
+                                 _ptr(qo_indptr), _ptr(kv_len), _ptr(bt_indptr), _ptr(bt), _ptr(tok_req),
+                                 _ptr(tok_pos), _ptr(tok_slot), _ptr(stream)))
+
+
+def mb_tables_release(slots, n: int, tables, owned, max_slots: int, max_pages: int, ring, state, num_pages: int,
+                      stream=None) -> None:
+    _check(lib().mb_tables_release(_ptr(slots), n, _ptr(tables), _ptr(owned), max_slots, max_pages, _ptr(ring),
+                                   _ptr(state), num_pages, _ptr(stream)))
+
+
+# ------------------------------------------------------ latent attention
+def mb_latent_append(ckv, ld: int, q, gain, pool, q_rope, tok_pos, tok_slot, T: int, num_pages: int, n_heads: int,
+                     head_dim: int, rank: int, rms_eps: float, rope_theta: float, stream=None) -> None:
+    _check(lib().mb_latent_append(_ptr(ckv), ld, _ptr(q), _ptr(gain), _ptr(pool), _ptr(q_rope), _ptr(tok_pos),
+                                  _ptr(tok_slot), T, num_pages, n_heads, head_dim, rank, rms_eps, rope_theta,
+                                  _ptr(stream)))
+
+
+def mb_latent_attention(q, q_rope, w_kv, pool, o, num_pages: int, n_heads: int, head_dim: int, rank: int, scale: float,
+                        num_reqs: int, T: int, qo_indptr, kv_len, bt_indptr, bt, workspace, stream=None) -> None:
+    _check(lib().mb_latent_attention(_ptr(q), _ptr(q_rope), _ptr(w_kv), _ptr(pool), _ptr(o), num_pages, n_heads,
+                                     head_dim, rank, scale, num_reqs, T, _ptr(qo_indptr), _ptr(kv_len),
+                                     _ptr(bt_indptr), _ptr(bt), _ptr(workspace), _ptr(stream)))
+
+
+def mb_latent_attention_workspace_bytes(T: int, n_heads: int, rank: int) -> int:
+    return int(lib().mb_latent_attention_workspace_bytes(T, n_heads, rank))
 
 
 # ------------------------------------------------------------- scheduler

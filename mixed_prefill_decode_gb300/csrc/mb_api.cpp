@@ -21,6 +21,7 @@
 #include "mb.h"
 #include "mb_internal.h"
 #include "mb_kernels.h"
+#include "mb_latent.h"
 #include "mb_spec.h"
 
 
@@ -1410,6 +1411,167 @@ mb_status mb_kv_copy_pages(void *const *pools, int32_t n_pools, int32_t num_page
   const cudaError_t e = mb::kv_copy_pages_run(pools, n_pools, n_kv_heads, head_dim, src, dst, n_pairs,
                                               static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return mb::cuda_fail(e, "mb_kv_copy_pages");
+  return MB_OK;
+}
+
+// ------------------------------------------- descriptors built on the GPU
+static mb_status check_tables(const char *who, int32_t n, int32_t max_slots, int32_t max_pages, int32_t num_pages) {
+  if (n < 0 || max_slots <= 0 || max_pages <= 0 || num_pages <= 0)
+    return fail(MB_EINVAL, "%s: sizes must be positive (the number of requests may be 0)", who);
+  if (n > mb::kTablesMaxReqs) return fail(MB_EUNSUPPORTED, "%s: more than %d requests", who, mb::kTablesMaxReqs);
+  if (max_slots > mb::kTablesMaxSlots) return fail(MB_EUNSUPPORTED, "%s: max_slots > %d", who, mb::kTablesMaxSlots);
+  if (max_pages > mb::kTablesMaxPages) return fail(MB_EUNSUPPORTED, "%s: max_pages > 2^20", who);
+  if (num_pages >= 1 << 27) return fail(MB_EUNSUPPORTED, "%s: num_pages must be below 2^27", who);
+  return MB_OK;
+}
+
+mb_status mb_batch_tables(const int32_t *slots, const int32_t *cached, const int32_t *new_tokens, int32_t num_reqs,
+                          int32_t T, int32_t bt_cap, int32_t *tables, int32_t *owned, int32_t max_slots,
+                          int32_t max_pages, const int32_t *ring, int32_t *state, int32_t num_pages,
+                          int32_t *qo_indptr, int32_t *kv_len, int32_t *bt_indptr, int32_t *bt, int32_t *tok_req,
+                          int32_t *tok_pos, int32_t *tok_slot, void *stream) {
+  // (an array of no elements may have no address)
+  if (!tables || !owned || !ring || !state || !qo_indptr || !bt_indptr || (bt_cap != 0 && !bt) ||
+      (num_reqs != 0 && (!slots || !cached || !new_tokens || !kv_len)) || (T != 0 && (!tok_req || !tok_pos || !tok_slot)))
+    return fail(MB_EINVAL, "mb_batch_tables: null argument");
+  if (T < 0 || bt_cap < 0) return fail(MB_EINVAL, "mb_batch_tables: T and bt_cap must not be negative");
+  mb_status st = check_tables("mb_batch_tables", num_reqs, max_slots, max_pages, num_pages);
+  if (st != MB_OK) return st;
+  if (T >= 1 << 30 || bt_cap >= 1 << 30) return fail(MB_EUNSUPPORTED, "mb_batch_tables: T and bt_cap must be below 2^30");
+  const int64_t reqs = 4ll * num_reqs, words = 4ll * T;
+  st = check_apart("mb_batch_tables",
+                   {{"tables", tables, 4ll * max_slots * max_pages},
+                    {"owned", owned, 4ll * max_slots},
+                    {"state", state, 16},
+                    {"qo_indptr", qo_indptr, reqs + 4},
+                    {"kv_len", kv_len, reqs},
+                    {"bt_indptr", bt_indptr, reqs + 4},
+                    {"bt", bt, 4ll * bt_cap},
+                    {"tok_req", tok_req, words},
+                    {"tok_pos", tok_pos, words},
+                    {"tok_slot", tok_slot, words}},
+                   {{"slots", slots, reqs}, {"cached", cached, reqs}, {"new_tokens", new_tokens, reqs}, {"ring", ring, 4ll * num_pages}});
+  if (st != MB_OK) return st;
+  mb::DeviceCtx *ctx = nullptr;
+  st = mb::device_ctx(&ctx);
+  if (st != MB_OK) return st;
+  const mb::TablesArgs a = {slots, cached, new_tokens, num_reqs, T, bt_cap, max_slots, max_pages, num_pages, tables, owned,
+                            const_cast<int32_t *>(ring), state, qo_indptr, kv_len, bt_indptr, bt, tok_req, tok_pos,
+                            tok_slot, ctx->err};
+  const cudaError_t e = mb::batch_tables_run(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return mb::cuda_fail(e, "mb_batch_tables");
+  return MB_OK;
+}
+
+mb_status mb_tables_release(const int32_t *slots, int32_t n, const int32_t *tables, int32_t *owned, int32_t max_slots,
+                            int32_t max_pages, int32_t *ring, int32_t *state, int32_t num_pages, void *stream) {
+  if ((n != 0 && !slots) || !tables || !owned || !ring || !state) return fail(MB_EINVAL, "mb_tables_release: null argument");
+  mb_status st = check_tables("mb_tables_release", n, max_slots, max_pages, num_pages);
+  if (st != MB_OK) return st;
+  st = check_apart("mb_tables_release",
+                   {{"owned", owned, 4ll * max_slots}, {"state", state, 16}, {"ring", ring, 4ll * num_pages}},
+                   {{"slots", slots, 4ll * n}, {"tables", tables, 4ll * max_slots * max_pages}});
+  if (st != MB_OK) return st;
+  if (n == 0) return MB_OK;
+  mb::DeviceCtx *ctx = nullptr;
+  st = mb::device_ctx(&ctx);
+  if (st != MB_OK) return st;
+  const mb::TablesArgs a = {slots, nullptr, nullptr, n, 0, 0, max_slots, max_pages, num_pages, const_cast<int32_t *>(tables),
+                            owned, ring, state, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, ctx->err};
+  const cudaError_t e = mb::tables_release_run(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return mb::cuda_fail(e, "mb_tables_release");
+  return MB_OK;
+}
+
+// ------------------------------------------------------- latent attention
+static mb_status check_latent(const char *who, int32_t T, int32_t num_pages, int32_t n_heads, int32_t head_dim,
+                              int32_t rank) {
+  if (T < 0 || num_pages <= 0 || n_heads <= 0) return fail(MB_EINVAL, "%s: sizes must be positive (T may be 0)", who);
+  if (head_dim != 64 && head_dim != 128) return fail(MB_EUNSUPPORTED, "%s: head_dim %d (supported: 64, 128)", who, head_dim);
+  if (rank != 256 && rank != 512) return fail(MB_EUNSUPPORTED, "%s: rank %d (supported: 256, 512)", who, rank);
+  if (n_heads > 128) return fail(MB_EUNSUPPORTED, "%s: %d heads > 128", who, n_heads);
+  if (num_pages >= 1 << 27) return fail(MB_EUNSUPPORTED, "%s: num_pages must be below 2^27", who);
+  if (T > 1 << 20) return fail(MB_EUNSUPPORTED, "%s: T > 2^20", who);
+  return MB_OK;
+}
+
+mb_status mb_latent_append(const void *ckv, int64_t ld, const void *q, const void *gain, void *pool, void *q_rope,
+                           const int32_t *tok_pos, const int32_t *tok_slot, int32_t T, int32_t num_pages,
+                           int32_t n_heads, int32_t head_dim, int32_t rank, float rms_eps, float rope_theta,
+                           void *stream) {
+  if (!ckv || !q || !gain || !pool || !q_rope || !tok_pos || !tok_slot)
+    return fail(MB_EINVAL, "mb_latent_append: null argument");
+  mb_status st = check_latent("mb_latent_append", T, num_pages, n_heads, head_dim, rank);
+  if (st != MB_OK) return st;
+  if (ld < rank + mb::kLatentRope || ld % 8 || ld > 1 << 30)
+    return fail(MB_EINVAL, "mb_latent_append: ld must be a multiple of 8, at least rank + 64");
+  if (!(rms_eps >= 0.f) || !(rope_theta > 0.f) || !std::isfinite(rms_eps) || !std::isfinite(rope_theta))
+    return fail(MB_EINVAL, "mb_latent_append: rms_eps must be at least 0 and rope_theta above 0");
+  for (const void *p : {ckv, q, gain, static_cast<const void *>(pool), static_cast<const void *>(q_rope)})
+    if (reinterpret_cast<uintptr_t>(p) % 16) return fail(MB_EINVAL, "mb_latent_append: pointers must be 16-byte aligned");
+  if (T == 0) return MB_OK;
+  const int64_t rows = 2ll * T * n_heads;
+  st = check_apart("mb_latent_append",
+                   {{"pool", pool, 32ll * num_pages * (rank + mb::kLatentRope)}, {"q_rope", q_rope, rows * mb::kLatentRope}},
+                   {{"ckv", ckv, 2 * ((T - 1) * ld + rank + mb::kLatentRope)},
+                    {"q", q, rows * (head_dim + mb::kLatentRope)},
+                    {"gain", gain, 2ll * rank},
+                    {"tok_pos", tok_pos, 4ll * T},
+                    {"tok_slot", tok_slot, 4ll * T}});
+  if (st != MB_OK) return st;
+  mb::DeviceCtx *ctx = nullptr;
+  st = mb::device_ctx(&ctx);
+  if (st != MB_OK) return st;
+  const mb::LatentAppendArgs a = {ckv, q, gain, pool, q_rope, tok_pos, tok_slot, ld, T, num_pages, n_heads, head_dim, rank,
+                                  rms_eps, rope_theta, ctx->err};
+  const cudaError_t e = mb::latent_append_run(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return mb::cuda_fail(e, "mb_latent_append");
+  return MB_OK;
+}
+
+int64_t mb_latent_attention_workspace_bytes(int32_t T, int32_t n_heads, int32_t rank) {
+  if (T < 0 || n_heads < 0 || rank < 0) return 0;
+  return static_cast<int64_t>(mb::latent_attention_workspace_bytes(T, n_heads, rank));
+}
+
+// What the two forms of latent attention ask of their arguments.
+static mb_status check_latent_attention(const char *who, const mb::LatentArgs &a, int64_t workspace_bytes) {
+  if (!a.q || !a.q_rope || !a.w_kv || !a.pool || !a.o || !a.qo_indptr || !a.kv_len || !a.bt_indptr || !a.bt || !a.workspace)
+    return fail(MB_EINVAL, "%s: null argument", who);
+  mb_status st = check_latent(who, a.T, a.num_pages, a.H, a.hd, a.rank);
+  if (st != MB_OK) return st;
+  if (a.n_reqs < 0) return fail(MB_EINVAL, "%s: num_reqs < 0", who);
+  if (!(a.scale > 0.f) || !std::isfinite(a.scale)) return fail(MB_EINVAL, "%s: scale must be positive and finite", who);
+  for (const void *p : {a.q, a.q_rope, a.w_kv, static_cast<const void *>(a.o)})
+    if (reinterpret_cast<uintptr_t>(p) % 16) return fail(MB_EINVAL, "%s: q, q_rope, w_kv and o must be 16-byte aligned", who);
+  if (reinterpret_cast<uintptr_t>(a.pool) % 128) return fail(MB_EINVAL, "%s: pool must be 128-byte aligned", who);
+  if (reinterpret_cast<uintptr_t>(a.workspace) % 256) return fail(MB_EINVAL, "%s: workspace must be 256-byte aligned", who);
+  const int64_t reqs = 4ll * a.n_reqs, rows = 2ll * a.T * a.H;
+  return check_apart(who, {{"o", a.o, rows * a.hd}, {"workspace", a.workspace, workspace_bytes}},
+                     {{"q", a.q, rows * (a.hd + mb::kLatentRope)},
+                      {"q_rope", a.q_rope, rows * mb::kLatentRope},
+                      {"w_kv", a.w_kv, 4ll * a.H * a.hd * a.rank},
+                      {"pool", a.pool, 32ll * a.num_pages * (a.rank + mb::kLatentRope)},
+                      {"qo_indptr", a.qo_indptr, reqs + 4},
+                      {"kv_len", a.kv_len, reqs},
+                      {"bt_indptr", a.bt_indptr, reqs + 4},
+                      {"bt", a.bt, 4}});
+}
+
+mb_status mb_latent_attention(const void *q, const void *q_rope, const void *w_kv, const void *pool, void *o,
+                              int32_t num_pages, int32_t n_heads, int32_t head_dim, int32_t rank, float scale,
+                              int32_t num_reqs, int32_t T, const int32_t *qo_indptr, const int32_t *kv_len,
+                              const int32_t *bt_indptr, const int32_t *bt, void *workspace, void *stream) {
+  mb::LatentArgs a = {q, q_rope, w_kv, pool, o, qo_indptr, kv_len, bt_indptr, bt, num_reqs, T, n_heads, head_dim, rank,
+                      num_pages, scale, workspace, nullptr, 0};
+  mb_status st = check_latent_attention("mb_latent_attention", a, mb_latent_attention_workspace_bytes(T, n_heads, rank));
+  if (st != MB_OK || num_reqs == 0 || T == 0) return st;
+  mb::DeviceCtx *ctx = nullptr;
+  st = mb::device_ctx(&ctx);
+  if (st != MB_OK) return st;
+  a.err = ctx->err;
+  const cudaError_t e = mb::latent_attention_run(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return mb::cuda_fail(e, "mb_latent_attention");
   return MB_OK;
 }
 

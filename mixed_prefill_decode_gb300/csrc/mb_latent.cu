@@ -1,0 +1,1017 @@
+// The latent cache of a layer whose heads' keys and values are linear maps of
+// one vector per token, and attention against it in its absorbed form.
+//
+// A cached token is a row of rank + 64 numbers: its vector c (normalised) and
+// one rotated key k_r that all heads share.  Head h with key rows W_uk,h [hd]
+// [rank] and value rows W_uv,h [hd][rank] attends by
+//
+//   s_j = scale (q_nope . (W_uk,h c_j) + q_rope . k_r,j),  p = softmax(s),  o = sum_j p_j W_uv,h c_j
+//
+// and, the maps being linear,
+//
+//   s_j = scale ((W_uk,h^T q_nope) . c_j + q_rope . k_r,j),  o = W_uv,h (sum_j p_j c_j):
+//
+// keys and values are the cached rows themselves.  A single token reads each
+// row once for all heads; a chunk of many does with the expanded form
+// (mb_latent_prefill.cu) what this one does with (2 rank + 64) / (2 hd + 64)
+// times the operations.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "mb_latent.h"
+#include "mb_latent_dev.cuh"
+#include "mb_launch.cuh"
+#include "mb_ptx.cuh"
+#include "mb_spec.h"
+
+namespace mb {
+namespace {
+
+using namespace dev;
+
+// ---------------------------------------------------------------- append
+// One CTA per token: its vector normalised, its key and the queries' last 64
+// numbers rotated (pairs (i, i + 32), frequency theta^(-2 i / 64)), vector and
+// key into the token's slot.  The angles are taken as in rope_append_kernel: a
+// split frequency and a two-constant reduction modulo 2 pi.  What bounds it is
+// HBM: every byte is read and written once; a head's 128 bytes go as eight
+// 16-byte vectors, four lanes to a head.
+constexpr int kAppendThreads = 256;
+constexpr float kTwoPiHi = 6.28318548202514648f;         // fp32(2 pi)
+constexpr float kTwoPiLo = -1.7484556000744893e-07f;     // 2 pi - kTwoPiHi
+constexpr int kRopeHalf = kLatentRope / 2;
+
+struct AppendParams {
+  const __nv_bfloat16 *ckv, *q, *gain;
+  __nv_bfloat16 *pool, *q_rope;
+  const int32_t *tok_pos, *tok_slot;
+  int64_t ld;
+  int num_pages, H, q_row, hd, rank;
+  float eps;
+  int *err;
+  float f_hi[kRopeHalf], f_lo[kRopeHalf];
+};
+
+__device__ __forceinline__ void rotate8(uint4 &a, uint4 &b, const float *cs, const float *sn) {
+  uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float a0 = bf16lo(x[e]), a1 = bf16hi(x[e]), b0 = bf16lo(y[e]), b1 = bf16hi(y[e]);
+    const float c0 = cs[2 * e], c1 = cs[2 * e + 1], s0 = sn[2 * e], s1 = sn[2 * e + 1];
+    x[e] = pack_bf16x2(a0 * c0 - b0 * s0, a1 * c1 - b1 * s1);
+    y[e] = pack_bf16x2(b0 * c0 + a0 * s0, b1 * c1 + a1 * s1);
+  }
+  a = make_uint4(x[0], x[1], x[2], x[3]);
+  b = make_uint4(y[0], y[1], y[2], y[3]);
+}
+
+__global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const __grid_constant__ AppendParams p) {
+  __shared__ float cs[kRopeHalf], sn[kRopeHalf], red[kAppendThreads / 32];
+  pdl_wait();
+  pdl_trigger();
+  const int t = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int slot = p.tok_slot[t], pos = p.tok_pos[t];
+  if (slot == -1) return;   // a row behind the batch's last token
+  if (slot < 0 || slot >= p.num_pages * static_cast<int64_t>(kPage) || pos < 0 || pos > (1 << 24)) {
+    if (tid == 0) atomicExch(p.err, kErrBounds);
+    return;
+  }
+  const uint4 *src = reinterpret_cast<const uint4 *>(p.ckv + t * p.ld);
+  uint4 *dst = reinterpret_cast<uint4 *>(p.pool + static_cast<int64_t>(slot) * (p.rank + kLatentRope));
+  const int nv = p.rank / 8;   // at most 64: two warps hold the vector
+  uint4 x = make_uint4(0, 0, 0, 0), g = x;
+  float ss = 0.f;
+  if (tid < nv) {
+    x = src[tid];
+    g = reinterpret_cast<const uint4 *>(p.gain)[tid];
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) ss += bf16lo(w[e]) * bf16lo(w[e]) + bf16hi(w[e]) * bf16hi(w[e]);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+  if (lane == 0) red[warp] = ss;
+  if (warp == 7) {   // the angles, by a warp that holds none of the vector
+    const int i = lane;
+    const float fp = static_cast<float>(pos);
+    const float hi = fp * p.f_hi[i];
+    const float lo = fmaf(fp, p.f_hi[i], -hi) + fp * p.f_lo[i];
+    const float k = rintf(hi * 0.15915494309189535f);
+    float r = fmaf(-k, kTwoPiHi, hi);
+    r = fmaf(-k, kTwoPiLo, r) + lo;
+    float sv, cv;
+    sincosf(r, &sv, &cv);
+    cs[i] = cv;
+    sn[i] = sv;
+  }
+  __syncthreads();
+  if (tid < nv) {
+    const float inv = rsqrtf((red[0] + red[1]) / static_cast<float>(p.rank) + p.eps);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w}, gw[4] = {g.x, g.y, g.z, g.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(bf16lo(w[e]) * inv * bf16lo(gw[e]), bf16hi(w[e]) * inv * bf16hi(gw[e]));
+    dst[tid] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  // rotated rows: the queries' heads, then (index H) the key; four lanes a row
+  const int part = tid & 3;
+  for (int h = tid >> 2; h <= p.H; h += kAppendThreads / 4) {
+    const uint4 *s = h < p.H ? reinterpret_cast<const uint4 *>(p.q + (static_cast<int64_t>(t) * p.H + h) * p.q_row + p.hd)
+                             : src + nv;
+    uint4 *d = h < p.H ? reinterpret_cast<uint4 *>(p.q_rope + (static_cast<int64_t>(t) * p.H + h) * kLatentRope) : dst + nv;
+    uint4 a = s[part], b = s[part + 4];
+    rotate8(a, b, cs + 8 * part, sn + 8 * part);
+    d[part] = a;
+    d[part + 4] = b;
+  }
+}
+
+// ------------------------------------------------- products head by head
+// C[t][h][n] = sum_k A[t][h][k] B_h(n, k) for every head: the queries through
+// W_uk^T (BMN: B_h is stored [k][n], n contiguous) and the outputs through
+// W_uv (stored [n][k]).  One CTA makes 128 tokens x BN of one head on tcgen05:
+// A and B wholly in shared memory, one barrier per 64-wide chunk of k, so the
+// products start as the first chunk lands.  Heads' weights are read once per
+// 128 tokens: for few tokens they are the time, for many the products.
+template <int KC, int BN, bool BMN>
+struct HeadCfg {
+  static constexpr int A_CHUNK = 128 * 128;
+  static constexpr int B_BYTES = KC * 64 * BN * 2;
+  static constexpr int OFF_B = KC * A_CHUNK;
+  static constexpr int OFF_CTRL = OFF_B + B_BYTES;
+  static constexpr int SMEM = OFF_CTRL + 256;
+  static constexpr uint32_t IDESC = idesc_bf16(128, BN, BMN);
+};
+
+struct HeadParams {
+  __nv_bfloat16 *C;
+  uint8_t *live;                 // [T]: which rows belong to a request
+  const int32_t *qo_indptr, *kv_len, *bt_indptr;
+  int n_reqs, T, H, N, a_col, b_row, b_rows;   // first column of A's row; head h's B starts at row b_row + h * b_rows
+  int *err;
+};
+
+template <int KC, int BN, bool BMN>
+__global__ void __launch_bounds__(128) head_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
+                                                        const __grid_constant__ CUtensorMap tmB,
+                                                        const __grid_constant__ HeadParams p) {
+  using C = HeadCfg<KC, BN, BMN>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_CTRL), *done = full + KC;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int n0 = blockIdx.x * BN, h = blockIdx.y, t0 = blockIdx.z * 128;
+  if (smem_u32(smem) & 1023u) {   // the swizzled layouts need a 1024-aligned base
+    pdl_wait();
+    if (tid == 0) atomicExch(p.err, kErrBounds);
+    return;
+  }
+  if (tid == 0) {
+    for (int c = 0; c < KC; ++c) mbar_init(&full[c], 1);
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+  }
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, BN < 32 ? 32 : BN);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();   // queries, weights, descriptor and outputs belong to earlier kernels of the stream
+  pdl_trigger();
+  if (tid == 0) {
+    const int row = p.b_row + h * p.b_rows;
+    for (int c = 0; c < KC; ++c) {
+      mbar_arrive_expect_tx(&full[c], C::A_CHUNK + 64 * BN * 2);
+      tma_load_3d(smem + c * C::A_CHUNK, &tmA, &full[c], p.a_col + 64 * c, h, t0);
+      if (BMN) {   // [64-wide n chunk][k][128 B]: 64 rows of k of each n chunk
+        for (int j = 0; j < BN / 64; ++j)
+          tma_load_2d(smem + C::OFF_B + j * (KC * 64 * 128) + c * 64 * 128, &tmB, &full[c], n0 + 64 * j, row + 64 * c);
+      } else {     // [64-wide k chunk][n][128 B]
+        tma_load_2d(smem + C::OFF_B + c * BN * 128, &tmB, &full[c], 64 * c, row + n0);
+      }
+    }
+  }
+  const int t = t0 + tid;
+  if (BMN && blockIdx.x == 0 && h == 0) {
+    // which of the tile's rows belong to a request (the others' outputs stay as they were)
+    __shared__ uint32_t rows[4];
+    if (tid < 4) rows[tid] = 0;
+    __syncthreads();
+    for (int r = tid; r < p.n_reqs; r += 128) {
+      const ReqWords w = load_req(p.qo_indptr, p.kv_len, p.bt_indptr, r);
+      if (!req_ok(w, p.T)) continue;
+      const int lo = max(w.q0 - t0, 0), hi = min(w.q1 - t0, 128);
+      for (int i = lo >> 5; i < 4 && 32 * i < hi; ++i) {
+        const int a = max(lo - 32 * i, 0), b = min(hi - 32 * i, 32);
+        if (a < b) atomicOr(&rows[i], (b == 32 ? 0xffffffffu : (1u << b) - 1u) & ~((1u << a) - 1u));
+      }
+    }
+    __syncthreads();
+    if (t < p.T) p.live[t] = (rows[tid >> 5] >> (tid & 31)) & 1u;
+  }
+  if (tid == 0) {
+    const uint64_t a0 = sdesc_sw128(smem_u32(smem), 16, 1024);
+    const uint64_t b0 = BMN ? sdesc_sw128(smem_u32(smem + C::OFF_B), KC * 64 * 128, 1024)
+                            : sdesc_sw128(smem_u32(smem + C::OFF_B), 16, 1024);
+    for (int c = 0; c < KC; ++c) {
+      if (!mbar_wait(&full[c], 0, abort_flag, p.err, kErrWaitMma)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const uint64_t a = a0 + ((c * C::A_CHUNK + kk * 32) >> 4);
+        const uint64_t b = b0 + (BMN ? ((c * 64 + kk * 16) * 128) >> 4 : (c * BN * 128 + kk * 32) >> 4);
+        mma_bf16(tmem, a, b, C::IDESC, (c > 0 || kk > 0) ? 1u : 0u);
+      }
+    }
+    mma_commit(done);
+  }
+  __syncwarp();
+  bool ok = mbar_wait(done, 0, abort_flag, p.err, kErrWaitEpilogue);
+  ok = __all_sync(0xffffffffu, ok) && !*abort_flag;
+  if (ok) {
+    tc_fence_after();
+    const bool mine = t < p.T && (BMN || p.live[t]);
+    uint4 *dst = reinterpret_cast<uint4 *>(p.C + (static_cast<int64_t>(t) * p.H + h) * p.N + n0);
+    for (int cc = 0; cc < BN / 32; ++cc) {
+      float v[32];
+      tmem_ld32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + cc * 32, v);
+      if (mine)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          dst[cc * 4 + k] = make_uint4(pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
+                                       pack_bf16x2(v[8 * k + 4], v[8 * k + 5]), pack_bf16x2(v[8 * k + 6], v[8 * k + 7]));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, BN < 32 ? 32 : BN);
+  }
+}
+
+// ------------------------------------------------------ absorbed attention
+// A unit is a tile of tokens of a request with up to 64 (token, head) rows; a
+// CTA streams its keys in blocks of 64 rows of the cache, each copied once by
+// TMA (a page's 16 rows per copy) and used twice, as keys and as values:
+//
+//   S   = Q K^T     M = 64 rows, N = 64 keys, K = rank + 64: a row of S is one
+//                   thread's, so its maximum and sum need no exchange
+//   O^T += V^T P^T  M = 128 numbers of the vectors, N = rows, K = 64 keys,
+//                   rank / 128 times: with the vectors on the M side the
+//                   accumulators of 64 rows take rank / 2 of the 512 columns of
+//                   TMEM, not all of them
+//
+// With more than 64 heads two CTAs side by side take half the heads each and
+// the same keys at the same time.  The probabilities are rounded to bf16 for
+// their product with V, as everywhere in this library; logits, maxima, sums and
+// accumulators are fp32.
+constexpr int kMaxCtas = 160;       // CTAs of a launch at most; sizes the workspace
+constexpr int kRecBytes = 8192;     // workspace: one record of 8 ints per CTA, then the partials
+constexpr int kBlk = 64;            // keys of a block
+constexpr int kCostUnit = 2;        // a unit's start and end, in blocks
+constexpr int kMinShare = 3;        // the least a CTA takes, in blocks
+
+struct AbsParams {
+  __nv_bfloat16 *oc;             // [T][H][rank]: sum_j p_j c_j
+  const __nv_bfloat16 *pool;
+  const int32_t *qo_indptr, *kv_len, *bt_indptr, *bt;
+  int n_reqs, T, H, Hc, HT, NT, N, num_pages;   // heads of a tile, head tiles, tokens of a tile, padded rows
+  float scale_log2;
+  int32_t *rec;
+  float *part;                   // [2 slots per CTA][64 rows][rank + 4]: o, m, l, pad
+  int *err;
+};
+
+template <int RANK>
+struct AbsCfg {
+  static constexpr int NC = RANK / 64 + 1;          // 64-wide chunks of a cached row
+  static constexpr int ATOM = NC * 1024;            // 8 rows: [chunk][8 rows][128 B]
+  static constexpr int PAGE_BYTES = 2 * ATOM;
+  static constexpr int STAGE = (kBlk / 8) * ATOM;
+  static constexpr int NST = RANK == 512 ? 2 : 4;
+  static constexpr int Q_CHUNK = 64 * 128;
+  static constexpr int DT = RANK / 128;             // tiles of 128 numbers of the vectors
+  static constexpr int NSEG = 4;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = OFF_Q + NC * Q_CHUNK;
+  static constexpr int OFF_P = OFF_K + NST * STAGE;
+  static constexpr int OFF_CTRL = OFF_P + 64 * 128;
+  static constexpr int SMEM = OFF_CTRL + 2048;
+  static constexpr int THREADS = 192;               // TMA, MMA, 4 softmax warps
+  static constexpr uint32_t IDESC_S = idesc_bf16(64, kBlk, false);
+  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr uint32_t O_COL = 128;            // S buffers at 0 and 64, O^T tile dt at 128 + 64 dt
+};
+
+// A piece of a unit, as the producer tells it to the other roles.
+struct AbsSeg {
+  int32_t nb, j0;        // blocks [j0, j0 + nb); nb 0: no more pieces
+  int32_t t0, toks;      // the tile's first row of q, its tokens
+  int32_t first;         // the last key that the tile's first token sees
+  int32_t kv, slot;      // partial slot, -1: the unit is whole
+  int32_t odd;           // the first key behind `first` whose vector holds an infinity or a NaN
+};
+
+struct AbsReq {
+  int t0, n, kv, b0, nkb, tiles;
+  int64_t unit, cost;    // of one unit, of all
+};
+
+template <int RANK>
+struct AbsCtrl {
+  using C = AbsCfg<RANK>;
+  uint64_t q_full, q_empty;
+  uint64_t k_full[C::NST], k_empty[C::NST];
+  uint64_t s_full[2], p_full, pv_done;
+  uint64_t seg_full[C::NSEG], seg_empty[C::NSEG];
+  uint64_t done;
+  AbsSeg seg[C::NSEG];
+  int64_t wsum[C::THREADS / 32];
+  int64_t start_base;
+  AbsReq start;
+  int32_t start_req;
+  uint32_t tmem;
+  int abort;
+  float col[64];         // one number per row: the rescaling, the reciprocal of its sum
+  int64_t base[64];      // where the row goes, -1: nowhere
+};
+
+__device__ __forceinline__ AbsReq abs_req(const AbsParams &p, const ReqWords w, bool *bad) {
+  AbsReq q;
+  *bad = !req_ok(w, p.T);
+  q.t0 = w.q0;
+  q.n = *bad ? 0 : w.q1 - w.q0;
+  q.kv = w.kv;
+  q.b0 = w.b0;
+  q.nkb = q.n ? (w.kv + kBlk - 1) / kBlk : 0;
+  q.tiles = (q.n + p.NT - 1) / p.NT;
+  q.unit = kCostUnit + q.nkb;
+  q.cost = q.unit * q.tiles;
+  return q;
+}
+
+template <int RANK>
+__global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
+    latent_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmR,
+                            const __grid_constant__ CUtensorMap tmK, const __grid_constant__ AbsParams p) {
+  using C = AbsCfg<RANK>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t *sQ = smem + C::OFF_Q, *sK = smem + C::OFF_K, *sP = smem + C::OFF_P;
+  static_assert(sizeof(AbsCtrl<RANK>) <= 2048, "control area");
+  static_assert(C::SMEM <= 232448, "shared memory");
+  AbsCtrl<RANK> &ct = *reinterpret_cast<AbsCtrl<RANK> *>(smem + C::OFF_CTRL);
+  volatile int *abort_flag = &ct.abort;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;   // (known uniform)
+  const int ht = blockIdx.x % p.HT, cta = blockIdx.x / p.HT, W_max = gridDim.x / p.HT;
+  if (smem_u32(smem) & 1023u) {   // the swizzled layouts need a 1024-aligned base
+    pdl_wait();
+    if (threadIdx.x == 0) {
+      atomicExch(p.err, kErrBounds);
+      p.rec[blockIdx.x * 8] = 0;
+    }
+    return;
+  }
+  if (threadIdx.x == 0) {
+    mbar_init(&ct.q_full, 1);
+    mbar_init(&ct.q_empty, 1);
+    for (int s = 0; s < C::NST; ++s) {
+      mbar_init(&ct.k_full[s], 1);
+      mbar_init(&ct.k_empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) mbar_init(&ct.s_full[b], 1);
+    mbar_init(&ct.p_full, 128);
+    mbar_init(&ct.pv_done, 1);
+    for (int s = 0; s < C::NSEG; ++s) {
+      mbar_init(&ct.seg_full[s], 1);
+      mbar_init(&ct.seg_empty[s], 5);   // the MMA issuer and the 4 softmax warps
+    }
+    mbar_init(&ct.done, 1);
+    ct.abort = 0;
+    ct.start_req = -1;
+    fence_mbar_init();
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmR);
+    prefetch_tmap(&tmK);
+  }
+  if (warp == 1) {
+    tmem_alloc(&ct.tmem, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  pdl_wait();   // the descriptor, queries, cache and outputs belong to earlier kernels of the stream
+  pdl_trigger();
+
+  // ---- this CTA's part of the line: [x0, x1) of `total`
+  const int per = (p.n_reqs + C::THREADS - 1) / C::THREADS;
+  const int r_lo = min(p.n_reqs, static_cast<int>(threadIdx.x) * per), r_hi = min(p.n_reqs, r_lo + per);
+  int64_t mine = 0;
+  AbsReq last{};
+  for (int r = r_lo; r < r_hi; ++r) {
+    bool bad;
+    last = abs_req(p, load_req(p.qo_indptr, p.kv_len, p.bt_indptr, r), &bad);
+    mine += last.cost;
+    if (bad && blockIdx.x == 0) atomicExch(p.err, kErrBounds);
+  }
+  int64_t inc = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, inc, off);
+    if (lane >= off) inc += v;
+  }
+  if (lane == 31) ct.wsum[warp] = inc;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ct.tmem, 0);
+  int64_t total = 0, pre = inc - mine;
+#pragma unroll
+  for (int w = 0; w < C::THREADS / 32; ++w) {
+    if (w < warp) pre += ct.wsum[w];
+    total += ct.wsum[w];
+  }
+  const int64_t W = total / kMinShare < 1 ? (total > 0 ? 1 : 0) : (total / kMinShare < W_max ? total / kMinShare : W_max);
+  const bool active = cta < W;
+  const int64_t x0 = active ? div64(total * cta, W) : 0, x1 = active ? div64(total * (cta + 1), W) : 0;
+  if (active && pre <= x0 && x0 < pre + mine) {
+    for (int r = r_lo; r < r_hi; ++r) {
+      bool bad;
+      if (per > 1) last = abs_req(p, load_req(p.qo_indptr, p.kv_len, p.bt_indptr, r), &bad);
+      if (x0 < pre + last.cost) {
+        ct.start_req = r;
+        ct.start = last;
+        ct.start_base = pre;
+        break;
+      }
+      pre += last.cost;
+    }
+  }
+  __syncthreads();
+
+  if (!active) {
+    if (threadIdx.x == 0) p.rec[blockIdx.x * 8] = 0;
+  } else if (warp == 0) {
+    // ------------------------------------------------ schedule, TMA producer
+    int32_t rec[5] = {0, 0, 0, 0, 0};
+    int r = ct.start_req;
+    bool bad;
+    AbsReq q = ct.start;
+    ReqWords nx{};
+    if (r + 1 < p.n_reqs) nx = load_req(p.qo_indptr, p.kv_len, p.bt_indptr, r + 1);
+    int u = static_cast<int>(div64(x0 - ct.start_base, q.unit));   // the unit that x0 lies in
+    int64_t base = ct.start_base + u * q.unit;
+    int kcnt = 0, nseg = 0, quse = 0;   // (quse: lane 0's)
+    bool ok = true;
+    while (ok && base < x1) {
+      auto cut = [&](int64_t x) {   // blocks of the unit that lie before x
+        const int64_t d = x - base - kCostUnit;
+        return d <= 0 ? 0 : static_cast<int>(min(static_cast<int64_t>(q.nkb), d));
+      };
+      auto owner = [&](int j) {     // the CTA whose part holds block j: the last w with total w / W <= its place
+        return static_cast<int>(div64((base + kCostUnit + j + 1) * W - 1, total));
+      };
+      const int j0 = cut(x0), j1 = cut(x1);
+      if (j1 > j0) {
+        const int first = owner(0), last_w = owner(q.nkb - 1);
+        const int i0 = u * p.NT, toks = min(p.NT, q.n - i0);
+        const int32_t *table = p.bt + q.b0;
+        const int n_pages = (q.kv + kPage - 1) / kPage;
+        auto page_of = [&](int blk) { return lane < 4 && 4 * blk + lane < n_pages ? table[4 * blk + lane] : 0; };
+        int cur = page_of(j0), nxt = j0 + 1 < j1 ? page_of(j0 + 1) : 0;
+        // the query tile
+        if (lane == 0) {
+          ok = mbar_wait(&ct.q_empty, (quse & 1) ^ 1, abort_flag, p.err, kErrWaitProducer);
+          if (ok) {
+            mbar_arrive_expect_tx(&ct.q_full, C::NC * p.Hc * p.NT * 128);
+            for (int ch = 0; ch < C::NC - 1; ++ch)
+              tma_load_3d(sQ + ch * C::Q_CHUNK, &tmQ, &ct.q_full, ch * 64, ht * p.Hc, q.t0 + i0);
+            tma_load_3d(sQ + (C::NC - 1) * C::Q_CHUNK, &tmR, &ct.q_full, 0, ht * p.Hc, q.t0 + i0);
+            ++quse;
+          }
+        }
+        // the piece's record for the other roles
+        const int ss = nseg % C::NSEG;
+        if (lane == 0 && ok) {
+          ok = mbar_wait(&ct.seg_empty[ss], ((nseg / C::NSEG) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer);
+          if (ok) {
+            AbsSeg &sg = ct.seg[ss];
+            sg.nb = j1 - j0;
+            sg.j0 = j0;
+            sg.t0 = q.t0 + i0;
+            sg.toks = toks;
+            sg.first = q.kv - q.n + i0;
+            sg.kv = q.kv;
+            sg.slot = first == last_w ? -1 : 2 * static_cast<int>(blockIdx.x) + (cta == first ? 1 : 0);
+            sg.odd = INT32_MAX;
+            mbar_arrive(&ct.seg_full[ss]);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        ++nseg;
+        if (first != last_w && cta == first) {
+          rec[0] = last_w - first + 1;
+          rec[1] = q.t0 + i0;
+          rec[2] = toks;
+        }
+        for (int j = j0; j < j1 && ok; ++j) {
+          const int np = min(4, n_pages - 4 * j), st = kcnt % C::NST;
+          const int after = j + 2 < j1 ? page_of(j + 2) : 0;
+          ok = __all_sync(0xffffffffu, mbar_wait(&ct.k_empty[st], ((kcnt / C::NST) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer));
+          if (!ok) break;
+          if (lane < np && (cur < 0 || cur >= p.num_pages)) {
+            atomicExch(p.err, kErrBounds);
+            cur = 0;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&ct.k_full[st], np * C::PAGE_BYTES);
+          __syncwarp();
+          if (lane < np)
+            tma_load_5d(sK + st * C::STAGE + lane * C::PAGE_BYTES, &tmK, &ct.k_full[st], 0, 0, 0, 0, cur);
+          ++kcnt;
+          cur = nxt;
+          nxt = after;
+        }
+      }
+      // the next unit on the line
+      base += q.unit;
+      if (++u == q.tiles) {
+        u = 0;
+        do {
+          ++r;
+          if (r >= p.n_reqs) break;
+          q = abs_req(p, nx, &bad);
+          if (r + 1 < p.n_reqs) nx = load_req(p.qo_indptr, p.kv_len, p.bt_indptr, r + 1);
+        } while (q.n == 0);
+        if (r >= p.n_reqs) break;
+      }
+    }
+    if (lane == 0) {
+      if (ok) {
+        const int ss = nseg % C::NSEG;
+        if (mbar_wait(&ct.seg_empty[ss], ((nseg / C::NSEG) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer)) {
+          ct.seg[ss].nb = 0;
+          mbar_arrive(&ct.seg_full[ss]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 3; ++k) p.rec[blockIdx.x * 8 + k] = rec[k];
+      // after an abort, let copies in flight land before the CTA exits (bounded)
+      if (!ok || *abort_flag) {
+        const uint64_t t_start = globaltimer();
+        auto drain = [&](uint64_t *bar, int use) {
+          while (!mbar_try_wait(smem_u32(bar), use & 1) && globaltimer() - t_start < kWaitLimitNs) {
+          }
+        };
+        for (int i = max(0, kcnt - C::NST); i < kcnt; ++i) drain(&ct.k_full[i % C::NST], i / C::NST);
+        if (quse > 0) drain(&ct.q_full, quse - 1);
+      }
+    }
+  } else if (warp == 1) {
+    // --------------------------------------------------------- MMA issuer
+    // S of a block goes out as soon as it (and Q) landed and the product of the
+    // block two before it is issued (its S buffer is then read); O^T as soon as
+    // P is written.  S runs on into the next piece.  The whole warp keeps the
+    // books, in step, and one elected lane issues.
+    const uint64_t qd0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
+    const uint64_t kd0 = sdesc_sw128(smem_u32(sK), 16, C::ATOM);
+    const uint64_t vd0 = sdesc_sw128(smem_u32(sK), 1024, C::ATOM);
+    const uint64_t pd0 = sdesc_sw128(smem_u32(sP), 16, 1024);
+    const uint32_t idesc_pv = idesc_bf16_ab(128, p.N, true, false);
+    int s_seg = 0, s_item = 0, s_nb = 0, s_lb = 0, s_q = 0;     // S: piece, block, blocks of the piece and place in it
+    int v_seg = 0, v_item = 0, v_nb = 0, v_lb = 0;              // O^T
+    bool s_in = false, v_in = false, s_end = false;
+    uint64_t t_idle = 0;
+    auto uni = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    auto ready = [](uint64_t *bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_test_wait(smem_u32(bar), parity)) != 0;
+    };
+    for (uint32_t spin = 1;; ++spin) {   // rounds without progress
+      bool progress = false;
+      if (!s_end && s_item < v_item + 2) {
+        if (!s_in && ready(&ct.seg_full[s_seg % C::NSEG], (s_seg / C::NSEG) & 1)) {
+          s_nb = uni(ct.seg[s_seg % C::NSEG].nb);
+          s_lb = 0;
+          s_in = true;
+          if (s_nb == 0) s_end = true;
+        }
+        if (s_in && !s_end) {
+          const int st = s_item % C::NST;
+          if ((s_lb > 0 || ready(&ct.q_full, s_q & 1)) && ready(&ct.k_full[st], (s_item / C::NST) & 1)) {
+            tc_fence_after();
+            const uint32_t d = tmem + 64 * (s_item & 1);
+            const uint64_t kd = kd0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
+            const bool last_blk = s_lb == s_nb - 1;
+            if (elect_one()) {
+#pragma unroll
+              for (int ch = 0; ch < C::NC; ++ch)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  mma_bf16(d, qd0 + ((ch * C::Q_CHUNK + kk * 32) >> 4), kd + ((ch * 1024 + kk * 32) >> 4), C::IDESC_S,
+                           (ch > 0 || kk > 0) ? 1u : 0u);
+              mma_commit(&ct.s_full[s_item & 1]);
+              if (last_blk) mma_commit(&ct.q_empty);
+            }
+            __syncwarp();
+            ++s_item;
+            if (++s_lb == s_nb) {
+              s_in = false;
+              ++s_seg;
+              ++s_q;
+            }
+            progress = true;
+          }
+        }
+      }
+      if (v_item < s_item) {
+        if (!v_in) {   // S of the piece is out: its record is there
+          v_nb = uni(ct.seg[v_seg % C::NSEG].nb);
+          v_lb = 0;
+          v_in = true;
+        }
+        if (ready(&ct.p_full, v_item & 1)) {
+          tc_fence_after();
+          const int st = v_item % C::NST;
+          const uint64_t vd = vd0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < kBlk / 16; ++ks)   // 16 keys (two atoms) per MMA; 128 numbers are two chunks
+#pragma unroll
+              for (int dt = 0; dt < C::DT; ++dt)
+                mma_bf16(tmem + C::O_COL + 64 * dt, vd + ((ks * 2 * C::ATOM + dt * 2048) >> 4), pd0 + ((ks * 32) >> 4),
+                         idesc_pv, (v_lb > 0 || ks > 0) ? 1u : 0u);
+            mma_commit(&ct.pv_done);
+            mma_commit(&ct.k_empty[st]);
+            if (v_lb + 1 == v_nb) mbar_arrive(&ct.seg_empty[v_seg % C::NSEG]);
+          }
+          __syncwarp();
+          ++v_item;
+          if (++v_lb == v_nb) {
+            v_in = false;
+            ++v_seg;
+          }
+          progress = true;
+        }
+      }
+      if (s_end && v_item == s_item) break;
+      if (progress) {
+        spin = 0;
+        t_idle = 0;
+      } else if ((spin & 255u) == 0) {
+        if (t_idle == 0) t_idle = globaltimer();
+        const bool late = globaltimer() - t_idle > kWaitLimitNs;
+        if (__any_sync(0xffffffffu, late || *abort_flag)) {
+          if (__any_sync(0xffffffffu, late) && lane == 0) {
+            *abort_flag = 1;
+            atomicExch(p.err, kErrWaitMma);
+          }
+          break;
+        }
+      }
+    }
+    // every MMA issued above has completed before TMEM is freed
+    if (elect_one()) mma_commit(&ct.done);
+    __syncwarp();
+    const uint64_t t_end = globaltimer();
+    while (!mbar_try_wait(smem_u32(&ct.done), 0) && globaltimer() - t_end < kWaitLimitNs) {
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------- softmax / epilogue
+    const int qu = warp & 3;                     // TMEM lane quarter: rows 16 qu .. 16 qu + 15 of S in its first 16 lanes
+    const int row = qu * 16 + (lane & 15);
+    const int tid = (warp - 2) * 32 + lane;      // of the 128
+    const uint32_t lane_base = static_cast<uint32_t>(qu * 32) << 16;
+    constexpr float kRescaleAbove = 8.f;         // log2 units
+    const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+    const int row_tok = row / p.Hc, row_head = ht * p.Hc + row % p.Hc;
+    int nseg = 0, item = 0;
+    // The four warps meet in barriers, which have no limit: a warp whose wait
+    // ran out goes on to the next one with `fail` set, and all leave together.
+    bool fail = false;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      if (!fail) fail = !__all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.err, kErrWaitSoftmax));
+    };
+    while (true) {
+      const int ss = nseg % C::NSEG;
+      wait(&ct.seg_full[ss], (nseg / C::NSEG) & 1);
+      if (named_bar_or(1, 128, fail)) break;
+      AbsSeg &sg = ct.seg[ss];
+      const int nb = sg.nb;
+      if (nb == 0) break;
+      const int j0 = sg.j0, first = sg.first, kv = sg.kv;
+      const bool live = lane < 16 && row_tok < sg.toks && row_head < p.H;
+      const int limit = first + row_tok;          // the last key that the row sees
+      float m_ref = -INFINITY, l = 0.f;
+      bool stop = false;
+      for (int lb = 0; lb < nb; ++lb, ++item) {
+        const int key0 = kBlk * (j0 + lb);
+        wait(&ct.s_full[item & 1], (item >> 1) & 1);
+        float sv[64];
+        float mx = -INFINITY;
+        if (!fail) {
+          tc_fence_after();
+          tmem_ld64(tmem + lane_base + 64 * (item & 1), sv);
+          const int vis = limit - key0;
+          if (vis < kBlk - 1)
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+              if (e > vis) sv[e] = -INFINITY;
+          float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 64; e += 8) {
+            m0 = max3f(m0, sv[e], sv[e + 1]);
+            m1 = max3f(m1, sv[e + 2], sv[e + 3]);
+            m2 = max3f(m2, sv[e + 4], sv[e + 5]);
+            m3 = max3f(m3, sv[e + 6], sv[e + 7]);
+          }
+          mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * p.scale_log2;
+          if (!live) mx = -INFINITY;
+          if (lb == 0) m_ref = mx;
+        }
+        // O^T holds a row as a column, in every warp's lanes: if a row rose
+        // more than 2^8 above its reference, all four warps scale it
+        const bool grow = mx > m_ref + kRescaleAbove;
+        if (named_bar_or(1, 128, grow || fail)) {
+          if (item > 0) wait(&ct.pv_done, (item - 1) & 1);   // O^T holds the blocks before
+          if (named_bar_or(1, 128, fail)) {
+            stop = true;
+            break;
+          }
+          tc_fence_after();
+          const float alpha = grow ? ex2_approx(m_ref - mx) : 1.f;
+          if (lane < 16) ct.col[row] = alpha;
+          named_bar_sync(1, 128);
+#pragma unroll 1
+          for (int cc = 0; cc < C::DT * 64; cc += 32) {
+            if ((cc & 63) >= p.N) continue;
+            float v[32];
+            tmem_ld32(tmem + lane_base + C::O_COL + cc, v);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] *= ct.col[(cc & 63) + k];
+            tmem_st32(tmem + lane_base + C::O_COL + cc, v);
+          }
+          if (grow) {
+            l *= alpha;
+            m_ref = mx;
+          }
+        }
+        const float negm = m_ref == -INFINITY ? 0.f : -m_ref;   // a row that has seen nothing yet
+        uint32_t pk[32];
+        float2 sum = make_float2(0.f, 0.f);
+        probs<64>(sv, sc2, negm, pk, sum);
+        l += sum.x + sum.y;
+        if (item > 0) wait(&ct.pv_done, (item - 1) & 1);   // P of the block before is read
+        if (live) {
+          uint8_t *prow = sP + (row >> 3) * 1024 + (row & 7) * 128;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4 *>(prow + ((k ^ (row & 7)) * 16)) = make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+        }
+        if (key0 + kBlk - 1 > first && tid < kBlk) {
+          // Keys that some row does not see: P is 0 there, but 0 times an
+          // infinity or a NaN is not.  Rows past the request's last key hold
+          // anything: zeroed.  So are those of the tile's own tokens with a value
+          // that is not finite; the rows that see one become NaN at the end.
+          const int key = key0 + tid;
+          if (key > first) {
+            uint8_t *vrow = sK + (item % C::NST) * C::STAGE + (tid >> 3) * C::ATOM + (tid & 7) * 128;
+            if (wipe_row<RANK / 64>(vrow, key >= kv)) atomicMin(&sg.odd, key);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(&ct.p_full);
+      }
+      if (stop) break;
+      // ---- the piece is done: sum_j p_j c_j of its rows, or its partial
+      wait(&ct.pv_done, (item - 1) & 1);
+      if (named_bar_or(1, 128, fail)) break;
+      tc_fence_after();
+      const int slot = sg.slot;
+      if (lane < 16) {
+        int64_t at = -1;
+        if (live) at = slot < 0 ? (static_cast<int64_t>(sg.t0 + row_tok) * p.H + row_head) * RANK
+                                : (static_cast<int64_t>(slot) * 64 + row) * (RANK + 4);
+        ct.base[row] = at;
+        if (live && sg.odd <= limit) l = NAN;
+        ct.col[row] = 1.f / l;
+        if (live && slot >= 0) *reinterpret_cast<float2 *>(p.part + at + RANK) = make_float2(m_ref, l);
+      }
+      named_bar_sync(1, 128);
+      const int rows = sg.toks * p.Hc;
+#pragma unroll 1
+      for (int cc = 0; cc < C::DT * 64; cc += 32) {
+        const int r0 = cc & 63, n = (cc >> 6) * 128 + qu * 32 + lane;   // rows from r0 on, number n of their vectors
+        if (r0 >= rows) continue;
+        float v[32];
+        tmem_ld32(tmem + lane_base + C::O_COL + cc, v);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const int64_t at = ct.base[r0 + k];
+          if (at < 0) continue;
+          if (slot < 0) p.oc[at + n] = __float2bfloat16_rn(v[k] * ct.col[r0 + k]);
+          else p.part[at + n] = v[k];
+        }
+      }
+      tc_fence_before();
+      ++nseg;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ct.seg_empty[ss]);
+    }
+    tc_fence_before();
+  }
+
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// Merge of the units that were cut: CTA (x, y) takes every gridDim.y-th row
+// group of the unit whose first piece CTA x computed.
+//   o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,   M = max_s m_s
+template <int RANK>
+__global__ void __launch_bounds__(256) latent_merge_kernel(const __grid_constant__ AbsParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const int x = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ht = x % p.HT;
+  const int pieces = p.rec[x * 8], t0 = p.rec[x * 8 + 1], toks = p.rec[x * 8 + 2];
+  if (pieces == 0) return;
+  // piece 0 in slot 2 x + 1, piece s > 0 in slot 2 (x + s HT)
+  auto src = [&](int s, int row) {
+    return p.part + (static_cast<int64_t>(s == 0 ? 2 * x + 1 : 2 * (x + s * p.HT)) * 64 + row) * (RANK + 4);
+  };
+  constexpr int PER = RANK / 128;   // float4s of a lane: columns 4 (lane + 32 k)
+  for (int row = blockIdx.y * 8 + warp; row < toks * p.Hc; row += gridDim.y * 8) {
+    const int head = ht * p.Hc + row % p.Hc;
+    if (head >= p.H) continue;
+    float M = -INFINITY;
+    for (int s = lane; s < pieces; s += 32) M = fmaxf(M, src(s, row)[RANK]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float L = 0.f;
+    float4 acc[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < pieces; ++s) {
+      const float *f = src(s, row);
+      const float2 ml = *reinterpret_cast<const float2 *>(f + RANK);
+      const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+      // (a sum that is NaN says that the row saw one; a piece of which it saw
+      // nothing has a sum of 0)
+      L += ml.x == -INFINITY ? ml.y : w * ml.y;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        const float4 v = reinterpret_cast<const float4 *>(f)[lane + 32 * k];
+        acc[k].x = fmaf(w, v.x, acc[k].x);
+        acc[k].y = fmaf(w, v.y, acc[k].y);
+        acc[k].z = fmaf(w, v.z, acc[k].z);
+        acc[k].w = fmaf(w, v.w, acc[k].w);
+      }
+    }
+    const float inv = 1.f / L;
+    uint2 *dst = reinterpret_cast<uint2 *>(p.oc + (static_cast<int64_t>(t0 + row / p.Hc) * p.H + head) * RANK);
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+      dst[lane + 32 * k] = make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv), pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+  }
+}
+
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+template <int KC, int BN, bool BMN>
+cudaError_t launch_head_gemm(const void *A, int64_t a_heads, int64_t a_row, const void *W, int64_t w_rows, int64_t w_cols,
+                             const HeadParams &p, cudaStream_t st) {
+  using C = HeadCfg<KC, BN, BMN>;
+  CUtensorMap ta, tb;
+  const uint64_t da[3] = {static_cast<uint64_t>(a_row), static_cast<uint64_t>(a_heads), static_cast<uint64_t>(p.T)};
+  const uint64_t sa[2] = {static_cast<uint64_t>(a_row) * 2, static_cast<uint64_t>(a_row) * 2 * a_heads};
+  const uint32_t ba[3] = {64, 1, 128};
+  cudaError_t e = encode_tmap(&ta, A, 3, da, sa, ba);
+  if (e == cudaSuccess) e = encode_tmap_2d(&tb, W, w_cols, w_rows, w_cols * 2, 64, BMN ? 64 : BN);
+  if (e == cudaSuccess) e = ensure_max_smem(reinterpret_cast<const void *>(head_gemm_kernel<KC, BN, BMN>), C::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(head_gemm_kernel<KC, BN, BMN>, dim3(p.N / BN, p.H, (p.T + 127) / 128), dim3(128), C::SMEM, st, 1, ta, tb, p);
+}
+
+template <int RANK>
+cudaError_t launch_attention(const LatentArgs &a, AbsParams &p, const void *qc, cudaStream_t st) {
+  using C = AbsCfg<RANK>;
+  const uint64_t H = a.H, T = a.T, R = RANK, W = RANK + kLatentRope;
+  CUtensorMap tq, tr, tk;
+  const uint64_t dq[3] = {R, H, T}, sq[2] = {R * 2, R * 2 * H};
+  const uint64_t dr[3] = {kLatentRope, H, T}, sr[2] = {kLatentRope * 2, kLatentRope * 2 * H};
+  const uint32_t bq[3] = {64, static_cast<uint32_t>(p.Hc), static_cast<uint32_t>(p.NT)};
+  const uint64_t dk[5] = {64, 8, C::NC, kPage / 8, static_cast<uint64_t>(a.num_pages)};
+  const uint64_t sk[4] = {W * 2, 128, 8 * W * 2, kPage * W * 2};
+  const uint32_t bk[5] = {64, 8, C::NC, kPage / 8, 1};
+  cudaError_t e = encode_tmap(&tq, qc, 3, dq, sq, bq);
+  if (e == cudaSuccess) e = encode_tmap(&tr, a.q_rope, 3, dr, sr, bq);
+  if (e == cudaSuccess) e = encode_tmap_5d(&tk, a.pool, dk, sk, bk);
+  if (e == cudaSuccess) e = ensure_max_smem(reinterpret_cast<const void *>(latent_attention_kernel<RANK>), C::SMEM);
+  if (e != cudaSuccess) return e;
+  const int ctas = std::min(device_sm_count(), kMaxCtas) / p.HT * p.HT;
+  e = launch_pdl(latent_attention_kernel<RANK>, dim3(ctas), dim3(C::THREADS), C::SMEM, st, 1, tq, tr, tk, p);
+  if (e == cudaSuccess) e = launch_pdl(latent_merge_kernel<RANK>, dim3(ctas, 4), dim3(256), 0, st, 1, p);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t latent_append_run(const LatentAppendArgs &a, cudaStream_t st) {
+  AppendParams p;
+  p.ckv = static_cast<const __nv_bfloat16 *>(a.ckv);
+  p.q = static_cast<const __nv_bfloat16 *>(a.q);
+  p.gain = static_cast<const __nv_bfloat16 *>(a.gain);
+  p.pool = static_cast<__nv_bfloat16 *>(a.pool);
+  p.q_rope = static_cast<__nv_bfloat16 *>(a.q_rope);
+  p.tok_pos = a.tok_pos;
+  p.tok_slot = a.tok_slot;
+  p.ld = a.ld;
+  p.num_pages = a.num_pages;
+  p.H = a.H;
+  p.q_row = a.hd + kLatentRope;
+  p.hd = a.hd;
+  p.rank = a.rank;
+  p.eps = a.eps;
+  p.err = a.err;
+  for (int i = 0; i < kRopeHalf; ++i) {
+    const double f = std::pow(static_cast<double>(a.theta), -2.0 * i / kLatentRope);
+    p.f_hi[i] = static_cast<float>(f);
+    p.f_lo[i] = static_cast<float>(f - static_cast<double>(p.f_hi[i]));
+  }
+  return launch_pdl(latent_append_kernel, dim3(a.T), dim3(kAppendThreads), 0, st, 1, p);
+}
+
+// q through W_uk [T][H][rank], sum_j p_j c_j [T][H][rank], which rows are live [T], the records, the partials
+size_t latent_attention_workspace_bytes(int64_t T, int64_t H, int64_t rank) {
+  return 2 * align256(static_cast<size_t>(T) * H * rank * 2) + align256(T) + kRecBytes +
+         static_cast<size_t>(2) * kMaxCtas * 64 * (rank + 4) * sizeof(float);
+}
+
+cudaError_t latent_attention_run(const LatentArgs &a, cudaStream_t st) {
+  uint8_t *w = static_cast<uint8_t *>(a.workspace);
+  const size_t rows = align256(static_cast<size_t>(a.T) * a.H * a.rank * 2);
+  __nv_bfloat16 *qc = reinterpret_cast<__nv_bfloat16 *>(w), *oc = reinterpret_cast<__nv_bfloat16 *>(w + rows);
+  uint8_t *live = w + 2 * rows;
+  AbsParams p;
+  p.oc = oc;
+  p.pool = static_cast<const __nv_bfloat16 *>(a.pool);
+  p.qo_indptr = a.qo_indptr;
+  p.kv_len = a.kv_len;
+  p.bt_indptr = a.bt_indptr;
+  p.bt = a.bt;
+  p.n_reqs = a.n_reqs;
+  p.T = a.T;
+  p.H = a.H;
+  p.HT = (a.H + 63) / 64;
+  p.Hc = (a.H + p.HT - 1) / p.HT;
+  p.NT = 64 / p.Hc;
+  p.N = (p.NT * p.Hc + 15) / 16 * 16;
+  p.num_pages = a.num_pages;
+  p.scale_log2 = a.scale * kLog2e;
+  p.rec = reinterpret_cast<int32_t *>(live + align256(a.T));
+  p.part = reinterpret_cast<float *>(live + align256(a.T) + kRecBytes);
+  p.err = a.err;
+  HeadParams h;
+  h.C = qc;
+  h.live = live;
+  h.qo_indptr = a.qo_indptr;
+  h.kv_len = a.kv_len;
+  h.bt_indptr = a.bt_indptr;
+  h.n_reqs = a.n_reqs;
+  h.T = a.T;
+  h.H = a.H;
+  h.N = a.rank;
+  h.a_col = 0;
+  h.b_row = 0;
+  h.b_rows = 2 * a.hd;
+  h.err = a.err;
+  const int64_t w_rows = static_cast<int64_t>(a.H) * 2 * a.hd;
+  cudaError_t e = a.hd == 128 ? launch_head_gemm<2, 128, true>(a.q, a.H, a.hd + kLatentRope, a.w_kv, w_rows, a.rank, h, st)
+                              : launch_head_gemm<1, 128, true>(a.q, a.H, a.hd + kLatentRope, a.w_kv, w_rows, a.rank, h, st);
+  if (e == cudaSuccess) e = a.rank == 512 ? launch_attention<512>(a, p, qc, st) : launch_attention<256>(a, p, qc, st);
+  if (e != cudaSuccess) return e;
+  h.C = static_cast<__nv_bfloat16 *>(a.o);
+  h.N = a.hd;
+  h.b_row = a.hd;
+  return a.rank == 512 ? launch_head_gemm<8, 64, false>(oc, a.H, a.rank, a.w_kv, w_rows, a.rank, h, st)
+                       : launch_head_gemm<4, 64, false>(oc, a.H, a.rank, a.w_kv, w_rows, a.rank, h, st);
+}
+
+}  // namespace mb

@@ -1,0 +1,87 @@
+// Device helpers shared by the latent-cache kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cstdint>
+
+#include "mb_kernels.h"
+#include "mb_ptx.cuh"
+
+namespace mb {
+namespace dev {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kMaxKeys = 1 << 24;   // keys of one request
+
+// A request's words of the descriptor.
+struct ReqWords {
+  int q0, q1, kv, b0, b1;
+};
+__device__ __forceinline__ ReqWords load_req(const int32_t *qo_indptr, const int32_t *kv_len, const int32_t *bt_indptr, int r) {
+  return {qo_indptr[r], qo_indptr[r + 1], kv_len[r], bt_indptr[r], bt_indptr[r + 1]};
+}
+// (compared before they are subtracted: the words may be anything)
+__device__ __forceinline__ bool req_ok(const ReqWords &w, int T) {
+  return w.q0 >= 0 && w.q1 >= w.q0 && w.q1 <= T && w.b0 >= 0 && w.b1 >= w.b0 && w.kv >= w.q1 - w.q0 && w.kv <= kMaxKeys &&
+         (w.kv + kPage - 1) / kPage <= w.b1 - w.b0;
+}
+
+// max(a, b, c) in one instruction.
+__device__ __forceinline__ float max3f(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// p = 2^(s scale + negm) of N logits, as bf16 pairs, added into `sum`.
+template <int N>
+__device__ __forceinline__ void probs(const float (&sv)[N], float2 sc2, float negm, uint32_t (&pk)[N / 2], float2 &sum) {
+  const float2 nm = make_float2(negm, negm);
+#pragma unroll
+  for (int c = 0; c < N; c += 2) {
+    const float2 x = __ffma2_rn(make_float2(sv[c], sv[c + 1]), sc2, nm);
+    const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+    sum = __fadd2_rn(sum, make_float2(p0, p1));
+    pk[c / 2] = pack_bf16x2(p0, p1);
+  }
+}
+
+// One lane of a converged warp (the same one each time).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
+  return is != 0;
+}
+
+__device__ __noinline__ int64_t div64(int64_t a, int64_t b) { return a / b; }
+
+// Zeroes a row of CHUNKS 64-wide chunks (1 KB apart) of a swizzled stage if
+// `stale`, or if it holds an infinity or a NaN (then true).
+template <int CHUNKS>
+__device__ __noinline__ bool wipe_row(uint8_t *row, bool stale) {
+  bool odd = false;
+  if (!stale) {
+    uint32_t special = 0;
+#pragma unroll 1
+    for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(row + c * 1024 + ((k + threadIdx.x) & 7) * 16);
+        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          special |= ((y[e] & 0x7F80u) == 0x7F80u || (y[e] & 0x7F800000u) == 0x7F800000u) ? 1u : 0u;
+      }
+    odd = special != 0;
+  }
+  if (stale || odd)
+#pragma unroll 1
+    for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        *reinterpret_cast<uint4 *>(row + c * 1024 + ((k + threadIdx.x) & 7) * 16) = make_uint4(0, 0, 0, 0);
+  return odd;
+}
+
+}  // namespace dev
+}  // namespace mb
