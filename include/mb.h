@@ -575,6 +575,19 @@ mb_status mb_latent_attention(const void *q, const void *q_rope, const void *w_k
                               const int32_t *bt_indptr, const int32_t *bt, void *workspace, void *stream);
 int64_t mb_latent_attention_workspace_bytes(int32_t T, int32_t n_heads, int32_t rank);
 
+/* The same attention in the expanded form, for prompt chunks: every head's keys
+ * and values are made from the requests' vectors once per call, then attended
+ * to.  kv_tokens: at least the sum of kv_len over the requests with tokens (at
+ * most 2^27); it sizes the workspace, and requests that do not fit record
+ * MB_EDEVICE and are left alone, with those behind them. */
+mb_status mb_latent_prefill(const void *q, const void *q_rope, const void *w_kv, const void *pool, void *o,
+                            int32_t num_pages, int32_t n_heads, int32_t head_dim, int32_t rank, float scale,
+                            int32_t num_reqs, int32_t T, const int32_t *qo_indptr, const int32_t *kv_len,
+                            const int32_t *bt_indptr, const int32_t *bt, int32_t kv_tokens, void *workspace,
+                            void *stream);
+int64_t mb_latent_prefill_workspace_bytes(int32_t kv_tokens, int32_t num_reqs, int32_t n_heads, int32_t head_dim,
+                                          int32_t rank);
+
 /* Adaptive chunk size (llm-stack-book 7.8, "Priority and Preemption Policies",
  * adaptive_chunk_size, and its exercise 4, which applies it in schedule()):
  * from the next mb_sched_pack on, every prefill chunk of a step is capped at

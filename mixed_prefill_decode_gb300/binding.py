@@ -110,6 +110,8 @@ _SIGS = {
     "mb_latent_append": (_I32, [_VP, _I64] + [_VP] * 6 + [_I32] * 5 + [ctypes.c_float] * 2 + [_VP]),
     "mb_latent_attention": (_I32, [_VP] * 5 + [_I32] * 4 + [ctypes.c_float] + [_I32] * 2 + [_VP] * 6),
     "mb_latent_attention_workspace_bytes": (_I64, [_I32] * 3),
+    "mb_latent_prefill": (_I32, [_VP] * 5 + [_I32] * 4 + [ctypes.c_float] + [_I32] * 2 + [_VP] * 4 + [_I32] + [_VP] * 2),
+    "mb_latent_prefill_workspace_bytes": (_I64, [_I32] * 5),
     "mb_sched_counts": (_I32, [_VP, c_int32_p]),
     "mb_sched_save": (_I32, [_VP, c_int64_p, _I64, c_int64_p]),
     "mb_sched_load": (_I32, [c_int64_p, _I64, ctypes.POINTER(_VP)]),
@@ -414,6 +416,18 @@ def mb_latent_attention(q, q_rope, w_kv, pool, o, num_pages: int, n_heads: int, 
 
 def mb_latent_attention_workspace_bytes(T: int, n_heads: int, rank: int) -> int:
     return int(lib().mb_latent_attention_workspace_bytes(T, n_heads, rank))
+
+
+def mb_latent_prefill(q, q_rope, w_kv, pool, o, num_pages: int, n_heads: int, head_dim: int, rank: int, scale: float,
+                      num_reqs: int, T: int, qo_indptr, kv_len, bt_indptr, bt, kv_tokens: int, workspace,
+                      stream=None) -> None:
+    _check(lib().mb_latent_prefill(_ptr(q), _ptr(q_rope), _ptr(w_kv), _ptr(pool), _ptr(o), num_pages, n_heads, head_dim,
+                                   rank, scale, num_reqs, T, _ptr(qo_indptr), _ptr(kv_len), _ptr(bt_indptr), _ptr(bt),
+                                   kv_tokens, _ptr(workspace), _ptr(stream)))
+
+
+def mb_latent_prefill_workspace_bytes(kv_tokens: int, num_reqs: int, n_heads: int, head_dim: int, rank: int) -> int:
+    return int(lib().mb_latent_prefill_workspace_bytes(kv_tokens, num_reqs, n_heads, head_dim, rank))
 
 
 # ------------------------------------------------------------- scheduler

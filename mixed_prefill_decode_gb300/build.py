@@ -22,7 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libmb.so")
 SOURCES = ["mb_api.cpp", "mb_sched.cpp", "mb_gemm.cu", "mb_attn.cu", "mb_elem.cu", "mb_tree.cu",
-           "mb_verify.cu", "mb_pages.cu", "mb_tables.cu", "mb_latent.cu"]
+           "mb_verify.cu", "mb_pages.cu", "mb_tables.cu", "mb_latent.cu", "mb_latent_prefill.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1575,6 +1575,34 @@ mb_status mb_latent_attention(const void *q, const void *q_rope, const void *w_k
   return MB_OK;
 }
 
+int64_t mb_latent_prefill_workspace_bytes(int32_t kv_tokens, int32_t num_reqs, int32_t n_heads, int32_t head_dim,
+                                          int32_t rank) {
+  if (kv_tokens < 0 || num_reqs < 0 || n_heads <= 0 || head_dim <= 0 || rank <= 0) return 0;
+  return static_cast<int64_t>(mb::latent_prefill_workspace_bytes(kv_tokens, num_reqs, n_heads, head_dim, rank));
+}
+
+mb_status mb_latent_prefill(const void *q, const void *q_rope, const void *w_kv, const void *pool, void *o,
+                            int32_t num_pages, int32_t n_heads, int32_t head_dim, int32_t rank, float scale,
+                            int32_t num_reqs, int32_t T, const int32_t *qo_indptr, const int32_t *kv_len,
+                            const int32_t *bt_indptr, const int32_t *bt, int32_t kv_tokens, void *workspace,
+                            void *stream) {
+  mb::LatentArgs a = {q, q_rope, w_kv, pool, o, qo_indptr, kv_len, bt_indptr, bt, num_reqs, T, n_heads, head_dim, rank,
+                      num_pages, scale, workspace, nullptr, kv_tokens};
+  if (kv_tokens < 0) return fail(MB_EINVAL, "mb_latent_prefill: kv_tokens < 0");
+  if (kv_tokens > 1 << 27) return fail(MB_EUNSUPPORTED, "mb_latent_prefill: kv_tokens > 2^27");
+  if (num_reqs > 1 << 20) return fail(MB_EUNSUPPORTED, "mb_latent_prefill: num_reqs > 2^20");
+  mb_status st = check_latent_attention("mb_latent_prefill", a,
+                                        mb_latent_prefill_workspace_bytes(kv_tokens, num_reqs, n_heads, head_dim, rank));
+  if (st != MB_OK || num_reqs == 0 || T == 0) return st;
+  mb::DeviceCtx *ctx = nullptr;
+  st = mb::device_ctx(&ctx);
+  if (st != MB_OK) return st;
+  a.err = ctx->err;
+  const cudaError_t e = mb::latent_prefill_run(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return mb::cuda_fail(e, "mb_latent_prefill");
+  return MB_OK;
+}
+
 // ------------------------------------------------------------------ step
 mb_status mb_step(mb_layer *L, mb_kv *kv, const mb_batch *b, const void *x_in, void *x_out, void *stream) {
   return mb_step_tree(L, kv, b, nullptr, x_in, x_out, stream);

@@ -53,7 +53,7 @@ __device__ __forceinline__ bool elect_one() {
   return is != 0;
 }
 
-__device__ __noinline__ int64_t div64(int64_t a, int64_t b) { return a / b; }
+static __device__ __noinline__ int64_t div64(int64_t a, int64_t b) { return a / b; }
 
 // Zeroes a row of CHUNKS 64-wide chunks (1 KB apart) of a swizzled stage if
 // `stale`, or if it holds an infinity or a NaN (then true).

@@ -1,0 +1,1259 @@
+// Latent attention of prompt chunks, in the expanded form: a cached token's
+// keys and values are made for every head from its vector, once, and its
+// request's tokens attend to them causally,
+//
+//   K_h = C W_uk,h^T,  V_h = C W_uv,h^T   (C: the request's vectors, kv x rank)
+//   o_i = sum_{j <= c + i} p_ij V_h,j,    p_i = softmax_j (scale (q_nope,i . K_h,j + q_rope,i . k_j))
+//
+// Making a key and a value costs 4 hd rank operations, attending to them
+// 2 (2 hd + 64) for each token that does, against 2 (2 rank + 64) in the
+// absorbed form: from about a hundred tokens on this form does less.
+//
+// What bounds it: the tensor cores, and beside them the chain of product,
+// softmax, product.  Keys and values of a head are 4 hd bytes a token; the heads
+// are taken in groups whose keys and values fit well inside L2, so they are
+// written, and read by every tile of queries, without going to HBM.
+//
+// Two kernels per group of heads, and a merge:
+//  * expand: 128 cached rows (8 pages, copied once by TMA) stay in shared memory
+//    as the A operand while the heads' weights stream past: M = 128 keys, N =
+//    2 hd (a head's key and value rows), K = rank.
+//  * attention: a unit is 256 tokens of a request and one head, as two 128-row
+//    query tiles that share the staged keys and values; S = Q K^T with K = hd +
+//    64, softmax with one thread per row, O += P V with P in TMEM.  Two groups of
+//    four softmax warps take turns, one per tile (with one tile: its even and its
+//    odd blocks), so products run during the other group's softmax.
+//  * merge: units cut by the schedule's borders, by log-sum-exp.
+//
+// The schedule: all units lie on one line, weighted by their blocks, and CTA w
+// of W takes the w-th of W equal parts, whatever the lengths; it is worked out
+// by every CTA from the device descriptor.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "mb_latent.h"
+#include "mb_latent_dev.cuh"
+#include "mb_launch.cuh"
+#include "mb_ptx.cuh"
+#include "mb_spec.h"
+
+namespace mb {
+namespace {
+
+using namespace dev;
+
+constexpr int kMaxCtas = 160;      // CTAs of an attention launch at most; sizes the workspace
+constexpr int kRecBytes = 8192;    // workspace: one record of 8 ints per CTA, then the partials
+constexpr int kBlk = 128;          // keys of a block
+constexpr int kGroupBytes = 48 << 20;   // keys and values of a group of heads at most (of one head, whatever it takes)
+// The schedule's weights: a block of one query tile, a block of two, a unit's
+// start and end, and the least a CTA takes (at least kCost2, so that no CTA
+// between the first and the last of a unit is left without a block).
+constexpr int kCost1 = 2, kCost2 = 3, kCostUnit = 5, kMinShare = 3;
+
+struct PreParams {
+  __nv_bfloat16 *kv;             // [heads of the group][rows][2 hd]: a head's keys and values
+  __nv_bfloat16 *o;
+  const int32_t *qo_indptr, *kv_len, *bt_indptr, *bt;
+  int n_reqs, T, H, h0, HG, num_pages;   // heads h0 .. h0 + HG - 1
+  int cap_blocks;                // blocks of 128 rows that kv has room for
+  float scale_log2;
+  int32_t *rec;
+  float *part;                   // [2 slots per CTA][256 rows][hd + 4]: o, m, l, pad
+  int *err;
+};
+
+// A request's blocks of keys (none if it has no tokens, or breaks a rule).
+__device__ __forceinline__ int key_blocks(const ReqWords &w, int T, bool *bad) {
+  *bad = !req_ok(w, T);
+  return *bad || w.q1 == w.q0 ? 0 : (w.kv + kBlk - 1) / kBlk;
+}
+
+// Sums over the CTA's threads: this thread's exclusive prefix, and the total.
+template <int WARPS>
+__device__ __forceinline__ int64_t cta_scan(int64_t mine, int64_t *sums, int64_t *total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t inc = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, inc, off);
+    if (lane >= off) inc += v;
+  }
+  __syncthreads();   // sums may still be read from the scan before
+  if (lane == 31) sums[warp] = inc;
+  __syncthreads();
+  int64_t pre = inc - mine, all = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) pre += sums[w];
+    all += sums[w];
+  }
+  *total = all;
+  return pre;
+}
+
+// ------------------------------------------------------------------ expand
+template <int HD, int RANK>
+struct ExpCfg {
+  static constexpr int NC = RANK / 64 + 1;
+  static constexpr int ATOM = NC * 1024;
+  static constexpr int PAGE_BYTES = 2 * ATOM;
+  static constexpr int A_BYTES = (kBlk / 8) * ATOM;
+  static constexpr int N = 2 * HD;
+  static constexpr int B_STAGE = N * 128;             // 64 of rank
+  static constexpr int KC = RANK / 64;
+  static constexpr int NB = HD == 128 && RANK == 512 ? 2 : 4;
+  static constexpr int OFF_B = A_BYTES;
+  static constexpr int OFF_CTRL = OFF_B + NB * B_STAGE;
+  static constexpr int SMEM = OFF_CTRL + 512;
+  static constexpr int THREADS = 192;                 // TMA, MMA, 4 epilogue warps
+  static constexpr uint32_t IDESC = idesc_bf16(128, N, false);
+};
+
+template <int HD, int RANK>
+struct ExpCtrl {
+  using C = ExpCfg<HD, RANK>;
+  uint64_t a_full, a_empty, b_full[C::NB], b_empty[C::NB], t_full[2], t_empty[2], done;
+  int64_t sums[C::THREADS / 32];
+  int64_t start_base;
+  int32_t start_req;
+  uint32_t tmem;
+  int abort;
+};
+
+__device__ __forceinline__ void store32(void *dst, const uint32_t *v) {   // 32 bytes: a whole sector
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map), "r"(smem_u32(src)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+
+template <int HD, int RANK>
+__global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
+    latent_expand_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmW,
+                         const __grid_constant__ CUtensorMap tmR, const __grid_constant__ PreParams p) {
+  using C = ExpCfg<HD, RANK>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t *sA = smem, *sB = smem + C::OFF_B;
+  static_assert(sizeof(ExpCtrl<HD, RANK>) <= 512 && C::SMEM <= 232448, "shared memory");
+  ExpCtrl<HD, RANK> &ct = *reinterpret_cast<ExpCtrl<HD, RANK> *>(smem + C::OFF_CTRL);
+  volatile int *abort_flag = &ct.abort;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;   // (known uniform)
+  if (smem_u32(smem) & 1023u) {   // the swizzled layouts need a 1024-aligned base
+    pdl_wait();
+    if (threadIdx.x == 0) atomicExch(p.err, kErrBounds);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    mbar_init(&ct.a_full, 1);
+    mbar_init(&ct.a_empty, 1);
+    for (int s = 0; s < C::NB; ++s) {
+      mbar_init(&ct.b_full[s], 1);
+      mbar_init(&ct.b_empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&ct.t_full[b], 1);
+      mbar_init(&ct.t_empty[b], 128);
+    }
+    mbar_init(&ct.done, 1);
+    ct.abort = 0;
+    ct.start_req = -1;
+    fence_mbar_init();
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmW);
+    prefetch_tmap(&tmR);
+  }
+  if (warp == 1) {
+    tmem_alloc(&ct.tmem, 512);
+    tmem_relinquish();
+  }
+  pdl_wait();   // descriptor, cache, weights and workspace belong to earlier kernels of the stream
+  pdl_trigger();
+
+  // ---- this CTA's items: (block of 128 keys, head), heads fastest
+  const int per = (p.n_reqs + C::THREADS - 1) / C::THREADS;
+  const int r_lo = min(p.n_reqs, static_cast<int>(threadIdx.x) * per), r_hi = min(p.n_reqs, r_lo + per);
+  int64_t mine = 0, total;
+  for (int r = r_lo; r < r_hi; ++r) {
+    bool bad;
+    mine += key_blocks(load_req(p.qo_indptr, p.kv_len, p.bt_indptr, r), p.T, &bad);
+    if (bad && blockIdx.x == 0) atomicExch(p.err, kErrBounds);
+  }
+  tc_fence_before();
+  int64_t pre = cta_scan<C::THREADS / 32>(mine, ct.sums, &total);   // (synchronises: TMEM's address is there)
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ct.tmem, 0);
+  if (total > p.cap_blocks) {
+    // the caller's room is too small for the requests behind: they are left alone
+    if (threadIdx.x == 0 && blockIdx.x == 0) atomicExch(p.err, kErrBounds);
+    total = p.cap_blocks;
+  }
+  const int64_t items = total * p.HG, W = min(static_cast<int64_t>(gridDim.x), items);
+  const bool active = blockIdx.x < W;
+  const int64_t x0 = active ? div64(items * blockIdx.x, W) : 0, x1 = active ? div64(items * (blockIdx.x + 1), W) : 0;
+  const int64_t b0 = active ? div64(x0, p.HG) : 0;
+  if (active && pre <= b0 && b0 < pre + mine) {
+    for (int r = r_lo; r < r_hi; ++r) {
+      bool bad;
+      const int b = key_blocks(load_req(p.qo_indptr, p.kv_len, p.bt_indptr, r), p.T, &bad);
+      if (b0 < pre + b) {
+        ct.start_req = r;
+        ct.start_base = pre;
+        break;
+      }
+      pre += b;
+    }
+  }
+  __syncthreads();
+  // Walks the blocks from b0 on: the request of block `blk` and its first key there.
+  struct Walk {
+    int r;
+    int64_t base;   // the request's first block
+    ReqWords w;
+    int blocks;
+  };
+  auto start = [&]() {
+    Walk k;
+    bool bad;
+    k.r = ct.start_req;
+    k.base = ct.start_base;
+    k.w = load_req(p.qo_indptr, p.kv_len, p.bt_indptr, k.r);
+    k.blocks = key_blocks(k.w, p.T, &bad);
+    return k;
+  };
+  auto reach = [&](Walk &k, int64_t blk) {
+    bool bad;
+    while (blk >= k.base + k.blocks && k.r + 1 < p.n_reqs) {
+      k.base += k.blocks;
+      k.w = load_req(p.qo_indptr, p.kv_len, p.bt_indptr, ++k.r);
+      k.blocks = key_blocks(k.w, p.T, &bad);
+    }
+  };
+
+  if (!active) {
+  } else if (warp == 0) {
+    // -------------------------------------------------------- TMA producer
+    Walk k = start();
+    int ause = 0, bcnt = 0;
+    bool ok = true;
+    int64_t blk = b0;
+    int hg = static_cast<int>(x0 - b0 * p.HG);
+    for (int64_t i = x0; i < x1 && ok; ++i) {
+      if (i == x0 || hg == 0) {
+        reach(k, blk);
+        const int j = static_cast<int>(blk - k.base), n_pages = (k.w.kv + kPage - 1) / kPage, np = min(8, n_pages - 8 * j);
+        int page = lane < np ? p.bt[k.w.b0 + 8 * j + lane] : 0;
+        if (lane < np && (page < 0 || page >= p.num_pages)) {
+          atomicExch(p.err, kErrBounds);
+          page = 0;
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(&ct.a_empty, (ause & 1) ^ 1, abort_flag, p.err, kErrWaitProducer));
+        if (!ok) break;
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the keys' copies below have left the stage
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(&ct.a_full, np * C::PAGE_BYTES);
+        __syncwarp();
+        if (lane < np) tma_load_5d(sA + lane * C::PAGE_BYTES, &tmK, &ct.a_full, 0, 0, 0, 0, page);
+        ++ause;
+      }
+      for (int c = 0; c < C::KC && ok; ++c, ++bcnt) {
+        const int st = bcnt % C::NB;
+        if (lane == 0) {
+          ok = mbar_wait(&ct.b_empty[st], ((bcnt / C::NB) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer);
+          if (ok) {
+            mbar_arrive_expect_tx(&ct.b_full[st], C::B_STAGE);
+            tma_load_2d(sB + st * C::B_STAGE, &tmW, &ct.b_full[st], 64 * c, (p.h0 + hg) * 2 * HD);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+      }
+      if (ok && p.h0 + hg == 0) {
+        // the rotated keys, once per call, as one row of 64 per token (what lies
+        // behind the request's last key is never attended to)
+        ok = __all_sync(0xffffffffu, mbar_wait(&ct.a_full, (ause - 1) & 1, abort_flag, p.err, kErrWaitProducer));
+        if (ok && lane < kBlk / 8) tma_store_2d(&tmR, sA + lane * C::ATOM + C::KC * 1024, 0, static_cast<int>(blk) * kBlk + 8 * lane);
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      }
+      if (++hg == p.HG) {
+        hg = 0;
+        ++blk;
+      }
+    }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (!ok || *abort_flag) {   // let copies in flight land before the CTA exits (bounded)
+      const uint64_t t_start = globaltimer();
+      auto drain = [&](uint64_t *bar, int use) {
+        while (!mbar_try_wait(smem_u32(bar), use & 1) && globaltimer() - t_start < kWaitLimitNs) {
+        }
+      };
+      if (lane == 0) {
+        for (int b = max(0, bcnt - C::NB); b < bcnt; ++b) drain(&ct.b_full[b % C::NB], b / C::NB);
+        if (ause > 0) drain(&ct.a_full, ause - 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      const uint64_t ad0 = sdesc_sw128(smem_u32(sA), 16, C::ATOM);
+      const uint64_t bd0 = sdesc_sw128(smem_u32(sB), 16, 1024);
+      auto wait = [&](uint64_t *bar, uint32_t par) { return mbar_wait(bar, par, abort_flag, p.err, kErrWaitMma); };
+      int ause = 0, bcnt = 0, acc = 0;
+      int hg = static_cast<int>(x0 - b0 * p.HG);
+      bool ok = true;
+      for (int64_t i = x0; i < x1 && ok; ++i, ++acc) {
+        if (i == x0 || hg == 0) {
+          ok = wait(&ct.a_full, ause & 1);
+          ++ause;
+        }
+        ok = ok && wait(&ct.t_empty[acc & 1], ((acc >> 1) & 1) ^ 1);
+        for (int c = 0; c < C::KC && ok; ++c, ++bcnt) {
+          const int st = bcnt % C::NB;
+          ok = wait(&ct.b_full[st], (bcnt / C::NB) & 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_bf16(tmem + 256 * (acc & 1), ad0 + ((c * 1024 + kk * 32) >> 4), bd0 + ((st * C::B_STAGE + kk * 32) >> 4),
+                     C::IDESC, (c > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&ct.b_empty[st]);
+        }
+        if (!ok) break;
+        mma_commit(&ct.t_full[acc & 1]);
+        if (++hg == p.HG) {
+          hg = 0;
+          mma_commit(&ct.a_empty);
+        }
+      }
+      // every MMA issued above has completed before TMEM is freed
+      mma_commit(&ct.done);
+      const uint64_t t_end = globaltimer();
+      while (!mbar_try_wait(smem_u32(&ct.done), 0) && globaltimer() - t_end < kWaitLimitNs) {
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    // One thread per key.  A value that is not finite would reach, times a
+    // probability of 0, tokens that do not see the key: such a value row is
+    // stored as zeros and the key as NaN, which the tokens that do see it get.
+    const int qu = warp & 3, row = qu * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(qu * 32) << 16;
+    Walk k = start();
+    int64_t blk = b0;
+    int hg = static_cast<int>(x0 - b0 * p.HG), acc = 0;
+    for (int64_t i = x0; i < x1; ++i, ++acc) {
+      if (i == x0 || hg == 0) reach(k, blk);
+      const bool fail = !mbar_wait(&ct.t_full[acc & 1], (acc >> 1) & 1, abort_flag, p.err, kErrWaitEpilogue);
+      if (__any_sync(0xffffffffu, fail)) break;   // tcgen05.ld below is warp-collective
+      tc_fence_after();
+      const bool stale = static_cast<int>(blk - k.base) * kBlk + row >= k.w.kv;
+      const uint32_t t = tmem + lane_base + 256 * (acc & 1);
+      uint8_t *dst = reinterpret_cast<uint8_t *>(p.kv + ((static_cast<int64_t>(hg) * p.cap_blocks + blk) * kBlk + row) * (2 * HD));
+      uint32_t pk[HD / 2];
+      float odd = 0.f;   // NaN if a value is not finite
+#pragma unroll
+      for (int cc = 0; cc < HD / 32; ++cc) {
+        float v[32];
+        tmem_ld32(t + HD + 32 * cc, v);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          pk[16 * cc + e / 2] = pack_bf16x2(v[e], v[e + 1]);
+          odd = fmaf(bf16lo(pk[16 * cc + e / 2]), 0.f, odd);
+          odd = fmaf(bf16hi(pk[16 * cc + e / 2]), 0.f, odd);
+        }
+      }
+      const bool wipe = stale || odd != 0.f;
+#pragma unroll
+      for (int e = 0; e < HD / 2; e += 8) {
+        if (wipe)
+#pragma unroll
+          for (int x = 0; x < 8; ++x) pk[e + x] = 0;
+        store32(dst + 2 * HD + 4 * e, pk + e);
+      }
+#pragma unroll
+      for (int cc = 0; cc < HD / 32; ++cc) {
+        float v[32];
+        tmem_ld32(t + 32 * cc, v);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          uint32_t x = pack_bf16x2(v[e], v[e + 1]);
+          if (wipe) x = stale ? 0u : 0x7FC07FC0u;
+          pk[e / 2] = x;
+        }
+        store32(dst + 64 * cc, pk);
+        store32(dst + 64 * cc + 32, pk + 8);
+      }
+      tc_fence_before();
+      mbar_arrive(&ct.t_empty[acc & 1]);
+      if (++hg == p.HG) {
+        hg = 0;
+        ++blk;
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// --------------------------------------------------------------- attention
+template <int HD>
+struct PreCfg {
+  static constexpr int UNIT = 128 * 128;              // [128 rows][64 bf16]: what the stages are made of
+  static constexpr int KU = HD / 64 + 1;              // of a block of keys (the last: their rotated part), of a query tile
+  static constexpr int VU = HD / 64;                  // of a block of values
+  static constexpr int QT_BYTES = KU * UNIT;
+  // One ring for keys and values, in the order they are used (K of a block, then
+  // its V): 128 KB hold 1.6 blocks, where rings of their own would leave values
+  // a single stage.
+  static constexpr int NU = HD == 128 ? 8 : 10;
+  static constexpr int NSEG = 4;
+  static constexpr int OFF_R = 2 * QT_BYTES;
+  static constexpr int OFF_CTRL = OFF_R + NU * UNIT;
+  static constexpr int OFF_ML = OFF_CTRL + 1024;      // (m, l) of 128 rows, from one warp group to the other
+  static constexpr int SMEM = OFF_ML + 1024;
+  static constexpr int THREADS = 320;                 // TMA, MMA, 2 x 4 softmax warps
+  static constexpr uint32_t IDESC_S = idesc_bf16(128, 128, false);
+  static constexpr uint32_t IDESC_PV = idesc_bf16(128, HD, true);
+  static constexpr uint32_t TMEM_COLS = 512;          // S/P buffers at 0 and 128, O of the two groups from 256
+  static constexpr uint32_t O_COL = 256;
+};
+
+// A piece of a unit, as the producer tells it to the other roles.
+struct PreSeg {
+  int32_t nb, j0, qt;    // blocks [j0, j0 + nb), query tiles; nb 0: no more pieces
+  int32_t t0, rows;      // first row of q, rows
+  int32_t h, first;      // head; the last key that the unit's first row sees
+  int32_t slot, qb;      // partial slot, -1: the unit is whole; Q buffer of tile 0 (tile 1: the other one)
+};
+
+struct PreReq {
+  int t0, n, c, row_blk;   // first row of q, tokens, cached tokens, first block of the workspace
+  int full, rem, a;        // units of 256 rows, rows of the last one if it is smaller, blocks of the cached tokens
+  int64_t head;            // cost of one head
+};
+
+template <int HD>
+struct PreCtrl {
+  using C = PreCfg<HD>;
+  uint64_t q_full[2], q_empty[2];
+  uint64_t full[C::NU], empty[C::NU];
+  uint64_t s_full[2], p_full[2], o_full[2];   // by warp group
+  uint64_t ml_full[2];    // the group's (m, l) are in shared memory
+  uint64_t ml_empty[2];   // the other group has read them and this group's O
+  uint64_t seg_full[C::NSEG], seg_empty[C::NSEG];
+  uint64_t done;
+  PreSeg seg[C::NSEG];
+  int64_t sums[C::THREADS / 32];
+  int64_t start_base;
+  PreReq start;
+  int32_t start_req;
+  uint32_t tmem;
+  int abort;
+};
+
+// Cost of the first u units of 256 rows of a request and head: unit k has a +
+// 2 (k + 1) blocks.
+__device__ __forceinline__ int64_t units_cost(int a, int64_t u) {
+  return u * (kCostUnit + static_cast<int64_t>(kCost2) * a) + kCost2 * u * (u + 1);
+}
+__device__ __forceinline__ int tail_blocks(const PreReq &q) { return (q.c + q.n + kBlk - 1) / kBlk; }
+
+__device__ __forceinline__ PreReq pre_req(const PreParams &p, const ReqWords &w, int64_t row_blk) {
+  PreReq q;
+  bool bad;
+  const int blocks = key_blocks(w, p.T, &bad);
+  q.t0 = w.q0;
+  q.n = blocks > 0 && row_blk + blocks <= p.cap_blocks ? w.q1 - w.q0 : 0;
+  q.c = w.kv - q.n;
+  q.row_blk = static_cast<int>(row_blk);
+  q.full = q.n / 256;
+  q.rem = q.n % 256;
+  q.a = (q.c + kBlk - 1) / kBlk;
+  q.head = q.n == 0 ? 0 : units_cost(q.a, q.full) + (q.rem ? kCostUnit + (q.rem > 128 ? kCost2 : kCost1) * static_cast<int64_t>(tail_blocks(q)) : 0);
+  return q;
+}
+
+// 32 columns at each of two addresses of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// Takes the keys behind `vis` out of a row's block of S (to -inf, in TMEM): a
+// pass of its own, for the few blocks on the diagonal.
+__device__ __forceinline__ void mask_block(uint32_t s_col, int vis) {
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    float v[32];
+    tmem_ld32(s_col + 32 * k, v);
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (32 * k + e > vis) v[e] = -INFINITY;
+    tmem_st32(s_col + 32 * k, v);
+  }
+}
+
+template <int HD>
+__global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
+    latent_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQR,
+                          const __grid_constant__ CUtensorMap tmKV, const __grid_constant__ CUtensorMap tmR,
+                          const __grid_constant__ PreParams p) {
+  using C = PreCfg<HD>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t *sQ = smem, *sR = smem + C::OFF_R;
+  static_assert(sizeof(PreCtrl<HD>) <= 1024 && C::SMEM <= 232448, "shared memory");
+  PreCtrl<HD> &ct = *reinterpret_cast<PreCtrl<HD> *>(smem + C::OFF_CTRL);
+  volatile int *abort_flag = &ct.abort;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;   // (known uniform)
+  if (smem_u32(smem) & 1023u) {   // the swizzled layouts need a 1024-aligned base
+    pdl_wait();
+    if (threadIdx.x == 0) {
+      atomicExch(p.err, kErrBounds);
+      p.rec[blockIdx.x * 8] = 0;
+    }
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&ct.q_full[b], 1);
+      mbar_init(&ct.q_empty[b], 1);
+      mbar_init(&ct.s_full[b], 1);
+      mbar_init(&ct.p_full[b], 128);
+      mbar_init(&ct.o_full[b], 1);
+      mbar_init(&ct.ml_full[b], 128);
+      mbar_init(&ct.ml_empty[b], 128);
+    }
+    for (int s = 0; s < C::NU; ++s) {
+      mbar_init(&ct.full[s], 1);
+      mbar_init(&ct.empty[s], 1);
+    }
+    for (int s = 0; s < C::NSEG; ++s) {
+      mbar_init(&ct.seg_full[s], 1);
+      mbar_init(&ct.seg_empty[s], 9);   // the MMA issuer and the 8 softmax warps
+    }
+    mbar_init(&ct.done, 1);
+    ct.abort = 0;
+    ct.start_req = -1;
+    fence_mbar_init();
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmQR);
+    prefetch_tmap(&tmKV);
+    prefetch_tmap(&tmR);
+  }
+  if (warp == 1) {
+    tmem_alloc(&ct.tmem, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  pdl_wait();   // the descriptor, queries, expanded keys and outputs belong to earlier kernels of the stream
+  pdl_trigger();
+
+  // ---- this CTA's part of the line: [x0, x1) of `total`
+  const int W_max = gridDim.x, cta = blockIdx.x;
+  const int per = (p.n_reqs + C::THREADS - 1) / C::THREADS;
+  const int r_lo = min(p.n_reqs, static_cast<int>(threadIdx.x) * per), r_hi = min(p.n_reqs, r_lo + per);
+  int64_t mine = 0, total;
+  for (int r = r_lo; r < r_hi; ++r) {
+    bool bad;
+    mine += key_blocks(load_req(p.qo_indptr, p.kv_len, p.bt_indptr, r), p.T, &bad);
+  }
+  tc_fence_before();
+  const int64_t blk0 = cta_scan<C::THREADS / 32>(mine, ct.sums, &total);   // (synchronises: TMEM's address is there)
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ct.tmem, 0);
+  auto next_blk = [&](const ReqWords &w, int64_t at) {
+    bool bad;
+    return at + key_blocks(w, p.T, &bad);
+  };
+  int64_t at = blk0;
+  mine = 0;
+  for (int r = r_lo; r < r_hi; ++r) {
+    const ReqWords w = load_req(p.qo_indptr, p.kv_len, p.bt_indptr, r);
+    mine += pre_req(p, w, at).head * p.HG;
+    at = next_blk(w, at);
+  }
+  int64_t pre = cta_scan<C::THREADS / 32>(mine, ct.sums, &total);
+  const int64_t W = total / kMinShare < 1 ? (total > 0 ? 1 : 0) : (total / kMinShare < W_max ? total / kMinShare : W_max);
+  const bool active = cta < W;
+  const int64_t x0 = active ? div64(total * cta, W) : 0, x1 = active ? div64(total * (cta + 1), W) : 0;
+  if (active && pre <= x0 && x0 < pre + mine) {
+    at = blk0;
+    for (int r = r_lo; r < r_hi; ++r) {
+      const ReqWords w = load_req(p.qo_indptr, p.kv_len, p.bt_indptr, r);
+      const PreReq q = pre_req(p, w, at);
+      if (x0 < pre + q.head * p.HG) {
+        ct.start_req = r;
+        ct.start = q;
+        ct.start_base = pre;
+        break;
+      }
+      pre += q.head * p.HG;
+      at = next_blk(w, at);
+    }
+  }
+  __syncthreads();
+
+  if (!active) {
+    if (threadIdx.x == 0) p.rec[cta * 8] = 0;
+  } else if (warp == 0) {
+    // ------------------------------------------------ schedule, TMA producer
+    if (lane == 0) {
+      int32_t rec[5] = {0, 0, 0, 0, 0};
+      int r = ct.start_req;
+      int64_t base = ct.start_base;
+      PreReq q = ct.start;
+      ReqWords w = load_req(p.qo_indptr, p.kv_len, p.bt_indptr, r);
+      int hg = static_cast<int>(div64(x0 - base, q.head));
+      base += hg * q.head;
+      int u = 0;   // the unit that x0 lies in: the last one whose start is not behind it
+      {
+        int lo = 0, hi = q.full + (q.rem ? 1 : 0);
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (units_cost(q.a, mid) <= x0 - base) lo = mid;
+          else hi = mid;
+        }
+        u = lo;
+        base += units_cost(q.a, u);
+      }
+      int cnt = 0, nseg = 0, quse[2] = {0, 0}, qsel = 0;
+      bool ok = true;
+      // a 128 x 64 part of the keys or values: columns x .. x + 63 of row y of `map`
+      auto send = [&](const CUtensorMap *map, int x, int y) {
+        const int st = cnt % C::NU;
+        if (!mbar_wait(&ct.empty[st], ((cnt / C::NU) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer)) return false;
+        mbar_arrive_expect_tx(&ct.full[st], C::UNIT);
+        tma_load_2d(sR + st * C::UNIT, map, &ct.full[st], x, y);
+        ++cnt;
+        return true;
+      };
+      while (ok && base < x1) {
+        // the unit (hg, u) of request r, on the line from `base`
+        const int rows = u < q.full ? 256 : q.rem, qt = rows > 128 ? 2 : 1, b = qt == 2 ? kCost2 : kCost1;
+        const int nkb = u < q.full ? q.a + 2 * (u + 1) : tail_blocks(q);
+        const int64_t cost = kCostUnit + static_cast<int64_t>(b) * nkb;
+        auto cut = [&](int64_t x) {   // blocks of the unit that lie before x
+          const int64_t d = x - base - kCostUnit;
+          if (d <= 0) return 0;
+          const int64_t n = qt == 2 ? (d + kCost2 - 1) / kCost2 : (d + kCost1 - 1) / kCost1;
+          return static_cast<int>(min(static_cast<int64_t>(nkb), n));
+        };
+        auto owner = [&](int j) {     // the CTA whose part holds block j: the last w with total w / W <= its place
+          return static_cast<int>(div64((base + kCostUnit + static_cast<int64_t>(b) * j + 1) * W - 1, total));
+        };
+        const int j0 = cut(x0), j1 = cut(x1);
+        if (j1 > j0) {
+          const int first = owner(0), last = owner(nkb - 1), i0 = 256 * u, h = p.h0 + hg;
+          const int krow = (hg * p.cap_blocks + q.row_blk) * kBlk, rrow = q.row_blk * kBlk;
+          for (int t = 0; t < qt && ok; ++t) {
+            const int qb = qsel ^ t;
+            ok = mbar_wait(&ct.q_empty[qb], (quse[qb] & 1) ^ 1, abort_flag, p.err, kErrWaitProducer);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&ct.q_full[qb], C::QT_BYTES);
+            for (int ch = 0; ch < C::KU - 1; ++ch)
+              tma_load_3d(sQ + qb * C::QT_BYTES + ch * C::UNIT, &tmQ, &ct.q_full[qb], ch * 64, h, q.t0 + i0 + 128 * t);
+            tma_load_3d(sQ + qb * C::QT_BYTES + (C::KU - 1) * C::UNIT, &tmQR, &ct.q_full[qb], 0, h, q.t0 + i0 + 128 * t);
+            ++quse[qb];
+          }
+          const int ss = nseg % C::NSEG;
+          ok = ok && mbar_wait(&ct.seg_empty[ss], ((nseg / C::NSEG) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer);
+          if (!ok) break;
+          PreSeg &sg = ct.seg[ss];
+          sg.nb = j1 - j0;
+          sg.j0 = j0;
+          sg.qt = qt;
+          sg.t0 = q.t0 + i0;
+          sg.rows = rows;
+          sg.h = h;
+          sg.first = q.c + i0;
+          sg.slot = first == last ? -1 : 2 * cta + (cta == first ? 1 : 0);
+          sg.qb = qsel;
+          mbar_arrive(&ct.seg_full[ss]);
+          ++nseg;
+          if (first != last && cta == first) {
+            rec[0] = last - first + 1;
+            rec[1] = q.t0 + i0;
+            rec[2] = h;
+            rec[3] = rows;
+          }
+          if (qt == 1) qsel ^= 1;
+          for (int j = j0; j < j1 && ok; ++j) {
+            for (int ch = 0; ch < C::KU - 1 && ok; ++ch) ok = send(&tmKV, 64 * ch, krow + kBlk * j);
+            if (ok) ok = send(&tmR, 0, rrow + kBlk * j);
+            for (int ch = 0; ch < C::VU && ok; ++ch) ok = send(&tmKV, HD + 64 * ch, krow + kBlk * j);
+          }
+        }
+        // the next unit on the line
+        base += cost;
+        if (++u == q.full + (q.rem ? 1 : 0)) {
+          u = 0;
+          if (++hg == p.HG) {
+            hg = 0;
+            int64_t blk = q.row_blk;
+            do {
+              blk = next_blk(w, blk);
+              if (++r >= p.n_reqs) break;
+              w = load_req(p.qo_indptr, p.kv_len, p.bt_indptr, r);
+              q = pre_req(p, w, blk);
+            } while (q.n == 0);
+            if (r >= p.n_reqs) break;
+          }
+        }
+      }
+      if (ok) {
+        const int ss = nseg % C::NSEG;
+        if (mbar_wait(&ct.seg_empty[ss], ((nseg / C::NSEG) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer)) {
+          ct.seg[ss].nb = 0;
+          mbar_arrive(&ct.seg_full[ss]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) p.rec[cta * 8 + k] = rec[k];
+      // after an abort, let copies in flight land before the CTA exits (bounded)
+      if (!ok || *abort_flag) {
+        const uint64_t t_start = globaltimer();
+        auto drain = [&](uint64_t *bar, int use) {
+          while (!mbar_try_wait(smem_u32(bar), use & 1) && globaltimer() - t_start < kWaitLimitNs) {
+          }
+        };
+        for (int i = max(0, cnt - C::NU); i < cnt; ++i) drain(&ct.full[i % C::NU], i / C::NU);
+        for (int b = 0; b < 2; ++b)
+          if (quse[b] > 0) drain(&ct.q_full[b], quse[b] - 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // --------------------------------------------------------- MMA issuer
+    // Items in order: block by block, tile by tile.  S of an item goes out
+    // as soon as its K (and Q) landed and the P V before the last one is
+    // issued (its S buffer is then free, in order); P V as soon as P is
+    // written and V landed.  S runs on into the next piece.  The whole warp
+    // keeps the books, in step, and one elected lane issues.
+    const uint64_t qd0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
+    const uint64_t kd0 = sdesc_sw128(smem_u32(sR), 16, 1024);
+    const uint64_t vd0 = sdesc_sw128(smem_u32(sR), 16, 1024);   // N chunk by chunk: one 64-wide product per unit
+    struct Cursor {
+      int seg, blk, item;      // pieces, blocks and items before it
+      int nb, qt, qb, lb, t;   // the piece, and the place in it
+      bool in;
+    };
+    Cursor s{0, 0, 0, 0, 0, 0, 0, 0, false}, v{0, 0, 0, 0, 0, 0, 0, 0, false};
+    int quse[2] = {0, 0};
+    bool s_end = false;
+    uint64_t t_idle = 0;
+    auto uni = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    auto ready = [](uint64_t *bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_test_wait(smem_u32(bar), parity)) != 0;
+    };
+    auto landed = [&](int first, int n) {   // units first .. first + n - 1 of the ring's sequence
+      for (int i = first; i < first + n; ++i)
+        if (!ready(&ct.full[i % C::NU], (i / C::NU) & 1)) return false;
+      return true;
+    };
+    auto enter = [&](Cursor &x) {
+      const PreSeg &sg = ct.seg[x.seg % C::NSEG];
+      x.nb = uni(sg.nb);
+      x.qt = uni(sg.qt);
+      x.qb = uni(sg.qb);
+      x.lb = x.t = 0;
+      x.in = true;
+    };
+    for (uint32_t spin = 1;; ++spin) {   // rounds without progress
+      bool progress = false;
+      if (!s_end && s.item < v.item + 2) {
+        if (!s.in && ready(&ct.seg_full[s.seg % C::NSEG], (s.seg / C::NSEG) & 1)) {
+          enter(s);
+          if (s.nb == 0) s_end = true;
+        }
+        if (s.in && !s_end) {
+          const int qb = s.qb ^ s.t, k0 = s.blk * (C::KU + C::VU);
+          if ((s.lb > 0 || ready(&ct.q_full[qb], quse[qb] & 1)) && landed(k0, C::KU)) {
+            tc_fence_after();
+            const uint32_t d = tmem + 128 * (s.item & 1);
+            const uint64_t qd = qd0 + static_cast<uint64_t>((qb * C::QT_BYTES) >> 4);
+            const bool last = s.lb == s.nb - 1, k_done = s.t + 1 == s.qt;
+            if (elect_one()) {
+#pragma unroll
+              for (int ch = 0; ch < C::KU; ++ch) {
+                const uint64_t kd = kd0 + static_cast<uint64_t>((((k0 + ch) % C::NU) * C::UNIT) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  mma_bf16(d, qd + ((ch * C::UNIT + kk * 32) >> 4), kd + ((kk * 32) >> 4), C::IDESC_S,
+                           (ch > 0 || kk > 0) ? 1u : 0u);
+              }
+              mma_commit(&ct.s_full[s.item & 1]);
+              if (last) mma_commit(&ct.q_empty[qb]);
+              if (k_done)
+#pragma unroll
+                for (int ch = 0; ch < C::KU; ++ch) mma_commit(&ct.empty[(k0 + ch) % C::NU]);
+            }
+            __syncwarp();
+            if (last) ++quse[qb];
+            ++s.item;
+            if (++s.t == s.qt) {
+              s.t = 0;
+              ++s.blk;
+              if (++s.lb == s.nb) {
+                s.in = false;
+                ++s.seg;
+              }
+            }
+            progress = true;
+          }
+        }
+      }
+      if (v.item < s.item) {
+        if (!v.in) enter(v);   // S of the piece is out: its record is there
+        const int v0 = v.blk * (C::KU + C::VU) + C::KU;
+        if (ready(&ct.p_full[v.item & 1], (v.item >> 1) & 1) && landed(v0, C::VU)) {
+          tc_fence_after();
+          const int w = v.item & 1;               // warp group, S buffer, O accumulator
+          const uint32_t pcol = tmem + 128 * w;
+          const bool first = v.lb < (v.qt == 1 ? 2 : 1);   // the group's first block of the piece
+          const bool v_done = v.t + 1 == v.qt, last = v_done && v.lb + 1 == v.nb;
+          if (elect_one()) {
+            const int u0 = v0 % C::NU;
+            if (C::VU == 1 || u0 + 1 < C::NU) {
+              // both halves side by side: N = hd, the halves 16 KB apart
+              const uint64_t vd = sdesc_sw128(smem_u32(sR) + u0 * C::UNIT, C::UNIT, 1024);
+#pragma unroll
+              for (int ks = 0; ks < 8; ++ks)   // 16 keys (two atoms) per MMA
+                mma_bf16_ts(tmem + C::O_COL + HD * w, pcol + ks * 8, vd + ((ks * 2048) >> 4), C::IDESC_PV,
+                            (!first || ks > 0) ? 1u : 0u);
+            } else {
+              // the ring's end lies between them: half by half
+              constexpr uint32_t IDESC_64 = idesc_bf16(128, 64, true);
+#pragma unroll
+              for (int ch = 0; ch < C::VU; ++ch) {
+                const uint64_t vd = vd0 + static_cast<uint64_t>((((v0 + ch) % C::NU) * C::UNIT) >> 4);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                  mma_bf16_ts(tmem + C::O_COL + HD * w + 64 * ch, pcol + ks * 8, vd + ((ks * 2048) >> 4), IDESC_64,
+                              (!first || ks > 0) ? 1u : 0u);
+              }
+            }
+            mma_commit(&ct.o_full[w]);
+            if (v_done)
+#pragma unroll
+              for (int ch = 0; ch < C::VU; ++ch) mma_commit(&ct.empty[(v0 + ch) % C::NU]);
+            if (last) mbar_arrive(&ct.seg_empty[v.seg % C::NSEG]);
+          }
+          __syncwarp();
+          ++v.item;
+          if (++v.t == v.qt) {
+            v.t = 0;
+            ++v.blk;
+            if (++v.lb == v.nb) {
+              v.in = false;
+              ++v.seg;
+            }
+          }
+          progress = true;
+        }
+      }
+      if (s_end && v.item == s.item) break;
+      if (progress) {
+        spin = 0;
+        t_idle = 0;
+      } else if ((spin & 255u) == 0) {
+        if (t_idle == 0) t_idle = globaltimer();
+        const bool late = globaltimer() - t_idle > kWaitLimitNs;
+        if (__any_sync(0xffffffffu, late || *abort_flag)) {
+          if (__any_sync(0xffffffffu, late) && lane == 0) {
+            *abort_flag = 1;
+            atomicExch(p.err, kErrWaitMma);
+          }
+          break;
+        }
+      }
+    }
+    // every MMA issued above has completed before TMEM is freed
+    if (elect_one()) mma_commit(&ct.done);
+    __syncwarp();
+    const uint64_t t_end = globaltimer();
+    while (!mbar_try_wait(smem_u32(&ct.done), 0) && globaltimer() - t_end < kWaitLimitNs) {
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------- softmax / epilogue
+    const int w = (warp - 2) >> 2;          // warp group: it takes every second item
+    const int qu = warp & 3;                // TMEM lane quarter
+    const int row = qu * 32 + lane;         // row of the tile
+    const uint32_t lane_base = static_cast<uint32_t>(qu * 32) << 16;
+    const uint32_t s_col = tmem + lane_base + 128 * w;
+    const uint32_t o_col = tmem + lane_base + C::O_COL + HD * w;
+    const uint32_t o_other = tmem + lane_base + C::O_COL + HD * (w ^ 1);
+    float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
+    constexpr float kRescaleAbove = 8.f;    // log2 units
+    const float scale = p.scale_log2;
+    const float2 sc2 = make_float2(scale, scale);
+    int nseg = 0, item0 = 0;
+    int lent[2] = {0, 0};     // times that group 0, 1 left its part of a piece to the other
+    bool lending = false;     // the other group may still be reading this one's O and (m, l)
+    bool ok = true;
+    while (true) {
+      const int ss = nseg % C::NSEG;
+      bool fail = !mbar_wait(&ct.seg_full[ss], (nseg / C::NSEG) & 1, abort_flag, p.err, kErrWaitSoftmax);
+      if (__any_sync(0xffffffffu, fail)) break;   // tcgen05.ld below is warp-collective
+      const PreSeg &sg = ct.seg[ss];
+      const int nb = sg.nb;
+      if (nb == 0) break;
+      const int qt = sg.qt, j0 = sg.j0;
+      const int items = nb * qt;
+      const int lb0 = (item0 & 1) ^ w;       // this group's first item of the piece
+      const int t = qt == 2 ? lb0 : 0;       // its query tile
+      if (lb0 >= items) {                    // one block, and it is the other group's
+        ++item0;
+        ++nseg;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ct.seg_empty[ss]);
+        continue;
+      }
+      const int rows = min(sg.rows - 128 * t, 128);
+      const bool idle = qu * 32 >= rows;     // no rows for this warp
+      const int limit = sg.first + 128 * t + row;   // the last key that the row sees
+      float m_ref = -INFINITY, l = 0.f;
+      for (int li = lb0; li < items; li += 2) {
+        const int item = item0 + li, lb = qt == 2 ? li >> 1 : li;
+        const int key0 = kBlk * (j0 + lb);
+        fail = !mbar_wait(&ct.s_full[w], (item >> 1) & 1, abort_flag, p.err, kErrWaitSoftmax);
+        if (__any_sync(0xffffffffu, fail)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (!idle) {
+          if (key0 + kBlk - 1 > sg.first + 128 * t + qu * 32) mask_block(s_col, limit - key0);
+          // The group's first block of the piece sets each row's reference
+          // maximum.  From then on one pass over S while it holds; if a row of
+          // the warp rose more than 2^8 above it, the reference moves, O is
+          // rescaled and the probabilities are taken again from S, intact
+          // until P is stored.
+          uint32_t pk_lo[32], pk_hi[32];
+          float2 lsum = make_float2(0.f, 0.f);
+          float mq0 = -INFINITY, mq1 = -INFINITY, mq2 = -INFINITY, mq3 = -INFINITY;
+          if (li < 2) {
+            float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+              float sv[32];
+              tmem_ld32(s_col + 32 * k, sv);
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                m0 = max3f(m0, sv[e], sv[e + 1]);
+                m1 = max3f(m1, sv[e + 2], sv[e + 3]);
+              }
+            }
+            m_ref = fmaxf(m0, m1) * scale;
+          }
+          // (Always so.  As a condition it keeps the exponentials behind the maxima.)
+          const bool apart = nb > 0;
+          float negm = m_ref == -INFINITY ? 0.f : -m_ref;
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            float sv[64];
+            tmem_ld64(s_col + 64 * hh, sv);
+#pragma unroll
+            for (int e = 0; e < 64; e += 8) {
+              mq0 = max3f(mq0, sv[e], sv[e + 1]);
+              mq1 = max3f(mq1, sv[e + 2], sv[e + 3]);
+              mq2 = max3f(mq2, sv[e + 4], sv[e + 5]);
+              mq3 = max3f(mq3, sv[e + 6], sv[e + 7]);
+            }
+            if (apart) probs<64>(sv, sc2, negm, hh ? pk_hi : pk_lo, lsum);
+          }
+          const float mx = fmaxf(fmaxf(mq0, mq1), fmaxf(mq2, mq3)) * scale;
+          const bool grow = mx > m_ref + kRescaleAbove;
+          if (__any_sync(0xffffffffu, grow)) {
+            if (li >= 2) {
+              // O holds the group's blocks before: their P V must be done
+              fail = !mbar_wait(&ct.o_full[w], ((item - 2) >> 1) & 1, abort_flag, p.err, kErrWaitSoftmax);
+              if (__any_sync(0xffffffffu, fail)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const float alpha = grow ? ex2_approx(m_ref - mx) : 1.f;
+#pragma unroll 1
+              for (int cc = 0; cc < HD / 32; ++cc) {
+                float v[32];
+                tmem_ld32(o_col + cc * 32, v);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[k] *= alpha;
+                tmem_st32(o_col + cc * 32, v);
+              }
+              if (grow) l *= alpha;
+            }
+            if (grow) m_ref = mx;
+            negm = m_ref == -INFINITY ? 0.f : -m_ref;   // a row that has seen nothing yet
+            // P of 32 keys goes over 16 columns of S that have been read
+            lsum = make_float2(0.f, 0.f);
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+              float sv[32];
+              uint32_t pk[16];
+              tmem_ld32(s_col + 32 * k, sv);
+              probs<32>(sv, sc2, negm, pk, lsum);
+              tmem_st16u(s_col + 16 * k, pk);
+            }
+          } else {
+            // P over S: keys 0-63 in columns 0-31, keys 64-127 in 32-63
+            tmem_st32u(s_col, pk_lo);
+            tmem_st32u(s_col + 32, pk_hi);
+          }
+          l += lsum.x + lsum.y;
+        }
+        if (lending) {
+          // P V of this item overwrites O: the other group must have read it
+          fail = !mbar_wait(&ct.ml_empty[w], (lent[w] - 1) & 1, abort_flag, p.err, kErrWaitSoftmax);
+          if (__any_sync(0xffffffffu, fail)) {
+            ok = false;
+            break;
+          }
+          lending = false;
+        }
+        tc_fence_before();
+        mbar_arrive(&ct.p_full[w]);
+      }
+      if (!ok) break;
+      // ---- the piece is done: its output, or its partial
+      const int last_item = item0 + items - 1;
+      const bool joint = qt == 1 && nb > 1;         // both groups had blocks of the tile
+      if (joint && (last_item & 1) != w) {
+        // the other group has the last block: it gets this one's m and l
+        ml[row] = make_float2(m_ref, l);
+        ++lent[w];
+        lending = true;
+        tc_fence_before();
+        mbar_arrive(&ct.ml_full[w]);
+      } else {
+        const int mine_last = qt == 2 ? item0 + items - 2 + lb0 : last_item;
+        fail = !mbar_wait(&ct.o_full[w], (mine_last >> 1) & 1, abort_flag, p.err, kErrWaitSoftmax);
+        float wa = 1.f, wb = 0.f;                     // weights of this group's O and the other's
+        if (joint) {
+          if (!fail) fail = !mbar_wait(&ct.ml_full[w ^ 1], lent[w ^ 1] & 1, abort_flag, p.err, kErrWaitSoftmax);
+          ++lent[w ^ 1];
+          if (!fail) fail = !mbar_wait(&ct.o_full[w ^ 1], ((last_item - 1) >> 1) & 1, abort_flag, p.err, kErrWaitSoftmax);
+          const float2 o = ml[row];
+          const float M = fmaxf(m_ref, o.x);
+          wa = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - M);
+          wb = o.x == -INFINITY ? 0.f : ex2_approx(o.x - M);
+          // (a group whose part of the row is NaN has that in its sum too)
+          l = (m_ref == -INFINITY ? l : wa * l) + (o.x == -INFINITY ? o.y : wb * o.y);
+          m_ref = M;
+        }
+        if (__any_sync(0xffffffffu, fail)) break;
+        tc_fence_after();
+        if (!idle) {
+          const bool valid = row < rows;
+          const int tok = sg.t0 + 128 * t + row, slot = sg.slot;
+          const float inv = 1.f / l;
+          uint4 *dst = reinterpret_cast<uint4 *>(p.o + (static_cast<int64_t>(tok) * p.H + sg.h) * HD);
+          float *part = p.part + (static_cast<int64_t>(max(slot, 0)) * 256 + 128 * t + row) * (HD + 4);
+#pragma unroll 1
+          for (int cc = 0; cc < HD / 32; ++cc) {
+            float v[32];
+            tmem_ld32(o_col + cc * 32, v);
+            if (joint) {
+              float x[32];
+              tmem_ld32(o_other + cc * 32, x);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] = wa * v[k] + wb * x[k];
+            }
+            if (valid && slot < 0) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                dst[cc * 4 + k] = make_uint4(pack_bf16x2(v[8 * k] * inv, v[8 * k + 1] * inv),
+                                             pack_bf16x2(v[8 * k + 2] * inv, v[8 * k + 3] * inv),
+                                             pack_bf16x2(v[8 * k + 4] * inv, v[8 * k + 5] * inv),
+                                             pack_bf16x2(v[8 * k + 6] * inv, v[8 * k + 7] * inv));
+            } else if (valid) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                reinterpret_cast<float4 *>(part + cc * 32)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            }
+          }
+          if (valid && slot >= 0) *reinterpret_cast<float2 *>(part + HD) = make_float2(m_ref, l);
+        }
+        tc_fence_before();
+        if (joint) mbar_arrive(&ct.ml_empty[w ^ 1]);
+      }
+      item0 += items;
+      ++nseg;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ct.seg_empty[ss]);
+    }
+    tc_fence_before();
+  }
+
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// Merge of the units that were cut: CTA (w, y) takes every gridDim.y-th row
+// group of the unit whose first piece CTA w computed; eight lanes a row.
+//   o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,   M = max_s m_s
+template <int HD>
+__global__ void __launch_bounds__(256) latent_prefill_merge_kernel(const __grid_constant__ PreParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const int w = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4 rec = *reinterpret_cast<const int4 *>(p.rec + w * 8);
+  const int pieces = rec.x, rows = rec.w;
+  if (pieces == 0) return;
+  // piece 0 in slot 2 w + 1, piece s > 0 in slot 2 (w + s)
+  auto src = [&](int s, int row) {
+    return p.part + (static_cast<int64_t>(s == 0 ? 2 * w + 1 : 2 * (w + s)) * 256 + row) * (HD + 4);
+  };
+  constexpr int PER = HD / 32;   // float4s of a lane: columns 4 (lane + 8 k)
+  const int l8 = lane & 7;
+  for (int row = (blockIdx.y * 8 + warp) * 4 + (lane >> 3); row < rows; row += gridDim.y * 32) {
+    float M = -INFINITY, L = 0.f;
+    float4 acc[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < pieces; ++s) {
+      const float *x = src(s, row);
+      float4 v[PER];
+#pragma unroll
+      for (int k = 0; k < PER; ++k) v[k] = reinterpret_cast<const float4 *>(x)[l8 + 8 * k];
+      const float2 ml = *reinterpret_cast<const float2 *>(x + HD);
+      if (ml.x == -INFINITY) {   // the row saw nothing in this piece, or only NaN
+        L += ml.y;
+        continue;
+      }
+      const float mn = fmaxf(M, ml.x);
+      const float a = M == -INFINITY ? 0.f : ex2_approx(M - mn), b = ex2_approx(ml.x - mn);
+      L = (M == -INFINITY ? L : L * a) + b * ml.y;
+      M = mn;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        acc[k].x = fmaf(acc[k].x, a, b * v[k].x);
+        acc[k].y = fmaf(acc[k].y, a, b * v[k].y);
+        acc[k].z = fmaf(acc[k].z, a, b * v[k].z);
+        acc[k].w = fmaf(acc[k].w, a, b * v[k].w);
+      }
+    }
+    const float inv = 1.f / L;
+    uint2 *dst = reinterpret_cast<uint2 *>(p.o + (static_cast<int64_t>(rec.y + row) * p.H + rec.z) * HD);
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+      dst[l8 + 8 * k] = make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv), pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+  }
+}
+
+// The workspace's keys: blocks of 128, each request's from a block of its own.
+int64_t cap_blocks(int64_t kv_tokens, int64_t n_reqs) { return kv_tokens / kBlk + n_reqs; }
+
+// Heads of a group: as many as keep its keys and values within kGroupBytes, evenly spread.
+int group_heads(int64_t blocks, int64_t H, int64_t hd) {
+  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(H, kGroupBytes / std::max<int64_t>(1, blocks * kBlk * 4 * hd)));
+  const int64_t groups = (H + most - 1) / most;
+  return static_cast<int>((H + groups - 1) / groups);
+}
+
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+template <int HD, int RANK>
+cudaError_t launch_expand(const CUtensorMap &tk, const CUtensorMap &tw, const CUtensorMap &tr, const PreParams &p, cudaStream_t st) {
+  using C = ExpCfg<HD, RANK>;
+  cudaError_t e = ensure_max_smem(reinterpret_cast<const void *>(latent_expand_kernel<HD, RANK>), C::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(latent_expand_kernel<HD, RANK>, dim3(device_sm_count()), dim3(C::THREADS), C::SMEM, st, 1, tk, tw, tr, p);
+}
+
+template <int HD>
+cudaError_t launch_prefill(const LatentArgs &a, PreParams &p, int group, __nv_bfloat16 *rope, cudaStream_t st) {
+  using C = PreCfg<HD>;
+  const uint64_t H = a.H, T = a.T, W = a.rank + kLatentRope, nc = a.rank / 64 + 1;
+  const uint64_t rows = static_cast<uint64_t>(p.cap_blocks) * kBlk;
+  CUtensorMap tq, tqr, tkv, tr, ts, tk, tw;
+  const uint64_t dq[3] = {HD + kLatentRope, H, T}, sq[2] = {(HD + kLatentRope) * 2, (HD + kLatentRope) * 2 * H};
+  const uint64_t dr[3] = {kLatentRope, H, T}, sr[2] = {kLatentRope * 2, kLatentRope * 2 * H};
+  const uint32_t bq[3] = {64, 1, 128};
+  const uint64_t dk[5] = {64, 8, nc, kPage / 8, static_cast<uint64_t>(a.num_pages)};
+  const uint64_t sk[4] = {W * 2, 128, 8 * W * 2, kPage * W * 2};
+  const uint32_t bk[5] = {64, 8, static_cast<uint32_t>(nc), kPage / 8, 1};
+  cudaError_t e = encode_tmap(&tq, a.q, 3, dq, sq, bq);
+  if (e == cudaSuccess) e = encode_tmap(&tqr, a.q_rope, 3, dr, sr, bq);
+  if (e == cudaSuccess) e = encode_tmap_2d(&tkv, p.kv, 2 * HD, rows * group, 4 * HD, 64, kBlk);
+  if (e == cudaSuccess) e = encode_tmap_2d(&tr, rope, kLatentRope, rows, kLatentRope * 2, 64, kBlk);
+  if (e == cudaSuccess) e = encode_tmap_2d(&ts, rope, kLatentRope, rows, kLatentRope * 2, 64, 8);
+  if (e == cudaSuccess) e = encode_tmap_5d(&tk, a.pool, dk, sk, bk);
+  if (e == cudaSuccess) e = encode_tmap_2d(&tw, a.w_kv, a.rank, H * 2 * HD, static_cast<uint64_t>(a.rank) * 2, 64, 2 * HD);
+  if (e == cudaSuccess) e = ensure_max_smem(reinterpret_cast<const void *>(latent_prefill_kernel<HD>), C::SMEM);
+  const int ctas = std::min(device_sm_count(), kMaxCtas);
+  for (p.h0 = 0; p.h0 < a.H && e == cudaSuccess; p.h0 += group) {
+    p.HG = std::min(group, a.H - p.h0);
+    e = a.rank == 512 ? launch_expand<HD, 512>(tk, tw, ts, p, st) : launch_expand<HD, 256>(tk, tw, ts, p, st);
+    if (e == cudaSuccess) e = launch_pdl(latent_prefill_kernel<HD>, dim3(ctas), dim3(C::THREADS), C::SMEM, st, 1, tq, tqr, tkv, tr, p);
+    if (e == cudaSuccess) e = launch_pdl(latent_prefill_merge_kernel<HD>, dim3(ctas, 4), dim3(256), 0, st, 1, p);
+  }
+  return e;
+}
+
+}  // namespace
+
+// a group's keys and values, the rotated keys, the records, the partials
+size_t latent_prefill_workspace_bytes(int64_t kv_tokens, int64_t n_reqs, int64_t H, int64_t hd, int64_t rank) {
+  (void)rank;
+  const int64_t blocks = cap_blocks(kv_tokens, n_reqs);
+  return align256(static_cast<size_t>(blocks) * kBlk * 4 * hd * group_heads(blocks, H, hd)) +
+         align256(static_cast<size_t>(blocks) * kBlk * kLatentRope * 2) + kRecBytes +
+         static_cast<size_t>(2) * kMaxCtas * 256 * (hd + 4) * sizeof(float);
+}
+
+cudaError_t latent_prefill_run(const LatentArgs &a, cudaStream_t st) {
+  const int64_t blocks = cap_blocks(a.kv_tokens, a.n_reqs);
+  const int group = group_heads(blocks, a.H, a.hd);
+  uint8_t *w = static_cast<uint8_t *>(a.workspace);
+  const size_t kv_bytes = align256(static_cast<size_t>(blocks) * kBlk * 4 * a.hd * group);
+  const size_t rope_bytes = align256(static_cast<size_t>(blocks) * kBlk * kLatentRope * 2);
+  PreParams p;
+  p.kv = reinterpret_cast<__nv_bfloat16 *>(w);
+  p.o = static_cast<__nv_bfloat16 *>(a.o);
+  p.qo_indptr = a.qo_indptr;
+  p.kv_len = a.kv_len;
+  p.bt_indptr = a.bt_indptr;
+  p.bt = a.bt;
+  p.n_reqs = a.n_reqs;
+  p.T = a.T;
+  p.H = a.H;
+  p.h0 = 0;
+  p.HG = group;
+  p.num_pages = a.num_pages;
+  p.cap_blocks = static_cast<int>(blocks);
+  p.scale_log2 = a.scale * kLog2e;
+  p.rec = reinterpret_cast<int32_t *>(w + kv_bytes + rope_bytes);
+  p.part = reinterpret_cast<float *>(w + kv_bytes + rope_bytes + kRecBytes);
+  p.err = a.err;
+  __nv_bfloat16 *rope = reinterpret_cast<__nv_bfloat16 *>(w + kv_bytes);
+  return a.hd == 128 ? launch_prefill<128>(a, p, group, rope, st) : launch_prefill<64>(a, p, group, rope, st);
+}
+
+}  // namespace mb

@@ -233,7 +233,57 @@ def test_absorbed_more_requests_than_threads(mb):
     b.check(b.run(mb, "absorbed"), "absorbed")
 
 
-@pytest.mark.parametrize("form", ["absorbed"])
+@pytest.mark.parametrize("H,hd,rank", [(1, 64, 256), (3, 128, 256), (8, 64, 512), (5, 128, 512), (40, 128, 512)])
+def test_expanded_chunks(mb, H, hd, rank):
+    """Chunks at tile, block and page edges, behind prefixes at theirs, with
+    single tokens and requests without any."""
+    reqs = [(0, 1), (0, 127), (0, 129), (5, 0), (128, 128), (127, 1), (3, 300)]
+    if H < 8:
+        reqs += [(0, 256), (0, 257), (15, 16), (500, 513), (0, 0), (1000, 2), (255, 130)]
+    b = Batch(reqs, H, hd, rank, seed=H + 20, lead=5)
+    b.check(b.run(mb, "expanded"), "expanded")
+
+
+@pytest.mark.parametrize("reqs,H,hd,rank", [([(9000, 40)], 3, 128, 512), ([(0, 2500)], 2, 64, 256), ([(3001, 700), (77, 5)], 2, 128, 256)])
+def test_expanded_long_caches_cut_over_many_ctas(mb, reqs, H, hd, rank):
+    b = Batch(reqs, H, hd, rank, seed=len(reqs) + 30)
+    b.check(b.run(mb, "expanded"), "expanded")
+
+
+def test_expanded_groups_of_heads(mb):
+    """Keys of 26,000 tokens: 13.4 MB a head, so seven heads are three groups."""
+    b = Batch([(25990, 10)], 7, 128, 512, seed=33)
+    b.check(b.run(mb, "expanded"), "expanded")
+
+
+def test_expanded_more_requests_than_threads(mb):
+    reqs = [(int(k) % 90, int(k) % 4) for k in np.random.default_rng(6).integers(0, 1000, size=700)]
+    b = Batch(reqs, 2, 64, 256, seed=7)
+    b.check(b.run(mb, "expanded"), "expanded")
+
+
+def test_expanded_room_too_small_leaves_the_requests_behind(mb):
+    b = Batch([(100, 28), (0, 128), (300, 20), (7, 3)], 2, 64, 256, seed=34)
+    b.room = lambda: 128 * 2 - 1     # with four requests: 1 + 4 blocks, and 1 + 1 + 3 + 1 are asked for
+    b.check(b.run(mb, "expanded", err=True), "expanded", only=[0, 1, 2])
+    b.room = lambda: 0               # four blocks: the third request does not fit any more, nor does what follows
+    b.check(b.run(mb, "expanded", err=True), "expanded", only=[0, 1])
+
+
+def test_the_forms_agree_on_a_mixed_batch(mb):
+    """Decodes and chunks of one descriptor, each form on its part: as each
+    form on the whole."""
+    b = Batch([(900, 1), (64, 1), (0, 1), (200, 150), (0, 33)], 8, 128, 512, seed=35)
+    d, o = b.dev(), b.out()
+    b.call(mb, "absorbed", d, o, b.work(mb, "absorbed"), n=3)
+    b.call(mb, "expanded", d, o, b.work(mb, "expanded"), n=2, at=3)
+    _status(mb, False)
+    got = f64(from_dev(o)).reshape(b.T, 8, 128)
+    b.check(np.where(np.arange(b.T)[:, None, None] < 3, got, np.nan), "absorbed", only=[0, 1, 2])
+    b.check(np.where(np.arange(b.T)[:, None, None] >= 3, got, np.nan), "expanded", only=[3, 4])
+
+
+@pytest.mark.parametrize("form", ["absorbed", "expanded"])
 def test_rows_do_not_depend_on_what_they_do_not_see(mb, form):
     """A vector that is not finite makes the rows that see it NaN; the others'
     bits stay."""
@@ -250,7 +300,7 @@ def test_rows_do_not_depend_on_what_they_do_not_see(mb, form):
     assert np.all(np.isnan(got[sees])) and np.array_equal(got[rows & ~sees], clean[rows & ~sees])
 
 
-@pytest.mark.parametrize("form", ["absorbed"])
+@pytest.mark.parametrize("form", ["absorbed", "expanded"])
 def test_large_logits(mb, form):
     """Maxima that rise by hundreds from block to block."""
     b = Batch([(400, 3)], 8, 64, 256, seed=9)
@@ -268,7 +318,7 @@ def test_large_logits(mb, form):
     assert np.array_equal(got[:3], b.run(mb, form)[:3])
 
 
-@pytest.mark.parametrize("form", ["absorbed"])
+@pytest.mark.parametrize("form", ["absorbed", "expanded"])
 @pytest.mark.parametrize("what", ["kv_short", "kv_huge", "table_short", "rows_behind", "rows_back", "negative"])
 def test_a_bad_request_is_left_alone(mb, form, what):
     b = Batch([(30, 2), (40, 2), (50, 1)], 8, 64, 256, seed=10, tail=0)
@@ -296,7 +346,7 @@ def test_a_bad_request_is_left_alone(mb, form, what):
         b.check(got, form, only=only)
 
 
-@pytest.mark.parametrize("form", ["absorbed"])
+@pytest.mark.parametrize("form", ["absorbed", "expanded"])
 @pytest.mark.parametrize("page", [-1, 2 ** 31 - 1, "P"])
 def test_a_page_out_of_range_is_read_as_page_0(mb, form, page):
     b = Batch([(30, 2), (40, 2)], 8, 64, 256, seed=11)
@@ -307,7 +357,7 @@ def test_a_page_out_of_range_is_read_as_page_0(mb, form, page):
     b.check(b.run(mb, form, err=True, d=d), form)
 
 
-@pytest.mark.parametrize("form", ["absorbed"])
+@pytest.mark.parametrize("form", ["absorbed", "expanded"])
 def test_pages_beyond_32_bit_offsets(mb, form):
     b = Batch([(200, 3), (33, 1)], 8, 128, 512, seed=12)
     P = (1 << 31) // (16 * 576) + 400
@@ -322,7 +372,7 @@ def test_pages_beyond_32_bit_offsets(mb, form):
     b.check(f64(from_dev(o)).reshape(b.T, b.H, b.hd), form)
 
 
-@pytest.mark.parametrize("form", ["absorbed"])
+@pytest.mark.parametrize("form", ["absorbed", "expanded"])
 def test_two_calls_at_once_and_a_graph(mb, form):
     """Calls on two side streams with a workspace each; then one captured and
     replayed with another batch's contents."""
@@ -357,7 +407,7 @@ def test_two_calls_at_once_and_a_graph(mb, form):
         x.check(f64(from_dev(oc)).reshape(x.T, 20, 128), form)
 
 
-@pytest.mark.parametrize("form", ["absorbed"])
+@pytest.mark.parametrize("form", ["absorbed", "expanded"])
 def test_runs_repeat_to_the_bit(mb, form):
     b = Batch([(2500, 1), (33, 2), (700, 1)], 40, 128, 512, seed=17)
     first = b.run(mb, form)

@@ -70,8 +70,9 @@ def test_tables_release_refuses(mb, over, status):
 def test_empty_calls_do_nothing(mb):
     _release(mb, n=0)
     _append(mb, T=0)
-    _attention(mb, T=0)
-    _attention(mb, num_reqs=0)
+    for form in FORMS:
+        _attention(mb, form, T=0)
+        _attention(mb, form, num_reqs=0)
 
 
 APP = ["ckv", "q", "gain", "pool", "q_rope", "tok_pos", "tok_slot"]
@@ -113,10 +114,13 @@ ATT_BYTES = dict(q=7 * 8 * 192 * 2, q_rope=7 * 8 * 64 * 2, w_kv=8 * 256 * 512 * 
 def _attention(mb, form="absorbed", **over):
     a = {**_args(ATT, {}), "num_pages": 4, "n_heads": 8, "head_dim": 128, "rank": 512, "scale": 0.07, "num_reqs": 3, "T": 7,
          **over}
-    mb.mb_latent_attention(**a)
+    if form == "absorbed":
+        mb.mb_latent_attention(**a)
+    else:
+        mb.mb_latent_prefill(**{"kv_tokens": 100, **a})
 
 
-FORMS = ["absorbed"]
+FORMS = ["absorbed", "expanded"]
 BAD = [*[({n: None}, "MB_EINVAL") for n in ATT], *[({n: G + 8}, "MB_EINVAL") for n in ("q", "q_rope", "w_kv", "o")],
        (dict(pool=4 * G + 64), "MB_EINVAL"), (dict(workspace=20 * G + 128), "MB_EINVAL"), (dict(T=-1), "MB_EINVAL"),
        (dict(num_reqs=-1), "MB_EINVAL"), (dict(num_pages=0), "MB_EINVAL"), (dict(n_heads=0), "MB_EINVAL"),
@@ -139,6 +143,12 @@ def test_attention_refuses_an_output_over_an_input(mb, form, other):
     for x in ((at + ATT_BYTES[other] - 1) & ~15, at - ATT_BYTES["o"] + 16):
         _refused(mb, lambda: _attention(mb, form, o=x), "MB_EINVAL", ("overlap", "o ", other))
     _refused(mb, lambda: _attention(mb, form, workspace=at), "MB_EINVAL", ("overlap", "workspace", other))
+
+
+@pytest.mark.parametrize("over,status", [(dict(kv_tokens=-1), "MB_EINVAL"), (dict(kv_tokens=(1 << 27) + 1), "MB_EUNSUPPORTED"),
+                                         (dict(num_reqs=(1 << 20) + 1), "MB_EUNSUPPORTED")])
+def test_expanded_refuses(mb, over, status):
+    _refused(mb, lambda: _attention(mb, "expanded", **over), status)
 
 
 # ------------------------------------------------------- the oracle's pins
