@@ -131,123 +131,108 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const __g
   }
 }
 
-// ------------------------------------------------- products head by head
-// C[t][h][n] = sum_k A[t][h][k] B_h(n, k) for every head: the queries through
-// W_uk^T (BMN: B_h is stored [k][n], n contiguous) and the outputs through
-// W_uv (stored [n][k]).  One CTA makes 128 tokens x BN of one head on tcgen05:
-// A and B wholly in shared memory, one barrier per 64-wide chunk of k, so the
-// products start as the first chunk lands.  Heads' weights are read once per
-// 128 tokens: for few tokens they are the time, for many the products.
-template <int KC, int BN, bool BMN>
-struct HeadCfg {
+// ------------------------------------------------------------- the queries
+// qc[t][h][r] = sum_d q[t][h][d] W_uk,h[d][r] for every head, rounded to bf16 for
+// the product with the cached rows.  One CTA makes 128 tokens x 128 columns of
+// one head on tcgen05, A and B wholly in shared memory, one barrier per 64 of
+// hd.  Heads' weights are read once per 128 tokens: for few tokens they (and the
+// launch) are the time, for many the products.
+constexpr int kQueryN = 128;
+
+template <int HD>
+struct QueryCfg {
+  static constexpr int KC = HD / 64;
   static constexpr int A_CHUNK = 128 * 128;
-  static constexpr int B_BYTES = KC * 64 * BN * 2;
-  static constexpr int OFF_B = KC * A_CHUNK;
-  static constexpr int OFF_CTRL = OFF_B + B_BYTES;
+  static constexpr int B_PART = 64 * 128;            // 64 of hd x 64 columns
+  static constexpr int OFF_B = KC * A_CHUNK;         // [64 columns][hd][128 B]: W_uk is stored [d][r]
+  static constexpr int OFF_CTRL = OFF_B + KC * (kQueryN / 64) * B_PART;
   static constexpr int SMEM = OFF_CTRL + 256;
-  static constexpr uint32_t IDESC = idesc_bf16(128, BN, BMN);
+  static constexpr uint32_t IDESC = idesc_bf16(128, kQueryN, true);
 };
 
-struct HeadParams {
-  __nv_bfloat16 *C;
-  uint8_t *live;                 // [T]: which rows belong to a request
-  const int32_t *qo_indptr, *kv_len, *bt_indptr;
-  int n_reqs, T, H, N, a_col, b_row, b_rows;   // first column of A's row; head h's B starts at row b_row + h * b_rows
+// What becomes of a token's row: its unit's pieces (0: no request's token, 1: oc
+// holds it), the CTA with the first one, and its place in the unit.
+struct TokRec {
+  int32_t pieces, first, place, pad;
+};
+
+struct QueryParams {
+  __nv_bfloat16 *qc;
+  TokRec *tok;
+  int T, H, rank;
   int *err;
 };
 
-template <int KC, int BN, bool BMN>
-__global__ void __launch_bounds__(128) head_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
-                                                        const __grid_constant__ CUtensorMap tmB,
-                                                        const __grid_constant__ HeadParams p) {
-  using C = HeadCfg<KC, BN, BMN>;
+template <int HD>
+__global__ void __launch_bounds__(128) latent_query_kernel(const __grid_constant__ CUtensorMap tmQ,
+                                                           const __grid_constant__ CUtensorMap tmW, const QueryParams p) {
+  using C = QueryCfg<HD>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_CTRL), *done = full + KC;
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_CTRL), *done = full + C::KC;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int tid = threadIdx.x, warp = tid >> 5;
-  const int n0 = blockIdx.x * BN, h = blockIdx.y, t0 = blockIdx.z * 128;
+  const int n0 = blockIdx.x * kQueryN, h = blockIdx.y, t0 = blockIdx.z * 128, t = t0 + tid;
   if (smem_u32(smem) & 1023u) {   // the swizzled layouts need a 1024-aligned base
     pdl_wait();
     if (tid == 0) atomicExch(p.err, kErrBounds);
     return;
   }
   if (tid == 0) {
-    for (int c = 0; c < KC; ++c) mbar_init(&full[c], 1);
+    for (int c = 0; c < C::KC; ++c) mbar_init(&full[c], 1);
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    prefetch_tmap(&tmA);
-    prefetch_tmap(&tmB);
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmW);
   }
   if (warp == 0) {
-    tmem_alloc(tmem_slot, BN < 32 ? 32 : BN);
+    tmem_alloc(tmem_slot, kQueryN);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_wait();   // queries, weights, descriptor and outputs belong to earlier kernels of the stream
+  // The call's first kernel: every other one starts only after all of this one's
+  // CTAs have passed this, so what earlier kernels of the stream wrote is there
+  // for them without a wait of their own.
+  pdl_wait();
   pdl_trigger();
   if (tid == 0) {
-    const int row = p.b_row + h * p.b_rows;
-    for (int c = 0; c < KC; ++c) {
-      mbar_arrive_expect_tx(&full[c], C::A_CHUNK + 64 * BN * 2);
-      tma_load_3d(smem + c * C::A_CHUNK, &tmA, &full[c], p.a_col + 64 * c, h, t0);
-      if (BMN) {   // [64-wide n chunk][k][128 B]: 64 rows of k of each n chunk
-        for (int j = 0; j < BN / 64; ++j)
-          tma_load_2d(smem + C::OFF_B + j * (KC * 64 * 128) + c * 64 * 128, &tmB, &full[c], n0 + 64 * j, row + 64 * c);
-      } else {     // [64-wide k chunk][n][128 B]
-        tma_load_2d(smem + C::OFF_B + c * BN * 128, &tmB, &full[c], 64 * c, row + n0);
-      }
-    }
-  }
-  const int t = t0 + tid;
-  if (BMN && blockIdx.x == 0 && h == 0) {
-    // which of the tile's rows belong to a request (the others' outputs stay as they were)
-    __shared__ uint32_t rows[4];
-    if (tid < 4) rows[tid] = 0;
-    __syncthreads();
-    for (int r = tid; r < p.n_reqs; r += 128) {
-      const ReqWords w = load_req(p.qo_indptr, p.kv_len, p.bt_indptr, r);
-      if (!req_ok(w, p.T)) continue;
-      const int lo = max(w.q0 - t0, 0), hi = min(w.q1 - t0, 128);
-      for (int i = lo >> 5; i < 4 && 32 * i < hi; ++i) {
-        const int a = max(lo - 32 * i, 0), b = min(hi - 32 * i, 32);
-        if (a < b) atomicOr(&rows[i], (b == 32 ? 0xffffffffu : (1u << b) - 1u) & ~((1u << a) - 1u));
-      }
-    }
-    __syncthreads();
-    if (t < p.T) p.live[t] = (rows[tid >> 5] >> (tid & 31)) & 1u;
-  }
-  if (tid == 0) {
     const uint64_t a0 = sdesc_sw128(smem_u32(smem), 16, 1024);
-    const uint64_t b0 = BMN ? sdesc_sw128(smem_u32(smem + C::OFF_B), KC * 64 * 128, 1024)
-                            : sdesc_sw128(smem_u32(smem + C::OFF_B), 16, 1024);
-    for (int c = 0; c < KC; ++c) {
+    const uint64_t b0 = sdesc_sw128(smem_u32(smem + C::OFF_B), C::KC * C::B_PART, 1024);
+    for (int c = 0; c < C::KC; ++c) {
+      mbar_arrive_expect_tx(&full[c], C::A_CHUNK + (kQueryN / 64) * C::B_PART);
+      for (int j = 0; j < kQueryN / 64; ++j)
+        tma_load_2d(smem + C::OFF_B + (j * C::KC + c) * C::B_PART, &tmW, &full[c], n0 + 64 * j, h * 2 * HD + 64 * c);
+      tma_load_3d(smem + c * C::A_CHUNK, &tmQ, &full[c], 64 * c, h, t0);
+    }
+    for (int c = 0; c < C::KC; ++c) {
       if (!mbar_wait(&full[c], 0, abort_flag, p.err, kErrWaitMma)) break;
       tc_fence_after();
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        const uint64_t a = a0 + ((c * C::A_CHUNK + kk * 32) >> 4);
-        const uint64_t b = b0 + (BMN ? ((c * 64 + kk * 16) * 128) >> 4 : (c * BN * 128 + kk * 32) >> 4);
-        mma_bf16(tmem, a, b, C::IDESC, (c > 0 || kk > 0) ? 1u : 0u);
-      }
+      for (int kk = 0; kk < 4; ++kk)
+        mma_bf16(tmem, a0 + ((c * C::A_CHUNK + kk * 32) >> 4), b0 + ((c * C::B_PART + kk * 2048) >> 4), C::IDESC,
+                 (c > 0 || kk > 0) ? 1u : 0u);
     }
     mma_commit(done);
+  } else if (blockIdx.x == 0 && h == 0) {
+    // (thread 0's row is thread 1's to clear)
+    if (t < p.T) p.tok[t].pieces = 0;
+    if (tid == 1) p.tok[t0].pieces = 0;
   }
   __syncwarp();
   bool ok = mbar_wait(done, 0, abort_flag, p.err, kErrWaitEpilogue);
   ok = __all_sync(0xffffffffu, ok) && !*abort_flag;
-  if (ok) {
+  if (ok && t0 + 32 * warp < p.T) {
     tc_fence_after();
-    const bool mine = t < p.T && (BMN || p.live[t]);
-    uint4 *dst = reinterpret_cast<uint4 *>(p.C + (static_cast<int64_t>(t) * p.H + h) * p.N + n0);
-    for (int cc = 0; cc < BN / 32; ++cc) {
+    uint4 *dst = reinterpret_cast<uint4 *>(p.qc + (static_cast<int64_t>(t) * p.H + h) * p.rank + n0);
+#pragma unroll 1
+    for (int cc = 0; cc < kQueryN / 32; ++cc) {
       float v[32];
       tmem_ld32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + cc * 32, v);
-      if (mine)
+      if (t < p.T)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           dst[cc * 4 + k] = make_uint4(pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
@@ -259,7 +244,7 @@ __global__ void __launch_bounds__(128) head_gemm_kernel(const __grid_constant__ 
   if (warp == 0) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, BN < 32 ? 32 : BN);
+    tmem_dealloc(tmem, kQueryN);
   }
 }
 
@@ -280,10 +265,13 @@ __global__ void __launch_bounds__(128) head_gemm_kernel(const __grid_constant__ 
 // their product with V, as everywhere in this library; logits, maxima, sums and
 // accumulators are fp32.
 constexpr int kMaxCtas = 160;       // CTAs of a launch at most; sizes the workspace
-constexpr int kRecBytes = 8192;     // workspace: one record of 8 ints per CTA, then the partials
+// Floats of a slot: whole lines only (with m and l behind each row the stores and
+// loads of a row began 16 bytes off a sector).
+__host__ __device__ constexpr int64_t part_floats(int64_t rank) { return 64 * rank + 128; }
 constexpr int kBlk = 64;            // keys of a block
 constexpr int kCostUnit = 2;        // a unit's start and end, in blocks
-constexpr int kMinShare = 3;        // the least a CTA takes, in blocks
+constexpr int kMinShare = 2;        // the least a CTA takes, in blocks
+constexpr int kAhead = 2;           // blocks beyond the one to be sent that are fetched into L2
 
 struct AbsParams {
   __nv_bfloat16 *oc;             // [T][H][rank]: sum_j p_j c_j
@@ -291,8 +279,8 @@ struct AbsParams {
   const int32_t *qo_indptr, *kv_len, *bt_indptr, *bt;
   int n_reqs, T, H, Hc, HT, NT, N, num_pages;   // heads of a tile, head tiles, tokens of a tile, padded rows
   float scale_log2;
-  int32_t *rec;
-  float *part;                   // [2 slots per CTA][64 rows][rank + 4]: o, m, l, pad
+  TokRec *tok;                   // [T]
+  float *part;                   // [2 slots per CTA]: o of 64 rows [64][rank], their m and l [64][2]
   int *err;
 };
 
@@ -311,7 +299,7 @@ struct AbsCfg {
   static constexpr int OFF_P = OFF_K + NST * STAGE;
   static constexpr int OFF_CTRL = OFF_P + 64 * 128;
   static constexpr int SMEM = OFF_CTRL + 2048;
-  static constexpr int THREADS = 192;               // TMA, MMA, 4 softmax warps
+  static constexpr int THREADS = 256;               // TMA, 2 MMA issuers, one idle, 4 softmax warps
   static constexpr uint32_t IDESC_S = idesc_bf16(64, kBlk, false);
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t O_COL = 128;            // S buffers at 0 and 64, O^T tile dt at 128 + 64 dt
@@ -335,8 +323,8 @@ template <int RANK>
 struct AbsCtrl {
   using C = AbsCfg<RANK>;
   uint64_t q_full, q_empty;
-  uint64_t k_full[C::NST], k_empty[C::NST];
-  uint64_t s_full[2], p_full, pv_done;
+  uint64_t k_full[C::NST], k_empty[C::NST][4];   // empty: page by page
+  uint64_t s_full[2], s_empty[2], p_full, pv_done;
   uint64_t seg_full[C::NSEG], seg_empty[C::NSEG];
   uint64_t done;
   AbsSeg seg[C::NSEG];
@@ -347,7 +335,6 @@ struct AbsCtrl {
   uint32_t tmem;
   int abort;
   float col[64];         // one number per row: the rescaling, the reciprocal of its sum
-  int64_t base[64];      // where the row goes, -1: nowhere
 };
 
 __device__ __forceinline__ AbsReq abs_req(const AbsParams &p, const ReqWords w, bool *bad) {
@@ -379,10 +366,7 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
   const int ht = blockIdx.x % p.HT, cta = blockIdx.x / p.HT, W_max = gridDim.x / p.HT;
   if (smem_u32(smem) & 1023u) {   // the swizzled layouts need a 1024-aligned base
     pdl_wait();
-    if (threadIdx.x == 0) {
-      atomicExch(p.err, kErrBounds);
-      p.rec[blockIdx.x * 8] = 0;
-    }
+    if (threadIdx.x == 0) atomicExch(p.err, kErrBounds);
     return;
   }
   if (threadIdx.x == 0) {
@@ -390,16 +374,19 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
     mbar_init(&ct.q_empty, 1);
     for (int s = 0; s < C::NST; ++s) {
       mbar_init(&ct.k_full[s], 1);
-      mbar_init(&ct.k_empty[s], 1);
+      for (int k = 0; k < 4; ++k) mbar_init(&ct.k_empty[s][k], 1);
     }
-    for (int b = 0; b < 2; ++b) mbar_init(&ct.s_full[b], 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&ct.s_full[b], 1);
+      mbar_init(&ct.s_empty[b], 4);
+    }
     mbar_init(&ct.p_full, 128);
     mbar_init(&ct.pv_done, 1);
     for (int s = 0; s < C::NSEG; ++s) {
       mbar_init(&ct.seg_full[s], 1);
-      mbar_init(&ct.seg_empty[s], 5);   // the MMA issuer and the 4 softmax warps
+      mbar_init(&ct.seg_empty[s], 6);   // the 2 MMA issuers and the 4 softmax warps
     }
-    mbar_init(&ct.done, 1);
+    mbar_init(&ct.done, 2);
     ct.abort = 0;
     ct.start_req = -1;
     fence_mbar_init();
@@ -411,8 +398,10 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
     tmem_alloc(&ct.tmem, C::TMEM_COLS);
     tmem_relinquish();
   }
-  pdl_wait();   // the descriptor, queries, cache and outputs belong to earlier kernels of the stream
-  pdl_trigger();
+  // Of what earlier kernels of the stream write, only the queries' products come
+  // from this call's first kernel; this one is launched once that one has seen
+  // all others finished, so the descriptor and the cache are there.  The producer
+  // waits before it loads queries, after its first blocks of keys.
 
   // ---- this CTA's part of the line: [x0, x1) of `total`
   const int per = (p.n_reqs + C::THREADS - 1) / C::THREADS;
@@ -461,10 +450,10 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
   __syncthreads();
 
   if (!active) {
-    if (threadIdx.x == 0) p.rec[blockIdx.x * 8] = 0;
+    pdl_wait();   // (no CTA ends, and with it the grid, before the kernel before)
+    pdl_trigger();
   } else if (warp == 0) {
     // ------------------------------------------------ schedule, TMA producer
-    int32_t rec[5] = {0, 0, 0, 0, 0};
     int r = ct.start_req;
     bool bad;
     AbsReq q = ct.start;
@@ -473,7 +462,7 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
     int u = static_cast<int>(div64(x0 - ct.start_base, q.unit));   // the unit that x0 lies in
     int64_t base = ct.start_base + u * q.unit;
     int kcnt = 0, nseg = 0, quse = 0;   // (quse: lane 0's)
-    bool ok = true;
+    bool ok = true, waited = false;
     while (ok && base < x1) {
       auto cut = [&](int64_t x) {   // blocks of the unit that lie before x
         const int64_t d = x - base - kCostUnit;
@@ -484,13 +473,58 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
       };
       const int j0 = cut(x0), j1 = cut(x1);
       if (j1 > j0) {
-        const int first = owner(0), last_w = owner(q.nkb - 1);
         const int i0 = u * p.NT, toks = min(p.NT, q.n - i0);
         const int32_t *table = p.bt + q.b0;
         const int n_pages = (q.kv + kPage - 1) / kPage;
-        auto page_of = [&](int blk) { return lane < 4 && 4 * blk + lane < n_pages ? table[4 * blk + lane] : 0; };
-        int cur = page_of(j0), nxt = j0 + 1 < j1 ? page_of(j0 + 1) : 0;
+        // Page ids, one per lane 0 to 3, of the block to be sent and the kAhead
+        // behind it, which are on their way to L2.
+        auto page_of = [&](int blk) {
+          int pg = lane < 4 && blk < j1 && 4 * blk + lane < n_pages ? table[4 * blk + lane] : -1;
+          if (lane < 4 && blk < j1 && 4 * blk + lane < n_pages && (pg < 0 || pg >= p.num_pages)) {
+            atomicExch(p.err, kErrBounds);
+            pg = 0;
+          }
+          return pg;
+        };
+        int pages[kAhead + 1], nxt;
+#pragma unroll
+        for (int k = 0; k <= kAhead; ++k) pages[k] = page_of(j0 + k);
+        nxt = page_of(j0 + kAhead + 1);
+#pragma unroll
+        for (int k = 1; k <= kAhead; ++k)
+          if (pages[k] >= 0) tma_prefetch_5d(&tmK, 0, 0, 0, 0, pages[k]);
+        int j = j0;
+        auto send = [&]() {   // block j
+          const int np = min(4, n_pages - 4 * j), st = kcnt % C::NST, cur = pages[0];
+          if (lane == 0) ok = mbar_wait(&ct.k_empty[st][0], ((kcnt / C::NST) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer);
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) return;
+          if (lane == 0) mbar_arrive_expect_tx(&ct.k_full[st], np * C::PAGE_BYTES);
+          __syncwarp();
+#pragma unroll 1
+          for (int k = 0; k < np; ++k) {
+            // (past the first, a page that is not given back in time is drained below)
+            if (k > 0) ok = __all_sync(0xffffffffu, mbar_wait(&ct.k_empty[st][k], ((kcnt / C::NST) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer));
+            if (!ok) return;
+            if (lane == k)
+              tma_load_5d(sK + st * C::STAGE + lane * C::PAGE_BYTES, &tmK, &ct.k_full[st], 0, 0, 0, 0, cur);
+          }
+          ++kcnt;
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) pages[k] = pages[k + 1];
+          pages[kAhead] = nxt;
+          if (nxt >= 0) tma_prefetch_5d(&tmK, 0, 0, 0, 0, nxt);
+          nxt = page_of(j + kAhead + 2);
+          ++j;
+        };
+        if (!waited) {   // the first blocks, before the kernel before has ended
+          while (ok && j < j1 && j - j0 < C::NST) send();
+          pdl_wait();
+          pdl_trigger();
+          waited = true;
+        }
         // the query tile
+        const int first = owner(0), last_w = owner(q.nkb - 1);
         if (lane == 0) {
           ok = mbar_wait(&ct.q_empty, (quse & 1) ^ 1, abort_flag, p.err, kErrWaitProducer);
           if (ok) {
@@ -521,28 +555,9 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
         ++nseg;
-        if (first != last_w && cta == first) {
-          rec[0] = last_w - first + 1;
-          rec[1] = q.t0 + i0;
-          rec[2] = toks;
-        }
-        for (int j = j0; j < j1 && ok; ++j) {
-          const int np = min(4, n_pages - 4 * j), st = kcnt % C::NST;
-          const int after = j + 2 < j1 ? page_of(j + 2) : 0;
-          ok = __all_sync(0xffffffffu, mbar_wait(&ct.k_empty[st], ((kcnt / C::NST) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer));
-          if (!ok) break;
-          if (lane < np && (cur < 0 || cur >= p.num_pages)) {
-            atomicExch(p.err, kErrBounds);
-            cur = 0;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(&ct.k_full[st], np * C::PAGE_BYTES);
-          __syncwarp();
-          if (lane < np)
-            tma_load_5d(sK + st * C::STAGE + lane * C::PAGE_BYTES, &tmK, &ct.k_full[st], 0, 0, 0, 0, cur);
-          ++kcnt;
-          cur = nxt;
-          nxt = after;
-        }
+        if (cta == first && ht == 0)
+          for (int i = lane; i < toks; i += 32) p.tok[q.t0 + i0 + i] = {last_w - first + 1, first, i, 0};
+        while (ok && j < j1) send();
       }
       // the next unit on the line
       base += q.unit;
@@ -557,6 +572,7 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
         if (r >= p.n_reqs) break;
       }
     }
+    if (!waited) pdl_wait();
     if (lane == 0) {
       if (ok) {
         const int ss = nseg % C::NSEG;
@@ -565,8 +581,6 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
           mbar_arrive(&ct.seg_full[ss]);
         }
       }
-#pragma unroll
-      for (int k = 0; k < 3; ++k) p.rec[blockIdx.x * 8 + k] = rec[k];
       // after an abort, let copies in flight land before the CTA exits (bounded)
       if (!ok || *abort_flag) {
         const uint64_t t_start = globaltimer();
@@ -578,120 +592,75 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
         if (quse > 0) drain(&ct.q_full, quse - 1);
       }
     }
-  } else if (warp == 1) {
-    // --------------------------------------------------------- MMA issuer
-    // S of a block goes out as soon as it (and Q) landed and the product of the
-    // block two before it is issued (its S buffer is then read); O^T as soon as
-    // P is written.  S runs on into the next piece.  The whole warp keeps the
-    // books, in step, and one elected lane issues.
-    const uint64_t qd0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
-    const uint64_t kd0 = sdesc_sw128(smem_u32(sK), 16, C::ATOM);
-    const uint64_t vd0 = sdesc_sw128(smem_u32(sK), 1024, C::ATOM);
-    const uint64_t pd0 = sdesc_sw128(smem_u32(sP), 16, 1024);
-    const uint32_t idesc_pv = idesc_bf16_ab(128, p.N, true, false);
-    int s_seg = 0, s_item = 0, s_nb = 0, s_lb = 0, s_q = 0;     // S: piece, block, blocks of the piece and place in it
-    int v_seg = 0, v_item = 0, v_nb = 0, v_lb = 0;              // O^T
-    bool s_in = false, v_in = false, s_end = false;
-    uint64_t t_idle = 0;
-    auto uni = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
-    auto ready = [](uint64_t *bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_test_wait(smem_u32(bar), parity)) != 0;
-    };
-    for (uint32_t spin = 1;; ++spin) {   // rounds without progress
-      bool progress = false;
-      if (!s_end && s_item < v_item + 2) {
-        if (!s_in && ready(&ct.seg_full[s_seg % C::NSEG], (s_seg / C::NSEG) & 1)) {
-          s_nb = uni(ct.seg[s_seg % C::NSEG].nb);
-          s_lb = 0;
-          s_in = true;
-          if (s_nb == 0) s_end = true;
-        }
-        if (s_in && !s_end) {
-          const int st = s_item % C::NST;
-          if ((s_lb > 0 || ready(&ct.q_full, s_q & 1)) && ready(&ct.k_full[st], (s_item / C::NST) & 1)) {
+  } else if (warp <= 2) {
+    // --------------------------------------------------------- MMA issuers
+    // Warp 1 issues S, a block ahead of the softmax (two buffers) and on into the
+    // next piece, warp 2 the products with V: neither's commits and waits hold
+    // up the other.
+    if (lane == 0) {
+      auto wait = [&](uint64_t *bar, uint32_t par) { return mbar_wait(bar, par, abort_flag, p.err, kErrWaitMma); };
+      const uint64_t kd0 = sdesc_sw128(smem_u32(sK), 16, C::ATOM);
+      const uint64_t qd0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t vd0 = sdesc_sw128(smem_u32(sK), 1024, C::ATOM);
+      const uint64_t pd0 = sdesc_sw128(smem_u32(sP), 16, 1024);
+      const uint32_t idesc_pv = idesc_bf16_ab(128, p.N, true, false);
+      int nseg = 0, item = 0;
+      bool ok = true;
+      while (ok) {
+        const int ss = nseg % C::NSEG;
+        ok = wait(&ct.seg_full[ss], (nseg / C::NSEG) & 1);
+        if (!ok) break;
+        const int nb = ct.seg[ss].nb;
+        if (nb == 0) break;
+        if (warp == 1) ok = wait(&ct.q_full, nseg & 1);
+        for (int lb = 0; lb < nb && ok; ++lb, ++item) {
+          const int st = item % C::NST;
+          if (warp == 1) {
+            ok = wait(&ct.k_full[st], (item / C::NST) & 1) && wait(&ct.s_empty[item & 1], ((item >> 1) & 1) ^ 1);
+            if (!ok) break;
             tc_fence_after();
-            const uint32_t d = tmem + 64 * (s_item & 1);
+            const uint32_t d = tmem + 64 * (item & 1);
             const uint64_t kd = kd0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
-            const bool last_blk = s_lb == s_nb - 1;
-            if (elect_one()) {
 #pragma unroll
-              for (int ch = 0; ch < C::NC; ++ch)
+            for (int ch = 0; ch < C::NC; ++ch)
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  mma_bf16(d, qd0 + ((ch * C::Q_CHUNK + kk * 32) >> 4), kd + ((ch * 1024 + kk * 32) >> 4), C::IDESC_S,
-                           (ch > 0 || kk > 0) ? 1u : 0u);
-              mma_commit(&ct.s_full[s_item & 1]);
-              if (last_blk) mma_commit(&ct.q_empty);
-            }
-            __syncwarp();
-            ++s_item;
-            if (++s_lb == s_nb) {
-              s_in = false;
-              ++s_seg;
-              ++s_q;
-            }
-            progress = true;
-          }
-        }
-      }
-      if (v_item < s_item) {
-        if (!v_in) {   // S of the piece is out: its record is there
-          v_nb = uni(ct.seg[v_seg % C::NSEG].nb);
-          v_lb = 0;
-          v_in = true;
-        }
-        if (ready(&ct.p_full, v_item & 1)) {
-          tc_fence_after();
-          const int st = v_item % C::NST;
-          const uint64_t vd = vd0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
-          if (elect_one()) {
+              for (int kk = 0; kk < 4; ++kk)
+                mma_bf16(d, qd0 + ((ch * C::Q_CHUNK + kk * 32) >> 4), kd + ((ch * 1024 + kk * 32) >> 4), C::IDESC_S,
+                         (ch > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(&ct.s_full[item & 1]);
+            if (lb + 1 == nb) mma_commit(&ct.q_empty);
+          } else {
+            ok = wait(&ct.p_full, item & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t vd = vd0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
 #pragma unroll
-            for (int ks = 0; ks < kBlk / 16; ++ks)   // 16 keys (two atoms) per MMA; 128 numbers are two chunks
+            for (int ks = 0; ks < kBlk / 16; ++ks) {   // 16 keys (a page) per MMA; 128 numbers are two chunks
 #pragma unroll
               for (int dt = 0; dt < C::DT; ++dt)
                 mma_bf16(tmem + C::O_COL + 64 * dt, vd + ((ks * 2 * C::ATOM + dt * 2048) >> 4), pd0 + ((ks * 32) >> 4),
-                         idesc_pv, (v_lb > 0 || ks > 0) ? 1u : 0u);
+                         idesc_pv, (lb > 0 || ks > 0) ? 1u : 0u);
+              mma_commit(&ct.k_empty[st][ks]);
+            }
             mma_commit(&ct.pv_done);
-            mma_commit(&ct.k_empty[st]);
-            if (v_lb + 1 == v_nb) mbar_arrive(&ct.seg_empty[v_seg % C::NSEG]);
           }
-          __syncwarp();
-          ++v_item;
-          if (++v_lb == v_nb) {
-            v_in = false;
-            ++v_seg;
-          }
-          progress = true;
         }
+        if (!ok) break;
+        ++nseg;
+        mbar_arrive(&ct.seg_empty[ss]);
       }
-      if (s_end && v_item == s_item) break;
-      if (progress) {
-        spin = 0;
-        t_idle = 0;
-      } else if ((spin & 255u) == 0) {
-        if (t_idle == 0) t_idle = globaltimer();
-        const bool late = globaltimer() - t_idle > kWaitLimitNs;
-        if (__any_sync(0xffffffffu, late || *abort_flag)) {
-          if (__any_sync(0xffffffffu, late) && lane == 0) {
-            *abort_flag = 1;
-            atomicExch(p.err, kErrWaitMma);
-          }
-          break;
-        }
+      // every MMA issued above has completed before TMEM is freed
+      mma_commit(&ct.done);
+      const uint64_t t_end = globaltimer();
+      while (!mbar_try_wait(smem_u32(&ct.done), 0) && globaltimer() - t_end < kWaitLimitNs) {
       }
     }
-    // every MMA issued above has completed before TMEM is freed
-    if (elect_one()) mma_commit(&ct.done);
     __syncwarp();
-    const uint64_t t_end = globaltimer();
-    while (!mbar_try_wait(smem_u32(&ct.done), 0) && globaltimer() - t_end < kWaitLimitNs) {
-    }
-    __syncwarp();
-  } else {
+  } else if (warp >= 4) {
     // ------------------------------------------------- softmax / epilogue
     const int qu = warp & 3;                     // TMEM lane quarter: rows 16 qu .. 16 qu + 15 of S in its first 16 lanes
     const int row = qu * 16 + (lane & 15);
-    const int tid = (warp - 2) * 32 + lane;      // of the 128
+    const int tid = (warp - 4) * 32 + lane;      // of the 128
     const uint32_t lane_base = static_cast<uint32_t>(qu * 32) << 16;
     constexpr float kRescaleAbove = 8.f;         // log2 units
     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
@@ -723,6 +692,9 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
         if (!fail) {
           tc_fence_after();
           tmem_ld64(tmem + lane_base + 64 * (item & 1), sv);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ct.s_empty[item & 1]);
           const int vis = limit - key0;
           if (vis < kBlk - 1)
 #pragma unroll
@@ -799,30 +771,32 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
       wait(&ct.pv_done, (item - 1) & 1);
       if (named_bar_or(1, 128, fail)) break;
       tc_fence_after();
-      const int slot = sg.slot;
+      // (the rows of a tile are one after another in oc as in a partial: more
+      // than one token only if the tile has all heads)
+      const int slot = sg.slot, rows = min(sg.toks * p.Hc, p.H - ht * p.Hc + (sg.toks - 1) * p.Hc);
       if (lane < 16) {
-        int64_t at = -1;
-        if (live) at = slot < 0 ? (static_cast<int64_t>(sg.t0 + row_tok) * p.H + row_head) * RANK
-                                : (static_cast<int64_t>(slot) * 64 + row) * (RANK + 4);
-        ct.base[row] = at;
         if (live && sg.odd <= limit) l = NAN;
         ct.col[row] = 1.f / l;
-        if (live && slot >= 0) *reinterpret_cast<float2 *>(p.part + at + RANK) = make_float2(m_ref, l);
+        if (live && slot >= 0)
+          *reinterpret_cast<float2 *>(p.part + slot * part_floats(RANK) + 64 * RANK + 2 * row) = make_float2(m_ref, l);
       }
       named_bar_sync(1, 128);
-      const int rows = sg.toks * p.Hc;
 #pragma unroll 1
       for (int cc = 0; cc < C::DT * 64; cc += 32) {
         const int r0 = cc & 63, n = (cc >> 6) * 128 + qu * 32 + lane;   // rows from r0 on, number n of their vectors
         if (r0 >= rows) continue;
         float v[32];
         tmem_ld32(tmem + lane_base + C::O_COL + cc, v);
+        if (slot < 0) {
+          __nv_bfloat16 *dst = p.oc + (static_cast<int64_t>(sg.t0) * p.H + ht * p.Hc + r0) * RANK + n;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const int64_t at = ct.base[r0 + k];
-          if (at < 0) continue;
-          if (slot < 0) p.oc[at + n] = __float2bfloat16_rn(v[k] * ct.col[r0 + k]);
-          else p.part[at + n] = v[k];
+          for (int k = 0; k < 32; ++k)
+            if (r0 + k < rows) dst[k * RANK] = __float2bfloat16_rn(v[k] * ct.col[r0 + k]);
+        } else {
+          float *dst = p.part + slot * part_floats(RANK) + r0 * RANK + n;
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (r0 + k < rows) dst[k * RANK] = v[k];
         }
       }
       tc_fence_before();
@@ -841,72 +815,227 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
   }
 }
 
-// Merge of the units that were cut: CTA (x, y) takes every gridDim.y-th row
-// group of the unit whose first piece CTA x computed.
-//   o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,   M = max_s m_s
-template <int RANK>
-__global__ void __launch_bounds__(256) latent_merge_kernel(const __grid_constant__ AbsParams p) {
+// ----------------------------------------------------------- cut units' rows
+// oc[t][h] = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,  M = max_s m_s, for the
+// tokens whose unit was cut.  A kernel of its own, without shared memory: beside
+// 200 KB of it L1 has room for so few lines on their way that bringing the
+// pieces in within the next kernel took 5 to 14 us (3 here).  A warp takes a
+// row, or, where there are few rows, a quarter of one with more pieces in flight.
+template <int RANK, int SPLIT>
+__global__ void __launch_bounds__(256) latent_merge_kernel(const AbsParams p) {
+  constexpr int PER = RANK / 128 / SPLIT, AHEAD = 16 / PER > 8 ? 8 : 16 / PER;   // vectors of a lane; pieces in flight
   pdl_wait();
   pdl_trigger();
-  const int x = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ht = x % p.HT;
-  const int pieces = p.rec[x * 8], t0 = p.rec[x * 8 + 1], toks = p.rec[x * 8 + 2];
-  if (pieces == 0) return;
-  // piece 0 in slot 2 x + 1, piece s > 0 in slot 2 (x + s HT)
-  auto src = [&](int s, int row) {
-    return p.part + (static_cast<int64_t>(s == 0 ? 2 * x + 1 : 2 * (x + s * p.HT)) * 64 + row) * (RANK + 4);
-  };
-  constexpr int PER = RANK / 128;   // float4s of a lane: columns 4 (lane + 32 k)
-  for (int row = blockIdx.y * 8 + warp; row < toks * p.Hc; row += gridDim.y * 8) {
-    const int head = ht * p.Hc + row % p.Hc;
-    if (head >= p.H) continue;
-    float M = -INFINITY;
-    for (int s = lane; s < pieces; s += 32) M = fmaxf(M, src(s, row)[RANK]);
+  const int lane = threadIdx.x & 31;
+  const int64_t slot = part_floats(RANK), items = static_cast<int64_t>(p.T) * p.H * SPLIT;
+  for (int64_t item = blockIdx.x * 8 + (threadIdx.x >> 5); item < items; item += gridDim.x * 8) {
+    const int64_t row = item / SPLIT;
+    const int t = static_cast<int>(row / p.H), h = static_cast<int>(row % p.H);
+    const TokRec rec = p.tok[t];
+    const int pieces = rec.pieces, col0 = static_cast<int>(item % SPLIT) * (RANK / SPLIT) + 4 * lane;   // and + 128 k
+    if (pieces <= 1) continue;
+    // piece 0 in slot 2 x0 + 1, piece s > 0 in slot 2 (x0 + s HT)
+    const int x0 = rec.first * p.HT + h / p.Hc;
+    const int place = rec.place * p.Hc + h % p.Hc;
+    const float *base = p.part + (2 * x0 + 1) * slot;
+    auto src = [&](int s) { return base + (s == 0 ? 0 : (2 * s * p.HT - 1) * slot); };
+    float2 ml[AHEAD];
+    float4 v[AHEAD][PER];
+    auto fetch = [&](int s0) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    float L = 0.f;
+      for (int s = 0; s < AHEAD; ++s) {
+        ml[s] = make_float2(-INFINITY, 0.f);
+        if (s0 + s < pieces) {
+          ml[s] = *reinterpret_cast<const float2 *>(src(s0 + s) + 64 * RANK + 2 * place);
+#pragma unroll
+          for (int k = 0; k < PER; ++k) v[s][k] = *reinterpret_cast<const float4 *>(src(s0 + s) + place * RANK + col0 + 128 * k);
+        }
+      }
+    };
+    fetch(0);
+    float M = -INFINITY, L = 0.f;
     float4 acc[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int s = 0; s < pieces; ++s) {
-      const float *f = src(s, row);
-      const float2 ml = *reinterpret_cast<const float2 *>(f + RANK);
-      const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+    for (int s0 = 0; s0 < pieces; s0 += AHEAD) {
+      float top = M;
+#pragma unroll
+      for (int s = 0; s < AHEAD; ++s) top = fmaxf(top, ml[s].x);
+      const float old = M == -INFINITY ? 0.f : ex2_approx(M - top);
       // (a sum that is NaN says that the row saw one; a piece of which it saw
       // nothing has a sum of 0)
-      L += ml.x == -INFINITY ? ml.y : w * ml.y;
+      L = M == -INFINITY ? L : L * old;
 #pragma unroll
       for (int k = 0; k < PER; ++k) {
-        const float4 v = reinterpret_cast<const float4 *>(f)[lane + 32 * k];
-        acc[k].x = fmaf(w, v.x, acc[k].x);
-        acc[k].y = fmaf(w, v.y, acc[k].y);
-        acc[k].z = fmaf(w, v.z, acc[k].z);
-        acc[k].w = fmaf(w, v.w, acc[k].w);
+        acc[k].x *= old;
+        acc[k].y *= old;
+        acc[k].z *= old;
+        acc[k].w *= old;
       }
+#pragma unroll
+      for (int s = 0; s < AHEAD; ++s) {
+        const float w = ml[s].x == -INFINITY ? 0.f : ex2_approx(ml[s].x - top);
+        L += ml[s].x == -INFINITY ? ml[s].y : w * ml[s].y;
+        if (w != 0.f)   // (0: no such piece, or the row saw nothing in it)
+#pragma unroll
+          for (int k = 0; k < PER; ++k) {
+            acc[k].x = fmaf(w, v[s][k].x, acc[k].x);
+            acc[k].y = fmaf(w, v[s][k].y, acc[k].y);
+            acc[k].z = fmaf(w, v[s][k].z, acc[k].z);
+            acc[k].w = fmaf(w, v[s][k].w, acc[k].w);
+          }
+      }
+      M = top;
+      if (s0 + AHEAD < pieces) fetch(s0 + AHEAD);
     }
     const float inv = 1.f / L;
-    uint2 *dst = reinterpret_cast<uint2 *>(p.oc + (static_cast<int64_t>(t0 + row / p.Hc) * p.H + head) * RANK);
+    uint2 *dst = reinterpret_cast<uint2 *>(p.oc + row * RANK + col0);
 #pragma unroll
     for (int k = 0; k < PER; ++k)
-      dst[lane + 32 * k] = make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv), pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+      dst[32 * k] = make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv), pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+  }
+}
+
+// ------------------------------------------------------------- the outputs
+// o[t][h] = W_uv,h oc[t][h]: one CTA makes TR tokens of one head, as D = W_uv (M =
+// hd) times the tokens' rows (N = TR), K = rank, all of it in shared memory.
+// W_uv is loaded before the wait for the rows.
+template <int HD, int RANK, int TR>
+struct OutCfg {
+  static constexpr int KC = RANK / 64;
+  static constexpr int W_CHUNK = HD * 128;
+  static constexpr int X_CHUNK = TR * 128;
+  static constexpr int OFF_X = KC * W_CHUNK;
+  static constexpr int OFF_CTRL = OFF_X + KC * X_CHUNK;
+  static constexpr int SMEM = OFF_CTRL + 256;
+  static constexpr uint32_t IDESC = idesc_bf16(HD, TR, false);
+};
+
+struct OutParams {
+  const TokRec *tok;
+  __nv_bfloat16 *o;
+  int T, H;
+  int *err;
+};
+
+template <int HD, int RANK, int TR>
+__global__ void __launch_bounds__(128, 1)
+    latent_out_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const OutParams p) {
+  using C = OutCfg<HD, RANK, TR>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  static_assert(C::SMEM <= 232448, "shared memory");
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_CTRL), *done = full + C::KC;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  uint8_t *live = smem + C::OFF_CTRL + 128;   // [TR]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = blockIdx.x, t0 = blockIdx.y * TR;
+  if (smem_u32(smem) & 1023u) {   // the swizzled layouts need a 1024-aligned base
+    pdl_wait();
+    if (tid == 0) atomicExch(p.err, kErrBounds);
+    return;
+  }
+  if (tid == 0) {
+    for (int c = 0; c < C::KC; ++c) mbar_init(&full[c], 1);
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    for (int c = 0; c < C::KC; ++c) {
+      mbar_arrive_expect_tx(&full[c], C::W_CHUNK + C::X_CHUNK);
+      tma_load_2d(smem + c * C::W_CHUNK, &tmW, &full[c], 64 * c, (2 * h + 1) * HD);
+    }
+    prefetch_tmap(&tmX);
+  }
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, TR);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();   // the rows are the kernel before's
+  pdl_trigger();
+  if (tid == 0) {
+    for (int c = 0; c < C::KC; ++c) tma_load_3d(smem + C::OFF_X + c * C::X_CHUNK, &tmX, &full[c], 64 * c, h, t0);
+    const uint64_t w0 = sdesc_sw128(smem_u32(smem), 16, 1024), x0 = sdesc_sw128(smem_u32(smem + C::OFF_X), 16, 1024);
+#pragma unroll 1
+    for (int c = 0; c < C::KC; ++c) {
+      if (!mbar_wait(&full[c], 0, abort_flag, p.err, kErrWaitMma)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_bf16(tmem, w0 + ((c * C::W_CHUNK + kk * 32) >> 4), x0 + ((c * C::X_CHUNK + kk * 32) >> 4), C::IDESC,
+                 (c > 0 || kk > 0) ? 1u : 0u);
+    }
+    mma_commit(done);
+  } else if (tid >= 128 - TR) {
+    const int k = tid - (128 - TR);
+    live[k] = t0 + k < p.T && p.tok[t0 + k].pieces > 0;
+  }
+  __syncthreads();
+  bool ok = mbar_wait(done, 0, abort_flag, p.err, kErrWaitEpilogue);
+  ok = __all_sync(0xffffffffu, ok) && !*abort_flag;
+  if (ok) {
+    tc_fence_after();
+    // (with M = 64 a quarter's rows are its first 16 lanes)
+    const int dim = HD == 128 ? warp * 32 + lane : warp * 16 + lane;
+#pragma unroll 1
+    for (int c0 = 0; c0 < TR; c0 += 32) {
+      float v[32];
+      tmem_ld32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c0, v);
+      __nv_bfloat16 *dst = p.o + (static_cast<int64_t>(t0 + c0) * p.H + h) * HD + dim;
+      const int64_t step = static_cast<int64_t>(p.H) * HD;
+      if (HD == 128 || lane < 16)
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          if (live[c0 + k]) dst[k * step] = __float2bfloat16_rn(v[k]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, TR);
   }
 }
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-template <int KC, int BN, bool BMN>
-cudaError_t launch_head_gemm(const void *A, int64_t a_heads, int64_t a_row, const void *W, int64_t w_rows, int64_t w_cols,
-                             const HeadParams &p, cudaStream_t st) {
-  using C = HeadCfg<KC, BN, BMN>;
-  CUtensorMap ta, tb;
-  const uint64_t da[3] = {static_cast<uint64_t>(a_row), static_cast<uint64_t>(a_heads), static_cast<uint64_t>(p.T)};
-  const uint64_t sa[2] = {static_cast<uint64_t>(a_row) * 2, static_cast<uint64_t>(a_row) * 2 * a_heads};
-  const uint32_t ba[3] = {64, 1, 128};
-  cudaError_t e = encode_tmap(&ta, A, 3, da, sa, ba);
-  if (e == cudaSuccess) e = encode_tmap_2d(&tb, W, w_cols, w_rows, w_cols * 2, 64, BMN ? 64 : BN);
-  if (e == cudaSuccess) e = ensure_max_smem(reinterpret_cast<const void *>(head_gemm_kernel<KC, BN, BMN>), C::SMEM);
+template <int HD>
+cudaError_t launch_query(const LatentArgs &a, const QueryParams &p, cudaStream_t st) {
+  using C = QueryCfg<HD>;
+  CUtensorMap tq, tw;
+  const uint64_t H = a.H, W = HD + kLatentRope;
+  const uint64_t dq[3] = {W, H, static_cast<uint64_t>(a.T)}, sq[2] = {W * 2, W * 2 * H};
+  const uint32_t bq[3] = {64, 1, 128};
+  cudaError_t e = encode_tmap(&tq, a.q, 3, dq, sq, bq);
+  if (e == cudaSuccess) e = encode_tmap_2d(&tw, a.w_kv, a.rank, H * 2 * HD, static_cast<uint64_t>(a.rank) * 2, 64, 64);
+  if (e == cudaSuccess) e = ensure_max_smem(reinterpret_cast<const void *>(latent_query_kernel<HD>), C::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl(head_gemm_kernel<KC, BN, BMN>, dim3(p.N / BN, p.H, (p.T + 127) / 128), dim3(128), C::SMEM, st, 1, ta, tb, p);
+  return launch_pdl(latent_query_kernel<HD>, dim3(a.rank / kQueryN, a.H, (a.T + 127) / 128), dim3(128), C::SMEM, st, 1, tq, tw, p);
+}
+
+template <int HD, int RANK, int TR>
+cudaError_t launch_out(const LatentArgs &a, const void *oc, const OutParams &p, cudaStream_t st) {
+  using C = OutCfg<HD, RANK, TR>;
+  CUtensorMap tw, tx;
+  const uint64_t H = a.H;
+  const uint64_t dx[3] = {RANK, H, static_cast<uint64_t>(a.T)}, sx[2] = {RANK * 2, RANK * 2 * H};
+  const uint32_t bx[3] = {64, 1, TR};
+  cudaError_t e = encode_tmap_2d(&tw, a.w_kv, RANK, H * 2 * HD, RANK * 2, 64, HD);
+  if (e == cudaSuccess) e = encode_tmap(&tx, oc, 3, dx, sx, bx);
+  if (e == cudaSuccess) e = ensure_max_smem(reinterpret_cast<const void *>(latent_out_kernel<HD, RANK, TR>), C::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(latent_out_kernel<HD, RANK, TR>, dim3(a.H, (a.T + TR - 1) / TR), dim3(128), C::SMEM, st, 1, tw, tx, p);
+}
+
+// Tiles of 32 tokens while their CTAs fit the SMs at once, else of 64.
+template <int HD, int RANK>
+cudaError_t launch_out(const LatentArgs &a, const void *oc, const OutParams &p, cudaStream_t st) {
+  return static_cast<int64_t>(a.H) * ((a.T + 31) / 32) <= device_sm_count() ? launch_out<HD, RANK, 32>(a, oc, p, st)
+                                                                            : launch_out<HD, RANK, 64>(a, oc, p, st);
 }
 
 template <int RANK>
@@ -927,8 +1056,12 @@ cudaError_t launch_attention(const LatentArgs &a, AbsParams &p, const void *qc, 
   if (e != cudaSuccess) return e;
   const int ctas = std::min(device_sm_count(), kMaxCtas) / p.HT * p.HT;
   e = launch_pdl(latent_attention_kernel<RANK>, dim3(ctas), dim3(C::THREADS), C::SMEM, st, 1, tq, tr, tk, p);
-  if (e == cudaSuccess) e = launch_pdl(latent_merge_kernel<RANK>, dim3(ctas, 4), dim3(256), 0, st, 1, p);
-  return e;
+  if (e != cudaSuccess) return e;
+  // a warp a row, or several where all fit the SMs at once (8 warps a CTA, 2 CTAs an SM)
+  const int64_t rows = static_cast<int64_t>(a.T) * a.H, room = 2ll * device_sm_count();
+  if (rows * (RANK / 128) <= room * 8)
+    return launch_pdl(latent_merge_kernel<RANK, RANK / 128>, dim3(static_cast<unsigned>((rows * (RANK / 128) + 7) / 8)), dim3(256), 0, st, 1, p);
+  return launch_pdl(latent_merge_kernel<RANK, 1>, dim3(static_cast<unsigned>(std::min((rows + 7) / 8, room))), dim3(256), 0, st, 1, p);
 }
 
 }  // namespace
@@ -958,17 +1091,17 @@ cudaError_t latent_append_run(const LatentAppendArgs &a, cudaStream_t st) {
   return launch_pdl(latent_append_kernel, dim3(a.T), dim3(kAppendThreads), 0, st, 1, p);
 }
 
-// q through W_uk [T][H][rank], sum_j p_j c_j [T][H][rank], which rows are live [T], the records, the partials
+// q through W_uk [T][H][rank], sum_j p_j c_j [T][H][rank], the tokens' records, the partials
 size_t latent_attention_workspace_bytes(int64_t T, int64_t H, int64_t rank) {
-  return 2 * align256(static_cast<size_t>(T) * H * rank * 2) + align256(T) + kRecBytes +
-         static_cast<size_t>(2) * kMaxCtas * 64 * (rank + 4) * sizeof(float);
+  return 2 * align256(static_cast<size_t>(T) * H * rank * 2) + align256(static_cast<size_t>(T) * sizeof(TokRec)) +
+         static_cast<size_t>(2) * kMaxCtas * part_floats(rank) * sizeof(float);
 }
 
 cudaError_t latent_attention_run(const LatentArgs &a, cudaStream_t st) {
   uint8_t *w = static_cast<uint8_t *>(a.workspace);
   const size_t rows = align256(static_cast<size_t>(a.T) * a.H * a.rank * 2);
   __nv_bfloat16 *qc = reinterpret_cast<__nv_bfloat16 *>(w), *oc = reinterpret_cast<__nv_bfloat16 *>(w + rows);
-  uint8_t *live = w + 2 * rows;
+  TokRec *tok = reinterpret_cast<TokRec *>(w + 2 * rows);
   AbsParams p;
   p.oc = oc;
   p.pool = static_cast<const __nv_bfloat16 *>(a.pool);
@@ -985,33 +1118,16 @@ cudaError_t latent_attention_run(const LatentArgs &a, cudaStream_t st) {
   p.N = (p.NT * p.Hc + 15) / 16 * 16;
   p.num_pages = a.num_pages;
   p.scale_log2 = a.scale * kLog2e;
-  p.rec = reinterpret_cast<int32_t *>(live + align256(a.T));
-  p.part = reinterpret_cast<float *>(live + align256(a.T) + kRecBytes);
+  p.tok = tok;
+  p.part = reinterpret_cast<float *>(w + 2 * rows + align256(static_cast<size_t>(a.T) * sizeof(TokRec)));
   p.err = a.err;
-  HeadParams h;
-  h.C = qc;
-  h.live = live;
-  h.qo_indptr = a.qo_indptr;
-  h.kv_len = a.kv_len;
-  h.bt_indptr = a.bt_indptr;
-  h.n_reqs = a.n_reqs;
-  h.T = a.T;
-  h.H = a.H;
-  h.N = a.rank;
-  h.a_col = 0;
-  h.b_row = 0;
-  h.b_rows = 2 * a.hd;
-  h.err = a.err;
-  const int64_t w_rows = static_cast<int64_t>(a.H) * 2 * a.hd;
-  cudaError_t e = a.hd == 128 ? launch_head_gemm<2, 128, true>(a.q, a.H, a.hd + kLatentRope, a.w_kv, w_rows, a.rank, h, st)
-                              : launch_head_gemm<1, 128, true>(a.q, a.H, a.hd + kLatentRope, a.w_kv, w_rows, a.rank, h, st);
+  const QueryParams qp = {qc, tok, a.T, a.H, a.rank, a.err};
+  cudaError_t e = a.hd == 128 ? launch_query<128>(a, qp, st) : launch_query<64>(a, qp, st);
   if (e == cudaSuccess) e = a.rank == 512 ? launch_attention<512>(a, p, qc, st) : launch_attention<256>(a, p, qc, st);
   if (e != cudaSuccess) return e;
-  h.C = static_cast<__nv_bfloat16 *>(a.o);
-  h.N = a.hd;
-  h.b_row = a.hd;
-  return a.rank == 512 ? launch_head_gemm<8, 64, false>(oc, a.H, a.rank, a.w_kv, w_rows, a.rank, h, st)
-                       : launch_head_gemm<4, 64, false>(oc, a.H, a.rank, a.w_kv, w_rows, a.rank, h, st);
+  const OutParams op = {tok, static_cast<__nv_bfloat16 *>(a.o), a.T, a.H, a.err};
+  if (a.hd == 128) return a.rank == 512 ? launch_out<128, 512>(a, oc, op, st) : launch_out<128, 256>(a, oc, op, st);
+  return a.rank == 512 ? launch_out<64, 512>(a, oc, op, st) : launch_out<64, 256>(a, oc, op, st);
 }
 
 }  // namespace mb

@@ -420,14 +420,17 @@ struct PreCfg {
   static constexpr int QT_BYTES = KU * UNIT;
   // One ring for keys and values, in the order they are used (K of a block, then
   // its V): 128 KB hold 1.6 blocks, where rings of their own would leave values
-  // a single stage.
+  // a single stage.  K of block b takes the places of K and V of blocks b - KB
+  // and b - VB and of what lies between, V of block b those of K of block b - VK.
   static constexpr int NU = HD == 128 ? 8 : 10;
+  static constexpr int KB = HD == 128 ? 2 : 3, VB = HD == 128 ? 2 : 4, VK = HD == 128 ? 1 : 3;
+  static constexpr int NB = 4;                        // barriers per kind, by block
   static constexpr int NSEG = 4;
   static constexpr int OFF_R = 2 * QT_BYTES;
   static constexpr int OFF_CTRL = OFF_R + NU * UNIT;
   static constexpr int OFF_ML = OFF_CTRL + 1024;      // (m, l) of 128 rows, from one warp group to the other
   static constexpr int SMEM = OFF_ML + 1024;
-  static constexpr int THREADS = 320;                 // TMA, MMA, 2 x 4 softmax warps
+  static constexpr int THREADS = 384;                 // TMA, 2 MMA issuers, one idle, 2 x 4 softmax warps
   static constexpr uint32_t IDESC_S = idesc_bf16(128, 128, false);
   static constexpr uint32_t IDESC_PV = idesc_bf16(128, HD, true);
   static constexpr uint32_t TMEM_COLS = 512;          // S/P buffers at 0 and 128, O of the two groups from 256
@@ -452,11 +455,12 @@ template <int HD>
 struct PreCtrl {
   using C = PreCfg<HD>;
   uint64_t q_full[2], q_empty[2];
-  uint64_t full[C::NU], empty[C::NU];
+  uint64_t k_full[C::NB], k_empty[C::NB], v_full[C::NB], v_empty[C::NB];   // by block; empty: both groups are done with it
   uint64_t s_full[2], p_full[2], o_full[2];   // by warp group
   uint64_t ml_full[2];    // the group's (m, l) are in shared memory
   uint64_t ml_empty[2];   // the other group has read them and this group's O
   uint64_t seg_full[C::NSEG], seg_empty[C::NSEG];
+  uint64_t turn[2];       // the first tile's P of a piece's first block is written (pieces of two tiles, in turn)
   uint64_t done;
   PreSeg seg[C::NSEG];
   int64_t sums[C::THREADS / 32];
@@ -537,22 +541,25 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ct.q_full[b], 1);
-      mbar_init(&ct.q_empty[b], 1);
+      mbar_init(&ct.q_empty[b], 2);
       mbar_init(&ct.s_full[b], 1);
       mbar_init(&ct.p_full[b], 128);
       mbar_init(&ct.o_full[b], 1);
       mbar_init(&ct.ml_full[b], 128);
       mbar_init(&ct.ml_empty[b], 128);
     }
-    for (int s = 0; s < C::NU; ++s) {
-      mbar_init(&ct.full[s], 1);
-      mbar_init(&ct.empty[s], 1);
+    for (int s = 0; s < C::NB; ++s) {
+      mbar_init(&ct.k_full[s], 1);
+      mbar_init(&ct.k_empty[s], 2);
+      mbar_init(&ct.v_full[s], 1);
+      mbar_init(&ct.v_empty[s], 2);
     }
     for (int s = 0; s < C::NSEG; ++s) {
       mbar_init(&ct.seg_full[s], 1);
-      mbar_init(&ct.seg_empty[s], 9);   // the MMA issuer and the 8 softmax warps
+      mbar_init(&ct.seg_empty[s], 10);   // the 2 MMA issuers and the 8 softmax warps
     }
-    mbar_init(&ct.done, 1);
+    for (int b = 0; b < 2; ++b) mbar_init(&ct.turn[b], 1);
+    mbar_init(&ct.done, 2);
     ct.abort = 0;
     ct.start_req = -1;
     fence_mbar_init();
@@ -636,16 +643,14 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
         u = lo;
         base += units_cost(q.a, u);
       }
-      int cnt = 0, nseg = 0, quse[2] = {0, 0}, qsel = 0;
-      bool ok = true;
-      // a 128 x 64 part of the keys or values: columns x .. x + 63 of row y of `map`
-      auto send = [&](const CUtensorMap *map, int x, int y) {
-        const int st = cnt % C::NU;
-        if (!mbar_wait(&ct.empty[st], ((cnt / C::NU) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer)) return false;
-        mbar_arrive_expect_tx(&ct.full[st], C::UNIT);
-        tma_load_2d(sR + st * C::UNIT, map, &ct.full[st], x, y);
-        ++cnt;
-        return true;
+      int blk = 0, nseg = 0, quse[2] = {0, 0}, qsel = 0;
+      bool ok = true, k_sent = false;
+      auto freed = [&](uint64_t *empty, int b) {   // block b (if there is one) of a kind has been used
+        return b < 0 || mbar_wait(&empty[b % C::NB], (b / C::NB) & 1, abort_flag, p.err, kErrWaitProducer);
+      };
+      // 128 x 64 parts of keys or values: columns x .. x + 63 of row y of `map` to place u of the ring
+      auto part = [&](int u, const CUtensorMap *map, uint64_t *full, int x, int y) {
+        tma_load_2d(sR + (u % C::NU) * C::UNIT, map, full, x, y);
       };
       while (ok && base < x1) {
         // the unit (hg, u) of request r, on the line from `base`
@@ -697,10 +702,19 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
             rec[3] = rows;
           }
           if (qt == 1) qsel ^= 1;
-          for (int j = j0; j < j1 && ok; ++j) {
-            for (int ch = 0; ch < C::KU - 1 && ok; ++ch) ok = send(&tmKV, 64 * ch, krow + kBlk * j);
-            if (ok) ok = send(&tmR, 0, rrow + kBlk * j);
-            for (int ch = 0; ch < C::VU && ok; ++ch) ok = send(&tmKV, HD + 64 * ch, krow + kBlk * j);
+          for (int j = j0; j < j1 && ok; ++j, ++blk) {
+            const int u0 = blk * (C::KU + C::VU), sb = blk % C::NB;
+            k_sent = false;
+            ok = freed(ct.k_empty, blk - C::KB) && freed(ct.v_empty, blk - C::VB);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&ct.k_full[sb], C::KU * C::UNIT);
+            for (int ch = 0; ch < C::KU - 1; ++ch) part(u0 + ch, &tmKV, &ct.k_full[sb], 64 * ch, krow + kBlk * j);
+            part(u0 + C::KU - 1, &tmR, &ct.k_full[sb], 0, rrow + kBlk * j);
+            k_sent = true;
+            ok = freed(ct.k_empty, blk - C::VK);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&ct.v_full[sb], C::VU * C::UNIT);
+            for (int ch = 0; ch < C::VU; ++ch) part(u0 + C::KU + ch, &tmKV, &ct.v_full[sb], HD + 64 * ch, krow + kBlk * j);
           }
         }
         // the next unit on the line
@@ -736,167 +750,106 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
           while (!mbar_try_wait(smem_u32(bar), use & 1) && globaltimer() - t_start < kWaitLimitNs) {
           }
         };
-        for (int i = max(0, cnt - C::NU); i < cnt; ++i) drain(&ct.full[i % C::NU], i / C::NU);
+        for (int b = max(0, blk - C::NB); b < blk; ++b) {
+          drain(&ct.k_full[b % C::NB], b / C::NB);
+          drain(&ct.v_full[b % C::NB], b / C::NB);
+        }
+        if (!ok && k_sent) drain(&ct.k_full[blk % C::NB], blk / C::NB);
         for (int b = 0; b < 2; ++b)
           if (quse[b] > 0) drain(&ct.q_full[b], quse[b] - 1);
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // --------------------------------------------------------- MMA issuer
-    // Items in order: block by block, tile by tile.  S of an item goes out
-    // as soon as its K (and Q) landed and the P V before the last one is
-    // issued (its S buffer is then free, in order); P V as soon as P is
-    // written and V landed.  S runs on into the next piece.  The whole warp
-    // keeps the books, in step, and one elected lane issues.
-    const uint64_t qd0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
-    const uint64_t kd0 = sdesc_sw128(smem_u32(sR), 16, 1024);
-    const uint64_t vd0 = sdesc_sw128(smem_u32(sR), 16, 1024);   // N chunk by chunk: one 64-wide product per unit
-    struct Cursor {
-      int seg, blk, item;      // pieces, blocks and items before it
-      int nb, qt, qb, lb, t;   // the piece, and the place in it
-      bool in;
-    };
-    Cursor s{0, 0, 0, 0, 0, 0, 0, 0, false}, v{0, 0, 0, 0, 0, 0, 0, 0, false};
-    int quse[2] = {0, 0};
-    bool s_end = false;
-    uint64_t t_idle = 0;
-    auto uni = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
-    auto ready = [](uint64_t *bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_test_wait(smem_u32(bar), parity)) != 0;
-    };
-    auto landed = [&](int first, int n) {   // units first .. first + n - 1 of the ring's sequence
-      for (int i = first; i < first + n; ++i)
-        if (!ready(&ct.full[i % C::NU], (i / C::NU) & 1)) return false;
-      return true;
-    };
-    auto enter = [&](Cursor &x) {
-      const PreSeg &sg = ct.seg[x.seg % C::NSEG];
-      x.nb = uni(sg.nb);
-      x.qt = uni(sg.qt);
-      x.qb = uni(sg.qb);
-      x.lb = x.t = 0;
-      x.in = true;
-    };
-    for (uint32_t spin = 1;; ++spin) {   // rounds without progress
-      bool progress = false;
-      if (!s_end && s.item < v.item + 2) {
-        if (!s.in && ready(&ct.seg_full[s.seg % C::NSEG], (s.seg / C::NSEG) & 1)) {
-          enter(s);
-          if (s.nb == 0) s_end = true;
-        }
-        if (s.in && !s_end) {
-          const int qb = s.qb ^ s.t, k0 = s.blk * (C::KU + C::VU);
-          if ((s.lb > 0 || ready(&ct.q_full[qb], quse[qb] & 1)) && landed(k0, C::KU)) {
-            tc_fence_after();
-            const uint32_t d = tmem + 128 * (s.item & 1);
-            const uint64_t qd = qd0 + static_cast<uint64_t>((qb * C::QT_BYTES) >> 4);
-            const bool last = s.lb == s.nb - 1, k_done = s.t + 1 == s.qt;
-            if (elect_one()) {
-#pragma unroll
-              for (int ch = 0; ch < C::KU; ++ch) {
-                const uint64_t kd = kd0 + static_cast<uint64_t>((((k0 + ch) % C::NU) * C::UNIT) >> 4);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  mma_bf16(d, qd + ((ch * C::UNIT + kk * 32) >> 4), kd + ((kk * 32) >> 4), C::IDESC_S,
-                           (ch > 0 || kk > 0) ? 1u : 0u);
-              }
-              mma_commit(&ct.s_full[s.item & 1]);
-              if (last) mma_commit(&ct.q_empty[qb]);
-              if (k_done)
-#pragma unroll
-                for (int ch = 0; ch < C::KU; ++ch) mma_commit(&ct.empty[(k0 + ch) % C::NU]);
-            }
-            __syncwarp();
-            if (last) ++quse[qb];
-            ++s.item;
-            if (++s.t == s.qt) {
-              s.t = 0;
-              ++s.blk;
-              if (++s.lb == s.nb) {
-                s.in = false;
-                ++s.seg;
-              }
-            }
-            progress = true;
-          }
-        }
-      }
-      if (v.item < s.item) {
-        if (!v.in) enter(v);   // S of the piece is out: its record is there
-        const int v0 = v.blk * (C::KU + C::VU) + C::KU;
-        if (ready(&ct.p_full[v.item & 1], (v.item >> 1) & 1) && landed(v0, C::VU)) {
+  } else if (warp <= 2) {
+    // -------------------------------------------------------- MMA issuers
+    // One per warp group, so that neither's commits and waits hold up the other's
+    // products (as one warp polling for both, a block of two tiles took 4,980
+    // cycles, of which it was issuing 3,600).  In turn: S of an item once its K
+    // (and Q) landed, P V once P is written and V landed, S of the group's next
+    // item behind it (P lies over S, so not before).
+    if (lane == 0) {
+      const int w = warp - 1;
+      const uint64_t qd0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t rd0 = sdesc_sw128(smem_u32(sR), 16, 1024);
+      const uint32_t s_col = tmem + 128 * w, o_col = tmem + C::O_COL + HD * w;
+      auto wait = [&](uint64_t *bar, uint32_t par) { return mbar_wait(bar, par, abort_flag, p.err, kErrWaitMma); };
+      int nseg = 0, item0 = 0, blk0 = 0, quse[2] = {0, 0}, both = 0;   // both: pieces of two tiles
+      bool ok = true;
+      while (ok) {
+        const int ss = nseg % C::NSEG;
+        ok = wait(&ct.seg_full[ss], (nseg / C::NSEG) & 1);
+        if (!ok) break;
+        const int nb = ct.seg[ss].nb, qt = ct.seg[ss].qt, qb0 = ct.seg[ss].qb;
+        if (nb == 0) break;
+        const int items = nb * qt, lb0 = (item0 & 1) ^ w, qb = qt == 2 ? qb0 ^ lb0 : qb0;
+        for (int li = lb0; li < items && ok; li += 2) {
+          const int blk = blk0 + (qt == 2 ? li >> 1 : li), sb = blk % C::NB, u0 = blk * (C::KU + C::VU);
+          if (li < 2) ok = wait(&ct.q_full[qb], quse[qb] & 1);
+          // the second tile starts half a block behind the first
+          if (qt == 2 && li == 1) ok = ok && wait(&ct.turn[both & 1], (both >> 1) & 1);
+          ok = ok && wait(&ct.k_full[sb], (blk / C::NB) & 1);
+          if (!ok) break;
           tc_fence_after();
-          const int w = v.item & 1;               // warp group, S buffer, O accumulator
-          const uint32_t pcol = tmem + 128 * w;
-          const bool first = v.lb < (v.qt == 1 ? 2 : 1);   // the group's first block of the piece
-          const bool v_done = v.t + 1 == v.qt, last = v_done && v.lb + 1 == v.nb;
-          if (elect_one()) {
-            const int u0 = v0 % C::NU;
-            if (C::VU == 1 || u0 + 1 < C::NU) {
-              // both halves side by side: N = hd, the halves 16 KB apart
-              const uint64_t vd = sdesc_sw128(smem_u32(sR) + u0 * C::UNIT, C::UNIT, 1024);
+          const uint64_t qd = qd0 + static_cast<uint64_t>((qb * C::QT_BYTES) >> 4);
 #pragma unroll
-              for (int ks = 0; ks < 8; ++ks)   // 16 keys (two atoms) per MMA
-                mma_bf16_ts(tmem + C::O_COL + HD * w, pcol + ks * 8, vd + ((ks * 2048) >> 4), C::IDESC_PV,
-                            (!first || ks > 0) ? 1u : 0u);
-            } else {
-              // the ring's end lies between them: half by half
-              constexpr uint32_t IDESC_64 = idesc_bf16(128, 64, true);
+          for (int ch = 0; ch < C::KU; ++ch) {
+            const uint64_t kd = rd0 + static_cast<uint64_t>((((u0 + ch) % C::NU) * C::UNIT) >> 4);
 #pragma unroll
-              for (int ch = 0; ch < C::VU; ++ch) {
-                const uint64_t vd = vd0 + static_cast<uint64_t>((((v0 + ch) % C::NU) * C::UNIT) >> 4);
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                  mma_bf16_ts(tmem + C::O_COL + HD * w + 64 * ch, pcol + ks * 8, vd + ((ks * 2048) >> 4), IDESC_64,
-                              (!first || ks > 0) ? 1u : 0u);
-              }
-            }
-            mma_commit(&ct.o_full[w]);
-            if (v_done)
-#pragma unroll
-              for (int ch = 0; ch < C::VU; ++ch) mma_commit(&ct.empty[(v0 + ch) % C::NU]);
-            if (last) mbar_arrive(&ct.seg_empty[v.seg % C::NSEG]);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16(s_col, qd + ((ch * C::UNIT + kk * 32) >> 4), kd + ((kk * 32) >> 4), C::IDESC_S, (ch > 0 || kk > 0) ? 1u : 0u);
           }
-          __syncwarp();
-          ++v.item;
-          if (++v.t == v.qt) {
-            v.t = 0;
-            ++v.blk;
-            if (++v.lb == v.nb) {
-              v.in = false;
-              ++v.seg;
+          mma_commit(&ct.s_full[w]);
+          mma_commit(&ct.k_empty[sb]);
+          if (qt == 1) mma_commit(&ct.k_empty[sb]);   // (for the other group, which does not take this block)
+          if (li + 2 >= items) {
+            mma_commit(&ct.q_empty[qb]);
+            if (qt == 2 || items == 1) mma_commit(&ct.q_empty[qb]);   // (no other user of the tile)
+          }
+          ok = wait(&ct.p_full[w], ((item0 + li) >> 1) & 1) && wait(&ct.v_full[sb], (blk / C::NB) & 1);
+          if (!ok) break;
+          if (qt == 2 && li == 0) mbar_arrive(&ct.turn[both & 1]);
+          tc_fence_after();
+          const int v0 = (u0 + C::KU) % C::NU;
+          if (C::VU == 1 || v0 + 1 < C::NU) {
+            // both halves side by side: N = hd, the halves 16 KB apart
+            const uint64_t vd = sdesc_sw128(smem_u32(sR) + v0 * C::UNIT, C::UNIT, 1024);
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)   // 16 keys (two atoms) per MMA
+              mma_bf16_ts(o_col, s_col + ks * 8, vd + ((ks * 2048) >> 4), C::IDESC_PV, (li >= 2 || ks > 0) ? 1u : 0u);
+          } else {
+            // the ring's end lies between them: half by half
+            constexpr uint32_t IDESC_64 = idesc_bf16(128, 64, true);
+#pragma unroll
+            for (int ch = 0; ch < C::VU; ++ch) {
+              const uint64_t vd = rd0 + static_cast<uint64_t>((((v0 + ch) % C::NU) * C::UNIT) >> 4);
+#pragma unroll
+              for (int ks = 0; ks < 8; ++ks)
+                mma_bf16_ts(o_col + 64 * ch, s_col + ks * 8, vd + ((ks * 2048) >> 4), IDESC_64, (li >= 2 || ks > 0) ? 1u : 0u);
             }
           }
-          progress = true;
+          mma_commit(&ct.o_full[w]);
+          mma_commit(&ct.v_empty[sb]);
+          if (qt == 1) mma_commit(&ct.v_empty[sb]);
         }
+        if (!ok) break;
+        // (both groups count a tile's uses: with one tile they share it)
+        if (qt == 2) ++quse[0], ++quse[1], ++both;
+        else ++quse[qb0];
+        item0 += items;
+        blk0 += nb;
+        ++nseg;
+        mbar_arrive(&ct.seg_empty[ss]);
       }
-      if (s_end && v.item == s.item) break;
-      if (progress) {
-        spin = 0;
-        t_idle = 0;
-      } else if ((spin & 255u) == 0) {
-        if (t_idle == 0) t_idle = globaltimer();
-        const bool late = globaltimer() - t_idle > kWaitLimitNs;
-        if (__any_sync(0xffffffffu, late || *abort_flag)) {
-          if (__any_sync(0xffffffffu, late) && lane == 0) {
-            *abort_flag = 1;
-            atomicExch(p.err, kErrWaitMma);
-          }
-          break;
-        }
+      // every MMA issued above has completed before TMEM is freed
+      mma_commit(&ct.done);
+      const uint64_t t_end = globaltimer();
+      while (!mbar_try_wait(smem_u32(&ct.done), 0) && globaltimer() - t_end < kWaitLimitNs) {
       }
     }
-    // every MMA issued above has completed before TMEM is freed
-    if (elect_one()) mma_commit(&ct.done);
     __syncwarp();
-    const uint64_t t_end = globaltimer();
-    while (!mbar_try_wait(smem_u32(&ct.done), 0) && globaltimer() - t_end < kWaitLimitNs) {
-    }
-    __syncwarp();
-  } else {
+  } else if (warp >= 4) {
     // ------------------------------------------------- softmax / epilogue
-    const int w = (warp - 2) >> 2;          // warp group: it takes every second item
+    const int w = (warp - 4) >> 2;          // warp group: it takes every second item
     const int qu = warp & 3;                // TMEM lane quarter
     const int row = qu * 32 + lane;         // row of the tile
     const uint32_t lane_base = static_cast<uint32_t>(qu * 32) << 16;
