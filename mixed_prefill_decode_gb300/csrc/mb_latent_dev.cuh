@@ -66,6 +66,11 @@ __device__ __forceinline__ void tma_prefetch_5d(const CUtensorMap *map, int32_t 
                : "memory");
 }
 
+// Bytes from a 16-byte boundary (a multiple of 16), into L2.
+__device__ __forceinline__ void l2_prefetch(const void *p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // Zeroes a row of CHUNKS 64-wide chunks (1 KB apart) of a swizzled stage if
 // `stale`, or if it holds an infinity or a NaN (then true).
 template <int CHUNKS>

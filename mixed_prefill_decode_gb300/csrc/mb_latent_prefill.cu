@@ -10,14 +10,14 @@
 // absorbed form: from about a hundred tokens on this form does less.
 //
 // What bounds it: the tensor cores, and beside them the chain of product,
-// softmax, product.  Keys and values of a head are 4 hd bytes a token; the heads
-// are taken in groups whose keys and values fit well inside L2, so they are
-// written, and read by every tile of queries, without going to HBM.
+// softmax, product.  Keys and values of a head are 4 hd bytes a token, written once
+// and read by every tile of queries.
 //
-// Two kernels per group of heads, and a merge:
-//  * expand: 128 cached rows (8 pages, copied once by TMA) stay in shared memory
-//    as the A operand while the heads' weights stream past: M = 128 keys, N =
-//    2 hd (a head's key and value rows), K = rank.
+// Two kernels, and a merge (per group of heads, if all heads' keys and values would
+// take more than 512 MB):
+//  * expand: 2 x 128 cached rows (8 pages a CTA, copied once by TMA) stay in shared
+//    memory as the A operand of a CTA pair while the heads' weights stream past:
+//    M = 256 keys, N = 2 hd (a head's key and value rows), K = rank.
 //  * attention: a unit is 256 tokens of a request and one head, as two 128-row
 //    query tiles that share the staged keys and values; S = Q K^T with K = hd +
 //    64, softmax with one thread per row, O += P V with P in TMEM.  Two groups of
@@ -49,7 +49,11 @@ using namespace dev;
 constexpr int kMaxCtas = 160;      // CTAs of an attention launch at most; sizes the workspace
 constexpr int kRecBytes = 8192;    // workspace: one record of 8 ints per CTA, then the partials
 constexpr int kBlk = 128;          // keys of a block
-constexpr int kGroupBytes = 48 << 20;   // keys and values of a group of heads at most (of one head, whatever it takes)
+__host__ __device__ constexpr int64_t part_floats(int64_t hd) { return 256 * (hd + 2); }   // of a slot
+// Keys and values of a group of heads at most (of one head, whatever it takes).
+// Groups that fit L2 were slower: 2,048 tokens at 8,192 keys, 40 heads, took 413 us as
+// one group of 168 MB, 448 as two, 517 as four (each starts and ends its kernels anew).
+constexpr int kGroupBytes = 512 << 20;
 // The schedule's weights: a block of one query tile, a block of two, a unit's
 // start and end, and the least a CTA takes (at least kCost2, so that no CTA
 // between the first and the last of a unit is left without a block).
@@ -58,12 +62,13 @@ constexpr int kCost1 = 2, kCost2 = 3, kCostUnit = 5, kMinShare = 3;
 struct PreParams {
   __nv_bfloat16 *kv;             // [heads of the group][rows][2 hd]: a head's keys and values
   __nv_bfloat16 *o;
+  const __nv_bfloat16 *w_kv;
   const int32_t *qo_indptr, *kv_len, *bt_indptr, *bt;
   int n_reqs, T, H, h0, HG, num_pages;   // heads h0 .. h0 + HG - 1
   int cap_blocks;                // blocks of 128 rows that kv has room for
   float scale_log2;
   int32_t *rec;
-  float *part;                   // [2 slots per CTA][256 rows][hd + 4]: o, m, l, pad
+  float *part;                   // [2 slots per CTA]: o of 256 rows [hd][256], their m and l [256][2]
   int *err;
 };
 
@@ -97,6 +102,10 @@ __device__ __forceinline__ int64_t cta_scan(int64_t mine, int64_t *sums, int64_t
 }
 
 // ------------------------------------------------------------------ expand
+// Over pairs of CTAs (cta_group::2): each has its own 128 cached rows as its half
+// of A and of the accumulators, and half of a head's weights as its half of B, so
+// a CTA takes in 32 bytes of weights a cycle instead of 64 (a CTA by itself took
+// three times as long: two stages of 32 KB did not cover a load's latency).
 template <int HD, int RANK>
 struct ExpCfg {
   static constexpr int NC = RANK / 64 + 1;
@@ -104,20 +113,21 @@ struct ExpCfg {
   static constexpr int PAGE_BYTES = 2 * ATOM;
   static constexpr int A_BYTES = (kBlk / 8) * ATOM;
   static constexpr int N = 2 * HD;
-  static constexpr int B_STAGE = N * 128;             // 64 of rank
+  static constexpr int B_STAGE = HD * 128;            // this CTA's half of the head's rows, 64 of rank
   static constexpr int KC = RANK / 64;
-  static constexpr int NB = HD == 128 && RANK == 512 ? 2 : 4;
+  static constexpr int NB = (HD == 128 ? 1 : 2) * (RANK == 512 ? 5 : 8);
   static constexpr int OFF_B = A_BYTES;
   static constexpr int OFF_CTRL = OFF_B + NB * B_STAGE;
   static constexpr int SMEM = OFF_CTRL + 512;
   static constexpr int THREADS = 192;                 // TMA, MMA, 4 epilogue warps
-  static constexpr uint32_t IDESC = idesc_bf16(128, N, false);
+  static constexpr uint32_t IDESC = idesc_bf16(256, N, false);
 };
 
 template <int HD, int RANK>
 struct ExpCtrl {
   using C = ExpCfg<HD, RANK>;
-  uint64_t a_full, a_empty, b_full[C::NB], b_empty[C::NB], t_full[2], t_empty[2], done;
+  uint64_t a_full, a_peer, a_empty;   // this CTA's rows; the other's (in rank 0); both CTAs' products with them done
+  uint64_t b_full[C::NB], b_empty[C::NB], t_full[2], t_empty[2], done;   // b_full, t_empty: rank 0's count for both
   int64_t sums[C::THREADS / 32];
   int64_t start_base;
   int32_t start_req;
@@ -148,13 +158,16 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
   ExpCtrl<HD, RANK> &ct = *reinterpret_cast<ExpCtrl<HD, RANK> *>(smem + C::OFF_CTRL);
   volatile int *abort_flag = &ct.abort;
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;   // (known uniform)
-  if (smem_u32(smem) & 1023u) {   // the swizzled layouts need a 1024-aligned base
+  const uint32_t rank = cluster_ctarank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  if (smem_u32(smem) & 1023u) {   // the swizzled layouts need a 1024-aligned base (the same in both CTAs)
     pdl_wait();
     if (threadIdx.x == 0) atomicExch(p.err, kErrBounds);
     return;
   }
   if (threadIdx.x == 0) {
     mbar_init(&ct.a_full, 1);
+    mbar_init(&ct.a_peer, 1);
     mbar_init(&ct.a_empty, 1);
     for (int s = 0; s < C::NB; ++s) {
       mbar_init(&ct.b_full[s], 1);
@@ -162,7 +175,7 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ct.t_full[b], 1);
-      mbar_init(&ct.t_empty[b], 128);
+      mbar_init(&ct.t_empty[b], 8);   // the epilogue warps of both CTAs
     }
     mbar_init(&ct.done, 1);
     ct.abort = 0;
@@ -173,13 +186,20 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
     prefetch_tmap(&tmR);
   }
   if (warp == 1) {
-    tmem_alloc(&ct.tmem, 512);
-    tmem_relinquish();
+    tmem_alloc_pair(&ct.tmem, 512);
+    tmem_relinquish_pair();
   }
   pdl_wait();   // descriptor, cache, weights and workspace belong to earlier kernels of the stream
   pdl_trigger();
+  if (threadIdx.x == 0) {
+    // The group's weights on their way to L2, a part by each CTA: all pairs ask
+    // for the same chunk at about the same time, and each would wait for HBM.
+    const int64_t bytes = static_cast<int64_t>(p.HG) * 2 * HD * RANK * 2, part = (bytes / gridDim.x + 127) / 128 * 128;
+    const int64_t from = part * blockIdx.x, n = min(part, bytes - from);
+    if (n > 0) l2_prefetch(reinterpret_cast<const uint8_t *>(p.w_kv + static_cast<int64_t>(p.h0) * 2 * HD * RANK) + from, static_cast<uint32_t>(n));
+  }
 
-  // ---- this CTA's items: (block of 128 keys, head), heads fastest
+  // ---- this pair's items: (two blocks of 128 keys, head), heads fastest
   const int per = (p.n_reqs + C::THREADS - 1) / C::THREADS;
   const int r_lo = min(p.n_reqs, static_cast<int>(threadIdx.x) * per), r_hi = min(p.n_reqs, r_lo + per);
   int64_t mine = 0, total;
@@ -189,7 +209,8 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
     if (bad && blockIdx.x == 0) atomicExch(p.err, kErrBounds);
   }
   tc_fence_before();
-  int64_t pre = cta_scan<C::THREADS / 32>(mine, ct.sums, &total);   // (synchronises: TMEM's address is there)
+  int64_t pre = cta_scan<C::THREADS / 32>(mine, ct.sums, &total);
+  cluster_sync();   // (both CTAs' barriers are set up, and TMEM's address is there)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ct.tmem, 0);
   if (total > p.cap_blocks) {
@@ -197,10 +218,11 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
     if (threadIdx.x == 0 && blockIdx.x == 0) atomicExch(p.err, kErrBounds);
     total = p.cap_blocks;
   }
-  const int64_t items = total * p.HG, W = min(static_cast<int64_t>(gridDim.x), items);
-  const bool active = blockIdx.x < W;
-  const int64_t x0 = active ? div64(items * blockIdx.x, W) : 0, x1 = active ? div64(items * (blockIdx.x + 1), W) : 0;
-  const int64_t b0 = active ? div64(x0, p.HG) : 0;
+  const int64_t items = (total + 1) / 2 * p.HG, W = min(static_cast<int64_t>(pairs), items);
+  const bool active = pair < W;
+  const int64_t x0 = active ? div64(items * pair, W) : 0, x1 = active ? div64(items * (pair + 1), W) : 0;
+  const int64_t p0 = active ? div64(x0, p.HG) : 0;   // the first pair of blocks
+  const int64_t b0 = min(2 * p0 + rank, total - 1);  // this CTA's first block (none: a stand-in)
   if (active && pre <= b0 && b0 < pre + mine) {
     for (int r = r_lo; r < r_hi; ++r) {
       bool bad;
@@ -214,7 +236,7 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
     }
   }
   __syncthreads();
-  // Walks the blocks from b0 on: the request of block `blk` and its first key there.
+  // Walks this CTA's blocks: the request of a block and where it starts.
   struct Walk {
     int r;
     int64_t base;   // the request's first block
@@ -238,6 +260,7 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
       k.blocks = key_blocks(k.w, p.T, &bad);
     }
   };
+  const int hg0 = static_cast<int>(x0 - p0 * p.HG);
 
   if (!active) {
   } else if (warp == 0) {
@@ -245,39 +268,53 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
     Walk k = start();
     int ause = 0, bcnt = 0;
     bool ok = true;
-    int64_t blk = b0;
-    int hg = static_cast<int>(x0 - b0 * p.HG);
+    int64_t blk = 2 * p0 + rank;
+    int hg = hg0;
+    const uint32_t peer_bar = mapa_shared(smem_u32(&ct.a_peer), 0);
     for (int64_t i = x0; i < x1 && ok; ++i) {
+      const bool have = blk < total;   // (the last pair of blocks may be one)
       if (i == x0 || hg == 0) {
-        reach(k, blk);
-        const int j = static_cast<int>(blk - k.base), n_pages = (k.w.kv + kPage - 1) / kPage, np = min(8, n_pages - 8 * j);
-        int page = lane < np ? p.bt[k.w.b0 + 8 * j + lane] : 0;
-        if (lane < np && (page < 0 || page >= p.num_pages)) {
-          atomicExch(p.err, kErrBounds);
-          page = 0;
-        }
         ok = __all_sync(0xffffffffu, mbar_wait(&ct.a_empty, (ause & 1) ^ 1, abort_flag, p.err, kErrWaitProducer));
         if (!ok) break;
         asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the keys' copies below have left the stage
         __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(&ct.a_full, np * C::PAGE_BYTES);
-        __syncwarp();
-        if (lane < np) tma_load_5d(sA + lane * C::PAGE_BYTES, &tmK, &ct.a_full, 0, 0, 0, 0, page);
+        if (have) {
+          reach(k, blk);
+          const int j = static_cast<int>(blk - k.base), n_pages = (k.w.kv + kPage - 1) / kPage, np = min(8, n_pages - 8 * j);
+          int page = lane < np ? p.bt[k.w.b0 + 8 * j + lane] : 0;
+          if (lane < np && (page < 0 || page >= p.num_pages)) {
+            atomicExch(p.err, kErrBounds);
+            page = 0;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&ct.a_full, np * C::PAGE_BYTES);
+          __syncwarp();
+          if (lane < np) tma_load_5d(sA + lane * C::PAGE_BYTES, &tmK, &ct.a_full, 0, 0, 0, 0, page);
+        } else if (lane == 0) {
+          mbar_arrive(&ct.a_full);
+        }
         ++ause;
       }
+      bool told = rank == 0 || (i > x0 && hg != 0);   // rank 0 knows that this CTA's rows are there
       for (int c = 0; c < C::KC && ok; ++c, ++bcnt) {
         const int st = bcnt % C::NB;
         if (lane == 0) {
           ok = mbar_wait(&ct.b_empty[st], ((bcnt / C::NB) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer);
           if (ok) {
-            mbar_arrive_expect_tx(&ct.b_full[st], C::B_STAGE);
-            tma_load_2d(sB + st * C::B_STAGE, &tmW, &ct.b_full[st], 64 * c, (p.h0 + hg) * 2 * HD);
+            if (rank == 0) mbar_arrive_expect_tx(&ct.b_full[st], 2 * C::B_STAGE);
+            tma_load_2d_pair(sB + st * C::B_STAGE, &tmW, mapa_shared(smem_u32(&ct.b_full[st]), 0), 64 * c,
+                             (p.h0 + hg) * 2 * HD + static_cast<int>(rank) * HD);
+          }
+          // (after the first weights, which go out while the rows are on their way)
+          if (ok && !told && (c == C::NB - 1 || c == C::KC - 1)) {
+            ok = mbar_wait(&ct.a_full, (ause - 1) & 1, abort_flag, p.err, kErrWaitProducer);
+            if (ok) mbar_arrive_remote(peer_bar);
+            told = true;
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
       }
-      if (ok && p.h0 + hg == 0) {
+      if (ok && have && p.h0 + hg == 0) {
         // the rotated keys, once per call, as one row of 64 per token (what lies
         // behind the request's last key is never attended to)
         ok = __all_sync(0xffffffffu, mbar_wait(&ct.a_full, (ause - 1) & 1, abort_flag, p.err, kErrWaitProducer));
@@ -286,7 +323,7 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
       }
       if (++hg == p.HG) {
         hg = 0;
-        ++blk;
+        blk += 2;
       }
     }
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -297,23 +334,26 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
         }
       };
       if (lane == 0) {
-        for (int b = max(0, bcnt - C::NB); b < bcnt; ++b) drain(&ct.b_full[b % C::NB], b / C::NB);
+        if (rank == 0)
+          for (int b = max(0, bcnt - C::NB); b < bcnt; ++b) drain(&ct.b_full[b % C::NB], b / C::NB);
+        else
+          while (bcnt > 0 && globaltimer() - t_start < kWaitLimitNs / 100) {   // (its weights count in rank 0: 20 ms)
+          }
         if (ause > 0) drain(&ct.a_full, ause - 1);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
-    if (lane == 0) {
+    if (rank == 0 && lane == 0) {
       const uint64_t ad0 = sdesc_sw128(smem_u32(sA), 16, C::ATOM);
       const uint64_t bd0 = sdesc_sw128(smem_u32(sB), 16, 1024);
       auto wait = [&](uint64_t *bar, uint32_t par) { return mbar_wait(bar, par, abort_flag, p.err, kErrWaitMma); };
-      int ause = 0, bcnt = 0, acc = 0;
-      int hg = static_cast<int>(x0 - b0 * p.HG);
+      int ause = 0, bcnt = 0, acc = 0, hg = hg0;
       bool ok = true;
       for (int64_t i = x0; i < x1 && ok; ++i, ++acc) {
         if (i == x0 || hg == 0) {
-          ok = wait(&ct.a_full, ause & 1);
+          ok = wait(&ct.a_full, ause & 1) && wait(&ct.a_peer, ause & 1);
           ++ause;
         }
         ok = ok && wait(&ct.t_empty[acc & 1], ((acc >> 1) & 1) ^ 1);
@@ -324,19 +364,19 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_bf16(tmem + 256 * (acc & 1), ad0 + ((c * 1024 + kk * 32) >> 4), bd0 + ((st * C::B_STAGE + kk * 32) >> 4),
-                     C::IDESC, (c > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(&ct.b_empty[st]);
+            mma_bf16_pair(tmem + 256 * (acc & 1), ad0 + ((c * 1024 + kk * 32) >> 4), bd0 + ((st * C::B_STAGE + kk * 32) >> 4),
+                          C::IDESC, (c > 0 || kk > 0) ? 1u : 0u);
+          mma_commit_pair(&ct.b_empty[st], 3);
         }
         if (!ok) break;
-        mma_commit(&ct.t_full[acc & 1]);
+        mma_commit_pair(&ct.t_full[acc & 1], 3);
         if (++hg == p.HG) {
           hg = 0;
-          mma_commit(&ct.a_empty);
+          mma_commit_pair(&ct.a_empty, 3);
         }
       }
       // every MMA issued above has completed before TMEM is freed
-      mma_commit(&ct.done);
+      mma_commit_pair(&ct.done, 1);
       const uint64_t t_end = globaltimer();
       while (!mbar_try_wait(smem_u32(&ct.done), 0) && globaltimer() - t_end < kWaitLimitNs) {
       }
@@ -350,64 +390,69 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
     const int qu = warp & 3, row = qu * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(qu * 32) << 16;
     Walk k = start();
-    int64_t blk = b0;
-    int hg = static_cast<int>(x0 - b0 * p.HG), acc = 0;
+    int64_t blk = 2 * p0 + rank;
+    int hg = hg0, acc = 0;
+    const uint32_t empty0 = mapa_shared(smem_u32(&ct.t_empty[0]), 0), empty1 = mapa_shared(smem_u32(&ct.t_empty[1]), 0);
     for (int64_t i = x0; i < x1; ++i, ++acc) {
-      if (i == x0 || hg == 0) reach(k, blk);
+      if (blk < total && (i == x0 || hg == 0)) reach(k, blk);
       const bool fail = !mbar_wait(&ct.t_full[acc & 1], (acc >> 1) & 1, abort_flag, p.err, kErrWaitEpilogue);
       if (__any_sync(0xffffffffu, fail)) break;   // tcgen05.ld below is warp-collective
       tc_fence_after();
-      const bool stale = static_cast<int>(blk - k.base) * kBlk + row >= k.w.kv;
-      const uint32_t t = tmem + lane_base + 256 * (acc & 1);
-      uint8_t *dst = reinterpret_cast<uint8_t *>(p.kv + ((static_cast<int64_t>(hg) * p.cap_blocks + blk) * kBlk + row) * (2 * HD));
-      uint32_t pk[HD / 2];
-      float odd = 0.f;   // NaN if a value is not finite
+      if (blk < total) {
+        const bool stale = static_cast<int>(blk - k.base) * kBlk + row >= k.w.kv;
+        const uint32_t t = tmem + lane_base + 256 * (acc & 1);
+        uint8_t *dst = reinterpret_cast<uint8_t *>(p.kv + ((static_cast<int64_t>(hg) * p.cap_blocks + blk) * kBlk + row) * (2 * HD));
+        uint32_t pk[HD / 2];
+        float odd = 0.f;   // NaN if a value is not finite
 #pragma unroll
-      for (int cc = 0; cc < HD / 32; ++cc) {
-        float v[32];
-        tmem_ld32(t + HD + 32 * cc, v);
+        for (int cc = 0; cc < HD / 32; ++cc) {
+          float v[32];
+          tmem_ld32(t + HD + 32 * cc, v);
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          pk[16 * cc + e / 2] = pack_bf16x2(v[e], v[e + 1]);
-          odd = fmaf(bf16lo(pk[16 * cc + e / 2]), 0.f, odd);
-          odd = fmaf(bf16hi(pk[16 * cc + e / 2]), 0.f, odd);
+          for (int e = 0; e < 32; e += 2) {
+            pk[16 * cc + e / 2] = pack_bf16x2(v[e], v[e + 1]);
+            odd = fmaf(bf16lo(pk[16 * cc + e / 2]), 0.f, odd);
+            odd = fmaf(bf16hi(pk[16 * cc + e / 2]), 0.f, odd);
+          }
         }
-      }
-      const bool wipe = stale || odd != 0.f;
+        const bool wipe = stale || odd != 0.f;
 #pragma unroll
-      for (int e = 0; e < HD / 2; e += 8) {
-        if (wipe)
+        for (int e = 0; e < HD / 2; e += 8) {
+          if (wipe)
 #pragma unroll
-          for (int x = 0; x < 8; ++x) pk[e + x] = 0;
-        store32(dst + 2 * HD + 4 * e, pk + e);
-      }
-#pragma unroll
-      for (int cc = 0; cc < HD / 32; ++cc) {
-        float v[32];
-        tmem_ld32(t + 32 * cc, v);
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          uint32_t x = pack_bf16x2(v[e], v[e + 1]);
-          if (wipe) x = stale ? 0u : 0x7FC07FC0u;
-          pk[e / 2] = x;
+            for (int x = 0; x < 8; ++x) pk[e + x] = 0;
+          store32(dst + 2 * HD + 4 * e, pk + e);
         }
-        store32(dst + 64 * cc, pk);
-        store32(dst + 64 * cc + 32, pk + 8);
+#pragma unroll
+        for (int cc = 0; cc < HD / 32; ++cc) {
+          float v[32];
+          tmem_ld32(t + 32 * cc, v);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            uint32_t x = pack_bf16x2(v[e], v[e + 1]);
+            if (wipe) x = stale ? 0u : 0x7FC07FC0u;
+            pk[e / 2] = x;
+          }
+          store32(dst + 64 * cc, pk);
+          store32(dst + 64 * cc + 32, pk + 8);
+        }
       }
       tc_fence_before();
-      mbar_arrive(&ct.t_empty[acc & 1]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(acc & 1 ? empty1 : empty0);
       if (++hg == p.HG) {
         hg = 0;
-        ++blk;
+        blk += 2;
       }
     }
     tc_fence_before();
   }
   __syncthreads();
+  cluster_sync();   // (neither CTA's shared memory or TMEM goes while the pair's products use it)
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -430,7 +475,7 @@ struct PreCfg {
   static constexpr int OFF_CTRL = OFF_R + NU * UNIT;
   static constexpr int OFF_ML = OFF_CTRL + 1024;      // (m, l) of 128 rows, from one warp group to the other
   static constexpr int SMEM = OFF_ML + 1024;
-  static constexpr int THREADS = 384;                 // TMA, 2 MMA issuers, one idle, 2 x 4 softmax warps
+  static constexpr int THREADS = 320;                 // TMA, MMA, 2 x 4 softmax warps
   static constexpr uint32_t IDESC_S = idesc_bf16(128, 128, false);
   static constexpr uint32_t IDESC_PV = idesc_bf16(128, HD, true);
   static constexpr uint32_t TMEM_COLS = 512;          // S/P buffers at 0 and 128, O of the two groups from 256
@@ -455,12 +500,11 @@ template <int HD>
 struct PreCtrl {
   using C = PreCfg<HD>;
   uint64_t q_full[2], q_empty[2];
-  uint64_t k_full[C::NB], k_empty[C::NB], v_full[C::NB], v_empty[C::NB];   // by block; empty: both groups are done with it
-  uint64_t s_full[2], p_full[2], o_full[2];   // by warp group
+  uint64_t k_full[C::NB], k_empty[C::NB], v_full[C::NB], v_empty[C::NB];   // by block
+  uint64_t s_full[2], p_half[2], p_full[2], h_full[2], o_full[2];   // by warp group: S; P of half the keys, of all; P V of them
   uint64_t ml_full[2];    // the group's (m, l) are in shared memory
   uint64_t ml_empty[2];   // the other group has read them and this group's O
   uint64_t seg_full[C::NSEG], seg_empty[C::NSEG];
-  uint64_t turn[2];       // the first tile's P of a piece's first block is written (pieces of two tiles, in turn)
   uint64_t done;
   PreSeg seg[C::NSEG];
   int64_t sums[C::THREADS / 32];
@@ -491,17 +535,6 @@ __device__ __forceinline__ PreReq pre_req(const PreParams &p, const ReqWords &w,
   q.a = (q.c + kBlk - 1) / kBlk;
   q.head = q.n == 0 ? 0 : units_cost(q.a, q.full) + (q.rem ? kCostUnit + (q.rem > 128 ? kCost2 : kCost1) * static_cast<int64_t>(tail_blocks(q)) : 0);
   return q;
-}
-
-// 32 columns at each of two addresses of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
-      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
 }
 
 // Takes the keys behind `vis` out of a row's block of S (to -inf, in TMEM): a
@@ -541,25 +574,26 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ct.q_full[b], 1);
-      mbar_init(&ct.q_empty[b], 2);
+      mbar_init(&ct.q_empty[b], 1);
       mbar_init(&ct.s_full[b], 1);
+      mbar_init(&ct.p_half[b], 128);
       mbar_init(&ct.p_full[b], 128);
+      mbar_init(&ct.h_full[b], 1);
       mbar_init(&ct.o_full[b], 1);
       mbar_init(&ct.ml_full[b], 128);
       mbar_init(&ct.ml_empty[b], 128);
     }
     for (int s = 0; s < C::NB; ++s) {
       mbar_init(&ct.k_full[s], 1);
-      mbar_init(&ct.k_empty[s], 2);
+      mbar_init(&ct.k_empty[s], 1);
       mbar_init(&ct.v_full[s], 1);
-      mbar_init(&ct.v_empty[s], 2);
+      mbar_init(&ct.v_empty[s], 1);
     }
     for (int s = 0; s < C::NSEG; ++s) {
       mbar_init(&ct.seg_full[s], 1);
-      mbar_init(&ct.seg_empty[s], 10);   // the 2 MMA issuers and the 8 softmax warps
+      mbar_init(&ct.seg_empty[s], 9);   // the MMA issuer and the 8 softmax warps
     }
-    for (int b = 0; b < 2; ++b) mbar_init(&ct.turn[b], 1);
-    mbar_init(&ct.done, 2);
+    mbar_init(&ct.done, 1);
     ct.abort = 0;
     ct.start_req = -1;
     fence_mbar_init();
@@ -760,96 +794,140 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
       }
     }
     __syncwarp();
-  } else if (warp <= 2) {
-    // -------------------------------------------------------- MMA issuers
-    // One per warp group, so that neither's commits and waits hold up the other's
-    // products (as one warp polling for both, a block of two tiles took 4,980
-    // cycles, of which it was issuing 3,600).  In turn: S of an item once its K
-    // (and Q) landed, P V once P is written and V landed, S of the group's next
-    // item behind it (P lies over S, so not before).
-    if (lane == 0) {
-      const int w = warp - 1;
-      const uint64_t qd0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
-      const uint64_t rd0 = sdesc_sw128(smem_u32(sR), 16, 1024);
-      const uint32_t s_col = tmem + 128 * w, o_col = tmem + C::O_COL + HD * w;
-      auto wait = [&](uint64_t *bar, uint32_t par) { return mbar_wait(bar, par, abort_flag, p.err, kErrWaitMma); };
-      int nseg = 0, item0 = 0, blk0 = 0, quse[2] = {0, 0}, both = 0;   // both: pieces of two tiles
-      bool ok = true;
-      while (ok) {
-        const int ss = nseg % C::NSEG;
-        ok = wait(&ct.seg_full[ss], (nseg / C::NSEG) & 1);
-        if (!ok) break;
-        const int nb = ct.seg[ss].nb, qt = ct.seg[ss].qt, qb0 = ct.seg[ss].qb;
-        if (nb == 0) break;
-        const int items = nb * qt, lb0 = (item0 & 1) ^ w, qb = qt == 2 ? qb0 ^ lb0 : qb0;
-        for (int li = lb0; li < items && ok; li += 2) {
-          const int blk = blk0 + (qt == 2 ? li >> 1 : li), sb = blk % C::NB, u0 = blk * (C::KU + C::VU);
-          if (li < 2) ok = wait(&ct.q_full[qb], quse[qb] & 1);
-          // the second tile starts half a block behind the first
-          if (qt == 2 && li == 1) ok = ok && wait(&ct.turn[both & 1], (both >> 1) & 1);
-          ok = ok && wait(&ct.k_full[sb], (blk / C::NB) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t qd = qd0 + static_cast<uint64_t>((qb * C::QT_BYTES) >> 4);
-#pragma unroll
-          for (int ch = 0; ch < C::KU; ++ch) {
-            const uint64_t kd = rd0 + static_cast<uint64_t>((((u0 + ch) % C::NU) * C::UNIT) >> 4);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_bf16(s_col, qd + ((ch * C::UNIT + kk * 32) >> 4), kd + ((kk * 32) >> 4), C::IDESC_S, (ch > 0 || kk > 0) ? 1u : 0u);
-          }
-          mma_commit(&ct.s_full[w]);
-          mma_commit(&ct.k_empty[sb]);
-          if (qt == 1) mma_commit(&ct.k_empty[sb]);   // (for the other group, which does not take this block)
-          if (li + 2 >= items) {
-            mma_commit(&ct.q_empty[qb]);
-            if (qt == 2 || items == 1) mma_commit(&ct.q_empty[qb]);   // (no other user of the tile)
-          }
-          ok = wait(&ct.p_full[w], ((item0 + li) >> 1) & 1) && wait(&ct.v_full[sb], (blk / C::NB) & 1);
-          if (!ok) break;
-          if (qt == 2 && li == 0) mbar_arrive(&ct.turn[both & 1]);
-          tc_fence_after();
-          const int v0 = (u0 + C::KU) % C::NU;
-          if (C::VU == 1 || v0 + 1 < C::NU) {
-            // both halves side by side: N = hd, the halves 16 KB apart
-            const uint64_t vd = sdesc_sw128(smem_u32(sR) + v0 * C::UNIT, C::UNIT, 1024);
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)   // 16 keys (two atoms) per MMA
-              mma_bf16_ts(o_col, s_col + ks * 8, vd + ((ks * 2048) >> 4), C::IDESC_PV, (li >= 2 || ks > 0) ? 1u : 0u);
-          } else {
-            // the ring's end lies between them: half by half
-            constexpr uint32_t IDESC_64 = idesc_bf16(128, 64, true);
-#pragma unroll
-            for (int ch = 0; ch < C::VU; ++ch) {
-              const uint64_t vd = rd0 + static_cast<uint64_t>((((v0 + ch) % C::NU) * C::UNIT) >> 4);
-#pragma unroll
-              for (int ks = 0; ks < 8; ++ks)
-                mma_bf16_ts(o_col + 64 * ch, s_col + ks * 8, vd + ((ks * 2048) >> 4), IDESC_64, (li >= 2 || ks > 0) ? 1u : 0u);
-            }
-          }
-          mma_commit(&ct.o_full[w]);
-          mma_commit(&ct.v_empty[sb]);
-          if (qt == 1) mma_commit(&ct.v_empty[sb]);
+  } else if (warp == 1) {
+    // --------------------------------------------------------- MMA issuer
+    // Items in order, block by block and tile by tile, so that they alternate
+    // between the groups: P V of an item, then S of the group's next one (P lies
+    // over S, so not before), while the other group is at its softmax.  (With an
+    // issuer per group, products of both interleaved, finished together and
+    // left both groups at their softmax together: 4,900 cycles a block of two
+    // tiles.)
+    // The whole warp keeps the books, in step, and one elected lane issues (the
+    // descriptors stay in uniform registers).
+    const uint32_t sq = smem_u32(sQ), sr = smem_u32(sR);
+    const uint64_t qd0 = sdesc_sw128(sq, 16, 1024), rd0 = sdesc_sw128(sr, 16, 1024);
+    auto uni = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    auto wait = [&](uint64_t *bar, uint32_t par) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag, p.err, kErrWaitMma)) != 0;
+    };
+    int s_seg = 0, s_item = 0, s_blk = 0, s_nb = 0, s_qt = 0, s_qb = 0, s_lb = 0, s_t = 0;   // S: before it, and the place in its piece
+    int v_seg = 0, v_item = 0, v_blk = 0, v_nb = 0, v_qt = 0, v_lb = 0, v_t = 0;             // P V
+    bool s_in = false, v_in = false, ok = true, end = false;
+    int quse0 = 0, quse1 = 0;
+    auto issue_s = [&]() {   // S of the next item, if there is one
+      if (end) return;
+      if (!s_in) {
+        ok = wait(&ct.seg_full[s_seg % C::NSEG], (s_seg / C::NSEG) & 1);
+        if (!ok) return;
+        const PreSeg &sg = ct.seg[s_seg % C::NSEG];
+        s_nb = uni(sg.nb);
+        s_qt = uni(sg.qt);
+        s_qb = uni(sg.qb);
+        s_lb = s_t = 0;
+        s_in = true;
+        if (s_nb == 0) {
+          end = true;
+          return;
         }
+      }
+      const int qb = s_qb ^ s_t, sb = s_blk % C::NB, u0 = s_blk * (C::KU + C::VU);
+      if (s_lb == 0) ok = wait(&ct.q_full[qb], (qb ? quse1 : quse0) & 1);
+      if (ok && s_t == 0) ok = wait(&ct.k_full[sb], (s_blk / C::NB) & 1);
+      if (!ok) return;
+      tc_fence_after();
+      const uint32_t d = tmem + 128 * (s_item & 1);
+      const uint64_t qd = qd0 + static_cast<uint64_t>((qb * C::QT_BYTES) >> 4);
+      const bool k_done = s_t + 1 == s_qt, last = s_lb + 1 == s_nb;
+      if (elect_one()) {
+#pragma unroll
+        for (int ch = 0; ch < C::KU; ++ch) {
+          const uint64_t kd = rd0 + static_cast<uint64_t>((((u0 + ch) % C::NU) * C::UNIT) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_bf16(d, qd + ((ch * C::UNIT + kk * 32) >> 4), kd + ((kk * 32) >> 4), C::IDESC_S, (ch > 0 || kk > 0) ? 1u : 0u);
+        }
+        mma_commit(&ct.s_full[s_item & 1]);
+        if (k_done) mma_commit(&ct.k_empty[sb]);
+        if (last) mma_commit(&ct.q_empty[qb]);
+      }
+      __syncwarp();
+      if (last) ++(qb ? quse1 : quse0);
+      ++s_item;
+      if (++s_t == s_qt) {
+        s_t = 0;
+        ++s_blk;
+        if (++s_lb == s_nb) {
+          s_in = false;
+          ++s_seg;
+        }
+      }
+    };
+    issue_s();
+    if (ok) issue_s();
+    while (ok && v_item < s_item) {
+      if (!v_in) {   // S of the piece is out: its record is there
+        const PreSeg &sg = ct.seg[v_seg % C::NSEG];
+        v_nb = uni(sg.nb);
+        v_qt = uni(sg.qt);
+        v_lb = v_t = 0;
+        v_in = true;
+      }
+      const int w = v_item & 1, sb = v_blk % C::NB, v0 = (v_blk * (C::KU + C::VU) + C::KU) % C::NU;
+      const uint32_t pcol = tmem + 128 * w, o_col = tmem + C::O_COL + HD * w, par = (v_item >> 1) & 1;
+      const bool first = v_lb < (v_qt == 1 ? 2 : 1);   // the group's first block of the piece
+      const bool v_done = v_t + 1 == v_qt, last = v_done && v_lb + 1 == v_nb;
+      ok = wait(&ct.p_half[w], par) && (v_t > 0 || wait(&ct.v_full[sb], (v_blk / C::NB) & 1));
+      if (!ok) break;
+      // P V, the first 64 keys while the softmax is at the others; hd as 64 and
+      // 64 where the ring's end lies between its halves
+      const bool side = C::VU == 1 || v0 + 1 < C::NU;
+      const uint64_t vd = side ? sdesc_sw128(sr + v0 * C::UNIT, C::UNIT, 1024) : rd0 + static_cast<uint64_t>((v0 * C::UNIT) >> 4);
+      constexpr uint32_t IDESC_64 = idesc_bf16(128, 64, true);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (half == 1) ok = wait(&ct.p_full[w], par);
         if (!ok) break;
-        // (both groups count a tile's uses: with one tile they share it)
-        if (qt == 2) ++quse[0], ++quse[1], ++both;
-        else ++quse[qb0];
-        item0 += items;
-        blk0 += nb;
-        ++nseg;
-        mbar_arrive(&ct.seg_empty[ss]);
+        tc_fence_after();
+        if (elect_one()) {
+          if (side) {
+#pragma unroll
+            for (int ks = 4 * half; ks < 4 * half + 4; ++ks)   // 16 keys (two atoms) per MMA
+              mma_bf16_ts(o_col, pcol + ks * 8, vd + ((ks * 2048) >> 4), C::IDESC_PV, (!first || ks > 0) ? 1u : 0u);
+          } else {
+#pragma unroll
+            for (int ch = 0; ch < C::VU; ++ch)
+#pragma unroll
+              for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+                mma_bf16_ts(o_col + 64 * ch, pcol + ks * 8, (ch ? rd0 : vd) + ((ks * 2048) >> 4), IDESC_64, (!first || ks > 0) ? 1u : 0u);
+          }
+          mma_commit(half ? &ct.o_full[w] : &ct.h_full[w]);
+          if (half == 1 && v_done) mma_commit(&ct.v_empty[sb]);
+          if (half == 1 && last) mbar_arrive(&ct.seg_empty[v_seg % C::NSEG]);
+        }
+        __syncwarp();
       }
-      // every MMA issued above has completed before TMEM is freed
-      mma_commit(&ct.done);
-      const uint64_t t_end = globaltimer();
-      while (!mbar_try_wait(smem_u32(&ct.done), 0) && globaltimer() - t_end < kWaitLimitNs) {
+      if (!ok) break;
+      ++v_item;
+      if (++v_t == v_qt) {
+        v_t = 0;
+        ++v_blk;
+        if (++v_lb == v_nb) {
+          v_in = false;
+          ++v_seg;
+        }
       }
+      issue_s();
+    }
+    // every MMA issued above has completed before TMEM is freed
+    if (elect_one()) mma_commit(&ct.done);
+    __syncwarp();
+    const uint64_t t_end = globaltimer();
+    while (!mbar_try_wait(smem_u32(&ct.done), 0) && globaltimer() - t_end < kWaitLimitNs) {
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else {
     // ------------------------------------------------- softmax / epilogue
-    const int w = (warp - 4) >> 2;          // warp group: it takes every second item
+    const int w = (warp - 2) >> 2;          // warp group: it takes every second item
     const int qu = warp & 3;                // TMEM lane quarter
     const int row = qu * 32 + lane;         // row of the tile
     const uint32_t lane_base = static_cast<uint32_t>(qu * 32) << 16;
@@ -857,7 +935,6 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
     const uint32_t o_col = tmem + lane_base + C::O_COL + HD * w;
     const uint32_t o_other = tmem + lane_base + C::O_COL + HD * (w ^ 1);
     float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
-    constexpr float kRescaleAbove = 8.f;    // log2 units
     const float scale = p.scale_log2;
     const float2 sc2 = make_float2(scale, scale);
     int nseg = 0, item0 = 0;
@@ -898,13 +975,7 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
         if (!idle) {
           if (key0 + kBlk - 1 > sg.first + 128 * t + qu * 32) mask_block(s_col, limit - key0);
           // The group's first block of the piece sets each row's reference
-          // maximum.  From then on one pass over S while it holds; if a row of
-          // the warp rose more than 2^8 above it, the reference moves, O is
-          // rescaled and the probabilities are taken again from S, intact
-          // until P is stored.
-          uint32_t pk_lo[32], pk_hi[32];
-          float2 lsum = make_float2(0.f, 0.f);
-          float mq0 = -INFINITY, mq1 = -INFINITY, mq2 = -INFINITY, mq3 = -INFINITY;
+          // maximum.
           if (li < 2) {
             float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll 1
@@ -919,62 +990,6 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
             }
             m_ref = fmaxf(m0, m1) * scale;
           }
-          // (Always so.  As a condition it keeps the exponentials behind the maxima.)
-          const bool apart = nb > 0;
-          float negm = m_ref == -INFINITY ? 0.f : -m_ref;
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            float sv[64];
-            tmem_ld64(s_col + 64 * hh, sv);
-#pragma unroll
-            for (int e = 0; e < 64; e += 8) {
-              mq0 = max3f(mq0, sv[e], sv[e + 1]);
-              mq1 = max3f(mq1, sv[e + 2], sv[e + 3]);
-              mq2 = max3f(mq2, sv[e + 4], sv[e + 5]);
-              mq3 = max3f(mq3, sv[e + 6], sv[e + 7]);
-            }
-            if (apart) probs<64>(sv, sc2, negm, hh ? pk_hi : pk_lo, lsum);
-          }
-          const float mx = fmaxf(fmaxf(mq0, mq1), fmaxf(mq2, mq3)) * scale;
-          const bool grow = mx > m_ref + kRescaleAbove;
-          if (__any_sync(0xffffffffu, grow)) {
-            if (li >= 2) {
-              // O holds the group's blocks before: their P V must be done
-              fail = !mbar_wait(&ct.o_full[w], ((item - 2) >> 1) & 1, abort_flag, p.err, kErrWaitSoftmax);
-              if (__any_sync(0xffffffffu, fail)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              const float alpha = grow ? ex2_approx(m_ref - mx) : 1.f;
-#pragma unroll 1
-              for (int cc = 0; cc < HD / 32; ++cc) {
-                float v[32];
-                tmem_ld32(o_col + cc * 32, v);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] *= alpha;
-                tmem_st32(o_col + cc * 32, v);
-              }
-              if (grow) l *= alpha;
-            }
-            if (grow) m_ref = mx;
-            negm = m_ref == -INFINITY ? 0.f : -m_ref;   // a row that has seen nothing yet
-            // P of 32 keys goes over 16 columns of S that have been read
-            lsum = make_float2(0.f, 0.f);
-#pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
-              float sv[32];
-              uint32_t pk[16];
-              tmem_ld32(s_col + 32 * k, sv);
-              probs<32>(sv, sc2, negm, pk, lsum);
-              tmem_st16u(s_col + 16 * k, pk);
-            }
-          } else {
-            // P over S: keys 0-63 in columns 0-31, keys 64-127 in 32-63
-            tmem_st32u(s_col, pk_lo);
-            tmem_st32u(s_col + 32, pk_hi);
-          }
-          l += lsum.x + lsum.y;
         }
         if (lending) {
           // P V of this item overwrites O: the other group must have read it
@@ -985,8 +1000,65 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
           }
           lending = false;
         }
-        tc_fence_before();
-        mbar_arrive(&ct.p_full[w]);
+        // Half the keys at a time, so that P V of the first runs beside the
+        // second.  No maximum is taken as long as the reference holds: a half
+        // whose probabilities sum to more than 2^14 says that a logit rose above
+        // it (P and the sums have room for far more); then the reference moves, O
+        // is rescaled and the half is taken again from S, intact until its P is
+        // stored.  P goes over S: keys 0-63 in columns 0-31, keys 64-127 in 32-63.
+#pragma unroll 1
+        for (int hh = 0; hh < 2; ++hh) {
+          if (!idle) {
+            float sv[64];
+            uint32_t pk[32];
+            float2 sum = make_float2(0.f, 0.f);
+            float negm = m_ref == -INFINITY ? 0.f : -m_ref;   // a row that has seen nothing yet
+            tmem_ld64(s_col + 64 * hh, sv);
+            probs<64>(sv, sc2, negm, pk, sum);
+            // (a row that has seen nothing has no reference to hold)
+            const bool grow = sum.x + sum.y > 16384.f || m_ref == -INFINITY;
+            if (__any_sync(0xffffffffu, grow)) {
+              // O holds the group's blocks before, and the half before: their P V must be done
+              fail = false;
+              if (hh == 1) fail = !mbar_wait(&ct.h_full[w], (item >> 1) & 1, abort_flag, p.err, kErrWaitSoftmax);
+              else if (li >= 2) fail = !mbar_wait(&ct.o_full[w], ((item - 2) >> 1) & 1, abort_flag, p.err, kErrWaitSoftmax);
+              if (__any_sync(0xffffffffu, fail)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              float mx = -INFINITY;
+              tmem_ld64(s_col + 64 * hh, sv);
+#pragma unroll
+              for (int e = 0; e < 64; e += 2) mx = max3f(mx, sv[e], sv[e + 1]);
+              mx *= scale;
+              const bool up = grow && mx > m_ref;
+              const float alpha = up ? ex2_approx(m_ref - mx) : 1.f;
+              if (hh == 1 || li >= 2) {
+#pragma unroll 1
+                for (int cc = 0; cc < HD / 32; ++cc) {
+                  float v[32];
+                  tmem_ld32(o_col + cc * 32, v);
+#pragma unroll
+                  for (int k = 0; k < 32; ++k) v[k] *= alpha;
+                  tmem_st32(o_col + cc * 32, v);
+                }
+              }
+              if (up) {
+                l *= alpha;
+                m_ref = mx;
+              }
+              negm = m_ref == -INFINITY ? 0.f : -m_ref;
+              sum = make_float2(0.f, 0.f);
+              probs<64>(sv, sc2, negm, pk, sum);
+            }
+            tmem_st32u(s_col + 32 * hh, pk);
+            l += sum.x + sum.y;
+          }
+          tc_fence_before();
+          mbar_arrive(hh ? &ct.p_full[w] : &ct.p_half[w]);
+        }
+        if (!ok) break;
       }
       if (!ok) break;
       // ---- the piece is done: its output, or its partial
@@ -1022,7 +1094,7 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
           const int tok = sg.t0 + 128 * t + row, slot = sg.slot;
           const float inv = 1.f / l;
           uint4 *dst = reinterpret_cast<uint4 *>(p.o + (static_cast<int64_t>(tok) * p.H + sg.h) * HD);
-          float *part = p.part + (static_cast<int64_t>(max(slot, 0)) * 256 + 128 * t + row) * (HD + 4);
+          float *part = p.part + max(slot, 0) * part_floats(HD) + 128 * t + row;
 #pragma unroll 1
           for (int cc = 0; cc < HD / 32; ++cc) {
             float v[32];
@@ -1040,13 +1112,14 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
                                              pack_bf16x2(v[8 * k + 2] * inv, v[8 * k + 3] * inv),
                                              pack_bf16x2(v[8 * k + 4] * inv, v[8 * k + 5] * inv),
                                              pack_bf16x2(v[8 * k + 6] * inv, v[8 * k + 7] * inv));
-            } else if (valid) {
+            } else if (slot >= 0) {
+              // (column by column: a warp's stores fill whole lines; row by row they
+              // took 5,000 cycles a piece.  Rows that are none have a place too.)
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                reinterpret_cast<float4 *>(part + cc * 32)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+              for (int k = 0; k < 32; ++k) part[(cc * 32 + k) * 256] = v[k];
             }
           }
-          if (valid && slot >= 0) *reinterpret_cast<float2 *>(part + HD) = make_float2(m_ref, l);
+          if (slot >= 0) reinterpret_cast<float2 *>(part - row - 128 * t + 256 * HD)[128 * t + row] = make_float2(m_ref, l);
         }
         tc_fence_before();
         if (joint) mbar_arrive(&ct.ml_empty[w ^ 1]);
@@ -1067,57 +1140,45 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
   }
 }
 
-// Merge of the units that were cut: CTA (w, y) takes every gridDim.y-th row
-// group of the unit whose first piece CTA w computed; eight lanes a row.
+// Merge of the units that were cut: CTA (w, y) takes rows 32 y .. 32 y + 31 of the
+// unit whose first piece CTA w computed, a lane a row, a warp HD / 8 columns.
 //   o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,   M = max_s m_s
 template <int HD>
 __global__ void __launch_bounds__(256) latent_prefill_merge_kernel(const __grid_constant__ PreParams p) {
+  constexpr int COLS = HD / 8;
   pdl_wait();
   pdl_trigger();
   const int w = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4 rec = *reinterpret_cast<const int4 *>(p.rec + w * 8);
-  const int pieces = rec.x, rows = rec.w;
-  if (pieces == 0) return;
+  const int pieces = rec.x, row = blockIdx.y * 32 + lane;
+  if (pieces == 0 || static_cast<int>(blockIdx.y) * 32 >= rec.w) return;
   // piece 0 in slot 2 w + 1, piece s > 0 in slot 2 (w + s)
-  auto src = [&](int s, int row) {
-    return p.part + (static_cast<int64_t>(s == 0 ? 2 * w + 1 : 2 * (w + s)) * 256 + row) * (HD + 4);
-  };
-  constexpr int PER = HD / 32;   // float4s of a lane: columns 4 (lane + 8 k)
-  const int l8 = lane & 7;
-  for (int row = (blockIdx.y * 8 + warp) * 4 + (lane >> 3); row < rows; row += gridDim.y * 32) {
-    float M = -INFINITY, L = 0.f;
-    float4 acc[PER];
+  auto src = [&](int s) { return p.part + (s == 0 ? 2 * w + 1 : 2 * (w + s)) * part_floats(HD); };
+  float M = -INFINITY, L = 0.f, acc[COLS];
 #pragma unroll
-    for (int k = 0; k < PER; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int s = 0; s < pieces; ++s) {
-      const float *x = src(s, row);
-      float4 v[PER];
+  for (int k = 0; k < COLS; ++k) acc[k] = 0.f;
+#pragma unroll 2
+  for (int s = 0; s < pieces; ++s) {
+    const float *x = src(s);
+    float v[COLS];
 #pragma unroll
-      for (int k = 0; k < PER; ++k) v[k] = reinterpret_cast<const float4 *>(x)[l8 + 8 * k];
-      const float2 ml = *reinterpret_cast<const float2 *>(x + HD);
-      if (ml.x == -INFINITY) {   // the row saw nothing in this piece, or only NaN
-        L += ml.y;
-        continue;
-      }
-      const float mn = fmaxf(M, ml.x);
-      const float a = M == -INFINITY ? 0.f : ex2_approx(M - mn), b = ex2_approx(ml.x - mn);
-      L = (M == -INFINITY ? L : L * a) + b * ml.y;
-      M = mn;
+    for (int k = 0; k < COLS; ++k) v[k] = x[(warp * COLS + k) * 256 + row];
+    const float2 ml = reinterpret_cast<const float2 *>(x + 256 * HD)[row];
+    const float mn = fmaxf(M, ml.x);
+    // (a piece of which the row saw nothing has a sum of 0, or NaN if it saw one)
+    const float a = M == -INFINITY ? 0.f : ex2_approx(M - mn), b = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mn);
+    L = (M == -INFINITY ? L : L * a) + (ml.x == -INFINITY ? ml.y : b * ml.y);
+    M = mn;
 #pragma unroll
-      for (int k = 0; k < PER; ++k) {
-        acc[k].x = fmaf(acc[k].x, a, b * v[k].x);
-        acc[k].y = fmaf(acc[k].y, a, b * v[k].y);
-        acc[k].z = fmaf(acc[k].z, a, b * v[k].z);
-        acc[k].w = fmaf(acc[k].w, a, b * v[k].w);
-      }
-    }
-    const float inv = 1.f / L;
-    uint2 *dst = reinterpret_cast<uint2 *>(p.o + (static_cast<int64_t>(rec.y + row) * p.H + rec.z) * HD);
-#pragma unroll
-    for (int k = 0; k < PER; ++k)
-      dst[l8 + 8 * k] = make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv), pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+    for (int k = 0; k < COLS; ++k) acc[k] = acc[k] * a + (b == 0.f ? 0.f : b * v[k]);
   }
+  if (row >= rec.w) return;
+  const float inv = 1.f / L;
+  uint4 *dst = reinterpret_cast<uint4 *>(p.o + (static_cast<int64_t>(rec.y + row) * p.H + rec.z) * HD + warp * COLS);
+#pragma unroll
+  for (int k = 0; k < COLS; k += 8)
+    dst[k / 8] = make_uint4(pack_bf16x2(acc[k] * inv, acc[k + 1] * inv), pack_bf16x2(acc[k + 2] * inv, acc[k + 3] * inv),
+                            pack_bf16x2(acc[k + 4] * inv, acc[k + 5] * inv), pack_bf16x2(acc[k + 6] * inv, acc[k + 7] * inv));
 }
 
 // The workspace's keys: blocks of 128, each request's from a block of its own.
@@ -1137,7 +1198,7 @@ cudaError_t launch_expand(const CUtensorMap &tk, const CUtensorMap &tw, const CU
   using C = ExpCfg<HD, RANK>;
   cudaError_t e = ensure_max_smem(reinterpret_cast<const void *>(latent_expand_kernel<HD, RANK>), C::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl(latent_expand_kernel<HD, RANK>, dim3(device_sm_count()), dim3(C::THREADS), C::SMEM, st, 1, tk, tw, tr, p);
+  return launch_pdl(latent_expand_kernel<HD, RANK>, dim3(device_sm_count() / 2 * 2), dim3(C::THREADS), C::SMEM, st, 2, tk, tw, tr, p);
 }
 
 template <int HD>
@@ -1158,14 +1219,14 @@ cudaError_t launch_prefill(const LatentArgs &a, PreParams &p, int group, __nv_bf
   if (e == cudaSuccess) e = encode_tmap_2d(&tr, rope, kLatentRope, rows, kLatentRope * 2, 64, kBlk);
   if (e == cudaSuccess) e = encode_tmap_2d(&ts, rope, kLatentRope, rows, kLatentRope * 2, 64, 8);
   if (e == cudaSuccess) e = encode_tmap_5d(&tk, a.pool, dk, sk, bk);
-  if (e == cudaSuccess) e = encode_tmap_2d(&tw, a.w_kv, a.rank, H * 2 * HD, static_cast<uint64_t>(a.rank) * 2, 64, 2 * HD);
+  if (e == cudaSuccess) e = encode_tmap_2d(&tw, a.w_kv, a.rank, H * 2 * HD, static_cast<uint64_t>(a.rank) * 2, 64, HD);
   if (e == cudaSuccess) e = ensure_max_smem(reinterpret_cast<const void *>(latent_prefill_kernel<HD>), C::SMEM);
   const int ctas = std::min(device_sm_count(), kMaxCtas);
   for (p.h0 = 0; p.h0 < a.H && e == cudaSuccess; p.h0 += group) {
     p.HG = std::min(group, a.H - p.h0);
     e = a.rank == 512 ? launch_expand<HD, 512>(tk, tw, ts, p, st) : launch_expand<HD, 256>(tk, tw, ts, p, st);
     if (e == cudaSuccess) e = launch_pdl(latent_prefill_kernel<HD>, dim3(ctas), dim3(C::THREADS), C::SMEM, st, 1, tq, tqr, tkv, tr, p);
-    if (e == cudaSuccess) e = launch_pdl(latent_prefill_merge_kernel<HD>, dim3(ctas, 4), dim3(256), 0, st, 1, p);
+    if (e == cudaSuccess) e = launch_pdl(latent_prefill_merge_kernel<HD>, dim3(ctas, 8), dim3(256), 0, st, 1, p);
   }
   return e;
 }
@@ -1178,7 +1239,7 @@ size_t latent_prefill_workspace_bytes(int64_t kv_tokens, int64_t n_reqs, int64_t
   const int64_t blocks = cap_blocks(kv_tokens, n_reqs);
   return align256(static_cast<size_t>(blocks) * kBlk * 4 * hd * group_heads(blocks, H, hd)) +
          align256(static_cast<size_t>(blocks) * kBlk * kLatentRope * 2) + kRecBytes +
-         static_cast<size_t>(2) * kMaxCtas * 256 * (hd + 4) * sizeof(float);
+         static_cast<size_t>(2) * kMaxCtas * part_floats(hd) * sizeof(float);
 }
 
 cudaError_t latent_prefill_run(const LatentArgs &a, cudaStream_t st) {
@@ -1190,6 +1251,7 @@ cudaError_t latent_prefill_run(const LatentArgs &a, cudaStream_t st) {
   PreParams p;
   p.kv = reinterpret_cast<__nv_bfloat16 *>(w);
   p.o = static_cast<__nv_bfloat16 *>(a.o);
+  p.w_kv = static_cast<const __nv_bfloat16 *>(a.w_kv);
   p.qo_indptr = a.qo_indptr;
   p.kv_len = a.kv_len;
   p.bt_indptr = a.bt_indptr;

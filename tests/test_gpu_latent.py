@@ -251,9 +251,12 @@ def test_expanded_long_caches_cut_over_many_ctas(mb, reqs, H, hd, rank):
 
 
 def test_expanded_groups_of_heads(mb):
-    """Keys of 26,000 tokens: 13.4 MB a head, so seven heads are three groups."""
-    b = Batch([(25990, 10)], 7, 128, 512, seed=33)
-    b.check(b.run(mb, "expanded"), "expanded")
+    """Keys of 26,000 tokens, 6.7 MB a head: 100 heads are two groups of 50."""
+    b = Batch([(25990, 10)], 100, 64, 256, seed=33)
+    got = b.run(mb, "expanded")
+    heads = [0, 49, 50, 99]
+    b.q, b.q_rope, b.w, b.H = b.q[:, heads], b.q_rope[:, heads], b.w[heads], len(heads)
+    b.check(got[:, heads], "expanded")
 
 
 def test_expanded_more_requests_than_threads(mb):
