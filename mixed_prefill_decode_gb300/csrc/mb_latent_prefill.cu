@@ -475,7 +475,7 @@ struct PreCfg {
   static constexpr int OFF_CTRL = OFF_R + NU * UNIT;
   static constexpr int OFF_ML = OFF_CTRL + 1024;      // (m, l) of 128 rows, from one warp group to the other
   static constexpr int SMEM = OFF_ML + 1024;
-  static constexpr int THREADS = 320;                 // TMA, MMA, 2 x 4 softmax warps
+  static constexpr int THREADS = 384;                 // TMA, 2 MMA issuers, one idle, 2 x 4 softmax warps
   static constexpr uint32_t IDESC_S = idesc_bf16(128, 128, false);
   static constexpr uint32_t IDESC_PV = idesc_bf16(128, HD, true);
   static constexpr uint32_t TMEM_COLS = 512;          // S/P buffers at 0 and 128, O of the two groups from 256
@@ -500,11 +500,12 @@ template <int HD>
 struct PreCtrl {
   using C = PreCfg<HD>;
   uint64_t q_full[2], q_empty[2];
-  uint64_t k_full[C::NB], k_empty[C::NB], v_full[C::NB], v_empty[C::NB];   // by block
+  uint64_t k_full[C::NB], k_empty[C::NB], v_full[C::NB], v_empty[C::NB];   // by block; empty: both groups are done with it
   uint64_t s_full[2], p_half[2], p_full[2], h_full[2], o_full[2];   // by warp group: S; P of half the keys, of all; P V of them
   uint64_t ml_full[2];    // the group's (m, l) are in shared memory
   uint64_t ml_empty[2];   // the other group has read them and this group's O
   uint64_t seg_full[C::NSEG], seg_empty[C::NSEG];
+  uint64_t turn[2];       // the other group's products are issued
   uint64_t done;
   PreSeg seg[C::NSEG];
   int64_t sums[C::THREADS / 32];
@@ -574,7 +575,7 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ct.q_full[b], 1);
-      mbar_init(&ct.q_empty[b], 1);
+      mbar_init(&ct.q_empty[b], 2);
       mbar_init(&ct.s_full[b], 1);
       mbar_init(&ct.p_half[b], 128);
       mbar_init(&ct.p_full[b], 128);
@@ -585,15 +586,16 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
     }
     for (int s = 0; s < C::NB; ++s) {
       mbar_init(&ct.k_full[s], 1);
-      mbar_init(&ct.k_empty[s], 1);
+      mbar_init(&ct.k_empty[s], 2);
       mbar_init(&ct.v_full[s], 1);
-      mbar_init(&ct.v_empty[s], 1);
+      mbar_init(&ct.v_empty[s], 2);
     }
     for (int s = 0; s < C::NSEG; ++s) {
       mbar_init(&ct.seg_full[s], 1);
-      mbar_init(&ct.seg_empty[s], 9);   // the MMA issuer and the 8 softmax warps
+      mbar_init(&ct.seg_empty[s], 10);   // the 2 MMA issuers and the 8 softmax warps
     }
-    mbar_init(&ct.done, 1);
+    for (int b = 0; b < 2; ++b) mbar_init(&ct.turn[b], 1);
+    mbar_init(&ct.done, 2);
     ct.abort = 0;
     ct.start_req = -1;
     fence_mbar_init();
@@ -794,129 +796,141 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // --------------------------------------------------------- MMA issuer
-    // Items in order, block by block and tile by tile, so that they alternate
-    // between the groups: P V of an item, then S of the group's next one (P lies
-    // over S, so not before), while the other group is at its softmax.  (With an
-    // issuer per group, products of both interleaved, finished together and
-    // left both groups at their softmax together: 4,900 cycles a block of two
-    // tiles.)
-    // The whole warp keeps the books, in step, and one elected lane issues (the
-    // descriptors stay in uniform registers).
-    const uint32_t sq = smem_u32(sQ), sr = smem_u32(sR);
-    const uint64_t qd0 = sdesc_sw128(sq, 16, 1024), rd0 = sdesc_sw128(sr, 16, 1024);
+  } else if (warp <= 2) {
+    // -------------------------------------------------------- MMA issuers
+    // One per group, strictly in turn: P V of the group's item, then S of its next
+    // one (P lies over S, so not before), while the other group is at its
+    // softmax.  Side by side without turns, both groups' products finished
+    // together and left both at their softmax together (4,900 cycles a block
+    // of two tiles); by one warp, its waits and commits lay between the products
+    // (4,250).  The whole warp keeps the books, in step, and one elected lane issues
+    // (the descriptors stay in uniform registers).
+    const int w = warp - 1;
+    const uint32_t sr = smem_u32(sR);
+    const uint64_t qd0 = sdesc_sw128(smem_u32(sQ), 16, 1024), rd0 = sdesc_sw128(sr, 16, 1024);
+    const uint32_t s_col = tmem + 128 * w, o_col = tmem + C::O_COL + HD * w;
     auto uni = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
     auto wait = [&](uint64_t *bar, uint32_t par) {
       return __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag, p.err, kErrWaitMma)) != 0;
     };
-    int s_seg = 0, s_item = 0, s_blk = 0, s_nb = 0, s_qt = 0, s_qb = 0, s_lb = 0, s_t = 0;   // S: before it, and the place in its piece
-    int v_seg = 0, v_item = 0, v_blk = 0, v_nb = 0, v_qt = 0, v_lb = 0, v_t = 0;             // P V
-    bool s_in = false, v_in = false, ok = true, end = false;
-    int quse0 = 0, quse1 = 0;
-    auto issue_s = [&]() {   // S of the next item, if there is one
-      if (end) return;
-      if (!s_in) {
-        ok = wait(&ct.seg_full[s_seg % C::NSEG], (s_seg / C::NSEG) & 1);
-        if (!ok) return;
-        const PreSeg &sg = ct.seg[s_seg % C::NSEG];
-        s_nb = uni(sg.nb);
-        s_qt = uni(sg.qt);
-        s_qb = uni(sg.qb);
-        s_lb = s_t = 0;
-        s_in = true;
-        if (s_nb == 0) {
-          end = true;
-          return;
-        }
-      }
-      const int qb = s_qb ^ s_t, sb = s_blk % C::NB, u0 = s_blk * (C::KU + C::VU);
-      if (s_lb == 0) ok = wait(&ct.q_full[qb], (qb ? quse1 : quse0) & 1);
-      if (ok && s_t == 0) ok = wait(&ct.k_full[sb], (s_blk / C::NB) & 1);
-      if (!ok) return;
-      tc_fence_after();
-      const uint32_t d = tmem + 128 * (s_item & 1);
-      const uint64_t qd = qd0 + static_cast<uint64_t>((qb * C::QT_BYTES) >> 4);
-      const bool k_done = s_t + 1 == s_qt, last = s_lb + 1 == s_nb;
-      if (elect_one()) {
-#pragma unroll
-        for (int ch = 0; ch < C::KU; ++ch) {
-          const uint64_t kd = rd0 + static_cast<uint64_t>((((u0 + ch) % C::NU) * C::UNIT) >> 4);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_bf16(d, qd + ((ch * C::UNIT + kk * 32) >> 4), kd + ((kk * 32) >> 4), C::IDESC_S, (ch > 0 || kk > 0) ? 1u : 0u);
-        }
-        mma_commit(&ct.s_full[s_item & 1]);
-        if (k_done) mma_commit(&ct.k_empty[sb]);
-        if (last) mma_commit(&ct.q_empty[qb]);
-      }
-      __syncwarp();
-      if (last) ++(qb ? quse1 : quse0);
-      ++s_item;
-      if (++s_t == s_qt) {
-        s_t = 0;
-        ++s_blk;
-        if (++s_lb == s_nb) {
-          s_in = false;
-          ++s_seg;
-        }
-      }
-    };
-    issue_s();
-    if (ok) issue_s();
-    while (ok && v_item < s_item) {
-      if (!v_in) {   // S of the piece is out: its record is there
-        const PreSeg &sg = ct.seg[v_seg % C::NSEG];
-        v_nb = uni(sg.nb);
-        v_qt = uni(sg.qt);
-        v_lb = v_t = 0;
-        v_in = true;
-      }
-      const int w = v_item & 1, sb = v_blk % C::NB, v0 = (v_blk * (C::KU + C::VU) + C::KU) % C::NU;
-      const uint32_t pcol = tmem + 128 * w, o_col = tmem + C::O_COL + HD * w, par = (v_item >> 1) & 1;
-      const bool first = v_lb < (v_qt == 1 ? 2 : 1);   // the group's first block of the piece
-      const bool v_done = v_t + 1 == v_qt, last = v_done && v_lb + 1 == v_nb;
-      ok = wait(&ct.p_half[w], par) && (v_t > 0 || wait(&ct.v_full[sb], (v_blk / C::NB) & 1));
+    int nseg = 0, item0 = 0, blk0 = 0, nb = 0, qt = 0, qb0 = 0, li = 0, items = 0;   // the piece, the place in it
+    int quse0 = 0, quse1 = 0, slot = 0;
+    int v_seg = -1, v_sb = 0, v_u = 0, v_ph = 0, v_par = 0;   // the item whose P V comes next (v_seg: the piece it ends, -1: none)
+    bool in = false, end = false, v_have = false, v_first = false, v_twice = false, ok = true;
+    while (ok) {
+      if (v_have) ok = wait(&ct.p_half[w], v_par) && wait(&ct.v_full[v_sb], v_ph);
+      if (ok && (w == 1 || slot > 0)) ok = wait(&ct.turn[w], (w == 1 ? slot : slot - 1) & 1);
       if (!ok) break;
-      // P V, the first 64 keys while the softmax is at the others; hd as 64 and
-      // 64 where the ring's end lies between its halves
-      const bool side = C::VU == 1 || v0 + 1 < C::NU;
-      const uint64_t vd = side ? sdesc_sw128(sr + v0 * C::UNIT, C::UNIT, 1024) : rd0 + static_cast<uint64_t>((v0 * C::UNIT) >> 4);
-      constexpr uint32_t IDESC_64 = idesc_bf16(128, 64, true);
+      tc_fence_after();
+      if (v_have) {
+        // P V, the first 64 keys while the softmax may be at the others; hd as 64
+        // and 64 where the ring's end lies between its halves
+        const bool side = C::VU == 1 || v_u + 1 < C::NU;
+        const uint64_t vd = side ? sdesc_sw128(sr + v_u * C::UNIT, C::UNIT, 1024) : rd0 + static_cast<uint64_t>((v_u * C::UNIT) >> 4);
+        constexpr uint32_t IDESC_64 = idesc_bf16(128, 64, true);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (half == 1) ok = wait(&ct.p_full[w], par);
+        for (int half = 0; half < 2; ++half) {
+          if (half == 1) ok = wait(&ct.p_full[w], v_par);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            if (side) {
+#pragma unroll
+              for (int ks = 4 * half; ks < 4 * half + 4; ++ks)   // 16 keys (two atoms) per MMA
+                mma_bf16_ts(o_col, s_col + ks * 8, vd + ((ks * 2048) >> 4), C::IDESC_PV, (!v_first || ks > 0) ? 1u : 0u);
+            } else {
+#pragma unroll
+              for (int ch = 0; ch < C::VU; ++ch)
+#pragma unroll
+                for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+                  mma_bf16_ts(o_col + 64 * ch, s_col + ks * 8, (ch ? rd0 : vd) + ((ks * 2048) >> 4), IDESC_64, (!v_first || ks > 0) ? 1u : 0u);
+            }
+            mma_commit(half ? &ct.o_full[w] : &ct.h_full[w]);
+            if (half == 1) {
+              mma_commit(&ct.v_empty[v_sb]);
+              if (v_twice) mma_commit(&ct.v_empty[v_sb]);   // (for the other group, which does not take this block)
+              if (v_seg >= 0) mbar_arrive(&ct.seg_empty[v_seg % C::NSEG]);
+            }
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+      // the group's next item
+      while (ok && !end && !in) {
+        ok = wait(&ct.seg_full[nseg % C::NSEG], (nseg / C::NSEG) & 1);
+        if (!ok) break;
+        const PreSeg &sg = ct.seg[nseg % C::NSEG];
+        nb = uni(sg.nb);
+        qt = uni(sg.qt);
+        qb0 = uni(sg.qb);
+        if (nb == 0) {
+          end = true;
+          break;
+        }
+        items = nb * qt;
+        li = (item0 & 1) ^ w;
+        in = li < items;
+        if (!in) {   // (one block, and it is the other group's)
+          if (lane == 0) mbar_arrive(&ct.seg_empty[nseg % C::NSEG]);
+          ++quse0, quse0 -= qb0, quse1 += qb0;
+          item0 += items;
+          blk0 += nb;
+          ++nseg;
+        }
+      }
+      if (!ok) break;
+      v_have = in;
+      if (in) {
+        const int blk = blk0 + (qt == 2 ? li >> 1 : li), sb = blk % C::NB, u0 = blk * (C::KU + C::VU);
+        const int qb = qt == 2 ? qb0 ^ (li & 1) : qb0;
+        if (li < 2) ok = wait(&ct.q_full[qb], (qb ? quse1 : quse0) & 1);
+        ok = ok && wait(&ct.k_full[sb], (blk / C::NB) & 1);
         if (!ok) break;
         tc_fence_after();
+        const uint64_t qd = qd0 + static_cast<uint64_t>((qb * C::QT_BYTES) >> 4);
+        const bool last = li + 2 >= items, lone = qt == 2 || items == 1;   // lone: the tile's only user
         if (elect_one()) {
-          if (side) {
 #pragma unroll
-            for (int ks = 4 * half; ks < 4 * half + 4; ++ks)   // 16 keys (two atoms) per MMA
-              mma_bf16_ts(o_col, pcol + ks * 8, vd + ((ks * 2048) >> 4), C::IDESC_PV, (!first || ks > 0) ? 1u : 0u);
-          } else {
+          for (int ch = 0; ch < C::KU; ++ch) {
+            const uint64_t kd = rd0 + static_cast<uint64_t>((((u0 + ch) % C::NU) * C::UNIT) >> 4);
 #pragma unroll
-            for (int ch = 0; ch < C::VU; ++ch)
-#pragma unroll
-              for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
-                mma_bf16_ts(o_col + 64 * ch, pcol + ks * 8, (ch ? rd0 : vd) + ((ks * 2048) >> 4), IDESC_64, (!first || ks > 0) ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16(s_col, qd + ((ch * C::UNIT + kk * 32) >> 4), kd + ((kk * 32) >> 4), C::IDESC_S, (ch > 0 || kk > 0) ? 1u : 0u);
           }
-          mma_commit(half ? &ct.o_full[w] : &ct.h_full[w]);
-          if (half == 1 && v_done) mma_commit(&ct.v_empty[sb]);
-          if (half == 1 && last) mbar_arrive(&ct.seg_empty[v_seg % C::NSEG]);
+          mbar_arrive(&ct.turn[w ^ 1]);
+          mma_commit(&ct.s_full[w]);
+          mma_commit(&ct.k_empty[sb]);
+          if (qt == 1) mma_commit(&ct.k_empty[sb]);
+          if (last) {
+            mma_commit(&ct.q_empty[qb]);
+            if (lone) mma_commit(&ct.q_empty[qb]);
+          }
         }
         __syncwarp();
-      }
-      if (!ok) break;
-      ++v_item;
-      if (++v_t == v_qt) {
-        v_t = 0;
-        ++v_blk;
-        if (++v_lb == v_nb) {
-          v_in = false;
-          ++v_seg;
+        v_first = li < 2;
+        v_twice = qt == 1;
+        v_sb = sb;
+        v_ph = (blk / C::NB) & 1;
+        v_u = (u0 + C::KU) % C::NU;
+        v_par = ((item0 + li) >> 1) & 1;
+        v_seg = last ? nseg : -1;
+        li += 2;
+        if (last) {
+          // (both groups count a tile's uses, whoever they are)
+          if (qt == 2) ++quse0, ++quse1;
+          else ++quse0, quse0 -= qb0, quse1 += qb0;
+          item0 += items;
+          blk0 += nb;
+          ++nseg;
+          in = false;
         }
+      } else {
+        if (elect_one()) mbar_arrive(&ct.turn[w ^ 1]);
+        __syncwarp();
       }
-      issue_s();
+      ++slot;
+      if (end && !v_have) break;
     }
     // every MMA issued above has completed before TMEM is freed
     if (elect_one()) mma_commit(&ct.done);
@@ -925,9 +939,9 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
     while (!mbar_try_wait(smem_u32(&ct.done), 0) && globaltimer() - t_end < kWaitLimitNs) {
     }
     __syncwarp();
-  } else {
+  } else if (warp >= 4) {
     // ------------------------------------------------- softmax / epilogue
-    const int w = (warp - 2) >> 2;          // warp group: it takes every second item
+    const int w = (warp - 4) >> 2;          // warp group: it takes every second item
     const int qu = warp & 3;                // TMEM lane quarter
     const int row = qu * 32 + lane;         // row of the tile
     const uint32_t lane_base = static_cast<uint32_t>(qu * 32) << 16;
