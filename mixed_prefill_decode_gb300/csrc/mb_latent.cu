@@ -596,31 +596,34 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
     // --------------------------------------------------------- MMA issuers
     // Warp 1 issues S, a block ahead of the softmax (two buffers) and on into the
     // next piece, warp 2 the products with V: neither's commits and waits hold
-    // up the other.
-    if (lane == 0) {
-      auto wait = [&](uint64_t *bar, uint32_t par) { return mbar_wait(bar, par, abort_flag, p.err, kErrWaitMma); };
-      const uint64_t kd0 = sdesc_sw128(smem_u32(sK), 16, C::ATOM);
-      const uint64_t qd0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
-      const uint64_t vd0 = sdesc_sw128(smem_u32(sK), 1024, C::ATOM);
-      const uint64_t pd0 = sdesc_sw128(smem_u32(sP), 16, 1024);
-      const uint32_t idesc_pv = idesc_bf16_ab(128, p.N, true, false);
-      int nseg = 0, item = 0;
-      bool ok = true;
-      while (ok) {
-        const int ss = nseg % C::NSEG;
-        ok = wait(&ct.seg_full[ss], (nseg / C::NSEG) & 1);
-        if (!ok) break;
-        const int nb = ct.seg[ss].nb;
-        if (nb == 0) break;
-        if (warp == 1) ok = wait(&ct.q_full, nseg & 1);
-        for (int lb = 0; lb < nb && ok; ++lb, ++item) {
-          const int st = item % C::NST;
-          if (warp == 1) {
-            ok = wait(&ct.k_full[st], (item / C::NST) & 1) && wait(&ct.s_empty[item & 1], ((item >> 1) & 1) ^ 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t d = tmem + 64 * (item & 1);
-            const uint64_t kd = kd0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
+    // up the other.  Each warp keeps the books, in step, and one elected lane issues
+    // (the descriptors stay in uniform registers).
+    auto wait = [&](uint64_t *bar, uint32_t par) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag, p.err, kErrWaitMma)) != 0;
+    };
+    const uint64_t kd0 = sdesc_sw128(smem_u32(sK), 16, C::ATOM);
+    const uint64_t qd0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
+    const uint64_t vd0 = sdesc_sw128(smem_u32(sK), 1024, C::ATOM);
+    const uint64_t pd0 = sdesc_sw128(smem_u32(sP), 16, 1024);
+    const uint32_t idesc_pv = idesc_bf16_ab(128, p.N, true, false);
+    int nseg = 0, item = 0;
+    bool ok = true;
+    while (ok) {
+      const int ss = nseg % C::NSEG;
+      ok = wait(&ct.seg_full[ss], (nseg / C::NSEG) & 1);
+      if (!ok) break;
+      const int nb = __shfl_sync(0xffffffffu, ct.seg[ss].nb, 0);
+      if (nb == 0) break;
+      if (warp == 1) ok = wait(&ct.q_full, nseg & 1);
+      for (int lb = 0; lb < nb && ok; ++lb, ++item) {
+        const int st = item % C::NST;
+        if (warp == 1) {
+          ok = wait(&ct.k_full[st], (item / C::NST) & 1) && wait(&ct.s_empty[item & 1], ((item >> 1) & 1) ^ 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t d = tmem + 64 * (item & 1);
+          const uint64_t kd = kd0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
+          if (elect_one()) {
 #pragma unroll
             for (int ch = 0; ch < C::NC; ++ch)
 #pragma unroll
@@ -629,11 +632,13 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
                          (ch > 0 || kk > 0) ? 1u : 0u);
             mma_commit(&ct.s_full[item & 1]);
             if (lb + 1 == nb) mma_commit(&ct.q_empty);
-          } else {
-            ok = wait(&ct.p_full, item & 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t vd = vd0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
+          }
+        } else {
+          ok = wait(&ct.p_full, item & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t vd = vd0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
+          if (elect_one()) {
 #pragma unroll
             for (int ks = 0; ks < kBlk / 16; ++ks) {   // 16 keys (a page) per MMA; 128 numbers are two chunks
 #pragma unroll
@@ -645,15 +650,17 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
             mma_commit(&ct.pv_done);
           }
         }
-        if (!ok) break;
-        ++nseg;
-        mbar_arrive(&ct.seg_empty[ss]);
+        __syncwarp();
       }
-      // every MMA issued above has completed before TMEM is freed
-      mma_commit(&ct.done);
-      const uint64_t t_end = globaltimer();
-      while (!mbar_try_wait(smem_u32(&ct.done), 0) && globaltimer() - t_end < kWaitLimitNs) {
-      }
+      if (!ok) break;
+      ++nseg;
+      if (lane == 0) mbar_arrive(&ct.seg_empty[ss]);
+    }
+    // every MMA issued above has completed before TMEM is freed
+    if (elect_one()) mma_commit(&ct.done);
+    __syncwarp();
+    const uint64_t t_end = globaltimer();
+    while (!mbar_try_wait(smem_u32(&ct.done), 0) && globaltimer() - t_end < kWaitLimitNs) {
     }
     __syncwarp();
   } else if (warp >= 4) {
