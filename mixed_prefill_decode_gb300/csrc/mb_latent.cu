@@ -270,8 +270,7 @@ constexpr int kMaxCtas = 160;       // CTAs of a launch at most; sizes the works
 __host__ __device__ constexpr int64_t part_floats(int64_t rank) { return 64 * rank + 128; }
 constexpr int kBlk = 64;            // keys of a block
 constexpr int kCostUnit = 2;        // a unit's start and end, in blocks
-constexpr int kMinShare = 2;        // the least a CTA takes, in blocks
-constexpr int kAhead = 2;           // blocks beyond the one to be sent that are fetched into L2
+constexpr int kMinShare = 1;        // the least a CTA takes, in blocks
 
 struct AbsParams {
   __nv_bfloat16 *oc;             // [T][H][rank]: sum_j p_j c_j
@@ -461,7 +460,7 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
     if (r + 1 < p.n_reqs) nx = load_req(p.qo_indptr, p.kv_len, p.bt_indptr, r + 1);
     int u = static_cast<int>(div64(x0 - ct.start_base, q.unit));   // the unit that x0 lies in
     int64_t base = ct.start_base + u * q.unit;
-    int kcnt = 0, nseg = 0, quse = 0;   // (quse: lane 0's)
+    int kcnt = 0, nseg = 0, quse = 0;
     bool ok = true, waited = false;
     while (ok && base < x1) {
       auto cut = [&](int64_t x) {   // blocks of the unit that lie before x
@@ -476,8 +475,10 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
         const int i0 = u * p.NT, toks = min(p.NT, q.n - i0);
         const int32_t *table = p.bt + q.b0;
         const int n_pages = (q.kv + kPage - 1) / kPage;
-        // Page ids, one per lane 0 to 3, of the block to be sent and the kAhead
-        // behind it, which are on their way to L2.
+        // Page ids, one per lane 0 to 3, of the block to be sent and the one behind
+        // it, which is on its way to L2 while it waits for a stage.  (96 requests at
+        // 1,024 to 8,192 keys 88 us; 90, 93 and 109 with one, two and four more blocks
+        // under way, 93 with none.)
         auto page_of = [&](int blk) {
           int pg = lane < 4 && blk < j1 && 4 * blk + lane < n_pages ? table[4 * blk + lane] : -1;
           if (lane < 4 && blk < j1 && 4 * blk + lane < n_pages && (pg < 0 || pg >= p.num_pages)) {
@@ -486,36 +487,32 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
           }
           return pg;
         };
-        int pages[kAhead + 1], nxt;
-#pragma unroll
-        for (int k = 0; k <= kAhead; ++k) pages[k] = page_of(j0 + k);
-        nxt = page_of(j0 + kAhead + 1);
-#pragma unroll
-        for (int k = 1; k <= kAhead; ++k)
-          if (pages[k] >= 0) tma_prefetch_5d(&tmK, 0, 0, 0, 0, pages[k]);
+        int cur = page_of(j0), nxt = page_of(j0 + 1);
         int j = j0;
         auto send = [&]() {   // block j
-          const int np = min(4, n_pages - 4 * j), st = kcnt % C::NST, cur = pages[0];
-          if (lane == 0) ok = mbar_wait(&ct.k_empty[st][0], ((kcnt / C::NST) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer);
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) return;
-          if (lane == 0) mbar_arrive_expect_tx(&ct.k_full[st], np * C::PAGE_BYTES);
-          __syncwarp();
-#pragma unroll 1
-          for (int k = 0; k < np; ++k) {
-            // (past the first, a page that is not given back in time is drained below)
-            if (k > 0) ok = __all_sync(0xffffffffu, mbar_wait(&ct.k_empty[st][k], ((kcnt / C::NST) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer));
-            if (!ok) return;
-            if (lane == k)
+          const int np = min(4, n_pages - 4 * j), st = kcnt % C::NST;
+          if (kcnt < C::NST) {   // nothing to wait for
+            if (lane == 0) mbar_arrive_expect_tx(&ct.k_full[st], np * C::PAGE_BYTES);
+            __syncwarp();
+            if (lane < np)
               tma_load_5d(sK + st * C::STAGE + lane * C::PAGE_BYTES, &tmK, &ct.k_full[st], 0, 0, 0, 0, cur);
+          } else {
+            ok = __all_sync(0xffffffffu, mbar_wait(&ct.k_empty[st][0], ((kcnt / C::NST) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer));
+            if (!ok) return;
+            if (lane == 0) mbar_arrive_expect_tx(&ct.k_full[st], np * C::PAGE_BYTES);
+            __syncwarp();
+#pragma unroll 1
+            for (int k = 0; k < np; ++k) {
+              // (past the first, a page that is not given back in time is drained below)
+              if (k > 0) ok = __all_sync(0xffffffffu, mbar_wait(&ct.k_empty[st][k], ((kcnt / C::NST) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer));
+              if (!ok) return;
+              if (lane == k)
+                tma_load_5d(sK + st * C::STAGE + lane * C::PAGE_BYTES, &tmK, &ct.k_full[st], 0, 0, 0, 0, cur);
+            }
           }
-          ++kcnt;
-#pragma unroll
-          for (int k = 0; k < kAhead; ++k) pages[k] = pages[k + 1];
-          pages[kAhead] = nxt;
-          if (nxt >= 0) tma_prefetch_5d(&tmK, 0, 0, 0, 0, nxt);
-          nxt = page_of(j + kAhead + 2);
-          ++j;
+          cur = nxt;
+          if (++kcnt >= C::NST && cur >= 0) tma_prefetch_5d(&tmK, 0, 0, 0, 0, cur);
+          nxt = page_of(++j + 1);
         };
         if (!waited) {   // the first blocks, before the kernel before has ended
           while (ok && j < j1 && j - j0 < C::NST) send();
@@ -523,18 +520,15 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
           pdl_trigger();
           waited = true;
         }
-        // the query tile
+        // the query tile, a copy per lane
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&ct.q_empty, (quse & 1) ^ 1, abort_flag, p.err, kErrWaitProducer));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&ct.q_full, C::NC * p.Hc * p.NT * 128);
+        __syncwarp();
+        if (lane < C::NC)
+          tma_load_3d(sQ + lane * C::Q_CHUNK, lane < C::NC - 1 ? &tmQ : &tmR, &ct.q_full, lane < C::NC - 1 ? lane * 64 : 0, ht * p.Hc, q.t0 + i0);
+        ++quse;
         const int first = owner(0), last_w = owner(q.nkb - 1);
-        if (lane == 0) {
-          ok = mbar_wait(&ct.q_empty, (quse & 1) ^ 1, abort_flag, p.err, kErrWaitProducer);
-          if (ok) {
-            mbar_arrive_expect_tx(&ct.q_full, C::NC * p.Hc * p.NT * 128);
-            for (int ch = 0; ch < C::NC - 1; ++ch)
-              tma_load_3d(sQ + ch * C::Q_CHUNK, &tmQ, &ct.q_full, ch * 64, ht * p.Hc, q.t0 + i0);
-            tma_load_3d(sQ + (C::NC - 1) * C::Q_CHUNK, &tmR, &ct.q_full, 0, ht * p.Hc, q.t0 + i0);
-            ++quse;
-          }
-        }
         // the piece's record for the other roles
         const int ss = nseg % C::NSEG;
         if (lane == 0 && ok) {
