@@ -74,25 +74,37 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const __g
   __shared__ float cs[kRopeHalf], sn[kRopeHalf], red[kAppendThreads / 32];
   pdl_wait();
   pdl_trigger();
-  const int t = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int t = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, part = tid & 3;
+  // Every load goes out at once: nothing of the token's depends on its place
+  // and position but where it goes and its angles.
   const int slot = p.tok_slot[t], pos = p.tok_pos[t];
+  const uint4 *src = reinterpret_cast<const uint4 *>(p.ckv + t * p.ld);
+  const int nv = p.rank / 8;   // at most 64: two warps hold the vector
+  uint4 x = make_uint4(0, 0, 0, 0), g = x, ra = x, rb = x;
+  if (tid < nv) {
+    x = src[tid];
+    g = reinterpret_cast<const uint4 *>(p.gain)[tid];
+  }
+  // rotated rows: the queries' heads, then (index H) the key; four lanes a row
+  auto row_of = [&](int h) {
+    return h < p.H ? reinterpret_cast<const uint4 *>(p.q + (static_cast<int64_t>(t) * p.H + h) * p.q_row + p.hd) : src + nv;
+  };
+  int h = tid >> 2;
+  if (h <= p.H) {
+    const uint4 *s = row_of(h);
+    ra = s[part];
+    rb = s[part + 4];
+  }
   if (slot == -1) return;   // a row behind the batch's last token
   if (slot < 0 || slot >= p.num_pages * static_cast<int64_t>(kPage) || pos < 0 || pos > (1 << 24)) {
     if (tid == 0) atomicExch(p.err, kErrBounds);
     return;
   }
-  const uint4 *src = reinterpret_cast<const uint4 *>(p.ckv + t * p.ld);
   uint4 *dst = reinterpret_cast<uint4 *>(p.pool + static_cast<int64_t>(slot) * (p.rank + kLatentRope));
-  const int nv = p.rank / 8;   // at most 64: two warps hold the vector
-  uint4 x = make_uint4(0, 0, 0, 0), g = x;
   float ss = 0.f;
-  if (tid < nv) {
-    x = src[tid];
-    g = reinterpret_cast<const uint4 *>(p.gain)[tid];
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) ss += bf16lo(w[e]) * bf16lo(w[e]) + bf16hi(w[e]) * bf16hi(w[e]);
-  }
+  for (int e = 0; e < 4; ++e) ss += bf16lo(xw[e]) * bf16lo(xw[e]) + bf16hi(xw[e]) * bf16hi(xw[e]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
   if (lane == 0) red[warp] = ss;
@@ -112,22 +124,23 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const __g
   __syncthreads();
   if (tid < nv) {
     const float inv = rsqrtf((red[0] + red[1]) / static_cast<float>(p.rank) + p.eps);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w}, gw[4] = {g.x, g.y, g.z, g.w};
+    const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
     uint32_t o[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(bf16lo(w[e]) * inv * bf16lo(gw[e]), bf16hi(w[e]) * inv * bf16hi(gw[e]));
+    for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(bf16lo(xw[e]) * inv * bf16lo(gw[e]), bf16hi(xw[e]) * inv * bf16hi(gw[e]));
     dst[tid] = make_uint4(o[0], o[1], o[2], o[3]);
   }
-  // rotated rows: the queries' heads, then (index H) the key; four lanes a row
-  const int part = tid & 3;
-  for (int h = tid >> 2; h <= p.H; h += kAppendThreads / 4) {
-    const uint4 *s = h < p.H ? reinterpret_cast<const uint4 *>(p.q + (static_cast<int64_t>(t) * p.H + h) * p.q_row + p.hd)
-                             : src + nv;
+  while (h <= p.H) {
     uint4 *d = h < p.H ? reinterpret_cast<uint4 *>(p.q_rope + (static_cast<int64_t>(t) * p.H + h) * kLatentRope) : dst + nv;
-    uint4 a = s[part], b = s[part + 4];
-    rotate8(a, b, cs + 8 * part, sn + 8 * part);
-    d[part] = a;
-    d[part + 4] = b;
+    rotate8(ra, rb, cs + 8 * part, sn + 8 * part);
+    d[part] = ra;
+    d[part + 4] = rb;
+    h += kAppendThreads / 4;
+    if (h <= p.H) {
+      const uint4 *s = row_of(h);
+      ra = s[part];
+      rb = s[part + 4];
+    }
   }
 }
 

@@ -12,7 +12,7 @@
 //
 // What bounds it: 4 bytes a page read and written and 12 a token; at 64
 // requests that is tens of KB, and the launch, the chain of loads (a
-// request's slot, then its row's page count) and the scans are the time.
+// request's slot, its row's page count, the page) and the scans are the time.
 // Every CTA scans all requests itself, so one launch does it: a second one
 // would cost what the whole call does.  What changes in place (page counts,
 // the ring's head) is written by the last CTA to have read it.
@@ -33,7 +33,7 @@ using namespace dev;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kElemsPerCta = 2048;   // pages and tokens that a CTA writes (four a thread)
+constexpr int kElemsPerCta = kThreads;   // pages and tokens that a CTA writes, one a thread while there are SMs
 // Sums stop here (2^30): no sum that is used is as large, and sums that stop
 // are still sums of non-negative numbers, whatever the order.
 constexpr uint32_t kSat = 1u << 30;
@@ -52,8 +52,7 @@ __device__ __forceinline__ uint2 block_scan2(uint2 v, uint2 *sums, uint2 *total)
       inc.y = sat_add(inc.y, y);
     }
   }
-  __syncthreads();   // sums may still be read from the scan before
-  if (lane == 31) sums[warp] = inc;
+  if (lane == 31) sums[warp] = inc;   // (each scan of a kernel has its own)
   __syncthreads();
   uint2 pre = make_uint2(0, 0), all = make_uint2(0, 0);
 #pragma unroll
@@ -79,28 +78,31 @@ __device__ __forceinline__ int owner(const int32_t *first, int n, int e) {
   return lo;
 }
 
-// Marks the slots that occur; `twice` those that occur again.
-__device__ __forceinline__ void mark_slots(const TablesArgs &a, uint32_t *once, uint32_t *twice) {
-  const int words = (a.max_slots + 31) / 32;
-  for (int i = threadIdx.x; i < words; i += kThreads) once[i] = twice[i] = 0;
-  __syncthreads();
-  for (int r = threadIdx.x; r < a.n; r += kThreads) {
-    const int s = a.slots[r];
-    if (s < 0 || s >= a.max_slots) continue;
+// Marks the slots that occur in row[0 .. n) (each thread its own range); `twice`
+// those that occur again.  The bits were cleared before the last barrier.
+__device__ __forceinline__ void mark_slots(const int32_t *row, int lo, int hi, int max_slots, uint32_t *once, uint32_t *twice) {
+  for (int r = lo; r < hi; ++r) {
+    const int s = row[r];
+    if (s < 0 || s >= max_slots) continue;
     const uint32_t bit = 1u << (s & 31);
     if (atomicOr(&once[s >> 5], bit) & bit) atomicOr(&twice[s >> 5], bit);
   }
   __syncthreads();
 }
 
-// True in the CTA that comes here last (then the counter is 0 again).
-__device__ __forceinline__ bool last_cta(int32_t *ctr) {
+// Counts this CTA among those that have read what the last one is to change
+// (thread 0's: how many came before).  Called behind a barrier; the answer is
+// asked for at the kernel's end only, so that nothing waits for it.
+__device__ __forceinline__ int arrive(int32_t *ctr) {
+  if (gridDim.x == 1 || threadIdx.x != 0) return 0;
+  __threadfence();
+  return atomicAdd(ctr, 1);
+}
+__device__ __forceinline__ bool last_cta(int32_t *ctr, int before) {
   __shared__ int last;
-  __syncthreads();   // every thread has read what the last CTA is to change
   if (threadIdx.x == 0) {
-    __threadfence();
-    last = atomicAdd(ctr, 1) == static_cast<int>(gridDim.x) - 1;
-    if (last) *ctr = 0;
+    last = before == static_cast<int>(gridDim.x) - 1;
+    if (last && gridDim.x > 1) *ctr = 0;
   }
   __syncthreads();
   return last != 0;
@@ -108,7 +110,8 @@ __device__ __forceinline__ bool last_cta(int32_t *ctr) {
 
 __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant__ TablesArgs a) {
   extern __shared__ int32_t sm[];
-  __shared__ uint2 sums[kWarps];
+  __shared__ uint2 sums[2][kWarps];
+  __shared__ uint32_t mosts[kWarps];
   int32_t *qo = sm, *bti = qo + a.n + 1, *ring0 = bti + a.n + 1, *have = ring0 + a.n, *first = have + a.n,
           *row = first + a.n;
   uint32_t *once = reinterpret_cast<uint32_t *>(row + a.n), *twice = once + (a.max_slots + 31) / 32;
@@ -118,14 +121,23 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
   const int lo = min(n, static_cast<int>(threadIdx.x) * per), hi = min(n, lo + per);
   const int head = a.state[0], count = a.state[1];
   const bool ring_ok = head >= 0 && head < a.num_pages && count >= 0 && count <= a.num_pages;
-  mark_slots(a, once, twice);
   bool bad = !ring_ok;
-  // ---- the requests' words, and what they ask for
+  // ---- the requests' words: all loads before anything waits for one
+  for (int r = lo; r < hi; ++r) {
+    const int s = a.slots[r];
+    first[r] = a.cached[r];
+    qo[r] = a.new_tokens[r];
+    row[r] = s;
+    have[r] = s >= 0 && s < a.max_slots ? a.owned[s] : -1;
+  }
+  for (int i = threadIdx.x; i < (a.max_slots + 31) / 32; i += kThreads) once[i] = twice[i] = 0;
+  __syncthreads();
+  mark_slots(row, lo, hi, a.max_slots, once, twice);
+  // ---- what they ask for
   uint2 sum = make_uint2(0, 0), total;
   for (int r = lo; r < hi; ++r) {
-    const int s = a.slots[r], c = a.cached[r], m = a.new_tokens[r];
+    const int s = row[r], c = first[r], m = qo[r], o = have[r];
     bool ok = ring_ok && s >= 0 && s < a.max_slots && !((twice[s >> 5] >> (s & 31)) & 1u);
-    const int o = ok ? a.owned[s] : 0;
     // (compared before they are added: the words may be anything)
     ok = ok && c >= 0 && m >= 0 && o >= 0 && o <= a.max_pages && c <= o * static_cast<int64_t>(kPage) &&
          static_cast<int64_t>(c) + m <= a.max_pages * static_cast<int64_t>(kPage);
@@ -137,7 +149,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
     const int need = ok ? max(0, (c + m + kPage - 1) / kPage - o) : 0;
     sum.x = sat_add(sum.x, need);
   }
-  uint2 at = block_scan2(sum, sums, &total);
+  uint2 at = block_scan2(sum, sums[0], &total);
   // ---- who is granted, and their tokens and pages
   sum = make_uint2(0, 0);
   uint32_t taken = 0;   // pages taken up to this thread's last granted request
@@ -152,7 +164,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
     sum.x = sat_add(sum.x, granted ? m : 0);
     sum.y = sat_add(sum.y, (c + (granted ? m : 0) + kPage - 1) / kPage);
   }
-  at = block_scan2(sum, sums, &total);
+  at = block_scan2(sum, sums[1], &total);
   const bool fits = total.x <= static_cast<uint32_t>(a.T) && total.y <= static_cast<uint32_t>(a.bt_cap);
   bad |= !fits;
   if (bad && blockIdx.x == 0) atomicExch(a.err, kErrBounds);
@@ -178,28 +190,9 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
       a.bt_indptr[n] = pages;
     }
   }
-  const bool last = last_cta(a.state + 2);   // (also: qo and bti are written)
-  if (last && !none) {
-    // the rows' page counts, and the ring's head: needs of granted requests
-    uint32_t most = taken;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
-    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5].x = most;
-    for (int r = lo; r < hi; ++r) {
-      const int listed = bti[r + 1] - bti[r];
-      if (row[r] >= 0 && listed > have[r]) a.owned[row[r]] = listed;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      most = 0;
-      for (int w = 0; w < kWarps; ++w) most = max(most, sums[w].x);
-      if (most > 0) {
-        a.state[0] = static_cast<int32_t>((static_cast<int64_t>(head) + most) % a.num_pages);
-        a.state[1] = count - static_cast<int32_t>(most);
-      }
-    }
-  }
-  // ---- pages and tokens, four at a time per thread
+  __syncthreads();   // qo and bti are written, and the words that the last CTA changes read
+  const int before = arrive(a.state + 2);
+  // ---- pages and tokens
   // page j of request r: in its row, or the ring's (j - have) after its first
   auto page_of = [&](int r, int j) {
     if (j < have[r]) return a.tables[static_cast<int64_t>(row[r]) * a.max_pages + j];
@@ -229,6 +222,24 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
     a.tok_pos[t] = pos;
     a.tok_slot[t] = slot;
   }
+  // ---- the rows' page counts, and the ring's head: needs of granted requests
+  if (!last_cta(a.state + 2, before) || none) return;
+  uint32_t most = taken;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
+  if ((threadIdx.x & 31) == 0) mosts[threadIdx.x >> 5] = most;
+  for (int r = lo; r < hi; ++r) {
+    const int listed = bti[r + 1] - bti[r];
+    if (row[r] >= 0 && listed > have[r]) a.owned[row[r]] = listed;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 0; w < kWarps; ++w) most = max(most, mosts[w]);
+    if (most > 0) {
+      a.state[0] = static_cast<int32_t>((static_cast<int64_t>(head) + most) % a.num_pages);
+      a.state[1] = count - static_cast<int32_t>(most);
+    }
+  }
 }
 
 // The pages of the requests to the ring's end, in the requests' order and
@@ -245,13 +256,19 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const __grid_constant
   const int lo = min(n, static_cast<int>(threadIdx.x) * per), hi = min(n, lo + per);
   const int head = a.state[0], count = a.state[1];
   const bool ring_ok = head >= 0 && head < a.num_pages && count >= 0 && count <= a.num_pages;
-  mark_slots(a, once, twice);
   bool bad = !ring_ok;
-  uint2 sum = make_uint2(0, 0), total;
   for (int r = lo; r < hi; ++r) {
     const int s = a.slots[r];
+    row[r] = s;
+    at0[r] = s >= 0 && s < a.max_slots ? a.owned[s] : -1;
+  }
+  for (int i = threadIdx.x; i < (a.max_slots + 31) / 32; i += kThreads) once[i] = twice[i] = 0;
+  __syncthreads();
+  mark_slots(row, lo, hi, a.max_slots, once, twice);
+  uint2 sum = make_uint2(0, 0), total;
+  for (int r = lo; r < hi; ++r) {
+    const int s = row[r], o = at0[r];
     bool ok = ring_ok && s >= 0 && s < a.max_slots && !((twice[s >> 5] >> (s & 31)) & 1u);
-    const int o = ok ? a.owned[s] : 0;
     ok = ok && o >= 0 && o <= a.max_pages;
     bad |= !ok;
     row[r] = ok ? s : -1;
@@ -268,21 +285,20 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const __grid_constant
     at.x = sat_add(at.x, o);
   }
   if (threadIdx.x == 0) at0[n] = static_cast<int32_t>(total.x);
-  const bool last = last_cta(a.state + 2);
-  if (!fits) return;
-  if (last) {
-    for (int r = lo; r < hi; ++r)
-      if (row[r] >= 0) a.owned[row[r]] = 0;
-    if (threadIdx.x == 0) a.state[1] = count + static_cast<int32_t>(total.x);
-  }
+  __syncthreads();   // at0 is written, and the words that the last CTA changes read
+  const int before = arrive(a.state + 2);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
 #pragma unroll 4
-  for (int64_t e = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; e < total.x; e += step) {
+  for (int64_t e = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; fits && e < total.x; e += step) {
     const int r = owner(at0, n, static_cast<int>(e));
     int64_t i = static_cast<int64_t>(head) + count + e;
     if (i >= a.num_pages) i -= a.num_pages;
     a.ring[i] = a.tables[static_cast<int64_t>(row[r]) * a.max_pages + (e - at0[r])];
   }
+  if (!last_cta(a.state + 2, before) || !fits) return;
+  for (int r = lo; r < hi; ++r)
+    if (row[r] >= 0) a.owned[row[r]] = 0;
+  if (threadIdx.x == 0) a.state[1] = count + static_cast<int32_t>(total.x);
 }
 
 int tables_grid(int64_t elems) {
