@@ -7,8 +7,8 @@
 // granted its tokens if need_r = 0 or the needs of the requests up to and
 // including it fit the free pages; otherwise it has none this time.  That
 // rule makes the pages taken a prefix of the ring, and the place of each
-// request's first page a prefix sum of the needs, so everything is two scans
-// over the requests and one write per page and token.
+// request's first page a prefix sum of the needs, so everything is a scan over
+// the requests (two where the pages run out) and one write per page and token.
 //
 // What bounds it: 4 bytes a page read and written and 12 a token; at 64
 // requests that is tens of KB, and the launch, the chain of loads (a
@@ -34,37 +34,45 @@ using namespace dev;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kElemsPerCta = kThreads;   // pages and tokens that a CTA writes, one a thread while there are SMs
+constexpr int kBatch = 2;                // of a thread, loaded together
 // Sums stop here (2^30): no sum that is used is as large, and sums that stop
 // are still sums of non-negative numbers, whatever the order.
 constexpr uint32_t kSat = 1u << 30;
 
 __device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) { return min(a + b, kSat); }
 
-// Exclusive prefix sums of two numbers per thread, and their totals.
-__device__ __forceinline__ uint2 block_scan2(uint2 v, uint2 *sums, uint2 *total) {
+// Exclusive prefix sums of N numbers per thread, and their totals.  (Each scan of
+// a kernel has shared sums of its own, so one barrier does.)
+template <int N>
+__device__ __forceinline__ void block_scan(uint32_t (&v)[N], uint32_t (*sums)[N], uint32_t (&total)[N]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint2 inc = v;
+  uint32_t inc[N];
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const uint32_t x = __shfl_up_sync(0xffffffffu, inc.x, off), y = __shfl_up_sync(0xffffffffu, inc.y, off);
-    if (lane >= off) {
-      inc.x = sat_add(inc.x, x);
-      inc.y = sat_add(inc.y, y);
+  for (int k = 0; k < N; ++k) inc[k] = v[k];
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, inc[k], off);
+      if (lane >= off) inc[k] = sat_add(inc[k], x);
     }
-  }
-  if (lane == 31) sums[warp] = inc;   // (each scan of a kernel has its own)
-  __syncthreads();
-  uint2 pre = make_uint2(0, 0), all = make_uint2(0, 0);
+  if (lane == 31)
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const uint2 s = sums[w];
-    if (w < warp) pre = make_uint2(sat_add(pre.x, s.x), sat_add(pre.y, s.y));
-    all = make_uint2(sat_add(all.x, s.x), sat_add(all.y, s.y));
+    for (int k = 0; k < N; ++k) sums[warp][k] = inc[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    uint32_t w = lane < kWarps ? sums[lane][k] : 0;
+#pragma unroll
+    for (int off = 1; off < kWarps; off <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, w, off);
+      if (lane >= off) w = sat_add(w, x);
+    }
+    total[k] = __shfl_sync(0xffffffffu, w, kWarps - 1);
+    const uint32_t before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+    const uint32_t mine = __shfl_up_sync(0xffffffffu, inc[k], 1);   // what this thread's lanes before it hold
+    v[k] = sat_add(warp > 0 ? before : 0, lane > 0 ? mine : 0);
   }
-  *total = all;
-  // (what this thread's lanes before it hold)
-  const uint32_t ex = __shfl_up_sync(0xffffffffu, inc.x, 1), ey = __shfl_up_sync(0xffffffffu, inc.y, 1);
-  return lane == 0 ? pre : make_uint2(sat_add(pre.x, ex), sat_add(pre.y, ey));
 }
 
 // The last index of first[0 .. n] (ascending, first[0] = 0) that is <= e.
@@ -94,9 +102,7 @@ __device__ __forceinline__ void mark_slots(const int32_t *row, int lo, int hi, i
 // (thread 0's: how many came before).  Called behind a barrier; the answer is
 // asked for at the kernel's end only, so that nothing waits for it.
 __device__ __forceinline__ int arrive(int32_t *ctr) {
-  if (gridDim.x == 1 || threadIdx.x != 0) return 0;
-  __threadfence();
-  return atomicAdd(ctr, 1);
+  return gridDim.x == 1 || threadIdx.x != 0 ? 0 : atomicAdd(ctr, 1);
 }
 __device__ __forceinline__ bool last_cta(int32_t *ctr, int before) {
   __shared__ int last;
@@ -110,8 +116,7 @@ __device__ __forceinline__ bool last_cta(int32_t *ctr, int before) {
 
 __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant__ TablesArgs a) {
   extern __shared__ int32_t sm[];
-  __shared__ uint2 sums[2][kWarps];
-  __shared__ uint32_t mosts[kWarps];
+  __shared__ uint32_t sums[kWarps][3], sums2[kWarps][2], mosts[kWarps];
   int32_t *qo = sm, *bti = qo + a.n + 1, *ring0 = bti + a.n + 1, *have = ring0 + a.n, *first = have + a.n,
           *row = first + a.n;
   uint32_t *once = reinterpret_cast<uint32_t *>(row + a.n), *twice = once + (a.max_slots + 31) / 32;
@@ -133,55 +138,65 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
   for (int i = threadIdx.x; i < (a.max_slots + 31) / 32; i += kThreads) once[i] = twice[i] = 0;
   __syncthreads();
   mark_slots(row, lo, hi, a.max_slots, once, twice);
-  // ---- what they ask for
-  uint2 sum = make_uint2(0, 0), total;
+  // ---- what they ask for: pages, tokens, and the pages listed if all is granted
+  uint32_t at[3] = {0, 0, 0}, total[3];
   for (int r = lo; r < hi; ++r) {
     const int s = row[r], c = first[r], m = qo[r], o = have[r];
     bool ok = ring_ok && s >= 0 && s < a.max_slots && !((twice[s >> 5] >> (s & 31)) & 1u);
     // (compared before they are added: the words may be anything)
-    ok = ok && c >= 0 && m >= 0 && o >= 0 && o <= a.max_pages && c <= o * static_cast<int64_t>(kPage) &&
-         static_cast<int64_t>(c) + m <= a.max_pages * static_cast<int64_t>(kPage);
+    ok = ok && c >= 0 && m >= 0 && o >= 0 && o <= a.max_pages && c <= o * kPage && m <= a.max_pages * kPage - c;
     bad |= !ok;
     row[r] = ok ? s : -1;
     first[r] = ok ? c : 0;
     have[r] = ok ? o : 0;
     qo[r] = ok ? m : 0;
-    const int need = ok ? max(0, (c + m + kPage - 1) / kPage - o) : 0;
-    sum.x = sat_add(sum.x, need);
+    const int listed = ok ? (c + m + kPage - 1) / kPage : 0;
+    at[0] = sat_add(at[0], ok ? max(0, listed - o) : 0);
+    at[1] = sat_add(at[1], ok ? m : 0);
+    at[2] = sat_add(at[2], listed);
   }
-  uint2 at = block_scan2(sum, sums[0], &total);
-  // ---- who is granted, and their tokens and pages
-  sum = make_uint2(0, 0);
-  uint32_t taken = 0;   // pages taken up to this thread's last granted request
-  for (int r = lo; r < hi; ++r) {
-    const int c = first[r], m = qo[r], o = have[r];
-    const int need = max(0, (c + m + kPage - 1) / kPage - o);
-    ring0[r] = static_cast<int32_t>(at.x);
-    at.x = sat_add(at.x, need);
-    const bool granted = need == 0 || at.x <= static_cast<uint32_t>(count);
-    if (!granted) qo[r] = 0;
-    if (granted && need) taken = at.x;
-    sum.x = sat_add(sum.x, granted ? m : 0);
-    sum.y = sat_add(sum.y, (c + (granted ? m : 0) + kPage - 1) / kPage);
+  block_scan<3>(at, sums, total);
+  uint32_t taken = total[0];   // pages taken (where they run out: up to this thread's last granted request)
+  if (taken > static_cast<uint32_t>(ring_ok ? count : 0)) {
+    // the free pages run out: who is granted, and their tokens and pages
+    uint32_t some[2] = {0, 0}, sub[2];
+    taken = 0;
+    uint32_t asked = at[0];
+    for (int r = lo; r < hi; ++r) {
+      const int c = first[r], m = qo[r], need = max(0, (c + m + kPage - 1) / kPage - have[r]);
+      asked = sat_add(asked, need);
+      const bool granted = need == 0 || asked <= static_cast<uint32_t>(count);
+      if (!granted) qo[r] = -1 - m;   // (its need still counts for those behind it)
+      else if (need) taken = asked;
+      some[0] = sat_add(some[0], granted ? m : 0);
+      some[1] = sat_add(some[1], (c + (granted ? m : 0) + kPage - 1) / kPage);
+    }
+    block_scan<2>(some, sums2, sub);
+    at[1] = some[0];
+    at[2] = some[1];
+    total[1] = sub[0];
+    total[2] = sub[1];
   }
-  at = block_scan2(sum, sums[1], &total);
-  const bool fits = total.x <= static_cast<uint32_t>(a.T) && total.y <= static_cast<uint32_t>(a.bt_cap);
+  const bool fits = total[1] <= static_cast<uint32_t>(a.T) && total[2] <= static_cast<uint32_t>(a.bt_cap);
   bad |= !fits;
   if (bad && blockIdx.x == 0) atomicExch(a.err, kErrBounds);
   const bool none = !fits;   // the caller's arrays are too short: nothing is granted, nothing changes
   for (int r = lo; r < hi; ++r) {
-    const int c = none ? 0 : first[r], m = none ? 0 : qo[r];
-    const int pages = (c + m + kPage - 1) / kPage;
-    qo[r] = none ? 0 : static_cast<int32_t>(at.x);
-    bti[r] = none ? 0 : static_cast<int32_t>(at.y);
-    at = make_uint2(sat_add(at.x, m), sat_add(at.y, pages));
+    const int asked = qo[r] < 0 ? -1 - qo[r] : qo[r];
+    const int c = none ? 0 : first[r], m = none || qo[r] < 0 ? 0 : qo[r];
+    ring0[r] = static_cast<int32_t>(at[0]);
+    at[0] = sat_add(at[0], max(0, (first[r] + asked + kPage - 1) / kPage - have[r]));
+    qo[r] = none ? 0 : static_cast<int32_t>(at[1]);
+    bti[r] = none ? 0 : static_cast<int32_t>(at[2]);
+    at[1] = sat_add(at[1], m);
+    at[2] = sat_add(at[2], (c + m + kPage - 1) / kPage);
     if (blockIdx.x == 0) {
       a.qo_indptr[r] = qo[r];
       a.bt_indptr[r] = bti[r];
       a.kv_len[r] = c + m;
     }
   }
-  const int tokens = none ? 0 : static_cast<int>(total.x), pages = none ? 0 : static_cast<int>(total.y);
+  const int tokens = none ? 0 : static_cast<int>(total[1]), pages = none ? 0 : static_cast<int>(total[2]);
   if (threadIdx.x == 0) {
     qo[n] = tokens;
     bti[n] = pages;
@@ -200,27 +215,41 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
     if (i >= a.num_pages) i -= a.num_pages;
     return a.ring[i];
   };
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads, at0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-#pragma unroll 4
-  for (int64_t e = at0; e < pages; e += step) {
-    const int r = owner(bti, n, static_cast<int>(e)), j = static_cast<int>(e) - bti[r];
-    const int page = page_of(r, j);
-    a.bt[e] = page;
-    if (j >= have[r]) a.tables[static_cast<int64_t>(row[r]) * a.max_pages + j] = page;
-  }
-#pragma unroll 4
-  for (int64_t t = at0; t < a.T; t += step) {
-    int r = -1, pos = -1, slot = -1;
-    if (t < tokens) {
-      r = owner(qo, n, static_cast<int>(t));
-      pos = first[r] + static_cast<int>(t) - qo[r];
-      const int page = page_of(r, pos / kPage);
-      if (page < 0 || page >= a.num_pages) atomicExch(a.err, kErrBounds);
-      else slot = page * kPage + pos % kPage;
+  // Pages, then tokens, kBatch at a time: their loads go out together.
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads, all = static_cast<int64_t>(pages) + a.T;
+  for (int64_t e0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; e0 < all; e0 += kBatch * step) {
+    int req[kBatch], place[kBatch], page[kBatch];   // the request, the page's place in its row or the token's position
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int64_t e = e0 + k * step, t = e - pages;
+      req[k] = place[k] = page[k] = -1;
+      if (e < pages) {
+        req[k] = owner(bti, n, static_cast<int>(e));
+        place[k] = static_cast<int>(e) - bti[req[k]];
+        page[k] = page_of(req[k], place[k]);
+      } else if (t < tokens) {
+        req[k] = owner(qo, n, static_cast<int>(t));
+        place[k] = first[req[k]] + static_cast<int>(t) - qo[req[k]];
+        page[k] = page_of(req[k], place[k] / kPage);
+      }
     }
-    a.tok_req[t] = r;
-    a.tok_pos[t] = pos;
-    a.tok_slot[t] = slot;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int64_t e = e0 + k * step, t = e - pages;
+      if (e < pages) {
+        a.bt[e] = page[k];
+        if (place[k] >= have[req[k]]) a.tables[static_cast<int64_t>(row[req[k]]) * a.max_pages + place[k]] = page[k];
+      } else if (e < all) {
+        int slot = -1;
+        if (t < tokens) {
+          if (page[k] < 0 || page[k] >= a.num_pages) atomicExch(a.err, kErrBounds);
+          else slot = page[k] * kPage + place[k] % kPage;
+        }
+        a.tok_req[t] = req[k];
+        a.tok_pos[t] = place[k];
+        a.tok_slot[t] = slot;
+      }
+    }
   }
   // ---- the rows' page counts, and the ring's head: needs of granted requests
   if (!last_cta(a.state + 2, before) || none) return;
@@ -247,7 +276,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
 // has room for.
 __global__ void __launch_bounds__(kThreads) release_kernel(const __grid_constant__ TablesArgs a) {
   extern __shared__ int32_t sm[];
-  __shared__ uint2 sums[kWarps];
+  __shared__ uint32_t sums[kWarps][1];
   int32_t *at0 = sm, *row = at0 + a.n + 1;
   uint32_t *once = reinterpret_cast<uint32_t *>(row + a.n), *twice = once + (a.max_slots + 31) / 32;
   pdl_wait();
@@ -265,7 +294,7 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const __grid_constant
   for (int i = threadIdx.x; i < (a.max_slots + 31) / 32; i += kThreads) once[i] = twice[i] = 0;
   __syncthreads();
   mark_slots(row, lo, hi, a.max_slots, once, twice);
-  uint2 sum = make_uint2(0, 0), total;
+  uint32_t at[1] = {0}, total[1];
   for (int r = lo; r < hi; ++r) {
     const int s = row[r], o = at0[r];
     bool ok = ring_ok && s >= 0 && s < a.max_slots && !((twice[s >> 5] >> (s & 31)) & 1u);
@@ -273,23 +302,23 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const __grid_constant
     bad |= !ok;
     row[r] = ok ? s : -1;
     at0[r] = ok ? o : 0;
-    sum.x = sat_add(sum.x, ok ? o : 0);
+    at[0] = sat_add(at[0], ok ? o : 0);
   }
-  uint2 at = block_scan2(sum, sums, &total);
-  const bool fits = ring_ok && total.x <= static_cast<uint32_t>(a.num_pages - count);
+  block_scan<1>(at, sums, total);
+  const bool fits = ring_ok && total[0] <= static_cast<uint32_t>(a.num_pages - count);
   bad |= !fits;
   if (bad && blockIdx.x == 0) atomicExch(a.err, kErrBounds);
   for (int r = lo; r < hi; ++r) {
     const int o = at0[r];
-    at0[r] = static_cast<int32_t>(at.x);
-    at.x = sat_add(at.x, o);
+    at0[r] = static_cast<int32_t>(at[0]);
+    at[0] = sat_add(at[0], o);
   }
-  if (threadIdx.x == 0) at0[n] = static_cast<int32_t>(total.x);
+  if (threadIdx.x == 0) at0[n] = static_cast<int32_t>(total[0]);
   __syncthreads();   // at0 is written, and the words that the last CTA changes read
   const int before = arrive(a.state + 2);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
 #pragma unroll 4
-  for (int64_t e = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; fits && e < total.x; e += step) {
+  for (int64_t e = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; fits && e < total[0]; e += step) {
     const int r = owner(at0, n, static_cast<int>(e));
     int64_t i = static_cast<int64_t>(head) + count + e;
     if (i >= a.num_pages) i -= a.num_pages;
@@ -298,7 +327,7 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const __grid_constant
   if (!last_cta(a.state + 2, before) || !fits) return;
   for (int r = lo; r < hi; ++r)
     if (row[r] >= 0) a.owned[row[r]] = 0;
-  if (threadIdx.x == 0) a.state[1] = count + static_cast<int32_t>(total.x);
+  if (threadIdx.x == 0) a.state[1] = count + static_cast<int32_t>(total[0]);
 }
 
 int tables_grid(int64_t elems) {
