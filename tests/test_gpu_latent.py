@@ -170,36 +170,46 @@ class Batch:
         return f64(self.pool[pages].reshape(-1, self.rank + 64)[:k])
 
     def check(self, got, form, only=None):
-        err = ref = 0.0
-        most = 0.0
-        touched = np.zeros(self.T, bool)
+        """Returns the largest share of the bound on all elements that was used."""
+        parts, touched = [], np.zeros(self.T, bool)
         for r, (c, n) in enumerate(self.reqs):
             if n == 0 or (only is not None and r not in only):
                 continue
             a = int(self.qo[r])
             touched[a:a + n] = True
-            q, qr, w, rows = f64(self.q[a:a + n])[:, :, :self.hd], f64(self.q_rope[a:a + n]), f64(self.w), self.rows(r)
-            o, p, z = OL.attention_request(q, qr, w, rows, self.scale)
-            lat = np.abs(rows[:, :self.rank])
-            for h in range(self.H):
-                wk, wv = w[h, :self.hd], w[h, self.hd:]
-                if form == "absorbed":
-                    E = U * self.scale * np.max(np.abs(q[:, h] @ wk) @ lat.T, axis=1)
-                else:
-                    E = U * self.scale * np.max(np.abs(q[:, h]) @ np.abs(rows[:, :self.rank] @ wk.T).T, axis=1)
-                E = E * 1.01 + 2.0 ** -18
-                A = (p[h] @ lat) @ np.abs(wv).T
-                tol = 1.01 * ((np.exp(2 * E) * (1 + U) ** 2 - 1)[:, None] * A + U * np.abs(o[:, h]))
-                d = np.abs(got[a:a + n, h] - o[:, h])
-                assert np.all(d <= tol), (r, h, float(np.max(d / tol)))
-                err += float(np.sum(d ** 2))
-                ref += float(np.sum(o[:, h] ** 2))
-                seen = np.isfinite(z[h])
-                most = max(most, max(float(np.std(z[h, i][seen[i]])) for i in range(n)))
+            parts.append(near_exact(got[a:a + n], f64(self.q[a:a + n])[:, :, :self.hd], f64(self.q_rope[a:a + n]),
+                                    f64(self.w), self.rows(r), self.scale, form))
         assert np.all(np.isnan(got[~touched])), "a row outside the requests was written"
-        share = np.sqrt(err / ref) / (U / np.sqrt(3.0) * np.sqrt(most ** 2 + 3))
-        assert share <= 2.0, share
-        return share
+        return all_elements(parts)
+
+
+def near_exact(got, q, q_rope, w, rows, scale, form):
+    """Every element of a request's rows within its bound; returns the squares
+    of the errors and of the exact values, and the logits' largest deviation."""
+    n, H, hd = q.shape
+    rank = w.shape[2]
+    o, p, z = OL.attention_request(q, q_rope, w, rows, scale)
+    lat, most = np.abs(rows[:, :rank]), 0.0
+    for h in range(H):
+        wk, wv = w[h, :hd], w[h, hd:]
+        if form == "absorbed":
+            E = U * scale * np.max(np.abs(q[:, h] @ wk) @ lat.T, axis=1)
+        else:
+            E = U * scale * np.max(np.abs(q[:, h]) @ np.abs(rows[:, :rank] @ wk.T).T, axis=1)
+        E = E * 1.01 + 2.0 ** -18
+        A = (p[h] @ lat) @ np.abs(wv).T
+        tol = 1.01 * ((np.exp(2 * E) * (1 + U) ** 2 - 1)[:, None] * A + U * np.abs(o[:, h]))
+        d = np.abs(got[:, h] - o[:, h])
+        assert np.all(d <= tol), (h, float(np.max(d / tol)))
+        most = max(most, max(float(np.std(z[h, i][np.isfinite(z[h, i])])) for i in range(n)))
+    return float(np.sum((got - o) ** 2)), float(np.sum(o ** 2)), most
+
+
+def all_elements(parts):
+    err, ref = sum(x[0] for x in parts), sum(x[1] for x in parts)
+    share = np.sqrt(err / ref) / (U / np.sqrt(3.0) * np.sqrt(max(x[2] for x in parts) ** 2 + 3))
+    assert share <= 2.0, share
+    return share
 
 
 SHAPES = [(1, 64, 256), (5, 64, 512), (8, 128, 512), (20, 128, 256), (32, 128, 512), (40, 128, 512), (64, 64, 256),
