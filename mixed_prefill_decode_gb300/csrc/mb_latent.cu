@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
   // Of what earlier kernels of the stream write, only the queries' products come
   // from this call's first kernel; this one is launched once that one has seen
   // all others finished, so the descriptor and the cache are there.  The producer
-  // waits before it loads queries, after its first blocks of keys.
+  // waits before it loads queries.
 
   // ---- this CTA's part of the line: [x0, x1) of `total`
   const int per = (p.n_reqs + C::THREADS - 1) / C::THREADS;
@@ -527,8 +527,10 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
           if (++kcnt >= C::NST && cur >= 0) tma_prefetch_5d(&tmK, 0, 0, 0, 0, cur);
           nxt = page_of(++j + 1);
         };
-        if (!waited) {   // the first blocks, before the kernel before has ended
-          while (ok && j < j1 && j - j0 < C::NST) send();
+        // (the kernel before has nearly always ended by now: its CTAs leave no room
+        // for this one's.  The queries go first: behind two blocks of keys they came
+        // 2 us later, as all CTAs' first blocks are more than HBM brings in that time.)
+        if (!waited) {
           pdl_wait();
           pdl_trigger();
           waited = true;
