@@ -193,7 +193,8 @@ mb_status mb_batch_validate(const mb_batch *batch, int32_t num_pages, int32_t ma
  * the last call (then clears it).  MB_EDEVICE if one was set.  layer: that
  * layer's steps; NULL: the standalone calls on the current device (mb_gemm,
  * mb_sample_greedy, mb_embed, mb_tree_attention, mb_verify_tree, mb_kv_compact,
- * mb_batch_tables, mb_tables_release, the mb_latent calls and mb_gemm_noalloc).  With NULL it allocates nothing, so callers of
+ * mb_batch_tables, mb_tables_release, the mb_latent calls and
+ * mb_gemm_noalloc).  With NULL it allocates nothing, so callers of
  * mb_gemm_noalloc can use it too. */
 mb_status mb_device_status(mb_layer *layer, void *stream);
 
@@ -504,9 +505,9 @@ mb_status mb_kv_copy_pages(void *const *pools, int32_t n_pools, int32_t num_page
  * [0, max_slots) or given twice, a negative length, cached beyond its pages,
  * more than max_pages pages) records MB_EDEVICE and counts as a request with no
  * tokens, keys or pages.  If the granted tokens exceed T, or the pages bt_cap,
- * the batch is empty (tok_* all -1), nothing changes hands and MB_EDEVICE is recorded.  A page
- * id in the ring or a row outside [0, num_pages) records MB_EDEVICE and gives
- * its tokens tok_slot -1.  num_reqs at most 8192, max_slots 65536, max_pages
+ * the batch is empty (tok_* all -1), nothing changes hands and MB_EDEVICE is
+ * recorded.  A page id in the ring or a row outside [0, num_pages) records
+ * MB_EDEVICE and gives its tokens tok_slot -1.  num_reqs at most 8192, max_slots 65536, max_pages
  * 2^20, num_pages below 2^27, T and bt_cap below 2^30.  All arrays device int32.
  * Errors: MB_EINVAL, MB_EUNSUPPORTED, MB_ECUDA. */
 mb_status mb_batch_tables(const int32_t *slots, const int32_t *cached, const int32_t *new_tokens, int32_t num_reqs,
@@ -543,8 +544,9 @@ mb_status mb_tables_release(const int32_t *slots, int32_t n, const int32_t *tabl
  * Rows outside every request are left as they were.  A request that breaks a
  * rule (kv_len below its tokens or above 2^24, a short table, rows outside
  * [0, T)) records MB_EDEVICE and its rows are left as they were; a page id out
- * of range is read as page 0, with MB_EDEVICE.  A vector or key that is not
- * finite makes the rows that see it NaN and reaches no other.  Logits, maxima,
+ * of range is read as page 0, with MB_EDEVICE.  A vector that is not finite
+ * makes the rows that see it NaN, a key acts on them through its logits (minus
+ * infinity: a weight of 0), and neither reaches any other row.  Logits, maxima,
  * sums and accumulators are fp32; rounded to bf16 on the way are the
  * probabilities, for their product with the values, and what a weight product
  * gives to the next one (q_nope W_uk and sum_j p_j c_j in the absorbed form, the

@@ -1499,7 +1499,8 @@ mb_status mb_latent_append(const void *ckv, int64_t ld, const void *q, const voi
                            const int32_t *tok_pos, const int32_t *tok_slot, int32_t T, int32_t num_pages,
                            int32_t n_heads, int32_t head_dim, int32_t rank, float rms_eps, float rope_theta,
                            void *stream) {
-  if (!ckv || !q || !gain || !pool || !q_rope || !tok_pos || !tok_slot)
+  // (an array of no elements may have no address)
+  if (!gain || !pool || (T != 0 && (!ckv || !q || !q_rope || !tok_pos || !tok_slot)))
     return fail(MB_EINVAL, "mb_latent_append: null argument");
   mb_status st = check_latent("mb_latent_append", T, num_pages, n_heads, head_dim, rank);
   if (st != MB_OK) return st;
@@ -1536,7 +1537,9 @@ int64_t mb_latent_attention_workspace_bytes(int32_t T, int32_t n_heads, int32_t 
 
 // What the two forms of latent attention ask of their arguments.
 static mb_status check_latent_attention(const char *who, const mb::LatentArgs &a, int64_t workspace_bytes) {
-  if (!a.q || !a.q_rope || !a.w_kv || !a.pool || !a.o || !a.qo_indptr || !a.kv_len || !a.bt_indptr || !a.bt || !a.workspace)
+  // (an array of no elements may have no address; a batch without tokens may list no pages)
+  if (!a.w_kv || !a.pool || !a.qo_indptr || !a.bt_indptr || !a.workspace || (a.n_reqs != 0 && !a.kv_len) ||
+      (a.T != 0 && (!a.q || !a.q_rope || !a.o || !a.bt)))
     return fail(MB_EINVAL, "%s: null argument", who);
   mb_status st = check_latent(who, a.T, a.num_pages, a.H, a.hd, a.rank);
   if (st != MB_OK) return st;

@@ -230,6 +230,11 @@ __global__ void __launch_bounds__(128) latent_query_kernel(const __grid_constant
                  (c > 0 || kk > 0) ? 1u : 0u);
     }
     mma_commit(done);
+    if (*abort_flag) {
+      const uint64_t t_start = globaltimer();
+      for (int c = 0; c < C::KC; ++c) drain(&full[c], 0, t_start);
+      drain(done, 0, t_start);
+    }
   } else if (blockIdx.x == 0 && h == 0) {
     // (thread 0's row is thread 1's to clear)
     if (t < p.T) p.tok[t].pieces = 0;
@@ -593,12 +598,8 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
       // after an abort, let copies in flight land before the CTA exits (bounded)
       if (!ok || *abort_flag) {
         const uint64_t t_start = globaltimer();
-        auto drain = [&](uint64_t *bar, int use) {
-          while (!mbar_try_wait(smem_u32(bar), use & 1) && globaltimer() - t_start < kWaitLimitNs) {
-          }
-        };
-        for (int i = max(0, kcnt - C::NST); i < kcnt; ++i) drain(&ct.k_full[i % C::NST], i / C::NST);
-        if (quse > 0) drain(&ct.q_full, quse - 1);
+        for (int i = max(0, kcnt - C::NST); i < kcnt; ++i) drain(&ct.k_full[i % C::NST], i / C::NST, t_start);
+        if (quse > 0) drain(&ct.q_full, quse - 1, t_start);
       }
     }
   } else if (warp <= 2) {
@@ -668,9 +669,7 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
     // every MMA issued above has completed before TMEM is freed
     if (elect_one()) mma_commit(&ct.done);
     __syncwarp();
-    const uint64_t t_end = globaltimer();
-    while (!mbar_try_wait(smem_u32(&ct.done), 0) && globaltimer() - t_end < kWaitLimitNs) {
-    }
+    drain(&ct.done, 0, globaltimer());
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------- softmax / epilogue
@@ -849,7 +848,9 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const AbsParams p) {
     const int t = static_cast<int>(row / p.H), h = static_cast<int>(row % p.H);
     const TokRec rec = p.tok[t];
     const int pieces = rec.pieces, col0 = static_cast<int>(item % SPLIT) * (RANK / SPLIT) + 4 * lane;   // and + 128 k
-    if (pieces <= 1) continue;
+    // (whole, or no request's; or, where requests of a bad descriptor overlap, the
+    // words of two records)
+    if (pieces <= 1 || (rec.first + pieces) * p.HT > kMaxCtas) continue;
     // piece 0 in slot 2 x0 + 1, piece s > 0 in slot 2 (x0 + s HT)
     const int x0 = rec.first * p.HT + h / p.Hc;
     const int place = rec.place * p.Hc + h % p.Hc;
@@ -985,6 +986,11 @@ __global__ void __launch_bounds__(128, 1)
                  (c > 0 || kk > 0) ? 1u : 0u);
     }
     mma_commit(done);
+    if (*abort_flag) {
+      const uint64_t t_start = globaltimer();
+      for (int c = 0; c < C::KC; ++c) drain(&full[c], 0, t_start);
+      drain(done, 0, t_start);
+    }
   } else if (tid >= 128 - TR) {
     const int k = tid - (128 - TR);
     live[k] = t0 + k < p.T && p.tok[t0 + k].pieces > 0;

@@ -59,6 +59,13 @@ __device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
   return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : div64_long(a, b);
 }
 
+// After a wait that ran out: lets the copies or products that `bar` counts land, at
+// most until the limit after t0, before the CTA exits.
+__device__ __forceinline__ void drain(uint64_t *bar, int use, uint64_t t0) {
+  while (!mbar_try_wait(smem_u32(bar), use & 1) && globaltimer() - t0 < kWaitLimitNs) {
+  }
+}
+
 // Fetch a tile into L2 ahead of its use (no shared memory, no completion).
 __device__ __forceinline__ void tma_prefetch_5d(const CUtensorMap *map, int32_t x0, int32_t x1, int32_t x2, int32_t x3, int32_t x4) {
   asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %3, %4, %5}];" ::"l"(map), "r"(x0), "r"(x1),

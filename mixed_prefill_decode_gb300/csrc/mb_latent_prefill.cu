@@ -329,17 +329,13 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (!ok || *abort_flag) {   // let copies in flight land before the CTA exits (bounded)
       const uint64_t t_start = globaltimer();
-      auto drain = [&](uint64_t *bar, int use) {
-        while (!mbar_try_wait(smem_u32(bar), use & 1) && globaltimer() - t_start < kWaitLimitNs) {
-        }
-      };
       if (lane == 0) {
         if (rank == 0)
-          for (int b = max(0, bcnt - C::NB); b < bcnt; ++b) drain(&ct.b_full[b % C::NB], b / C::NB);
+          for (int b = max(0, bcnt - C::NB); b < bcnt; ++b) drain(&ct.b_full[b % C::NB], b / C::NB, t_start);
         else
           while (bcnt > 0 && globaltimer() - t_start < kWaitLimitNs / 100) {   // (its weights count in rank 0: 20 ms)
           }
-        if (ause > 0) drain(&ct.a_full, ause - 1);
+        if (ause > 0) drain(&ct.a_full, ause - 1, t_start);
       }
     }
     __syncwarp();
@@ -377,9 +373,7 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
       }
       // every MMA issued above has completed before TMEM is freed
       mma_commit_pair(&ct.done, 1);
-      const uint64_t t_end = globaltimer();
-      while (!mbar_try_wait(smem_u32(&ct.done), 0) && globaltimer() - t_end < kWaitLimitNs) {
-      }
+      drain(&ct.done, 0, globaltimer());
     }
     __syncwarp();
   } else {
@@ -782,17 +776,13 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
       // after an abort, let copies in flight land before the CTA exits (bounded)
       if (!ok || *abort_flag) {
         const uint64_t t_start = globaltimer();
-        auto drain = [&](uint64_t *bar, int use) {
-          while (!mbar_try_wait(smem_u32(bar), use & 1) && globaltimer() - t_start < kWaitLimitNs) {
-          }
-        };
         for (int b = max(0, blk - C::NB); b < blk; ++b) {
-          drain(&ct.k_full[b % C::NB], b / C::NB);
-          drain(&ct.v_full[b % C::NB], b / C::NB);
+          drain(&ct.k_full[b % C::NB], b / C::NB, t_start);
+          drain(&ct.v_full[b % C::NB], b / C::NB, t_start);
         }
-        if (!ok && k_sent) drain(&ct.k_full[blk % C::NB], blk / C::NB);
+        if (!ok && k_sent) drain(&ct.k_full[blk % C::NB], blk / C::NB, t_start);
         for (int b = 0; b < 2; ++b)
-          if (quse[b] > 0) drain(&ct.q_full[b], quse[b] - 1);
+          if (quse[b] > 0) drain(&ct.q_full[b], quse[b] - 1, t_start);
       }
     }
     __syncwarp();
@@ -935,9 +925,7 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
     // every MMA issued above has completed before TMEM is freed
     if (elect_one()) mma_commit(&ct.done);
     __syncwarp();
-    const uint64_t t_end = globaltimer();
-    while (!mbar_try_wait(smem_u32(&ct.done), 0) && globaltimer() - t_end < kWaitLimitNs) {
-    }
+    drain(&ct.done, 0, globaltimer());
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------- softmax / epilogue

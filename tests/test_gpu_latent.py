@@ -4,8 +4,9 @@ Append.  A bf16 output is off by its rounding, 2^-8 of the value (half a
 step), and by the fp32 arithmetic before it: the sum of rank squares and the
 reciprocal root, at most (rank + 4) 2^-24 relative; for a rotated number
 a cos - b sin, 2^-22 (|a| + |b|) from products and sines and 2^-19 (|a| + |b|) from
-the angle (good to 2^-20 rad up to 10^5, where the reduction's constants leave
-k 2^-49 and the products 2^-48 of the angle).
+the angle (good to 2^-20 rad up to 2^24: the reduction's constants leave 2^-47 a
+turn, of 2^21.4 turns, the products 2^-48 of the angle, and the two steps round
+numbers below 8 by 2^-22 each).
 
 Attention.  Let p be the exact probabilities, y = sum_j p_j c_j, o = W_uv y,
 S the largest standard deviation of a row's logits, and let every rounding to
@@ -64,7 +65,7 @@ def _status(mb, err):
 # ----------------------------------------------------------------- append
 @pytest.mark.parametrize("T,H,hd,rank,ld,far", [
     (1, 1, 64, 256, 320, 5), (3, 5, 64, 512, 584, 70), (17, 40, 128, 512, 832, 100000), (33, 128, 128, 256, 320, 40000),
-    (700, 32, 128, 512, 576, 33000)])
+    (700, 32, 128, 512, 576, 33000), (9, 2, 64, 256, 320, 1 << 24)])
 def test_append(mb, T, H, hd, rank, ld, far):
     rng = np.random.default_rng(T)
     P, eps, theta = T // 16 + 4, 1e-6, 10000.0

@@ -75,6 +75,14 @@ def test_empty_calls_do_nothing(mb):
         _attention(mb, form, num_reqs=0)
 
 
+def test_arrays_of_no_elements_may_have_no_address(mb):
+    _append(mb, T=0, **{n: None for n in ("ckv", "q", "q_rope", "tok_pos", "tok_slot")})
+    for form in FORMS:
+        _attention(mb, form, T=0, **{n: None for n in ("q", "q_rope", "o", "bt")})
+        _attention(mb, form, T=0, num_reqs=0, **{n: None for n in ("q", "q_rope", "o", "bt", "kv_len")})
+        _refused(mb, lambda: _attention(mb, form, T=0, kv_len=None), "MB_EINVAL")
+
+
 APP = ["ckv", "q", "gain", "pool", "q_rope", "tok_pos", "tok_slot"]
 APP_BYTES = dict(ckv=2 * (2 * 832 + 576), q=3 * 8 * 192 * 2, gain=1024, pool=4 * 16 * 576 * 2, q_rope=3 * 8 * 64 * 2,
                  tok_pos=12, tok_slot=12)
