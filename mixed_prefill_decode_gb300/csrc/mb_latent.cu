@@ -292,7 +292,7 @@ constexpr int kMinShare = 1;        // the least a CTA takes, in blocks
 
 struct AbsParams {
   __nv_bfloat16 *oc;             // [T][H][rank]: sum_j p_j c_j
-  const __nv_bfloat16 *pool;
+  const uint8_t *pool;
   const int32_t *qo_indptr, *kv_len, *bt_indptr, *bt;
   int n_reqs, T, H, Hc, HT, NT, N, num_pages;   // heads of a tile, head tiles, tokens of a tile, padded rows
   float scale_log2;
@@ -301,15 +301,26 @@ struct AbsParams {
   int *err;
 };
 
+// Queries of a tile and of a single token (vectors, then rotated), the parts of the
+// cache's pages.
+struct AbsMaps {
+  CUtensorMap q[2][2], k[2];
+};
+
 template <int RANK>
 struct AbsCfg {
   static constexpr int NC = RANK / 64 + 1;          // 64-wide chunks of a cached row
-  static constexpr int ATOM = NC * 1024;            // 8 rows: [chunk][8 rows][128 B]
-  static constexpr int PAGE_BYTES = 2 * ATOM;
-  static constexpr int STAGE = (kBlk / 8) * ATOM;
+  static constexpr int DT = RANK / 128;             // tiles of 128 numbers of the vectors
+  // A stage holds a block in two parts, each [page][8 rows of 2][chunk][8 rows][128 B]:
+  // half of the vectors, and the other half with the rotated keys.  Parts are
+  // loaded, waited for and given back by themselves, so S begins when the first has
+  // come (16 requests at 8,192 keys, 128 heads: 68 us; 72 with whole blocks given back
+  // page by page; 86 with five parts, whose copies of 4 KB come at 18 bytes a cycle).
+  static constexpr int C0 = DT, C1 = DT + 1;        // chunks of the parts
+  static constexpr int PART0 = C0 * kBlk * 128, PART1 = C1 * kBlk * 128;
+  static constexpr int STAGE = PART0 + PART1, PAGE_BYTES = STAGE / 4;
   static constexpr int NST = RANK == 512 ? 2 : 4;
   static constexpr int Q_CHUNK = 64 * 128;
-  static constexpr int DT = RANK / 128;             // tiles of 128 numbers of the vectors
   static constexpr int NSEG = 4;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = OFF_Q + NC * Q_CHUNK;
@@ -340,7 +351,7 @@ template <int RANK>
 struct AbsCtrl {
   using C = AbsCfg<RANK>;
   uint64_t q_full, q_empty;
-  uint64_t k_full[C::NST], k_empty[C::NST][4];   // empty: page by page
+  uint64_t k_full[C::NST][2], k_empty[C::NST][2];
   uint64_t s_full[2], s_empty[2], p_full, pv_done;
   uint64_t seg_full[C::NSEG], seg_empty[C::NSEG];
   uint64_t done;
@@ -370,8 +381,7 @@ __device__ __forceinline__ AbsReq abs_req(const AbsParams &p, const ReqWords w, 
 
 template <int RANK>
 __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
-    latent_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmR,
-                            const __grid_constant__ CUtensorMap tmK, const __grid_constant__ AbsParams p) {
+    latent_attention_kernel(const __grid_constant__ AbsMaps maps, const __grid_constant__ AbsParams p) {
   using C = AbsCfg<RANK>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *sQ = smem + C::OFF_Q, *sK = smem + C::OFF_K, *sP = smem + C::OFF_P;
@@ -390,8 +400,10 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
     mbar_init(&ct.q_full, 1);
     mbar_init(&ct.q_empty, 1);
     for (int s = 0; s < C::NST; ++s) {
-      mbar_init(&ct.k_full[s], 1);
-      for (int k = 0; k < 4; ++k) mbar_init(&ct.k_empty[s][k], 1);
+      for (int g = 0; g < 2; ++g) {
+        mbar_init(&ct.k_full[s][g], 1);
+        mbar_init(&ct.k_empty[s][g], 1);
+      }
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ct.s_full[b], 1);
@@ -407,9 +419,10 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
     ct.abort = 0;
     ct.start_req = -1;
     fence_mbar_init();
-    prefetch_tmap(&tmQ);
-    prefetch_tmap(&tmR);
-    prefetch_tmap(&tmK);
+    for (int i = 0; i < 2; ++i) {
+      prefetch_tmap(&maps.k[i]);
+      for (int k = 0; k < 2; ++k) prefetch_tmap(&maps.q[i][k]);
+    }
   }
   if (warp == 1) {
     tmem_alloc(&ct.tmem, C::TMEM_COLS);
@@ -418,7 +431,8 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
   // Of what earlier kernels of the stream write, only the queries' products come
   // from this call's first kernel; this one is launched once that one has seen
   // all others finished, so the descriptor and the cache are there.  The producer
-  // waits before it loads queries.
+  // waits before it loads queries.  (That kernel has nearly always ended by then: its
+  // CTAs leave no room for this one's.)
 
   // ---- this CTA's part of the line: [x0, x1) of `total`
   const int per = (p.n_reqs + C::THREADS - 1) / C::THREADS;
@@ -478,7 +492,8 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
     if (r + 1 < p.n_reqs) nx = load_req(p.qo_indptr, p.kv_len, p.bt_indptr, r + 1);
     int u = static_cast<int>(div64(x0 - ct.start_base, q.unit));   // the unit that x0 lies in
     int64_t base = ct.start_base + u * q.unit;
-    int kcnt = 0, nseg = 0, quse = 0;
+    int kcnt = 0, sent = 0, nseg = 0, quse = 0;   // sent: parts of blocks
+    const int pl = lane & 3;   // a lane's page of a block
     bool ok = true, waited = false;
     while (ok && base < x1) {
       auto cut = [&](int64_t x) {   // blocks of the unit that lie before x
@@ -493,65 +508,67 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
         const int i0 = u * p.NT, toks = min(p.NT, q.n - i0);
         const int32_t *table = p.bt + q.b0;
         const int n_pages = (q.kv + kPage - 1) / kPage;
-        // Page ids, one per lane 0 to 3, of the block to be sent and the one behind
-        // it, which is on its way to L2 while it waits for a stage.  (96 requests at
-        // 1,024 to 8,192 keys 88 us; 90, 93 and 109 with one, two and four more blocks
-        // under way, 93 with none.)
-        auto page_of = [&](int blk) {
-          int pg = lane < 4 && blk < j1 && 4 * blk + lane < n_pages ? table[4 * blk + lane] : -1;
-          if (lane < 4 && blk < j1 && 4 * blk + lane < n_pages && (pg < 0 || pg >= p.num_pages)) {
-            atomicExch(p.err, kErrBounds);
-            pg = 0;
-          }
-          return pg;
-        };
+        // Page ids, a lane's, of the block to be sent and the one behind it, which is
+        // on its way to L2 while it waits for a stage.  (96 requests at 1,024 to
+        // 8,192 keys 88 us; 90, 93 and 109 with one, two and four more blocks under
+        // way, 93 with none.)  They are looked at when they are used: their loads
+        // take as long as a product.
+        auto page_of = [&](int blk) { return blk < j1 && 4 * blk + pl < n_pages ? table[4 * blk + pl] : -1; };
         int cur = page_of(j0), nxt = page_of(j0 + 1);
         int j = j0;
-        auto send = [&]() {   // block j
-          const int np = min(4, n_pages - 4 * j), st = kcnt % C::NST;
+        auto send = [&]() {   // block j: lane 4 g + k copies part g of page k
+          const int np = min(4, n_pages - 4 * j), st = kcnt % C::NST, part = lane >> 2;
+          int page = pl < np ? cur : 0;
+          if (page < 0 || page >= p.num_pages) {
+            atomicExch(p.err, kErrBounds);
+            page = 0;
+          }
+          auto bytes = [&](int g) { return np * ((g ? C::PART1 : C::PART0) / 4); };
+          auto copy = [&](int g) {
+            tma_load_5d(sK + st * C::STAGE + g * C::PART0 + pl * ((g ? C::PART1 : C::PART0) / 4), &maps.k[g], &ct.k_full[st][g], 0, 0,
+                        g * C::C0, 0, page);
+          };
           if (kcnt < C::NST) {   // nothing to wait for
-            if (lane == 0) mbar_arrive_expect_tx(&ct.k_full[st], np * C::PAGE_BYTES);
+            if (lane < 2) mbar_arrive_expect_tx(&ct.k_full[st][lane], bytes(lane));
             __syncwarp();
-            if (lane < np)
-              tma_load_5d(sK + st * C::STAGE + lane * C::PAGE_BYTES, &tmK, &ct.k_full[st], 0, 0, 0, 0, cur);
+            if (part < 2 && pl < np) copy(part);
+            sent += 2;
           } else {
-            ok = __all_sync(0xffffffffu, mbar_wait(&ct.k_empty[st][0], ((kcnt / C::NST) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer));
-            if (!ok) return;
-            if (lane == 0) mbar_arrive_expect_tx(&ct.k_full[st], np * C::PAGE_BYTES);
-            __syncwarp();
 #pragma unroll 1
-            for (int k = 0; k < np; ++k) {
-              // (past the first, a page that is not given back in time is drained below)
-              if (k > 0) ok = __all_sync(0xffffffffu, mbar_wait(&ct.k_empty[st][k], ((kcnt / C::NST) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer));
+            for (int g = 0; g < 2; ++g, ++sent) {
+              ok = __all_sync(0xffffffffu, mbar_wait(&ct.k_empty[st][g], ((kcnt / C::NST) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer));
               if (!ok) return;
-              if (lane == k)
-                tma_load_5d(sK + st * C::STAGE + lane * C::PAGE_BYTES, &tmK, &ct.k_full[st], 0, 0, 0, 0, cur);
+              if (lane == 0) mbar_arrive_expect_tx(&ct.k_full[st][g], bytes(g));
+              __syncwarp();
+              if (part == g && pl < np) copy(g);
             }
           }
           cur = nxt;
-          if (++kcnt >= C::NST && cur >= 0) tma_prefetch_5d(&tmK, 0, 0, 0, 0, cur);
+          if (++kcnt >= C::NST && lane < 4 && cur >= 0 && cur < p.num_pages)
+            l2_prefetch(p.pool + cur * static_cast<int64_t>(C::PAGE_BYTES), C::PAGE_BYTES);
           nxt = page_of(++j + 1);
         };
-        // (the kernel before has nearly always ended by now: its CTAs leave no room
-        // for this one's.  The queries go first: behind two blocks of keys they came
-        // 2 us later, as all CTAs' first blocks are more than HBM brings in that time.)
         if (!waited) {
           pdl_wait();
           pdl_trigger();
           waited = true;
         }
-        // the query tile, a copy per lane
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(&ct.q_empty, (quse & 1) ^ 1, abort_flag, p.err, kErrWaitProducer));
+        // the query tile, a copy per lane.  (Before the first keys: behind two blocks
+        // of them it came 2 us later, as all CTAs' first blocks are more than HBM
+        // brings in that time.)
+        ok = __all_sync(0xffffffffu, mbar_wait(&ct.q_empty, (quse & 1) ^ 1, abort_flag, p.err, kErrWaitProducer));
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&ct.q_full, C::NC * p.Hc * p.NT * 128);
+        const int one = toks == 1;
+        if (lane == 0) mbar_arrive_expect_tx(&ct.q_full, C::NC * p.Hc * (one ? 1 : p.NT) * 128);
         __syncwarp();
         if (lane < C::NC)
-          tma_load_3d(sQ + lane * C::Q_CHUNK, lane < C::NC - 1 ? &tmQ : &tmR, &ct.q_full, lane < C::NC - 1 ? lane * 64 : 0, ht * p.Hc, q.t0 + i0);
+          tma_load_3d(sQ + lane * C::Q_CHUNK, &maps.q[one][lane == C::NC - 1], &ct.q_full, lane < C::NC - 1 ? lane * 64 : 0, ht * p.Hc, q.t0 + i0);
         ++quse;
+        while (j < j1 && kcnt < C::NST) send();
         const int first = owner(0), last_w = owner(q.nkb - 1);
         // the piece's record for the other roles
         const int ss = nseg % C::NSEG;
-        if (lane == 0 && ok) {
+        if (lane == 0) {
           ok = mbar_wait(&ct.seg_empty[ss], ((nseg / C::NSEG) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer);
           if (ok) {
             AbsSeg &sg = ct.seg[ss];
@@ -598,7 +615,7 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
       // after an abort, let copies in flight land before the CTA exits (bounded)
       if (!ok || *abort_flag) {
         const uint64_t t_start = globaltimer();
-        for (int i = max(0, kcnt - C::NST); i < kcnt; ++i) drain(&ct.k_full[i % C::NST], i / C::NST, t_start);
+        for (int i = max(0, sent - 2 * C::NST); i < sent; ++i) drain(&ct.k_full[i / 2 % C::NST][i % 2], i / 2 / C::NST, t_start);
         if (quse > 0) drain(&ct.q_full, quse - 1, t_start);
       }
     }
@@ -611,9 +628,9 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
     auto wait = [&](uint64_t *bar, uint32_t par) {
       return __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag, p.err, kErrWaitMma)) != 0;
     };
-    const uint64_t kd0 = sdesc_sw128(smem_u32(sK), 16, C::ATOM);
+    const uint64_t kd0 = sdesc_sw128(smem_u32(sK), 16, C::C0 * 1024), kd1 = sdesc_sw128(smem_u32(sK + C::PART0), 16, C::C1 * 1024);
     const uint64_t qd0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
-    const uint64_t vd0 = sdesc_sw128(smem_u32(sK), 1024, C::ATOM);
+    const uint64_t vd0 = sdesc_sw128(smem_u32(sK), 1024, C::C0 * 1024), vd1 = sdesc_sw128(smem_u32(sK + C::PART0), 1024, C::C1 * 1024);
     const uint64_t pd0 = sdesc_sw128(smem_u32(sP), 16, 1024);
     const uint32_t idesc_pv = idesc_bf16_ab(128, p.N, true, false);
     int nseg = 0, item = 0;
@@ -628,34 +645,45 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
       for (int lb = 0; lb < nb && ok; ++lb, ++item) {
         const int st = item % C::NST;
         if (warp == 1) {
-          ok = wait(&ct.k_full[st], (item / C::NST) & 1) && wait(&ct.s_empty[item & 1], ((item >> 1) & 1) ^ 1);
-          if (!ok) break;
-          tc_fence_after();
+          ok = wait(&ct.s_empty[item & 1], ((item >> 1) & 1) ^ 1);
           const uint32_t d = tmem + 64 * (item & 1);
-          const uint64_t kd = kd0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
-          if (elect_one()) {
+          const uint64_t at = static_cast<uint64_t>((st * C::STAGE) >> 4);
 #pragma unroll
-            for (int ch = 0; ch < C::NC; ++ch)
+          for (int g = 0; g < 2; ++g) {   // the parts, as they come
+            ok = ok && wait(&ct.k_full[st][g], (item / C::NST) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t kd = (g ? kd1 : kd0) + at;
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_bf16(d, qd0 + ((ch * C::Q_CHUNK + kk * 32) >> 4), kd + ((ch * 1024 + kk * 32) >> 4), C::IDESC_S,
-                         (ch > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(&ct.s_full[item & 1]);
-            if (lb + 1 == nb) mma_commit(&ct.q_empty);
+              for (int ch = 0; ch < (g ? C::C1 : C::C0); ++ch)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  mma_bf16(d, qd0 + (((g * C::C0 + ch) * C::Q_CHUNK + kk * 32) >> 4), kd + ((ch * 1024 + kk * 32) >> 4), C::IDESC_S,
+                           (g > 0 || ch > 0 || kk > 0) ? 1u : 0u);
+              if (g == 1) {
+                mma_commit(&ct.s_full[item & 1]);
+                if (lb + 1 == nb) mma_commit(&ct.q_empty);
+              }
+            }
+            __syncwarp();
           }
+          if (!ok) break;
         } else {
           ok = wait(&ct.p_full, item & 1);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t vd = vd0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
+          const uint64_t at = static_cast<uint64_t>((st * C::STAGE) >> 4);
           if (elect_one()) {
 #pragma unroll
-            for (int ks = 0; ks < kBlk / 16; ++ks) {   // 16 keys (a page) per MMA; 128 numbers are two chunks
+            for (int dt = 0; dt < C::DT; ++dt) {
+              const int g = dt >= C::DT / 2, cc = g ? C::C1 : C::C0;   // the tile's part, and its chunks
+              const uint64_t vd = (g ? vd1 : vd0) + at + (((2 * dt - g * C::C0) * 1024) >> 4);
 #pragma unroll
-              for (int dt = 0; dt < C::DT; ++dt)
-                mma_bf16(tmem + C::O_COL + 64 * dt, vd + ((ks * 2 * C::ATOM + dt * 2048) >> 4), pd0 + ((ks * 32) >> 4),
-                         idesc_pv, (lb > 0 || ks > 0) ? 1u : 0u);
-              mma_commit(&ct.k_empty[st][ks]);
+              for (int ks = 0; ks < kBlk / 16; ++ks)   // 16 keys (a page) per MMA
+                mma_bf16(tmem + C::O_COL + 64 * dt, vd + ((ks * 2 * cc * 1024) >> 4), pd0 + ((ks * 32) >> 4), idesc_pv,
+                         (lb > 0 || ks > 0) ? 1u : 0u);
+              if (dt % (C::DT / 2) == C::DT / 2 - 1) mma_commit(&ct.k_empty[st][g]);
             }
             mma_commit(&ct.pv_done);
           }
@@ -773,8 +801,9 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
           // that is not finite; the rows that see one become NaN at the end.
           const int key = key0 + tid;
           if (key > first) {
-            uint8_t *vrow = sK + (item % C::NST) * C::STAGE + (tid >> 3) * C::ATOM + (tid & 7) * 128;
-            if (wipe_row<RANK / 64>(vrow, key >= kv)) atomicMin(&sg.odd, key);
+            uint8_t *stage = sK + (item % C::NST) * C::STAGE, *row0 = stage + (tid >> 3) * (C::C0 * 1024) + (tid & 7) * 128,
+                    *row1 = stage + C::PART0 + (tid >> 3) * (C::C1 * 1024) + (tid & 7) * 128;
+            if (wipe_row<C::DT>(row0, row1, key >= kv)) atomicMin(&sg.odd, key);
           }
         }
         fence_proxy_async_smem();
@@ -1064,20 +1093,23 @@ template <int RANK>
 cudaError_t launch_attention(const LatentArgs &a, AbsParams &p, const void *qc, cudaStream_t st) {
   using C = AbsCfg<RANK>;
   const uint64_t H = a.H, T = a.T, R = RANK, W = RANK + kLatentRope;
-  CUtensorMap tq, tr, tk;
+  AbsMaps m;
   const uint64_t dq[3] = {R, H, T}, sq[2] = {R * 2, R * 2 * H};
   const uint64_t dr[3] = {kLatentRope, H, T}, sr[2] = {kLatentRope * 2, kLatentRope * 2 * H};
-  const uint32_t bq[3] = {64, static_cast<uint32_t>(p.Hc), static_cast<uint32_t>(p.NT)};
   const uint64_t dk[5] = {64, 8, C::NC, kPage / 8, static_cast<uint64_t>(a.num_pages)};
   const uint64_t sk[4] = {W * 2, 128, 8 * W * 2, kPage * W * 2};
-  const uint32_t bk[5] = {64, 8, C::NC, kPage / 8, 1};
-  cudaError_t e = encode_tmap(&tq, qc, 3, dq, sq, bq);
-  if (e == cudaSuccess) e = encode_tmap(&tr, a.q_rope, 3, dr, sr, bq);
-  if (e == cudaSuccess) e = encode_tmap_5d(&tk, a.pool, dk, sk, bk);
+  cudaError_t e = cudaSuccess;
+  for (uint32_t i = 0; i < 2 && e == cudaSuccess; ++i) {   // (q: i = 1, a single token)
+    const uint32_t bq[3] = {64, static_cast<uint32_t>(p.Hc), i ? 1u : static_cast<uint32_t>(p.NT)};
+    const uint32_t bk[5] = {64, 8, static_cast<uint32_t>(i ? C::C1 : C::C0), kPage / 8, 1};
+    e = encode_tmap(&m.q[i][0], qc, 3, dq, sq, bq);
+    if (e == cudaSuccess) e = encode_tmap(&m.q[i][1], a.q_rope, 3, dr, sr, bq);
+    if (e == cudaSuccess) e = encode_tmap_5d(&m.k[i], a.pool, dk, sk, bk);
+  }
   if (e == cudaSuccess) e = ensure_max_smem(reinterpret_cast<const void *>(latent_attention_kernel<RANK>), C::SMEM);
   if (e != cudaSuccess) return e;
   const int ctas = std::min(device_sm_count(), kMaxCtas) / p.HT * p.HT;
-  e = launch_pdl(latent_attention_kernel<RANK>, dim3(ctas), dim3(C::THREADS), C::SMEM, st, 1, tq, tr, tk, p);
+  e = launch_pdl(latent_attention_kernel<RANK>, dim3(ctas), dim3(C::THREADS), C::SMEM, st, 1, m, p);
   if (e != cudaSuccess) return e;
   // a warp a row, or several where all fit the SMs at once (8 warps a CTA, 2 CTAs an SM)
   const int64_t rows = static_cast<int64_t>(a.T) * a.H, room = 2ll * device_sm_count();
@@ -1126,7 +1158,7 @@ cudaError_t latent_attention_run(const LatentArgs &a, cudaStream_t st) {
   TokRec *tok = reinterpret_cast<TokRec *>(w + 2 * rows);
   AbsParams p;
   p.oc = oc;
-  p.pool = static_cast<const __nv_bfloat16 *>(a.pool);
+  p.pool = static_cast<const uint8_t *>(a.pool);
   p.qo_indptr = a.qo_indptr;
   p.kv_len = a.kv_len;
   p.bt_indptr = a.bt_indptr;

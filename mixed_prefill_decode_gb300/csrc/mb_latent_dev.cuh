@@ -66,30 +66,24 @@ __device__ __forceinline__ void drain(uint64_t *bar, int use, uint64_t t0) {
   }
 }
 
-// Fetch a tile into L2 ahead of its use (no shared memory, no completion).
-__device__ __forceinline__ void tma_prefetch_5d(const CUtensorMap *map, int32_t x0, int32_t x1, int32_t x2, int32_t x3, int32_t x4) {
-  asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %3, %4, %5}];" ::"l"(map), "r"(x0), "r"(x1),
-               "r"(x2), "r"(x3), "r"(x4)
-               : "memory");
-}
-
 // Bytes from a 16-byte boundary (a multiple of 16), into L2.
 __device__ __forceinline__ void l2_prefetch(const void *p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
-// Zeroes a row of CHUNKS 64-wide chunks (1 KB apart) of a swizzled stage if
+// Zeroes a key's row, two parts of CHUNKS swizzled 128-byte chunks (1 KB apart), if
 // `stale`, or if it holds an infinity or a NaN (then true).
 template <int CHUNKS>
-__device__ __noinline__ bool wipe_row(uint8_t *row, bool stale) {
+__device__ __noinline__ bool wipe_row(uint8_t *row0, uint8_t *row1, bool stale) {
   bool odd = false;
   if (!stale) {
     uint32_t special = 0;
 #pragma unroll 1
-    for (int c = 0; c < CHUNKS; ++c)
+    for (int c = 0; c < 2 * CHUNKS; ++c)
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(row + c * 1024 + ((k + threadIdx.x) & 7) * 16);
+        const uint8_t *at = (c < CHUNKS ? row0 : row1 - CHUNKS * 1024) + c * 1024;
+        const uint4 x = *reinterpret_cast<const uint4 *>(at + ((k + threadIdx.x) & 7) * 16);
         const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -99,10 +93,10 @@ __device__ __noinline__ bool wipe_row(uint8_t *row, bool stale) {
   }
   if (stale || odd)
 #pragma unroll 1
-    for (int c = 0; c < CHUNKS; ++c)
+    for (int c = 0; c < 2 * CHUNKS; ++c)
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        *reinterpret_cast<uint4 *>(row + c * 1024 + ((k + threadIdx.x) & 7) * 16) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>((c < CHUNKS ? row0 : row1 - CHUNKS * 1024) + c * 1024 + ((k + threadIdx.x) & 7) * 16) = make_uint4(0, 0, 0, 0);
   return odd;
 }
 
