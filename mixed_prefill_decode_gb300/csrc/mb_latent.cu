@@ -861,22 +861,23 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
 
 // ----------------------------------------------------------- cut units' rows
 // oc[t][h] = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,  M = max_s m_s, for the
-// tokens whose unit was cut.  A kernel of its own, without shared memory: beside
-// 200 KB of it L1 has room for so few lines on their way that bringing the
+// tokens whose unit was cut.  A kernel of its own, with little shared memory:
+// beside 200 KB of it L1 has room for so few lines on their way that bringing the
 // pieces in within the next kernel took 5 to 14 us (3 here).  A warp takes a
-// row, or, where there are few rows, a quarter of one with more pieces in flight.
-template <int RANK, int SPLIT>
+// row; where there are few rows, and each may have a hundred pieces, the CTA's
+// eight warps take every eighth piece of one.
+template <int RANK, int WARPS>
 __global__ void __launch_bounds__(256) latent_merge_kernel(const AbsParams p) {
-  constexpr int PER = RANK / 128 / SPLIT, AHEAD = 16 / PER > 8 ? 8 : 16 / PER;   // vectors of a lane; pieces in flight
+  constexpr int PER = RANK / 128, AHEAD = 16 / PER;   // vectors of a lane; pieces in flight
+  __shared__ float sh_acc[WARPS == 1 ? 1 : WARPS][WARPS == 1 ? 1 : RANK], sh_m[WARPS], sh_l[WARPS];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int64_t slot = part_floats(RANK), items = static_cast<int64_t>(p.T) * p.H * SPLIT;
-  for (int64_t item = blockIdx.x * 8 + (threadIdx.x >> 5); item < items; item += gridDim.x * 8) {
-    const int64_t row = item / SPLIT;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = WARPS == 1 ? 0 : warp;
+  const int64_t slot = part_floats(RANK), rows = static_cast<int64_t>(p.T) * p.H;
+  for (int64_t row = WARPS == 1 ? blockIdx.x * 8 + warp : blockIdx.x; row < rows; row += gridDim.x * (8 / WARPS)) {
     const int t = static_cast<int>(row / p.H), h = static_cast<int>(row % p.H);
     const TokRec rec = p.tok[t];
-    const int pieces = rec.pieces, col0 = static_cast<int>(item % SPLIT) * (RANK / SPLIT) + 4 * lane;   // and + 128 k
+    const int pieces = rec.pieces;
     // (whole, or no request's; or, where requests of a bad descriptor overlap, the
     // words of two records)
     if (pieces <= 1 || (rec.first + pieces) * p.HT > kMaxCtas) continue;
@@ -891,19 +892,20 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const AbsParams p) {
 #pragma unroll
       for (int s = 0; s < AHEAD; ++s) {
         ml[s] = make_float2(-INFINITY, 0.f);
-        if (s0 + s < pieces) {
-          ml[s] = *reinterpret_cast<const float2 *>(src(s0 + s) + 64 * RANK + 2 * place);
+        if (s0 + s * WARPS < pieces) {
+          ml[s] = *reinterpret_cast<const float2 *>(src(s0 + s * WARPS) + 64 * RANK + 2 * place);
 #pragma unroll
-          for (int k = 0; k < PER; ++k) v[s][k] = *reinterpret_cast<const float4 *>(src(s0 + s) + place * RANK + col0 + 128 * k);
+          for (int k = 0; k < PER; ++k)
+            v[s][k] = *reinterpret_cast<const float4 *>(src(s0 + s * WARPS) + place * RANK + 4 * lane + 128 * k);
         }
       }
     };
-    fetch(0);
+    fetch(share);
     float M = -INFINITY, L = 0.f;
     float4 acc[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < pieces; s0 += AHEAD) {
+    for (int s0 = share; s0 < pieces; s0 += AHEAD * WARPS) {
       float top = M;
 #pragma unroll
       for (int s = 0; s < AHEAD; ++s) top = fmaxf(top, ml[s].x);
@@ -932,13 +934,39 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const AbsParams p) {
           }
       }
       M = top;
-      if (s0 + AHEAD < pieces) fetch(s0 + AHEAD);
+      if (s0 + AHEAD * WARPS < pieces) fetch(s0 + AHEAD * WARPS);
     }
-    const float inv = 1.f / L;
-    uint2 *dst = reinterpret_cast<uint2 *>(p.oc + row * RANK + col0);
+    if (WARPS == 1) {
+      const float inv = 1.f / L;
+      uint2 *dst = reinterpret_cast<uint2 *>(p.oc + row * RANK + 4 * lane);
 #pragma unroll
-    for (int k = 0; k < PER; ++k)
-      dst[32 * k] = make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv), pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+      for (int k = 0; k < PER; ++k)
+        dst[32 * k] = make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv), pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+      continue;
+    }
+    // the warps' shares, two columns a thread
+    if (lane == 0) sh_m[share] = M, sh_l[share] = L;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) *reinterpret_cast<float4 *>(&sh_acc[share][4 * lane + 128 * k]) = acc[k];
+    __syncthreads();
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) top = fmaxf(top, sh_m[w]);
+    float2 sum = make_float2(0.f, 0.f);
+    L = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float a = sh_m[w] == -INFINITY ? 0.f : ex2_approx(sh_m[w] - top);
+      L += sh_m[w] == -INFINITY ? sh_l[w] : a * sh_l[w];
+      if (2 * threadIdx.x < RANK && a != 0.f) {
+        const float2 x = *reinterpret_cast<const float2 *>(&sh_acc[w][2 * threadIdx.x]);
+        sum.x = fmaf(a, x.x, sum.x);
+        sum.y = fmaf(a, x.y, sum.y);
+      }
+    }
+    if (2 * threadIdx.x < RANK)
+      reinterpret_cast<uint32_t *>(p.oc + row * RANK)[threadIdx.x] = pack_bf16x2(sum.x / L, sum.y / L);
+    __syncthreads();   // the next row's shares go where these are
   }
 }
 
@@ -1111,10 +1139,9 @@ cudaError_t launch_attention(const LatentArgs &a, AbsParams &p, const void *qc, 
   const int ctas = std::min(device_sm_count(), kMaxCtas) / p.HT * p.HT;
   e = launch_pdl(latent_attention_kernel<RANK>, dim3(ctas), dim3(C::THREADS), C::SMEM, st, 1, m, p);
   if (e != cudaSuccess) return e;
-  // a warp a row, or several where all fit the SMs at once (8 warps a CTA, 2 CTAs an SM)
+  // a CTA a row where all fit the SMs at once (two an SM), else a warp
   const int64_t rows = static_cast<int64_t>(a.T) * a.H, room = 2ll * device_sm_count();
-  if (rows * (RANK / 128) <= room * 8)
-    return launch_pdl(latent_merge_kernel<RANK, RANK / 128>, dim3(static_cast<unsigned>((rows * (RANK / 128) + 7) / 8)), dim3(256), 0, st, 1, p);
+  if (rows <= room) return launch_pdl(latent_merge_kernel<RANK, 8>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, st, 1, p);
   return launch_pdl(latent_merge_kernel<RANK, 1>, dim3(static_cast<unsigned>(std::min((rows + 7) / 8, room))), dim3(256), 0, st, 1, p);
 }
 
