@@ -47,7 +47,7 @@ namespace {
 using namespace dev;
 
 constexpr int kMaxCtas = 160;      // CTAs of an attention launch at most; sizes the workspace
-constexpr int kRecBytes = 8192;    // workspace: one record of 8 ints per CTA, then the partials
+constexpr int kRecBytes = 8192, kPartsBytes = 20480;   // workspace: a record of 8 ints and a PrePart per CTA
 constexpr int kBlk = 128;          // keys of a block
 __host__ __device__ constexpr int64_t part_floats(int64_t hd) { return 256 * (hd + 2); }   // of a slot
 // Keys and values of a group of heads at most (of one head, whatever it takes).
@@ -59,6 +59,7 @@ constexpr int kGroupBytes = 512 << 20;
 // between the first and the last of a unit is left without a block).
 constexpr int kCost1 = 2, kCost2 = 3, kCostUnit = 5, kMinShare = 3;
 
+struct PrePart;
 struct PreParams {
   __nv_bfloat16 *kv;             // [heads of the group][rows][2 hd]: a head's keys and values
   __nv_bfloat16 *o;
@@ -68,6 +69,8 @@ struct PreParams {
   int cap_blocks;                // blocks of 128 rows that kv has room for
   float scale_log2;
   int32_t *rec;
+  PrePart *parts;                // of the attention kernel's CTAs
+  int ctas;
   float *part;                   // [2 slots per CTA]: o of 256 rows [hd][256], their m and l [256][2]
   int *err;
 };
@@ -78,19 +81,19 @@ __device__ __forceinline__ int key_blocks(const ReqWords &w, int T, bool *bad) {
   return *bad || w.q1 == w.q0 ? 0 : (w.kv + kBlk - 1) / kBlk;
 }
 
-// Sums over the CTA's threads: this thread's exclusive prefix, and the total.
-template <int WARPS>
-__device__ __forceinline__ int64_t cta_scan(int64_t mine, int64_t *sums, int64_t *total) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// Sums over the threads of WARPS warps (named barrier BAR): this thread's exclusive
+// prefix, and the total.
+template <int WARPS, int BAR>
+__device__ __forceinline__ int64_t warps_scan(int64_t mine, int warp, int64_t *sums, int64_t *total) {
+  const int lane = threadIdx.x & 31;
   int64_t inc = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const int64_t v = __shfl_up_sync(0xffffffffu, inc, off);
     if (lane >= off) inc += v;
   }
-  __syncthreads();   // sums may still be read from the scan before
   if (lane == 31) sums[warp] = inc;
-  __syncthreads();
+  named_bar_sync(BAR, 32 * WARPS);
   int64_t pre = inc - mine, all = 0;
 #pragma unroll
   for (int w = 0; w < WARPS; ++w) {
@@ -101,11 +104,102 @@ __device__ __forceinline__ int64_t cta_scan(int64_t mine, int64_t *sums, int64_t
   return pre;
 }
 
+// ------------------------------------------------------------ the schedule
+struct PreReq {
+  int t0, n, c, row_blk;   // first row of q, tokens, cached tokens, first block of the workspace
+  int full, rem, a;        // units of 256 rows, rows of the last one if it is smaller, blocks of the cached tokens
+  int64_t head;            // cost of one head
+};
+
+// Cost of the first u units of 256 rows of a request and head: unit k has a +
+// 2 (k + 1) blocks.
+__device__ __forceinline__ int64_t units_cost(int a, int64_t u) {
+  return u * (kCostUnit + static_cast<int64_t>(kCost2) * a) + kCost2 * u * (u + 1);
+}
+__device__ __forceinline__ int tail_blocks(const PreReq &q) { return (q.c + q.n + kBlk - 1) / kBlk; }
+
+__device__ __forceinline__ PreReq pre_req(const PreParams &p, const ReqWords &w, int64_t row_blk) {
+  PreReq q;
+  bool bad;
+  const int blocks = key_blocks(w, p.T, &bad);
+  q.t0 = w.q0;
+  q.n = blocks > 0 && row_blk + blocks <= p.cap_blocks ? w.q1 - w.q0 : 0;
+  q.c = w.kv - q.n;
+  q.row_blk = static_cast<int>(row_blk);
+  q.full = q.n / 256;
+  q.rem = q.n % 256;
+  q.a = (q.c + kBlk - 1) / kBlk;
+  q.head = q.n == 0 ? 0 : units_cost(q.a, q.full) + (q.rem ? kCostUnit + (q.rem > 128 ? kCost2 : kCost1) * static_cast<int64_t>(tail_blocks(q)) : 0);
+  return q;
+}
+
+// Where a CTA's part of the line begins: the request, head of the group and unit, and
+// the unit's place on the line.
+struct __align__(16) PrePart {
+  int64_t total, base, x0, x1;   // of the line; the unit's; the part
+  int32_t req, hg, u;            // req -1: the CTA has no part
+  PreReq q;
+};
+
+// Works out where the parts w0, w0 + step, ... of W_max begin: by 128 threads (warps
+// from `warp0` on), each for the parts that begin in its requests.  sums: 8 numbers.
+__device__ __forceinline__ void line_parts(const PreParams &p, PrePart *parts, int W_max, int w0, int step, int warp0, int64_t *sums) {
+  const int tid = threadIdx.x - 32 * warp0, per = (p.n_reqs + 127) / 128;
+  const int r_lo = min(p.n_reqs, tid * per), r_hi = min(p.n_reqs, r_lo + per);
+  bool bad;
+  int64_t mine = 0, total;
+  for (int r = r_lo; r < r_hi; ++r) mine += key_blocks(load_req(p.qo_indptr, p.kv_len, p.bt_indptr, r), p.T, &bad);
+  const int64_t blk0 = warps_scan<4, 1>(mine, tid >> 5, sums, &total);
+  int64_t at = blk0;
+  mine = 0;
+  for (int r = r_lo; r < r_hi; ++r) {
+    const ReqWords w = load_req(p.qo_indptr, p.kv_len, p.bt_indptr, r);
+    mine += pre_req(p, w, at).head * p.HG;
+    at += key_blocks(w, p.T, &bad);
+  }
+  const int64_t pre = warps_scan<4, 1>(mine, tid >> 5, sums + 4, &total);
+  const int64_t W = min(max(total / kMinShare, static_cast<int64_t>(total > 0)), static_cast<int64_t>(W_max));
+  for (int w = w0; w < W_max; w += step) {
+    if (w >= W) {
+      if (tid == 0) parts[w].req = -1;
+      continue;
+    }
+    PrePart o;
+    o.total = total;
+    o.x0 = div64(total * w, W);
+    o.x1 = div64(total * (w + 1), W);
+    if (o.x0 < pre || o.x0 >= pre + mine) continue;
+    o.base = pre;
+    o.req = r_lo;
+    at = blk0;
+    for (;; ++o.req) {
+      const ReqWords q = load_req(p.qo_indptr, p.kv_len, p.bt_indptr, o.req);
+      o.q = pre_req(p, q, at);
+      if (o.x0 < o.base + o.q.head * p.HG) break;
+      o.base += o.q.head * p.HG;
+      at += key_blocks(q, p.T, &bad);
+    }
+    o.hg = static_cast<int>(div64(o.x0 - o.base, o.q.head));
+    o.base += o.hg * o.q.head;
+    int lo = 0, hi = o.q.full + (o.q.rem ? 1 : 0);   // the unit that x0 lies in: the last one that does not begin behind it
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (units_cost(o.q.a, mid) <= o.x0 - o.base) lo = mid;
+      else hi = mid;
+    }
+    o.u = lo;
+    o.base += units_cost(o.q.a, lo);
+    parts[w] = o;
+  }
+}
+
+// ------------------------------------------------------------------ expand
 // ------------------------------------------------------------------ expand
 // Over pairs of CTAs (cta_group::2): each has its own 128 cached rows as its half
 // of A and of the accumulators, and half of a head's weights as its half of B, so
 // a CTA takes in 32 bytes of weights a cycle instead of 64 (a CTA by itself took
-// three times as long: two stages of 32 KB did not cover a load's latency).
+// three times as long: two stages of 32 KB did not cover a load's latency).  Four
+// more warps meanwhile work out where the parts of the next kernel's CTAs begin.
 template <int HD, int RANK>
 struct ExpCfg {
   static constexpr int NC = RANK / 64 + 1;
@@ -119,7 +213,7 @@ struct ExpCfg {
   static constexpr int OFF_B = A_BYTES;
   static constexpr int OFF_CTRL = OFF_B + NB * B_STAGE;
   static constexpr int SMEM = OFF_CTRL + 512;
-  static constexpr int THREADS = 192;                 // TMA, MMA, 4 epilogue warps
+  static constexpr int WARPS = 6, THREADS = 320;      // TMA, MMA, 4 epilogue warps; and 4 for the schedule
   static constexpr uint32_t IDESC = idesc_bf16(256, N, false);
 };
 
@@ -128,7 +222,7 @@ struct ExpCtrl {
   using C = ExpCfg<HD, RANK>;
   uint64_t a_full, a_peer, a_empty;   // this CTA's rows; the other's (in rank 0); both CTAs' products with them done
   uint64_t b_full[C::NB], b_empty[C::NB], t_full[2], t_empty[2], done;   // b_full, t_empty: rank 0's count for both
-  int64_t sums[C::THREADS / 32];
+  int64_t sums[C::WARPS], line_sums[8];
   int64_t start_base;
   int32_t start_req;
   uint32_t tmem;
@@ -162,7 +256,10 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   if (smem_u32(smem) & 1023u) {   // the swizzled layouts need a 1024-aligned base (the same in both CTAs)
     pdl_wait();
-    if (threadIdx.x == 0) atomicExch(p.err, kErrBounds);
+    if (threadIdx.x == 0) {
+      atomicExch(p.err, kErrBounds);
+      for (int w = blockIdx.x; w < p.ctas; w += gridDim.x) p.parts[w].req = -1;
+    }
     return;
   }
   if (threadIdx.x == 0) {
@@ -200,16 +297,18 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
   }
 
   // ---- this pair's items: (two blocks of 128 keys, head), heads fastest
-  const int per = (p.n_reqs + C::THREADS - 1) / C::THREADS;
-  const int r_lo = min(p.n_reqs, static_cast<int>(threadIdx.x) * per), r_hi = min(p.n_reqs, r_lo + per);
-  int64_t mine = 0, total;
+  constexpr int SCAN = 32 * C::WARPS;
+  const int per = (p.n_reqs + SCAN - 1) / SCAN;
+  const int r_lo = warp < C::WARPS ? min(p.n_reqs, static_cast<int>(threadIdx.x) * per) : 0;
+  const int r_hi = warp < C::WARPS ? min(p.n_reqs, r_lo + per) : 0;
+  int64_t mine = 0, total = 0, pre = 0;
   for (int r = r_lo; r < r_hi; ++r) {
     bool bad;
     mine += key_blocks(load_req(p.qo_indptr, p.kv_len, p.bt_indptr, r), p.T, &bad);
     if (bad && blockIdx.x == 0) atomicExch(p.err, kErrBounds);
   }
+  if (warp < C::WARPS) pre = warps_scan<C::WARPS, 2>(mine, warp, ct.sums, &total);
   tc_fence_before();
-  int64_t pre = cta_scan<C::THREADS / 32>(mine, ct.sums, &total);
   cluster_sync();   // (both CTAs' barriers are set up, and TMEM's address is there)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ct.tmem, 0);
@@ -235,7 +334,7 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
       pre += b;
     }
   }
-  __syncthreads();
+  if (warp < C::WARPS) named_bar_sync(2, SCAN);
   // Walks this CTA's blocks: the request of a block and where it starts.
   struct Walk {
     int r;
@@ -262,7 +361,9 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
   };
   const int hg0 = static_cast<int>(x0 - p0 * p.HG);
 
-  if (!active) {
+  if (warp >= C::WARPS) {
+    line_parts(p, p.parts, p.ctas, blockIdx.x, gridDim.x, C::WARPS, ct.line_sums);
+  } else if (!active) {
   } else if (warp == 0) {
     // -------------------------------------------------------- TMA producer
     Walk k = start();
@@ -484,12 +585,6 @@ struct PreSeg {
   int32_t slot, qb;      // partial slot, -1: the unit is whole; Q buffer of tile 0 (tile 1: the other one)
 };
 
-struct PreReq {
-  int t0, n, c, row_blk;   // first row of q, tokens, cached tokens, first block of the workspace
-  int full, rem, a;        // units of 256 rows, rows of the last one if it is smaller, blocks of the cached tokens
-  int64_t head;            // cost of one head
-};
-
 template <int HD>
 struct PreCtrl {
   using C = PreCfg<HD>;
@@ -502,35 +597,9 @@ struct PreCtrl {
   uint64_t turn[2];       // the other group's products are issued
   uint64_t done;
   PreSeg seg[C::NSEG];
-  int64_t sums[C::THREADS / 32];
-  int64_t start_base;
-  PreReq start;
-  int32_t start_req;
   uint32_t tmem;
   int abort;
 };
-
-// Cost of the first u units of 256 rows of a request and head: unit k has a +
-// 2 (k + 1) blocks.
-__device__ __forceinline__ int64_t units_cost(int a, int64_t u) {
-  return u * (kCostUnit + static_cast<int64_t>(kCost2) * a) + kCost2 * u * (u + 1);
-}
-__device__ __forceinline__ int tail_blocks(const PreReq &q) { return (q.c + q.n + kBlk - 1) / kBlk; }
-
-__device__ __forceinline__ PreReq pre_req(const PreParams &p, const ReqWords &w, int64_t row_blk) {
-  PreReq q;
-  bool bad;
-  const int blocks = key_blocks(w, p.T, &bad);
-  q.t0 = w.q0;
-  q.n = blocks > 0 && row_blk + blocks <= p.cap_blocks ? w.q1 - w.q0 : 0;
-  q.c = w.kv - q.n;
-  q.row_blk = static_cast<int>(row_blk);
-  q.full = q.n / 256;
-  q.rem = q.n % 256;
-  q.a = (q.c + kBlk - 1) / kBlk;
-  q.head = q.n == 0 ? 0 : units_cost(q.a, q.full) + (q.rem ? kCostUnit + (q.rem > 128 ? kCost2 : kCost1) * static_cast<int64_t>(tail_blocks(q)) : 0);
-  return q;
-}
 
 // Takes the keys behind `vis` out of a row's block of S (to -inf, in TMEM): a
 // pass of its own, for the few blocks on the diagonal.
@@ -591,7 +660,6 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
     for (int b = 0; b < 2; ++b) mbar_init(&ct.turn[b], 1);
     mbar_init(&ct.done, 2);
     ct.abort = 0;
-    ct.start_req = -1;
     fence_mbar_init();
     prefetch_tmap(&tmQ);
     prefetch_tmap(&tmQR);
@@ -602,84 +670,35 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
     tmem_alloc(&ct.tmem, C::TMEM_COLS);
     tmem_relinquish();
   }
-  pdl_wait();   // the descriptor, queries, expanded keys and outputs belong to earlier kernels of the stream
-  pdl_trigger();
-
-  // ---- this CTA's part of the line: [x0, x1) of `total`
-  const int W_max = gridDim.x, cta = blockIdx.x;
-  const int per = (p.n_reqs + C::THREADS - 1) / C::THREADS;
-  const int r_lo = min(p.n_reqs, static_cast<int>(threadIdx.x) * per), r_hi = min(p.n_reqs, r_lo + per);
-  int64_t mine = 0, total;
-  for (int r = r_lo; r < r_hi; ++r) {
-    bool bad;
-    mine += key_blocks(load_req(p.qo_indptr, p.kv_len, p.bt_indptr, r), p.T, &bad);
-  }
   tc_fence_before();
-  const int64_t blk0 = cta_scan<C::THREADS / 32>(mine, ct.sums, &total);   // (synchronises: TMEM's address is there)
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ct.tmem, 0);
-  auto next_blk = [&](const ReqWords &w, int64_t at) {
-    bool bad;
-    return at + key_blocks(w, p.T, &bad);
-  };
-  int64_t at = blk0;
-  mine = 0;
-  for (int r = r_lo; r < r_hi; ++r) {
-    const ReqWords w = load_req(p.qo_indptr, p.kv_len, p.bt_indptr, r);
-    mine += pre_req(p, w, at).head * p.HG;
-    at = next_blk(w, at);
-  }
-  int64_t pre = cta_scan<C::THREADS / 32>(mine, ct.sums, &total);
-  const int64_t W = total / kMinShare < 1 ? (total > 0 ? 1 : 0) : (total / kMinShare < W_max ? total / kMinShare : W_max);
-  const bool active = cta < W;
-  const int64_t x0 = active ? div64(total * cta, W) : 0, x1 = active ? div64(total * (cta + 1), W) : 0;
-  if (active && pre <= x0 && x0 < pre + mine) {
-    at = blk0;
-    for (int r = r_lo; r < r_hi; ++r) {
-      const ReqWords w = load_req(p.qo_indptr, p.kv_len, p.bt_indptr, r);
-      const PreReq q = pre_req(p, w, at);
-      if (x0 < pre + q.head * p.HG) {
-        ct.start_req = r;
-        ct.start = q;
-        ct.start_base = pre;
-        break;
-      }
-      pre += q.head * p.HG;
-      at = next_blk(w, at);
-    }
-  }
-  __syncthreads();
+  const int cta = blockIdx.x;
 
-  if (!active) {
-    if (threadIdx.x == 0) p.rec[cta * 8] = 0;
-  } else if (warp == 0) {
+  if (warp == 0) {
     // ------------------------------------------------ schedule, TMA producer
+    // (Only this thread waits for the kernel before: the other roles read what its
+    // copies bring and what it tells them.)
     if (lane == 0) {
-      int32_t rec[5] = {0, 0, 0, 0, 0};
-      int r = ct.start_req;
-      int64_t base = ct.start_base;
-      PreReq q = ct.start;
-      ReqWords w = load_req(p.qo_indptr, p.kv_len, p.bt_indptr, r);
-      int hg = static_cast<int>(div64(x0 - base, q.head));
-      base += hg * q.head;
-      int u = 0;   // the unit that x0 lies in: the last one whose start is not behind it
-      {
-        int lo = 0, hi = q.full + (q.rem ? 1 : 0);
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (units_cost(q.a, mid) <= x0 - base) lo = mid;
-          else hi = mid;
-        }
-        u = lo;
-        base += units_cost(q.a, u);
-      }
+      pdl_wait();
+      pdl_trigger();
+      const PrePart part = p.parts[cta];
+      int32_t rec[4] = {0, 0, 0, 0};
+      int r = part.req, hg = part.hg, u = part.u;
+      PreReq q = part.q;
+      const int64_t total = part.total, x0 = part.x0, x1 = r >= 0 ? part.x1 : 0;
+      const int64_t W = min(max(total / kMinShare, static_cast<int64_t>(total > 0)), static_cast<int64_t>(p.ctas));
+      int64_t base = r >= 0 ? part.base : 0;
+      ReqWords w{};
+      if (r >= 0) w = load_req(p.qo_indptr, p.kv_len, p.bt_indptr, r);
       int blk = 0, nseg = 0, quse[2] = {0, 0}, qsel = 0;
       bool ok = true, k_sent = false;
       auto freed = [&](uint64_t *empty, int b) {   // block b (if there is one) of a kind has been used
         return b < 0 || mbar_wait(&empty[b % C::NB], (b / C::NB) & 1, abort_flag, p.err, kErrWaitProducer);
       };
       // 128 x 64 parts of keys or values: columns x .. x + 63 of row y of `map` to place u of the ring
-      auto part = [&](int u, const CUtensorMap *map, uint64_t *full, int x, int y) {
+      auto tile = [&](int u, const CUtensorMap *map, uint64_t *full, int x, int y) {
         tma_load_2d(sR + (u % C::NU) * C::UNIT, map, full, x, y);
       };
       while (ok && base < x1) {
@@ -698,7 +717,7 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
         };
         const int j0 = cut(x0), j1 = cut(x1);
         if (j1 > j0) {
-          const int first = owner(0), last = owner(nkb - 1), i0 = 256 * u, h = p.h0 + hg;
+          const int i0 = 256 * u, h = p.h0 + hg;
           const int krow = (hg * p.cap_blocks + q.row_blk) * kBlk, rrow = q.row_blk * kBlk;
           for (int t = 0; t < qt && ok; ++t) {
             const int qb = qsel ^ t;
@@ -710,6 +729,25 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
             tma_load_3d(sQ + qb * C::QT_BYTES + (C::KU - 1) * C::UNIT, &tmQR, &ct.q_full[qb], 0, h, q.t0 + i0 + 128 * t);
             ++quse[qb];
           }
+          auto send = [&](int j) {   // block j
+            const int u0 = blk * (C::KU + C::VU), sb = blk % C::NB;
+            ok = freed(ct.k_empty, blk - C::KB) && freed(ct.v_empty, blk - C::VB);
+            if (!ok) return;
+            mbar_arrive_expect_tx(&ct.k_full[sb], C::KU * C::UNIT);
+            for (int ch = 0; ch < C::KU - 1; ++ch) tile(u0 + ch, &tmKV, &ct.k_full[sb], 64 * ch, krow + kBlk * j);
+            tile(u0 + C::KU - 1, &tmR, &ct.k_full[sb], 0, rrow + kBlk * j);
+            k_sent = true;
+            ok = freed(ct.k_empty, blk - C::VK);
+            if (!ok) return;
+            mbar_arrive_expect_tx(&ct.v_full[sb], C::VU * C::UNIT);
+            for (int ch = 0; ch < C::VU; ++ch) tile(u0 + C::KU + ch, &tmKV, &ct.v_full[sb], HD + 64 * ch, krow + kBlk * j);
+            ++blk;
+            k_sent = false;
+          };
+          if (!ok) break;
+          int j = j0;
+          if (blk == 0) send(j++);   // (nothing to wait for: on its way before the books are kept)
+          const int first = owner(0), last = owner(nkb - 1);
           const int ss = nseg % C::NSEG;
           ok = ok && mbar_wait(&ct.seg_empty[ss], ((nseg / C::NSEG) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer);
           if (!ok) break;
@@ -732,20 +770,7 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
             rec[3] = rows;
           }
           if (qt == 1) qsel ^= 1;
-          for (int j = j0; j < j1 && ok; ++j, ++blk) {
-            const int u0 = blk * (C::KU + C::VU), sb = blk % C::NB;
-            k_sent = false;
-            ok = freed(ct.k_empty, blk - C::KB) && freed(ct.v_empty, blk - C::VB);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&ct.k_full[sb], C::KU * C::UNIT);
-            for (int ch = 0; ch < C::KU - 1; ++ch) part(u0 + ch, &tmKV, &ct.k_full[sb], 64 * ch, krow + kBlk * j);
-            part(u0 + C::KU - 1, &tmR, &ct.k_full[sb], 0, rrow + kBlk * j);
-            k_sent = true;
-            ok = freed(ct.k_empty, blk - C::VK);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&ct.v_full[sb], C::VU * C::UNIT);
-            for (int ch = 0; ch < C::VU; ++ch) part(u0 + C::KU + ch, &tmKV, &ct.v_full[sb], HD + 64 * ch, krow + kBlk * j);
-          }
+          while (ok && j < j1) send(j++);
         }
         // the next unit on the line
         base += cost;
@@ -753,12 +778,13 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
           u = 0;
           if (++hg == p.HG) {
             hg = 0;
-            int64_t blk = q.row_blk;
+            int64_t row_blk = q.row_blk;
             do {
-              blk = next_blk(w, blk);
+              bool bad;
+              row_blk += key_blocks(w, p.T, &bad);
               if (++r >= p.n_reqs) break;
               w = load_req(p.qo_indptr, p.kv_len, p.bt_indptr, r);
-              q = pre_req(p, w, blk);
+              q = pre_req(p, w, row_blk);
             } while (q.n == 0);
             if (r >= p.n_reqs) break;
           }
@@ -1223,7 +1249,7 @@ cudaError_t launch_prefill(const LatentArgs &a, PreParams &p, int group, __nv_bf
   if (e == cudaSuccess) e = encode_tmap_5d(&tk, a.pool, dk, sk, bk);
   if (e == cudaSuccess) e = encode_tmap_2d(&tw, a.w_kv, a.rank, H * 2 * HD, static_cast<uint64_t>(a.rank) * 2, 64, HD);
   if (e == cudaSuccess) e = ensure_max_smem(reinterpret_cast<const void *>(latent_prefill_kernel<HD>), C::SMEM);
-  const int ctas = std::min(device_sm_count(), kMaxCtas);
+  const int ctas = p.ctas;
   for (p.h0 = 0; p.h0 < a.H && e == cudaSuccess; p.h0 += group) {
     p.HG = std::min(group, a.H - p.h0);
     e = a.rank == 512 ? launch_expand<HD, 512>(tk, tw, ts, p, st) : launch_expand<HD, 256>(tk, tw, ts, p, st);
@@ -1235,12 +1261,12 @@ cudaError_t launch_prefill(const LatentArgs &a, PreParams &p, int group, __nv_bf
 
 }  // namespace
 
-// a group's keys and values, the rotated keys, the records, the partials
+// a group's keys and values, the rotated keys, the records and parts, the partials
 size_t latent_prefill_workspace_bytes(int64_t kv_tokens, int64_t n_reqs, int64_t H, int64_t hd, int64_t rank) {
   (void)rank;
   const int64_t blocks = cap_blocks(kv_tokens, n_reqs);
   return align256(static_cast<size_t>(blocks) * kBlk * 4 * hd * group_heads(blocks, H, hd)) +
-         align256(static_cast<size_t>(blocks) * kBlk * kLatentRope * 2) + kRecBytes +
+         align256(static_cast<size_t>(blocks) * kBlk * kLatentRope * 2) + kRecBytes + kPartsBytes +
          static_cast<size_t>(2) * kMaxCtas * part_floats(hd) * sizeof(float);
 }
 
@@ -1267,7 +1293,10 @@ cudaError_t latent_prefill_run(const LatentArgs &a, cudaStream_t st) {
   p.cap_blocks = static_cast<int>(blocks);
   p.scale_log2 = a.scale * kLog2e;
   p.rec = reinterpret_cast<int32_t *>(w + kv_bytes + rope_bytes);
-  p.part = reinterpret_cast<float *>(w + kv_bytes + rope_bytes + kRecBytes);
+  static_assert(kMaxCtas * 32 <= kRecBytes && kMaxCtas * sizeof(PrePart) <= kPartsBytes, "workspace");
+  p.parts = reinterpret_cast<PrePart *>(w + kv_bytes + rope_bytes + kRecBytes);
+  p.ctas = std::min(device_sm_count(), kMaxCtas);
+  p.part = reinterpret_cast<float *>(w + kv_bytes + rope_bytes + kRecBytes + kPartsBytes);
   p.err = a.err;
   __nv_bfloat16 *rope = reinterpret_cast<__nv_bfloat16 *>(w + kv_bytes);
   return a.hd == 128 ? launch_prefill<128>(a, p, group, rope, st) : launch_prefill<64>(a, p, group, rope, st);
