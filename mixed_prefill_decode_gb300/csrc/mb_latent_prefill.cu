@@ -286,14 +286,20 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
     tmem_alloc_pair(&ct.tmem, 512);
     tmem_relinquish_pair();
   }
+  tc_fence_before();
+  cluster_sync();   // (both CTAs' barriers are set up, and TMEM's address is there)
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ct.tmem, 0);
   pdl_wait();   // descriptor, cache, weights and workspace belong to earlier kernels of the stream
   pdl_trigger();
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 32 * C::WARPS) {
     // The group's weights on their way to L2, a part by each CTA: all pairs ask
     // for the same chunk at about the same time, and each would wait for HBM.
-    const int64_t bytes = static_cast<int64_t>(p.HG) * 2 * HD * RANK * 2, part = (bytes / gridDim.x + 127) / 128 * 128;
-    const int64_t from = part * blockIdx.x, n = min(part, bytes - from);
-    if (n > 0) l2_prefetch(reinterpret_cast<const uint8_t *>(p.w_kv + static_cast<int64_t>(p.h0) * 2 * HD * RANK) + from, static_cast<uint32_t>(n));
+    const uint32_t lines = static_cast<uint32_t>(p.HG) * (2 * HD * RANK * 2 / 128), part = (lines + gridDim.x - 1) / gridDim.x;
+    const uint32_t from = part * blockIdx.x;
+    if (from < lines)
+      l2_prefetch(reinterpret_cast<const uint8_t *>(p.w_kv + static_cast<int64_t>(p.h0) * 2 * HD * RANK) + from * 128ll,
+                  min(part, lines - from) * 128);
   }
 
   // ---- this pair's items: (two blocks of 128 keys, head), heads fastest
@@ -308,10 +314,6 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
     if (bad && blockIdx.x == 0) atomicExch(p.err, kErrBounds);
   }
   if (warp < C::WARPS) pre = warps_scan<C::WARPS, 2>(mine, warp, ct.sums, &total);
-  tc_fence_before();
-  cluster_sync();   // (both CTAs' barriers are set up, and TMEM's address is there)
-  tc_fence_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, ct.tmem, 0);
   if (total > p.cap_blocks) {
     // the caller's room is too small for the requests behind: they are left alone
     if (threadIdx.x == 0 && blockIdx.x == 0) atomicExch(p.err, kErrBounds);
