@@ -235,6 +235,37 @@ __device__ __forceinline__ void store32(void *dst, const uint32_t *v) {   // 32 
                : "memory");
 }
 
+// The pair's form of a 5D tile load: counted on an mbarrier of either CTA.
+__device__ __forceinline__ void tma_load_5d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int32_t x0, int32_t x4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %4, %4, %5}], "
+      "[%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(bar), "r"(x0), "r"(0), "r"(x4)
+      : "memory");
+}
+
+// 64 fp32 columns of 16 TMEM lanes (16x256b shape, x8), waited on before returning:
+// thread t gets columns 8 i + 2 (t % 4) and the next one of lane t / 4 in v[0][2 i]
+// and v[0][2 i + 1], of lane t / 4 + 8 in v[1].
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, float (&v)[2][16]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k >> 1][2 * i + (k & 1)] = __uint_as_float(r[4 * i + k]);
+}
+
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int32_t x, int32_t y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map), "r"(smem_u32(src)),
                "r"(x), "r"(y)
@@ -404,8 +435,8 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
           ok = mbar_wait(&ct.b_empty[st], ((bcnt / C::NB) & 1) ^ 1, abort_flag, p.err, kErrWaitProducer);
           if (ok) {
             if (rank == 0) mbar_arrive_expect_tx(&ct.b_full[st], 2 * C::B_STAGE);
-            tma_load_2d_pair(sB + st * C::B_STAGE, &tmW, mapa_shared(smem_u32(&ct.b_full[st]), 0), 64 * c,
-                             (p.h0 + hg) * 2 * HD + static_cast<int>(rank) * HD);
+            tma_load_5d_pair(sB + st * C::B_STAGE, &tmW, mapa_shared(smem_u32(&ct.b_full[st]), 0), 64 * c,
+                             ((p.h0 + hg) * 2 + static_cast<int>(rank)) * (HD / 64));
           }
           // (after the first weights, which go out while the rows are on their way)
           if (ok && !told && (c == C::NB - 1 || c == C::KC - 1)) {
@@ -481,10 +512,14 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
-    // One thread per key.  A value that is not finite would reach, times a
+    // Four threads per key, 16 of each 64 numbers a thread: the weights' rows are
+    // loaded in the order that makes them neighbours (row 8 i + 2 q + e of 64 is
+    // 16 q + 2 i + e), so a key's 128 bytes go out together.  (One thread per key
+    // stored single sectors, 2,048 an item, which took 2.2 us and kept the weights'
+    // loads waiting: 4.4 us an item.)  A value that is not finite would reach, times a
     // probability of 0, tokens that do not see the key: such a value row is
     // stored as zeros and the key as NaN, which the tokens that do see it get.
-    const int qu = warp & 3, row = qu * 32 + lane;
+    const int qu = warp & 3, quad = lane & 3;
     const uint32_t lane_base = static_cast<uint32_t>(qu * 32) << 16;
     Walk k = start();
     int64_t blk = 2 * p0 + rank;
@@ -496,42 +531,56 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
       if (__any_sync(0xffffffffu, fail)) break;   // tcgen05.ld below is warp-collective
       tc_fence_after();
       if (blk < total) {
-        const bool stale = static_cast<int>(blk - k.base) * kBlk + row >= k.w.kv;
-        const uint32_t t = tmem + lane_base + 256 * (acc & 1);
-        uint8_t *dst = reinterpret_cast<uint8_t *>(p.kv + ((static_cast<int64_t>(hg) * p.cap_blocks + blk) * kBlk + row) * (2 * HD));
-        uint32_t pk[HD / 2];
-        float odd = 0.f;   // NaN if a value is not finite
+        const int key0 = static_cast<int>(blk - k.base) * kBlk;
+        uint8_t *kv = reinterpret_cast<uint8_t *>(p.kv + (static_cast<int64_t>(hg) * p.cap_blocks + blk) * kBlk * (2 * HD));
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {   // 16 keys of the warp's 32: a thread has keys row and row + 8
+          const uint32_t t = tmem + lane_base + (static_cast<uint32_t>(half * 16) << 16) + 256 * (acc & 1);
+          const int row = qu * 32 + half * 16 + (lane >> 2);
+          uint8_t *dst = kv + row * (4 * HD) + 32 * quad;
+          uint32_t pk[2][HD / 8];
+          float odd[2] = {0.f, 0.f};   // NaN if a value is not finite
+          bool stale[2], wipe[2];
 #pragma unroll
-        for (int cc = 0; cc < HD / 32; ++cc) {
-          float v[32];
-          tmem_ld32(t + HD + 32 * cc, v);
+          for (int b = 0; b < HD / 64; ++b) {
+            float v[2][16];
+            tmem_ld_rows(t + HD + 64 * b, v);
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            pk[16 * cc + e / 2] = pack_bf16x2(v[e], v[e + 1]);
-            odd = fmaf(bf16lo(pk[16 * cc + e / 2]), 0.f, odd);
-            odd = fmaf(bf16hi(pk[16 * cc + e / 2]), 0.f, odd);
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const uint32_t x = pack_bf16x2(v[r][2 * e], v[r][2 * e + 1]);
+                pk[r][8 * b + e] = x;
+                odd[r] = fmaf(bf16lo(x), 0.f, odd[r]);
+                odd[r] = fmaf(bf16hi(x), 0.f, odd[r]);
+              }
           }
-        }
-        const bool wipe = stale || odd != 0.f;
 #pragma unroll
-        for (int e = 0; e < HD / 2; e += 8) {
-          if (wipe)
+          for (int r = 0; r < 2; ++r) {
+            odd[r] += __shfl_xor_sync(0xffffffffu, odd[r], 1);
+            odd[r] += __shfl_xor_sync(0xffffffffu, odd[r], 2);
+            stale[r] = key0 + row + 8 * r >= k.w.kv;
+            wipe[r] = stale[r] || odd[r] != 0.f;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) pk[e + x] = 0;
-          store32(dst + 2 * HD + 4 * e, pk + e);
-        }
+            for (int b = 0; b < HD / 64; ++b) {
+              if (wipe[r])
 #pragma unroll
-        for (int cc = 0; cc < HD / 32; ++cc) {
-          float v[32];
-          tmem_ld32(t + 32 * cc, v);
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            uint32_t x = pack_bf16x2(v[e], v[e + 1]);
-            if (wipe) x = stale ? 0u : 0x7FC07FC0u;
-            pk[e / 2] = x;
+                for (int e = 0; e < 8; ++e) pk[r][8 * b + e] = 0;
+              store32(dst + r * 8 * (4 * HD) + 2 * HD + 128 * b, pk[r] + 8 * b);
+            }
           }
-          store32(dst + 64 * cc, pk);
-          store32(dst + 64 * cc + 32, pk + 8);
+#pragma unroll
+          for (int b = 0; b < HD / 64; ++b) {
+            float v[2][16];
+            tmem_ld_rows(t + 64 * b, v);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              uint32_t x[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] = wipe[r] ? (stale[r] ? 0u : 0x7FC07FC0u) : pack_bf16x2(v[r][2 * e], v[r][2 * e + 1]);
+              store32(dst + r * 8 * (4 * HD) + 128 * b, x);
+            }
+          }
         }
       }
       tc_fence_before();
@@ -1249,7 +1298,10 @@ cudaError_t launch_prefill(const LatentArgs &a, PreParams &p, int group, __nv_bf
   if (e == cudaSuccess) e = encode_tmap_2d(&tr, rope, kLatentRope, rows, kLatentRope * 2, 64, kBlk);
   if (e == cudaSuccess) e = encode_tmap_2d(&ts, rope, kLatentRope, rows, kLatentRope * 2, 64, 8);
   if (e == cudaSuccess) e = encode_tmap_5d(&tk, a.pool, dk, sk, bk);
-  if (e == cudaSuccess) e = encode_tmap_2d(&tw, a.w_kv, a.rank, H * 2 * HD, static_cast<uint64_t>(a.rank) * 2, 64, HD);
+  // the weights' rows, 64 at a time, in the order in which the expansion stores what they make
+  const uint64_t R = a.rank, dw[5] = {R, 2, 4, 8, H * 2 * HD / 64}, sw[4] = {R * 2, 16 * R * 2, 2 * R * 2, 64 * R * 2};
+  const uint32_t bw[5] = {64, 2, 4, 8, HD / 64};
+  if (e == cudaSuccess) e = encode_tmap_5d(&tw, a.w_kv, dw, sw, bw);
   if (e == cudaSuccess) e = ensure_max_smem(reinterpret_cast<const void *>(latent_prefill_kernel<HD>), C::SMEM);
   const int ctas = p.ctas;
   for (p.h0 = 0; p.h0 < a.H && e == cudaSuccess; p.h0 += group) {
