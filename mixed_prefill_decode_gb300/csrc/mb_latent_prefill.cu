@@ -475,10 +475,14 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
-    if (rank == 0 && lane == 0) {
+    // (the warp keeps the books, in step, and one elected lane issues: the
+    // descriptors stay in uniform registers)
+    if (rank == 0) {
       const uint64_t ad0 = sdesc_sw128(smem_u32(sA), 16, C::ATOM);
       const uint64_t bd0 = sdesc_sw128(smem_u32(sB), 16, 1024);
-      auto wait = [&](uint64_t *bar, uint32_t par) { return mbar_wait(bar, par, abort_flag, p.err, kErrWaitMma); };
+      auto wait = [&](uint64_t *bar, uint32_t par) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag, p.err, kErrWaitMma)) != 0;
+      };
       int ause = 0, bcnt = 0, acc = 0, hg = hg0;
       bool ok = true;
       for (int64_t i = x0; i < x1 && ok; ++i, ++acc) {
@@ -487,26 +491,31 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
           ++ause;
         }
         ok = ok && wait(&ct.t_empty[acc & 1], ((acc >> 1) & 1) ^ 1);
-        for (int c = 0; c < C::KC && ok; ++c, ++bcnt) {
+        const bool last = ++hg == p.HG;
+        if (last) hg = 0;
+        const uint32_t d = tmem + 256 * (acc & 1);
+#pragma unroll
+        for (int c = 0; c < C::KC; ++c, ++bcnt) {
           const int st = bcnt % C::NB;
-          ok = wait(&ct.b_full[st], (bcnt / C::NB) & 1);
+          ok = ok && wait(&ct.b_full[st], (bcnt / C::NB) & 1);
           if (!ok) break;
           tc_fence_after();
+          const uint64_t bd = bd0 + static_cast<uint64_t>((st * C::B_STAGE) >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_bf16_pair(tmem + 256 * (acc & 1), ad0 + ((c * 1024 + kk * 32) >> 4), bd0 + ((st * C::B_STAGE + kk * 32) >> 4),
-                          C::IDESC, (c > 0 || kk > 0) ? 1u : 0u);
-          mma_commit_pair(&ct.b_empty[st], 3);
-        }
-        if (!ok) break;
-        mma_commit_pair(&ct.t_full[acc & 1], 3);
-        if (++hg == p.HG) {
-          hg = 0;
-          mma_commit_pair(&ct.a_empty, 3);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16_pair(d, ad0 + ((c * 1024 + kk * 32) >> 4), bd + ((kk * 32) >> 4), C::IDESC, (c > 0 || kk > 0) ? 1u : 0u);
+            mma_commit_pair(&ct.b_empty[st], 3);
+            if (c == C::KC - 1) {
+              mma_commit_pair(&ct.t_full[acc & 1], 3);
+              if (last) mma_commit_pair(&ct.a_empty, 3);
+            }
+          }
+          __syncwarp();
         }
       }
       // every MMA issued above has completed before TMEM is freed
-      mma_commit_pair(&ct.done, 1);
+      if (elect_one()) mma_commit_pair(&ct.done, 1);
       drain(&ct.done, 0, globaltimer());
     }
     __syncwarp();
