@@ -1262,11 +1262,12 @@ __global__ void __launch_bounds__(256) latent_prefill_merge_kernel(const __grid_
   }
   if (row >= rec.w) return;
   const float inv = 1.f / L;
-  uint4 *dst = reinterpret_cast<uint4 *>(p.o + (static_cast<int64_t>(rec.y + row) * p.H + rec.z) * HD + warp * COLS);
+  __nv_bfloat16 *dst = p.o + (static_cast<int64_t>(rec.y + row) * p.H + rec.z) * HD + warp * COLS;
+  uint32_t x[COLS / 2];
 #pragma unroll
-  for (int k = 0; k < COLS; k += 8)
-    dst[k / 8] = make_uint4(pack_bf16x2(acc[k] * inv, acc[k + 1] * inv), pack_bf16x2(acc[k + 2] * inv, acc[k + 3] * inv),
-                            pack_bf16x2(acc[k + 4] * inv, acc[k + 5] * inv), pack_bf16x2(acc[k + 6] * inv, acc[k + 7] * inv));
+  for (int k = 0; k < COLS / 2; ++k) x[k] = pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+  if constexpr (COLS == 16) store32(dst, x);   // a whole sector a lane
+  else *reinterpret_cast<uint4 *>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
 }
 
 // The workspace's keys: blocks of 128, each request's from a block of its own.
