@@ -11,7 +11,9 @@
 //
 // What bounds it: the tensor cores, and beside them the chain of product,
 // softmax, product.  Keys and values of a head are 4 hd bytes a token, written once
-// and read by every tile of queries.
+// and read by every tile of queries.  Measured, replayed in a graph: 2,048 tokens at
+// 8,192 keys, 40 heads of 128, rank 512 313 us, 1.47 PFLOP/s (expansion 57, attention
+// 240); 512 tokens of 32 heads 30 us: three launches and the chain of two blocks.
 //
 // Two kernels, and a merge (per group of heads, if all heads' keys and values would
 // take more than 512 MB):
@@ -26,8 +28,8 @@
 //  * merge: units cut by the schedule's borders, by log-sum-exp.
 //
 // The schedule: all units lie on one line, weighted by their blocks, and CTA w
-// of W takes the w-th of W equal parts, whatever the lengths; it is worked out
-// by every CTA from the device descriptor.
+// of W takes the w-th of W equal parts, whatever the lengths.  Warps of the
+// expansion that have nothing else to do work it out from the device descriptor.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -200,6 +202,8 @@ __device__ __forceinline__ void line_parts(const PreParams &p, PrePart *parts, i
 // a CTA takes in 32 bytes of weights a cycle instead of 64 (a CTA by itself took
 // three times as long: two stages of 32 KB did not cover a load's latency).  Four
 // more warps meanwhile work out where the parts of the next kernel's CTAs begin.
+// An item, 2 x 128 keys and a head of 128 at rank 512, takes 2.7 us (2.1 by the
+// products' cycles; 2.5 without its loads).
 template <int HD, int RANK>
 struct ExpCfg {
   static constexpr int NC = RANK / 64 + 1;
