@@ -1178,8 +1178,9 @@ cudaError_t latent_append_run(const LatentAppendArgs &a, cudaStream_t st) {
   p.rank = a.rank;
   p.eps = a.eps;
   p.err = a.err;
+  const double step = -std::log2(static_cast<double>(a.theta)) * 2 / kLatentRope;
   for (int i = 0; i < kRopeHalf; ++i) {
-    const double f = std::pow(static_cast<double>(a.theta), -2.0 * i / kLatentRope);
+    const double f = std::exp2(i * step);   // (good to 2^-46 at any theta)
     p.f_hi[i] = static_cast<float>(f);
     p.f_lo[i] = static_cast<float>(f - static_cast<double>(p.f_hi[i]));
   }
