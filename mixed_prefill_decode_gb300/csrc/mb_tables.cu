@@ -17,9 +17,9 @@
 // would cost what the whole call does.  What changes in place (page counts,
 // the ring's head) is written by the last CTA to have read it.
 //
-// Measured, replayed in a graph: 64 decodes at 1,125 keys 5.0 us, 256 decodes and
-// two chunks of 3,967 tokens (512 to 32,768 keys) 5.8 (10.7 and 12 with one load
-// waiting for the other, a scan for each sum and an element a thread at a time).
+// Measured, replayed in a graph: 64 decodes at 1,125 keys 5.0 us (10.7 with one load
+// waiting for the other, a scan for each sum and an element a thread at a time), 256
+// decodes and two chunks of 3,967 tokens (512 to 32,768 keys) 5.7.
 
 #include <cuda_runtime.h>
 
