@@ -147,22 +147,23 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const __g
 
 // ------------------------------------------------------------- the queries
 // qc[t][h][r] = sum_d q[t][h][d] W_uk,h[d][r] for every head, rounded to bf16 for
-// the product with the cached rows.  One CTA makes 128 tokens x 128 columns of
+// the product with the cached rows.  One CTA makes TOK tokens x 128 columns of
 // one head on tcgen05, A and B wholly in shared memory, one barrier per 64 of
-// hd.  Heads' weights are read once per 128 tokens: for few tokens they (and the
-// launch) are the time, for many the products.  64 tokens of 32 heads 2.3 us from
+// hd; the result leaves by TMA from where A was.  Heads' weights are read once per
+// TOK tokens: for few tokens they (and the launch) are the time, for many the
+// stores.  64 tokens of 32 heads 2.3 us from
 // the kernel before's end, 16 of 128 heads (16 MB of weights) 3.3 to 5.6.
 constexpr int kQueryN = 128;
 
-template <int HD>
+template <int HD, int TOK>
 struct QueryCfg {
   static constexpr int KC = HD / 64;
-  static constexpr int A_CHUNK = 128 * 128;
+  static constexpr int A_CHUNK = TOK * 128;
   static constexpr int B_PART = 64 * 128;            // 64 of hd x 64 columns
   static constexpr int OFF_B = KC * A_CHUNK;         // [64 columns][hd][128 B]: W_uk is stored [d][r]
   static constexpr int OFF_CTRL = OFF_B + KC * (kQueryN / 64) * B_PART;
   static constexpr int SMEM = OFF_CTRL + 256;
-  static constexpr uint32_t IDESC = idesc_bf16(128, kQueryN, true);
+  static constexpr uint32_t IDESC = idesc_bf16(TOK, kQueryN, true);
 };
 
 // What becomes of a token's row: its unit's pieces (0: no request's token, 1: oc
@@ -172,22 +173,21 @@ struct TokRec {
 };
 
 struct QueryParams {
-  __nv_bfloat16 *qc;
   TokRec *tok;
-  int T, H, rank;
+  int T;
   int *err;
 };
 
-template <int HD>
-__global__ void __launch_bounds__(128) latent_query_kernel(const __grid_constant__ CUtensorMap tmQ,
-                                                           const __grid_constant__ CUtensorMap tmW, const QueryParams p) {
-  using C = QueryCfg<HD>;
+template <int HD, int TOK>
+__global__ void __launch_bounds__(128) latent_query_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmW,
+                                                           const __grid_constant__ CUtensorMap tmO, const QueryParams p) {
+  using C = QueryCfg<HD, TOK>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_CTRL), *done = full + C::KC;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int tid = threadIdx.x, warp = tid >> 5;
-  const int n0 = blockIdx.x * kQueryN, h = blockIdx.y, t0 = blockIdx.z * 128, t = t0 + tid;
+  const int n0 = blockIdx.x * kQueryN, h = blockIdx.y, t0 = blockIdx.z * TOK;
   if (smem_u32(smem) & 1023u) {   // the swizzled layouts need a 1024-aligned base
     pdl_wait();
     if (tid == 0) atomicExch(p.err, kErrBounds);
@@ -239,25 +239,29 @@ __global__ void __launch_bounds__(128) latent_query_kernel(const __grid_constant
     }
   } else if (blockIdx.x == 0 && h == 0) {
     // (thread 0's row is thread 1's to clear)
-    if (t < p.T) p.tok[t].pieces = 0;
+    if (tid < TOK && t0 + tid < p.T) p.tok[t0 + tid].pieces = 0;
     if (tid == 1) p.tok[t0].pieces = 0;
   }
   __syncwarp();
   bool ok = mbar_wait(done, 0, abort_flag, p.err, kErrWaitEpilogue);
   ok = __all_sync(0xffffffffu, ok) && !*abort_flag;
-  if (ok && t0 + 32 * warp < p.T) {
+  if (ok) {
     tc_fence_after();
-    uint4 *dst = reinterpret_cast<uint4 *>(p.qc + (static_cast<int64_t>(t) * p.H + h) * p.rank + n0);
-#pragma unroll 1
+    // (with 64 tokens a quarter's rows are its first 16 lanes)
+    const int lane = tid & 31, row = TOK == 128 ? tid : 16 * warp + lane;
+    uint8_t *dst = smem + (row >> 3) * 1024 + (row & 7) * 128;   // [64 columns][tokens][128 B], swizzled
+#pragma unroll
     for (int cc = 0; cc < kQueryN / 32; ++cc) {
       float v[32];
       tmem_ld32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + cc * 32, v);
-      if (t < p.T)
+      if (TOK == 128 || lane < 16)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          dst[cc * 4 + k] = make_uint4(pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
-                                       pack_bf16x2(v[8 * k + 4], v[8 * k + 5]), pack_bf16x2(v[8 * k + 6], v[8 * k + 7]));
+          *reinterpret_cast<uint4 *>(dst + (cc >> 1) * (TOK * 128) + ((((cc & 1) * 4 + k) ^ (row & 7)) * 16)) =
+              make_uint4(pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
+                         pack_bf16x2(v[8 * k + 4], v[8 * k + 5]), pack_bf16x2(v[8 * k + 6], v[8 * k + 7]));
     }
+    fence_proxy_async_smem();
   }
   tc_fence_before();
   __syncthreads();
@@ -265,6 +269,11 @@ __global__ void __launch_bounds__(128) latent_query_kernel(const __grid_constant
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, kQueryN);
+    // (tokens behind T are none of the map's)
+    if (ok && tid == 0) {
+      for (int j = 0; j < kQueryN / 64; ++j) tma_store_3d(&tmO, smem + j * (TOK * 128), n0 + 64 * j, h, t0);
+      asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+    }
   }
 }
 
@@ -1095,18 +1104,25 @@ __global__ void __launch_bounds__(128, 1)
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-template <int HD>
-cudaError_t launch_query(const LatentArgs &a, const QueryParams &p, cudaStream_t st) {
-  using C = QueryCfg<HD>;
-  CUtensorMap tq, tw;
-  const uint64_t H = a.H, W = HD + kLatentRope;
-  const uint64_t dq[3] = {W, H, static_cast<uint64_t>(a.T)}, sq[2] = {W * 2, W * 2 * H};
-  const uint32_t bq[3] = {64, 1, 128};
-  cudaError_t e = encode_tmap(&tq, a.q, 3, dq, sq, bq);
-  if (e == cudaSuccess) e = encode_tmap_2d(&tw, a.w_kv, a.rank, H * 2 * HD, static_cast<uint64_t>(a.rank) * 2, 64, 64);
-  if (e == cudaSuccess) e = ensure_max_smem(reinterpret_cast<const void *>(latent_query_kernel<HD>), C::SMEM);
+template <int HD, int TOK>
+cudaError_t launch_query(const LatentArgs &a, void *qc, const QueryParams &p, cudaStream_t st) {
+  using C = QueryCfg<HD, TOK>;
+  static_assert(2 * TOK * 128 <= C::OFF_CTRL, "shared memory");
+  CUtensorMap tq, tw, to;
+  const uint64_t H = a.H, W = HD + kLatentRope, R = a.rank, T = a.T;
+  const uint64_t dq[3] = {W, H, T}, sq[2] = {W * 2, W * 2 * H}, dc[3] = {R, H, T}, sc[2] = {R * 2, R * 2 * H};
+  const uint32_t box[3] = {64, 1, TOK};
+  cudaError_t e = encode_tmap(&tq, a.q, 3, dq, sq, box);
+  if (e == cudaSuccess) e = encode_tmap(&to, qc, 3, dc, sc, box);
+  if (e == cudaSuccess) e = encode_tmap_2d(&tw, a.w_kv, R, H * 2 * HD, R * 2, 64, 64);
+  if (e == cudaSuccess) e = ensure_max_smem(reinterpret_cast<const void *>(latent_query_kernel<HD, TOK>), C::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl(latent_query_kernel<HD>, dim3(a.rank / kQueryN, a.H, (a.T + 127) / 128), dim3(128), C::SMEM, st, 1, tq, tw, p);
+  return launch_pdl(latent_query_kernel<HD, TOK>, dim3(a.rank / kQueryN, a.H, (a.T + TOK - 1) / TOK), dim3(128), C::SMEM, st, 1, tq, tw, to, p);
+}
+
+template <int HD>
+cudaError_t launch_query(const LatentArgs &a, void *qc, const QueryParams &p, cudaStream_t st) {
+  return a.T <= 64 ? launch_query<HD, 64>(a, qc, p, st) : launch_query<HD, 128>(a, qc, p, st);
 }
 
 template <int HD, int RANK, int TR>
@@ -1220,8 +1236,8 @@ cudaError_t latent_attention_run(const LatentArgs &a, cudaStream_t st) {
   p.tok = tok;
   p.part = reinterpret_cast<float *>(w + 2 * rows + align256(static_cast<size_t>(a.T) * sizeof(TokRec)));
   p.err = a.err;
-  const QueryParams qp = {qc, tok, a.T, a.H, a.rank, a.err};
-  cudaError_t e = a.hd == 128 ? launch_query<128>(a, qp, st) : launch_query<64>(a, qp, st);
+  const QueryParams qp = {tok, a.T, a.err};
+  cudaError_t e = a.hd == 128 ? launch_query<128>(a, qc, qp, st) : launch_query<64>(a, qc, qp, st);
   if (e == cudaSuccess) e = a.rank == 512 ? launch_attention<512>(a, p, qc, st) : launch_attention<256>(a, p, qc, st);
   if (e != cudaSuccess) return e;
   const OutParams op = {tok, static_cast<__nv_bfloat16 *>(a.o), a.T, a.H, a.err};
