@@ -992,19 +992,22 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const AbsParams p) {
 }
 
 // ------------------------------------------------------------- the outputs
-// o[t][h] = W_uv,h oc[t][h]: one CTA makes TR tokens of one head, as D = W_uv (M =
-// hd) times the tokens' rows (N = TR), K = rank, all of it in shared memory.
-// W_uv is loaded before the wait for the rows.  What bounds it is latency: 3 us from
-// the merge's end (the rows' copies 2), for 64 tokens as for 16.
+// o[t][h] = W_uv,h oc[t][h], K = rank, in one of two shapes:
+//  * 32 or 64 tokens a CTA, D = W_uv (M = hd) times the tokens' rows (N), all of it in
+//    shared memory; W_uv is loaded before the wait for the rows.  What bounds it is
+//    latency: 3 us from the merge's end (the rows' copies 2), for 64 tokens as for 16.
+//  * 128 tokens a CTA, D = the tokens' rows (M = 128) times W_uv^T (N = hd), in a ring of
+//    64 of rank a stage, two CTAs an SM, so that one's loads and stores run beside the
+//    other's products, and W_uv is read once per 128 tokens.
 template <int HD, int RANK, int TR>
 struct OutCfg {
-  static constexpr int KC = RANK / 64;
-  static constexpr int W_CHUNK = HD * 128;
-  static constexpr int X_CHUNK = TR * 128;
-  static constexpr int OFF_X = KC * W_CHUNK;
-  static constexpr int OFF_CTRL = OFF_X + KC * X_CHUNK;
+  static constexpr bool TILE = TR == 128;           // the tokens on the M side
+  static constexpr int KC = RANK / 64, NST = TILE ? (HD == 128 ? 3 : 4) : KC;
+  static constexpr int W_CHUNK = HD * 128, STAGE = W_CHUNK + TR * 128;
+  static constexpr int OFF_CTRL = NST * STAGE;
   static constexpr int SMEM = OFF_CTRL + 256;
-  static constexpr uint32_t IDESC = idesc_bf16(HD, TR, false);
+  static constexpr int COLS = TILE ? HD : TR;       // of the accumulator
+  static constexpr uint32_t IDESC = TILE ? idesc_bf16(128, HD, false) : idesc_bf16(HD, TR, false);
 };
 
 struct OutParams {
@@ -1015,35 +1018,40 @@ struct OutParams {
 };
 
 template <int HD, int RANK, int TR>
-__global__ void __launch_bounds__(128, 1)
+__global__ void __launch_bounds__(128)
     latent_out_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const OutParams p) {
   using C = OutCfg<HD, RANK, TR>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  static_assert(C::SMEM <= 232448, "shared memory");
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_CTRL), *done = full + C::KC;
+  static_assert(C::SMEM <= 232448 && (2 * C::NST + 1) * 8 + 8 <= 192, "shared memory");
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_CTRL), *empty = full + C::NST, *done = empty + C::NST;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  uint8_t *live = smem + C::OFF_CTRL + 128;   // [TR]
+  uint8_t *live = smem + C::OFF_CTRL + 192;   // [TR]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x, t0 = blockIdx.y * TR;
+  auto load_w = [&](int c) {
+    mbar_arrive_expect_tx(&full[c % C::NST], C::STAGE);
+    tma_load_2d(smem + c % C::NST * C::STAGE, &tmW, &full[c % C::NST], 64 * c, (2 * h + 1) * HD);
+  };
+  auto load_x = [&](int c) { tma_load_3d(smem + c % C::NST * C::STAGE + C::W_CHUNK, &tmX, &full[c % C::NST], 64 * c, h, t0); };
   if (smem_u32(smem) & 1023u) {   // the swizzled layouts need a 1024-aligned base
     pdl_wait();
     if (tid == 0) atomicExch(p.err, kErrBounds);
     return;
   }
   if (tid == 0) {
-    for (int c = 0; c < C::KC; ++c) mbar_init(&full[c], 1);
+    for (int c = 0; c < C::NST; ++c) {
+      mbar_init(&full[c], 1);
+      mbar_init(&empty[c], 1);
+    }
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    for (int c = 0; c < C::KC; ++c) {
-      mbar_arrive_expect_tx(&full[c], C::W_CHUNK + C::X_CHUNK);
-      tma_load_2d(smem + c * C::W_CHUNK, &tmW, &full[c], 64 * c, (2 * h + 1) * HD);
-    }
+    for (int c = 0; c < C::NST; ++c) load_w(c);
     prefetch_tmap(&tmX);
   }
   if (warp == 0) {
-    tmem_alloc(tmem_slot, TR);
+    tmem_alloc(tmem_slot, C::COLS);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -1052,25 +1060,40 @@ __global__ void __launch_bounds__(128, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_wait();   // the rows are the kernel before's
   pdl_trigger();
+  bool mine = false;   // the thread's token is a request's
+  if (C::TILE) mine = t0 + tid < p.T && p.tok[t0 + tid].pieces > 0;
   if (tid == 0) {
-    for (int c = 0; c < C::KC; ++c) tma_load_3d(smem + C::OFF_X + c * C::X_CHUNK, &tmX, &full[c], 64 * c, h, t0);
-    const uint64_t w0 = sdesc_sw128(smem_u32(smem), 16, 1024), x0 = sdesc_sw128(smem_u32(smem + C::OFF_X), 16, 1024);
+    for (int c = 0; c < C::NST; ++c) load_x(c);
+    const uint64_t w0 = sdesc_sw128(smem_u32(smem), 16, 1024), x0 = sdesc_sw128(smem_u32(smem + C::W_CHUNK), 16, 1024);
+    int sent = C::NST;
+    bool ok = true;
 #pragma unroll 1
     for (int c = 0; c < C::KC; ++c) {
-      if (!mbar_wait(&full[c], 0, abort_flag, p.err, kErrWaitMma)) break;
+      const int st = c % C::NST;
+      ok = mbar_wait(&full[st], (c / C::NST) & 1, abort_flag, p.err, kErrWaitMma);
+      if (!ok) break;
       tc_fence_after();
+      const uint64_t w = w0 + static_cast<uint64_t>((st * C::STAGE) >> 4), x = x0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        mma_bf16(tmem, w0 + ((c * C::W_CHUNK + kk * 32) >> 4), x0 + ((c * C::X_CHUNK + kk * 32) >> 4), C::IDESC,
-                 (c > 0 || kk > 0) ? 1u : 0u);
+        mma_bf16(tmem, (C::TILE ? x : w) + ((kk * 32) >> 4), (C::TILE ? w : x) + ((kk * 32) >> 4), C::IDESC, (c > 0 || kk > 0) ? 1u : 0u);
+      if (C::NST < C::KC) {
+        mma_commit(&empty[st]);
+        if (c > 0 && sent < C::KC) {   // the stage of the chunk before
+          ok = mbar_wait(&empty[(c - 1) % C::NST], ((c - 1) / C::NST) & 1, abort_flag, p.err, kErrWaitProducer);
+          if (!ok) break;
+          load_w(sent);
+          load_x(sent++);
+        }
+      }
     }
     mma_commit(done);
-    if (*abort_flag) {
+    if (!ok) {
       const uint64_t t_start = globaltimer();
-      for (int c = 0; c < C::KC; ++c) drain(&full[c], 0, t_start);
+      for (int c = sent - C::NST; c < sent; ++c) drain(&full[c % C::NST], c / C::NST, t_start);
       drain(done, 0, t_start);
     }
-  } else if (tid >= 128 - TR) {
+  } else if (!C::TILE && tid >= 128 - TR) {
     const int k = tid - (128 - TR);
     live[k] = t0 + k < p.T && p.tok[t0 + k].pieces > 0;
   }
@@ -1081,16 +1104,25 @@ __global__ void __launch_bounds__(128, 1)
     tc_fence_after();
     // (with M = 64 a quarter's rows are its first 16 lanes)
     const int dim = HD == 128 ? warp * 32 + lane : warp * 16 + lane;
+    const int64_t step = static_cast<int64_t>(p.H) * HD;
 #pragma unroll 1
-    for (int c0 = 0; c0 < TR; c0 += 32) {
+    for (int c0 = 0; c0 < C::COLS; c0 += 32) {
       float v[32];
       tmem_ld32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c0, v);
-      __nv_bfloat16 *dst = p.o + (static_cast<int64_t>(t0 + c0) * p.H + h) * HD + dim;
-      const int64_t step = static_cast<int64_t>(p.H) * HD;
-      if (HD == 128 || lane < 16)
+      if (C::TILE) {
+        if (!mine) continue;
+        uint32_t x[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) x[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+        __nv_bfloat16 *dst = p.o + (t0 + tid) * step + h * HD + c0;
+        store32(dst, x);
+        store32(dst + 16, x + 8);
+      } else if (HD == 128 || lane < 16) {
+        __nv_bfloat16 *dst = p.o + (t0 + c0) * step + h * HD + dim;
 #pragma unroll
         for (int k = 0; k < 32; ++k)
           if (live[c0 + k]) dst[k * step] = __float2bfloat16_rn(v[k]);
+      }
     }
   }
   tc_fence_before();
@@ -1098,7 +1130,7 @@ __global__ void __launch_bounds__(128, 1)
   if (warp == 0) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, TR);
+    tmem_dealloc(tmem, C::COLS);
   }
 }
 
@@ -1140,12 +1172,14 @@ cudaError_t launch_out(const LatentArgs &a, const void *oc, const OutParams &p, 
 }
 
 // Tiles of 32 tokens while their CTAs fit the SMs at once (96 requests, 40 heads: the
-// call takes 86.8 us, 88.7 with tiles of 64), else of 64 (64 requests of 500 keys, 128
-// heads: 42 us, 47 with tiles of 32).
+// call takes 86.8 us, 88.7 with tiles of 64), of 64 while those do (64 requests of 500
+// keys, 128 heads: 42.1 us, 47.0 with tiles of 32, 44.5 with 128), else of 128 (140
+// requests of 300 keys, 128 heads: 58.3 us, 64.0 with 64).
 template <int HD, int RANK>
 cudaError_t launch_out(const LatentArgs &a, const void *oc, const OutParams &p, cudaStream_t st) {
-  return static_cast<int64_t>(a.H) * ((a.T + 31) / 32) <= device_sm_count() ? launch_out<HD, RANK, 32>(a, oc, p, st)
-                                                                            : launch_out<HD, RANK, 64>(a, oc, p, st);
+  const int64_t sms = device_sm_count(), H = a.H;
+  if (H * ((a.T + 31) / 32) <= sms) return launch_out<HD, RANK, 32>(a, oc, p, st);
+  return H * ((a.T + 63) / 64) <= sms ? launch_out<HD, RANK, 64>(a, oc, p, st) : launch_out<HD, RANK, 128>(a, oc, p, st);
 }
 
 template <int RANK>

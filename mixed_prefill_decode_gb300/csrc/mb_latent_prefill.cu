@@ -233,12 +233,6 @@ struct ExpCtrl {
   int abort;
 };
 
-__device__ __forceinline__ void store32(void *dst, const uint32_t *v) {   // 32 bytes: a whole sector
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-
 // The pair's form of a 5D tile load: counted on an mbarrier of either CTA.
 __device__ __forceinline__ void tma_load_5d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int32_t x0, int32_t x4) {
   asm volatile(
