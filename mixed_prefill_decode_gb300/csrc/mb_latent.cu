@@ -895,13 +895,11 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const AbsParams p) {
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = WARPS == 1 ? 0 : warp;
   const int64_t slot = part_floats(RANK), rows = static_cast<int64_t>(p.T) * p.H;
-  for (int64_t row = WARPS == 1 ? blockIdx.x * 8 + warp : blockIdx.x; row < rows; row += gridDim.x * (8 / WARPS)) {
-    const int t = static_cast<int>(row / p.H), h = static_cast<int>(row % p.H);
-    const TokRec rec = p.tok[t];
-    const int pieces = rec.pieces;
+  auto merge = [&](int64_t row, const TokRec rec) {
+    const int pieces = rec.pieces, h = static_cast<int>(row % p.H);
     // (whole, or no request's; or, where requests of a bad descriptor overlap, the
     // words of two records)
-    if (pieces <= 1 || (rec.first + pieces) * p.HT > kMaxCtas) continue;
+    if (pieces <= 1 || (rec.first + pieces) * p.HT > kMaxCtas) return;
     // piece 0 in slot 2 x0 + 1, piece s > 0 in slot 2 (x0 + s HT)
     const int x0 = rec.first * p.HT + h / p.Hc;
     const int place = rec.place * p.Hc + h % p.Hc;
@@ -963,7 +961,7 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const AbsParams p) {
 #pragma unroll
       for (int k = 0; k < PER; ++k)
         dst[32 * k] = make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv), pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
-      continue;
+      return;
     }
     // the warps' shares, two columns a thread
     if (lane == 0) sh_m[share] = M, sh_l[share] = L;
@@ -987,7 +985,22 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const AbsParams p) {
     }
     if (2 * threadIdx.x < RANK)
       reinterpret_cast<uint32_t *>(p.oc + row * RANK)[threadIdx.x] = pack_bf16x2(sum.x / L, sum.y / L);
-    __syncthreads();   // the next row's shares go where these are
+  };
+  if (WARPS > 1) {   // (a CTA per row)
+    if (blockIdx.x < rows) merge(blockIdx.x, p.tok[blockIdx.x / p.H]);
+    return;
+  }
+  // the records of a warp's next 32 rows at once: most rows are whole
+  const int64_t step = gridDim.x * 8;
+  for (int64_t row0 = blockIdx.x * 8 + warp; row0 < rows; row0 += 32 * step) {
+    const int64_t row = row0 + lane * step;
+    TokRec rec = {0, 0, 0, 0};
+    if (row < rows) rec = p.tok[row / p.H];
+    for (uint32_t left = __ballot_sync(0xffffffffu, rec.pieces > 1); left; left &= left - 1) {
+      const int i = __ffs(left) - 1;
+      merge(row0 + i * step, {__shfl_sync(0xffffffffu, rec.pieces, i), __shfl_sync(0xffffffffu, rec.first, i),
+                              __shfl_sync(0xffffffffu, rec.place, i), 0});
+    }
   }
 }
 
