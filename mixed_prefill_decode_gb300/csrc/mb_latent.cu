@@ -383,7 +383,7 @@ struct AbsCtrl {
   int32_t start_req;
   uint32_t tmem;
   int abort;
-  float col[64];         // one number per row: the rescaling, the reciprocal of its sum
+  alignas(16) float col[64];   // one number per row: the rescaling, the reciprocal of its sum
 };
 
 __device__ __forceinline__ AbsReq abs_req(const AbsParams &p, const ReqWords w, bool *bad) {
@@ -855,13 +855,17 @@ __global__ void __launch_bounds__(AbsCfg<RANK>::THREADS, 1)
         if (slot < 0) {
           __nv_bfloat16 *dst = p.oc + (static_cast<int64_t>(sg.t0) * p.H + ht * p.Hc + r0) * RANK + n;
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (r0 + k < rows) dst[k * RANK] = __float2bfloat16_rn(v[k] * ct.col[r0 + k]);
+          for (int k = 0; k < 32; k += 4) {
+            const float4 c = *reinterpret_cast<const float4 *>(ct.col + r0 + k);
+            store_if(r0 + k < rows, dst + k * RANK, __float2bfloat16_rn(v[k] * c.x));
+            store_if(r0 + k + 1 < rows, dst + (k + 1) * RANK, __float2bfloat16_rn(v[k + 1] * c.y));
+            store_if(r0 + k + 2 < rows, dst + (k + 2) * RANK, __float2bfloat16_rn(v[k + 2] * c.z));
+            store_if(r0 + k + 3 < rows, dst + (k + 3) * RANK, __float2bfloat16_rn(v[k + 3] * c.w));
+          }
         } else {
           float *dst = p.part + slot * part_floats(RANK) + r0 * RANK + n;
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (r0 + k < rows) dst[k * RANK] = v[k];
+          for (int k = 0; k < 32; ++k) store_if(r0 + k < rows, dst + k * RANK, v[k]);
         }
       }
       tc_fence_before();
@@ -1035,11 +1039,10 @@ __global__ void __launch_bounds__(128)
     latent_out_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const OutParams p) {
   using C = OutCfg<HD, RANK, TR>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  static_assert(C::SMEM <= 232448 && (2 * C::NST + 1) * 8 + 8 <= 192, "shared memory");
+  static_assert(C::SMEM <= 232448 && (2 * C::NST + 1) * 8 + 8 <= 256, "shared memory");
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_CTRL), *empty = full + C::NST, *done = empty + C::NST;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  uint8_t *live = smem + C::OFF_CTRL + 192;   // [TR]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x, t0 = blockIdx.y * TR;
   auto load_w = [&](int c) {
@@ -1073,8 +1076,16 @@ __global__ void __launch_bounds__(128)
   const uint32_t tmem = *tmem_slot;
   pdl_wait();   // the rows are the kernel before's
   pdl_trigger();
-  bool mine = false;   // the thread's token is a request's
+  // tokens that are a request's: the thread's own, or a bit for each of the tile's
+  bool mine = false;
+  uint32_t live[2] = {0, 0};
   if (C::TILE) mine = t0 + tid < p.T && p.tok[t0 + tid].pieces > 0;
+  else
+#pragma unroll
+    for (int k = 0; k < TR / 32; ++k) {
+      const int t = t0 + 32 * k + lane;
+      live[k] = __ballot_sync(0xffffffffu, t < p.T && p.tok[t].pieces > 0);
+    }
   if (tid == 0) {
     for (int c = 0; c < C::NST; ++c) load_x(c);
     const uint64_t w0 = sdesc_sw128(smem_u32(smem), 16, 1024), x0 = sdesc_sw128(smem_u32(smem + C::W_CHUNK), 16, 1024);
@@ -1106,9 +1117,6 @@ __global__ void __launch_bounds__(128)
       for (int c = sent - C::NST; c < sent; ++c) drain(&full[c % C::NST], c / C::NST, t_start);
       drain(done, 0, t_start);
     }
-  } else if (!C::TILE && tid >= 128 - TR) {
-    const int k = tid - (128 - TR);
-    live[k] = t0 + k < p.T && p.tok[t0 + k].pieces > 0;
   }
   __syncthreads();
   bool ok = mbar_wait(done, 0, abort_flag, p.err, kErrWaitEpilogue);
@@ -1118,7 +1126,7 @@ __global__ void __launch_bounds__(128)
     // (with M = 64 a quarter's rows are its first 16 lanes)
     const int dim = HD == 128 ? warp * 32 + lane : warp * 16 + lane;
     const int64_t step = static_cast<int64_t>(p.H) * HD;
-#pragma unroll 1
+#pragma unroll
     for (int c0 = 0; c0 < C::COLS; c0 += 32) {
       float v[32];
       tmem_ld32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c0, v);
@@ -1133,8 +1141,7 @@ __global__ void __launch_bounds__(128)
       } else if (HD == 128 || lane < 16) {
         __nv_bfloat16 *dst = p.o + (t0 + c0) * step + h * HD + dim;
 #pragma unroll
-        for (int k = 0; k < 32; ++k)
-          if (live[c0 + k]) dst[k * step] = __float2bfloat16_rn(v[k]);
+        for (int k = 0; k < 32; ++k) store_if((live[(c0 / 32) & 1] >> k) & 1, dst + k * step, __float2bfloat16_rn(v[k]));
       }
     }
   }

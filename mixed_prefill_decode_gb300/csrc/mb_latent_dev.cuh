@@ -77,6 +77,19 @@ __device__ __forceinline__ void store32(void *dst, const uint32_t *v) {   // 32 
                : "memory");
 }
 
+// Stores under a predicate.  (With an `if` each, stores of an unrolled loop became
+// branches: 20 cycles a store of a warp instead of 16.)
+__device__ __forceinline__ void store_if(bool yes, __nv_bfloat16 *dst, __nv_bfloat16 v) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p st.global.b16 [%0], %1;\n\t}" ::"l"(dst),
+               "h"(__bfloat16_as_ushort(v)), "r"(static_cast<uint32_t>(yes))
+               : "memory");
+}
+__device__ __forceinline__ void store_if(bool yes, float *dst, float v) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p st.global.f32 [%0], %1;\n\t}" ::"l"(dst), "f"(v),
+               "r"(static_cast<uint32_t>(yes))
+               : "memory");
+}
+
 // A tile of shared memory to global memory (part of the thread's current bulk group).
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int32_t x, int32_t y, int32_t z) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
