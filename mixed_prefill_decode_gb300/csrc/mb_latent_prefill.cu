@@ -1227,11 +1227,11 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
 }
 
 // Merge of the units that were cut: CTA (w, y) takes rows 32 y .. 32 y + 31 of the
-// unit whose first piece CTA w computed, a lane a row, a warp HD / 8 columns.
+// unit whose first piece CTA w computed, a lane a row, a warp 8 columns.
 //   o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,   M = max_s m_s
 template <int HD>
-__global__ void __launch_bounds__(256) latent_prefill_merge_kernel(const __grid_constant__ PreParams p) {
-  constexpr int COLS = HD / 8;
+__global__ void __launch_bounds__(4 * HD) latent_prefill_merge_kernel(const __grid_constant__ PreParams p) {
+  constexpr int COLS = 8;
   pdl_wait();
   pdl_trigger();
   const int w = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1243,7 +1243,7 @@ __global__ void __launch_bounds__(256) latent_prefill_merge_kernel(const __grid_
   float M = -INFINITY, L = 0.f, acc[COLS];
 #pragma unroll
   for (int k = 0; k < COLS; ++k) acc[k] = 0.f;
-#pragma unroll 2
+#pragma unroll 4
   for (int s = 0; s < pieces; ++s) {
     const float *x = src(s);
     float v[COLS];
@@ -1258,14 +1258,17 @@ __global__ void __launch_bounds__(256) latent_prefill_merge_kernel(const __grid_
 #pragma unroll
     for (int k = 0; k < COLS; ++k) acc[k] = acc[k] * a + (b == 0.f ? 0.f : b * v[k]);
   }
-  if (row >= rec.w) return;
   const float inv = 1.f / L;
-  __nv_bfloat16 *dst = p.o + (static_cast<int64_t>(rec.y + row) * p.H + rec.z) * HD + warp * COLS;
   uint32_t x[COLS / 2];
 #pragma unroll
   for (int k = 0; k < COLS / 2; ++k) x[k] = pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-  if constexpr (COLS == 16) store32(dst, x);   // a whole sector a lane
-  else *reinterpret_cast<uint4 *>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
+  // out row by row: HD / 8 threads a row
+  __shared__ uint4 sh[32][HD / 8 + 1];
+  sh[lane][warp] = make_uint4(x[0], x[1], x[2], x[3]);
+  __syncthreads();
+  const int r = threadIdx.x / (HD / 8), c = threadIdx.x % (HD / 8), out = blockIdx.y * 32 + r;
+  if (out < rec.w)
+    reinterpret_cast<uint4 *>(p.o + (static_cast<int64_t>(rec.y + out) * p.H + rec.z) * HD)[c] = sh[r][c];
 }
 
 // The workspace's keys: blocks of 128, each request's from a block of its own.
@@ -1316,7 +1319,7 @@ cudaError_t launch_prefill(const LatentArgs &a, PreParams &p, int group, __nv_bf
     p.HG = std::min(group, a.H - p.h0);
     e = a.rank == 512 ? launch_expand<HD, 512>(tk, tw, ts, p, st) : launch_expand<HD, 256>(tk, tw, ts, p, st);
     if (e == cudaSuccess) e = launch_pdl(latent_prefill_kernel<HD>, dim3(ctas), dim3(C::THREADS), C::SMEM, st, 1, tq, tqr, tkv, tr, p);
-    if (e == cudaSuccess) e = launch_pdl(latent_prefill_merge_kernel<HD>, dim3(ctas, 8), dim3(256), 0, st, 1, p);
+    if (e == cudaSuccess) e = launch_pdl(latent_prefill_merge_kernel<HD>, dim3(ctas, 8), dim3(4 * HD), 0, st, 1, p);
   }
   return e;
 }
