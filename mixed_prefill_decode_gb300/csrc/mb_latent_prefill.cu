@@ -1179,7 +1179,7 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
           const bool valid = row < rows;
           const int tok = sg.t0 + 128 * t + row, slot = sg.slot;
           const float inv = 1.f / l;
-          uint4 *dst = reinterpret_cast<uint4 *>(p.o + (static_cast<int64_t>(tok) * p.H + sg.h) * HD);
+          __nv_bfloat16 *dst = p.o + (static_cast<int64_t>(tok) * p.H + sg.h) * HD;
           float *part = p.part + max(slot, 0) * part_floats(HD) + 128 * t + row;
 #pragma unroll 1
           for (int cc = 0; cc < HD / 32; ++cc) {
@@ -1192,12 +1192,11 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
               for (int k = 0; k < 32; ++k) v[k] = wa * v[k] + wb * x[k];
             }
             if (valid && slot < 0) {
+              uint32_t x[16];
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                dst[cc * 4 + k] = make_uint4(pack_bf16x2(v[8 * k] * inv, v[8 * k + 1] * inv),
-                                             pack_bf16x2(v[8 * k + 2] * inv, v[8 * k + 3] * inv),
-                                             pack_bf16x2(v[8 * k + 4] * inv, v[8 * k + 5] * inv),
-                                             pack_bf16x2(v[8 * k + 6] * inv, v[8 * k + 7] * inv));
+              for (int k = 0; k < 16; ++k) x[k] = pack_bf16x2(v[2 * k] * inv, v[2 * k + 1] * inv);
+              store32(dst + cc * 32, x);
+              store32(dst + cc * 32 + 16, x + 8);
             } else if (slot >= 0) {
               // (column by column: a warp's stores fill whole lines; row by row they
               // took 5,000 cycles a piece.  Rows that are none have a place too.)
