@@ -151,8 +151,8 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const __g
 // one head on tcgen05, A and B wholly in shared memory, one barrier per 64 of
 // hd; the result leaves by TMA from where A was.  Heads' weights are read once per
 // TOK tokens: for few tokens they (and the launch) are the time, for many the
-// stores.  64 tokens of 32 heads 2.3 us from
-// the kernel before's end, 16 of 128 heads (16 MB of weights) 3.3 to 5.6.
+// stores.  64 tokens of 32 heads 2.3 us from the kernel before's end, 16 of 128 heads
+// (16 MB of weights) 4, 256 of 128 heads (and 34 MB of results) 14.
 constexpr int kQueryN = 128;
 
 template <int HD, int TOK>
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(128) latent_query_kernel(const __grid_constant
 // it, P V 96, the copies write 72: 2,500 cycles at 128 bytes; a block takes 2,900).
 // Measured, the whole call replayed in a graph (head 128, rank 512): 96 ragged requests
 // of 1,024 to 8,192 keys, 40 heads 87 us, of which the stream of 390 MB about 60 (6.5
-// TB/s); 16 x 8,192 keys, 128 heads 67; 64 x 1,125 keys, 32 heads 34; one request 18.
+// TB/s); 16 x 8,192 keys, 128 heads 66; 64 x 1,125 keys, 32 heads 35; one request 16 to 18.
 constexpr int kMaxCtas = 160;       // CTAs of a launch at most; sizes the workspace
 // Floats of a slot: whole lines only (with m and l behind each row the stores and
 // loads of a row began 16 bytes off a sector).
@@ -335,7 +335,7 @@ struct AbsCfg {
   // A stage holds a block in two parts, each [page][8 rows of 2][chunk][8 rows][128 B]:
   // half of the vectors, and the other half with the rotated keys.  Parts are
   // loaded, waited for and given back by themselves, so S begins when the first has
-  // come (16 requests at 8,192 keys, 128 heads: 68 us; 72 with whole blocks given back
+  // come (16 requests at 8,192 keys, 128 heads: 67 us; 72 with whole blocks given back
   // page by page; 86 with five parts, whose copies of 4 KB come at 18 bytes a cycle).
   static constexpr int C0 = DT, C1 = DT + 1;        // chunks of the parts
   static constexpr int PART0 = C0 * kBlk * 128, PART1 = C1 * kBlk * 128;

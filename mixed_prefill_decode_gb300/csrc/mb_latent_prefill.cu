@@ -12,8 +12,8 @@
 // What bounds it: the tensor cores, and beside them the chain of product,
 // softmax, product.  Keys and values of a head are 4 hd bytes a token, written once
 // and read by every tile of queries.  Measured, replayed in a graph: 2,048 tokens at
-// 8,192 keys, 40 heads of 128, rank 512 313 us, 1.47 PFLOP/s (expansion 57, attention
-// 240); 512 tokens of 32 heads 30 us: three launches and the chain of two blocks.
+// 8,192 keys, 40 heads of 128, rank 512 308 us, 1.50 PFLOP/s (expansion 57, attention
+// 240); 512 tokens of 32 heads 28 us: three launches and the chain of two blocks.
 //
 // Two kernels, and a merge (per group of heads, if all heads' keys and values would
 // take more than 512 MB):

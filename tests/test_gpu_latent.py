@@ -238,6 +238,15 @@ def test_absorbed_long_caches_cut_over_many_ctas(mb, reqs, H, hd, rank):
     b.check(b.run(mb, "absorbed"), "absorbed")
 
 
+@pytest.mark.parametrize("H,hd,rank", [(128, 128, 512), (97, 64, 512), (100, 128, 256), (80, 64, 256)])
+def test_absorbed_many_rows(mb, H, hd, rank):
+    """More rows than the merge's warps, outputs by tiles of 128 tokens, the
+    first of them of no request."""
+    reqs = [(int(k), 1 + int(k) % 5 // 4) for k in np.random.default_rng(8).integers(0, 200, size=40)] + [(2500, 1)]
+    b = Batch(reqs, H, hd, rank, seed=H + 40, lead=130, tail=70)
+    b.check(b.run(mb, "absorbed"), "absorbed")
+
+
 def test_absorbed_more_requests_than_threads(mb):
     reqs = [(int(k) % 90, int(k) % 3) for k in np.random.default_rng(5).integers(0, 1000, size=700)]
     b = Batch(reqs, 4, 64, 256, seed=6)
