@@ -1076,6 +1076,9 @@ __global__ void __launch_bounds__(128)
   const uint32_t tmem = *tmem_slot;
   pdl_wait();   // the rows are the kernel before's
   pdl_trigger();
+  if (tid == 0)
+    for (int c = 0; c < C::NST; ++c) load_x(c);
+  __syncwarp();
   // tokens that are a request's: the thread's own, or a bit for each of the tile's
   bool mine = false;
   uint32_t live[2] = {0, 0};
@@ -1087,7 +1090,6 @@ __global__ void __launch_bounds__(128)
       live[k] = __ballot_sync(0xffffffffu, t < p.T && p.tok[t].pieces > 0);
     }
   if (tid == 0) {
-    for (int c = 0; c < C::NST; ++c) load_x(c);
     const uint64_t w0 = sdesc_sw128(smem_u32(smem), 16, 1024), x0 = sdesc_sw128(smem_u32(smem + C::W_CHUNK), 16, 1024);
     int sent = C::NST;
     bool ok = true;
@@ -1136,8 +1138,8 @@ __global__ void __launch_bounds__(128)
 #pragma unroll
         for (int k = 0; k < 16; ++k) x[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
         __nv_bfloat16 *dst = p.o + (t0 + tid) * step + h * HD + c0;
-        store32(dst, x);
-        store32(dst + 16, x + 8);
+        store_out(dst, x);
+        store_out(dst + 16, x + 8);
       } else if (HD == 128 || lane < 16) {
         __nv_bfloat16 *dst = p.o + (t0 + c0) * step + h * HD + dim;
 #pragma unroll

@@ -71,10 +71,20 @@ __device__ __forceinline__ void l2_prefetch(const void *p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
-__device__ __forceinline__ void store32(void *dst, const uint32_t *v) {   // 32 bytes: a whole sector
+__device__ __forceinline__ void store32(void *dst, const uint32_t *v) {   // 32 bytes from a boundary of them: a whole sector
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
+}
+
+// 32 bytes of an output, which need not begin on a boundary of them.
+__device__ __forceinline__ void store_out(void *dst, const uint32_t *v) {
+  if ((reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
+    store32(dst, v);
+  } else {
+    reinterpret_cast<uint4 *>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4 *>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
 }
 
 // Stores under a predicate.  (With an `if` each, stores of an unrolled loop became

@@ -1195,8 +1195,8 @@ __global__ void __launch_bounds__(PreCfg<HD>::THREADS, 1)
               uint32_t x[16];
 #pragma unroll
               for (int k = 0; k < 16; ++k) x[k] = pack_bf16x2(v[2 * k] * inv, v[2 * k + 1] * inv);
-              store32(dst + cc * 32, x);
-              store32(dst + cc * 32 + 16, x + 8);
+              store_out(dst + cc * 32, x);
+              store_out(dst + cc * 32 + 16, x + 8);
             } else if (slot >= 0) {
               // (column by column: a warp's stores fill whole lines; row by row they
               // took 5,000 cycles a piece.  Rows that are none have a place too.)

@@ -247,6 +247,28 @@ def test_absorbed_many_rows(mb, H, hd, rank):
     b.check(b.run(mb, "absorbed"), "absorbed")
 
 
+@pytest.mark.parametrize("form,reqs,H", [("absorbed", [(300, 1)] * 40 + [(0, 130)], 128), ("absorbed", [(300, 1), (70, 2)], 8),
+                                         ("expanded", [(0, 400), (300, 20), (64, 1)], 8),
+                                         ("expanded", [(5000, 40)], 2)])
+def test_arrays_on_16_byte_boundaries(mb, form, reqs, H):
+    """Inputs and outputs that begin 16 bytes behind a boundary of 256: the same
+    bits, and nothing around them."""
+    b = Batch(reqs, H, 64, 256, seed=50)
+    want = b.out()
+    b.call(mb, form, b.dev(), want, b.work(mb, form))
+    d = b.dev()
+    for k in ("q", "q_rope", "w"):
+        buf = torch.empty(d[k].numel() + 8, dtype=d[k].dtype, device="cuda")
+        buf[8:] = d[k].reshape(-1)
+        d[k] = buf[8:]
+        assert d[k].data_ptr() % 32 == 16
+    buf = torch.full((b.T * H * 64 + 16,), float("nan"), dtype=torch.bfloat16, device="cuda")
+    b.call(mb, form, d, buf[8:-8], b.work(mb, form))
+    _status(mb, False)
+    assert torch.equal(buf[8:-8].view(torch.int16), want.reshape(-1).view(torch.int16))
+    assert torch.all(torch.isnan(buf[:8])).item() and torch.all(torch.isnan(buf[-8:])).item()
+
+
 def test_absorbed_more_requests_than_threads(mb):
     reqs = [(int(k) % 90, int(k) % 3) for k in np.random.default_rng(5).integers(0, 1000, size=700)]
     b = Batch(reqs, 4, 64, 256, seed=6)
