@@ -309,7 +309,7 @@ constexpr int kMaxCtas = 160;       // CTAs of a launch at most; sizes the works
 // loads of a row began 16 bytes off a sector).
 __host__ __device__ constexpr int64_t part_floats(int64_t rank) { return 64 * rank + 128; }
 constexpr int kBlk = 64;            // keys of a block
-constexpr int kCostUnit = 2;        // a unit's start and end, in blocks
+constexpr int kCostUnit = 3;        // a unit's start and end, in blocks (1 to 4: within 5 %; short units like more, long ones less)
 
 struct AbsParams {
   __nv_bfloat16 *oc;             // [T][H][rank]: sum_j p_j c_j
