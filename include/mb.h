@@ -538,7 +538,8 @@ mb_status mb_tables_release(const int32_t *slots, int32_t n, const int32_t *tabl
  *   q_rope  device bf16 [T][heads][64], rotated
  *   w_kv    device bf16 [heads][2 head_dim][rank]
  *   o       device bf16 [T][heads * head_dim]
- * Descriptor arrays are DEVICE int32 as in mb_tree_attention, but the first
+ * all 16-byte aligned, the attention's pool 128-byte; arrays of no elements may
+ * be NULL.  Descriptor arrays are DEVICE int32 as in mb_tree_attention, but the first
  * request may start at any row (qo_indptr[0] >= 0), so a batch of decodes and
  * chunks is two calls on parts of one descriptor; a request may have no tokens.
  * Rows outside every request are left as they were.  A request that breaks a
