@@ -553,8 +553,10 @@ mb_status mb_tables_release(const int32_t *slots, int32_t n, const int32_t *tabl
  * gives to the next one (q_nope W_uk and sum_j p_j c_j in the absorbed form, the
  * keys and values in the expanded one).  workspace: 256-byte aligned device
  * memory, needs no initialisation; a call owns it until it completes (calls on
- * unordered streams, graphs that may run at once, need one each).  No output may
- * overlap an input.  T at most 2^20.  Errors: MB_EINVAL, MB_EUNSUPPORTED, MB_ECUDA. */
+ * unordered streams, graphs that may run at once, need one each).  Neither size
+ * below falls as an argument grows, so the workspace of the largest call does for
+ * every smaller one.  No output may overlap an input.  T at most 2^20.
+ * Errors: MB_EINVAL, MB_EUNSUPPORTED, MB_ECUDA. */
 
 /* The new tokens' cache rows, and their queries' rotation: token t of T goes to
  * place tok_slot[t] (page * 16 + slot; -1: the row is passed over) with

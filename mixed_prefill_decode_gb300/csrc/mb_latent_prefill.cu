@@ -1273,11 +1273,23 @@ __global__ void __launch_bounds__(4 * HD) latent_prefill_merge_kernel(const __gr
 // The workspace's keys: blocks of 128, each request's from a block of its own.
 int64_t cap_blocks(int64_t kv_tokens, int64_t n_reqs) { return kv_tokens / kBlk + n_reqs; }
 
+int64_t head_bytes(int64_t blocks, int64_t hd) { return blocks * kBlk * 4 * hd; }   // one head's keys and values
+
 // Heads of a group: as many as keep its keys and values within kGroupBytes, evenly spread.
 int group_heads(int64_t blocks, int64_t H, int64_t hd) {
-  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(H, kGroupBytes / std::max<int64_t>(1, blocks * kBlk * 4 * hd)));
+  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(H, kGroupBytes / std::max<int64_t>(1, head_bytes(blocks, hd))));
   const int64_t groups = (H + most - 1) / most;
   return static_cast<int>((H + groups - 1) / groups);
+}
+
+// Room for a group's keys and values: what all heads take, at most kGroupBytes, and
+// one head's at least.  The even spread may need about half of that (just above
+// kGroupBytes two groups have half the heads each), but a size that followed it
+// would fall as a batch grows, and a workspace of the largest call has to do for
+// every smaller one.
+size_t kv_room(int64_t blocks, int64_t H, int64_t hd) {
+  const int64_t one = head_bytes(blocks, hd);
+  return std::max<int64_t>(one, std::min<int64_t>(H * one, kGroupBytes));
 }
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -1329,7 +1341,7 @@ cudaError_t launch_prefill(const LatentArgs &a, PreParams &p, int group, __nv_bf
 size_t latent_prefill_workspace_bytes(int64_t kv_tokens, int64_t n_reqs, int64_t H, int64_t hd, int64_t rank) {
   (void)rank;
   const int64_t blocks = cap_blocks(kv_tokens, n_reqs);
-  return align256(static_cast<size_t>(blocks) * kBlk * 4 * hd * group_heads(blocks, H, hd)) +
+  return align256(kv_room(blocks, H, hd)) +
          align256(static_cast<size_t>(blocks) * kBlk * kLatentRope * 2) + kRecBytes + kPartsBytes +
          static_cast<size_t>(2) * kMaxCtas * part_floats(hd) * sizeof(float);
 }
@@ -1338,7 +1350,7 @@ cudaError_t latent_prefill_run(const LatentArgs &a, cudaStream_t st) {
   const int64_t blocks = cap_blocks(a.kv_tokens, a.n_reqs);
   const int group = group_heads(blocks, a.H, a.hd);
   uint8_t *w = static_cast<uint8_t *>(a.workspace);
-  const size_t kv_bytes = align256(static_cast<size_t>(blocks) * kBlk * 4 * a.hd * group);
+  const size_t kv_bytes = align256(kv_room(blocks, a.H, a.hd));
   const size_t rope_bytes = align256(static_cast<size_t>(blocks) * kBlk * kLatentRope * 2);
   PreParams p;
   p.kv = reinterpret_cast<__nv_bfloat16 *>(w);

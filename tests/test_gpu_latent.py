@@ -458,3 +458,49 @@ def test_runs_repeat_to_the_bit(mb, form):
     first = b.run(mb, form)
     for _ in range(20):
         assert np.array_equal(b.run(mb, form), first, equal_nan=True)
+
+
+# -------------------------------------------------------------- workspace
+class Guarded:
+    """A workspace of `size` bytes, all NaN, with a known pattern behind it."""
+
+    def __init__(self, size):
+        self.size, self.buf = size, torch.full((size + 65536,), 0xFF, dtype=torch.uint8, device="cuda")
+        self.buf[size:] = 0x5A
+
+    def check(self):
+        assert torch.all(self.buf[self.size:] == 0x5A).item(), "written behind the workspace"
+
+
+@pytest.mark.parametrize("form", ["absorbed", "expanded"])
+def test_one_workspace_for_calls_of_all_sizes(mb, form):
+    """The workspace of the largest batch, for it, for smaller ones, and for it again."""
+    H, hd, rank = 20, 128, 512
+    batches = [Batch(reqs, H, hd, rank, seed=60 + i, tail=0) for i, reqs in enumerate(
+        ([(700, 40), (0, 130), (2000, 1), (64, 1)], [(0, 1)], [(0, 300)], [(60, 4), (0, 0), (127, 1)], [(3000, 5)]))]
+    batches.append(batches[0])
+    T, kv, n = (max(f(b) for b in batches) for f in (lambda b: b.T, lambda b: b.room(), lambda b: len(b.reqs)))
+    w = Guarded(mb.mb_latent_attention_workspace_bytes(T, H, rank) if form == "absorbed" else
+                mb.mb_latent_prefill_workspace_bytes(kv, n, H, hd, rank))
+    for b in batches:
+        o = b.out()
+        b.call(mb, form, b.dev(), o, w.buf)
+        _status(mb, False)
+        w.check()
+        b.check(f64(from_dev(o)).reshape(b.T, H, hd), form)
+
+
+def test_one_expanded_workspace_on_both_sides_of_the_groups(mb):
+    """128 heads of 128: their keys and values are one group up to 8,191 tokens of
+    one request, two behind.  The workspace of the largest call, for all."""
+    H, hd, rank, heads = 128, 128, 256, [0, 63, 64, 127]
+    w = Guarded(mb.mb_latent_prefill_workspace_bytes(8400, 2, H, hd, rank))
+    for reqs in ([(8390, 10)], [(8000, 5)], [(8060, 3), (100, 30)], [(70, 60)], [(8390, 10)]):
+        b = Batch(reqs, H, hd, rank, seed=70 + reqs[0][1], tail=0)
+        o = b.out()
+        b.call(mb, "expanded", b.dev(), o, w.buf)
+        _status(mb, False)
+        w.check()
+        got = f64(from_dev(o)).reshape(b.T, H, hd)
+        b.q, b.q_rope, b.w, b.H = b.q[:, heads], b.q_rope[:, heads], b.w[heads], len(heads)
+        b.check(got[:, heads], "expanded")

@@ -197,3 +197,43 @@ def test_oracle_tables_hand_trace():
     assert owned.tolist() == [1, 0, 2]
     count, bad = OL.tables_release([2], tables, owned, ring, head, count, 5)
     assert count == 3 and not bad and ring.tolist() == [9, 8, 6, 5, 5] and owned.tolist() == [1, 0, 0]
+
+
+# ---------------------------------------------------------- workspace sizes
+def _never_falls(size, axes, fixed):
+    """`size` over every axis, the others at each of `fixed`'s values."""
+    for at in fixed:
+        for axis, values in axes.items():
+            sizes = [size(**{**at, axis: v}) for v in values]
+            assert sizes == sorted(sizes), (at, axis, values[int(np.argmin(np.diff(sizes)))])
+
+
+def test_expanded_workspace_never_falls_as_a_batch_grows(mb):
+    """A workspace of the largest call does for every smaller one, across the
+    sizes where the heads begin to be taken in groups (512 MB of keys and values:
+    8,192 keys of 128 heads of 128)."""
+    axes = dict(kv_tokens=[0, 1, 127, 128, 4000, 8000, 8063, 8064, 8191, 8192, 8320, 13000, 16384, 26000, 26112, 32768, 52000,
+                           1 << 20, (1 << 20) + 128, 1 << 21, 1 << 22, 1 << 24, 1 << 27],
+                num_reqs=[0, 1, 2, 8, 33, 64, 65, 128, 129, 1000, 4096, 8192, 1 << 14, 1 << 17, 1 << 20],
+                n_heads=list(range(1, 129)), head_dim=[64, 128], rank=[256, 512])
+    fixed = [dict(kv_tokens=kv, num_reqs=n, n_heads=H, head_dim=hd, rank=512)
+             for kv in (1, 8000, 8320, 26000, 1 << 20, 1 << 27) for n in (1, 8, 64, 1 << 20) for H in (1, 40, 128) for hd in (64, 128)]
+    _never_falls(mb.mb_latent_prefill_workspace_bytes, axes, fixed)
+
+
+@pytest.mark.parametrize("kv,n,H,hd", [(26000, 1, 40, 128), (26112, 1, 40, 128), (8320, 1, 128, 128), (26000, 1, 100, 64),
+                                       (1 << 21, 1, 3, 64), (1 << 27, 1, 128, 128), (0, 1, 1, 64)])
+def test_expanded_workspace_holds_what_a_group_takes(mb, kv, n, H, hd):
+    """The groups' keys and values (4 bytes a number of a head's keys), evenly
+    spread, and the rotated keys, by blocks of 128 keys."""
+    blocks = kv // 128 + n
+    most = max(1, min(H, (512 << 20) // (blocks * 128 * 4 * hd)))
+    group = -(-H // -(-H // most))
+    part = 2 * 160 * 256 * (hd + 2) * 4 + 8192 + 20480
+    assert mb.mb_latent_prefill_workspace_bytes(kv, n, H, hd, 256) >= blocks * 128 * (4 * hd * group + 128) + part
+
+
+def test_absorbed_workspace_never_falls_as_a_batch_grows(mb):
+    axes = dict(T=[0, 1, 2, 63, 64, 65, 1000, 1 << 20], n_heads=list(range(1, 129)), rank=[256, 512])
+    _never_falls(mb.mb_latent_attention_workspace_bytes, axes,
+                 [dict(T=T, n_heads=H, rank=r) for T in (0, 7, 1 << 20) for H in (1, 40, 128) for r in (256, 512)])
