@@ -934,7 +934,7 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const AbsParams p) {
       for (int s = 0; s < AHEAD; ++s) top = fmaxf(top, ml[s].x);
       const float old = M == -INFINITY ? 0.f : ex2_approx(M - top);
       // (a sum that is NaN says that the row saw one; a piece of which it saw
-      // nothing has a sum of 0)
+      // nothing has a sum of 0, and so has one with logits of minus infinity only)
       L = M == -INFINITY ? L : L * old;
 #pragma unroll
       for (int k = 0; k < PER; ++k) {
@@ -947,7 +947,7 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const AbsParams p) {
       for (int s = 0; s < AHEAD; ++s) {
         const float w = ml[s].x == -INFINITY ? 0.f : ex2_approx(ml[s].x - top);
         L += ml[s].x == -INFINITY ? ml[s].y : w * ml[s].y;
-        if (w != 0.f)   // (0: no such piece, or the row saw nothing in it)
+        if (s0 + s * WARPS < pieces)   // (with a weight of 0 too: a vector that is not finite leaves NaN there)
 #pragma unroll
           for (int k = 0; k < PER; ++k) {
             acc[k].x = fmaf(w, v[s][k].x, acc[k].x);
@@ -981,7 +981,7 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const AbsParams p) {
     for (int w = 0; w < WARPS; ++w) {
       const float a = sh_m[w] == -INFINITY ? 0.f : ex2_approx(sh_m[w] - top);
       L += sh_m[w] == -INFINITY ? sh_l[w] : a * sh_l[w];
-      if (2 * threadIdx.x < RANK && a != 0.f) {
+      if (2 * threadIdx.x < RANK) {   // (a warp without pieces has zeros; as above, whatever the weight)
         const float2 x = *reinterpret_cast<const float2 *>(&sh_acc[w][2 * threadIdx.x]);
         sum.x = fmaf(a, x.x, sum.x);
         sum.y = fmaf(a, x.y, sum.y);

@@ -504,3 +504,36 @@ def test_one_expanded_workspace_on_both_sides_of_the_groups(mb):
         got = f64(from_dev(o)).reshape(b.T, H, hd)
         b.q, b.q_rope, b.w, b.H = b.q[:, heads], b.q_rope[:, heads], b.w[heads], len(heads)
         b.check(got[:, heads], "expanded")
+
+
+# ------------------------------------------- values that are not finite, pieces
+@pytest.mark.parametrize("form", ["absorbed", "expanded"])
+@pytest.mark.parametrize("n,H,hd,rank", [(1, 8, 64, 256), (3, 128, 64, 512)])
+def test_a_vector_that_is_not_finite_in_a_piece_without_weight(mb, form, n, H, hd, rank):
+    """The last key is a block, and in so short a batch a piece, of its own.  An
+    infinite number in its vector gives about half of the heads a logit of minus
+    infinity, so the piece's weight is 0, but a vector that is not finite makes
+    its rows NaN whatever its weight."""
+    b = Batch([(192, 1)] * n, H, hd, rank, seed=80 + n)
+    clean = b.run(mb, form)
+    assert np.all(np.isfinite(clean[:n]))
+    for r in range(n):
+        b.pool[b.bt[b.bti[r] + 12], 0, 7] = 0x7F80
+    towards = np.einsum("thd,hd->th", f64(b.q[:n])[:, :, :hd], f64(b.w)[:, :hd, 7])
+    assert np.any(towards < 0) and np.any(towards > 0)
+    got = b.run(mb, form)
+    assert np.all(np.isnan(got[:n]))
+
+
+def test_a_vector_that_is_not_finite_far_below_the_others(mb):
+    """The same with a logit so low that the piece's weight is 0 in fp32 beside the
+    rest: its key alone is far down, its vector's product with q' is 0 times infinity
+    or of either sign."""
+    b = Batch([(192, 1)], 8, 64, 256, seed=90)
+    b.q_rope[:, :, 1:] = 0
+    b.q_rope[:, :, 0] = 0x4080                                # 4
+    b.pool[b.bt[12], 0, 256] = 0xC47A                         # -1,000: 500 powers of two below
+    want = b.run(mb, "absorbed")
+    b.check(want, "absorbed")
+    b.pool[b.bt[12], 0, 7] = 0x7F80
+    assert np.all(np.isnan(b.run(mb, "absorbed")[:1]))
