@@ -506,9 +506,10 @@ mb_status mb_kv_copy_pages(void *const *pools, int32_t n_pools, int32_t num_page
  * more than max_pages pages) records MB_EDEVICE and counts as a request with no
  * tokens, keys or pages.  If the granted tokens exceed T, or the pages bt_cap,
  * the batch is empty (tok_* all -1), nothing changes hands and MB_EDEVICE is
- * recorded.  A page id in the ring or a row outside [0, num_pages) records
- * MB_EDEVICE and gives its tokens tok_slot -1.  num_reqs at most 8192, max_slots 65536, max_pages
- * 2^20, num_pages below 2^27, T and bt_cap below 2^30.  All arrays device int32.
+ * recorded.  A listed page id, of a row or from the ring, outside [0, num_pages)
+ * records MB_EDEVICE and gives its new tokens tok_slot -1.  num_reqs at most 8192,
+ * max_slots 65536, max_pages 2^20, num_pages below 2^27, T and bt_cap below 2^30.
+ * All arrays device int32.
  * Errors: MB_EINVAL, MB_EUNSUPPORTED, MB_ECUDA. */
 mb_status mb_batch_tables(const int32_t *slots, const int32_t *cached, const int32_t *new_tokens, int32_t num_reqs,
                           int32_t T, int32_t bt_cap, int32_t *tables, int32_t *owned, int32_t max_slots,

@@ -240,18 +240,15 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int64_t e = e0 + k * step, t = e - pages;
+      const bool known = page[k] >= 0 && page[k] < a.num_pages;
+      if (!known && (e < pages || (e < all && t < tokens))) atomicExch(a.err, kErrBounds);
       if (e < pages) {
         a.bt[e] = page[k];
         if (place[k] >= have[req[k]]) a.tables[static_cast<int64_t>(row[req[k]]) * a.max_pages + place[k]] = page[k];
       } else if (e < all) {
-        int slot = -1;
-        if (t < tokens) {
-          if (page[k] < 0 || page[k] >= a.num_pages) atomicExch(a.err, kErrBounds);
-          else slot = page[k] * kPage + place[k] % kPage;
-        }
         a.tok_req[t] = req[k];
         a.tok_pos[t] = place[k];
-        a.tok_slot[t] = slot;
+        a.tok_slot[t] = known ? page[k] * kPage + place[k] % kPage : -1;   // (behind the last token: page -1)
       }
     }
   }

@@ -79,6 +79,7 @@ def batch_tables(slots, cached, new, T, bt_cap, tables, owned, ring, head, count
             owned[s] += 1
         mine = [int(x) for x in tables[s, :-(-(c + m) // PAGE)]] if c + m else []
         bt += mine
+        bad |= any(not 0 <= page < num_pages for page in mine)
         kv.append(c + m)
         for p in range(c, c + m):
             req.append(r)

@@ -195,3 +195,27 @@ def test_captured_and_replayed_the_step_follows_the_lengths(mb):
         cached = want[1]
         c.same()
     mb.mb_device_status(None, _stream())
+
+
+@pytest.mark.parametrize("page", [16, -1, 2 ** 31 - 1])
+def test_a_listed_page_out_of_range_is_recorded(mb, page):
+    """A page of cached tokens only, in a row: no token's place needs it, but the
+    descriptor lists it."""
+    c = Cache(16, 4, 8, seed=10)
+    c.step(mb, [1, 2], [0, 0], [40, 17], T=64)
+    c.tables[1, 0] = page
+    c.d["tables"].copy_(_i32(c.tables))
+    got = c.step(mb, [1, 2], [40, 17], [1, 1], T=64, err=True)
+    assert np.all(got["slot"][:2] >= 0)
+    c.step(mb, [2], [18], [1], T=64)             # not among these requests' pages
+
+
+def test_an_unlisted_page_out_of_range_is_not(mb):
+    """A row may hold more pages than the batch lists, and the ring any number."""
+    c = Cache(16, 4, 8, seed=11)
+    c.step(mb, [1], [0], [60], T=64)
+    c.tables[1, 3] = 99
+    c.ring[(c.head + c.count - 1) % 16] = -5
+    c.d["tables"].copy_(_i32(c.tables))
+    c.d["ring"].copy_(_i32(c.ring))
+    c.step(mb, [1], [40], [3], T=64)
