@@ -556,7 +556,7 @@ mb_status mb_tables_release(const int32_t *slots, int32_t n, const int32_t *tabl
  * memory, needs no initialisation; a call owns it until it completes (calls on
  * unordered streams, graphs that may run at once, need one each).  Neither size
  * below falls as an argument grows, so the workspace of the largest call does for
- * every smaller one.  No output may overlap an input.  T at most 2^20.
+ * every smaller one.  No output may overlap an input.  T and num_reqs at most 2^20.
  * Errors: MB_EINVAL, MB_EUNSUPPORTED, MB_ECUDA. */
 
 /* The new tokens' cache rows, and their queries' rotation: token t of T goes to

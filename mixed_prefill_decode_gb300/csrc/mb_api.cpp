@@ -1544,6 +1544,7 @@ static mb_status check_latent_attention(const char *who, const mb::LatentArgs &a
   mb_status st = check_latent(who, a.T, a.num_pages, a.H, a.hd, a.rank);
   if (st != MB_OK) return st;
   if (a.n_reqs < 0) return fail(MB_EINVAL, "%s: num_reqs < 0", who);
+  if (a.n_reqs > mb::kLatentMaxReqs) return fail(MB_EUNSUPPORTED, "%s: num_reqs > 2^20", who);
   if (!(a.scale > 0.f) || !std::isfinite(a.scale)) return fail(MB_EINVAL, "%s: scale must be positive and finite", who);
   for (const void *p : {a.q, a.q_rope, a.w_kv, static_cast<const void *>(a.o)})
     if (reinterpret_cast<uintptr_t>(p) % 16) return fail(MB_EINVAL, "%s: q, q_rope, w_kv and o must be 16-byte aligned", who);
@@ -1593,7 +1594,6 @@ mb_status mb_latent_prefill(const void *q, const void *q_rope, const void *w_kv,
                       num_pages, scale, workspace, nullptr, kv_tokens};
   if (kv_tokens < 0) return fail(MB_EINVAL, "mb_latent_prefill: kv_tokens < 0");
   if (kv_tokens > 1 << 27) return fail(MB_EUNSUPPORTED, "mb_latent_prefill: kv_tokens > 2^27");
-  if (num_reqs > 1 << 20) return fail(MB_EUNSUPPORTED, "mb_latent_prefill: num_reqs > 2^20");
   mb_status st = check_latent_attention("mb_latent_prefill", a,
                                         mb_latent_prefill_workspace_bytes(kv_tokens, num_reqs, n_heads, head_dim, rank));
   if (st != MB_OK || num_reqs == 0 || T == 0) return st;

@@ -7,6 +7,7 @@
 namespace mb {
 
 constexpr int kLatentRope = 64;          // dimensions of the rotated key that all heads share
+constexpr int kLatentMaxReqs = 1 << 20;  // requests of an attention call (a thread's range of them is counted in 32 bits)
 constexpr int kTablesMaxReqs = 8192;     // requests of one descriptor (their sums sit in shared memory)
 constexpr int kTablesMaxSlots = 65536;   // rows of the tables (a bit each, twice, in shared memory)
 constexpr int kTablesMaxPages = 1 << 20; // pages of one request: 2^24 tokens

@@ -237,3 +237,10 @@ def test_absorbed_workspace_never_falls_as_a_batch_grows(mb):
     axes = dict(T=[0, 1, 2, 63, 64, 65, 1000, 1 << 20], n_heads=list(range(1, 129)), rank=[256, 512])
     _never_falls(mb.mb_latent_attention_workspace_bytes, axes,
                  [dict(T=T, n_heads=H, rank=r) for T in (0, 7, 1 << 20) for H in (1, 40, 128) for r in (256, 512)])
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("n", [(1 << 20) + 1, 2 ** 31 - 1])
+def test_attention_refuses_more_requests_than_it_counts(mb, form, n):
+    _refused(mb, lambda: _attention(mb, form, num_reqs=n, T=0, **{k: (i + 1) << 40 for i, k in enumerate(ATT)}),
+             "MB_EUNSUPPORTED", ("num_reqs",))
