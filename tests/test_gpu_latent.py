@@ -537,3 +537,12 @@ def test_a_vector_that_is_not_finite_far_below_the_others(mb):
     b.check(want, "absorbed")
     b.pool[b.bt[12], 0, 7] = 0x7F80
     assert np.all(np.isnan(b.run(mb, "absorbed")[:1]))
+
+
+@pytest.mark.parametrize("form", ["absorbed", "expanded"])
+def test_few_requests_with_tokens_among_many_without(mb, form):
+    reqs = [(0, 0)] * 20000
+    for r, x in ((0, (70, 1)), (255, (0, 2)), (256, (300, 1)), (9999, (100, 3)), (19999, (130, 2))):
+        reqs[r] = x
+    b = Batch(reqs, 2, 64, 256, seed=95)
+    b.check(b.run(mb, form), form)
