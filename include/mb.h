@@ -36,6 +36,8 @@
  *     void*; NULL = the legacy default stream).  Argument and descriptor
  *     errors are returned before anything is launched.  A device-side check
  *     that fails records an error word that mb_device_status() reports.
+ *   - The first call on a device allocates the library's own memory there: make
+ *     it before any stream capture.
  *   - There is no CPU fallback: without a usable sm_103a device every compute
  *     call returns MB_ECUDA or MB_EUNSUPPORTED.
  */
@@ -574,7 +576,9 @@ mb_status mb_latent_append(const void *ckv, int64_t ld, const void *q, const voi
 
 /* Attention in the absorbed form, for decodes and a few drafted tokens: W_uk is
  * applied to the queries and W_uv to the outputs, and the cached rows are read
- * as they are, once for all heads (and for up to 64 / heads tokens of a request). */
+ * as they are, once for all heads (and for up to 64 / heads tokens of a request).
+ * The two weight products take all T rows, so a call on a few requests of a large
+ * step costs time and workspace for the whole step's rows. */
 mb_status mb_latent_attention(const void *q, const void *q_rope, const void *w_kv, const void *pool, void *o,
                               int32_t num_pages, int32_t n_heads, int32_t head_dim, int32_t rank, float scale,
                               int32_t num_reqs, int32_t T, const int32_t *qo_indptr, const int32_t *kv_len,
@@ -584,8 +588,8 @@ int64_t mb_latent_attention_workspace_bytes(int32_t T, int32_t n_heads, int32_t 
 /* The same attention in the expanded form, for prompt chunks: every head's keys
  * and values are made from the requests' vectors once per call, then attended
  * to.  kv_tokens: at least the sum of kv_len over the requests with tokens (at
- * most 2^27); it sizes the workspace, and requests that do not fit record
- * MB_EDEVICE and are left alone, with those behind them. */
+ * most 2^27); it sizes the workspace (whatever the rank), and requests that do not
+ * fit record MB_EDEVICE and are left alone, with those behind them. */
 mb_status mb_latent_prefill(const void *q, const void *q_rope, const void *w_kv, const void *pool, void *o,
                             int32_t num_pages, int32_t n_heads, int32_t head_dim, int32_t rank, float scale,
                             int32_t num_reqs, int32_t T, const int32_t *qo_indptr, const int32_t *kv_len,

@@ -1582,7 +1582,7 @@ mb_status mb_latent_attention(const void *q, const void *q_rope, const void *w_k
 int64_t mb_latent_prefill_workspace_bytes(int32_t kv_tokens, int32_t num_reqs, int32_t n_heads, int32_t head_dim,
                                           int32_t rank) {
   if (kv_tokens < 0 || num_reqs < 0 || n_heads <= 0 || head_dim <= 0 || rank <= 0) return 0;
-  return static_cast<int64_t>(mb::latent_prefill_workspace_bytes(kv_tokens, num_reqs, n_heads, head_dim, rank));
+  return static_cast<int64_t>(mb::latent_prefill_workspace_bytes(kv_tokens, num_reqs, n_heads, head_dim));
 }
 
 mb_status mb_latent_prefill(const void *q, const void *q_rope, const void *w_kv, const void *pool, void *o,

@@ -38,10 +38,11 @@ using namespace dev;
 // One CTA per token: its vector normalised, its key and the queries' last 64
 // numbers rotated (pairs (i, i + 32), frequency theta^(-2 i / 64)), vector and
 // key into the token's slot.  The angles are taken as in rope_append_kernel: a
-// split frequency and a two-constant reduction modulo 2 pi.  What bounds it is
-// HBM: every byte is read and written once; a head's 128 bytes go as eight
-// 16-byte vectors, four lanes to a head.  2,144 tokens of 40 heads, rank 512: 6.4 us
-// for 27 MB (4.2 TB/s), 64 of 32 heads 2.5: the latency of one load and a store.
+// split frequency and a two-constant reduction modulo 2 pi.  Every byte is read and
+// written once; a head's 128 bytes go as eight 16-byte vectors, four lanes to a
+// head.  64 tokens of 32 heads take 2.5 us: the latency of one load and a store.  2,144
+// of 40 heads, rank 512, 27 MB, take 5.9 to 6.4 (4.2 to 4.5 TB/s): 40 registers a thread
+// leave room for 6 CTAs on an SM, so they are three waves of a load, a barrier and a store.
 constexpr int kAppendThreads = 256;
 constexpr float kTwoPiHi = 6.28318548202514648f;         // fp32(2 pi)
 constexpr float kTwoPiLo = -1.7484556000744893e-07f;     // 2 pi - kTwoPiHi
@@ -151,7 +152,9 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const __g
 // one head on tcgen05, A and B wholly in shared memory, one barrier per 64 of
 // hd; the result leaves by TMA from where A was.  Heads' weights are read once per
 // TOK tokens: for few tokens they (and the launch) are the time, for many the
-// stores.  64 tokens of 32 heads 2.3 us from the kernel before's end, 16 of 128 heads
+// stores.  All T rows are multiplied, whoever has them (96 decodes of 40 heads in a step of
+// 2,144 tokens take 133 us, 86 by themselves).  64 tokens of 32 heads 2.3 us from the kernel
+// before's end, 16 of 128 heads
 // (16 MB of weights) 4, 256 of 128 heads (and 34 MB of results) 14.
 constexpr int kQueryN = 128;
 
@@ -302,8 +305,9 @@ __global__ void __launch_bounds__(128) latent_query_kernel(const __grid_constant
 // share, S and P V with N = 64 take 1,920), shared memory with 128 (S reads 144 KB of
 // it, P V 96, the copies write 72: 2,500 cycles at 128 bytes; a block takes 2,900).
 // Measured, the whole call replayed in a graph (head 128, rank 512): 96 ragged requests
-// of 1,024 to 8,192 keys, 40 heads 87 us, of which the stream of 390 MB about 60 (6.5
-// TB/s); 16 x 8,192 keys, 128 heads 66; 64 x 1,125 keys, 32 heads 35; one request 16 to 18.
+// of 1,024 to 8,192 keys, 40 heads 87 us (this kernel by itself, under the profiler, 72 for
+// 390 MB: 5.4 TB/s); 16 x 8,192 keys, 128 heads 66; 64 x 1,125 keys, 32 heads 35; one
+// request 16 to 18.
 constexpr int kMaxCtas = 160;       // CTAs of a launch at most; sizes the workspace
 // Floats of a slot: whole lines only (with m and l behind each row the stores and
 // loads of a row began 16 bytes off a sector).
@@ -312,7 +316,7 @@ constexpr int kBlk = 64;            // keys of a block
 constexpr int kCostUnit = 3;        // a unit's start and end, in blocks (1 to 4: within 5 %; short units like more, long ones less)
 
 struct AbsParams {
-  __nv_bfloat16 *oc;             // [T][H][rank]: sum_j p_j c_j
+  __nv_bfloat16 *oc;             // [T][H][rank]: sum_j p_j c_j, an operand of the product with W_uv (so bf16)
   const uint8_t *pool;
   const int32_t *qo_indptr, *kv_len, *bt_indptr, *bt;
   int n_reqs, T, H, Hc, HT, NT, N, num_pages;   // heads of a tile, head tiles, tokens of a tile, padded rows

@@ -54,7 +54,7 @@ struct LatentArgs {
 };
 size_t latent_attention_workspace_bytes(int64_t T, int64_t H, int64_t rank);
 cudaError_t latent_attention_run(const LatentArgs &a, cudaStream_t st);
-size_t latent_prefill_workspace_bytes(int64_t kv_tokens, int64_t n_reqs, int64_t H, int64_t hd, int64_t rank);
+size_t latent_prefill_workspace_bytes(int64_t kv_tokens, int64_t n_reqs, int64_t H, int64_t hd);   // (of any rank)
 cudaError_t latent_prefill_run(const LatentArgs &a, cudaStream_t st);
 
 }  // namespace mb

@@ -7,7 +7,10 @@
 //
 // Making a key and a value costs 4 hd rank operations, attending to them
 // 2 (2 hd + 64) for each token that does, against 2 (2 rank + 64) in the
-// absorbed form: from about a hundred tokens on this form does less.
+// absorbed form: from hd rank / (rank - hd) tokens on this form does less, 171 for 128
+// and 512, 85 for 64 and 256.  Measured at 8,192 keys it is the faster one from fewer:
+// 40 heads of 128, rank 512, 64 tokens 121 us against 109, 96 tokens 113 against 132;
+// 32 heads of 64, rank 256, 51 against 43 and 51 against 56.
 //
 // What bounds it: the tensor cores, and beside them the chain of product,
 // softmax, product.  Keys and values of a head are 4 hd bytes a token, written once
@@ -55,6 +58,8 @@ __host__ __device__ constexpr int64_t part_floats(int64_t hd) { return 256 * (hd
 // Keys and values of a group of heads at most (of one head, whatever it takes).
 // Groups that fit L2 were slower: 2,048 tokens at 8,192 keys, 40 heads, took 413 us as
 // one group of 168 MB, 448 as two, 517 as four (each starts and ends its kernels anew).
+// 128 heads of 128, 2,048 tokens: at 8,064 keys, the last of one group, 1,000 us (1.30 of
+// the operations' time), at 8,192, two groups of 64 heads, 1,019 (1.30).
 constexpr int kGroupBytes = 512 << 20;
 // The schedule's weights: a block of one query tile, a block of two, a unit's
 // start and end, and the least a CTA takes (at least kCost2, so that no CTA
@@ -195,7 +200,6 @@ __device__ __forceinline__ void line_parts(const PreParams &p, PrePart *parts, i
   }
 }
 
-// ------------------------------------------------------------------ expand
 // ------------------------------------------------------------------ expand
 // Over pairs of CTAs (cta_group::2): each has its own 128 cached rows as its half
 // of A and of the accumulators, and half of a head's weights as its half of B, so
@@ -519,6 +523,8 @@ __global__ void __launch_bounds__(ExpCfg<HD, RANK>::THREADS, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
+    // Keys and values are rounded to bf16 here: they are operands of the attention's
+    // products, which take 16 bits, and half the bytes on their way.
     // Four threads per key, 16 of each 64 numbers a thread: the weights' rows are
     // loaded in the order that makes them neighbours (row 8 i + 2 q + e of 64 is
     // 16 q + 2 i + e), so a key's 128 bytes go out together.  (One thread per key
@@ -1338,8 +1344,7 @@ cudaError_t launch_prefill(const LatentArgs &a, PreParams &p, int group, __nv_bf
 }  // namespace
 
 // a group's keys and values, the rotated keys, the records and parts, the partials
-size_t latent_prefill_workspace_bytes(int64_t kv_tokens, int64_t n_reqs, int64_t H, int64_t hd, int64_t rank) {
-  (void)rank;
+size_t latent_prefill_workspace_bytes(int64_t kv_tokens, int64_t n_reqs, int64_t H, int64_t hd) {
   const int64_t blocks = cap_blocks(kv_tokens, n_reqs);
   return align256(kv_room(blocks, H, hd)) +
          align256(static_cast<size_t>(blocks) * kBlk * kLatentRope * 2) + kRecBytes + kPartsBytes +

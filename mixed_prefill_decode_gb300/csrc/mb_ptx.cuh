@@ -66,8 +66,10 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 // Let the next kernel of the stream be scheduled once every CTA of this grid
 // has run this (or exited): its CTAs then take SMs as this grid's free up and
 // run their set-up, and wait in pdl_wait() for this grid to finish.  Every
-// kernel here issues it after its own pdl_wait(), and reads or writes
-// nothing an earlier kernel touches before that wait.
+// kernel here issues it after its own pdl_wait().  So when a call's second kernel
+// starts, all kernels from before the call have finished and their writes are
+// visible: before its wait a kernel may read what those left (weights, descriptors),
+// but nothing that a kernel of its own call writes, and it writes nothing.
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Non-blocking probe of a phase (try_wait may suspend the thread for a while;
