@@ -305,8 +305,8 @@ __global__ void __launch_bounds__(128) latent_query_kernel(const __grid_constant
 // share, S and P V with N = 64 take 1,920), shared memory with 128 (S reads 144 KB of
 // it, P V 96, the copies write 72: 2,500 cycles at 128 bytes; a block takes 2,900).
 // Measured, the whole call replayed in a graph (head 128, rank 512): 96 ragged requests
-// of 1,024 to 8,192 keys, 40 heads 87 us (this kernel by itself, under the profiler, 72 for
-// 390 MB: 5.4 TB/s); 16 x 8,192 keys, 128 heads 66; 64 x 1,125 keys, 32 heads 35; one
+// of 1,024 to 8,192 keys, 40 heads 87 us (this kernel by itself, under the profiler, 74 for
+// 390 MB: 5.3 TB/s); 16 x 8,192 keys, 128 heads 66; 64 x 1,125 keys, 32 heads 35; one
 // request 16 to 18.
 constexpr int kMaxCtas = 160;       // CTAs of a launch at most; sizes the workspace
 // Floats of a slot: whole lines only (with m and l behind each row the stores and
